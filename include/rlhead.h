@@ -70,6 +70,13 @@ extern "C" {
                                                 gradient has a dense softmax part            */
 #define RL_STATUS_NONFINITE          0x0100  /* a non-finite loss or logsumexp               */
 #define RL_STATUS_TIMEOUT            0x0200  /* a kernel's bounded wait ran out; outputs invalid */
+/* bits of the generation operators (rl_page_plan .. rl_sample) */
+#define RL_STATUS_LENGTHS            0x0400  /* a negative length, lengths that do not add up, or a
+                                                length above the bound the caller gave         */
+#define RL_STATUS_PAGES              0x0800  /* the page pool ran out, or a table row is too short */
+#define RL_STATUS_PAGE_ID            0x1000  /* a page id or cache slot outside the cache       */
+#define RL_STATUS_KNOB               0x2000  /* a sampling knob or random number out of range   */
+#define RL_STATUS_CAPACITY           0x4000  /* the support does not fit the caller's buffers   */
 
 /* ---- knobs ---------------------------------------------------------------------- */
 typedef enum { RL_LOSS_IPO = 0, RL_LOSS_ICEPOP = 1, RL_LOSS_REINFORCE = 2 } rl_loss_type;
@@ -478,6 +485,73 @@ typedef struct rl_rc_named {
  * enum). */
 int rl_rollout_metrics_named(const rl_rc_metrics* metrics, const rl_rc_params* params,
                              rl_rc_named* named, void* stream);
+
+/* ---- generation: the steps of a rollout batch's decode step ---------------------------
+ * The rollouts that the head trains on come from an engine that decodes groups of samples
+ * of the same prompt, and records per token the sampler's log q and its support
+ * ("TokenSupport", pull request #4233).  Four operators make one decode step over a paged
+ * cache of keys and values, in this order:
+ *   rl_page_plan     pages for the step's tokens, their cache slots and positions
+ *   rl_kv_append     the step's keys and values into the cache
+ *   rl_prefix_attn   attention over the group's shared prompt and the request's own keys
+ *   rl_sample        the next token, its log q, and the sampler support as CSR rows
+ * The cache: k_cache and v_cache [n_pages, Hkv, page_size, D], dense, 16-byte aligned; slot
+ * s is entry s % page_size of page s / page_size.  A group's prompt is stored once, in pages
+ * of the group's own table (make them by a plan whose requests are the groups); a request's
+ * table holds the pages of its own tokens only, so that a prompt may end inside a page.
+ * Requests of one group are consecutive: group g has requests [group_offsets[g],
+ * group_offsets[g+1]), and a request outside every group has no prefix.
+ * Lengths live on the device, so that a step can be captured in a CUDA graph and replayed
+ * as they change; the host gives upper bounds.  Lengths and pages are checked on the device:
+ * bad ones set RL_STATUS_* bits and are never followed out of the caller's buffers. */
+typedef enum { RL_DTYPE_F32 = 0, RL_DTYPE_BF16 = 1, RL_DTYPE_F16 = 2 } rl_dtype;
+
+/* Page tables and slots from lengths.  Request r has ctx_lens[r] tokens in its own pages and
+ * adds q_lens[r].  Pages it lacks are handed out from free_pages, in request order, starting
+ * at index *free_used:  table[r][j] for ceil(ctx/page_size) <= j < ceil((ctx+q)/page_size).
+ * Entries that are there are kept.  Same inputs, same outputs: a second call with the same
+ * lengths and the same *free_used hands out the same pages.
+ * A pool that runs out or a row shorter than the request needs sets RL_STATUS_PAGES; a page
+ * id outside [0, n_pages) sets RL_STATUS_PAGE_ID; either way the slots concerned are -1 and
+ * the entries concerned are -1 (past the row's end none is written).  A negative length
+ * counts as 0 and sets RL_STATUS_LENGTHS, as does sum(q_lens) != T: slots and positions past
+ * the sum are -1, tokens past T are left out. */
+typedef struct rl_page_plan_args {
+    int64_t R;                      /* requests, < 2^31 */
+    int64_t T;                      /* tokens of the step, the length of slot_map / positions */
+    const int32_t* q_lens;          /* device [R] tokens added by this step */
+    const int32_t* ctx_lens;        /* device [R] tokens already in the request's own pages */
+    int32_t* block_table;           /* device [R, table_width] in/out */
+    int64_t table_width;
+    const int32_t* free_pages;      /* device [n_free] page ids to hand out */
+    int64_t n_free;
+    const int32_t* free_used;       /* device [1] ids handed out before; NULL = 0 */
+    int32_t* free_used_out;         /* device [1] ids handed out after this step; not free_used */
+    const int32_t* group_offsets;   /* device [G+1]; NULL = no groups */
+    const int32_t* prefix_lens;     /* device [G] */
+    int64_t G;
+    int64_t n_pages;                /* pages of the cache */
+    int32_t page_size;              /* 16, 32, 64 or 128 */
+    int32_t* cu_q;                  /* device [R+1] out: first token of each request */
+    int32_t* kv_lens;               /* device [R] out: ctx + q */
+    int64_t* slot_map;              /* device [T] out: cache slot of each token */
+    int32_t* positions;             /* device [T] out: prefix + ctx + index in the step; NULL to skip */
+} rl_page_plan_args;
+int rl_page_plan(const rl_page_plan_args* args, int32_t* dev_status, void* stream);
+
+/* k_cache[slot] = k[t], v_cache[slot] = v[t] for every token with slot_map[t] >= 0.  k, v:
+ * [T, Hkv, D] with any token and head strides (in elements; a token's head is contiguous).
+ * A slot at or past n_pages * page_size is left out and sets RL_STATUS_PAGE_ID.  Slots are
+ * distinct (of equal slots, either token's values may stay).  bf16 or fp16. */
+typedef struct rl_kv_append_args {
+    const void *k, *v;
+    int64_t k_stride_t, k_stride_h, v_stride_t, v_stride_h;
+    const int64_t* slot_map;        /* device [T] */
+    void *k_cache, *v_cache;
+    int64_t T, n_pages;
+    int32_t Hkv, D, page_size, dtype;
+} rl_kv_append_args;
+int rl_kv_append(const rl_kv_append_args* args, int32_t* dev_status, void* stream);
 
 /* ---- utilities ------------------------------------------------------------------ */
 /* The head contraction alone: D[M, N] fp32 = A[M, K] * B[N, K]^T, A and B bf16 row-major

@@ -13,6 +13,8 @@ Functions carry the C names:
   elementwise: rl_policy_loss_elementwise (+ rl_policy_loss_elementwise_noalloc in C)
   rollout:     rl_rollout_correction (IS / RS weights, veto, batch normalisation, metric
                sums), rl_rollout_metrics_named (the page's named metrics from those sums)
+  generation:  rl_page_plan, rl_kv_append, rl_prefix_attn, rl_sample (one decode step of a
+               rollout batch; lm_head_gb300.generation)
   utilities:   rl_gemm_bf16, rl_gemm_bf16_tn, rl_status_read, rl_wait_selftest,
                rl_set_option / rl_get_option, rl_profile_enable / rl_profile_read,
                rl_kernel_launch_count, the *_workspace_bytes queries
@@ -45,7 +47,8 @@ RL_GRAD_BF16, RL_GRAD_SPLIT = 0, 1
 STATUS_BITS = {
     0x0001: "OFFSETS", 0x0002: "ID_RANGE", 0x0004: "LOGQ", 0x0008: "LABEL_MISSING",
     0x0010: "SUPPORT_MASS", 0x0020: "EMPTY_ROW", 0x0040: "ROW_ORDER",
-    0x0080: "SPARSE_INELIGIBLE", 0x0100: "NONFINITE", 0x0200: "TIMEOUT",
+    0x0080: "SPARSE_INELIGIBLE", 0x0100: "NONFINITE", 0x0200: "TIMEOUT", 0x0400: "LENGTHS",
+    0x0800: "PAGES", 0x1000: "PAGE_ID", 0x2000: "KNOB", 0x4000: "CAPACITY",
 }
 RL_PG_MAX_CURVE = 16
 
@@ -131,9 +134,14 @@ class RlRcNamed(ctypes.Structure):
         "is_ratio_max_final")]
 
 
+from .generation import (  # noqa: E402
+    RL_DTYPE_BF16, RL_DTYPE_F16, RL_DTYPE_F32, PagePlan, RlKvAppendArgs, RlPagePlanArgs, rl_kv_append, rl_page_plan)
+from . import generation as _generation  # noqa: E402
+
 _lib = None
 
 _SIGS = {
+    **_generation.SIGS,
     "rl_head_saved_bytes": (ctypes.c_size_t, [ctypes.c_int64, ctypes.c_int64]),
     "rl_head_saved_bytes_ex": (ctypes.c_size_t, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int64,
                                                  ctypes.POINTER(RlParams)]),

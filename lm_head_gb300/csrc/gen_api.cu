@@ -1,0 +1,66 @@
+// C ABI of the generation path (declared in include/rlhead.h): host-side argument checks
+// and dispatch.  Nothing here allocates device memory or synchronises.
+#include <cmath>
+
+#include "internal.h"
+
+using namespace rl;
+
+namespace {
+
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+int fail(int code, const char* msg) {
+    set_last_error(msg);
+    return code;
+}
+
+int check_device() {
+    int dev = 0, major = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess || major != 10)
+        return fail(RL_ERR_UNSUPPORTED, "needs an sm_100-family GPU");
+    return RL_OK;
+}
+
+bool page_size_ok(int32_t p) { return p == 16 || p == 32 || p == 64 || p == 128; }
+
+constexpr int64_t kMax31 = int64_t(1) << 31;
+
+}  // namespace
+
+extern "C" {
+
+int rl_page_plan(const rl_page_plan_args* a, int32_t* dev_status, void* stream) {
+    if (!a || !dev_status) return fail(RL_ERR_ARG, "args/dev_status is NULL");
+    if (a->R < 0 || a->T < 0 || a->G < 0 || a->n_free < 0 || a->n_pages < 0 || a->table_width < 0)
+        return fail(RL_ERR_ARG, "negative size");
+    if (!page_size_ok(a->page_size)) return fail(RL_ERR_UNSUPPORTED, "page_size must be 16, 32, 64 or 128");
+    if (a->R >= kMax31 || a->T >= kMax31 || a->G >= kMax31 || a->n_free >= kMax31 || a->n_pages >= kMax31)
+        return fail(RL_ERR_UNSUPPORTED, "R, T, G, n_free or n_pages too large");
+    if (!a->cu_q || !a->free_used_out || (a->R > 0 && (!a->q_lens || !a->ctx_lens || !a->kv_lens)) ||
+        (a->T > 0 && !a->slot_map) || (a->R > 0 && a->table_width > 0 && !a->block_table) ||
+        (a->n_free > 0 && !a->free_pages))
+        return fail(RL_ERR_ARG, "required pointer is NULL");
+    if (a->G > 0 && (!a->group_offsets || !a->prefix_lens))
+        return fail(RL_ERR_ARG, "group_offsets/prefix_lens NULL with G > 0");
+    if (a->free_used == a->free_used_out) return fail(RL_ERR_ARG, "free_used_out must not be free_used");
+    int rc = check_device();
+    return rc != RL_OK ? rc : page_plan_impl(a, dev_status, static_cast<cudaStream_t>(stream));
+}
+
+int rl_kv_append(const rl_kv_append_args* a, int32_t* dev_status, void* stream) {
+    if (!a || !dev_status) return fail(RL_ERR_ARG, "args/dev_status is NULL");
+    if (a->T < 0 || a->n_pages < 0 || a->Hkv <= 0 || a->D <= 0) return fail(RL_ERR_ARG, "negative or zero size");
+    if (!page_size_ok(a->page_size)) return fail(RL_ERR_UNSUPPORTED, "page_size must be 16, 32, 64 or 128");
+    if (a->dtype != RL_DTYPE_BF16 && a->dtype != RL_DTYPE_F16) return fail(RL_ERR_UNSUPPORTED, "dtype must be bf16 or fp16");
+    if (a->T >= kMax31 || a->n_pages >= kMax31 || int64_t(a->Hkv) * a->D >= (int64_t(1) << 24))
+        return fail(RL_ERR_UNSUPPORTED, "T, n_pages or Hkv * D too large");
+    if (a->T > 0 && (!a->k || !a->v || !a->slot_map)) return fail(RL_ERR_ARG, "k/v/slot_map is NULL");
+    if (a->T > 0 && a->n_pages > 0 && (!a->k_cache || !a->v_cache)) return fail(RL_ERR_ARG, "cache is NULL");
+    if (!aligned(a->k_cache, 16) || !aligned(a->v_cache, 16)) return fail(RL_ERR_ARG, "cache not 16-byte aligned");
+    int rc = check_device();
+    return rc != RL_OK ? rc : kv_append_impl(a, dev_status, static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

@@ -171,5 +171,8 @@ int rollout_named_impl(const rl_rc_metrics* m, const rl_rc_params* p, rl_rc_name
 int wait_selftest_impl(int32_t* status, cudaStream_t stream);
 int gemm_util_impl(const void* A, int a_mn, const void* B, int b_mn, int64_t M, int64_t N, int64_t K,
                    float* D, int32_t* status, cudaStream_t stream);
+// generation path
+int page_plan_impl(const rl_page_plan_args* a, int32_t* status, cudaStream_t stream);
+int kv_append_impl(const rl_kv_append_args* a, int32_t* status, cudaStream_t stream);
 
 }  // namespace rl

@@ -1,0 +1,140 @@
+"""Binding of the generation operators (include/rlhead.h, "generation"): page plans, cache
+writes, attention over a shared prefix, and sampling with the head's support rows.
+
+Argument marshalling only, as in the package's other calls.  Every function takes its output
+buffers through `out` / `status`, so that a decode loop allocates nothing after its first step
+(and can be captured in a CUDA graph); without them it makes them.  The status word is
+never cleared by the library: read it with status_bits() and zero it.
+"""
+from __future__ import annotations
+
+import ctypes
+import dataclasses
+from typing import Optional
+
+import torch
+
+RL_DTYPE_F32, RL_DTYPE_BF16, RL_DTYPE_F16 = 0, 1, 2
+_DTYPES = {torch.float32: RL_DTYPE_F32, torch.bfloat16: RL_DTYPE_BF16, torch.float16: RL_DTYPE_F16}
+_P, _I64, _I32, _F = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_float
+
+
+class RlPagePlanArgs(ctypes.Structure):
+    _fields_ = [("R", _I64), ("T", _I64), ("q_lens", _P), ("ctx_lens", _P), ("block_table", _P),
+                ("table_width", _I64), ("free_pages", _P), ("n_free", _I64), ("free_used", _P),
+                ("free_used_out", _P), ("group_offsets", _P), ("prefix_lens", _P), ("G", _I64), ("n_pages", _I64),
+                ("page_size", _I32), ("cu_q", _P), ("kv_lens", _P), ("slot_map", _P), ("positions", _P)]
+
+
+class RlKvAppendArgs(ctypes.Structure):
+    _fields_ = [("k", _P), ("v", _P), ("k_stride_t", _I64), ("k_stride_h", _I64), ("v_stride_t", _I64),
+                ("v_stride_h", _I64), ("slot_map", _P), ("k_cache", _P), ("v_cache", _P), ("T", _I64),
+                ("n_pages", _I64), ("Hkv", _I32), ("D", _I32), ("page_size", _I32), ("dtype", _I32)]
+
+
+SIGS = {
+    "rl_page_plan": (ctypes.c_int, [_P, _P, _P]),
+    "rl_kv_append": (ctypes.c_int, [_P, _P, _P]),
+}
+
+
+def _rh():
+    import lm_head_gb300
+    return lm_head_gb300
+
+
+def _err(msg):
+    return _rh().RLHeadError(msg)
+
+
+def _call(name, *args, stream=None):
+    rh = _rh()
+    s = torch.cuda.current_stream() if stream is None else stream
+    rh._check(getattr(rh.load(), name)(*args, s.cuda_stream))
+
+
+def _dev(name, t, dtype, n=None, optional=False):
+    """Device address of a contiguous tensor of `dtype` (and `n` elements)."""
+    if t is None:
+        if optional:
+            return None
+        raise _err(f"{name} is missing")
+    if not t.is_cuda:
+        raise _err(f"{name}: librlhead takes device tensors; got a CPU tensor")
+    if t.dtype != dtype or not t.is_contiguous():
+        raise _err(f"{name}: expected contiguous {dtype}, got {t.dtype}")
+    if n is not None and t.numel() != n:
+        raise _err(f"{name}: expected {n} elements, got {t.numel()}")
+    return t.data_ptr()
+
+
+def _status(status, device):
+    return torch.zeros(1, dtype=torch.int32, device=device) if status is None else status
+
+
+@dataclasses.dataclass
+class PagePlan:
+    """What rl_page_plan writes (include/rlhead.h, rl_page_plan_args)."""
+    cu_q: torch.Tensor          # [R+1] int32
+    kv_lens: torch.Tensor       # [R] int32
+    slot_map: torch.Tensor      # [T] int64
+    positions: torch.Tensor     # [T] int32
+    free_used: torch.Tensor     # [1] int32: pass it as the next step's free_used
+    status: torch.Tensor        # [1] int32
+
+    def status_bits(self) -> int:
+        return int(self.status.item())
+
+
+def rl_page_plan(q_lens, ctx_lens, block_table, free_pages, *, page_size: int, n_pages: int, n_tokens: int,
+                 free_used=None, group_offsets=None, prefix_lens=None, out: Optional[PagePlan] = None, status=None,
+                 stream=None) -> PagePlan:
+    """Pages for a step's tokens: extends `block_table` [R, W] in place from the pool
+    `free_pages` and returns the token offsets, key lengths, cache slots and positions.
+    n_tokens is sum(q_lens), known to whoever sized the step's tensors."""
+    R, W = block_table.shape
+    i32 = torch.int32
+    if out is None:
+        dev = block_table.device
+        if not block_table.is_cuda:
+            raise _err("block_table: librlhead takes device tensors; got a CPU tensor")
+        out = PagePlan(torch.empty(R + 1, dtype=i32, device=dev), torch.empty(R, dtype=i32, device=dev),
+                       torch.empty(n_tokens, dtype=torch.int64, device=dev), torch.empty(n_tokens, dtype=i32, device=dev),
+                       torch.empty(1, dtype=i32, device=dev), _status(status, dev))
+    elif status is not None:
+        out = dataclasses.replace(out, status=status)
+    G = 0 if group_offsets is None else group_offsets.numel() - 1
+    a = RlPagePlanArgs(R, n_tokens, _dev("q_lens", q_lens, i32, R), _dev("ctx_lens", ctx_lens, i32, R),
+                       _dev("block_table", block_table, i32), W, _dev("free_pages", free_pages, i32),
+                       free_pages.numel(), _dev("free_used", free_used, i32, 1, True),
+                       _dev("out.free_used", out.free_used, i32, 1),
+                       _dev("group_offsets", group_offsets, i32, None, True),
+                       _dev("prefix_lens", prefix_lens, i32, G, G == 0), G, n_pages, page_size,
+                       _dev("out.cu_q", out.cu_q, i32, R + 1), _dev("out.kv_lens", out.kv_lens, i32, R),
+                       _dev("out.slot_map", out.slot_map, torch.int64, n_tokens),
+                       _dev("out.positions", out.positions, i32, n_tokens, True))
+    _call("rl_page_plan", ctypes.byref(a), _dev("status", out.status, i32, 1), stream=stream)
+    return out
+
+
+def _cache(k_cache, v_cache):
+    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.dtype != v_cache.dtype:
+        raise _err("k_cache / v_cache: two tensors [n_pages, Hkv, page_size, D] of one type")
+    dt = k_cache.dtype
+    return _dev("k_cache", k_cache, dt), _dev("v_cache", v_cache, dt), _DTYPES.get(dt, -1)
+
+
+def rl_kv_append(k, v, slot_map, k_cache, v_cache, *, status=None, stream=None) -> torch.Tensor:
+    """k_cache[slot] = k[t], v_cache[slot] = v[t] (k, v [T, Hkv, D], any token and head
+    strides) for the tokens whose slot is not negative.  Returns the status word."""
+    kc, vc, dt = _cache(k_cache, v_cache)
+    n_pages, Hkv, page, D = k_cache.shape
+    T = slot_map.numel()
+    for name, t in (("k", k), ("v", v)):
+        if not t.is_cuda or t.dtype != k_cache.dtype or tuple(t.shape) != (T, Hkv, D) or (D > 1 and t.stride(2) != 1):
+            raise _err(f"{name}: expected a device tensor [{T}, {Hkv}, {D}] of the cache's type with dense heads")
+    status = _status(status, k_cache.device)
+    a = RlKvAppendArgs(k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1), v.stride(0), v.stride(1),
+                       _dev("slot_map", slot_map, torch.int64, T), kc, vc, T, n_pages, Hkv, D, page, dt)
+    _call("rl_kv_append", ctypes.byref(a), _dev("status", status, torch.int32, 1), stream=stream)
+    return status

@@ -1,0 +1,80 @@
+"""Generation operators, host side: arguments that are refused before any device work (no
+GPU needed), and the binding's own checks."""
+import ctypes
+
+import pytest
+import torch
+
+import lm_head_gb300 as rh
+from lm_head_gb300 import generation as gen
+
+FAKE = 1 << 20          # 16-byte aligned, never dereferenced: the host checks fail first
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from lm_head_gb300 import build
+    build.build()
+    return rh.load()
+
+
+def _fill(cls, **kw):
+    a = cls()
+    for name, typ in cls._fields_:
+        if name in kw:
+            setattr(a, name, kw[name])
+        elif typ is ctypes.c_void_p:
+            setattr(a, name, FAKE)
+    return a
+
+
+def _refused(lib, fn, make, changes, status=FAKE, tail=()):
+    for change, want in changes:
+        a = make(**change)
+        assert getattr(lib, fn)(ctypes.byref(a), *tail, status, None) == want, change
+    assert getattr(lib, fn)(None, *tail, status, None) == rh.RL_ERR_ARG
+    good = make()
+    assert getattr(lib, fn)(ctypes.byref(good), *tail, None, None) == rh.RL_ERR_ARG      # no status word
+
+
+def test_struct_sizes():
+    assert ctypes.sizeof(gen.RlPagePlanArgs) == 19 * 8
+    assert ctypes.sizeof(gen.RlKvAppendArgs) == 11 * 8 + 4 * 4
+
+
+def test_page_plan_refusals(lib):
+    def make(**kw):
+        return _fill(gen.RlPagePlanArgs, **{**dict(R=4, T=8, table_width=2, n_free=8, G=2, n_pages=8, page_size=16,
+                                                   free_used_out=FAKE + 64), **kw})
+    arg, uns = rh.RL_ERR_ARG, rh.RL_ERR_UNSUPPORTED
+    _refused(lib, "rl_page_plan", make, [
+        (dict(R=-1), arg), (dict(T=-1), arg), (dict(G=-1), arg), (dict(n_free=-1), arg), (dict(n_pages=-1), arg),
+        (dict(table_width=-1), arg), (dict(page_size=0), uns), (dict(page_size=24), uns), (dict(page_size=256), uns),
+        (dict(R=1 << 31), uns), (dict(T=1 << 31), uns), (dict(n_pages=1 << 31), uns),
+        (dict(q_lens=None), arg), (dict(ctx_lens=None), arg), (dict(block_table=None), arg), (dict(cu_q=None), arg),
+        (dict(kv_lens=None), arg), (dict(slot_map=None), arg), (dict(free_pages=None), arg),
+        (dict(group_offsets=None), arg), (dict(prefix_lens=None), arg), (dict(free_used_out=None), arg),
+        (dict(free_used_out=FAKE), arg)])
+
+
+def test_kv_append_refusals(lib):
+    def make(**kw):
+        return _fill(gen.RlKvAppendArgs, **{**dict(T=8, n_pages=4, Hkv=2, D=64, page_size=16, dtype=rh.RL_DTYPE_BF16), **kw})
+    arg, uns = rh.RL_ERR_ARG, rh.RL_ERR_UNSUPPORTED
+    _refused(lib, "rl_kv_append", make, [
+        (dict(T=-1), arg), (dict(n_pages=-1), arg), (dict(Hkv=0), arg), (dict(D=0), arg), (dict(page_size=17), uns),
+        (dict(dtype=rh.RL_DTYPE_F32), uns), (dict(dtype=9), uns), (dict(T=1 << 31), uns), (dict(k=None), arg),
+        (dict(v=None), arg), (dict(slot_map=None), arg), (dict(k_cache=None), arg), (dict(v_cache=FAKE + 8), arg)])
+
+
+def test_binding_refuses_host_tensors_and_wrong_types():
+    i32 = torch.int32
+    with pytest.raises(rh.RLHeadError):
+        rh.rl_page_plan(torch.ones(2, dtype=i32), torch.ones(2, dtype=i32), torch.zeros(2, 3, dtype=i32),
+                        torch.arange(9, dtype=i32), page_size=16, n_pages=9, n_tokens=2)
+    k = torch.zeros(3, 2, 64, dtype=torch.bfloat16)
+    cache = torch.zeros(4, 2, 16, 64, dtype=torch.bfloat16)
+    with pytest.raises(rh.RLHeadError):
+        rh.rl_kv_append(k, k, torch.zeros(3, dtype=torch.int64), cache, cache)
+    with pytest.raises(rh.RLHeadError):
+        rh.rl_kv_append(k, k, torch.zeros(3, dtype=torch.int64), cache, cache[:, :, :8])
