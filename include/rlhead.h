@@ -553,6 +553,47 @@ typedef struct rl_kv_append_args {
 } rl_kv_append_args;
 int rl_kv_append(const rl_kv_append_args* args, int32_t* dev_status, void* stream);
 
+/* Sampling from logits, K draws a row.  With z the row's logits and T its temperature,
+ * x = (z - max z) / T and w = e^x:
+ *   candidates   the top_k largest logits (ties: the lower index first) with w >= min_p and
+ *                w >= 2^-100
+ *   support S    their shortest prefix, in descending order (ties: the lower index first),
+ *                whose sum of w reaches top_p times the candidates' sum; at least one token
+ *   q(i)         w_i / sum_S w
+ *   draw u       the first token i of S, in index order, with sum_{j in S, j <= i} w_j > u sum_S w
+ * Sums that decide a token or a set member are carried to about 2^-37 of the largest weight, so that these
+ * agree with exact arithmetic except where a random number falls that near to a border.
+ * T = 0 is greedy: S is the largest logit (the lowest index of equal ones).  top_k outside
+ * [1, V), top_p >= 1 and min_p <= 0 leave their cut out; top_p <= 0 and min_p > 1 keep one
+ * token and the likeliest tokens.  T < 0 or not finite (greedy is used), a NaN knob (its cut is
+ * left out) and u outside [0, 1) (clamped) set RL_STATUS_KNOB.  NaN and +inf logits count as
+ * -inf and set RL_STATUS_NONFINITE.  A row with no logit above -inf gets tokens -1, log q -inf,
+ * an empty support and RL_STATUS_EMPTY_ROW.
+ * The support rows are the head's (rl_support): of a row with a cut in effect (greedy included)
+ * all of S, ascending, replayed = 1; of any other row draws 1 .. K-1 in ascending order,
+ * repeats kept, replayed = 0 (draw 0 is the label).  offsets[N] is the true total even when it
+ * exceeds `capacity`; entries past it are not written and RL_STATUS_CAPACITY is set. */
+typedef struct rl_sample_args {
+    const void* logits;             /* device [N, V], rows row_stride elements apart */
+    int64_t N, V, row_stride;       /* V <= 2^20 */
+    int32_t dtype;                  /* rl_dtype */
+    int32_t K;                      /* draws a row, 1 .. 1024 */
+    const float* temperature;       /* device [N]; NULL = 1 */
+    const int32_t* top_k;           /* device [N]; NULL = none */
+    const float* top_p;             /* device [N]; NULL = none */
+    const float* min_p;             /* device [N]; NULL = none */
+    const float* u;                 /* device [N, K] in [0, 1) */
+    int32_t* tokens;                /* device [N, K] */
+    float* logq;                    /* device [N, K]; NULL to skip */
+    int64_t* offsets;               /* device [N+1]; NULL: no support is written */
+    int32_t* ids;                   /* device [capacity] */
+    float* support_logq;            /* device [capacity] */
+    int64_t capacity;
+    uint8_t* replayed;              /* device [N]; NULL to skip */
+} rl_sample_args;
+size_t rl_sample_workspace_bytes(int64_t N, int64_t V, int32_t K);
+int rl_sample(const rl_sample_args* args, void* ws, size_t ws_bytes, int32_t* dev_status, void* stream);
+
 /* ---- utilities ------------------------------------------------------------------ */
 /* The head contraction alone: D[M, N] fp32 = A[M, K] * B[N, K]^T, A and B bf16 row-major
  * (K contiguous), device pointers, 16-byte aligned; K % 8 == 0, N % 4 == 0.  Same tcgen05

@@ -135,7 +135,8 @@ class RlRcNamed(ctypes.Structure):
 
 
 from .generation import (  # noqa: E402
-    RL_DTYPE_BF16, RL_DTYPE_F16, RL_DTYPE_F32, PagePlan, RlKvAppendArgs, RlPagePlanArgs, rl_kv_append, rl_page_plan)
+    RL_DTYPE_BF16, RL_DTYPE_F16, RL_DTYPE_F32, PagePlan, RlKvAppendArgs, RlPagePlanArgs, RlSampleArgs,
+    SampleOut, rl_kv_append, rl_page_plan, rl_sample, rl_sample_workspace_bytes)
 from . import generation as _generation  # noqa: E402
 
 _lib = None

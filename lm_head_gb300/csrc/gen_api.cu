@@ -25,6 +25,7 @@ int check_device() {
 
 bool page_size_ok(int32_t p) { return p == 16 || p == 32 || p == 64 || p == 128; }
 
+constexpr int64_t kMaxVocab = int64_t(1) << 20;
 constexpr int64_t kMax31 = int64_t(1) << 31;
 
 }  // namespace
@@ -61,6 +62,34 @@ int rl_kv_append(const rl_kv_append_args* a, int32_t* dev_status, void* stream) 
     if (!aligned(a->k_cache, 16) || !aligned(a->v_cache, 16)) return fail(RL_ERR_ARG, "cache not 16-byte aligned");
     int rc = check_device();
     return rc != RL_OK ? rc : kv_append_impl(a, dev_status, static_cast<cudaStream_t>(stream));
+}
+
+size_t rl_sample_workspace_bytes(int64_t N, int64_t V, int32_t K) {
+    if (N < 0 || V <= 0 || V > kMaxVocab || K <= 0) return 0;
+    return sample_ws_bytes(N, V);
+}
+
+int rl_sample(const rl_sample_args* a, void* ws, size_t ws_bytes, int32_t* dev_status, void* stream) {
+    if (!a || !dev_status) return fail(RL_ERR_ARG, "args/dev_status is NULL");
+    if (a->N < 0 || a->V <= 0 || a->K <= 0 || a->capacity < 0) return fail(RL_ERR_ARG, "negative or zero size");
+    if (a->dtype != RL_DTYPE_F32 && a->dtype != RL_DTYPE_BF16 && a->dtype != RL_DTYPE_F16)
+        return fail(RL_ERR_UNSUPPORTED, "dtype must be fp32, bf16 or fp16");
+    if (a->V > kMaxVocab || a->N >= kMax31 || a->K > 1024) return fail(RL_ERR_UNSUPPORTED, "N, V or K too large");
+    if (a->N > 1 && a->row_stride < a->V) return fail(RL_ERR_ARG, "row_stride smaller than V");
+    if (a->N > 0 && (!a->logits || !a->u || !a->tokens)) return fail(RL_ERR_ARG, "logits/u/tokens is NULL");
+    if (a->offsets && a->capacity > 0 && (!a->ids || !a->support_logq))
+        return fail(RL_ERR_ARG, "ids/support_logq NULL with capacity > 0");
+    if (!aligned(a->logits, a->dtype == RL_DTYPE_F32 ? 4 : 2)) return fail(RL_ERR_ARG, "logits not aligned to their type");
+    if (ws_bytes < rl_sample_workspace_bytes(a->N, a->V, a->K)) return fail(RL_ERR_WORKSPACE, "sampling workspace too small");
+    if (!ws || !aligned(ws, 16)) return fail(RL_ERR_ARG, "ws is NULL or not 16-byte aligned");
+    int rc = check_device();
+    if (rc != RL_OK) return rc;
+    if (a->N == 0) {
+        if (a->offsets && cudaMemsetAsync(a->offsets, 0, sizeof(int64_t), static_cast<cudaStream_t>(stream)) != cudaSuccess)
+            return fail(RL_ERR_CUDA, "cudaMemsetAsync failed");
+        return RL_OK;
+    }
+    return sample_impl(a, ws, dev_status, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

@@ -32,9 +32,18 @@ class RlKvAppendArgs(ctypes.Structure):
                 ("n_pages", _I64), ("Hkv", _I32), ("D", _I32), ("page_size", _I32), ("dtype", _I32)]
 
 
+class RlSampleArgs(ctypes.Structure):
+    _fields_ = [("logits", _P), ("N", _I64), ("V", _I64), ("row_stride", _I64), ("dtype", _I32), ("K", _I32),
+                ("temperature", _P), ("top_k", _P), ("top_p", _P), ("min_p", _P), ("u", _P), ("tokens", _P),
+                ("logq", _P), ("offsets", _P), ("ids", _P), ("support_logq", _P), ("capacity", _I64),
+                ("replayed", _P)]
+
+
 SIGS = {
     "rl_page_plan": (ctypes.c_int, [_P, _P, _P]),
     "rl_kv_append": (ctypes.c_int, [_P, _P, _P]),
+    "rl_sample_workspace_bytes": (ctypes.c_size_t, [_I64, _I64, _I32]),
+    "rl_sample": (ctypes.c_int, [_P, _P, ctypes.c_size_t, _P, _P]),
 }
 
 
@@ -138,3 +147,65 @@ def rl_kv_append(k, v, slot_map, k_cache, v_cache, *, status=None, stream=None) 
                        _dev("slot_map", slot_map, torch.int64, T), kc, vc, T, n_pages, Hkv, D, page, dt)
     _call("rl_kv_append", ctypes.byref(a), _dev("status", status, torch.int32, 1), stream=stream)
     return status
+
+
+@dataclasses.dataclass
+class SampleOut:
+    """What rl_sample writes (include/rlhead.h, rl_sample_args).  The support rows are the
+    head's CSR: HeadBatch takes offsets, ids[:nnz], support_logq[:nnz] and replayed as they are."""
+    tokens: torch.Tensor                     # [N, K] int32
+    logq: torch.Tensor                       # [N, K] fp32
+    offsets: Optional[torch.Tensor]          # [N+1] int64
+    ids: Optional[torch.Tensor]              # [capacity] int32
+    support_logq: Optional[torch.Tensor]     # [capacity] fp32
+    replayed: torch.Tensor                   # [N] uint8
+    ws: torch.Tensor
+    status: torch.Tensor
+
+    def status_bits(self) -> int:
+        return int(self.status.item())
+
+    def nnz(self) -> int:
+        """Support entries (a device read): more than the buffers hold if CAPACITY is set."""
+        return int(self.offsets[-1].item())
+
+
+def rl_sample_workspace_bytes(N: int, V: int, K: int) -> int:
+    return int(_rh().load().rl_sample_workspace_bytes(N, V, K))
+
+
+def rl_sample(logits, u, *, temperature=None, top_k=None, top_p=None, min_p=None, capacity: int = 0,
+              out: Optional[SampleOut] = None, ws=None, status=None, stream=None) -> SampleOut:
+    """K draws a row (u [N, K] in [0, 1)) from logits [N, V] (fp32, bf16 or fp16; any row
+    stride) under each row's temperature, top-k, top-p and min-p ([N] tensors or None), with
+    the log-probability of each draw under the truncated distribution.  capacity > 0 also
+    writes the sampler support rows, up to that many entries."""
+    f32, i32 = torch.float32, torch.int32
+    if not logits.is_cuda or logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise _err("logits: expected a device tensor [N, V] with dense rows")
+    N, V = logits.shape
+    if u.dim() != 2 or u.shape[0] != N:
+        raise _err(f"u: expected [{N}, K]")
+    K = u.shape[1]
+    if out is None:
+        dev = logits.device
+        e = lambda n, dt: torch.empty(n, dtype=dt, device=dev)  # noqa: E731
+        if ws is None:   # zeroed once: every call leaves its counter at zero
+            ws = torch.zeros(max(rl_sample_workspace_bytes(N, V, K), 1), dtype=torch.uint8, device=dev)
+        out = SampleOut(e((N, K), i32), e((N, K), f32), e(N + 1, torch.int64) if capacity else None,
+                        torch.zeros(capacity, dtype=i32, device=dev) if capacity else None,
+                        torch.zeros(capacity, dtype=f32, device=dev) if capacity else None, e(N, torch.uint8), ws,
+                        _status(status, dev))
+    elif status is not None or ws is not None:
+        out = dataclasses.replace(out, status=out.status if status is None else status, ws=out.ws if ws is None else ws)
+    a = RlSampleArgs(logits.data_ptr(), N, V, logits.stride(0) if N > 1 else V, _DTYPES.get(logits.dtype, -1), K,
+                     _dev("temperature", temperature, f32, N, True), _dev("top_k", top_k, i32, N, True),
+                     _dev("top_p", top_p, f32, N, True), _dev("min_p", min_p, f32, N, True), _dev("u", u, f32, N * K),
+                     _dev("out.tokens", out.tokens, i32, N * K), _dev("out.logq", out.logq, f32, N * K, True),
+                     _dev("out.offsets", out.offsets, torch.int64, N + 1, True),
+                     _dev("out.ids", out.ids, i32, capacity, True),
+                     _dev("out.support_logq", out.support_logq, f32, capacity, True), capacity,
+                     _dev("out.replayed", out.replayed, torch.uint8, N, True))
+    _call("rl_sample", ctypes.byref(a), _dev("ws", out.ws, torch.uint8), out.ws.numel(),
+          _dev("status", out.status, i32, 1), stream=stream)
+    return out

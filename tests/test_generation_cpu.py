@@ -78,3 +78,19 @@ def test_binding_refuses_host_tensors_and_wrong_types():
         rh.rl_kv_append(k, k, torch.zeros(3, dtype=torch.int64), cache, cache)
     with pytest.raises(rh.RLHeadError):
         rh.rl_kv_append(k, k, torch.zeros(3, dtype=torch.int64), cache, cache[:, :, :8])
+
+
+def test_sample_refusals(lib):
+    def make(**kw):
+        return _fill(gen.RlSampleArgs, **{**dict(N=4, V=1000, row_stride=1000, dtype=rh.RL_DTYPE_F32, K=2, capacity=10), **kw})
+    arg, uns = rh.RL_ERR_ARG, rh.RL_ERR_UNSUPPORTED
+    _refused(lib, "rl_sample", make, [
+        (dict(N=-1), arg), (dict(V=0), arg), (dict(K=0), arg), (dict(capacity=-1), arg), (dict(K=1025), uns),
+        (dict(V=(1 << 20) + 1, row_stride=1 << 21), uns), (dict(dtype=3), uns), (dict(row_stride=999), arg),
+        (dict(logits=None), arg), (dict(u=None), arg), (dict(tokens=None), arg), (dict(ids=None), arg),
+        (dict(support_logq=None), arg), (dict(logits=FAKE + 2), arg)], tail=(FAKE, 1 << 30))
+    a = make()
+    assert lib.rl_sample(ctypes.byref(a), FAKE, 64, FAKE, None) == rh.RL_ERR_WORKSPACE
+    assert lib.rl_sample(ctypes.byref(a), None, 1 << 30, FAKE, None) == rh.RL_ERR_ARG
+    assert rh.rl_sample_workspace_bytes(4, 1000, 2) > 0 and rh.rl_sample_workspace_bytes(4, 1 << 21, 2) == 0
+    assert ctypes.sizeof(gen.RlSampleArgs) == 17 * 8
