@@ -553,6 +553,41 @@ typedef struct rl_kv_append_args {
 } rl_kv_append_args;
 int rl_kv_append(const rl_kv_append_args* args, int32_t* dev_status, void* stream);
 
+/* out[t] = sum_j softmax_j(scale q_t . k_j) v_j: token i of request r's q_len step tokens
+ * (rows cu_q[r] .. cu_q[r+1]) sees its group's whole prefix and its own keys
+ * 0 .. kv_lens[r] - q_len + i.  Query head h reads key head h / (Hq / Hkv).  A group's prefix
+ * is read once for all the queries of the group.  Scores, softmax statistics and sums in
+ * fp32; the weights are rounded to the cache's type for the second product.  A row that sees
+ * no key gets out = 0 and lse = -inf, as do rows past cu_q[R].  What the pages hold past a
+ * length (never written entries, NaN included) does not reach the results; a key or value
+ * inside a length that is not finite may reach every row of its request's step.
+ * cu_q that decreases or leaves [0, T], kv_lens[r] < q_len, or a length above its bound sets
+ * RL_STATUS_LENGTHS; a page id outside the cache sets RL_STATUS_PAGE_ID; the rows concerned
+ * then hold no useful value. */
+typedef struct rl_prefix_attn_args {
+    const void* q;                  /* device [T, Hq, D], strides in elements, 16-byte aligned rows */
+    int64_t q_stride_t, q_stride_h;
+    const void *k_cache, *v_cache;  /* device [n_pages, Hkv, page_size, D] */
+    int64_t n_pages;
+    int64_t T, R, G;
+    const int32_t* cu_q;            /* device [R+1] */
+    const int32_t* kv_lens;         /* device [R] own keys, the step's included */
+    const int32_t* block_table;     /* device [R, table_width] */
+    int64_t table_width;
+    const int32_t* group_offsets;   /* device [G+1]; NULL (with G = 0): no shared prefixes */
+    const int32_t* prefix_lens;     /* device [G] */
+    const int32_t* prefix_table;    /* device [G, prefix_width] */
+    int64_t prefix_width;
+    int64_t max_q, max_kv, max_prefix;   /* host bounds on q_len, kv_lens, prefix_lens */
+    int32_t Hq, Hkv, D, page_size, dtype;   /* D 64 or 128; page_size 16, 32, 64, 128; bf16 / fp16 */
+    float scale;
+    void* out;                      /* device [T, Hq, D] dense */
+    float* lse;                     /* device [T, Hq] natural log of the sum; NULL to skip */
+} rl_prefix_attn_args;
+/* Depends on sizes and bounds only, not on the pointers. */
+size_t rl_prefix_attn_workspace_bytes(const rl_prefix_attn_args* args);
+int rl_prefix_attn(const rl_prefix_attn_args* args, void* ws, size_t ws_bytes, int32_t* dev_status, void* stream);
+
 /* Sampling from logits, K draws a row.  With z the row's logits and T its temperature,
  * x = (z - max z) / T and w = e^x:
  *   candidates   the top_k largest logits (ties: the lower index first) with w >= min_p and

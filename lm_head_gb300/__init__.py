@@ -135,8 +135,9 @@ class RlRcNamed(ctypes.Structure):
 
 
 from .generation import (  # noqa: E402
-    RL_DTYPE_BF16, RL_DTYPE_F16, RL_DTYPE_F32, PagePlan, RlKvAppendArgs, RlPagePlanArgs, RlSampleArgs,
-    SampleOut, rl_kv_append, rl_page_plan, rl_sample, rl_sample_workspace_bytes)
+    RL_DTYPE_BF16, RL_DTYPE_F16, RL_DTYPE_F32, AttnOut, PagePlan, RlKvAppendArgs, RlPagePlanArgs,
+    RlPrefixAttnArgs, RlSampleArgs,
+    SampleOut, rl_kv_append, rl_page_plan, rl_prefix_attn, rl_sample, rl_sample_workspace_bytes)
 from . import generation as _generation  # noqa: E402
 
 _lib = None

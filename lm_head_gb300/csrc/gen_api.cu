@@ -28,6 +28,23 @@ bool page_size_ok(int32_t p) { return p == 16 || p == 32 || p == 64 || p == 128;
 constexpr int64_t kMaxVocab = int64_t(1) << 20;
 constexpr int64_t kMax31 = int64_t(1) << 31;
 
+int check_attn_sizes(const rl_prefix_attn_args* a) {
+    if (!a) return fail(RL_ERR_ARG, "args is NULL");
+    if (a->T < 0 || a->R < 0 || a->G < 0 || a->n_pages < 0 || a->table_width < 0 || a->prefix_width < 0 || a->max_q < 0 ||
+        a->max_kv < 0 || a->max_prefix < 0)
+        return fail(RL_ERR_ARG, "negative size");
+    if (a->Hkv <= 0 || a->Hq <= 0 || a->Hq % a->Hkv != 0) return fail(RL_ERR_ARG, "Hq must be a positive multiple of Hkv");
+    if (a->D != 64 && a->D != 128) return fail(RL_ERR_UNSUPPORTED, "D must be 64 or 128");
+    if (!page_size_ok(a->page_size)) return fail(RL_ERR_UNSUPPORTED, "page_size must be 16, 32, 64 or 128");
+    if (a->dtype != RL_DTYPE_BF16 && a->dtype != RL_DTYPE_F16) return fail(RL_ERR_UNSUPPORTED, "dtype must be bf16 or fp16");
+    if (a->T >= kMax31 || a->R >= kMax31 || a->G >= kMax31 || a->Hq > 4096 || a->T * a->Hq >= kMax31 || a->n_pages >= kMax31 ||
+        a->n_pages * a->Hkv * a->page_size >= kMax31 || a->max_q >= kMax31 || a->max_kv >= kMax31 || a->max_prefix >= kMax31)
+        return fail(RL_ERR_UNSUPPORTED, "sizes too large (rows of queries and rows of the cache below 2^31)");
+    if (a->T > 0 && a->R > 0 && a->max_q < 1) return fail(RL_ERR_ARG, "max_q must bound the step's lengths");
+    if (!std::isfinite(a->scale)) return fail(RL_ERR_ARG, "scale is not finite");
+    return RL_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -62,6 +79,32 @@ int rl_kv_append(const rl_kv_append_args* a, int32_t* dev_status, void* stream) 
     if (!aligned(a->k_cache, 16) || !aligned(a->v_cache, 16)) return fail(RL_ERR_ARG, "cache not 16-byte aligned");
     int rc = check_device();
     return rc != RL_OK ? rc : kv_append_impl(a, dev_status, static_cast<cudaStream_t>(stream));
+}
+
+size_t rl_prefix_attn_workspace_bytes(const rl_prefix_attn_args* a) {
+    if (check_attn_sizes(a) != RL_OK) return 0;
+    return prefix_attn_ws_bytes(a);
+}
+
+int rl_prefix_attn(const rl_prefix_attn_args* a, void* ws, size_t ws_bytes, int32_t* dev_status, void* stream) {
+    int rc = check_attn_sizes(a);
+    if (rc != RL_OK) return rc;
+    if (!dev_status) return fail(RL_ERR_ARG, "dev_status is NULL");
+    if (a->T > 0) {
+        if (!a->q || !a->out || !a->cu_q) return fail(RL_ERR_ARG, "q/out/cu_q is NULL");
+        if (a->R > 0 && (!a->kv_lens || (a->table_width > 0 && !a->block_table))) return fail(RL_ERR_ARG, "kv_lens/block_table is NULL");
+        if (a->G > 0 && (!a->group_offsets || !a->prefix_lens || (a->prefix_width > 0 && !a->prefix_table)))
+            return fail(RL_ERR_ARG, "group_offsets/prefix_lens/prefix_table NULL with G > 0");
+        if (!a->k_cache || !a->v_cache || a->n_pages == 0) return fail(RL_ERR_ARG, "the cache is missing");
+        if (!aligned(a->k_cache, 16) || !aligned(a->v_cache, 16) || !aligned(a->out, 16)) return fail(RL_ERR_ARG, "cache/out not 16-byte aligned");
+        if (!aligned(a->q, 16) || a->q_stride_t % 8 != 0 || a->q_stride_h % 8 != 0)
+            return fail(RL_ERR_ARG, "q rows not 16-byte aligned");
+        const size_t need = prefix_attn_ws_bytes(a);
+        if (ws_bytes < need) return fail(RL_ERR_WORKSPACE, "attention workspace too small");
+        if (need > 0 && (!ws || !aligned(ws, 16))) return fail(RL_ERR_ARG, "ws is NULL or not 16-byte aligned");
+    }
+    rc = check_device();
+    return rc != RL_OK ? rc : prefix_attn_impl(a, ws, dev_status, static_cast<cudaStream_t>(stream));
 }
 
 size_t rl_sample_workspace_bytes(int64_t N, int64_t V, int32_t K) {

@@ -173,6 +173,8 @@ int gemm_util_impl(const void* A, int a_mn, const void* B, int b_mn, int64_t M, 
                    float* D, int32_t* status, cudaStream_t stream);
 // generation path
 int page_plan_impl(const rl_page_plan_args* a, int32_t* status, cudaStream_t stream);
+size_t prefix_attn_ws_bytes(const rl_prefix_attn_args* a);
+int prefix_attn_impl(const rl_prefix_attn_args* a, void* ws, int32_t* status, cudaStream_t stream);
 size_t sample_ws_bytes(int64_t N, int64_t V);
 int sample_impl(const rl_sample_args* a, void* ws, int32_t* status, cudaStream_t stream);
 int kv_append_impl(const rl_kv_append_args* a, int32_t* status, cudaStream_t stream);

@@ -32,6 +32,15 @@ class RlKvAppendArgs(ctypes.Structure):
                 ("n_pages", _I64), ("Hkv", _I32), ("D", _I32), ("page_size", _I32), ("dtype", _I32)]
 
 
+class RlPrefixAttnArgs(ctypes.Structure):
+    _fields_ = [("q", _P), ("q_stride_t", _I64), ("q_stride_h", _I64), ("k_cache", _P), ("v_cache", _P),
+                ("n_pages", _I64), ("T", _I64), ("R", _I64), ("G", _I64), ("cu_q", _P), ("kv_lens", _P),
+                ("block_table", _P), ("table_width", _I64), ("group_offsets", _P), ("prefix_lens", _P),
+                ("prefix_table", _P), ("prefix_width", _I64), ("max_q", _I64), ("max_kv", _I64), ("max_prefix", _I64),
+                ("Hq", _I32), ("Hkv", _I32), ("D", _I32), ("page_size", _I32), ("dtype", _I32), ("scale", _F),
+                ("out", _P), ("lse", _P)]
+
+
 class RlSampleArgs(ctypes.Structure):
     _fields_ = [("logits", _P), ("N", _I64), ("V", _I64), ("row_stride", _I64), ("dtype", _I32), ("K", _I32),
                 ("temperature", _P), ("top_k", _P), ("top_p", _P), ("min_p", _P), ("u", _P), ("tokens", _P),
@@ -42,6 +51,8 @@ class RlSampleArgs(ctypes.Structure):
 SIGS = {
     "rl_page_plan": (ctypes.c_int, [_P, _P, _P]),
     "rl_kv_append": (ctypes.c_int, [_P, _P, _P]),
+    "rl_prefix_attn_workspace_bytes": (ctypes.c_size_t, [_P]),
+    "rl_prefix_attn": (ctypes.c_int, [_P, _P, ctypes.c_size_t, _P, _P]),
     "rl_sample_workspace_bytes": (ctypes.c_size_t, [_I64, _I64, _I32]),
     "rl_sample": (ctypes.c_int, [_P, _P, ctypes.c_size_t, _P, _P]),
 }
@@ -147,6 +158,59 @@ def rl_kv_append(k, v, slot_map, k_cache, v_cache, *, status=None, stream=None) 
                        _dev("slot_map", slot_map, torch.int64, T), kc, vc, T, n_pages, Hkv, D, page, dt)
     _call("rl_kv_append", ctypes.byref(a), _dev("status", status, torch.int32, 1), stream=stream)
     return status
+
+
+@dataclasses.dataclass
+class AttnOut:
+    out: torch.Tensor           # [T, Hq, D], the cache's type
+    lse: Optional[torch.Tensor]  # [T, Hq] fp32
+    ws: torch.Tensor
+    status: torch.Tensor
+
+    def status_bits(self) -> int:
+        return int(self.status.item())
+
+
+def rl_prefix_attn(q, k_cache, v_cache, cu_q, kv_lens, block_table, *, max_q: int, max_kv: int, group_offsets=None,
+                   prefix_lens=None, prefix_table=None, max_prefix: int = 0, scale: Optional[float] = None,
+                   out: Optional[AttnOut] = None, ws=None, status=None, stream=None) -> AttnOut:
+    """Attention of a step's queries q [T, Hq, D] (any token and head strides) over their
+    group's shared prefix and each request's own keys, causal within the step.  max_q, max_kv
+    and max_prefix bound the device lengths.  scale: 1 / sqrt(D) by default."""
+    rh = _rh()
+    kc, vc, dt = _cache(k_cache, v_cache)
+    n_pages, Hkv, page, D = k_cache.shape
+    if not q.is_cuda or q.dim() != 3 or q.dtype != k_cache.dtype or q.shape[2] != D or q.stride(2) != 1:
+        raise _err(f"q: expected a device tensor [T, Hq, {D}] of the cache's type with dense heads")
+    T, Hq, _ = q.shape
+    i32 = torch.int32
+    R, W = block_table.shape
+    G = 0 if group_offsets is None else group_offsets.numel() - 1
+    WP = 0
+    if G:
+        if prefix_table is None or prefix_table.dim() != 2 or prefix_table.shape[0] != G:
+            raise _err(f"prefix_table: expected [{G}, pages]")
+        WP = prefix_table.shape[1]
+    a = RlPrefixAttnArgs(q.data_ptr(), q.stride(0), q.stride(1), kc, vc, n_pages, T, R, G, _dev("cu_q", cu_q, i32, R + 1),
+                         _dev("kv_lens", kv_lens, i32, R), _dev("block_table", block_table, i32), W,
+                         _dev("group_offsets", group_offsets, i32, None, True),
+                         _dev("prefix_lens", prefix_lens, i32, G, G == 0),
+                         _dev("prefix_table", prefix_table, i32, None, G == 0), WP, max_q, max_kv, max_prefix, Hq, Hkv, D,
+                         page, dt, D ** -0.5 if scale is None else scale)
+    if out is None:
+        dev = q.device
+        if ws is None:
+            n = int(rh.load().rl_prefix_attn_workspace_bytes(ctypes.byref(a)))
+            ws = torch.empty(max(n, 1), dtype=torch.uint8, device=dev)
+        out = AttnOut(torch.empty(T, Hq, D, dtype=q.dtype, device=dev), torch.empty(T, Hq, dtype=torch.float32, device=dev),
+                      ws, _status(status, dev))
+    elif status is not None or ws is not None:
+        out = dataclasses.replace(out, status=out.status if status is None else status, ws=out.ws if ws is None else ws)
+    a.out = _dev("out.out", out.out, q.dtype, T * Hq * D)
+    a.lse = _dev("out.lse", out.lse, torch.float32, T * Hq, True)
+    _call("rl_prefix_attn", ctypes.byref(a), _dev("ws", out.ws, torch.uint8), out.ws.numel(),
+          _dev("status", out.status, i32, 1), stream=stream)
+    return out
 
 
 @dataclasses.dataclass

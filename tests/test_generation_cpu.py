@@ -94,3 +94,25 @@ def test_sample_refusals(lib):
     assert lib.rl_sample(ctypes.byref(a), None, 1 << 30, FAKE, None) == rh.RL_ERR_ARG
     assert rh.rl_sample_workspace_bytes(4, 1000, 2) > 0 and rh.rl_sample_workspace_bytes(4, 1 << 21, 2) == 0
     assert ctypes.sizeof(gen.RlSampleArgs) == 17 * 8
+
+
+def test_prefix_attn_refusals(lib):
+    def make(**kw):
+        return _fill(gen.RlPrefixAttnArgs, **{**dict(q_stride_t=256, q_stride_h=64, n_pages=8, T=4, R=2, G=1, table_width=2,
+                                                     prefix_width=2, max_q=2, max_kv=32, max_prefix=32, Hq=4, Hkv=2, D=64,
+                                                     page_size=16, dtype=rh.RL_DTYPE_BF16, scale=0.1), **kw})
+    arg, uns = rh.RL_ERR_ARG, rh.RL_ERR_UNSUPPORTED
+    _refused(lib, "rl_prefix_attn", make, [
+        (dict(T=-1), arg), (dict(R=-1), arg), (dict(G=-1), arg), (dict(max_kv=-1), arg), (dict(max_prefix=-1), arg),
+        (dict(Hq=3), arg), (dict(Hkv=0), arg), (dict(D=96), uns), (dict(page_size=48), uns), (dict(dtype=0), uns),
+        (dict(T=1 << 30), uns), (dict(n_pages=1 << 27), uns), (dict(max_q=0), arg), (dict(scale=float("nan")), arg),
+        (dict(q=None), arg), (dict(out=None), arg), (dict(cu_q=None), arg), (dict(kv_lens=None), arg),
+        (dict(block_table=None), arg), (dict(group_offsets=None), arg), (dict(prefix_lens=None), arg),
+        (dict(prefix_table=None), arg), (dict(k_cache=None), arg), (dict(v_cache=FAKE + 2), arg), (dict(q=FAKE + 2), arg),
+        (dict(q_stride_t=255), arg), (dict(q_stride_h=60), arg), (dict(n_pages=0), arg)], tail=(FAKE, 1 << 40))
+    a = make()
+    assert lib.rl_prefix_attn(ctypes.byref(a), FAKE, 16, FAKE, None) == rh.RL_ERR_WORKSPACE
+    assert lib.rl_prefix_attn(ctypes.byref(a), None, 1 << 40, FAKE, None) == rh.RL_ERR_ARG
+    bad = make(D=96)
+    assert lib.rl_prefix_attn_workspace_bytes(ctypes.byref(bad)) == 0
+    assert ctypes.sizeof(gen.RlPrefixAttnArgs) == 22 * 8 + 6 * 4
