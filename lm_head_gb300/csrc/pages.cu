@@ -3,7 +3,8 @@
 //  page_plan_kernel   one launch: every block covers a stretch of the step's tokens, and scans
 //                     the requests' lengths (tiles of 2048 in shared memory) up to the end of its
 //                     stretch; block b also writes the per-request outputs of tiles b,
-//                     b + grid, ...  No second launch, no block waits for another.
+//                     b + grid, ...  A new page's table entry is written with the first token in it
+//                     (every new page has one).  No second launch, no block waits for another.
 //  kv_append_kernel   16 bytes a thread and step, four loads in flight.
 #include <climits>
 
@@ -15,6 +16,7 @@ namespace rl {
 constexpr int kPlanThreads = 256;
 constexpr int kPlanItems = 8;                           // consecutive requests of one thread
 constexpr int kPlanTile = kPlanThreads * kPlanItems;
+constexpr int kPlanGroups = 1024;
 
 // Exclusive block scan of two 64-bit sums; returns the thread's prefix, totals in (ta, tb).
 struct Scan2 {
@@ -64,12 +66,23 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanArgs 
     // cached tokens; its prefix length
     __shared__ int s_q[kPlanTile + 1], s_n[kPlanTile + 1], s_ctx[kPlanTile], s_pre[kPlanTile];
     __shared__ long long warp_a[kPlanThreads / 32], warp_b[kPlanThreads / 32];
+    __shared__ int s_go[kPlanGroups + 1], s_pl[kPlanGroups];     // the groups, where they fit
     const rl_page_plan_args& a = p.a;
+    const bool grouped = a.group_offsets && a.G > 0 && a.positions;
+    const bool go_shared = grouped && a.G <= kPlanGroups;
+    if (go_shared)
+        for (int i = threadIdx.x; i <= a.G; i += kPlanThreads) {
+            s_go[i] = a.group_offsets[i];
+            if (i < a.G) s_pl[i] = a.prefix_lens[i];
+        }
+    const int* go = go_shared ? s_go : a.group_offsets;
+    const int* pl = go_shared ? s_pl : a.prefix_lens;            // read after the scan's barriers
     const long long used = a.free_used ? max(*a.free_used, 0) : 0;
     const long long W = a.table_width;
     const int mask = a.page_size - 1;
     const long long t0 = min(blockIdx.x * p.tokens_per_block, static_cast<long long>(a.T));
-    const long long t1 = min(t0 + p.tokens_per_block, static_cast<long long>(a.T));
+    // the last block goes on past T, for the table entries of tokens that the step leaves out
+    const long long t1 = blockIdx.x == gridDim.x - 1 ? LLONG_MAX : t0 + p.tokens_per_block;
     const long long tiles = (a.R + kPlanTile - 1) / kPlanTile;
     long long cu = 0, pages = 0;             // tokens and new pages before this tile
     int bits = 0;
@@ -139,17 +152,15 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanArgs 
             // tile-relative sums past 2^31 are cut there: they lie past T, which is below it
             long long iq = s.a, in = s.b;
             int g = 0;
-            bool grouped = false;
-            if (a.group_offsets && a.G > 0 && a.positions) {
+            if (grouped && tokens) {
                 const long long r = r0 + threadIdx.x * kPlanItems;
                 int lo = 0, hi = static_cast<int>(a.G);   // first g with group_offsets[g + 1] > r
                 while (lo < hi) {
                     const int mid = (lo + hi) >> 1;
-                    if (a.group_offsets[mid + 1] > r) hi = mid;
+                    if (go[mid + 1] > r) hi = mid;
                     else lo = mid + 1;
                 }
                 g = lo;
-                grouped = true;
             }
 #pragma unroll
             for (int k = 0; k < kPlanItems; ++k) {
@@ -158,9 +169,9 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanArgs 
                 s_n[i] = static_cast<int>(min(in, static_cast<long long>(INT_MAX)));
                 s_ctx[i] = ctx[k];
                 int pre = 0;
-                if (grouped && i < n) {
-                    while (g < a.G && a.group_offsets[g + 1] <= r0 + i) ++g;
-                    if (g < a.G && a.group_offsets[g] <= r0 + i) pre = max(a.prefix_lens[g], 0);
+                if (grouped && tokens && i < n) {
+                    while (g < a.G && go[g + 1] <= r0 + i) ++g;
+                    if (g < a.G && go[g] <= r0 + i) pre = max(pl[g], 0);
                 }
                 s_pre[i] = pre;
                 iq += q[k];
@@ -176,21 +187,6 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanArgs 
                 s_n[kPlanTile] = static_cast<int>(min(in, static_cast<long long>(INT_MAX)));
             }
             __syncthreads();
-        }
-        if (mine) {
-            // the tile's new table entries, one page a thread and step
-            for (long long j = threadIdx.x; j < tn; j += kPlanThreads) {
-                int lo = 0, hi = n;                        // last i with s_n[i] <= j
-                while (hi - lo > 1) {
-                    const int mid = (lo + hi) >> 1;
-                    if (s_n[mid] <= j) lo = mid;
-                    else hi = mid;
-                }
-                const long long had = min((static_cast<long long>(s_ctx[lo]) + mask) >> p.shift, W);
-                const long long pi = had + (j - s_n[lo]);
-                const int page = page_at(r0 + lo, lo, pi);
-                a.block_table[(r0 + lo) * W + pi] = page;
-            }
         }
         if (tokens) {
             const long long b0 = max(t0, cu), b1 = min(t1, cu + tq);
@@ -219,10 +215,12 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanArgs 
                         page_r = lo;
                         page_i = pi;
                     }
+                    // the first token of a new page writes its entry
+                    if ((at & mask) == 0 && pi < W) a.block_table[(r0 + lo) * W + pi] = page;
                     slot[k] = page < 0 ? -1 : (static_cast<long long>(page) << p.shift) + (at & mask);
                     pos[k] = static_cast<int>(min(at + s_pre[lo], static_cast<long long>(INT_MAX)));
                 }
-                const bool whole = ta == t && tb == t + 4;
+                const bool whole = ta == t && tb == t + 4 && tb <= a.T;
                 if (whole && (reinterpret_cast<uintptr_t>(a.slot_map) & 15) == 0) {
                     longlong2* d = reinterpret_cast<longlong2*>(a.slot_map + t);
                     d[0] = make_longlong2(slot[0], slot[1]);
@@ -230,7 +228,7 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanArgs 
                 } else {
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        if (t + k >= ta && t + k < tb) a.slot_map[t + k] = slot[k];
+                        if (t + k >= ta && t + k < min(tb, static_cast<long long>(a.T))) a.slot_map[t + k] = slot[k];
                 }
                 if (a.positions) {
                     if (whole && (reinterpret_cast<uintptr_t>(a.positions) & 15) == 0) {
@@ -238,7 +236,7 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanArgs 
                     } else {
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            if (t + k >= ta && t + k < tb) a.positions[t + k] = pos[k];
+                            if (t + k >= ta && t + k < min(tb, static_cast<long long>(a.T))) a.positions[t + k] = pos[k];
                     }
                 }
             }
@@ -252,7 +250,7 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanArgs 
                 if (cu != a.T) bits |= RL_STATUS_LENGTHS;
             }
             // tokens that no request has
-            for (long long t = max(t0, cu) + threadIdx.x; t < t1; t += kPlanThreads) {
+            for (long long t = max(t0, cu) + threadIdx.x; t < min(t1, static_cast<long long>(a.T)); t += kPlanThreads) {
                 a.slot_map[t] = -1;
                 if (a.positions) a.positions[t] = -1;
             }
@@ -264,7 +262,7 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanArgs 
         if (a.T != 0) bits |= RL_STATUS_LENGTHS;
     }
     if (tiles == 0)
-        for (long long t = t0 + threadIdx.x; t < t1; t += kPlanThreads) {
+        for (long long t = t0 + threadIdx.x; t < min(t1, static_cast<long long>(a.T)); t += kPlanThreads) {
             a.slot_map[t] = -1;
             if (a.positions) a.positions[t] = -1;
         }

@@ -10,6 +10,8 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import struct
+import sys
 from typing import Optional
 
 import torch
@@ -58,30 +60,56 @@ SIGS = {
 }
 
 
-def _rh():
-    import lm_head_gb300
-    return lm_head_gb300
+def _packer(cls):
+    """The C struct's bytes from the field values (None: a null pointer), several times faster
+    than filling the ctypes structure."""
+    code = {_P: "P", _I64: "q", _I32: "i", _F: "f"}
+    fmt = struct.Struct("@" + "".join(code[t] for _, t in cls._fields_) + "0q")
+    assert fmt.size == ctypes.sizeof(cls)
+    return fmt.pack
+
+
+_pack_plan, _pack_append, _pack_attn, _pack_sample = (
+    _packer(c) for c in (RlPagePlanArgs, RlKvAppendArgs, RlPrefixAttnArgs, RlSampleArgs))
 
 
 def _err(msg):
-    return _rh().RLHeadError(msg)
+    return sys.modules["lm_head_gb300"].RLHeadError(msg)
 
 
-def _call(name, *args, stream=None):
-    rh = _rh()
-    s = torch.cuda.current_stream() if stream is None else stream
-    rh._check(getattr(rh.load(), name)(*args, s.cuda_stream))
+_lib = None
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _load():
+    global _lib
+    if _lib is None:
+        _lib = sys.modules["lm_head_gb300"].load()
+    return _lib
+
+
+def _stream(stream, t):
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None:
+        return _raw_stream(t.device.index)
+    return torch.cuda.current_stream(t.device).cuda_stream
+
+
+def _check(rc):
+    if rc:
+        sys.modules["lm_head_gb300"]._check(rc)
 
 
 def _dev(name, t, dtype, n=None, optional=False):
-    """Device address of a contiguous tensor of `dtype` (and `n` elements)."""
+    """Device address of a contiguous tensor of `dtype` (and `n` elements); 0 for none."""
     if t is None:
         if optional:
-            return None
+            return 0
         raise _err(f"{name} is missing")
     if not t.is_cuda:
         raise _err(f"{name}: librlhead takes device tensors; got a CPU tensor")
-    if t.dtype != dtype or not t.is_contiguous():
+    if t.dtype is not dtype or not t.is_contiguous():
         raise _err(f"{name}: expected contiguous {dtype}, got {t.dtype}")
     if n is not None and t.numel() != n:
         raise _err(f"{name}: expected {n} elements, got {t.numel()}")
@@ -124,7 +152,7 @@ def rl_page_plan(q_lens, ctx_lens, block_table, free_pages, *, page_size: int, n
     elif status is not None:
         out = dataclasses.replace(out, status=status)
     G = 0 if group_offsets is None else group_offsets.numel() - 1
-    a = RlPagePlanArgs(R, n_tokens, _dev("q_lens", q_lens, i32, R), _dev("ctx_lens", ctx_lens, i32, R),
+    a = _pack_plan(R, n_tokens, _dev("q_lens", q_lens, i32, R), _dev("ctx_lens", ctx_lens, i32, R),
                        _dev("block_table", block_table, i32), W, _dev("free_pages", free_pages, i32),
                        free_pages.numel(), _dev("free_used", free_used, i32, 1, True),
                        _dev("out.free_used", out.free_used, i32, 1),
@@ -133,7 +161,7 @@ def rl_page_plan(q_lens, ctx_lens, block_table, free_pages, *, page_size: int, n
                        _dev("out.cu_q", out.cu_q, i32, R + 1), _dev("out.kv_lens", out.kv_lens, i32, R),
                        _dev("out.slot_map", out.slot_map, torch.int64, n_tokens),
                        _dev("out.positions", out.positions, i32, n_tokens, True))
-    _call("rl_page_plan", ctypes.byref(a), _dev("status", out.status, i32, 1), stream=stream)
+    _check(_load().rl_page_plan(a, _dev("status", out.status, i32, 1), _stream(stream, block_table)))
     return out
 
 
@@ -154,9 +182,9 @@ def rl_kv_append(k, v, slot_map, k_cache, v_cache, *, status=None, stream=None) 
         if not t.is_cuda or t.dtype != k_cache.dtype or tuple(t.shape) != (T, Hkv, D) or (D > 1 and t.stride(2) != 1):
             raise _err(f"{name}: expected a device tensor [{T}, {Hkv}, {D}] of the cache's type with dense heads")
     status = _status(status, k_cache.device)
-    a = RlKvAppendArgs(k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1), v.stride(0), v.stride(1),
+    a = _pack_append(k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1), v.stride(0), v.stride(1),
                        _dev("slot_map", slot_map, torch.int64, T), kc, vc, T, n_pages, Hkv, D, page, dt)
-    _call("rl_kv_append", ctypes.byref(a), _dev("status", status, torch.int32, 1), stream=stream)
+    _check(_load().rl_kv_append(a, _dev("status", status, torch.int32, 1), _stream(stream, k_cache)))
     return status
 
 
@@ -177,7 +205,6 @@ def rl_prefix_attn(q, k_cache, v_cache, cu_q, kv_lens, block_table, *, max_q: in
     """Attention of a step's queries q [T, Hq, D] (any token and head strides) over their
     group's shared prefix and each request's own keys, causal within the step.  max_q, max_kv
     and max_prefix bound the device lengths.  scale: 1 / sqrt(D) by default."""
-    rh = _rh()
     kc, vc, dt = _cache(k_cache, v_cache)
     n_pages, Hkv, page, D = k_cache.shape
     if not q.is_cuda or q.dim() != 3 or q.dtype != k_cache.dtype or q.shape[2] != D or q.stride(2) != 1:
@@ -191,25 +218,24 @@ def rl_prefix_attn(q, k_cache, v_cache, cu_q, kv_lens, block_table, *, max_q: in
         if prefix_table is None or prefix_table.dim() != 2 or prefix_table.shape[0] != G:
             raise _err(f"prefix_table: expected [{G}, pages]")
         WP = prefix_table.shape[1]
-    a = RlPrefixAttnArgs(q.data_ptr(), q.stride(0), q.stride(1), kc, vc, n_pages, T, R, G, _dev("cu_q", cu_q, i32, R + 1),
-                         _dev("kv_lens", kv_lens, i32, R), _dev("block_table", block_table, i32), W,
-                         _dev("group_offsets", group_offsets, i32, None, True),
-                         _dev("prefix_lens", prefix_lens, i32, G, G == 0),
-                         _dev("prefix_table", prefix_table, i32, None, G == 0), WP, max_q, max_kv, max_prefix, Hq, Hkv, D,
-                         page, dt, D ** -0.5 if scale is None else scale)
+    head = (q.data_ptr(), q.stride(0), q.stride(1), kc, vc, n_pages, T, R, G, _dev("cu_q", cu_q, i32, R + 1),
+            _dev("kv_lens", kv_lens, i32, R), _dev("block_table", block_table, i32), W,
+            _dev("group_offsets", group_offsets, i32, None, True), _dev("prefix_lens", prefix_lens, i32, G, G == 0),
+            _dev("prefix_table", prefix_table, i32, None, G == 0), WP, max_q, max_kv, max_prefix, Hq, Hkv, D, page, dt,
+            D ** -0.5 if scale is None else scale)
     if out is None:
         dev = q.device
         if ws is None:
-            n = int(rh.load().rl_prefix_attn_workspace_bytes(ctypes.byref(a)))
+            n = int(_load().rl_prefix_attn_workspace_bytes(_pack_attn(*head, 0, 0)))
             ws = torch.empty(max(n, 1), dtype=torch.uint8, device=dev)
         out = AttnOut(torch.empty(T, Hq, D, dtype=q.dtype, device=dev), torch.empty(T, Hq, dtype=torch.float32, device=dev),
                       ws, _status(status, dev))
     elif status is not None or ws is not None:
         out = dataclasses.replace(out, status=out.status if status is None else status, ws=out.ws if ws is None else ws)
-    a.out = _dev("out.out", out.out, q.dtype, T * Hq * D)
-    a.lse = _dev("out.lse", out.lse, torch.float32, T * Hq, True)
-    _call("rl_prefix_attn", ctypes.byref(a), _dev("ws", out.ws, torch.uint8), out.ws.numel(),
-          _dev("status", out.status, i32, 1), stream=stream)
+    a = _pack_attn(*head, _dev("out.out", out.out, q.dtype, T * Hq * D),
+                   _dev("out.lse", out.lse, torch.float32, T * Hq, True))
+    _check(_load().rl_prefix_attn(a, _dev("ws", out.ws, torch.uint8), out.ws.numel(),
+                                  _dev("status", out.status, i32, 1), _stream(stream, q)))
     return out
 
 
@@ -235,7 +261,7 @@ class SampleOut:
 
 
 def rl_sample_workspace_bytes(N: int, V: int, K: int) -> int:
-    return int(_rh().load().rl_sample_workspace_bytes(N, V, K))
+    return int(_load().rl_sample_workspace_bytes(N, V, K))
 
 
 def rl_sample(logits, u, *, temperature=None, top_k=None, top_p=None, min_p=None, capacity: int = 0,
@@ -262,7 +288,7 @@ def rl_sample(logits, u, *, temperature=None, top_k=None, top_p=None, min_p=None
                         _status(status, dev))
     elif status is not None or ws is not None:
         out = dataclasses.replace(out, status=out.status if status is None else status, ws=out.ws if ws is None else ws)
-    a = RlSampleArgs(logits.data_ptr(), N, V, logits.stride(0) if N > 1 else V, _DTYPES.get(logits.dtype, -1), K,
+    a = _pack_sample(logits.data_ptr(), N, V, logits.stride(0) if N > 1 else V, _DTYPES.get(logits.dtype, -1), K,
                      _dev("temperature", temperature, f32, N, True), _dev("top_k", top_k, i32, N, True),
                      _dev("top_p", top_p, f32, N, True), _dev("min_p", min_p, f32, N, True), _dev("u", u, f32, N * K),
                      _dev("out.tokens", out.tokens, i32, N * K), _dev("out.logq", out.logq, f32, N * K, True),
@@ -270,6 +296,6 @@ def rl_sample(logits, u, *, temperature=None, top_k=None, top_p=None, min_p=None
                      _dev("out.ids", out.ids, i32, capacity, True),
                      _dev("out.support_logq", out.support_logq, f32, capacity, True), capacity,
                      _dev("out.replayed", out.replayed, torch.uint8, N, True))
-    _call("rl_sample", ctypes.byref(a), _dev("ws", out.ws, torch.uint8), out.ws.numel(),
-          _dev("status", out.status, i32, 1), stream=stream)
+    _check(_load().rl_sample(a, _dev("ws", out.ws, torch.uint8), out.ws.numel(), _dev("status", out.status, i32, 1),
+                             _stream(stream, logits)))
     return out
