@@ -11,16 +11,16 @@
 // fp64 would do the same at a fiftieth of the rate on this part.
 //
 //  1. stats_kernel   one warp per 1024 logits: the largest of each 128, and where a row needs
-//                    it the sum of weights, with a reference of the chunk's own so that no
-//                    pass for the row's maximum comes first.  The only pass over all logits.
+//                    them the sums of weights of each 128, with a reference of the chunk's own so
+//                    that no pass for the row's maximum comes first.  The only pass over all logits.
 //  2. select_kernel  one block a row: the kept set as a threshold (key, index), by collecting
 //                    the candidates into shared memory and sorting them when a bound from the
 //                    128-wide maxima shows that few can matter, else after a histogram that
-//                    brackets the border; then the weights of each chunk's kept tokens, and
-//                    each draw by a search over the chunks and a scan of one chunk.
-//                    Whole rows (no cut) take the chunk sums of 1.  Sums over chunks of kept
-//                    tokens are integers (units of 2^-50): their order does not matter.
-//  3. emit_kernel    the support rows, one warp a chunk.
+//                    brackets the border; then the weight of each part's kept tokens, and each
+//                    draw by a search over the parts and a scan of one.  Whole rows (no cut)
+//                    take the sums of 1.  Sums are integers (units of 2^-50 of the largest
+//                    weight in a part, 2^-44 over parts): their order does not matter.
+//  3. emit_kernel    the support rows, one warp a part.
 #include <cfloat>
 #include <climits>
 #include <cmath>
@@ -40,29 +40,36 @@ constexpr int kListCap = 4096;             // candidates sorted in shared memory
 constexpr int kBins = 2048;
 constexpr float kWholeRef = 1900.f;        // |max * log2(e) / T| up to which a chunk needs no reference
 constexpr float kLog2eHi = 1.44269502162933349609f, kLog2eLo = 1.92596299112661746887e-8f;
-constexpr double kUnit = 1125899906842624.0;   // 2^50
 
-// 2^(i/2048), i = 0..31, as float pairs
-static __device__ __constant__ float kFine2Hi[32] = {
-    1.000000000e+00f, 1.000338554e+00f, 1.000677109e+00f, 1.001015902e+00f, 1.001354694e+00f, 1.001693726e+00f,
-    1.002032757e+00f, 1.002371907e+00f, 1.002711296e+00f, 1.003050685e+00f, 1.003390193e+00f, 1.003729939e+00f,
-    1.004069686e+00f, 1.004409552e+00f, 1.004749537e+00f, 1.005089641e+00f, 1.005429864e+00f, 1.005770206e+00f,
-    1.006110668e+00f, 1.006451249e+00f, 1.006791949e+00f, 1.007132769e+00f, 1.007473707e+00f, 1.007814765e+00f,
-    1.008155942e+00f, 1.008497119e+00f, 1.008838534e+00f, 1.009180069e+00f, 1.009521723e+00f, 1.009863377e+00f,
-    1.010205269e+00f, 1.010547161e+00f};
-static __device__ __constant__ float kFine2Lo[32] = {
-    0.000000000e+00f, -4.632964234e-08f, 2.192841819e-08f, -3.360561251e-08f, 2.552565270e-08f, -3.905755364e-08f,
-    1.110217429e-08f, 5.683439142e-08f, -2.103134022e-08f, 1.596242782e-08f, 4.864528691e-08f, -4.215315741e-08f,
-    -1.797542026e-08f, 2.008129441e-09f, 1.783642567e-08f, 2.954841349e-08f, 3.718305308e-08f, 4.077931948e-08f,
-    4.037620016e-08f, 3.601268972e-08f, 2.772780583e-08f, 1.556056972e-08f, -4.499763340e-10f, -2.026478008e-08f,
-    -4.384477847e-08f, 4.805839993e-08f, 1.706526653e-08f, -1.757578438e-08f, -5.582563389e-08f, 2.156413892e-08f,
-    -2.378589947e-08f, 4.658198804e-08f};
-
-struct ChunkStat {
-    float max;
-    int ref;            // the sum is in units of 2^ref; INT_MIN: of the weight of `max`
-    double sum;
+// Entry j: bits of the float nearest 2^(j/2048) less j << 12 (so that adding the phase's bits
+// gives the scaled value), and the relative error of that float.  Made by the compiler, by the
+// exponential series in double.
+struct ExpTable {
+    uint32_t bits[2048];
+    float rho[2048];
 };
+constexpr double exp2_series(double x) {              // 0 <= x < 1
+    const double y = x * 0.693147180559945309417;
+    double t = 1.0, s = 1.0;
+    for (int i = 1; i < 26; ++i) {
+        t *= y / i;
+        s += t;
+    }
+    return s;
+}
+constexpr ExpTable make_exp_table() {
+    ExpTable t{};
+    for (int j = 0; j < 2048; ++j) {
+        const double v = exp2_series(j / 2048.0);
+        const float h = static_cast<float>(v);        // in [1, 2): 1 + mantissa / 2^23
+        const uint32_t mant = static_cast<uint32_t>((static_cast<double>(h) - 1.0) * 8388608.0);
+        t.bits[j] = (0x3f800000u | mant) - (static_cast<uint32_t>(j) << 12);
+        t.rho[j] = static_cast<float>((v - static_cast<double>(h)) / static_cast<double>(h));
+    }
+    return t;
+}
+static __device__ const ExpTable kExpTable = make_exp_table();
+
 struct RowRec {
     float M;            // the row's largest logit
     FF inv_t;           // 1 / T
@@ -76,13 +83,14 @@ enum { kRowEmpty = 0, kRowWhole = 1, kRowCut = 2 };
 struct SampleArgs {
     rl_sample_args a;
     int32_t* status;
-    int nc, ns;              // chunks, 128-wide parts of a row
-    ChunkStat* stat;         // [N, nc]
-    float* submax;           // [N, ns]
-    int* ccnt;               // [N, nc] kept tokens of each chunk
-    int* count;              // [N] entries of the support row
-    RowRec* rec;             // [N]
-    unsigned* done;          // rows finished (back to zero at the end of a call)
+    int nc, ns;                    // chunks of 1024, parts of 128 of a row
+    float* submax;                 // [N, ns] largest logit of a part
+    unsigned long long* subsum;    // [N, ns] sum of its weights in units of 2^(ref - 50)
+    int* ref;                      // [N, nc] the chunk's ref; INT_MIN: the weight of its largest logit
+    int* cpre;                     // [N, ns] kept tokens of the parts before
+    int* count;                    // [N] entries of the support row
+    RowRec* rec;                   // [N]
+    unsigned* done;                // rows finished (back to zero at the end of a call)
 };
 
 struct Knobs {
@@ -164,13 +172,8 @@ RL_DEVINL void load4(const T* row, int i, int V, float (&z)[4], bool& bad) {
     }
 }
 
-// Table entry j: bits of 2^(j/2048) less j << 12 (so that adding the phase's bits gives the
-// scaled value), and the relative error of that float.
 RL_DEVINL void fill_table(float2* tab, int tid, int threads) {
-    for (int j = tid; j < 2048; j += threads) {
-        const FF v = ff_mul({kExp2Hi[j >> 5], kExp2Lo[j >> 5]}, {kFine2Hi[j & 31], kFine2Lo[j & 31]});
-        tab[j] = make_float2(__uint_as_float(__float_as_uint(v.hi) - (static_cast<uint32_t>(j) << 12)), v.lo / v.hi);
-    }
+    for (int j = tid; j < 2048; j += threads) tab[j] = make_float2(__uint_as_float(kExpTable.bits[j]), kExpTable.rho[j]);
 }
 // 2^(p + e - ref) as hi + v, for p - ref in [-66, 1] and magic = 6144 - ref: 6144 + x has
 // 2^-11 as its last place, so the sum's bits are 0x45C00000 + 2048 n + j.
@@ -188,6 +191,25 @@ RL_DEVINL void phase_rel(float z, float m, FF c, float& p, float& e) {
     p = __fmul_rn(d.hi, c.hi);
     e = fmaf(d.lo, c.hi, fmaf(d.hi, c.lo, fmaf(d.hi, c.hi, -p)));
 }
+// Sum of up to four weights of at most 1 in a lane: the high part on a grid of 2^-19, where such
+// sums are exact, the rest apart; a warp's total in units of 2^-50, rounded at 2^-39 a lane.
+// Both become integers through the bits of a sum with a constant of the right last place.
+struct LaneSum {
+    float top = 0.f, low = 0.f;
+    RL_DEVINL void add(float hi, float v) {
+        const float wh = __fadd_rn(hi, v), wl = __fsub_rn(v, __fsub_rn(wh, hi));
+        const float t = __fsub_rn(__fadd_rn(wh, 24.f), 24.f);
+        top += t;
+        low += __fsub_rn(wh, t);
+        low += wl;
+    }
+    RL_DEVINL unsigned long long warp_total() const {
+        const uint32_t a = __reduce_add_sync(0xffffffffu, __float_as_uint(__fadd_rn(top, 24.f)) - 0x41c00000u);
+        const int b = __reduce_add_sync(0xffffffffu, static_cast<int>(__float_as_uint(__fadd_rn(low, 0x1.8p-16f)) - 0x37c00000u));
+        const long long w = (static_cast<long long>(a) << 31) + (static_cast<long long>(b) << 11);
+        return w > 0 ? static_cast<unsigned long long>(w) : 0ull;
+    }
+};
 // The weight of z relative to M in units of 2^-50; `zlow` = M - 64 / c, at least
 // -FLT_MAX: below it the weight is 0 (M itself where the difference is lost).
 RL_DEVINL unsigned long long weight_fixed(float z, float M, FF c, float zlow, const float2* tab) {
@@ -203,6 +225,22 @@ RL_DEVINL unsigned long long weight_fixed(float z, float M, FF c, float zlow, co
     const unsigned long long w = sh >= 0 ? m << sh : (sh > -25 ? (m + (1ull << (-sh - 1))) >> -sh : 0ull);
     return w + static_cast<long long>(__float2int_rn(wl * 1125899906842624.f));
 }
+// floor(f x) for 0 <= f < 1
+RL_DEVINL unsigned long long fraction_of(float f, unsigned long long x) {
+    const uint32_t b = __float_as_uint(f);
+    const int e = static_cast<int>(b >> 23);             // f = m 2^(e - 150)
+    const unsigned long long m = (b & 0x7fffffu) | (e ? 0x800000u : 0u);
+    const int sh = e - 150 + 64;                         // m 2^sh = f 2^64 (below 2^-64 it hardly matters)
+    const unsigned long long q = sh >= 0 ? m << sh : sh > -64 ? m >> -sh : 0ull;
+    return __umul64hi(q, x);
+}
+// ln x for a positive float pair: one Newton step from the float's, to about 2^-46 absolute.
+RL_DEVINL FF ln_pair(FF x) {
+    const float y = logf(x.hi);
+    const FF r = ff_mul(x, exp_ff(-y));                  // 1 + d
+    const float d = __fadd_rn(__fsub_rn(r.hi, 1.f), r.lo);
+    return fast_two_sum(y, fmaf(-0.5f * d, d, d));
+}
 // ln q of a token
 RL_DEVINL float log_q(float z, const RowRec& r) {
     const FF d = two_sum(z, -r.M);
@@ -216,7 +254,7 @@ RL_DEVINL float log_q(float z, const RowRec& r) {
 constexpr int kStatThreads = 256;
 
 template <typename T, bool kVec>
-__global__ void __launch_bounds__(kStatThreads) stats_kernel(const SampleArgs g) {
+__global__ void __launch_bounds__(kStatThreads, 3) stats_kernel(const SampleArgs g) {
     __shared__ float2 tab[2048];
     const rl_sample_args& a = g.a;
     fill_table(tab, threadIdx.x, kStatThreads);
@@ -244,26 +282,18 @@ __global__ void __launch_bounds__(kStatThreads) stats_kernel(const SampleArgs g)
         if (lane < kSubs && c * kSubs + lane < g.ns) g.submax[r * g.ns + c * kSubs + lane] = z_of(mine);
         const float m = z_of(cmax);
         const Knobs q = load_knobs(a, r);
-        ChunkStat st{m, 0, 0.0};
-        if (q.total && m > -INFINITY) {
+        if (!q.total) continue;
+        unsigned long long part = 0;
+        int ref_out = 0;
+        if (m > -INFINITY) {
             const FF cs = scale_of(q.T);
             const float pm = m * cs.hi;
-            uint32_t top_sum = 0;
-            int low_sum = 0;
-            float S = 0.f, L = 0.f;
-            // hi part on a grid of 2^-18 (sums of 32 values up to 1 are exact), the rest apart
-            auto add = [&](float hi, float v) {
-                const float wh = __fadd_rn(hi, v), wl = __fsub_rn(v, __fsub_rn(wh, hi));
-                const float top = __fsub_rn(__fadd_rn(wh, 48.f), 48.f);
-                S += top;
-                L += __fsub_rn(wh, top);
-                L += wl;
-            };
             if (fabsf(pm) < kWholeRef) {
                 const float ref = ceilf(pm), magic = 6144.f - ref, zlow = fmaxf((ref - 64.f) / cs.hi, -FLT_MAX);
-                st.ref = static_cast<int>(ref);
+                ref_out = static_cast<int>(ref);
 #pragma unroll
-                for (int s = 0; s < kSubs; ++s)
+                for (int s = 0; s < kSubs; ++s) {
+                    LaneSum acc;
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const float x = fmaxf(z[s][j], zlow);
@@ -272,27 +302,32 @@ __global__ void __launch_bounds__(kStatThreads) stats_kernel(const SampleArgs g)
                         float hi, v;
                         weight_pair(p, e, magic, tab, hi, v);
                         const bool in = z[s][j] >= zlow;
-                        add(in ? hi : 0.f, in ? v : 0.f);
+                        acc.add(in ? hi : 0.f, in ? v : 0.f);
                     }
+                    const unsigned long long t = acc.warp_total();
+                    if (lane == s) part = t;
+                }
             } else {
                 const float zlow = fmaxf(m - 64.f / cs.hi, -FLT_MAX);
-                st.ref = INT_MIN;
+                ref_out = INT_MIN;
 #pragma unroll
-                for (int s = 0; s < kSubs; ++s)
+                for (int s = 0; s < kSubs; ++s) {
+                    LaneSum acc;
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const bool in = z[s][j] >= zlow;
                         float p, e, hi, v;
                         phase_rel(in ? z[s][j] : m, m, cs, p, e);
                         weight_pair(p, e, 6144.f, tab, hi, v);
-                        add(in ? hi : 0.f, in ? v : 0.f);
+                        acc.add(in ? hi : 0.f, in ? v : 0.f);
                     }
+                    const unsigned long long t = acc.warp_total();
+                    if (lane == s) part = t;
+                }
             }
-            top_sum = __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(S * 262144.f));
-            low_sum = __reduce_add_sync(0xffffffffu, __float2int_rn(L * 549755813888.f));
-            st.sum = static_cast<double>(top_sum) * 3.814697265625e-06 + static_cast<double>(low_sum) * 1.8189894035458565e-12;
         }
-        if (lane == 0) g.stat[r * g.nc + c] = st;
+        if (lane < kSubs && c * kSubs + lane < g.ns) g.subsum[r * g.ns + c * kSubs + lane] = part;
+        if (lane == 0) g.ref[r * g.nc + c] = ref_out;
     }
     if (bad) set_status(g.status, RL_STATUS_NONFINITE);
 }
@@ -303,35 +338,32 @@ constexpr int kSelWarps = kSelThreads / 32;
 
 // How a logit lies to the bracket: above it, in it, or below.
 struct Bracket {
-    int mode;               // 0: everything in; 1: everything above; 2: linear bin b; 3: key >> shift == b
+    int mode;               // 0: everything in; 1: everything above; 2: bin b of (hi - z) scale; 3: key >> shift == b
     float hi, scale;
     int shift;
     uint32_t b;
 };
-RL_DEVINL int linear_bin(float z, float hi, float scale) {
-    return static_cast<int>(fminf((hi - z) * scale, static_cast<float>(kBins - 1)));
-}
-RL_DEVINL int place(const Bracket& k, float z, uint32_t key) {   // > 0 above, 0 in, < 0 below
+RL_DEVINL int place(const Bracket& k, uint32_t key) {            // modes 0, 1, 3: > 0 above, 0 in, < 0 below
     if (k.mode == 0) return 0;
     if (k.mode == 1) return 1;
-    if (k.mode == 2) return static_cast<int>(k.b) - linear_bin(z, k.hi, k.scale);
     const uint32_t x = k.shift < 32 ? key >> k.shift : 0;
     return x > k.b ? 1 : x == k.b ? 0 : -1;
 }
 
 struct SelShared {
     unsigned long long red[kSelWarps];
-    double redd[kSelWarps];
     float2 tab[2048];
     unsigned long long comp[kListCap];     // candidates: key << 32 | ~index
     unsigned long long wt[kListCap];       // their weights; the histogram before that
-    unsigned n_list, bin_lo;
     unsigned long long bin_before, bin_inside;
+    unsigned long long unit;               // 2^62 over the weight of M in its chunk's units
+    unsigned n_list, n_sub, bin_lo;
     int pick;
     float fpick;
     RowRec rec;
-    // then: unsigned long long / double cs[nc], int cnt[nc], int in[nc]
+    // then: unsigned long long cs[ns]; int cnt[ns], in[ns]; uint16_t subs[ns]
 };
+constexpr size_t kSelPart = sizeof(unsigned long long) + 2 * sizeof(int) + sizeof(uint16_t);
 
 template <typename T>
 RL_DEVINL T block_sum(T v, T* red) {                    // every thread gets the sum, in a fixed order
@@ -378,82 +410,131 @@ template <typename T, bool kVec>
 struct Row {
     const SampleArgs& g;
     SelShared& s;
-    unsigned long long* cs;      // [nc] kept weight of each chunk (units of 2^-50)
-    int* cnt;                    // [nc] kept tokens
-    int* in;                     // [nc] tokens in the bracket
+    unsigned long long* cs;      // [ns] kept weight of each part (units of 2^-50)
+    int* cnt;                    // [ns] kept tokens
+    int* in;                     // [ns] tokens in the bracket
+    uint16_t* subs;              // the parts that a pass reads
     const T* row;
     const float* submax;
     int V, tid, lane, warp;
-    float M, zlow;               // zlow: weights are 0 from here down
+    float M, zlow;               // zlow: weights are 0 below
     FF c;
     uint32_t bkey;               // the set that selection starts from: key > bkey, or equal and
     int btie;                    // index <= btie
 
     RL_DEVINL unsigned long long weight(float z) const { return weight_fixed(z, M, c, zlow, s.tab); }
-
-    // f(z, index) for every logit >= lo, a warp a chunk; after(chunk) once a chunk, by all lanes
-    template <typename F, typename G>
-    RL_DEVINL void each(float lo, F f, G after) {
-        bool bad = false;
-        for (int ch = warp; ch < g.nc; ch += kSelWarps) {
-            const int n = min(kSubs, g.ns - ch * kSubs);
-            for (int q = 0; q < n; ++q) {
-                if (submax[ch * kSubs + q] < lo) continue;
-                float z[4];
-                const int i = ch * kChunk + q * kSub + lane * 4;
-                load4<T, kVec>(row, i, V, z, bad);
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (z[j] >= lo && z[j] > -INFINITY) f(z[j], i + j);
-            }
-            after(ch);
-        }
-    }
     RL_DEVINL bool in_base(uint32_t key, int i) const { return key > bkey || (key == bkey && i <= btie); }
 
-    // One pass: weight and number of the logits above the bracket by chunk, those in it listed.
+    // Lists the parts with a logit >= lo, and clears the sums; returns how many there are.
+    RL_DEVINL int list_parts(float lo) {
+        __syncthreads();
+        if (tid == 0) s.n_sub = 0;
+        __syncthreads();
+        for (int i0 = 0; i0 < g.ns; i0 += kSelThreads) {
+            const int i = i0 + tid;
+            const bool hit = i < g.ns && submax[i] >= lo;
+            const unsigned m = __ballot_sync(0xffffffffu, hit);
+            unsigned at = 0;
+            if (lane == 0 && m) at = atomicAdd(&s.n_sub, __popc(m));
+            at = __shfl_sync(0xffffffffu, at, 0);
+            if (hit) subs[at + __popc(m & ((1u << lane) - 1u))] = static_cast<uint16_t>(i);
+            if (i < g.ns) {
+                cs[i] = 0;
+                cnt[i] = 0;
+                in[i] = 0;
+            }
+        }
+        __syncthreads();
+        return static_cast<int>(s.n_sub);
+    }
+    // f(z, index) for the logits of the listed parts, by all lanes together, a warp a part with four
+    // parts' loads in flight; after(part) once a part.
+    template <typename F, typename G>
+    RL_DEVINL void each(F f, G after) {
+        bool bad = false;
+        const int n = static_cast<int>(s.n_sub);
+        for (int i0 = warp * 4; i0 < n; i0 += kSelWarps * 4) {
+            float z[4][4];
+            int part[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                part[q] = i0 + q < n ? subs[i0 + q] : -1;
+                if (part[q] >= 0) load4<T, kVec>(row, part[q] * kSub + lane * 4, V, z[q], bad);
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                if (part[q] < 0) break;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) f(z[q][j], part[q] * kSub + lane * 4 + j);
+                after(part[q]);
+            }
+        }
+    }
+
+    // One pass: weight and number of the logits above the bracket by part, those in it listed.
     RL_DEVINL void collect(const Bracket& k, float lo) {
+        list_parts(lo);
         if (tid == 0) s.n_list = 0;
         __syncthreads();
-        unsigned long long acc = 0;
+        LaneSum acc;
         int n = 0, inside = 0;
-        each(lo, [&](float z, int i) {
-                const uint32_t key = key_of(z);
-                if (!in_base(key, i)) return;
-                const int pl = place(k, z, key);
-                if (pl > 0) {
-                    acc += weight(z);
-                    ++n;
-                } else if (pl == 0) {
+        const float fb = static_cast<float>(k.b);
+        const bool all_base = btie == INT_MAX && key_of(lo) >= bkey;
+        each([&](float z, int i) {
+                bool up, mid;
+                if (k.mode == 2) {
+                    const float x = fminf((k.hi - z) * k.scale, static_cast<float>(kBins - 1));
+                    up = x < fb;
+                    mid = !up && x < fb + 1.f;
+                } else {
+                    const int pl = place(k, key_of(z));
+                    up = pl > 0;
+                    mid = pl == 0;
+                }
+                const bool in_set = z >= lo && z > -INFINITY && (all_base || in_base(key_of(z), i));
+                up = up && in_set;
+                if (__any_sync(0xffffffffu, up)) {
+                    const bool w = up && z >= zlow;
+                    float p, e, hi, v;
+                    phase_rel(w ? z : M, M, c, p, e);
+                    weight_pair(p, e, 6144.f, s.tab, hi, v);
+                    acc.add(w ? hi : 0.f, w ? v : 0.f);
+                    n += up ? 1 : 0;
+                }
+                if (mid && in_set) {
                     ++inside;
                     const unsigned at = atomicAdd(&s.n_list, 1u);
-                    if (at < kListCap) s.comp[at] = (static_cast<unsigned long long>(key) << 32) | static_cast<uint32_t>(~i);
+                    if (at < kListCap) s.comp[at] = (static_cast<unsigned long long>(key_of(z)) << 32) | static_cast<uint32_t>(~i);
                 }
             },
-            [&](int ch) {
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
+            [&](int part) {
                 n = __reduce_add_sync(0xffffffffu, n);
-                inside = __reduce_add_sync(0xffffffffu, inside);
-                if (lane == 0) {
-                    cs[ch] = acc;
-                    cnt[ch] = n;
-                    in[ch] = inside;
+                if (n) {
+                    const unsigned long long w = acc.warp_total();
+                    if (lane == 0) {
+                        cs[part] = w;
+                        cnt[part] = n;
+                    }
+                    acc = LaneSum();
                 }
-                acc = 0;
+                if (__any_sync(0xffffffffu, inside)) {
+                    inside = __reduce_add_sync(0xffffffffu, inside);
+                    if (lane == 0) in[part] = inside;
+                }
                 n = inside = 0;
             });
         __syncthreads();
     }
-    RL_DEVINL double sum_weight() {
-        double v = 0.0;
-        for (int ch = tid; ch < g.nc; ch += kSelThreads) v += static_cast<double>(cs[ch]);
-        return block_sum(v, s.redd);
+    // Totals over the parts: weight in units of 2^-44, numbers.
+    RL_DEVINL unsigned long long sum_weight() {
+        unsigned long long v = 0;
+        for (int i = tid; i < g.ns; i += kSelThreads) v += cs[i] >> 6;
+        return block_sum(v, s.red);
     }
     RL_DEVINL long long sum_int(const int* x) {
-        long long v = 0;
-        for (int ch = tid; ch < g.nc; ch += kSelThreads) v += x[ch];
-        return static_cast<long long>(block_sum(static_cast<unsigned long long>(v), s.red));
+        unsigned long long v = 0;
+        for (int i = tid; i < g.ns; i += kSelThreads) v += static_cast<unsigned>(x[i]);
+        return static_cast<long long>(block_sum(v, s.red));
     }
     // The list in descending order (ties: the lower index first), and its weights.
     RL_DEVINL void sort_list(int n) {
@@ -471,39 +552,42 @@ struct Row {
                         s.comp[j] = x;
                     }
                 }
-                __syncthreads();
+                // with one pair a thread, pairs up to 32 apart stay within a warp's 64 entries
+                const int next = step > 1 ? step >> 1 : size;
+                if (step > 32 || next > 32 || m > kSelThreads * 2) __syncthreads();
+                else __syncwarp();
             }
+        __syncthreads();
         for (int i = tid; i < n; i += kSelThreads) s.wt[i] = weight(z_of(static_cast<uint32_t>(s.comp[i] >> 32)));
         __syncthreads();
     }
-    // How many of the sorted list come before the sum (above + those before) reaches target.
-    RL_DEVINL int keep_by_weight(int n, double above, double target, double& all) {
+    // How many of the sorted list come before the sum (above + those before) reaches target
+    // (both in units of 2^-44).
+    RL_DEVINL int keep_by_weight(int n, unsigned long long above, unsigned long long target) {
+        const unsigned long long rest = target > above ? target - above : 0ull;
+        const unsigned long long lim = rest >> 58 ? ~0ull : rest << 6;
         constexpr int kPer = kListCap / kSelThreads;
-        unsigned long long v[kPer], t = 0;
+        const int per = (n + kSelThreads - 1) / kSelThreads;
+        unsigned long long t = 0;
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) {
-            const int i = tid * kPer + j;
-            v[j] = i < n ? s.wt[i] : 0;
-            t += v[j];
-        }
+        for (int j = 0; j < kPer; ++j)
+            if (j < per && tid * per + j < n) t += s.wt[tid * per + j];
         unsigned long long p = block_scan(t, s.red);
         unsigned long long keep = 0;
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) {
-            const int i = tid * kPer + j;
-            if (i < n && above + static_cast<double>(p) < target) ++keep;
-            p += v[j];
-        }
-        const unsigned long long k = block_sum(keep, s.red);
-        all = above + static_cast<double>(block_sum(t, s.red));
-        return static_cast<int>(k);
+        for (int j = 0; j < kPer; ++j)
+            if (j < per && tid * per + j < n) {
+                if (p < lim) ++keep;
+                p += s.wt[tid * per + j];
+            }
+        return static_cast<int>(block_sum(keep, s.red));
     }
     // The first `keep` of the sorted list join the kept tokens; the border becomes the base.
     RL_DEVINL void close_list(int n, int keep) {
         for (int i = tid; i < keep; i += kSelThreads) {
-            const int ch = static_cast<int>(~static_cast<uint32_t>(s.comp[i])) / kChunk;
-            atomicAdd(&cs[ch], s.wt[i]);
-            atomicAdd(&cnt[ch], 1);
+            const int part = static_cast<int>(~static_cast<uint32_t>(s.comp[i])) / kSub;
+            atomicAdd(&cs[part], s.wt[i]);
+            atomicAdd(&cnt[part], 1);
         }
         if (n > 0) {
             const unsigned long long e = s.comp[keep > 0 ? keep - 1 : 0];
@@ -544,16 +628,18 @@ struct Row {
         __syncthreads();
     }
 
-    // Cuts the base set (of logits >= lo) to its first `k` tokens (by_count) or to the shortest
-    // prefix whose weight reaches `target`; cs / cnt then hold the kept ones, bkey / btie the
-    // border.  `mass`: the base set's weight (for the histogram by weight).  True: the sorted list
-    // begins with the whole kept set.
-    RL_DEVINL bool cut(bool by_count, long long k, double target, double mass, float lo, bool few) {
+    // Cuts the base set (of logits >= lo) to its first `k` tokens (k > 0) or to the shortest prefix
+    // whose weight reaches `top_p` of `mass` (the base set's weight, units of 2^-44); cs / cnt then
+    // hold the kept ones, bkey / btie the border.  True: the sorted list begins with the whole
+    // kept set.
+    RL_DEVINL bool cut(long long k, float top_p, unsigned long long mass, float lo, bool few) {
+        const bool by_count = k > 0;
+        const unsigned long long target = by_count ? 0ull : fraction_of(fmaxf(top_p, 0.f), mass);
         Bracket b{0, 0.f, 0.f, 0, 0};
         if (few) {                                  // likely few enough to list them all
             collect(b, lo);
             if (s.n_list <= kListCap) {
-                finish(by_count, k, target, b);
+                finish(k, target, b);
                 return true;
             }
         }
@@ -563,21 +649,22 @@ struct Row {
         unsigned long long before = 0, inside = 0;
         b.mode = 2;
         b.hi = M;
-        b.scale = static_cast<float>(kBins) / (M - lo);      // inf - the range is one value - or 0 end in mode 3
+        b.scale = static_cast<float>(kBins) / (M - lo);      // inf (one value) and 0 (too wide) end in mode 3
         if (b.scale > 0.f && b.scale <= FLT_MAX) {
+            list_parts(lo);
             for (int i = tid; i < kBins; i += kSelThreads) h32[i] = 0;
             __syncthreads();
-            const float q = static_cast<float>(2147483648.0 / (mass / kUnit));
-            each(lo, [&](float z, int i) {
-                    if (!in_base(key_of(z), i)) return;
+            const float q = 2147483648.f / (static_cast<float>(mass) * 0x1p-44f);
+            const bool all_base = btie == INT_MAX && key_of(lo) >= bkey;
+            each([&](float z, int i) {
                     // a rounded weight: this only says where to look
                     const uint32_t w = by_count ? 1u : __float2uint_rn(exp2_approx((z - M) * c.hi) * q);
-                    if (w) atomicAdd(&h32[linear_bin(z, b.hi, b.scale)], w);
+                    const float x = fminf((b.hi - z) * b.scale, static_cast<float>(kBins - 1));
+                    if (z >= lo && z > -INFINITY && w && (all_base || in_base(key_of(z), i))) atomicAdd(&h32[static_cast<int>(x)], w);
                 },
                 [](int) {});
             __syncthreads();
-            find_bin(h32, by_count ? static_cast<unsigned long long>(k)
-                                   : static_cast<unsigned long long>(fmin(target / mass, 1.0) * 2147483648.0),
+            find_bin(h32, by_count ? static_cast<unsigned long long>(k) : static_cast<unsigned long long>(fmaxf(top_p, 0.f) * 2147483648.f),
                      kBins, bin, before, inside);
             b.b = bin;
             for (int tries = 0; tries < kBins; ++tries) {
@@ -585,42 +672,41 @@ struct Row {
                 if (s.n_list > kListCap) break;
                 // the border may lie a bin further, by the rounding of the histogram's weights
                 if (by_count) break;
-                const double above = sum_weight();
+                const unsigned long long above = sum_weight();
                 if (above >= target && b.b > 0) {
                     --b.b;
                     continue;
                 }
                 unsigned long long t = 0;
                 const int n = static_cast<int>(s.n_list);
-                for (int i = tid; i < n; i += kSelThreads) t += weight(z_of(static_cast<uint32_t>(s.comp[i] >> 32)));
-                const double all = above + static_cast<double>(block_sum(t, s.red));
-                if (all < target && b.b < kBins - 1) {
+                for (int i = tid; i < n; i += kSelThreads) t += weight(z_of(static_cast<uint32_t>(s.comp[i] >> 32))) >> 6;
+                if (above + block_sum(t, s.red) < target && b.b < kBins - 1) {
                     ++b.b;
                     continue;
                 }
                 break;
             }
             if (s.n_list <= kListCap) {
-                finish(by_count, k, target, b);
+                finish(k, target, b);
                 return false;
             }
         }
-        // digits of the key, 11 + 11 + 10 bits, weights in units of 2^-40
+        // digits of the key, 11 + 11 + 10 bits
         b.mode = 3;
-        unsigned long long rest = by_count ? static_cast<unsigned long long>(k)
-                                           : static_cast<unsigned long long>(fmax(ceil(target / 1024.0), 1.0));
+        unsigned long long rest = by_count ? static_cast<unsigned long long>(k) : max(target, 1ull);
         uint32_t prefix = 0;
         for (int level = 0; level < 3; ++level) {
             const int shift = level == 0 ? 21 : level == 1 ? 10 : 0, bits = level == 2 ? 10 : 11;
+            list_parts(lo);
             for (int i = tid; i < kBins; i += kSelThreads) h64[i] = 0;
             __syncthreads();
-            each(lo, [&](float z, int i) {
+            each([&](float z, int i) {
                     const uint32_t key = key_of(z);
-                    if (!in_base(key, i)) return;
+                    if (!(z >= lo && z > -INFINITY) || !in_base(key, i)) return;
                     if (level > 0 && (key >> (shift + bits)) != prefix) return;
                     // descending order: bin 0 holds the largest digit
                     const uint32_t d = (1u << bits) - 1u - ((key >> shift) & ((1u << bits) - 1u));
-                    atomicAdd(&h64[d], by_count ? 1ull : weight(z) >> 10);
+                    atomicAdd(&h64[d], by_count ? 1ull : weight(z) >> 6);
                 },
                 [](int) {});
             __syncthreads();
@@ -629,41 +715,42 @@ struct Row {
             prefix = (prefix << bits) | ((1u << bits) - 1u - bin);
             b.shift = shift;
             b.b = prefix;
-            __syncthreads();
             collect(b, lo);
             if (s.n_list <= kListCap) break;
         }
-        finish(by_count, k, target, b);
+        finish(k, target, b);
         return false;
     }
     // After a collect: how many of the bracket's tokens stay, and the border.
-    RL_DEVINL void finish(bool by_count, long long k, double target, const Bracket& b) {
-        const long long n_above = sum_int(cnt);
-        const double above = sum_weight();
+    RL_DEVINL void finish(long long k, unsigned long long target, const Bracket& b) {
+        const bool by_count = k > 0;
+        const bool all_in = b.mode == 0;
+        const long long n_above = all_in ? 0 : sum_int(cnt);
+        const unsigned long long above = all_in ? 0 : sum_weight();
         const long long n = s.n_list;
         __syncthreads();
         if (n <= kListCap) {
             sort_list(static_cast<int>(n));
-            double all;
-            long long keep = by_count ? min(max(k - n_above, 0ll), n) : keep_by_weight(static_cast<int>(n), above, target, all);
+            long long keep = by_count ? min(max(k - n_above, 0ll), n) : keep_by_weight(static_cast<int>(n), above, target);
             if (keep == 0 && n_above == 0 && n > 0) keep = 1;
             close_list(static_cast<int>(n), static_cast<int>(keep));
             return;
         }
         // more equal logits than the list holds (the bracket is one key): the lowest indices stay
         const uint32_t key = b.b;
-        const unsigned long long w = weight(z_of(key));
-        long long keep = by_count ? k - n_above : (w == 0 ? n : static_cast<long long>(ceil(fmax(target - above, 0.0) / static_cast<double>(w))));
+        const unsigned long long w = weight(z_of(key)), w44 = w >> 6;
+        const unsigned long long rest = target > above ? target - above : 0ull;
+        long long keep = by_count ? k - n_above : w44 == 0 ? n : static_cast<long long>(min((rest + w44 - 1) / w44, 1ull << 40));
         keep = min(max(keep, n_above == 0 ? 1ll : 0ll), n);
         if (tid == 0) {
             s.pick = -1;
             long long left = keep;
-            for (int ch = 0; ch < g.nc; ++ch) {
-                const int t = static_cast<int>(min(left, static_cast<long long>(in[ch])));
-                cs[ch] += w * static_cast<unsigned long long>(t);
-                cnt[ch] += t;
-                if (t > 0 && left <= in[ch]) {       // the last kept one is the left-th of this chunk
-                    s.pick = ch;
+            for (int i = 0; i < g.ns; ++i) {
+                const int t = static_cast<int>(min(left, static_cast<long long>(in[i])));
+                cs[i] += w * static_cast<unsigned long long>(t);
+                cnt[i] += t;
+                if (t > 0 && left <= in[i]) {        // the last kept one is the left-th of this part
+                    s.pick = i;
                     s.bin_lo = static_cast<unsigned>(left);
                     break;
                 }
@@ -671,33 +758,26 @@ struct Row {
             }
         }
         __syncthreads();
-        const int ch = s.pick;
+        const int part = s.pick;
         __syncthreads();
-        if (ch >= 0 && warp == 0) {
-            int want = static_cast<int>(s.bin_lo), at = -1;
+        if (part >= 0 && warp == 0) {
             bool bad = false;
-            for (int q = 0; q < min(kSubs, g.ns - ch * kSubs) && at < 0; ++q) {
-                float z[4];
-                const int i0 = ch * kChunk + q * kSub + lane * 4;
-                load4<T, kVec>(row, i0, V, z, bad);
-                int m = 0;
+            float z[4];
+            const int i0 = part * kSub + lane * 4;
+            load4<T, kVec>(row, i0, V, z, bad);
+            bool is[4];
+            int m = 0, left = static_cast<int>(s.bin_lo), at = -1;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) m += (z[j] > -INFINITY && key_of(z[j]) == key && in_base(key, i0 + j)) ? 1 : 0;
-                int incl = m;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const int x = __shfl_up_sync(0xffffffffu, incl, o);
-                    if (lane >= o) incl += x;
-                }
-                int found = -1, left = want - (incl - m);
-                if (left >= 1 && left <= m) {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        if (z[j] > -INFINITY && key_of(z[j]) == key && in_base(key, i0 + j) && --left == 0) found = i0 + j;
-                }
-                at = static_cast<int>(__reduce_max_sync(0xffffffffu, static_cast<unsigned>(found + 1))) - 1;
-                want -= __shfl_sync(0xffffffffu, incl, 31);
+            for (int j = 0; j < 4; ++j) {
+                is[j] = z[j] > -INFINITY && key_of(z[j]) == key && in_base(key, i0 + j);
+                const unsigned bal = __ballot_sync(0xffffffffu, is[j]);
+                left -= __popc(bal & ((1u << lane) - 1u));
+                m += is[j] ? 1 : 0;
             }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (is[j] && --left == 0) at = i0 + j;
+            at = static_cast<int>(__reduce_max_sync(0xffffffffu, static_cast<unsigned>(at + 1))) - 1;
             if (lane == 0) s.pick = at;
         }
         __syncthreads();
@@ -706,80 +786,66 @@ struct Row {
         __syncthreads();
     }
 
-    // One draw by one warp; cs holds the inclusive sums of the chunks' weights, as doubles.
-    RL_DEVINL void draw(long long r, int d, double total) {
-        auto pre = [&](int ch) { return __longlong_as_double(static_cast<long long>(cs[ch])); };
+    // One draw by one warp; cs holds the inclusive sums of the parts' weights in units of 2^-44.
+    RL_DEVINL void draw(long long r, int d, unsigned long long total) {
         float u = g.a.u[r * g.a.K + d];
         if (!(u >= 0.f) || !(u < 1.f)) {
             if (lane == 0) set_status(g.status, RL_STATUS_KNOB);
             u = u >= 1.f ? 1.f - 5.9604645e-8f : 0.f;
         }
-        const double target = static_cast<double>(u) * total;
-        int lo = 0, hi = g.nc - 1;                   // first chunk whose inclusive sum passes the target
+        const unsigned long long target = fraction_of(u, total);
+        int lo = 0, hi = g.ns - 1;                   // first part whose inclusive sum passes the target
         while (lo < hi) {
             const int mid = (lo + hi) >> 1;
-            if (pre(mid) > target) hi = mid;
+            if (cs[mid] > target) hi = mid;
             else lo = mid + 1;
         }
-        const double rest = target - (lo > 0 ? pre(lo - 1) : 0.0);
-        const unsigned long long want = rest > 0.0 ? static_cast<unsigned long long>(rest) : 0ull;
-        unsigned long long run = 0;
-        int at = -1, last = -1;
-        float zat = 0.f, zlast = 0.f;
+        const unsigned long long before = lo > 0 ? cs[lo - 1] : 0ull;
+        const unsigned long long want = (target > before ? target - before : 0ull) << 6;
         bool bad = false;
-        for (int q = 0; q < min(kSubs, g.ns - lo * kSubs) && at < 0; ++q) {
-            float z[4];
-            const int i0 = lo * kChunk + q * kSub + lane * 4;
-            load4<T, kVec>(row, i0, V, z, bad);
-            unsigned long long w[4], mine = 0;
-            int my_last = -1;
-            float my_z = 0.f;
+        float z[4];
+        const int i0 = lo * kSub + lane * 4;
+        load4<T, kVec>(row, i0, V, z, bad);
+        unsigned long long w[4], mine = 0;
+        int my_last = -1;
+        float my_z = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const bool in_set = z[j] > -INFINITY && in_base(key_of(z[j]), i0 + j);
+            w[j] = in_set ? weight(z[j]) : 0ull;
+            mine += w[j];
+            if (in_set) {
+                my_last = i0 + j;
+                my_z = z[j];
+            }
+        }
+        unsigned long long incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const unsigned long long x = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += x;
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, incl > want);
+        int at = my_last;
+        float zat = my_z;
+        int src;
+        if (hit) {
+            src = __ffs(hit) - 1;
+            unsigned long long p = incl - mine;
+            bool got = false;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                w[j] = z[j] > -INFINITY && in_base(key_of(z[j]), i0 + j) ? weight(z[j]) : 0ull;
-                mine += w[j];
-                if (z[j] > -INFINITY && in_base(key_of(z[j]), i0 + j)) {
-                    my_last = i0 + j;
-                    my_z = z[j];
+                p += w[j];
+                if (!got && p > want) {
+                    got = true;
+                    at = i0 + j;
+                    zat = z[j];
                 }
             }
-            unsigned long long incl = mine;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const unsigned long long x = __shfl_up_sync(0xffffffffu, incl, o);
-                if (lane >= o) incl += x;
-            }
-            const unsigned hit = __ballot_sync(0xffffffffu, run + incl > want);
-            if (hit) {
-                const int src = __ffs(hit) - 1;
-                unsigned long long p = run + incl - mine;
-                int f = 0;
-                bool got = false;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    p += w[j];
-                    if (!got && p > want) {
-                        got = true;
-                        f = j;
-                    }
-                }
-                const float zf = f == 0 ? z[0] : f == 1 ? z[1] : f == 2 ? z[2] : z[3];
-                at = __shfl_sync(0xffffffffu, i0 + f, src);
-                zat = __shfl_sync(0xffffffffu, zf, src);
-            }
-            const unsigned any = __ballot_sync(0xffffffffu, my_last >= 0);
-            if (any) {
-                const int src = 31 - __clz(any);
-                last = __shfl_sync(0xffffffffu, my_last, src);
-                zlast = __shfl_sync(0xffffffffu, my_z, src);
-            }
-            run += __shfl_sync(0xffffffffu, incl, 31);
+        } else {                // the target met the part's sum to the last place
+            src = 31 - __clz(__ballot_sync(0xffffffffu, my_last >= 0) | 1u);
         }
-        if (at < 0) {           // the target met the chunk's sum to the last place
-            at = last;
-            zat = zlast;
-        }
-        if (lane == 0) {
+        if (lane == src) {
             g.a.tokens[r * g.a.K + d] = at;
             if (g.a.logq) g.a.logq[r * g.a.K + d] = log_q(zat, s.rec);
         }
@@ -814,7 +880,7 @@ RL_DEVINL uint32_t kth_submax(SelShared& s, const float* submax, int ns, int k) 
 }
 
 template <typename T, bool kVec>
-__global__ void __launch_bounds__(kSelThreads) select_kernel(const SampleArgs g) {
+__global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SampleArgs g) {
     extern __shared__ __align__(16) uint8_t raw[];
     SelShared& s = *reinterpret_cast<SelShared*>(raw);
     const rl_sample_args& a = g.a;
@@ -822,25 +888,24 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SampleArgs g)
     const int tid = threadIdx.x;
     const int V = static_cast<int>(a.V);
     unsigned long long* cs = reinterpret_cast<unsigned long long*>(raw + sizeof(SelShared));
-    int* cnt = reinterpret_cast<int*>(cs + g.nc);
-    Row<T, kVec> w{g, s, cs, cnt, cnt + g.nc, static_cast<const T*>(a.logits) + r * a.row_stride, g.submax + r * g.ns, V,
+    int* cnt = reinterpret_cast<int*>(cs + g.ns);
+    Row<T, kVec> w{g, s, cs, cnt, cnt + g.ns, reinterpret_cast<uint16_t*>(cnt + 2 * g.ns),
+                   static_cast<const T*>(a.logits) + r * a.row_stride, g.submax + r * g.ns, V,
                    tid, tid & 31, tid >> 5, 0.f, 0.f, {0.f, 0.f}, 0u, INT_MAX};
-    const ChunkStat* stat = g.stat + r * g.nc;
     const Knobs q = load_knobs(a, r);
     fill_table(s.tab, tid, kSelThreads);
     unsigned long long mk = 0;
-    for (int ch = tid; ch < g.nc; ch += kSelThreads) mk = max(mk, static_cast<unsigned long long>(key_of(stat[ch].max)));
+    for (int i = tid; i < g.ns; i += kSelThreads) mk = max(mk, static_cast<unsigned long long>(key_of(w.submax[i] + 0.f)));
     const float M = z_of(static_cast<uint32_t>(block_max(mk, s.red)));
     w.M = M;
     int count = 0, mode = kRowEmpty, bits = tid == 0 ? q.bits : 0;
-    double total = 0.0;
 
     if (!(M > -INFINITY)) {
         for (int d = tid; d < a.K; d += kSelThreads) {
             a.tokens[r * a.K + d] = -1;
             if (a.logq) a.logq[r * a.K + d] = -INFINITY;
         }
-        for (int ch = tid; ch < g.nc; ch += kSelThreads) cnt[ch] = 0;
+        for (int i = tid; i < g.ns; i += kSelThreads) cnt[i] = 0;
         bits |= tid == 0 ? RL_STATUS_EMPTY_ROW : 0;
         if (tid == 0) s.rec = RowRec{M, {1.f, 0.f}, {0.f, 0.f}, 0u, -1, kRowEmpty};
     } else if (q.greedy) {
@@ -863,7 +928,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SampleArgs g)
             at = static_cast<int>(__reduce_min_sync(0xffffffffu, static_cast<unsigned>(at)));
             if (w.lane == 0) s.pick = at;
         }
-        for (int ch = tid; ch < g.nc; ch += kSelThreads) cnt[ch] = 0;
+        for (int i = tid; i < g.ns; i += kSelThreads) cnt[i] = 0;
         __syncthreads();
         const int at = s.pick;
         for (int d = tid; d < a.K; d += kSelThreads) {
@@ -871,139 +936,144 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SampleArgs g)
             if (a.logq) a.logq[r * a.K + d] = 0.f;
         }
         if (tid == 0) {
-            cnt[at / kChunk] = 1;
+            cnt[at / kSub] = 1;
             s.rec = RowRec{M, {1.f, 0.f}, {0.f, 0.f}, key_of(M), at, kRowCut};
         }
         count = 1;
         mode = kRowCut;
         __syncthreads();
+        if (a.offsets)
+            for (int i = tid; i < g.ns; i += kSelThreads) g.cpre[r * g.ns + i] = i > at / kSub ? 1 : 0;
     } else {
         w.c = scale_of(q.T);
         w.zlow = fmaxf(M - 64.f / w.c.hi, -FLT_MAX);
-        // the least logit whose weight is at least min_p and 2^-100
+        // the least logit whose weight is at least min_p and 2^-100: M + T ln(...), rounded up
         if (tid == 0) {
-            const double lim = static_cast<double>(M) + static_cast<double>(q.T) * log(fmax(static_cast<double>(q.mp), 0x1p-100));
-            float f = __double2float_ru(lim);
+            FF lim = q.mp > 0.f ? ln_pair({fmaxf(q.mp, 7.888609e-31f), 0.f}) : FF{-69.31472016f, 1.5413417e-06f};
+            lim = ff_add(ff_mul(lim, {q.T, 0.f}), {M, 0.f});
+            const float f = lim.lo > 0.f ? nextafterf(lim.hi, INFINITY) : lim.hi;
             s.fpick = fminf(fmaxf(f, -FLT_MAX), M) + 0.f;
+            // 2^(ref - p) for M's phase p: what turns its chunk's units into M's weight
+            const float pm = __fmul_rn(M, w.c.hi);
+            if (fabsf(pm) < kWholeRef) {
+                float hi, v;
+                weight_pair(-pm, -fmaf(M, w.c.lo, fmaf(M, w.c.hi, -pm)), 6144.f + ceilf(pm), s.tab, hi, v);
+                s.unit = (static_cast<unsigned long long>(hi * 8388608.f) << 39) + static_cast<long long>(v * 0x1p62f);
+            }
         }
         __syncthreads();
         const float zmin = s.fpick;
         w.bkey = key_of(zmin);
         w.btie = INT_MAX;
-        bool fixed = true;                              // cs in units of 2^-50, else (whole rows) weights
+        unsigned long long mass = 0;                    // units of 2^-44
         if (q.total) {
-            // the chunks' sums relative to M's weight
-            const double cd = 1.4426950408889634 / static_cast<double>(q.T);
-            const double pm = static_cast<double>(M) * cd;
-            const bool plain = fabsf(M * w.c.hi) < kWholeRef;
-            const double ref = ceil(static_cast<double>(M * w.c.hi));
-            const double f = plain ? exp2(ref - pm) : 1.0;
-            double v = 0.0;
-            for (int ch = tid; ch < g.nc; ch += kSelThreads) {
-                const ChunkStat st = stat[ch];
-                double x = 0.0;
-                if (st.sum > 0.0) {
-                    if (plain && st.ref != INT_MIN) {
-                        const int n = st.ref - static_cast<int>(ref);
-                        x = n < -200 ? 0.0 : st.sum * f * __longlong_as_double(static_cast<long long>(1023 + n) << 52);
-                    } else {
-                        x = st.sum * exp2(st.ref == INT_MIN ? (static_cast<double>(st.max) - M) * cd : st.ref - pm);
+            // the parts' sums relative to M's weight, in units of 2^-50
+            const float pm = __fmul_rn(M, w.c.hi);
+            const bool plain = fabsf(pm) < kWholeRef;
+            const int ref = plain ? static_cast<int>(ceilf(pm)) : 0;
+            const unsigned long long unit = s.unit;
+            unsigned long long v = 0;
+            for (int i = tid; i < g.ns; i += kSelThreads) {
+                unsigned long long x = g.subsum[r * g.ns + i];
+                const int rc = g.ref[r * g.nc + i / kSubs];
+                if (x) {
+                    if (plain && rc != INT_MIN) {
+                        const int n = ref - rc;
+                        x = n < 64 ? __umul64hi(x << 2, unit) >> n : 0ull;
+                    } else {                            // very large logits: the slow way
+                        const double cd = 1.4426950408889634 / static_cast<double>(q.T);
+                        float cm = -INFINITY;
+                        for (int j = i / kSubs * kSubs; j < min(i / kSubs * kSubs + kSubs, g.ns); ++j) cm = fmaxf(cm, w.submax[j]);
+                        const double d = rc == INT_MIN ? (static_cast<double>(cm) - M) * cd : rc - M * cd;
+                        x = static_cast<unsigned long long>(static_cast<double>(x) * exp2(d));
                     }
                 }
-                x = x < 0x1p-52 ? 0.0 : x * kUnit;       // below what a draw can tell from nothing
-                cs[ch] = static_cast<unsigned long long>(__double_as_longlong(x));
-                v += x;
+                cs[i] = x;
+                v += x >> 6;
             }
-            total = block_sum(v, s.redd);
-            fixed = false;
+            mass = block_sum(v, s.red);
         }
         if (!q.cut) {
             mode = kRowWhole;
             count = a.K - 1;
         } else {
             mode = kRowCut;
-            double mass = total;
             float lo = zmin;
-            bool done = false, listed = false;
+            bool listed = false;
             if (q.k < V) {
                 bool few = false;
                 if (q.k <= g.ns) {
                     lo = fmaxf(lo, z_of(kth_submax(s, w.submax, g.ns, q.k)));
                     few = q.k <= kListCap / 2;
                 }
-                listed = w.cut(true, q.k, 0.0, 0.0, lo, few);
-                done = true;
+                listed = w.cut(q.k, 0.f, 0ull, lo, few);
             } else if (!q.total) {                      // min_p alone so far: all of its tokens
-                unsigned long long hit = 0;
-                for (int i = tid; i < g.ns; i += kSelThreads) hit += w.submax[i] >= lo ? 1 : 0;
-                const bool few = block_sum(hit, s.red) * 10 < static_cast<unsigned long long>(g.ns) * 9;
+                const bool few = w.list_parts(lo) * 10 < g.ns * 9;
                 Bracket b{few ? 0 : 1, 0.f, 0.f, 0, 0};
                 w.collect(b, lo);
                 if (few && s.n_list > kListCap) {
                     b.mode = 1;
-                    __syncthreads();
                     w.collect(b, lo);
                 }
-                if (b.mode == 0) w.finish(true, V, 0.0, b);
+                if (b.mode == 0) w.finish(V, 0ull, b);
                 listed = b.mode == 0;
-                done = true;
             }
-            if (done) mass = w.sum_weight();
+            if (!q.total && q.p < 1.f) mass = w.sum_weight();
             if (q.p < 1.f) {
-                const double target = static_cast<double>(q.p) * mass;
                 if (listed) {
                     // the whole set is the sorted list's head
                     const int n = static_cast<int>(w.sum_int(w.cnt));
-                    double all;
-                    int keep = w.keep_by_weight(n, 0.0, target, all);
-                    keep = max(keep, 1);
-                    for (int ch = tid; ch < g.nc; ch += kSelThreads) {
-                        cs[ch] = 0;
-                        cnt[ch] = 0;
+                    const int keep = max(w.keep_by_weight(n, 0ull, fraction_of(fmaxf(q.p, 0.f), mass)), 1);
+                    for (int i = tid; i < g.ns; i += kSelThreads) {
+                        cs[i] = 0;
+                        cnt[i] = 0;
                     }
                     __syncthreads();
                     w.close_list(n, keep);
                 } else {
                     // a logit whose weight is below (1 - p) mass / V cannot be needed
-                    if (tid == 0) {
-                        const double rest = (1.0 - fmax(static_cast<double>(q.p), 0.0)) * (mass / kUnit) / static_cast<double>(V) * 0.999;
-                        const double lim = static_cast<double>(M) + static_cast<double>(q.T) * log(fmin(fmax(rest, 0x1p-100), 1.0));
-                        s.fpick = fminf(fmaxf(__double2float_rd(lim), -FLT_MAX), M) + 0.f;
-                    }
-                    __syncthreads();
-                    lo = fmaxf(lo, s.fpick);
-                    unsigned long long hit = 0;
-                    for (int i = tid; i < g.ns; i += kSelThreads) hit += w.submax[i] >= lo ? 1 : 0;
-                    const bool few = block_sum(hit, s.red) * 10 < static_cast<unsigned long long>(g.ns) * 9;
-                    w.cut(false, 0, target, mass, lo, few);
+                    const float rest = (1.f - fmaxf(q.p, 0.f)) * (static_cast<float>(mass) * 0x1p-44f) / static_cast<float>(V) * 0.999f;
+                    const float need = M + q.T * fminf(logf(fmaxf(rest, 7.9e-31f)), 0.f);
+                    lo = fmaxf(lo, fminf(need - 0x1p-18f * (q.T + fabsf(M)), M));
+                    w.cut(0, q.p, mass, lo, w.list_parts(lo) * 10 < g.ns * 9);
                 }
             }
-            fixed = true;
-            count = static_cast<int>(w.sum_int(w.cnt));
         }
-        // inclusive sums over the chunks (in place: a thread's own consecutive chunks, then a scan)
-        const int per = (g.nc + kSelThreads - 1) / kSelThreads;
-        double t = 0.0;
+        // inclusive sums over the parts, of weights (in place) and of the kept tokens
+        const int per = (g.ns + kSelThreads - 1) / kSelThreads;
+        unsigned long long t = 0, tn = 0;
         for (int j = 0; j < per; ++j) {
-            const int ch = tid * per + j;
-            if (ch < g.nc) {
-                t += fixed ? static_cast<double>(cs[ch]) : __longlong_as_double(static_cast<long long>(cs[ch]));
-                cs[ch] = static_cast<unsigned long long>(__double_as_longlong(t));
+            const int i = tid * per + j;
+            if (i < g.ns) {
+                t += cs[i] >> 6;
+                cs[i] = t;
+                if (mode == kRowCut) tn += static_cast<unsigned>(cnt[i]);
             }
         }
-        const double before = block_scan(t, s.redd);
+        const unsigned long long before = block_scan(t, s.red);
         for (int j = 0; j < per; ++j) {
-            const int ch = tid * per + j;
-            if (ch < g.nc)
-                cs[ch] = static_cast<unsigned long long>(
-                    __double_as_longlong(__longlong_as_double(static_cast<long long>(cs[ch])) + before));
+            const int i = tid * per + j;
+            if (i < g.ns) cs[i] += before;
+        }
+        if (mode == kRowCut) {
+            unsigned long long p = block_scan(tn, s.red);
+            if (a.offsets)
+                for (int j = 0; j < per; ++j) {
+                    const int i = tid * per + j;
+                    if (i < g.ns) {
+                        g.cpre[r * g.ns + i] = static_cast<int>(p);
+                        p += static_cast<unsigned>(cnt[i]);
+                    }
+                }
+            count = static_cast<int>(block_sum(tn, s.red));
         }
         __syncthreads();
-        total = __longlong_as_double(static_cast<long long>(cs[g.nc - 1]));
+        const unsigned long long total = cs[g.ns - 1];
         if (tid == 0) {
-            const double lw = log(total / kUnit);
-            const float h = static_cast<float>(lw);
-            s.rec = RowRec{M, inv_of(q.T), {h, static_cast<float>(lw - h)}, w.bkey, w.btie, mode};
+            // total / 2^44 as a float pair
+            const float th = __ull2float_rz(total);
+            const float tl = static_cast<float>(static_cast<long long>(total - static_cast<unsigned long long>(th)));
+            s.rec = RowRec{M, inv_of(q.T), ln_pair(fast_two_sum(th * 0x1p-44f, tl * 0x1p-44f)), w.bkey, w.btie, mode};
         }
         __syncthreads();
         for (int d = w.warp; d < a.K; d += kSelWarps) w.draw(r, d, total);
@@ -1011,8 +1081,6 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SampleArgs g)
     __syncthreads();
     if (a.replayed && tid == 0) a.replayed[r] = q.cut ? 1 : 0;
     if (a.offsets) {
-        if (mode == kRowCut)
-            for (int ch = tid; ch < g.nc; ch += kSelThreads) g.ccnt[r * g.nc + ch] = cnt[ch];
         if (tid == 0) {
             g.count[r] = count;
             g.rec[r] = s.rec;
@@ -1058,6 +1126,8 @@ constexpr int kEmitThreads = 256;
 template <typename T, bool kVec>
 __global__ void __launch_bounds__(kEmitThreads) emit_kernel(const SampleArgs g) {
     __shared__ int sorted[1024];
+    __shared__ float kept_z[kEmitThreads / 32][kSub];
+    __shared__ uint8_t kept_i[kEmitThreads / 32][kSub];
     const rl_sample_args& a = g.a;
     const int lane = threadIdx.x & 31;
     const int parts = gridDim.x;
@@ -1088,50 +1158,61 @@ __global__ void __launch_bounds__(kEmitThreads) emit_kernel(const SampleArgs g) 
             for (int i = threadIdx.x; i < a.K - 1; i += kEmitThreads)
                 if (base + i < a.capacity) {
                     a.ids[base + i] = sorted[i];
-                    a.support_logq[base + i] = log_q(to_f(row[sorted[i]]), rec);
+                    a.support_logq[base + i] = log_q(to_f(row[max(sorted[i], 0)]) + 0.f, rec);
                 }
             __syncthreads();
         } else if (rec.mode == kRowCut) {
-            const int* ccnt = g.ccnt + r * g.nc;
-            for (int ch = blockIdx.x * (kEmitThreads / 32) + (threadIdx.x >> 5); ch < g.nc; ch += parts * (kEmitThreads / 32)) {
-                const int n = ccnt[ch];
-                if (n == 0) continue;
-                int before = 0;
-                for (int i = lane; i < ch; i += 32) before += ccnt[i];
-                long long at = base + __reduce_add_sync(0xffffffffu, before);
-                int left = n;
-                for (int q = 0; q < min(kSubs, g.ns - ch * kSubs) && left > 0; ++q) {
-                    if (key_of(g.submax[r * g.ns + ch * kSubs + q] + 0.f) < rec.key) continue;
-                    float z[4];
-                    const int i0 = ch * kChunk + q * kSub + lane * 4;
-                    load4<T, kVec>(row, i0, V, z, bad);
-                    bool keep[4];
-                    int m = 0;
+            const int* cpre = g.cpre + r * g.ns;
+            float* kz = kept_z[threadIdx.x >> 5];
+            uint8_t* ki = kept_i[threadIdx.x >> 5];
+            const float zk = z_of(rec.key);
+            const int total = static_cast<int>(min(static_cast<long long>(a.offsets[r + 1]) - base, static_cast<long long>(INT_MAX)));
+            // 32 parts a warp and step; those that keep tokens four at a time
+            for (int p0 = (blockIdx.x * (kEmitThreads / 32) + (threadIdx.x >> 5)) * 32; p0 < g.ns; p0 += parts * kEmitThreads) {
+                const int mine = p0 + lane;
+                const int from = mine < g.ns ? cpre[mine] : 0;
+                const int to = mine < g.ns ? (mine + 1 < g.ns ? cpre[mine + 1] : total) : 0;
+                unsigned todo = __ballot_sync(0xffffffffu, to > from);
+                while (todo) {
+                    float z[4][4];
+                    int part[4];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const uint32_t k = key_of(z[j]);
-                        keep[j] = z[j] > -INFINITY && (k > rec.key || (k == rec.key && i0 + j <= rec.tie));
-                        m += keep[j] ? 1 : 0;
+                    for (int q = 0; q < 4; ++q) {
+                        part[q] = todo ? __ffs(todo) - 1 : -1;
+                        todo &= todo - 1u;
+                        if (part[q] >= 0) load4<T, kVec>(row, (p0 + part[q]) * kSub + lane * 4, V, z[q], bad);
                     }
-                    int incl = m;
 #pragma unroll
-                    for (int o = 1; o < 32; o <<= 1) {
-                        const int x = __shfl_up_sync(0xffffffffu, incl, o);
-                        if (lane >= o) incl += x;
-                    }
-                    long long p = at + incl - m;
+                    for (int q = 0; q < 4; ++q) {
+                        if (part[q] < 0) break;
+                        // the part's kept logits one after another in shared memory, then dense arithmetic
+                        const int i0 = (p0 + part[q]) * kSub + lane * 4;
+                        int place = 0, have = 0;
+                        unsigned keeps = 0;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        if (keep[j]) {
-                            if (p < a.capacity) {
-                                a.ids[p] = i0 + j;
-                                a.support_logq[p] = log_q(z[j], rec);
-                            }
-                            ++p;
+                        for (int j = 0; j < 4; ++j) {
+                            const bool keep = z[q][j] > zk || (z[q][j] == zk && i0 + j <= rec.tie);
+                            const unsigned m = __ballot_sync(0xffffffffu, keep);
+                            place += __popc(m & ((1u << lane) - 1u));
+                            have += __popc(m);
+                            keeps |= (keep ? 1u : 0u) << j;
                         }
-                    const int all = __shfl_sync(0xffffffffu, incl, 31);
-                    at += all;
-                    left -= all;
+                        __syncwarp();
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            if ((keeps >> j) & 1u) {
+                                kz[place] = z[q][j];
+                                ki[place] = static_cast<uint8_t>(lane * 4 + j);
+                                ++place;
+                            }
+                        __syncwarp();
+                        const long long at = base + __shfl_sync(0xffffffffu, from, part[q]);
+                        for (int i = lane; i < have; i += 32) {
+                            if (at + i >= a.capacity) break;
+                            a.ids[at + i] = (p0 + part[q]) * kSub + ki[i];
+                            a.support_logq[at + i] = log_q(kz[i], rec);
+                        }
+                    }
                 }
             }
         }
@@ -1145,9 +1226,10 @@ static SampleArgs sample_view(void* ws, const rl_sample_args* a, size_t* bytes) 
     g.ns = static_cast<int>((a->V + kSub - 1) / kSub);
     Carve cv(ws);
     g.done = cv.take<unsigned>(64);
-    g.stat = cv.take<ChunkStat>(static_cast<size_t>(a->N) * g.nc);
     g.submax = cv.take<float>(static_cast<size_t>(a->N) * g.ns);
-    g.ccnt = cv.take<int>(static_cast<size_t>(a->N) * g.nc);
+    g.subsum = cv.take<unsigned long long>(static_cast<size_t>(a->N) * g.ns);
+    g.ref = cv.take<int>(static_cast<size_t>(a->N) * g.nc);
+    g.cpre = cv.take<int>(static_cast<size_t>(a->N) * g.ns);
     g.count = cv.take<int>(static_cast<size_t>(a->N));
     g.rec = cv.take<RowRec>(static_cast<size_t>(a->N));
     if (bytes) *bytes = align_up(cv.off, 256);
@@ -1167,9 +1249,9 @@ template <typename T, bool kVec>
 static int sample_run(const SampleArgs& g, cudaStream_t stream) {
     const long long units = g.a.N * g.nc;
     long long blocks = (units + kStatThreads / 32 - 1) / (kStatThreads / 32);
-    const long long cap = 4ll * num_sms();
+    const long long cap = 3ll * num_sms();
     if (blocks > cap) blocks = cap;
-    const size_t smem = sizeof(SelShared) + static_cast<size_t>(g.nc) * (sizeof(unsigned long long) + 2 * sizeof(int));
+    const size_t smem = sizeof(SelShared) + static_cast<size_t>(g.ns) * kSelPart;
     if (cudaFuncSetAttribute(select_kernel<T, kVec>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
         return RL_ERR_CUDA;
     ProfScope prof(RL_PROF_OTHER, stream);
@@ -1177,8 +1259,8 @@ static int sample_run(const SampleArgs& g, cudaStream_t stream) {
     select_kernel<T, kVec><<<static_cast<unsigned>(g.a.N), kSelThreads, smem, stream>>>(g);
     int launches = 2;
     if (g.a.offsets) {
-        // a block takes eight chunks a step; rows beyond the grid's share are looped over
-        const int parts = static_cast<int>((g.nc + 31) / 32);
+        // a block takes 256 parts a step; rows beyond the grid's share are looped over
+        const int parts = static_cast<int>((g.ns + kEmitThreads - 1) / kEmitThreads);
         const dim3 grid(static_cast<unsigned>(parts), static_cast<unsigned>(g.a.N < 16384 ? g.a.N : 16384), 1);
         emit_kernel<T, kVec><<<grid, kEmitThreads, 0, stream>>>(g);
         ++launches;
