@@ -144,32 +144,47 @@ RL_DEVINL float to_f(float x) { return x; }
 RL_DEVINL float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
 RL_DEVINL float to_f(__half x) { return __half2float(x); }
 
-// Four logits from element i on; past the row's end -inf.  NaN and +inf become -inf (`bad`).
-template <typename T, bool kVec>
-RL_DEVINL void load4(const T* row, int i, int V, float (&z)[4], bool& bad) {
-    if (kVec && i + 4 <= V) {
-        if constexpr (sizeof(T) == 4) {
-            const float4 q = __ldg(reinterpret_cast<const float4*>(row + i));
-            z[0] = q.x; z[1] = q.y; z[2] = q.z; z[3] = q.w;
+// Four logits as they lie in memory.
+template <typename T>
+struct Quad {
+    T t[4];
+    template <bool kVec>
+    RL_DEVINL void load(const T* row, int i, int V) {         // from element i on; past the row's end -inf
+        if (kVec && i + 4 <= V) {
+            if constexpr (sizeof(T) == 4) {
+                const float4 q = __ldg(reinterpret_cast<const float4*>(row + i));
+                memcpy(t, &q, 16);
+            } else {
+                const uint2 q = __ldg(reinterpret_cast<const uint2*>(row + i));
+                memcpy(t, &q, 8);
+            }
         } else {
-            const uint2 q = __ldg(reinterpret_cast<const uint2*>(row + i));
-            T t[4];
-            memcpy(t, &q, 8);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) z[j] = to_f(t[j]);
+            for (int j = 0; j < 4; ++j) t[j] = i + j < V ? row[i + j] : static_cast<T>(-INFINITY);
         }
-    } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) z[j] = i + j < V ? to_f(row[i + j]) : -INFINITY;
     }
+    RL_DEVINL void get(float (&z)[4]) const {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        if (!(z[j] < INFINITY)) {
-            bad = true;
-            z[j] = -INFINITY;
-        }
-        z[j] += 0.f;
+        for (int j = 0; j < 4; ++j) z[j] = to_f(t[j]);
     }
+};
+template <typename T, bool kVec>
+RL_DEVINL void load4_raw(const T* row, int i, int V, float (&z)[4]) {
+    Quad<T> q;
+    q.template load<kVec>(row, i, V);
+    q.get(z);
+}
+// Four logits with NaN and +inf as -inf, and no -0.
+template <typename T, bool kVec>
+RL_DEVINL void load4(const T* row, int i, int V, float (&z)[4]) {
+    load4_raw<T, kVec>(row, i, V, z);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) z[j] = (z[j] < INFINITY ? z[j] : -INFINITY) + 0.f;
+}
+RL_DEVINL float max_nan(float a, float b) {           // NaN if either is
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
 }
 
 RL_DEVINL void fill_table(float2* tab, int tid, int threads) {
@@ -254,7 +269,7 @@ RL_DEVINL float log_q(float z, const RowRec& r) {
 constexpr int kStatThreads = 256;
 
 template <typename T, bool kVec>
-__global__ void __launch_bounds__(kStatThreads, 3) stats_kernel(const SampleArgs g) {
+__global__ void __launch_bounds__(kStatThreads, 2) stats_kernel(const SampleArgs g) {
     __shared__ float2 tab[2048];
     const rl_sample_args& a = g.a;
     fill_table(tab, threadIdx.x, kStatThreads);
@@ -264,24 +279,45 @@ __global__ void __launch_bounds__(kStatThreads, 3) stats_kernel(const SampleArgs
     const long long warps = static_cast<long long>(gridDim.x) * (kStatThreads / 32);
     const long long units = a.N * g.nc;
     bool bad = false;
-    for (long long id = static_cast<long long>(blockIdx.x) * (kStatThreads / 32) + (threadIdx.x >> 5); id < units; id += warps) {
+    // a chunk's logits as they lie in memory, the next chunk's on their way while one is worked on
+    Quad<T> raw[kSubs], ahead[kSubs];
+    Knobs q, q_ahead;
+    auto fetch = [&](long long id) {
+        const long long r = id / g.nc;
+        const T* row = static_cast<const T*>(a.logits) + r * a.row_stride;
+        q_ahead = load_knobs(a, r);
+#pragma unroll
+        for (int s = 0; s < kSubs; ++s) ahead[s].template load<kVec>(row, static_cast<int>(id - r * g.nc) * kChunk + s * kSub + lane * 4, V);
+    };
+    long long id = static_cast<long long>(blockIdx.x) * (kStatThreads / 32) + (threadIdx.x >> 5);
+    if (id < units) fetch(id);
+    for (; id < units; id += warps) {
         const long long r = id / g.nc;
         const int c = static_cast<int>(id - r * g.nc);
-        const T* row = static_cast<const T*>(a.logits) + r * a.row_stride;
+#pragma unroll
+        for (int s = 0; s < kSubs; ++s) raw[s] = ahead[s];
+        q = q_ahead;
+        if (id + warps < units) fetch(id + warps);
         float z[kSubs][4];
 #pragma unroll
-        for (int s = 0; s < kSubs; ++s) load4<T, kVec>(row, c * kChunk + s * kSub + lane * 4, V, z[s], bad);
+        for (int s = 0; s < kSubs; ++s) raw[s].get(z[s]);
         uint32_t cmax = 0, mine = 0;
 #pragma unroll
         for (int s = 0; s < kSubs; ++s) {
-            const float m = fmaxf(fmaxf(z[s][0], z[s][1]), fmaxf(z[s][2], z[s][3]));
-            const uint32_t k = __reduce_max_sync(0xffffffffu, key_of(m));
+            float m = max_nan(max_nan(z[s][0], z[s][1]), max_nan(z[s][2], z[s][3]));
+            uint32_t k = __reduce_max_sync(0xffffffffu, key_of(m));
+            if (k >= 0xff800000u) {                   // NaN or +inf among them
+                bad = true;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) z[s][j] = z[s][j] < INFINITY ? z[s][j] : -INFINITY;
+                m = fmaxf(fmaxf(z[s][0], z[s][1]), fmaxf(z[s][2], z[s][3]));
+                k = __reduce_max_sync(0xffffffffu, key_of(m));
+            }
             cmax = max(cmax, k);
             if (lane == s) mine = k;
         }
         if (lane < kSubs && c * kSubs + lane < g.ns) g.submax[r * g.ns + c * kSubs + lane] = z_of(mine);
         const float m = z_of(cmax);
-        const Knobs q = load_knobs(a, r);
         if (!q.total) continue;
         unsigned long long part = 0;
         int ref_out = 0;
@@ -294,16 +330,22 @@ __global__ void __launch_bounds__(kStatThreads, 3) stats_kernel(const SampleArgs
 #pragma unroll
                 for (int s = 0; s < kSubs; ++s) {
                     LaneSum acc;
+                    float hi[4], v[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const float x = fmaxf(z[s][j], zlow);
                         const float p = __fmul_rn(x, cs.hi);
                         const float e = fmaf(x, cs.lo, fmaf(x, cs.hi, -p));
-                        float hi, v;
-                        weight_pair(p, e, magic, tab, hi, v);
-                        const bool in = z[s][j] >= zlow;
-                        acc.add(in ? hi : 0.f, in ? v : 0.f);
+                        weight_pair(p, e, magic, tab, hi[j], v[j]);
                     }
+                    const float least = fminf(fminf(z[s][0], z[s][1]), fminf(z[s][2], z[s][3]));
+                    if (__any_sync(0xffffffffu, least < zlow)) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            if (z[s][j] < zlow) hi[j] = v[j] = 0.f;
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) acc.add(hi[j], v[j]);
                     const unsigned long long t = acc.warp_total();
                     if (lane == s) part = t;
                 }
@@ -447,11 +489,10 @@ struct Row {
         __syncthreads();
         return static_cast<int>(s.n_sub);
     }
-    // f(z, index) for the logits of the listed parts, by all lanes together, a warp a part with four
-    // parts' loads in flight; after(part) once a part.
-    template <typename F, typename G>
-    RL_DEVINL void each(F f, G after) {
-        bool bad = false;
+    // f(z[4], first index, part) for the logits of the listed parts, by all lanes together, a warp a
+    // part with four parts' loads in flight.
+    template <typename F>
+    RL_DEVINL void each(F f) {
         const int n = static_cast<int>(s.n_sub);
         for (int i0 = warp * 4; i0 < n; i0 += kSelWarps * 4) {
             float z[4][4];
@@ -459,14 +500,12 @@ struct Row {
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 part[q] = i0 + q < n ? subs[i0 + q] : -1;
-                if (part[q] >= 0) load4<T, kVec>(row, part[q] * kSub + lane * 4, V, z[q], bad);
+                if (part[q] >= 0) load4<T, kVec>(row, part[q] * kSub + lane * 4, V, z[q]);
             }
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 if (part[q] < 0) break;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) f(z[q][j], part[q] * kSub + lane * 4 + j);
-                after(part[q]);
+                f(z[q], part[q] * kSub + lane * 4, part[q]);
             }
         }
     }
@@ -476,53 +515,63 @@ struct Row {
         list_parts(lo);
         if (tid == 0) s.n_list = 0;
         __syncthreads();
-        LaneSum acc;
-        int n = 0, inside = 0;
         const float fb = static_cast<float>(k.b);
         const bool all_base = btie == INT_MAX && key_of(lo) >= bkey;
-        each([&](float z, int i) {
-                bool up, mid;
+        each([&](const float(&z)[4], int i0, int part) {
+            bool up[4], mid[4], any_up = false, any_mid = false;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
                 if (k.mode == 2) {
-                    const float x = fminf((k.hi - z) * k.scale, static_cast<float>(kBins - 1));
-                    up = x < fb;
-                    mid = !up && x < fb + 1.f;
+                    const float x = fminf((k.hi - z[j]) * k.scale, static_cast<float>(kBins - 1));
+                    up[j] = x < fb;
+                    mid[j] = !up[j] && x < fb + 1.f;
                 } else {
-                    const int pl = place(k, key_of(z));
-                    up = pl > 0;
-                    mid = pl == 0;
+                    const int pl = place(k, key_of(z[j]));
+                    up[j] = pl > 0;
+                    mid[j] = pl == 0;
                 }
-                const bool in_set = z >= lo && z > -INFINITY && (all_base || in_base(key_of(z), i));
-                up = up && in_set;
-                if (__any_sync(0xffffffffu, up)) {
-                    const bool w = up && z >= zlow;
-                    float p, e, hi, v;
-                    phase_rel(w ? z : M, M, c, p, e);
-                    weight_pair(p, e, 6144.f, s.tab, hi, v);
-                    acc.add(w ? hi : 0.f, w ? v : 0.f);
-                    n += up ? 1 : 0;
+                const bool in_set = z[j] >= lo && z[j] > -INFINITY && (all_base || in_base(key_of(z[j]), i0 + j));
+                up[j] = up[j] && in_set;
+                mid[j] = mid[j] && in_set;
+                any_up |= up[j];
+                any_mid |= mid[j];
+            }
+            if (__any_sync(0xffffffffu, any_up)) {
+                LaneSum acc;
+                int n = 0;
+                float hi[4], v[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const bool w = up[j] && z[j] >= zlow;
+                    float p, e;
+                    phase_rel(w ? z[j] : M, M, c, p, e);
+                    weight_pair(p, e, 6144.f, s.tab, hi[j], v[j]);
+                    if (!w) hi[j] = v[j] = 0.f;
+                    n += up[j] ? 1 : 0;
                 }
-                if (mid && in_set) {
-                    ++inside;
-                    const unsigned at = atomicAdd(&s.n_list, 1u);
-                    if (at < kListCap) s.comp[at] = (static_cast<unsigned long long>(key_of(z)) << 32) | static_cast<uint32_t>(~i);
-                }
-            },
-            [&](int part) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc.add(hi[j], v[j]);
                 n = __reduce_add_sync(0xffffffffu, n);
-                if (n) {
-                    const unsigned long long w = acc.warp_total();
-                    if (lane == 0) {
-                        cs[part] = w;
-                        cnt[part] = n;
+                const unsigned long long w = acc.warp_total();
+                if (lane == 0) {
+                    cs[part] = w;
+                    cnt[part] = n;
+                }
+            }
+            if (__any_sync(0xffffffffu, any_mid)) {
+                int inside = 0;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (mid[j]) {
+                        ++inside;
+                        const unsigned at = atomicAdd(&s.n_list, 1u);
+                        if (at < kListCap)
+                            s.comp[at] = (static_cast<unsigned long long>(key_of(z[j])) << 32) | static_cast<uint32_t>(~(i0 + j));
                     }
-                    acc = LaneSum();
-                }
-                if (__any_sync(0xffffffffu, inside)) {
-                    inside = __reduce_add_sync(0xffffffffu, inside);
-                    if (lane == 0) in[part] = inside;
-                }
-                n = inside = 0;
-            });
+                inside = __reduce_add_sync(0xffffffffu, inside);
+                if (lane == 0) in[part] = inside;
+            }
+        });
         __syncthreads();
     }
     // Totals over the parts: weight in units of 2^-44, numbers.
@@ -656,13 +705,20 @@ struct Row {
             __syncthreads();
             const float q = 2147483648.f / (static_cast<float>(mass) * 0x1p-44f);
             const bool all_base = btie == INT_MAX && key_of(lo) >= bkey;
-            each([&](float z, int i) {
-                    // a rounded weight: this only says where to look
-                    const uint32_t w = by_count ? 1u : __float2uint_rn(exp2_approx((z - M) * c.hi) * q);
-                    const float x = fminf((b.hi - z) * b.scale, static_cast<float>(kBins - 1));
-                    if (z >= lo && z > -INFINITY && w && (all_base || in_base(key_of(z), i))) atomicAdd(&h32[static_cast<int>(x)], w);
-                },
-                [](int) {});
+            each([&](const float(&z)[4], int i0, int) {
+                // a rounded weight: this only says where to look
+                uint32_t w[4];
+                int bin_of[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    w[j] = by_count ? 1u : __float2uint_rn(exp2_approx((z[j] - M) * c.hi) * q);
+                    bin_of[j] = static_cast<int>(fminf((b.hi - z[j]) * b.scale, static_cast<float>(kBins - 1)));
+                    if (!(z[j] >= lo && z[j] > -INFINITY) || !(all_base || in_base(key_of(z[j]), i0 + j))) w[j] = 0;
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (w[j]) atomicAdd(&h32[bin_of[j]], w[j]);
+            });
             __syncthreads();
             find_bin(h32, by_count ? static_cast<unsigned long long>(k) : static_cast<unsigned long long>(fmaxf(top_p, 0.f) * 2147483648.f),
                      kBins, bin, before, inside);
@@ -700,15 +756,17 @@ struct Row {
             list_parts(lo);
             for (int i = tid; i < kBins; i += kSelThreads) h64[i] = 0;
             __syncthreads();
-            each([&](float z, int i) {
-                    const uint32_t key = key_of(z);
-                    if (!(z >= lo && z > -INFINITY) || !in_base(key, i)) return;
-                    if (level > 0 && (key >> (shift + bits)) != prefix) return;
+            each([&](const float(&z)[4], int i0, int) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t key = key_of(z[j]);
+                    if (!(z[j] >= lo && z[j] > -INFINITY) || !in_base(key, i0 + j)) continue;
+                    if (level > 0 && (key >> (shift + bits)) != prefix) continue;
                     // descending order: bin 0 holds the largest digit
                     const uint32_t d = (1u << bits) - 1u - ((key >> shift) & ((1u << bits) - 1u));
-                    atomicAdd(&h64[d], by_count ? 1ull : weight(z) >> 6);
-                },
-                [](int) {});
+                    atomicAdd(&h64[d], by_count ? 1ull : weight(z[j]) >> 6);
+                }
+            });
             __syncthreads();
             find_bin(h64, rest, 1 << bits, bin, before, inside);
             rest = rest > before ? rest - before : 1;
@@ -761,10 +819,9 @@ struct Row {
         const int part = s.pick;
         __syncthreads();
         if (part >= 0 && warp == 0) {
-            bool bad = false;
             float z[4];
             const int i0 = part * kSub + lane * 4;
-            load4<T, kVec>(row, i0, V, z, bad);
+            load4<T, kVec>(row, i0, V, z);
             bool is[4];
             int m = 0, left = static_cast<int>(s.bin_lo), at = -1;
 #pragma unroll
@@ -802,10 +859,9 @@ struct Row {
         }
         const unsigned long long before = lo > 0 ? cs[lo - 1] : 0ull;
         const unsigned long long want = (target > before ? target - before : 0ull) << 6;
-        bool bad = false;
         float z[4];
         const int i0 = lo * kSub + lane * 4;
-        load4<T, kVec>(row, i0, V, z, bad);
+        load4<T, kVec>(row, i0, V, z);
         unsigned long long w[4], mine = 0;
         int my_last = -1;
         float my_z = 0.f;
@@ -919,8 +975,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SampleArgs
         const int sub = static_cast<int>(~block_max(first, s.red));
         if (w.warp == 0) {
             float z[4];
-            bool bad = false;
-            load4<T, kVec>(w.row, sub * kSub + w.lane * 4, V, z, bad);
+            load4<T, kVec>(w.row, sub * kSub + w.lane * 4, V, z);
             int at = INT_MAX;
 #pragma unroll
             for (int j = 3; j >= 0; --j)
@@ -1132,7 +1187,6 @@ __global__ void __launch_bounds__(kEmitThreads) emit_kernel(const SampleArgs g) 
     const int lane = threadIdx.x & 31;
     const int parts = gridDim.x;
     const int V = static_cast<int>(a.V);
-    bool bad = false;
     for (long long r = blockIdx.y; r < a.N; r += gridDim.y) {
         const RowRec rec = g.rec[r];
         const T* row = static_cast<const T*>(a.logits) + r * a.row_stride;
@@ -1180,7 +1234,7 @@ __global__ void __launch_bounds__(kEmitThreads) emit_kernel(const SampleArgs g) 
                     for (int q = 0; q < 4; ++q) {
                         part[q] = todo ? __ffs(todo) - 1 : -1;
                         todo &= todo - 1u;
-                        if (part[q] >= 0) load4<T, kVec>(row, (p0 + part[q]) * kSub + lane * 4, V, z[q], bad);
+                        if (part[q] >= 0) load4_raw<T, kVec>(row, (p0 + part[q]) * kSub + lane * 4, V, z[q]);
                     }
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
@@ -1191,7 +1245,7 @@ __global__ void __launch_bounds__(kEmitThreads) emit_kernel(const SampleArgs g) 
                         unsigned keeps = 0;
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
-                            const bool keep = z[q][j] > zk || (z[q][j] == zk && i0 + j <= rec.tie);
+                            const bool keep = (z[q][j] > zk && z[q][j] < INFINITY) || (z[q][j] == zk && i0 + j <= rec.tie);
                             const unsigned m = __ballot_sync(0xffffffffu, keep);
                             place += __popc(m & ((1u << lane) - 1u));
                             have += __popc(m);
@@ -1201,7 +1255,7 @@ __global__ void __launch_bounds__(kEmitThreads) emit_kernel(const SampleArgs g) 
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
                             if ((keeps >> j) & 1u) {
-                                kz[place] = z[q][j];
+                                kz[place] = z[q][j] + 0.f;
                                 ki[place] = static_cast<uint8_t>(lane * 4 + j);
                                 ++place;
                             }
@@ -1249,7 +1303,7 @@ template <typename T, bool kVec>
 static int sample_run(const SampleArgs& g, cudaStream_t stream) {
     const long long units = g.a.N * g.nc;
     long long blocks = (units + kStatThreads / 32 - 1) / (kStatThreads / 32);
-    const long long cap = 3ll * num_sms();
+    const long long cap = 2ll * num_sms();
     if (blocks > cap) blocks = cap;
     const size_t smem = sizeof(SelShared) + static_cast<size_t>(g.ns) * kSelPart;
     if (cudaFuncSetAttribute(select_kernel<T, kVec>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
