@@ -5,7 +5,7 @@
 // the total: a sum over up to the whole vocabulary decides which of two neighbours it is, so
 // fp32 sums would give another token every few thousand draws.  Weights and sums are therefore
 // carried to about 2^-37 of the largest weight:
-//   w = 2^p, p = (z - ref) log2(e) / T as a float pair (p, e);  p = n + j/2048 + r, exactly;
+//   w = 2^p, p = z log2(e) / T - ref with the factor as two floats;  p = n + j/2048 + r;
 //   2^(j/2048) = hi (1 + rho) from a table, 2^r - 1 = r ln2 + (r ln2)^2 / 2 (the next term is
 //   below 2^-40), so w = 2^n hi (1 + rho + ...) is the unevaluated pair (2^n hi, v).
 // fp64 would do the same at a fiftieth of the rate on this part.
@@ -190,37 +190,34 @@ RL_DEVINL float max_nan(float a, float b) {           // NaN if either is
 RL_DEVINL void fill_table(float2* tab, int tid, int threads) {
     for (int j = tid; j < 2048; j += threads) tab[j] = make_float2(__uint_as_float(kExpTable.bits[j]), kExpTable.rho[j]);
 }
-// 2^(p + e - ref) as hi + v, for p - ref in [-66, 1] and magic = 6144 - ref: 6144 + x has
-// 2^-11 as its last place, so the sum's bits are 0x45C00000 + 2048 n + j.
-RL_DEVINL void weight_pair(float p, float e, float magic, const float2* tab, float& hi, float& v) {
-    const float t = __fadd_rn(p, magic);
-    const float r = __fadd_rn(__fsub_rn(p, __fsub_rn(t, magic)), e);
+// 2^(x c - ref) as hi + v, for x c - ref in [-66, 1] and magic = 6144 - ref: the last place of
+// 6144 + y is 2^-11, so the bits of t are 0x45C00000 + 2048 n + j for the nearest n + j/2048, and
+// what is left of x c, r, comes from one more product.  (x + x_lo for an argument of two floats.)
+RL_DEVINL void weight_pair(float x, float x_lo, FF c, float magic, const float2* tab, float& hi, float& v) {
+    const float t = fmaf(x, c.hi, magic);
+    float r = fmaf(x, c.hi, -__fsub_rn(t, magic));
+    r = fmaf(x, c.lo, r);
+    r = fmaf(x_lo, c.hi, r);
     const uint32_t tb = __float_as_uint(t);
     const float2 q = tab[tb & 2047u];
     hi = __uint_as_float(__float_as_uint(q.x) + (tb << 12));
     v = hi * fmaf(r, fmaf(r, 0.24022650695910072f, 0.69314718055994531f), q.y);
 }
-// p, e of (z - m) * c
-RL_DEVINL void phase_rel(float z, float m, FF c, float& p, float& e) {
-    const FF d = two_sum(z, -m);
-    p = __fmul_rn(d.hi, c.hi);
-    e = fmaf(d.lo, c.hi, fmaf(d.hi, c.lo, fmaf(d.hi, c.hi, -p)));
-}
-// Sum of up to four weights of at most 1 in a lane: the high part on a grid of 2^-19, where such
-// sums are exact, the rest apart; a warp's total in units of 2^-50, rounded at 2^-39 a lane.
-// Both become integers through the bits of a sum with a constant of the right last place.
+// Sum of up to four weights of at most 1 in a lane, hi + v each: in a float that starts at 24, so
+// that it only takes whole steps of 2^-19, and the rest apart.  Both become integers through
+// their bits; a warp's total is (top << 31) + (low << 11) in units of 2^-50, rounded at 2^-39 a lane.
 struct LaneSum {
-    float top = 0.f, low = 0.f;
+    float top = 24.f, low = 0.f;
     RL_DEVINL void add(float hi, float v) {
-        const float wh = __fadd_rn(hi, v), wl = __fsub_rn(v, __fsub_rn(wh, hi));
-        const float t = __fsub_rn(__fadd_rn(wh, 24.f), 24.f);
-        top += t;
-        low += __fsub_rn(wh, t);
-        low += wl;
+        const float n = __fadd_rn(top, __fadd_rn(hi, v));
+        low += __fadd_rn(__fsub_rn(hi, __fsub_rn(n, top)), v);
+        top = n;
     }
-    RL_DEVINL unsigned long long warp_total() const {
-        const uint32_t a = __reduce_add_sync(0xffffffffu, __float_as_uint(__fadd_rn(top, 24.f)) - 0x41c00000u);
-        const int b = __reduce_add_sync(0xffffffffu, static_cast<int>(__float_as_uint(__fadd_rn(low, 0x1.8p-16f)) - 0x37c00000u));
+    RL_DEVINL uint32_t warp_top() const { return __reduce_add_sync(0xffffffffu, __float_as_uint(top) - 0x41c00000u); }
+    RL_DEVINL int warp_low() const {
+        return __reduce_add_sync(0xffffffffu, static_cast<int>(__float_as_uint(__fadd_rn(low, 0x1.8p-16f)) - 0x37c00000u));
+    }
+    static RL_DEVINL unsigned long long total(uint32_t a, int b) {
         const long long w = (static_cast<long long>(a) << 31) + (static_cast<long long>(b) << 11);
         return w > 0 ? static_cast<unsigned long long>(w) : 0ull;
     }
@@ -229,9 +226,9 @@ struct LaneSum {
 // -FLT_MAX: below it the weight is 0 (M itself where the difference is lost).
 RL_DEVINL unsigned long long weight_fixed(float z, float M, FF c, float zlow, const float2* tab) {
     if (!(z >= zlow)) return 0ull;
-    float p, e, hi, v;
-    phase_rel(z, M, c, p, e);
-    weight_pair(p, e, 6144.f, tab, hi, v);
+    float hi, v;
+    const FF d = two_sum(z, -M);
+    weight_pair(d.hi, d.lo, c, 6144.f, tab, hi, v);
     const float wh = __fadd_rn(hi, v), wl = __fsub_rn(v, __fsub_rn(wh, hi));
     if (!(wh < 2.f)) return 0ull;             // differences past the range of floats
     const uint32_t b = __float_as_uint(wh);
@@ -319,8 +316,8 @@ __global__ void __launch_bounds__(kStatThreads, 2) stats_kernel(const SampleArgs
         if (lane < kSubs && c * kSubs + lane < g.ns) g.submax[r * g.ns + c * kSubs + lane] = z_of(mine);
         const float m = z_of(cmax);
         if (!q.total) continue;
-        unsigned long long part = 0;
-        int ref_out = 0;
+        uint32_t part_top = 0;
+        int part_low = 0, ref_out = 0;
         if (m > -INFINITY) {
             const FF cs = scale_of(q.T);
             const float pm = m * cs.hi;
@@ -333,10 +330,7 @@ __global__ void __launch_bounds__(kStatThreads, 2) stats_kernel(const SampleArgs
                     float hi[4], v[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        const float x = fmaxf(z[s][j], zlow);
-                        const float p = __fmul_rn(x, cs.hi);
-                        const float e = fmaf(x, cs.lo, fmaf(x, cs.hi, -p));
-                        weight_pair(p, e, magic, tab, hi[j], v[j]);
+                        weight_pair(fmaxf(z[s][j], zlow), 0.f, cs, magic, tab, hi[j], v[j]);
                     }
                     const float least = fminf(fminf(z[s][0], z[s][1]), fminf(z[s][2], z[s][3]));
                     if (__any_sync(0xffffffffu, least < zlow)) {
@@ -346,8 +340,12 @@ __global__ void __launch_bounds__(kStatThreads, 2) stats_kernel(const SampleArgs
                     }
 #pragma unroll
                     for (int j = 0; j < 4; ++j) acc.add(hi[j], v[j]);
-                    const unsigned long long t = acc.warp_total();
-                    if (lane == s) part = t;
+                    const uint32_t t = acc.warp_top();
+                    const int l = acc.warp_low();
+                    if (lane == s) {
+                        part_top = t;
+                        part_low = l;
+                    }
                 }
             } else {
                 const float zlow = fmaxf(m - 64.f / cs.hi, -FLT_MAX);
@@ -358,17 +356,21 @@ __global__ void __launch_bounds__(kStatThreads, 2) stats_kernel(const SampleArgs
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const bool in = z[s][j] >= zlow;
-                        float p, e, hi, v;
-                        phase_rel(in ? z[s][j] : m, m, cs, p, e);
-                        weight_pair(p, e, 6144.f, tab, hi, v);
+                        float hi, v;
+                        const FF d = two_sum(in ? z[s][j] : m, -m);
+                        weight_pair(d.hi, d.lo, cs, 6144.f, tab, hi, v);
                         acc.add(in ? hi : 0.f, in ? v : 0.f);
                     }
-                    const unsigned long long t = acc.warp_total();
-                    if (lane == s) part = t;
+                    const uint32_t t = acc.warp_top();
+                    const int l = acc.warp_low();
+                    if (lane == s) {
+                        part_top = t;
+                        part_low = l;
+                    }
                 }
             }
         }
-        if (lane < kSubs && c * kSubs + lane < g.ns) g.subsum[r * g.ns + c * kSubs + lane] = part;
+        if (lane < kSubs && c * kSubs + lane < g.ns) g.subsum[r * g.ns + c * kSubs + lane] = LaneSum::total(part_top, part_low);
         if (lane == 0) g.ref[r * g.nc + c] = ref_out;
     }
     if (bad) set_status(g.status, RL_STATUS_NONFINITE);
@@ -543,18 +545,18 @@ struct Row {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const bool w = up[j] && z[j] >= zlow;
-                    float p, e;
-                    phase_rel(w ? z[j] : M, M, c, p, e);
-                    weight_pair(p, e, 6144.f, s.tab, hi[j], v[j]);
+                    const FF d = two_sum(w ? z[j] : M, -M);
+                    weight_pair(d.hi, d.lo, c, 6144.f, s.tab, hi[j], v[j]);
                     if (!w) hi[j] = v[j] = 0.f;
                     n += up[j] ? 1 : 0;
                 }
 #pragma unroll
                 for (int j = 0; j < 4; ++j) acc.add(hi[j], v[j]);
                 n = __reduce_add_sync(0xffffffffu, n);
-                const unsigned long long w = acc.warp_total();
+                const uint32_t wt = acc.warp_top();
+                const int wl = acc.warp_low();
                 if (lane == 0) {
-                    cs[part] = w;
+                    cs[part] = LaneSum::total(wt, wl);
                     cnt[part] = n;
                 }
             }
@@ -1012,7 +1014,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SampleArgs
             const float pm = __fmul_rn(M, w.c.hi);
             if (fabsf(pm) < kWholeRef) {
                 float hi, v;
-                weight_pair(-pm, -fmaf(M, w.c.lo, fmaf(M, w.c.hi, -pm)), 6144.f + ceilf(pm), s.tab, hi, v);
+                weight_pair(-M, 0.f, w.c, 6144.f + ceilf(pm), s.tab, hi, v);
                 s.unit = (static_cast<unsigned long long>(hi * 8388608.f) << 39) + static_cast<long long>(v * 0x1p62f);
             }
         }
