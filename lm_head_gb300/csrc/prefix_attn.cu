@@ -11,8 +11,11 @@
 //                       key head, times the step's tokens): four warps, each with 16 of a stage's 64
 //                       keys and statistics of its own, joined at the end.  Keys and values come by
 //                       TMA, page by page, into a ring of stages; a fifth warp issues the copies.
-//  2. join_kernel       one warp a row.
+//  2. tile_attn_kernel  a part with more rows, on the 5th-generation tensor cores
+//                       (prefix_attn_tc.cuh).
+//  3. join_kernel       one warp a row.
 #include <climits>
+#include <type_traits>
 
 #include <cuda_fp16.h>
 
@@ -32,6 +35,7 @@ struct AttnArgs {
     int sp, so;           // parts of the prefix, of the own keys
     int chunk_p, chunk_o; // keys of a part, multiples of kStageKeys
     int tiles_p, tiles_o; // row tiles: of all groups together, of one request
+    int run_p, run_o;     // whether the launch does the prefixes' parts, the own keys' parts
     float* ml;            // [sp + so][T * Hq][2]: max (in log2 units), sum
     float* po;            // [sp + so][T * Hq][D] numerators
 };
@@ -55,7 +59,7 @@ RL_DEVINL int clamp_t(int x, long long T) { return static_cast<int>(min(max(stat
 RL_DEVINL bool find_item(const AttnArgs& p, long long id, int tile_rows, Item& it, int& bits) {
     const rl_prefix_attn_args& a = p.a;
     const int lane = threadIdx.x & 31;
-    const long long prefix_items = static_cast<long long>(p.sp) * a.Hkv * p.tiles_p;
+    const long long prefix_items = p.run_p ? static_cast<long long>(p.sp) * a.Hkv * p.tiles_p : 0;
     if (id < prefix_items) {
         const int split = static_cast<int>(id % p.sp);
         it.h = static_cast<int>(id / p.sp % a.Hkv);
@@ -142,6 +146,19 @@ RL_DEVINL int page_of(const AttnArgs& p, const int32_t* table, int k, int shift,
     return page;
 }
 
+// Rows past the last request, where no join follows that writes them.
+template <typename T, int D>
+RL_DEVINL void clear_padding(const AttnArgs& p, int threads) {
+    const rl_prefix_attn_args& a = p.a;
+    const int tr = a.R > 0 ? clamp_t(a.cu_q[a.R], a.T) : 0;
+    for (long long t = tr + static_cast<long long>(blockIdx.x); t < a.T; t += gridDim.x) {
+        for (int x = threadIdx.x; x < a.Hq * D / 8; x += threads)
+            reinterpret_cast<uint4*>(static_cast<T*>(a.out) + t * a.Hq * D)[x] = make_uint4(0, 0, 0, 0);
+        if (a.lse)
+            for (int x = threadIdx.x; x < a.Hq; x += threads) a.lse[t * a.Hq + x] = -INFINITY;
+    }
+}
+
 template <typename T>
 struct Mma;
 template <>
@@ -212,16 +229,7 @@ __global__ void __launch_bounds__(kWarpThreads)
     }
     Item it;
     int bits = 0;
-    if (p.sp + p.so == 1) {
-        // no join follows: rows of no request are written here
-        const int tr = a.R > 0 ? clamp_t(a.cu_q[a.R], a.T) : 0;
-        for (long long t = tr + static_cast<long long>(blockIdx.x); t < a.T; t += gridDim.x) {
-            for (int x = threadIdx.x; x < a.Hq * D / 8; x += kWarpThreads)
-                reinterpret_cast<uint4*>(static_cast<T*>(a.out) + t * a.Hq * D)[x] = make_uint4(0, 0, 0, 0);
-            if (a.lse)
-                for (int x = threadIdx.x; x < a.Hq; x += kWarpThreads) a.lse[t * a.Hq + x] = -INFINITY;
-        }
-    }
+    if (p.sp + p.so == 1) clear_padding<T, D>(p, kWarpThreads);
     const bool any = find_item(p, blockIdx.x, kWarpRows, it, bits);   // every warp for itself
     __syncthreads();
     if (!any) {
@@ -453,7 +461,13 @@ __global__ void __launch_bounds__(kWarpThreads)
     }
 }
 
-// ---- 2. the parts of a row joined -----------------------------------------------------
+}  // namespace rl
+
+#include "prefix_attn_tc.cuh"
+
+namespace rl {
+
+// ---- 3. the parts of a row joined -----------------------------------------------------
 constexpr int kJoinThreads = 256;
 
 template <typename T, int D>
@@ -506,33 +520,45 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttnArgs p) {
 }
 
 // ---- host ------------------------------------------------------------------------------
-// How the keys are cut into parts: so many that the parts of all row tiles fill the device a few
-// times, none shorter than 256 keys.
-static int parts_of(int64_t keys, int64_t items, int64_t target, int* chunk) {
-    int64_t n = items > 0 ? (target + items - 1) / items : 1;
+// Which kernel does the parts with so many query rows: mma.sync tiles of 16 (kWarp), one tensor-core
+// tile of 128 rows that takes two key tiles at a time (kKeys: bound by reading the keys), or two
+// tiles of rows (kRows: bound by the products and exponentials).
+enum AttnKind { kWarp = 0, kKeys = 1, kRows = 2 };
+static AttnKind kind_of(int64_t rows) { return rows <= kWarpRows ? kWarp : rows <= kTileRows ? kKeys : kRows; }
+static int rows_of(AttnKind k) { return k == kWarp ? kWarpRows : k == kKeys ? kTileRows : 2 * kTileRows; }
+
+// How the keys are cut into parts: as many as let the blocks of all row tiles fill the device (the
+// light blocks of kWarp several times over; kRows once, since each part of its rows costs a
+// numerator to write and read again), none shorter than 256 keys.
+static int parts_of(AttnKind kind, int64_t keys, int64_t items, int* chunk) {
+    const int64_t target = (kind == kWarp ? 4ll : kind == kKeys ? 2ll : 1ll) * num_sms();
+    const int64_t unit = kind == kWarp ? kStageKeys : kTileKeys;
+    int64_t n = items > 0 ? (kind == kWarp ? (target + items - 1) / items : target / items) : 1;
     const int64_t most = (keys + 255) / 256;
     if (n > most) n = most;
     if (n > 64) n = 64;
     if (n < 1) n = 1;
     int64_t c = (keys + n - 1) / n;
-    c = (c + kStageKeys - 1) / kStageKeys * kStageKeys;
-    if (c < kStageKeys) c = kStageKeys;
+    c = (c + unit - 1) / unit * unit;
+    if (c < unit) c = unit;
     *chunk = static_cast<int>(c);
     return static_cast<int>(keys > 0 ? (keys + c - 1) / c : 1);
 }
 
-static AttnArgs attn_view(const rl_prefix_attn_args* a, void* ws, size_t* bytes) {
+static AttnArgs attn_view(const rl_prefix_attn_args* a, void* ws, size_t* bytes, AttnKind* kp, AttnKind* ko) {
     AttnArgs p{};
     p.a = *a;
     p.gq = a->Hq / a->Hkv;
     p.c = a->scale * kLog2e;
     const bool prefix = a->G > 0 && a->max_prefix > 0;
-    p.tiles_p = prefix ? static_cast<int>(a->T * p.gq / kWarpRows + a->G) : 0;
-    p.tiles_o = static_cast<int>((a->max_q * p.gq + kWarpRows - 1) / kWarpRows);
-    const int64_t items_p = static_cast<int64_t>(p.tiles_p) * a->Hkv, items_o = a->R * p.tiles_o * a->Hkv;
-    const int64_t target = 4ll * num_sms();
-    p.sp = prefix ? parts_of(a->max_prefix, items_p, target, &p.chunk_p) : 0;
-    p.so = parts_of(a->max_kv, items_o, target, &p.chunk_o);
+    *kp = kind_of(prefix ? (a->T * p.gq + a->G - 1) / a->G : 0);
+    *ko = kind_of(a->max_q * p.gq);
+    const int rp = rows_of(*kp), ro = rows_of(*ko);
+    p.tiles_p = prefix ? static_cast<int>(a->T * p.gq / rp + a->G) : 0;      // a bound: each group rounds up once
+    p.tiles_o = static_cast<int>((a->max_q * p.gq + ro - 1) / ro);
+    const int64_t about = a->T * p.gq / rp > a->G ? a->T * p.gq / rp : a->G; // row tiles to expect
+    p.sp = prefix ? parts_of(*kp, a->max_prefix, about * a->Hkv, &p.chunk_p) : 0;
+    p.so = parts_of(*ko, a->max_kv, a->R * p.tiles_o * a->Hkv, &p.chunk_o);
     Carve cv(ws);
     const size_t rows = static_cast<size_t>(a->T) * a->Hq;
     const int parts = p.sp + p.so;
@@ -546,35 +572,55 @@ static AttnArgs attn_view(const rl_prefix_attn_args* a, void* ws, size_t* bytes)
 
 size_t prefix_attn_ws_bytes(const rl_prefix_attn_args* a) {
     size_t b = 0;
-    attn_view(a, nullptr, &b);
+    AttnKind kp, ko;
+    attn_view(a, nullptr, &b, &kp, &ko);
     return b;
 }
 
 template <typename T, int D>
-static int attn_run(const AttnArgs& p, cudaStream_t stream) {
+static int launch_parts(AttnArgs p, AttnKind kind, bool prefix, bool own, cudaStream_t stream, int* launches) {
     const rl_prefix_attn_args& a = p.a;
-    CUtensorMap tmK, tmV;
-    const int64_t rows = a.n_pages * a.Hkv * a.page_size;
-    const int box = a.page_size < kStageKeys ? a.page_size : kStageKeys;
-    const CUtensorMapDataType dt = a.dtype == RL_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-    int rc = make_tmap_2d(&tmK, a.k_cache, dt, 2, rows, D, D, 64, box, 128);
-    if (rc == RL_OK) rc = make_tmap_2d(&tmV, a.v_cache, dt, 2, rows, D, D, 64, box, 128);
-    if (rc != RL_OK) return rc;
-    if (cudaFuncSetAttribute(warp_attn_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, warp_smem_bytes<D>()) != cudaSuccess)
-        return RL_ERR_CUDA;
-    const int64_t items = static_cast<int64_t>(p.sp) * a.Hkv * p.tiles_p + static_cast<int64_t>(p.so) * a.Hkv * a.R * p.tiles_o;
+    p.run_p = prefix;
+    p.run_o = own;
+    const int64_t items = (prefix ? static_cast<int64_t>(p.sp) * a.Hkv * p.tiles_p : 0) +
+                          (own ? static_cast<int64_t>(p.so) * a.Hkv * a.R * p.tiles_o : 0);
+    if (items == 0) return RL_OK;
     if (items >= INT_MAX) {
         set_last_error("too many parts for one launch");
         return RL_ERR_UNSUPPORTED;
     }
+    CUtensorMap tmK, tmV;
+    const int64_t rows = a.n_pages * a.Hkv * a.page_size;
+    const int most = kind == kWarp ? kStageKeys : kTileKeys;
+    const int box = a.page_size < most ? a.page_size : most;
+    const CUtensorMapDataType dt = a.dtype == RL_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    int rc = make_tmap_2d(&tmK, a.k_cache, dt, 2, rows, D, D, 64, box, 128);
+    if (rc == RL_OK) rc = make_tmap_2d(&tmV, a.v_cache, dt, 2, rows, D, D, 64, box, 128);
+    if (rc != RL_OK) return rc;
+    const auto kernel = kind == kWarp ? warp_attn_kernel<T, D> : kind == kKeys ? tile_attn_kernel<T, D, true> : tile_attn_kernel<T, D, false>;
+    const int smem = kind == kWarp   ? warp_smem_bytes<D>()
+                     : kind == kKeys ? TileShape<D, true>::kSmemBytes
+                                     : TileShape<D, false>::kSmemBytes;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return RL_ERR_CUDA;
+    kernel<<<static_cast<unsigned>(items), kind == kWarp ? kWarpThreads : kTileThreads, smem, stream>>>(tmK, tmV, p);
+    ++*launches;
+    return RL_OK;
+}
+
+template <typename T, int D>
+static int attn_run(const AttnArgs& p, AttnKind kp, AttnKind ko, cudaStream_t stream) {
+    const rl_prefix_attn_args& a = p.a;
     ProfScope prof(RL_PROF_OTHER, stream);
-    int launches = 0;
-    if (items > 0) {
-        warp_attn_kernel<T, D><<<static_cast<unsigned>(items), kWarpThreads, warp_smem_bytes<D>(), stream>>>(tmK, tmV, p);
-        ++launches;
+    int launches = 0, rc;
+    if (p.sp > 0 && kp == ko) {
+        rc = launch_parts<T, D>(p, kp, true, true, stream, &launches);
+    } else {
+        rc = p.sp > 0 ? launch_parts<T, D>(p, kp, true, false, stream, &launches) : RL_OK;
+        if (rc == RL_OK) rc = launch_parts<T, D>(p, ko, false, true, stream, &launches);
     }
+    if (rc != RL_OK) return rc;
     const int64_t rows_q = a.T * a.Hq;
-    if (p.sp + p.so > 1 || items == 0) {
+    if (p.sp + p.so > 1 || launches == 0) {
         join_kernel<T, D><<<static_cast<unsigned>((rows_q + kJoinThreads / 32 - 1) / (kJoinThreads / 32)), kJoinThreads, 0, stream>>>(p);
         ++launches;
     }
@@ -584,11 +630,13 @@ static int attn_run(const AttnArgs& p, cudaStream_t stream) {
 
 int prefix_attn_impl(const rl_prefix_attn_args* a, void* ws, int32_t* status, cudaStream_t stream) {
     if (a->T == 0) return RL_OK;
-    AttnArgs p = attn_view(a, ws, nullptr);
+    AttnKind kp, ko;
+    AttnArgs p = attn_view(a, ws, nullptr, &kp, &ko);
     p.status = status;
     p.wait_ns = wait_limit_ns();
-    if (a->dtype == RL_DTYPE_BF16) return a->D == 128 ? attn_run<__nv_bfloat16, 128>(p, stream) : attn_run<__nv_bfloat16, 64>(p, stream);
-    return a->D == 128 ? attn_run<__half, 128>(p, stream) : attn_run<__half, 64>(p, stream);
+    if (a->dtype == RL_DTYPE_BF16)
+        return a->D == 128 ? attn_run<__nv_bfloat16, 128>(p, kp, ko, stream) : attn_run<__nv_bfloat16, 64>(p, kp, ko, stream);
+    return a->D == 128 ? attn_run<__half, 128>(p, kp, ko, stream) : attn_run<__half, 64>(p, kp, ko, stream);
 }
 
 }  // namespace rl

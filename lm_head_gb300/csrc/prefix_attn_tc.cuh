@@ -1,0 +1,481 @@
+// Attention parts on the 5th-generation tensor cores, for parts with more than 16 query rows.
+//
+// One block, 384 threads, 128 keys a step:
+//   warp 0       copies K and V tiles, page by page, into a ring of shared-memory units (TMA);
+//                pages past the last key are filled with zeros by a copy that starts past the cache
+//   warp 1       issues the products, one lane:  S = Q K^T (both in shared memory),
+//                O += P V (P in TMEM, V in shared memory, key-major)
+//   warps 4-7    softmax of accumulator 0, a thread a row: its 128 scores come from TMEM at once,
+//   warps 8-11   of accumulator 1;  P goes back to TMEM over the scores
+// TMEM: S0, S1 (128 columns each), O0, O1 (D columns each).  While one accumulator's scores are
+// exponentiated the tensor core works on the other's products.  The two accumulators are
+//   kKeys2 = false   two tiles of 128 rows over the same keys (256 rows a block)
+//   kKeys2 = true    the even and the odd key tiles of one tile of up to 128 rows, joined at the
+//                    end through shared memory: for parts that are bound by reading the keys
+// The running maximum is only followed when it grows by more than 2^8: until then the weights
+// stay below 2^8 of it and O is left alone.  That O may be rescaled is known from the scores'
+// barrier: the scores' product was issued after the last product into O.
+//
+// Every wait is bounded; a wait that runs out raises the block's abort flag, all roles leave
+// their loops, and copies and products in flight are waited for before TMEM is released.
+#pragma once
+
+#include "gemm_tc.cuh"
+#include "internal.h"
+
+namespace rl {
+
+constexpr int kTileRows = 128;
+constexpr int kTileKeys = 128;
+constexpr int kTileThreads = 384;
+
+template <int D, bool kKeys2>
+struct TileShape {
+    static constexpr int kUnitBytes = kTileKeys * D * 2;
+    static constexpr int kQTiles = kKeys2 ? 1 : 2;
+    static constexpr int kQBytes = kQTiles * kTileRows * D * 2;
+    static constexpr int kUnits = D == 128 ? (kKeys2 ? 5 : 4) : 8;
+    // the join of the two accumulators reuses the ring: O1 and (m, l) of 128 rows
+    static constexpr int kSmemBytes = kUnits * kUnitBytes + kQBytes + 1024 + 256;
+    static_assert(kUnits * kUnitBytes >= kTileRows * (D + 4) * 4 + kTileRows * 8, "the ring holds the join's data");
+};
+
+template <typename T>
+constexpr uint32_t tile_idesc(uint32_t n, bool b_mn) {
+    return (std::is_same<T, __nv_bfloat16>::value ? idesc_bf16_f32(kTileRows, n)
+                                                  : ((1u << 4) | ((n >> 3) << 17) | ((kTileRows >> 4) << 24))) |
+           (b_mn ? 1u << 16 : 0u);
+}
+// D[tmem] (+)= A[tmem] * B[smem]^T
+RL_DEVINL void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+RL_DEVINL void tmem_st_32x32(uint32_t taddr, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+RL_DEVINL void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+template <typename T, int D, bool kKeys2>
+__global__ void __launch_bounds__(kTileThreads, 1)
+    tile_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const AttnArgs p) {
+    using Shape = TileShape<D, kKeys2>;
+    constexpr int kUnits = Shape::kUnits, kUnit = Shape::kUnitBytes;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    uint8_t* sq = smem + kUnits * kUnit;
+    uint64_t* full = reinterpret_cast<uint64_t*>(sq + Shape::kQBytes);
+    uint64_t* empty = full + kUnits;
+    uint64_t* s_full = empty + kUnits;      // [2] scores of an accumulator are in TMEM
+    uint64_t* p_ready = s_full + 2;         // [2] its weights are
+    uint64_t* o_full = p_ready + 2;         // [2] its last product is done
+    uint64_t* done_bar = o_full + 2;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done_bar + 1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    const rl_prefix_attn_args& a = p.a;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (p.sp + p.so == 1) clear_padding<T, D>(p, kTileThreads);
+    Item it;
+    int bits = 0;
+    constexpr int kItemRows = kKeys2 ? kTileRows : 2 * kTileRows;
+    if (!find_item(p, blockIdx.x, kItemRows, it, bits)) {             // every warp for itself, all alike
+        if (threadIdx.x == 0) set_status(p.status, bits);
+        return;
+    }
+    const int rows = min(it.rows - it.m0, kItemRows);                 // of this block, at least 1
+    const int n = it.k1 > it.k0 ? (it.k1 - it.k0 + kTileKeys - 1) / kTileKeys : 0;
+    const bool two = kKeys2 ? n > 1 : rows > kTileRows;               // the second accumulator is in use
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kUnits; ++s) {
+            mbar_init(full + s, 1);
+            mbar_init(empty + s, 1);
+        }
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(s_full + t, 1);
+            mbar_init(p_ready + t, 4);
+            mbar_init(o_full + t, 1);
+        }
+        mbar_init(done_bar, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&tmK);
+        tma_prefetch_desc(&tmV);
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+    }
+    // queries: rows of 128 bytes with the 128-byte swizzle, 64 columns a sub-tile; zeros past the rows
+    if (n > 0)
+        for (int x = threadIdx.x; x < Shape::kQTiles * kTileRows * (D / 8); x += kTileThreads) {
+            const int r = x / (D / 8), ch = x % (D / 8);
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (r < rows) {
+                const int m = it.m0 + r;
+                v = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + (it.t0 + m / p.gq) * a.q_stride_t +
+                                                    static_cast<int64_t>(it.h * p.gq + m % p.gq) * a.q_stride_h + ch * 8);
+            }
+            const int tile = r / kTileRows, rr = r % kTileRows;
+            *reinterpret_cast<uint4*>(sq + tile * kTileRows * D * 2 + (ch >> 3) * kTileRows * 128 + rr * 128 +
+                                      (((ch & 7) ^ (rr & 7)) << 4)) = v;
+        }
+    fence_proxy_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    if (warp == 0) {
+        // ---------------- copies ----------------
+        const int box = min(a.page_size, kTileKeys);
+        const int per = kTileKeys / box;
+        const int shift = 31 - __clz(a.page_size);
+        const int past = static_cast<int>(a.n_pages * a.Hkv * a.page_size);     // a row past the cache: zeros
+        int unit = 0;
+        uint32_t phase = 0;
+        int issued = 0;
+        bool ok = true;
+        auto load = [&](const CUtensorMap* map, int tile) {
+            const int key = it.k0 + tile * kTileKeys + lane * box;
+            int row = past;
+            if (lane < per && key < it.k1)
+                row = (page_of(p, it.table, key, shift, bits) * a.Hkv + it.h) * a.page_size + (key & (a.page_size - 1));
+            ok = mbar_wait(empty + unit, phase ^ 1u, p.status, p.wait_ns) && !*abort_flag;
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) {
+                *abort_flag = 1;
+                return;
+            }
+            if (lane == 0) mbar_arrive_expect_tx(full + unit, kUnit);
+            __syncwarp();
+            if (lane < per)
+#pragma unroll
+                for (int x = 0; x < D / 64; ++x)
+                    tma_load_2d(map, full + unit, smem + unit * kUnit + x * kTileKeys * 128 + lane * box * 128, x * 64, row);
+            ++issued;
+            if (++unit == kUnits) {
+                unit = 0;
+                phase ^= 1u;
+            }
+        };
+        if (kKeys2) {
+            for (int i = 0; i < 2 && i < n && ok; ++i) load(&tmK, i);
+            for (int i = 0; i < n && ok; ++i) {
+                load(&tmV, i);
+                if (i + 2 < n && ok) load(&tmK, i + 2);
+            }
+        } else {
+            for (int i = 0; i < n && ok; ++i) {
+                load(&tmK, i);
+                if (ok) load(&tmV, i);
+            }
+        }
+        set_status(p.status, bits);
+        __syncwarp();
+        if (!ok && lane == 0)       // what was issued lands before the block can end
+            for (int s = max(0, issued - kUnits); s < issued; ++s) mbar_wait(full + s % kUnits, (s / kUnits) & 1, p.status);
+    } else if (warp == 1) {
+        if (lane == 0 && n > 0) {
+            // ---------------- products ----------------
+            constexpr uint32_t kIdescS = tile_idesc<T>(kTileKeys, false), kIdescO = tile_idesc<T>(D, true);
+            int unit = 0;
+            uint32_t phase = 0;
+            bool ok = true, issued = false;
+            auto wait_unit = [&]() {
+                ok = ok && mbar_wait(full + unit, phase, p.status, p.wait_ns) && !*abort_flag;
+                tc_fence_after();
+            };
+            auto next_unit = [&]() {
+                umma_commit(empty + unit);
+                if (++unit == kUnits) {
+                    unit = 0;
+                    phase ^= 1u;
+                }
+            };
+            auto scores = [&](int t) {
+                const uint32_t k = smem_addr(smem + unit * kUnit), q = smem_addr(sq) + (kKeys2 ? 0 : t * kTileRows * D * 2);
+#pragma unroll
+                for (int x = 0; x < D / 16; ++x) {
+                    const uint32_t off = (x >> 2) * 128 * 128 + (x & 3) * 32;
+                    umma_bf16(tmem + t * kTileKeys, sdesc_kmajor_sw128(q + off), sdesc_kmajor_sw128(k + off), kIdescS, x != 0);
+                }
+                issued = true;
+                umma_commit(s_full + t);
+            };
+            auto values = [&](int t, bool first) {
+                const uint32_t v = smem_addr(smem + unit * kUnit);
+#pragma unroll
+                for (int x = 0; x < kTileKeys / 16; ++x)
+                    umma_ts(tmem + 2 * kTileKeys + t * D, tmem + t * kTileKeys + x * 8,
+                            sdesc_mnmajor_sw128(v + x * 2048, kTileKeys * 128), kIdescO, !(first && x == 0));
+            };
+            auto wait_p = [&](int t, int i) {
+                ok = ok && mbar_wait(p_ready + t, i & 1, p.status, p.wait_ns) && !*abort_flag;
+                tc_fence_after();
+            };
+            if (kKeys2) {
+                for (int i = 0; i < 2 && i < n; ++i) {
+                    wait_unit();
+                    if (!ok) break;
+                    scores(i);
+                    next_unit();
+                }
+                for (int i = 0; i < n && ok; ++i) {
+                    const int t = i & 1;
+                    wait_p(t, i >> 1);
+                    wait_unit();
+                    if (!ok) break;
+                    values(t, i < 2);
+                    next_unit();
+                    if (i + 2 >= n) umma_commit(o_full + t);
+                    if (i + 2 < n) {
+                        wait_unit();
+                        if (!ok) break;
+                        scores(t);
+                        next_unit();
+                    }
+                }
+            } else {
+                wait_unit();
+                if (ok) {
+                    scores(0);
+                    if (two) scores(1);
+                    next_unit();
+                }
+                for (int i = 0; i < n && ok; ++i) {
+                    // V of this step is the current unit, K of the next step the one after it
+                    const int vu = unit;
+                    const uint32_t vp = phase;
+                    for (int t = 0; t < (two ? 2 : 1); ++t) {
+                        wait_p(t, i);
+                        unit = vu;
+                        phase = vp;
+                        if (t == 0) wait_unit();
+                        if (!ok) break;
+                        values(t, i == 0);
+                        if (i + 1 == n) umma_commit(o_full + t);
+                        const bool last_t = t == 1 || !two;
+                        if (last_t) umma_commit(empty + unit);
+                        if (++unit == kUnits) {
+                            unit = 0;
+                            phase ^= 1u;
+                        }
+                        if (i + 1 < n) {
+                            if (t == 0) wait_unit();
+                            if (!ok) break;
+                            scores(t);
+                            if (last_t) next_unit();
+                        }
+                    }
+                }
+            }
+            if (!ok) *abort_flag = 1;
+            if (issued) {           // every product is done before TMEM is released
+                umma_commit(done_bar);
+                mbar_wait(done_bar, 0, p.status);
+            }
+        }
+    } else if (warp >= 4) {
+        // ---------------- softmax ----------------
+        const int t = (warp - 4) >> 2;
+        const int r = (warp & 3) * 32 + lane;                         // row of the tile
+        const bool active = n > 0 && (t == 0 || two);
+        const int m_row = it.m0 + (kKeys2 ? 0 : t * kTileRows) + r;
+        const bool valid = m_row < it.rows && (kKeys2 || m_row - it.m0 < rows);
+        const int lim = min(it.k1, min(it.len, it.lim0 + it.step * (m_row / p.gq)));     // keys below this are seen
+        const uint32_t ts = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + t * kTileKeys;
+        const uint32_t to = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + 2 * kTileKeys + t * D;
+        float m = -INFINITY, l = 0.f;
+        bool ok = true;
+        int steps = 0;
+        if (active)
+            for (int i = kKeys2 ? t : 0; i < n; i += kKeys2 ? 2 : 1, ++steps) {
+                ok = mbar_wait(s_full + t, steps & 1, p.status, p.wait_ns) && !*abort_flag;
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                tc_fence_after();
+                uint32_t s[4][32];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) tmem_ld_32x32(ts + x * 32, s[x]);
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                                 : "+r"(s[x][0]), "+r"(s[x][1]), "+r"(s[x][2]), "+r"(s[x][3]), "+r"(s[x][4]), "+r"(s[x][5]),
+                                   "+r"(s[x][6]), "+r"(s[x][7]), "+r"(s[x][8]), "+r"(s[x][9]), "+r"(s[x][10]), "+r"(s[x][11]),
+                                   "+r"(s[x][12]), "+r"(s[x][13]), "+r"(s[x][14]), "+r"(s[x][15]), "+r"(s[x][16]),
+                                   "+r"(s[x][17]), "+r"(s[x][18]), "+r"(s[x][19]), "+r"(s[x][20]), "+r"(s[x][21]),
+                                   "+r"(s[x][22]), "+r"(s[x][23]), "+r"(s[x][24]), "+r"(s[x][25]), "+r"(s[x][26]),
+                                   "+r"(s[x][27]), "+r"(s[x][28]), "+r"(s[x][29]), "+r"(s[x][30]), "+r"(s[x][31])
+                                 :
+                                 : "memory");
+                const int key0 = it.k0 + i * kTileKeys;
+                if (__any_sync(0xffffffffu, key0 + kTileKeys > lim)) {
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (key0 + x * 32 + j >= lim) s[x][j] = 0xff800000u;
+                }
+                float mx = -INFINITY;
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) mx = fmaxf(mx, __uint_as_float(s[x][j]));
+                // follow the maximum when it has grown past what the weights' type bears easily
+                const float grown = (mx - m) * p.c;
+                if (__any_sync(0xffffffffu, grown > 8.f || (m == -INFINITY && mx > -INFINITY))) {
+                    const float mn = fmaxf(m, mx);
+                    const float f = m == -INFINITY ? 0.f : exp2_approx((m - mn) * p.c);
+                    m = mn;
+                    l *= f;
+                    if (steps > 0) {
+#pragma unroll 1
+                        for (int x = 0; x < D / 32; ++x) {
+                            uint32_t o[32];
+                            tmem_load_row32(to + x * 32, o);
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                            tmem_st_32x32(to + x * 32, o);
+                        }
+                    }
+                }
+                const float mc = m == -INFINITY ? 0.f : m * p.c;
+                float l0 = 0.f, l1 = 0.f;
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    uint32_t w[32];
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        const float e0 = exp2_approx(fmaf(__uint_as_float(s[2 * x + (j >> 4)][(2 * j) & 31]), p.c, -mc));
+                        const float e1 = exp2_approx(fmaf(__uint_as_float(s[2 * x + (j >> 4)][(2 * j + 1) & 31]), p.c, -mc));
+                        l0 += e0;
+                        l1 += e1;
+                        w[j] = Mma<T>::pack(e0, e1);
+                    }
+                    tmem_st_32x32(ts + x * 32, w);
+                }
+                l += l0 + l1;
+                if (t == (kKeys2 ? (n - 1) & 1 : 0) && i == n - 1 && it.k1 < key0 + kTileKeys) {
+                    // the last values' page may hold anything past the last key
+                    const int u = kKeys2 ? (n == 1 ? 1 : 2 * n - 1) : 2 * n - 1;      // its place in the ring's order
+                    ok = mbar_wait(full + u % kUnits, (u / kUnits) & 1, p.status, p.wait_ns) && !*abort_flag;
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    uint8_t* v = smem + (u % kUnits) * kUnit;
+                    const int first = it.k1 - key0;
+                    for (int y = (warp & 3) * 32 + lane; y < (kTileKeys - first) * (D / 8); y += 128) {
+                        const int key = first + y / (D / 8), ch = y % (D / 8);
+                        *reinterpret_cast<uint4*>(v + (ch >> 3) * kTileKeys * 128 + key * 128 + ((ch & 7) << 4)) = make_uint4(0, 0, 0, 0);
+                    }
+                    fence_proxy_async_smem();
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_ready + t);
+            }
+        if (active && ok) {
+            ok = mbar_wait(o_full + t, 0, p.status, p.wait_ns) && !*abort_flag;
+            ok = __all_sync(0xffffffffu, ok);
+            if (kKeys2 && two) {        // the ring is free for the join when both are done
+                ok = ok && mbar_wait(o_full + (t ^ 1), 0, p.status, p.wait_ns);
+                ok = __all_sync(0xffffffffu, ok);
+            }
+            tc_fence_after();
+        }
+        if (!ok) *abort_flag = 1;
+        // ---------------- results ----------------
+        float2* jm = reinterpret_cast<float2*>(smem);                 // (m, l) of accumulator 1
+        float* jo = reinterpret_cast<float*>(smem + kTileRows * 8);   // its O, rows of D + 4
+        float f0 = 1.f, f1 = 0.f;
+        if (kKeys2 && two) {
+            if (t == 1) {
+                jm[r] = make_float2(m, l);
+                if (ok)
+#pragma unroll 1
+                    for (int x = 0; x < D / 32; ++x) {
+                        uint32_t o[32];
+                        tmem_load_row32(to + x * 32, o);
+#pragma unroll
+                        for (int j = 0; j < 32; j += 4)
+                            *reinterpret_cast<uint4*>(jo + r * (D + 4) + x * 32 + j) = make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+                    }
+            }
+            asm volatile("bar.sync 1, 256;" ::: "memory");
+            if (t == 0) {
+                const float2 q = jm[r];
+                const float mn = fmaxf(m, q.x);
+                f0 = m == -INFINITY ? 0.f : exp2_approx((m - mn) * p.c);
+                f1 = q.x == -INFINITY ? 0.f : exp2_approx((q.x - mn) * p.c);
+                l = l * f0 + q.y * f1;
+                m = mn;
+            }
+        }
+        const bool writes = kKeys2 ? t == 0 : (t == 0 || rows > kTileRows);
+        if (writes && !__any_sync(0xffffffffu, !ok || *abort_flag != 0)) {
+            const long long rows_all = a.T * a.Hq;
+            const long long row = static_cast<long long>(it.t0 + m_row / p.gq) * a.Hq + it.h * p.gq + m_row % p.gq;
+            const bool whole = p.sp + p.so == 1;
+            const float inv = whole ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
+            if (n > 0) {
+#pragma unroll 1
+                for (int x = 0; x < D / 32; ++x) {
+                    uint32_t o[32];
+                    __syncwarp();
+                    tmem_load_row32(to + x * 32, o);
+                    if (!valid) continue;
+                    float v[32];
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(o[j]) * f0;
+                    if (kKeys2 && two)
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[j] = fmaf(jo[r * (D + 4) + x * 32 + j], f1, v[j]);
+                    if (whole) {
+#pragma unroll
+                        for (int j = 0; j < 32; j += 8)
+                            *reinterpret_cast<uint4*>(static_cast<T*>(a.out) + row * D + x * 32 + j) =
+                                make_uint4(Mma<T>::pack(v[j] * inv, v[j + 1] * inv), Mma<T>::pack(v[j + 2] * inv, v[j + 3] * inv),
+                                           Mma<T>::pack(v[j + 4] * inv, v[j + 5] * inv), Mma<T>::pack(v[j + 6] * inv, v[j + 7] * inv));
+                    } else if (l > 0.f) {
+#pragma unroll
+                        for (int j = 0; j < 32; j += 4)
+                            *reinterpret_cast<float4*>(p.po + (it.part * rows_all + row) * D + x * 32 + j) =
+                                make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+                    }
+                }
+            } else if (whole && valid) {
+                for (int j = 0; j < D; j += 8) *reinterpret_cast<uint4*>(static_cast<T*>(a.out) + row * D + j) = make_uint4(0, 0, 0, 0);
+            }
+            if (valid) {
+                const float ml = m == -INFINITY ? m : m * p.c;        // in log2 units
+                if (whole) {
+                    if (a.lse) a.lse[row] = l > 0.f ? (ml + log2f(l)) * kLn2 : -INFINITY;
+                } else {
+                    *reinterpret_cast<float2*>(p.ml + (it.part * rows_all + row) * 2) = make_float2(ml, l);
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+}  // namespace rl

@@ -105,7 +105,7 @@ def test_prefix_attn_refusals(lib):
     _refused(lib, "rl_prefix_attn", make, [
         (dict(T=-1), arg), (dict(R=-1), arg), (dict(G=-1), arg), (dict(max_kv=-1), arg), (dict(max_prefix=-1), arg),
         (dict(Hq=3), arg), (dict(Hkv=0), arg), (dict(D=96), uns), (dict(page_size=48), uns), (dict(dtype=0), uns),
-        (dict(T=1 << 30), uns), (dict(n_pages=1 << 27), uns), (dict(max_q=0), arg), (dict(scale=float("nan")), arg),
+        (dict(T=1 << 30), uns), (dict(n_pages=1 << 27), uns), (dict(max_q=0), arg), (dict(scale=float("nan")), arg), (dict(scale=-0.1), arg), (dict(scale=-0.1), arg),
         (dict(q=None), arg), (dict(out=None), arg), (dict(cu_q=None), arg), (dict(kv_lens=None), arg),
         (dict(block_table=None), arg), (dict(group_offsets=None), arg), (dict(prefix_lens=None), arg),
         (dict(prefix_table=None), arg), (dict(k_cache=None), arg), (dict(v_cache=FAKE + 2), arg), (dict(q=FAKE + 2), arg),

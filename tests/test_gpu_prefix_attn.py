@@ -124,6 +124,26 @@ def test_steps_of_several_tokens_are_causal(q_lens, Hq, Hkv, D, page):
         Case([2, 3], [37, 150], q_lens, kv, Hq, Hkv, D, page, dtype, sum(q_lens)).check()
 
 
+@pytest.mark.parametrize("prefix", [1, 63, 127, 128, 129, 256, 257, 383, 1000, 2050])
+@pytest.mark.parametrize("groups,Hq,Hkv,D,page", [([17], 1, 1, 64, 16), ([8, 8], 8, 2, 128, 32), ([33], 8, 2, 128, 64),
+                                                  ([16, 40], 12, 2, 64, 128), ([64], 16, 2, 128, 16)])
+def test_many_rows_share_a_prefix(groups, Hq, Hkv, D, page, prefix):
+    """17 to 512 query rows of a key head over a prefix that ends at, before and after a tile; own
+    lengths from one."""
+    R = sum(groups)
+    kv = [1 + (7 * i) % 70 for i in range(R)]
+    Case(groups, [max(prefix - 5 * i, 1) for i in range(len(groups))], [1] * R, kv, Hq, Hkv, D, page,
+         BF if D == 128 else HF, prefix + R).check()
+
+
+@pytest.mark.parametrize("n", [9, 32, 33, 64, 65, 128, 129, 300])
+def test_a_long_step_of_one_request(n):
+    """Causal tiles: rows 18 to 600, with and without cached keys, without a prefix."""
+    for ctx in (0, 1, 127, 200):
+        Case([], [], [n], [n + ctx], 2, 1, 64, 64, BF, n + ctx).check()
+    Case([1], [129], [n], [n + 77], 4, 2, 128, 16, HF, n).check()
+
+
 def test_requests_outside_groups_and_groups_without_requests():
     Case([0, 2, 0, 1], [64, 50, 9, 100], [1, 2, 1, 1, 3], [5, 2, 40, 1, 3], 8, 4, 128, 16, BF, 3, stray=1).check()
 
