@@ -3,12 +3,16 @@
 // One block, 384 threads, 128 keys a step:
 //   warp 0       copies K and V tiles, page by page, into a ring of shared-memory units (TMA);
 //                pages past the last key are filled with zeros by a copy that starts past the cache
-//   warp 1       issues the products, one lane:  S = Q K^T (both in shared memory),
-//                O += P V (P in TMEM, V in shared memory, key-major)
+//   warp 1       issues the products:  S = Q K^T (both in shared memory), O += P V (P in TMEM, V in
+//                shared memory, key-major).  The whole warp runs the loop and an elected lane issues, with
+//                operands the compiler can see to be alike in all lanes: from one lane's branch
+//                each instruction took about 100 cycles to issue, longer than it runs.
 //   warps 4-7    softmax of accumulator 0, a thread a row: its 128 scores come from TMEM at once,
 //   warps 8-11   of accumulator 1;  P goes back to TMEM over the scores
 // TMEM: S0, S1 (128 columns each), O0, O1 (D columns each).  While one accumulator's scores are
-// exponentiated the tensor core works on the other's products.  The two accumulators are
+// exponentiated the tensor core works on the other's products, and the values of
+// a tile's first 64 keys are taken while the weights of the others are still being made.  The two
+// accumulators are
 //   kKeys2 = false   two tiles of 128 rows over the same keys (256 rows a block)
 //   kKeys2 = true    the even and the odd key tiles of one tile of up to 128 rows, joined at the
 //                    end through shared memory: for parts that are bound by reading the keys
@@ -66,6 +70,12 @@ RL_DEVINL void tmem_st_32x32(uint32_t taddr, const uint32_t (&r)[32]) {
         "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
         : "memory");
 }
+RL_DEVINL bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+RL_DEVINL uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
 RL_DEVINL void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 template <typename T, int D, bool kKeys2>
@@ -79,13 +89,14 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     uint64_t* full = reinterpret_cast<uint64_t*>(sq + Shape::kQBytes);
     uint64_t* empty = full + kUnits;
     uint64_t* s_full = empty + kUnits;      // [2] scores of an accumulator are in TMEM
-    uint64_t* p_ready = s_full + 2;         // [2] its weights are
+    uint64_t* p_half = s_full + 2;          // [2] its weights of the first 64 keys are
+    uint64_t* p_ready = p_half + 2;         // [2] all of them are
     uint64_t* o_full = p_ready + 2;         // [2] its last product is done
     uint64_t* done_bar = o_full + 2;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done_bar + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     const rl_prefix_attn_args& a = p.a;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = static_cast<int>(uniform(threadIdx.x >> 5)), lane = threadIdx.x & 31;
 
     if (p.sp + p.so == 1) clear_padding<T, D>(p, kTileThreads);
     Item it;
@@ -96,7 +107,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         return;
     }
     const int rows = min(it.rows - it.m0, kItemRows);                 // of this block, at least 1
-    const int n = it.k1 > it.k0 ? (it.k1 - it.k0 + kTileKeys - 1) / kTileKeys : 0;
+    const int n = static_cast<int>(uniform(it.k1 > it.k0 ? (it.k1 - it.k0 + kTileKeys - 1) / kTileKeys : 0));
     const bool two = kKeys2 ? n > 1 : rows > kTileRows;               // the second accumulator is in use
 
     if (threadIdx.x == 0) {
@@ -106,6 +117,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
         for (int t = 0; t < 2; ++t) {
             mbar_init(s_full + t, 1);
+            mbar_init(p_half + t, 4);
             mbar_init(p_ready + t, 4);
             mbar_init(o_full + t, 1);
         }
@@ -137,7 +149,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = uniform(*tmem_slot);
 
     if (warp == 0) {
         // ---------------- copies ----------------
@@ -189,7 +201,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         if (!ok && lane == 0)       // what was issued lands before the block can end
             for (int s = max(0, issued - kUnits); s < issued; ++s) mbar_wait(full + s % kUnits, (s / kUnits) & 1, p.status);
     } else if (warp == 1) {
-        if (lane == 0 && n > 0) {
+        if (n > 0) {
             // ---------------- products ----------------
             constexpr uint32_t kIdescS = tile_idesc<T>(kTileKeys, false), kIdescO = tile_idesc<T>(D, true);
             int unit = 0;
@@ -197,34 +209,61 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             bool ok = true, issued = false;
             auto wait_unit = [&]() {
                 ok = ok && mbar_wait(full + unit, phase, p.status, p.wait_ns) && !*abort_flag;
+                ok = __all_sync(0xffffffffu, ok);
                 tc_fence_after();
             };
+            auto commit = [&](uint64_t* bar) {
+                if (elect_one()) umma_commit(bar);
+                __syncwarp();
+            };
             auto next_unit = [&]() {
-                umma_commit(empty + unit);
+                commit(empty + unit);
                 if (++unit == kUnits) {
                     unit = 0;
                     phase ^= 1u;
                 }
             };
+            // descriptors of the ring's first unit and of the queries; a step within them adds its
+            // distance in 16-byte steps (addresses stay below 2^18, so nothing carries out)
+            const uint64_t dk = sdesc_kmajor_sw128(smem_addr(smem)), dq = sdesc_kmajor_sw128(smem_addr(sq));
+            const uint64_t dv = sdesc_mnmajor_sw128(smem_addr(smem), kTileKeys * 128);
             auto scores = [&](int t) {
-                const uint32_t k = smem_addr(smem + unit * kUnit), q = smem_addr(sq) + (kKeys2 ? 0 : t * kTileRows * D * 2);
+                const uint64_t k = dk + uniform(unit * (kUnit >> 4));
+                const uint64_t q = dq + (kKeys2 ? 0u : uniform(t * ((kTileRows * D * 2) >> 4)));
+                const uint32_t d = uniform(tmem + t * kTileKeys);
+                if (elect_one()) {
 #pragma unroll
-                for (int x = 0; x < D / 16; ++x) {
-                    const uint32_t off = (x >> 2) * 128 * 128 + (x & 3) * 32;
-                    umma_bf16(tmem + t * kTileKeys, sdesc_kmajor_sw128(q + off), sdesc_kmajor_sw128(k + off), kIdescS, x != 0);
+                    for (int x = 0; x < D / 16; ++x) {
+                        const uint32_t off = ((x >> 2) * 128 * 128 + (x & 3) * 32) >> 4;
+                        umma_bf16(d, q + off, k + off, kIdescS, x != 0);
+                    }
+                    umma_commit(s_full + t);
                 }
+                __syncwarp();
                 issued = true;
-                umma_commit(s_full + t);
             };
-            auto values = [&](int t, bool first) {
-                const uint32_t v = smem_addr(smem + unit * kUnit);
+            // O += P V of step i of accumulator t, in two halves of the keys
+            auto values = [&](int t, int i) {
+                const uint64_t v = dv + uniform(unit * (kUnit >> 4));
+                const uint32_t o = uniform(tmem + 2 * kTileKeys + t * D), w = uniform(tmem + t * kTileKeys);
+                const uint32_t more = uniform(i != 0);
+                if (elect_one()) {
 #pragma unroll
-                for (int x = 0; x < kTileKeys / 16; ++x)
-                    umma_ts(tmem + 2 * kTileKeys + t * D, tmem + t * kTileKeys + x * 8,
-                            sdesc_mnmajor_sw128(v + x * 2048, kTileKeys * 128), kIdescO, !(first && x == 0));
+                    for (int x = 0; x < kTileKeys / 32; ++x) umma_ts(o, w + x * 8, v + x * (2048 >> 4), kIdescO, x != 0 ? 1u : more);
+                }
+                __syncwarp();
+                ok = ok && mbar_wait(p_ready + t, i & 1, p.status, p.wait_ns) && !*abort_flag;
+                ok = __all_sync(0xffffffffu, ok);
+                tc_fence_after();
+                if (ok && elect_one()) {
+#pragma unroll
+                    for (int x = kTileKeys / 32; x < kTileKeys / 16; ++x) umma_ts(o, w + x * 8, v + x * (2048 >> 4), kIdescO, 1u);
+                }
+                __syncwarp();
             };
             auto wait_p = [&](int t, int i) {
-                ok = ok && mbar_wait(p_ready + t, i & 1, p.status, p.wait_ns) && !*abort_flag;
+                ok = ok && mbar_wait(p_half + t, i & 1, p.status, p.wait_ns) && !*abort_flag;
+                ok = __all_sync(0xffffffffu, ok);
                 tc_fence_after();
             };
             if (kKeys2) {
@@ -239,9 +278,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     wait_p(t, i >> 1);
                     wait_unit();
                     if (!ok) break;
-                    values(t, i < 2);
+                    values(t, i >> 1);
+                    if (!ok) break;
                     next_unit();
-                    if (i + 2 >= n) umma_commit(o_full + t);
+                    if (i + 2 >= n) commit(o_full + t);
                     if (i + 2 < n) {
                         wait_unit();
                         if (!ok) break;
@@ -266,10 +306,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                         phase = vp;
                         if (t == 0) wait_unit();
                         if (!ok) break;
-                        values(t, i == 0);
-                        if (i + 1 == n) umma_commit(o_full + t);
+                        values(t, i);
+                        if (!ok) break;
+                        if (i + 1 == n) commit(o_full + t);
                         const bool last_t = t == 1 || !two;
-                        if (last_t) umma_commit(empty + unit);
+                        if (last_t) commit(empty + unit);
                         if (++unit == kUnits) {
                             unit = 0;
                             phase ^= 1u;
@@ -285,7 +326,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             }
             if (!ok) *abort_flag = 1;
             if (issued) {           // every product is done before TMEM is released
-                umma_commit(done_bar);
+                commit(done_bar);
                 mbar_wait(done_bar, 0, p.status);
             }
         }
@@ -330,11 +371,28 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                         for (int j = 0; j < 32; ++j)
                             if (key0 + x * 32 + j >= lim) s[x][j] = 0xff800000u;
                 }
-                float mx = -INFINITY;
+                float mx4[4];
 #pragma unroll
-                for (int x = 0; x < 4; ++x)
+                for (int x = 0; x < 4; ++x) mx4[x] = __uint_as_float(s[x][0]);
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) mx = fmaxf(mx, __uint_as_float(s[x][j]));
+                for (int j = 1; j < 32; ++j)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) mx4[x] = fmaxf(mx4[x], __uint_as_float(s[x][j]));
+                const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
+                if (t == (kKeys2 ? (n - 1) & 1 : 0) && i == n - 1 && it.k1 < key0 + kTileKeys) {
+                    // the last values' page may hold anything past the last key
+                    const int u = kKeys2 ? (n == 1 ? 1 : 2 * n - 1) : 2 * n - 1;      // its place in the ring's order
+                    ok = mbar_wait(full + u % kUnits, (u / kUnits) & 1, p.status, p.wait_ns) && !*abort_flag;
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    uint8_t* v = smem + (u % kUnits) * kUnit;
+                    const int first = it.k1 - key0;
+                    for (int y = (warp & 3) * 32 + lane; y < (kTileKeys - first) * (D / 8); y += 128) {
+                        const int key = first + y / (D / 8), ch = y % (D / 8);
+                        *reinterpret_cast<uint4*>(v + (ch >> 3) * kTileKeys * 128 + key * 128 + ((ch & 7) << 4)) = make_uint4(0, 0, 0, 0);
+                    }
+                    fence_proxy_async_smem();
+                }
                 // follow the maximum when it has grown past what the weights' type bears easily
                 const float grown = (mx - m) * p.c;
                 if (__any_sync(0xffffffffu, grown > 8.f || (m == -INFINITY && mx > -INFINITY))) {
@@ -354,7 +412,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     }
                 }
                 const float mc = m == -INFINITY ? 0.f : m * p.c;
-                float l0 = 0.f, l1 = 0.f;
+                float l4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     uint32_t w[32];
@@ -362,31 +420,17 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     for (int j = 0; j < 32; ++j) {
                         const float e0 = exp2_approx(fmaf(__uint_as_float(s[2 * x + (j >> 4)][(2 * j) & 31]), p.c, -mc));
                         const float e1 = exp2_approx(fmaf(__uint_as_float(s[2 * x + (j >> 4)][(2 * j + 1) & 31]), p.c, -mc));
-                        l0 += e0;
-                        l1 += e1;
+                        l4[(j & 1) * 2] += e0;
+                        l4[(j & 1) * 2 + 1] += e1;
                         w[j] = Mma<T>::pack(e0, e1);
                     }
                     tmem_st_32x32(ts + x * 32, w);
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive((x == 0 ? p_half : p_ready) + t);
                 }
-                l += l0 + l1;
-                if (t == (kKeys2 ? (n - 1) & 1 : 0) && i == n - 1 && it.k1 < key0 + kTileKeys) {
-                    // the last values' page may hold anything past the last key
-                    const int u = kKeys2 ? (n == 1 ? 1 : 2 * n - 1) : 2 * n - 1;      // its place in the ring's order
-                    ok = mbar_wait(full + u % kUnits, (u / kUnits) & 1, p.status, p.wait_ns) && !*abort_flag;
-                    ok = __all_sync(0xffffffffu, ok);
-                    if (!ok) break;
-                    uint8_t* v = smem + (u % kUnits) * kUnit;
-                    const int first = it.k1 - key0;
-                    for (int y = (warp & 3) * 32 + lane; y < (kTileKeys - first) * (D / 8); y += 128) {
-                        const int key = first + y / (D / 8), ch = y % (D / 8);
-                        *reinterpret_cast<uint4*>(v + (ch >> 3) * kTileKeys * 128 + key * 128 + ((ch & 7) << 4)) = make_uint4(0, 0, 0, 0);
-                    }
-                    fence_proxy_async_smem();
-                }
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(p_ready + t);
+                l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
             }
         if (active && ok) {
             ok = mbar_wait(o_full + t, 0, p.status, p.wait_ns) && !*abort_flag;
