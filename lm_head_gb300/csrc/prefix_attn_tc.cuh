@@ -92,7 +92,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     uint64_t* p_half = s_full + 2;          // [2] its weights of the first 64 keys are
     uint64_t* p_ready = p_half + 2;         // [2] all of them are
     uint64_t* o_full = p_ready + 2;         // [2] its last product is done
-    uint64_t* done_bar = o_full + 2;
+    uint64_t* q_full = o_full + 2;          // the queries are in shared memory
+    uint64_t* done_bar = q_full + 1;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done_bar + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     const rl_prefix_attn_args& a = p.a;
@@ -121,6 +122,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             mbar_init(p_ready + t, 4);
             mbar_init(o_full + t, 1);
         }
+        mbar_init(q_full, 8);
         mbar_init(done_bar, 1);
         *abort_flag = 0;
         fence_mbar_init();
@@ -131,21 +133,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         tmem_alloc(tmem_slot, 512);
         tmem_relinquish();
     }
-    // queries: rows of 128 bytes with the 128-byte swizzle, 64 columns a sub-tile; zeros past the rows
-    if (n > 0)
-        for (int x = threadIdx.x; x < Shape::kQTiles * kTileRows * (D / 8); x += kTileThreads) {
-            const int r = x / (D / 8), ch = x % (D / 8);
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (r < rows) {
-                const int m = it.m0 + r;
-                v = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + (it.t0 + m / p.gq) * a.q_stride_t +
-                                                    static_cast<int64_t>(it.h * p.gq + m % p.gq) * a.q_stride_h + ch * 8);
-            }
-            const int tile = r / kTileRows, rr = r % kTileRows;
-            *reinterpret_cast<uint4*>(sq + tile * kTileRows * D * 2 + (ch >> 3) * kTileRows * 128 + rr * 128 +
-                                      (((ch & 7) ^ (rr & 7)) << 4)) = v;
-        }
-    fence_proxy_async_smem();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -206,7 +193,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             constexpr uint32_t kIdescS = tile_idesc<T>(kTileKeys, false), kIdescO = tile_idesc<T>(D, true);
             int unit = 0;
             uint32_t phase = 0;
-            bool ok = true, issued = false;
+            bool issued = false;
+            bool ok = mbar_wait(q_full, 0, p.status, p.wait_ns) && !*abort_flag;
+            ok = __all_sync(0xffffffffu, ok);
             auto wait_unit = [&]() {
                 ok = ok && mbar_wait(full + unit, phase, p.status, p.wait_ns) && !*abort_flag;
                 ok = __all_sync(0xffffffffu, ok);
@@ -331,6 +320,23 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             }
         }
     } else if (warp >= 4) {
+        // queries: rows of 128 bytes with the 128-byte swizzle, 64 columns a sub-tile; zeros past the rows
+        if (n > 0) {
+            for (int x = threadIdx.x - 128; x < Shape::kQTiles * kTileRows * (D / 8); x += 256) {
+                const int r = x / (D / 8), ch = x % (D / 8);
+                const int m = it.m0 + (r < rows ? r : 0);
+                const T* src = static_cast<const T*>(a.q) + (it.t0 + m / p.gq) * a.q_stride_t +
+                               static_cast<int64_t>(it.h * p.gq + m % p.gq) * a.q_stride_h + ch * 8;
+                const int tile = r / kTileRows, rr = r % kTileRows;
+                const uint32_t dst = smem_addr(sq) + tile * kTileRows * D * 2 + (ch >> 3) * kTileRows * 128 + rr * 128 +
+                                     (((ch & 7) ^ (rr & 7)) << 4);
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(r < rows ? 16 : 0) : "memory");
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(q_full);
+        }
         // ---------------- softmax ----------------
         const int t = (warp - 4) >> 2;
         const int r = (warp & 3) * 32 + lane;                         // row of the tile
