@@ -36,6 +36,7 @@ struct AttnArgs {
     int chunk_p, chunk_o; // keys of a part, multiples of kStageKeys
     int tiles_p, tiles_o; // row tiles: of all groups together, of one request
     int run_p, run_o;     // whether the launch does the prefixes' parts, the own keys' parts
+    int both;             // the own keys' blocks do their group's prefix first (sp = 0, so = 1)
     float* ml;            // [sp + so][T * Hq][2]: max (in log2 units), sum
     float* po;            // [sp + so][T * Hq][D] numerators
 };
@@ -50,10 +51,43 @@ struct Item {
     int step;
     int k0, k1;            // the part's keys
     int h, part;
+    int r;                 // request (parts of own keys)
 };
 
 // tokens [first, last) of a request, clamped to the call's
 RL_DEVINL int clamp_t(int x, long long T) { return static_cast<int>(min(max(static_cast<long long>(x), 0ll), T)); }
+
+// The keys of group g's prefix from k0 on, at most `chunk` of them.
+RL_DEVINL void prefix_keys(const AttnArgs& p, long long g, int k0, int chunk, Item& it, int& bits) {
+    const rl_prefix_attn_args& a = p.a;
+    int len = a.prefix_lens[g];
+    const long long most = min(static_cast<long long>(a.max_prefix), static_cast<long long>(a.prefix_width * a.page_size));
+    if (len < 0 || len > most) {
+        bits |= RL_STATUS_LENGTHS;
+        len = static_cast<int>(min(max(static_cast<long long>(len), 0ll), most));
+    }
+    it.table = a.prefix_table + g * a.prefix_width;
+    it.len = len;
+    it.lim0 = len;
+    it.step = 0;
+    it.k0 = k0;
+    it.k1 = static_cast<int>(min(static_cast<long long>(k0) + chunk, static_cast<long long>(len)));
+}
+// The whole prefix of the group of `it`'s request (none: no keys).  All lanes of a warp together.
+RL_DEVINL void find_prefix(const AttnArgs& p, const Item& it, Item& pre, int& bits) {
+    const rl_prefix_attn_args& a = p.a;
+    const int lane = threadIdx.x & 31;
+    pre.k0 = pre.k1 = 0;
+    for (long long g0 = 0; g0 < a.G; g0 += 32) {
+        const long long g = g0 + lane;
+        const bool mine = g < a.G && a.group_offsets[g] <= it.r && it.r < a.group_offsets[g + 1];
+        const unsigned hit = __ballot_sync(0xffffffffu, mine);
+        if (hit) {
+            prefix_keys(p, g0 + __ffs(hit) - 1, 0, INT_MAX, pre, bits);
+            return;
+        }
+    }
+}
 
 // Which part block `id` does; false: none.  All lanes of one warp call it together.
 RL_DEVINL bool find_item(const AttnArgs& p, long long id, int tile_rows, Item& it, int& bits) {
@@ -89,19 +123,7 @@ RL_DEVINL bool find_item(const AttnArgs& p, long long id, int tile_rows, Item& i
                 it.t0 = __shfl_sync(0xffffffffu, ta, src);
                 it.rows = static_cast<int>(__shfl_sync(0xffffffffu, rows, src));
                 it.m0 = __shfl_sync(0xffffffffu, mine, src) * tile_rows;
-                const long long gg = g0 + src;
-                int len = a.prefix_lens[gg];
-                const long long most = min(static_cast<long long>(a.max_prefix), static_cast<long long>(a.prefix_width * a.page_size));
-                if (len < 0 || len > most) {
-                    bits |= RL_STATUS_LENGTHS;
-                    len = static_cast<int>(min(max(static_cast<long long>(len), 0ll), most));
-                }
-                it.table = a.prefix_table + gg * a.prefix_width;
-                it.len = len;
-                it.lim0 = len;
-                it.step = 0;
-                it.k0 = split * p.chunk_p;
-                it.k1 = min(it.k0 + p.chunk_p, len);
+                prefix_keys(p, g0 + src, split * p.chunk_p, p.chunk_p, it, bits);
                 return true;
             }
             tile -= __shfl_sync(0xffffffffu, incl, 31);
@@ -115,6 +137,7 @@ RL_DEVINL bool find_item(const AttnArgs& p, long long id, int tile_rows, Item& i
     const long long r = rt / p.tiles_o;
     const int tile = static_cast<int>(rt % p.tiles_o);
     it.part = p.sp + split;
+    it.r = static_cast<int>(r);
     const int ca = a.cu_q[r], cb = a.cu_q[r + 1];
     const int ta = clamp_t(ca, a.T), tb = max(clamp_t(cb, a.T), ta);
     int n = tb - ta, kv = a.kv_lens[r];
@@ -132,7 +155,7 @@ RL_DEVINL bool find_item(const AttnArgs& p, long long id, int tile_rows, Item& i
     const int last = (min(it.m0 + tile_rows, it.rows) - 1) / p.gq;   // last token of the tile
     it.len = min(kv, it.lim0 + last);
     it.k0 = split * p.chunk_o;
-    it.k1 = min(it.k0 + p.chunk_o, it.len);
+    it.k1 = static_cast<int>(min(static_cast<long long>(it.k0) + p.chunk_o, static_cast<long long>(it.len)));
     return true;
 }
 
@@ -557,8 +580,14 @@ static AttnArgs attn_view(const rl_prefix_attn_args* a, void* ws, size_t* bytes,
     p.tiles_p = prefix ? static_cast<int>(a->T * p.gq / rp + a->G) : 0;      // a bound: each group rounds up once
     p.tiles_o = static_cast<int>((a->max_q * p.gq + ro - 1) / ro);
     const int64_t about = a->T * p.gq / rp > a->G ? a->T * p.gq / rp : a->G; // row tiles to expect
-    p.sp = prefix ? parts_of(*kp, a->max_prefix, about * a->Hkv, &p.chunk_p) : 0;
-    p.so = parts_of(*ko, a->max_kv, a->R * p.tiles_o * a->Hkv, &p.chunk_o);
+    // Requests that bring a tile of rows or more each, and enough of them to fill the device: one block
+    // takes a tile of a request over the prefix and the own keys, and nothing is left to join.
+    // (32 requests of 0 to 256 tokens, 8 heads a key head, on up to 4096 shared keys: 58 us so,
+    // 125 us in two parts and a join.)
+    p.both = prefix && *ko == kRows && a->R > 0 && a->T * p.gq / a->R >= 2 * kTileRows && a->T * p.gq / ro * a->Hkv >= num_sms() / 2;
+    p.sp = prefix && !p.both ? parts_of(*kp, a->max_prefix, about * a->Hkv, &p.chunk_p) : 0;
+    p.so = p.both ? 1 : parts_of(*ko, a->max_kv, a->R * p.tiles_o * a->Hkv, &p.chunk_o);
+    if (p.both) p.chunk_o = INT_MAX;
     Carve cv(ws);
     const size_t rows = static_cast<size_t>(a->T) * a->Hq;
     const int parts = p.sp + p.so;

@@ -20,6 +20,10 @@
 // stay below 2^8 of it and O is left alone.  That O may be rescaled is known from the scores'
 // barrier: the scores' product was issued after the last product into O.
 //
+// The keys of a block are a stretch of a prefix (all rows see all of it), a stretch of a request's own
+// keys (causal), or one after the other: where every request of a step brings at least a tile of
+// rows, its blocks run over the prefix and its own keys and write the result at once.
+//
 // Every wait is bounded; a wait that runs out raises the block's abort flag, all roles leave
 // their loops, and copies and products in flight are waited for before TMEM is released.
 #pragma once
@@ -39,9 +43,10 @@ struct TileShape {
     static constexpr int kQTiles = kKeys2 ? 1 : 2;
     static constexpr int kQBytes = kQTiles * kTileRows * D * 2;
     static constexpr int kUnits = D == 128 ? (kKeys2 ? 5 : 4) : 8;
-    // the join of the two accumulators reuses the ring: O1 and (m, l) of 128 rows
+    // results pass through the memory of the ring and the queries: rows of two accumulators, (m, l)
+    static constexpr int kRowBytes = (D + 4) * 4;         // padded: 16-byte steps of 32 rows on all banks
     static constexpr int kSmemBytes = kUnits * kUnitBytes + kQBytes + 1024 + 256;
-    static_assert(kUnits * kUnitBytes >= kTileRows * (D + 4) * 4 + kTileRows * 8, "the ring holds the join's data");
+    static_assert(kUnits * kUnitBytes + kQBytes >= 2 * kTileRows * kRowBytes + kTileRows * 8, "the results fit");
 };
 
 template <typename T>
@@ -69,6 +74,10 @@ RL_DEVINL void tmem_st_32x32(uint32_t taddr, const uint32_t (&r)[32]) {
         "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
         "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
         : "memory");
+}
+// One bulk copy shared -> global (16-byte aligned, size a multiple of 16), in the thread's bulk group.
+RL_DEVINL void bulk_store(void* dst, const void* src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_addr(src)), "r"(bytes) : "memory");
 }
 RL_DEVINL bool elect_one() {
     uint32_t r;
@@ -108,7 +117,14 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         return;
     }
     const int rows = min(it.rows - it.m0, kItemRows);                 // of this block, at least 1
-    const int n = static_cast<int>(uniform(it.k1 > it.k0 ? (it.k1 - it.k0 + kTileKeys - 1) / kTileKeys : 0));
+    // key tiles: `na` of the prefix stretch (it2 of a block that does both), then those of the own keys
+    Item pre = it;
+    if (p.both) find_prefix(p, it, pre, bits);
+    else if (it.step) pre.k1 = pre.k0 = 0;
+    if (!p.both && !it.step) it.k1 = it.k0 = 0;
+    const int na = static_cast<int>(uniform(pre.k1 > pre.k0 ? (pre.k1 - pre.k0 + kTileKeys - 1) / kTileKeys : 0));
+    const int nb = static_cast<int>(uniform(it.k1 > it.k0 ? (it.k1 - it.k0 + kTileKeys - 1) / kTileKeys : 0));
+    const int n = na + nb;
     const bool two = kKeys2 ? n > 1 : rows > kTileRows;               // the second accumulator is in use
 
     if (threadIdx.x == 0) {
@@ -149,10 +165,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         int issued = 0;
         bool ok = true;
         auto load = [&](const CUtensorMap* map, int tile) {
-            const int key = it.k0 + tile * kTileKeys + lane * box;
+            const bool in_a = tile < na;
+            const int key = (in_a ? pre.k0 + tile * kTileKeys : it.k0 + (tile - na) * kTileKeys) + lane * box;
             int row = past;
-            if (lane < per && key < it.k1)
-                row = (page_of(p, it.table, key, shift, bits) * a.Hkv + it.h) * a.page_size + (key & (a.page_size - 1));
+            if (lane < per && key < (in_a ? pre.k1 : it.k1))
+                row = (page_of(p, in_a ? pre.table : it.table, key, shift, bits) * a.Hkv + it.h) * a.page_size + (key & (a.page_size - 1));
             ok = mbar_wait(empty + unit, phase ^ 1u, p.status, p.wait_ns) && !*abort_flag;
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) {
@@ -322,11 +339,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     } else if (warp >= 4) {
         // queries: rows of 128 bytes with the 128-byte swizzle, 64 columns a sub-tile; zeros past the rows
         if (n > 0) {
-            for (int x = threadIdx.x - 128; x < Shape::kQTiles * kTileRows * (D / 8); x += 256) {
-                const int r = x / (D / 8), ch = x % (D / 8);
-                const int m = it.m0 + (r < rows ? r : 0);
-                const T* src = static_cast<const T*>(a.q) + (it.t0 + m / p.gq) * a.q_stride_t +
-                               static_cast<int64_t>(it.h * p.gq + m % p.gq) * a.q_stride_h + ch * 8;
+            const int ch = (threadIdx.x - 128) % (D / 8), first = it.m0 / p.gq, rem = it.m0 % p.gq;
+            const float inv = 1.f / static_cast<float>(p.gq);
+            const T* base = static_cast<const T*>(a.q) + (it.t0 + first) * a.q_stride_t + static_cast<int64_t>(it.h * p.gq) * a.q_stride_h + ch * 8;
+            for (int r = (threadIdx.x - 128) / (D / 8); r < Shape::kQTiles * kTileRows; r += 256 / (D / 8)) {
+                const int x = rem + (r < rows ? r : 0);
+                const int dt = static_cast<int>((static_cast<float>(x) + 0.5f) * inv);        // x / gq: x is small
+                const T* src = base + dt * a.q_stride_t + (x - dt * p.gq) * a.q_stride_h;
                 const int tile = r / kTileRows, rr = r % kTileRows;
                 const uint32_t dst = smem_addr(sq) + tile * kTileRows * D * 2 + (ch >> 3) * kTileRows * 128 + rr * 128 +
                                      (((ch & 7) ^ (rr & 7)) << 4);
@@ -343,7 +362,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const bool active = n > 0 && (t == 0 || two);
         const int m_row = it.m0 + (kKeys2 ? 0 : t * kTileRows) + r;
         const bool valid = m_row < it.rows && (kKeys2 || m_row - it.m0 < rows);
-        const int lim = min(it.k1, min(it.len, it.lim0 + it.step * (m_row / p.gq)));     // keys below this are seen
+        const int lim_own = min(it.k1, it.lim0 + it.step * (m_row / p.gq));          // own keys below this are seen
         const uint32_t ts = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + t * kTileKeys;
         const uint32_t to = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + 2 * kTileKeys + t * D;
         float m = -INFINITY, l = 0.f;
@@ -369,7 +388,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                                    "+r"(s[x][27]), "+r"(s[x][28]), "+r"(s[x][29]), "+r"(s[x][30]), "+r"(s[x][31])
                                  :
                                  : "memory");
-                const int key0 = it.k0 + i * kTileKeys;
+                const bool in_a = i < na;
+                const int key0 = in_a ? pre.k0 + i * kTileKeys : it.k0 + (i - na) * kTileKeys;
+                const int last = in_a ? pre.k1 : it.k1, lim = in_a ? pre.k1 : lim_own;
                 if (__any_sync(0xffffffffu, key0 + kTileKeys > lim)) {
 #pragma unroll
                     for (int x = 0; x < 4; ++x)
@@ -385,14 +406,14 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
                     for (int x = 0; x < 4; ++x) mx4[x] = fmaxf(mx4[x], __uint_as_float(s[x][j]));
                 const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
-                if (t == (kKeys2 ? (n - 1) & 1 : 0) && i == n - 1 && it.k1 < key0 + kTileKeys) {
+                if ((kKeys2 || t == 0) && last < key0 + kTileKeys) {
                     // the last values' page may hold anything past the last key
-                    const int u = kKeys2 ? (n == 1 ? 1 : 2 * n - 1) : 2 * n - 1;      // its place in the ring's order
+                    const int u = !kKeys2 || i == n - 1 ? (n == 1 ? 1 : kKeys2 ? 2 * n - 1 : 2 * i + 1) : 2 * i + 2;  // place in the ring's order
                     ok = mbar_wait(full + u % kUnits, (u / kUnits) & 1, p.status, p.wait_ns) && !*abort_flag;
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
                     uint8_t* v = smem + (u % kUnits) * kUnit;
-                    const int first = it.k1 - key0;
+                    const int first = last - key0;
                     for (int y = (warp & 3) * 32 + lane; y < (kTileKeys - first) * (D / 8); y += 128) {
                         const int key = first + y / (D / 8), ch = y % (D / 8);
                         *reinterpret_cast<uint4*>(v + (ch >> 3) * kTileKeys * 128 + key * 128 + ((ch & 7) << 4)) = make_uint4(0, 0, 0, 0);
@@ -438,19 +459,15 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 }
                 l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
             }
-        if (active && ok) {
-            ok = mbar_wait(o_full + t, 0, p.status, p.wait_ns) && !*abort_flag;
+        if (n > 0 && ok) {                  // with all products done the ring and the queries are free
+            ok = mbar_wait(o_full, 0, p.status, p.wait_ns) && (!two || mbar_wait(o_full + 1, 0, p.status, p.wait_ns)) && !*abort_flag;
             ok = __all_sync(0xffffffffu, ok);
-            if (kKeys2 && two) {        // the ring is free for the join when both are done
-                ok = ok && mbar_wait(o_full + (t ^ 1), 0, p.status, p.wait_ns);
-                ok = __all_sync(0xffffffffu, ok);
-            }
             tc_fence_after();
         }
         if (!ok) *abort_flag = 1;
         // ---------------- results ----------------
-        float2* jm = reinterpret_cast<float2*>(smem);                 // (m, l) of accumulator 1
-        float* jo = reinterpret_cast<float*>(smem + kTileRows * 8);   // its O, rows of D + 4
+        float* stage = reinterpret_cast<float*>(smem + t * kTileRows * Shape::kRowBytes + r * Shape::kRowBytes);   // this row's
+        float2* jm = reinterpret_cast<float2*>(smem + 2 * kTileRows * Shape::kRowBytes);       // (m, l) of accumulator 1
         float f0 = 1.f, f1 = 0.f;
         if (kKeys2 && two) {
             if (t == 1) {
@@ -461,8 +478,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                         uint32_t o[32];
                         tmem_load_row32(to + x * 32, o);
 #pragma unroll
-                        for (int j = 0; j < 32; j += 4)
-                            *reinterpret_cast<uint4*>(jo + r * (D + 4) + x * 32 + j) = make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+                        for (int j = 0; j < 32; j += 4) *reinterpret_cast<uint4*>(stage + x * 32 + j) = make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
                     }
             }
             asm volatile("bar.sync 1, 256;" ::: "memory");
@@ -480,37 +496,44 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             const long long rows_all = a.T * a.Hq;
             const long long row = static_cast<long long>(it.t0 + m_row / p.gq) * a.Hq + it.h * p.gq + m_row % p.gq;
             const bool whole = p.sp + p.so == 1;
-            const float inv = whole ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
-            if (n > 0) {
+            if (whole) f0 *= l > 0.f ? 1.f / l : 0.f, f1 *= l > 0.f ? 1.f / l : 0.f;
+            // a row through shared memory, so that it leaves in one piece
 #pragma unroll 1
-                for (int x = 0; x < D / 32; ++x) {
+            for (int x = 0; x < D / 32; ++x) {
+                float v[32];
+                if (n > 0) {
                     uint32_t o[32];
-                    __syncwarp();
                     tmem_load_row32(to + x * 32, o);
-                    if (!valid) continue;
-                    float v[32];
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(o[j]) * f0;
-                    if (kKeys2 && two)
+                    for (int j = 0; j < 32; ++j) v[j] = f0 > 0.f ? __uint_as_float(o[j]) * f0 : 0.f;
+                    if (kKeys2 && two && f1 > 0.f)
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) v[j] = fmaf(jo[r * (D + 4) + x * 32 + j], f1, v[j]);
-                    if (whole) {
+                        for (int j = 0; j < 32; j += 4) {
+                            const float4 q = *reinterpret_cast<const float4*>(stage + kTileRows * (D + 4) + x * 32 + j);
+                            v[j] = fmaf(q.x, f1, v[j]);
+                            v[j + 1] = fmaf(q.y, f1, v[j + 1]);
+                            v[j + 2] = fmaf(q.z, f1, v[j + 2]);
+                            v[j + 3] = fmaf(q.w, f1, v[j + 3]);
+                        }
+                } else {
 #pragma unroll
-                        for (int j = 0; j < 32; j += 8)
-                            *reinterpret_cast<uint4*>(static_cast<T*>(a.out) + row * D + x * 32 + j) =
-                                make_uint4(Mma<T>::pack(v[j] * inv, v[j + 1] * inv), Mma<T>::pack(v[j + 2] * inv, v[j + 3] * inv),
-                                           Mma<T>::pack(v[j + 4] * inv, v[j + 5] * inv), Mma<T>::pack(v[j + 6] * inv, v[j + 7] * inv));
-                    } else if (l > 0.f) {
-#pragma unroll
-                        for (int j = 0; j < 32; j += 4)
-                            *reinterpret_cast<float4*>(p.po + (it.part * rows_all + row) * D + x * 32 + j) =
-                                make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
-                    }
+                    for (int j = 0; j < 32; ++j) v[j] = 0.f;
                 }
-            } else if (whole && valid) {
-                for (int j = 0; j < D; j += 8) *reinterpret_cast<uint4*>(static_cast<T*>(a.out) + row * D + j) = make_uint4(0, 0, 0, 0);
+                if (whole) {
+#pragma unroll
+                    for (int j = 0; j < 32; j += 8)
+                        *reinterpret_cast<uint4*>(reinterpret_cast<T*>(stage) + x * 32 + j) =
+                            make_uint4(Mma<T>::pack(v[j], v[j + 1]), Mma<T>::pack(v[j + 2], v[j + 3]), Mma<T>::pack(v[j + 4], v[j + 5]),
+                                       Mma<T>::pack(v[j + 6], v[j + 7]));
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 32; j += 4) *reinterpret_cast<float4*>(stage + x * 32 + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+                }
             }
+            fence_proxy_async_smem();
             if (valid) {
+                void* dst = whole ? static_cast<void*>(static_cast<T*>(a.out) + row * D) : static_cast<void*>(p.po + (it.part * rows_all + row) * D);
+                if (whole || l > 0.f) bulk_store(dst, stage, whole ? D * 2 : D * 4);
                 const float ml = m == -INFINITY ? m : m * p.c;        // in log2 units
                 if (whole) {
                     if (a.lse) a.lse[row] = l > 0.f ? (ml + log2f(l)) * kLn2 : -INFINITY;
@@ -518,6 +541,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     *reinterpret_cast<float2*>(p.ml + (it.part * rows_all + row) * 2) = make_float2(ml, l);
                 }
             }
+            bulk_commit();
+            bulk_wait_all();
         }
     }
     tc_fence_before();
