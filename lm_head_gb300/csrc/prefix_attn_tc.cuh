@@ -114,6 +114,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     constexpr int kItemRows = kKeys2 ? kTileRows : 2 * kTileRows;
     if (!find_item(p, blockIdx.x, kItemRows, it, bits)) {             // every warp for itself, all alike
         if (threadIdx.x == 0) set_status(p.status, bits);
+        wait_for_previous();
         return;
     }
     const int rows = min(it.rows - it.m0, kItemRows);                 // of this block, at least 1
@@ -148,6 +149,21 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     if (warp == 1) {
         tmem_alloc(tmem_slot, 512);
         tmem_relinquish();
+    }
+    // queries: rows of 128 bytes with the 128-byte swizzle, 64 columns a sub-tile; zeros past the rows
+    if (warp >= 4 && n > 0) {
+        const int ch = (threadIdx.x - 128) % (D / 8), first = it.m0 / p.gq, rem = it.m0 % p.gq;
+        const float inv = 1.f / static_cast<float>(p.gq);
+        const T* base = static_cast<const T*>(a.q) + (it.t0 + first) * a.q_stride_t + static_cast<int64_t>(it.h * p.gq) * a.q_stride_h + ch * 8;
+        for (int r = (threadIdx.x - 128) / (D / 8); r < Shape::kQTiles * kTileRows; r += 256 / (D / 8)) {
+            const int x = rem + (r < rows ? r : 0);
+            const int dt = static_cast<int>((static_cast<float>(x) + 0.5f) * inv);        // x / gq: x is small
+            const T* src = base + dt * a.q_stride_t + (x - dt * p.gq) * a.q_stride_h;
+            const int tile = r / kTileRows, rr = r % kTileRows;
+            const uint32_t dst = smem_addr(sq) + tile * kTileRows * D * 2 + (ch >> 3) * kTileRows * 128 + rr * 128 +
+                                 (((ch & 7) ^ (rr & 7)) << 4);
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(r < rows ? 16 : 0) : "memory");
+        }
     }
     tc_fence_before();
     __syncthreads();
@@ -337,20 +353,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             }
         }
     } else if (warp >= 4) {
-        // queries: rows of 128 bytes with the 128-byte swizzle, 64 columns a sub-tile; zeros past the rows
         if (n > 0) {
-            const int ch = (threadIdx.x - 128) % (D / 8), first = it.m0 / p.gq, rem = it.m0 % p.gq;
-            const float inv = 1.f / static_cast<float>(p.gq);
-            const T* base = static_cast<const T*>(a.q) + (it.t0 + first) * a.q_stride_t + static_cast<int64_t>(it.h * p.gq) * a.q_stride_h + ch * 8;
-            for (int r = (threadIdx.x - 128) / (D / 8); r < Shape::kQTiles * kTileRows; r += 256 / (D / 8)) {
-                const int x = rem + (r < rows ? r : 0);
-                const int dt = static_cast<int>((static_cast<float>(x) + 0.5f) * inv);        // x / gq: x is small
-                const T* src = base + dt * a.q_stride_t + (x - dt * p.gq) * a.q_stride_h;
-                const int tile = r / kTileRows, rr = r % kTileRows;
-                const uint32_t dst = smem_addr(sq) + tile * kTileRows * D * 2 + (ch >> 3) * kTileRows * 128 + rr * 128 +
-                                     (((ch & 7) ^ (rr & 7)) << 4);
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(r < rows ? 16 : 0) : "memory");
-            }
             asm volatile("cp.async.wait_all;" ::: "memory");
             fence_proxy_async_smem();
             __syncwarp();
@@ -465,6 +468,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             tc_fence_after();
         }
         if (!ok) *abort_flag = 1;
+        let_next_start();
         // ---------------- results ----------------
         float* stage = reinterpret_cast<float*>(smem + t * kTileRows * Shape::kRowBytes + r * Shape::kRowBytes);   // this row's
         float2* jm = reinterpret_cast<float2*>(smem + 2 * kTileRows * Shape::kRowBytes);       // (m, l) of accumulator 1
@@ -551,6 +555,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
+    wait_for_previous();
 }
 
 }  // namespace rl
