@@ -54,8 +54,8 @@ int rl_page_plan(const rl_page_plan_args* a, int32_t* dev_status, void* stream) 
     if (a->R < 0 || a->T < 0 || a->G < 0 || a->n_free < 0 || a->n_pages < 0 || a->table_width < 0)
         return fail(RL_ERR_ARG, "negative size");
     if (!page_size_ok(a->page_size)) return fail(RL_ERR_UNSUPPORTED, "page_size must be 16, 32, 64 or 128");
-    if (a->R >= kMax31 || a->T >= kMax31 || a->G >= kMax31 || a->n_free >= kMax31 || a->n_pages >= kMax31)
-        return fail(RL_ERR_UNSUPPORTED, "R, T, G, n_free or n_pages too large");
+    if (a->R >= kMax31 || a->T >= kMax31 || a->G >= kMax31 || a->n_free >= kMax31 || a->n_pages >= kMax31 || a->table_width >= kMax31)
+        return fail(RL_ERR_UNSUPPORTED, "R, T, G, n_free, n_pages or table_width too large");
     if (!a->cu_q || !a->free_used_out || (a->R > 0 && (!a->q_lens || !a->ctx_lens || !a->kv_lens)) ||
         (a->T > 0 && !a->slot_map) || (a->R > 0 && a->table_width > 0 && !a->block_table) ||
         (a->n_free > 0 && !a->free_pages))

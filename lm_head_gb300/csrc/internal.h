@@ -1,6 +1,7 @@
 // Host-side declarations shared by the translation units of librlhead.
 #pragma once
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <cuda_runtime.h>
@@ -84,6 +85,17 @@ struct ProfScope {
     ~ProfScope();
 };
 void set_last_error(const char* msg);
+// Lets a kernel use `bytes` of dynamic shared memory, once a device (`done`: one bit each).
+template <typename K>
+inline bool allow_smem(K kernel, int bytes, std::atomic<uint64_t>& done) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return false;
+    const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+    if (bit && (done.load(std::memory_order_relaxed) & bit)) return true;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+    done.fetch_or(bit, std::memory_order_relaxed);
+    return true;
+}
 int num_sms();
 // Limit of the kernels' work-loop waits, ns (RL_OPT_WAIT_LIMIT_US; read at each launch).
 uint64_t wait_limit_ns();

@@ -54,6 +54,9 @@ RL_DEVINL Scan2 block_scan2(long long a, long long b, long long* warp_a, long lo
     return {pa + ia - a, pb + ib - b};
 }
 
+// pages that x tokens take
+RL_DEVINL uint32_t pages_of(uint32_t x, int shift, uint32_t mask) { return (x >> shift) + ((x & mask) ? 1u : 0u); }
+
 struct PlanArgs {
     rl_page_plan_args a;
     int32_t* status;
@@ -78,12 +81,14 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanArgs 
     const int* go = go_shared ? s_go : a.group_offsets;
     const int* pl = go_shared ? s_pl : a.prefix_lens;            // read after the scan's barriers
     const long long used = a.free_used ? max(*a.free_used, 0) : 0;
-    const long long W = a.table_width;
-    const int mask = a.page_size - 1;
+    const uint32_t W = static_cast<uint32_t>(a.table_width);
+    const uint32_t mask = static_cast<uint32_t>(a.page_size) - 1u;
     const long long t0 = min(blockIdx.x * p.tokens_per_block, static_cast<long long>(a.T));
+    const long long t1 = min(t0 + p.tokens_per_block, static_cast<long long>(a.T));
     // the last block goes on past T, for the table entries of tokens that the step leaves out
-    const long long t1 = blockIdx.x == gridDim.x - 1 ? LLONG_MAX : t0 + p.tokens_per_block;
+    const bool closes = blockIdx.x == gridDim.x - 1;
     const long long tiles = (a.R + kPlanTile - 1) / kPlanTile;
+    const bool aligned = ((reinterpret_cast<uintptr_t>(a.q_lens) | reinterpret_cast<uintptr_t>(a.ctx_lens)) & 15) == 0;
     long long cu = 0, pages = 0;             // tokens and new pages before this tile
     int bits = 0;
     if (blockIdx.x == 0 && threadIdx.x == 0) {
@@ -92,19 +97,19 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanArgs 
     }
 
     // page of the request's table entry `pi`: one of the pages handed out now, or one it has
-    auto page_at = [&](long long r, int i, long long pi) -> int {
-        const long long had = min((static_cast<long long>(s_ctx[i]) + mask) >> p.shift, W);
+    auto page_at = [&](long long r, int i, uint32_t pi) -> int {
+        const uint32_t had = min(pages_of(static_cast<uint32_t>(s_ctx[i]), p.shift, mask), W);
         int page = -1;
         if (pi >= W) {
             bits |= RL_STATUS_PAGES;
         } else if (pi < had) {
-            page = a.block_table[r * W + pi];
+            page = a.block_table[r * a.table_width + pi];
             if (page < 0 || page >= a.n_pages) {
                 page = -1;
                 bits |= RL_STATUS_PAGE_ID;
             }
         } else {
-            const long long k = used + pages + s_n[i] + (pi - had);
+            const long long k = used + pages + s_n[i] + static_cast<int>(pi - had);
             if (k >= a.n_free) {
                 bits |= RL_STATUS_PAGES;
             } else {
@@ -121,16 +126,26 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanArgs 
     for (long long tile = 0; tile < tiles; ++tile) {
         const bool mine = tile % gridDim.x == blockIdx.x;
         const long long next_mine = tile + (blockIdx.x + gridDim.x - tile % gridDim.x) % gridDim.x;
-        if (cu >= t1 && next_mine >= tiles) break;        // the block's tokens and tiles are done
+        if (!closes && cu >= t1 && next_mine >= tiles) break;        // the block's tokens and tiles are done
         const long long r0 = tile * kPlanTile;
         const int n = static_cast<int>(min(static_cast<long long>(kPlanTile), a.R - r0));
         int q[kPlanItems], ctx[kPlanItems], fresh[kPlanItems];
-        long long qs = 0, ns = 0;
+        long long qs = 0;
+        uint32_t ns = 0;                     // at most 8 * 2^28
+        const int mine0 = threadIdx.x * kPlanItems;
+        if (aligned && mine0 + kPlanItems <= n) {
 #pragma unroll
-        for (int k = 0; k < kPlanItems; ++k) {
-            const int i = threadIdx.x * kPlanItems + k;
-            q[k] = i < n ? a.q_lens[r0 + i] : 0;
-            ctx[k] = i < n ? a.ctx_lens[r0 + i] : 0;
+            for (int k = 0; k < kPlanItems; k += 4) {
+                const int4 x = *reinterpret_cast<const int4*>(a.q_lens + r0 + mine0 + k), y = *reinterpret_cast<const int4*>(a.ctx_lens + r0 + mine0 + k);
+                q[k] = x.x; q[k + 1] = x.y; q[k + 2] = x.z; q[k + 3] = x.w;
+                ctx[k] = y.x; ctx[k + 1] = y.y; ctx[k + 2] = y.z; ctx[k + 3] = y.w;
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < kPlanItems; ++k) {
+                q[k] = mine0 + k < n ? a.q_lens[r0 + mine0 + k] : 0;
+                ctx[k] = mine0 + k < n ? a.ctx_lens[r0 + mine0 + k] : 0;
+            }
         }
 #pragma unroll
         for (int k = 0; k < kPlanItems; ++k) {
@@ -139,16 +154,18 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanArgs 
                 q[k] = max(q[k], 0);
                 ctx[k] = max(ctx[k], 0);
             }
-            const long long had = min((static_cast<long long>(ctx[k]) + mask) >> p.shift, W);
-            const long long need = min((static_cast<long long>(ctx[k]) + q[k] + mask) >> p.shift, W);
-            fresh[k] = static_cast<int>(need - had);
+            const uint32_t had = pages_of(static_cast<uint32_t>(ctx[k]), p.shift, mask);
+            const uint32_t need = pages_of(static_cast<uint32_t>(ctx[k]) + static_cast<uint32_t>(q[k]), p.shift, mask);
+            fresh[k] = static_cast<int>(min(need, W) - min(had, W));
+            if (mine && need > W && q[k] > 0) bits |= RL_STATUS_PAGES;
             qs += q[k];
-            ns += fresh[k];
+            ns += static_cast<uint32_t>(fresh[k]);
         }
         long long tq, tn;
-        const Scan2 s = block_scan2(qs, ns, warp_a, warp_b, tq, tn);
+        const Scan2 s = block_scan2(qs, static_cast<long long>(ns), warp_a, warp_b, tq, tn);
         const bool tokens = cu < t1 && cu + tq > t0;      // some of the block's tokens are here
-        if (mine || tokens) {
+        const bool excess = closes && cu + tq > a.T;
+        if (mine || tokens || excess) {
             // tile-relative sums past 2^31 are cut there: they lie past T, which is below it
             long long iq = s.a, in = s.b;
             int g = 0;
@@ -193,34 +210,42 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanArgs 
             // four consecutive tokens a thread, aligned to the block's first token (a multiple of 4)
             for (long long t = (b0 & ~3ll) + threadIdx.x * 4; t < b1; t += kPlanThreads * 4) {
                 const long long ta = max(t, b0), tb = min(t + 4, b1);
-                int lo = 0, hi = n;                        // last i with s_q[i] <= ta - cu
+                // tokens of the tile fit 31 bits up to T; those past it are clamped with the sums
+                const int x0 = static_cast<int>(min(t - cu, static_cast<long long>(INT_MAX - 4))), xa = static_cast<int>(min(ta - cu, static_cast<long long>(INT_MAX - 4)));
+                const int take = static_cast<int>(tb - t), skip = static_cast<int>(ta - t);
+                int lo = 0, hi = n;                        // last i with s_q[i] <= xa
                 while (hi - lo > 1) {
                     const int mid = (lo + hi) >> 1;
-                    if (s_q[mid] <= ta - cu) lo = mid;
+                    if (s_q[mid] <= xa) lo = mid;
                     else hi = mid;
                 }
                 long long slot[4];
                 int pos[4];
-                int page = -1, page_r = -1;
-                long long page_i = -1;
+                int page = -1, page_r = -1, from = s_q[lo], to = s_q[lo + 1], ctx0 = s_ctx[lo], pre0 = s_pre[lo];
+                uint32_t page_i = 0;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const long long x = t + k;
-                    if (x < ta || x >= tb) continue;
-                    while (s_q[lo + 1] <= x - cu) ++lo;
-                    const long long at = static_cast<long long>(s_ctx[lo]) + (x - cu - s_q[lo]);
-                    const long long pi = at >> p.shift;
+                    if (k < skip || k >= take) continue;
+                    if (x0 + k >= to) {
+                        while (lo + 1 < kPlanTile && s_q[lo + 1] <= x0 + k) ++lo;
+                        from = s_q[lo];
+                        to = s_q[lo + 1];
+                        ctx0 = s_ctx[lo];
+                        pre0 = s_pre[lo];
+                    }
+                    const uint32_t at = static_cast<uint32_t>(ctx0) + static_cast<uint32_t>(x0 + k - from);
+                    const uint32_t pi = at >> p.shift;
                     if (lo != page_r || pi != page_i) {
                         page = page_at(r0 + lo, lo, pi);
                         page_r = lo;
                         page_i = pi;
                     }
                     // the first token of a new page writes its entry
-                    if ((at & mask) == 0 && pi < W) a.block_table[(r0 + lo) * W + pi] = page;
+                    if ((at & mask) == 0 && pi < W) a.block_table[(r0 + lo) * a.table_width + pi] = page;
                     slot[k] = page < 0 ? -1 : (static_cast<long long>(page) << p.shift) + (at & mask);
-                    pos[k] = static_cast<int>(min(at + s_pre[lo], static_cast<long long>(INT_MAX)));
+                    pos[k] = static_cast<int>(min(static_cast<unsigned long long>(at) + pre0, static_cast<unsigned long long>(INT_MAX)));
                 }
-                const bool whole = ta == t && tb == t + 4 && tb <= a.T;
+                const bool whole = ta == t && tb == t + 4;
                 if (whole && (reinterpret_cast<uintptr_t>(a.slot_map) & 15) == 0) {
                     longlong2* d = reinterpret_cast<longlong2*>(a.slot_map + t);
                     d[0] = make_longlong2(slot[0], slot[1]);
@@ -228,7 +253,7 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanArgs 
                 } else {
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        if (t + k >= ta && t + k < min(tb, static_cast<long long>(a.T))) a.slot_map[t + k] = slot[k];
+                        if (t + k >= ta && t + k < tb) a.slot_map[t + k] = slot[k];
                 }
                 if (a.positions) {
                     if (whole && (reinterpret_cast<uintptr_t>(a.positions) & 15) == 0) {
@@ -236,9 +261,24 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanArgs 
                     } else {
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            if (t + k >= ta && t + k < min(tb, static_cast<long long>(a.T))) a.positions[t + k] = pos[k];
+                            if (t + k >= ta && t + k < tb) a.positions[t + k] = pos[k];
                     }
                 }
+            }
+        }
+        if (excess) {
+            // the new pages whose first token lies past T, one a thread and step (a row's width bounds them)
+            for (long long j = threadIdx.x; j < tn; j += kPlanThreads) {
+                int lo = 0, hi = n;                        // last i with s_n[i] <= j
+                while (hi - lo > 1) {
+                    const int mid = (lo + hi) >> 1;
+                    if (s_n[mid] <= j) lo = mid;
+                    else hi = mid;
+                }
+                const uint32_t c = static_cast<uint32_t>(s_ctx[lo]);
+                const uint32_t pi = min(pages_of(c, p.shift, mask), W) + static_cast<uint32_t>(j - s_n[lo]);
+                const long long first = (static_cast<long long>(pi) << p.shift) - c;      // in the request's step
+                if (pi < W && cu + s_q[lo] + first >= a.T) a.block_table[(r0 + lo) * a.table_width + pi] = page_at(r0 + lo, lo, pi);
             }
         }
         cu += tq;
@@ -250,19 +290,19 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanArgs 
                 if (cu != a.T) bits |= RL_STATUS_LENGTHS;
             }
             // tokens that no request has
-            for (long long t = max(t0, cu) + threadIdx.x; t < min(t1, static_cast<long long>(a.T)); t += kPlanThreads) {
+            for (long long t = max(t0, cu) + threadIdx.x; t < t1; t += kPlanThreads) {
                 a.slot_map[t] = -1;
                 if (a.positions) a.positions[t] = -1;
             }
         }
-        if (mine || tokens) __syncthreads();               // the tile's shared arrays have been read
+        if (mine || tokens || excess) __syncthreads();               // the tile's shared arrays have been read
     }
     if (tiles == 0 && blockIdx.x == 0 && threadIdx.x == 0) {
         *a.free_used_out = static_cast<int>(used);
         if (a.T != 0) bits |= RL_STATUS_LENGTHS;
     }
     if (tiles == 0)
-        for (long long t = t0 + threadIdx.x; t < min(t1, static_cast<long long>(a.T)); t += kPlanThreads) {
+        for (long long t = t0 + threadIdx.x; t < t1; t += kPlanThreads) {
             a.slot_map[t] = -1;
             if (a.positions) a.positions[t] = -1;
         }
@@ -274,8 +314,10 @@ int page_plan_impl(const rl_page_plan_args* a, int32_t* status, cudaStream_t str
     p.a = *a;
     p.status = status;
     p.shift = __builtin_ctz(static_cast<unsigned>(a->page_size));
-    // up to four blocks a multiprocessor, a whole number of 1024-token steps each
-    const long long cap = 4ll * num_sms();
+    // up to two blocks a multiprocessor, a whole number of 1024-token steps each (every block scans the
+    // lengths up to its tokens, so more of them scan more: four a multiprocessor took 39 us against
+    // 26 us for 8192 requests and 2.1M tokens)
+    const long long cap = 2ll * num_sms();
     const long long steps = (a->T + 1023) / 1024;
     p.tokens_per_block = ((steps + cap - 1) / cap) * 1024;
     if (p.tokens_per_block == 0) p.tokens_per_block = 1024;

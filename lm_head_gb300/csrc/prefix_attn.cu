@@ -666,7 +666,8 @@ static int launch_parts(AttnArgs p, AttnKind kind, bool prefix, bool own, bool f
     const int smem = kind == kWarp   ? warp_smem_bytes<D>()
                      : kind == kKeys ? TileShape<D, true>::kSmemBytes
                                      : TileShape<D, false>::kSmemBytes;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return RL_ERR_CUDA;
+    static std::atomic<uint64_t> done[3];
+    if (!allow_smem(kernel, smem, done[kind])) return RL_ERR_CUDA;
     ++*launches;
     return launch(kernel, items, kind == kWarp ? kWarpThreads : kTileThreads, smem, follows, stream, tmK, tmV, p);
 }

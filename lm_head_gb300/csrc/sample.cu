@@ -407,6 +407,7 @@ struct SelShared {
     RowRec rec;
     // then: unsigned long long cs[ns]; int cnt[ns], in[ns]; uint16_t subs[ns]
 };
+constexpr size_t kMaxParts = (1 << 20) / kSub;      // V <= 2^20
 constexpr size_t kSelPart = sizeof(unsigned long long) + 2 * sizeof(int) + sizeof(uint16_t);
 
 template <typename T>
@@ -1308,8 +1309,8 @@ static int sample_run(const SampleArgs& g, cudaStream_t stream) {
     const long long cap = 2ll * num_sms();
     if (blocks > cap) blocks = cap;
     const size_t smem = sizeof(SelShared) + static_cast<size_t>(g.ns) * kSelPart;
-    if (cudaFuncSetAttribute(select_kernel<T, kVec>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
-        return RL_ERR_CUDA;
+    static std::atomic<uint64_t> done{0};
+    if (!allow_smem(select_kernel<T, kVec>, static_cast<int>(sizeof(SelShared) + kMaxParts * kSelPart), done)) return RL_ERR_CUDA;
     ProfScope prof(RL_PROF_OTHER, stream);
     stats_kernel<T, kVec><<<static_cast<unsigned>(blocks), kStatThreads, 0, stream>>>(g);
     select_kernel<T, kVec><<<static_cast<unsigned>(g.a.N), kSelThreads, smem, stream>>>(g);

@@ -146,6 +146,18 @@ def test_plan_bad_inputs_set_status_and_stay_in_bounds():
     check_plan([3, 2, 4, 1], [1, 1, 1, 1], t2, np.arange(4), None, page, 9, 10, want_bits=PAGE_ID)
 
 
+def test_plan_lengths_far_past_the_step():
+    """Lengths whose sum passes T by far, up to 2^31 - 1 each: the call ends at once, the table holds
+    what the rows have room for, and nothing past the buffers is written."""
+    page, W, big = 16, 3, 2 ** 31 - 1
+    t = np.full((5, W), -1)
+    p, table = run_plan([big, 5, big, 7, big], [0, 0, big, 3, 17], t, np.arange(30), None, page, 30, 40)
+    assert p.status_bits() & LENGTHS and p.status_bits() & PAGES
+    np.testing.assert_array_equal(table[0], [0, 1, 2])
+    np.testing.assert_array_equal(table[1], [3, -1, -1])
+    assert p.slot_map.cpu().tolist() == list(range(40))
+
+
 def test_plan_without_requests():
     p, _ = run_plan(np.zeros(0), np.zeros(0), np.zeros((0, 2)), np.arange(3), 2, 16, 3, 0)
     assert p.cu_q.tolist() == [0] and int(p.free_used.item()) == 2 and p.status_bits() == 0
