@@ -53,6 +53,11 @@ RL_DEVINL float exp2_approx(float x) {  // hardware 2^x (MUFU EX2, about 2 ulp; 
     return y;
 }
 
+// Programmatic launches: a kernel lets the next one's blocks start, and waits for the one before it
+// (its results, and that it ends first).
+RL_DEVINL void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+RL_DEVINL void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // ---------------------------------------------------------------------------------
 // Shared-memory addresses, mbarriers
 // ---------------------------------------------------------------------------------

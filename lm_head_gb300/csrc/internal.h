@@ -96,6 +96,22 @@ inline bool allow_smem(K kernel, int bytes, std::atomic<uint64_t>& done) {
     done.fetch_or(bit, std::memory_order_relaxed);
     return true;
 }
+// `follows`: a programmatic launch, which may start beside the kernel before it on the stream; it calls
+// wait_for_previous itself.
+template <typename K, typename... A>
+inline int launch_after(K kernel, dim3 grid, int threads, size_t smem, bool follows, cudaStream_t stream, const A&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = follows ? 1 : 0;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? RL_OK : RL_ERR_CUDA;
+}
 int num_sms();
 // Limit of the kernels' work-loop waits, ns (RL_OPT_WAIT_LIMIT_US; read at each launch).
 uint64_t wait_limit_ns();

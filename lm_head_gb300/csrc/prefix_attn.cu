@@ -233,12 +233,9 @@ template <int D>
 constexpr int warp_stage_bytes() { return 2 * kStageKeys * D * 2; }
 template <int D>
 constexpr int warp_smem_bytes() { return kWarpStages * warp_stage_bytes<D>() + 1024 + 256; }
-// Programmatic launches: a kernel lets the next one's blocks start, and waits for the one before it
-// (its results, and that it ends first).  The next one is let in when a block has its sums: let in at
-// the start, its waiting blocks held registers that this one's blocks needed (139 us instead of
+// The kernels of a call are programmatic launches.  The next one is let in when a block has its sums:
+// let in at the start, its waiting blocks held registers that this one's blocks needed (139 us instead of
 // 133 for 64 requests of up to 4096 keys).
-RL_DEVINL void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-RL_DEVINL void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kWarpThreads)
@@ -626,22 +623,6 @@ size_t prefix_attn_ws_bytes(const rl_prefix_attn_args* a) {
     return b;
 }
 
-// `follows`: the kernel may start beside the one before it on the stream, which it waits for itself.
-template <typename K, typename... A>
-static int launch(K kernel, int64_t blocks, int threads, size_t smem, bool follows, cudaStream_t stream, const A&... args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(blocks), 1, 1);
-    cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = follows ? 1 : 0;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? RL_OK : RL_ERR_CUDA;
-}
-
 template <typename T, int D>
 static int launch_parts(AttnArgs p, AttnKind kind, bool prefix, bool own, bool follows, cudaStream_t stream, int* launches) {
     const rl_prefix_attn_args& a = p.a;
@@ -669,7 +650,7 @@ static int launch_parts(AttnArgs p, AttnKind kind, bool prefix, bool own, bool f
     static std::atomic<uint64_t> done[3];
     if (!allow_smem(kernel, smem, done[kind])) return RL_ERR_CUDA;
     ++*launches;
-    return launch(kernel, items, kind == kWarp ? kWarpThreads : kTileThreads, smem, follows, stream, tmK, tmV, p);
+    return launch_after(kernel, dim3(static_cast<unsigned>(items)), kind == kWarp ? kWarpThreads : kTileThreads, smem, follows, stream, tmK, tmV, p);
 }
 
 template <typename T, int D>
@@ -686,7 +667,7 @@ static int attn_run(const AttnArgs& p, AttnKind kp, AttnKind ko, cudaStream_t st
     if (rc != RL_OK) return rc;
     const int64_t rows_q = a.T * a.Hq;
     if (p.sp + p.so > 1 || launches == 0) {
-        rc = launch(join_kernel<T, D>, (rows_q + kJoinThreads / 32 - 1) / (kJoinThreads / 32), kJoinThreads, 0, launches > 0, stream, p);
+        rc = launch_after(join_kernel<T, D>, dim3(static_cast<unsigned>((rows_q + kJoinThreads / 32 - 1) / (kJoinThreads / 32))), kJoinThreads, 0, launches > 0, stream, p);
         if (rc != RL_OK) return rc;
         ++launches;
     }

@@ -374,6 +374,7 @@ __global__ void __launch_bounds__(kStatThreads, 2) stats_kernel(const SampleArgs
         if (lane == 0) g.ref[r * g.nc + c] = ref_out;
     }
     if (bad) set_status(g.status, RL_STATUS_NONFINITE);
+    let_next_start();
 }
 
 // ---- 2. selection and draws ------------------------------------------------------------
@@ -540,20 +541,25 @@ struct Row {
                 any_mid |= mid[j];
             }
             if (__any_sync(0xffffffffu, any_up)) {
-                LaneSum acc;
+                // those above one after another in shared memory, so that few of them cost few weights
+                float* dense = reinterpret_cast<float*>(s.wt) + warp * kSub;      // the list has no weights yet
                 int n = 0;
-                float hi[4], v[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const bool w = up[j] && z[j] >= zlow;
-                    const FF d = two_sum(w ? z[j] : M, -M);
-                    weight_pair(d.hi, d.lo, c, 6144.f, s.tab, hi[j], v[j]);
-                    if (!w) hi[j] = v[j] = 0.f;
-                    n += up[j] ? 1 : 0;
+                    const unsigned m = __ballot_sync(0xffffffffu, up[j]);
+                    if (up[j]) dense[n + __popc(m & ((1u << lane) - 1u))] = z[j];
+                    n += __popc(m);
                 }
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc.add(hi[j], v[j]);
-                n = __reduce_add_sync(0xffffffffu, n);
+                __syncwarp();
+                LaneSum acc;
+                for (int i = lane; i < n; i += 32) {
+                    const float x = dense[i];
+                    const FF d = two_sum(fmaxf(x, zlow), -M);
+                    float hi, v;
+                    weight_pair(d.hi, d.lo, c, 6144.f, s.tab, hi, v);
+                    if (x >= zlow) acc.add(hi, v);
+                }
+                __syncwarp();
                 const uint32_t wt = acc.warp_top();
                 const int wl = acc.warp_low();
                 if (lane == 0) {
@@ -953,6 +959,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SampleArgs
                    tid, tid & 31, tid >> 5, 0.f, 0.f, {0.f, 0.f}, 0u, INT_MAX};
     const Knobs q = load_knobs(a, r);
     fill_table(s.tab, tid, kSelThreads);
+    wait_for_previous();
     unsigned long long mk = 0;
     for (int i = tid; i < g.ns; i += kSelThreads) mk = max(mk, static_cast<unsigned long long>(key_of(w.submax[i] + 0.f)));
     const float M = z_of(static_cast<uint32_t>(block_max(mk, s.red)));
@@ -1137,6 +1144,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SampleArgs
         for (int d = w.warp; d < a.K; d += kSelWarps) w.draw(r, d, total);
     }
     __syncthreads();
+    let_next_start();
     if (a.replayed && tid == 0) a.replayed[r] = q.cut ? 1 : 0;
     if (a.offsets) {
         if (tid == 0) {
@@ -1190,6 +1198,7 @@ __global__ void __launch_bounds__(kEmitThreads) emit_kernel(const SampleArgs g) 
     const int lane = threadIdx.x & 31;
     const int parts = gridDim.x;
     const int V = static_cast<int>(a.V);
+    wait_for_previous();
     for (long long r = blockIdx.y; r < a.N; r += gridDim.y) {
         const RowRec rec = g.rec[r];
         const T* row = static_cast<const T*>(a.logits) + r * a.row_stride;
@@ -1313,13 +1322,15 @@ static int sample_run(const SampleArgs& g, cudaStream_t stream) {
     if (!allow_smem(select_kernel<T, kVec>, static_cast<int>(sizeof(SelShared) + kMaxParts * kSelPart), done)) return RL_ERR_CUDA;
     ProfScope prof(RL_PROF_OTHER, stream);
     stats_kernel<T, kVec><<<static_cast<unsigned>(blocks), kStatThreads, 0, stream>>>(g);
-    select_kernel<T, kVec><<<static_cast<unsigned>(g.a.N), kSelThreads, smem, stream>>>(g);
     int launches = 2;
+    int rc = launch_after(select_kernel<T, kVec>, dim3(static_cast<unsigned>(g.a.N)), kSelThreads, smem, true, stream, g);
+    if (rc != RL_OK) return rc;
     if (g.a.offsets) {
         // a block takes 256 parts a step; rows beyond the grid's share are looped over
         const int parts = static_cast<int>((g.ns + kEmitThreads - 1) / kEmitThreads);
         const dim3 grid(static_cast<unsigned>(parts), static_cast<unsigned>(g.a.N < 16384 ? g.a.N : 16384), 1);
-        emit_kernel<T, kVec><<<grid, kEmitThreads, 0, stream>>>(g);
+        rc = launch_after(emit_kernel<T, kVec>, grid, kEmitThreads, 0, true, stream, g);
+        if (rc != RL_OK) return rc;
         ++launches;
     }
     count_launch(launches);

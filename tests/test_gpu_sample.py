@@ -178,6 +178,13 @@ def test_strided_and_unaligned_rows(dt):
             check(z, rand_u(z.shape[0], 3, 2), **knobs(kind, z.shape[0], V, 3))
 
 
+def test_the_largest_vocabulary():
+    V = 1 << 20
+    z = logits(3, V, "bf16", 21)
+    for kn in ({}, {"top_k": [7, 100000, 0], "top_p": [0.9, 0.5, 0.97]}):
+        check(z, rand_u(3, 3, 6), **kn)
+
+
 def test_capacity_is_respected():
     N, V = 5, 4000
     z, kn = logits(N, V, "fp32", 2), dict(top_p=np.full(5, 0.9))
