@@ -584,7 +584,7 @@ typedef struct rl_prefix_attn_args {
     void* out;                      /* device [T, Hq, D] dense */
     float* lse;                     /* device [T, Hq] natural log of the sum; NULL to skip */
 } rl_prefix_attn_args;
-/* Depends on sizes and bounds only, not on the pointers. */
+/* Depends on sizes and bounds only, not on the pointers; 16-byte aligned, with any contents. */
 size_t rl_prefix_attn_workspace_bytes(const rl_prefix_attn_args* args);
 int rl_prefix_attn(const rl_prefix_attn_args* args, void* ws, size_t ws_bytes, int32_t* dev_status, void* stream);
 
@@ -596,7 +596,7 @@ int rl_prefix_attn(const rl_prefix_attn_args* args, void* ws, size_t ws_bytes, i
  *                whose sum of w reaches top_p times the candidates' sum; at least one token
  *   q(i)         w_i / sum_S w
  *   draw u       the first token i of S, in index order, with sum_{j in S, j <= i} w_j > u sum_S w
- * Sums that decide a token or a set member are carried to about 2^-37 of the largest weight, so that these
+ * Sums that decide a token or a set member are carried to about 2^-36 of the largest weight, so that these
  * agree with exact arithmetic except where a random number falls that near to a border.
  * T = 0 is greedy: S is the largest logit (the lowest index of equal ones).  top_k outside
  * [1, V), top_p >= 1 and min_p <= 0 leave their cut out; top_p <= 0 and min_p > 1 keep one
@@ -626,6 +626,8 @@ typedef struct rl_sample_args {
     int64_t capacity;
     uint8_t* replayed;              /* device [N]; NULL to skip */
 } rl_sample_args;
+/* Zero the workspace once before its first use (16-byte aligned): every call leaves its counter
+ * at zero again.  Calls that overlap on the GPU must not share a workspace. */
 size_t rl_sample_workspace_bytes(int64_t N, int64_t V, int32_t K);
 int rl_sample(const rl_sample_args* args, void* ws, size_t ws_bytes, int32_t* dev_status, void* stream);
 

@@ -5,7 +5,11 @@
 //                     stretch; block b also writes the per-request outputs of tiles b,
 //                     b + grid, ...  A new page's table entry is written with the first token in it
 //                     (every new page has one).  No second launch, no block waits for another.
-//  kv_append_kernel   16 bytes a thread and step, four loads in flight.
+//                     26 us for 8192 requests with 2.1M tokens (25 MB written, 0.96 TB/s: every block
+//                     scans the lengths up to its tokens), 8 us for 128 requests of one token (a
+//                     chain of dependent loads and barriers in one block).
+//  kv_append_kernel   16 bytes a thread and step, four loads in flight.  65,536 tokens of 8 heads of
+//                     128 in 91.5 us: 5.9 TB/s, 88 % of a plain copy; 128 tokens of 4 heads in 3.1 us.
 #include <climits>
 
 #include "common.cuh"
