@@ -504,23 +504,32 @@ struct Row {
         return static_cast<int>(s.n_sub);
     }
     // f(z[4], first index, part) for the logits of the listed parts, by all lanes together, a warp a
-    // part with four parts' loads in flight.
+    // part, the next two parts' logits on their way.  (Four parts at a time, unrolled, ran out of
+    // the instruction cache.)
     template <typename F>
     RL_DEVINL void each(F f) {
         const int n = static_cast<int>(s.n_sub);
-        for (int i0 = warp * 4; i0 < n; i0 += kSelWarps * 4) {
-            float z[4][4];
-            int part[4];
+        Quad<T> ahead[2];
+        int part[2];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                part[q] = i0 + q < n ? subs[i0 + q] : -1;
-                if (part[q] >= 0) load4<T, kVec>(row, part[q] * kSub + lane * 4, V, z[q]);
-            }
+        for (int q = 0; q < 2; ++q) {
+            const int i = warp + q * kSelWarps;
+            part[q] = i < n ? subs[i] : -1;
+            if (part[q] >= 0) ahead[q].template load<kVec>(row, part[q] * kSub + lane * 4, V);
+        }
+#pragma unroll 1
+        for (int i = warp; i < n; i += kSelWarps) {
+            float z[4];
+            ahead[0].get(z);
+            const int now = part[0];
+            ahead[0] = ahead[1];
+            part[0] = part[1];
+            const int next = i + 2 * kSelWarps;
+            part[1] = next < n ? subs[next] : -1;
+            if (part[1] >= 0) ahead[1].template load<kVec>(row, part[1] * kSub + lane * 4, V);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                if (part[q] < 0) break;
-                f(z[q], part[q] * kSub + lane * 4, part[q]);
-            }
+            for (int j = 0; j < 4; ++j) z[j] = (z[j] < INFINITY ? z[j] : -INFINITY) + 0.f;
+            f(z, now * kSub + lane * 4, now);
         }
     }
 
