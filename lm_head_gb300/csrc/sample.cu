@@ -26,11 +26,12 @@
 //   stats   63 us for 256 fp32 rows (2.5 TB/s): bound by instruction issue, some 40 a logit where
 //           sums are taken; the float-pair sum is what equality with exact arithmetic costs.
 //   select  17 us for 128 whole rows with 17 draws (latency: barriers and one part a draw);
-//           229 us for 256 rows whose nucleus is some 20,000 tokens: two passes over the row by one
-//           block, at a third to a half of its issue slots.  Clusters of 2, 4 and 8 blocks that
-//           share the passes were slower (400 to 900 us): the others wait while the first sorts,
-//           scans and draws.
-//   emit    63 us for the 5 million entries of those rows.
+//           195 us for 256 rows whose nucleus is some 20,000 tokens: two passes over the row by one
+//           block, bound by issue and the instruction cache.  Clusters of 2, 4 and 8 blocks that
+//           share the passes were slower (the whole call 533 to 1036 us against 356 then): the
+//           others wait while the first sorts, scans and draws.  So was a block of 1024 threads
+//           alone on its multiprocessor for such rows (451 us against 317).
+//   emit    70 us for the 5 million entries of those rows.
 #include <cfloat>
 #include <climits>
 #include <cmath>
@@ -1252,52 +1253,57 @@ __global__ void __launch_bounds__(kEmitThreads) emit_kernel(const SampleArgs g) 
             uint8_t* ki = kept_i[threadIdx.x >> 5];
             const float zk = z_of(rec.key);
             const int total = static_cast<int>(min(static_cast<long long>(a.offsets[r + 1]) - base, static_cast<long long>(INT_MAX)));
-            // 32 parts a warp and step; those that keep tokens four at a time
+            // 32 parts a warp and step
             for (int p0 = (blockIdx.x * (kEmitThreads / 32) + (threadIdx.x >> 5)) * 32; p0 < g.ns; p0 += parts * kEmitThreads) {
                 const int mine = p0 + lane;
                 const int from = mine < g.ns ? cpre[mine] : 0;
                 const int to = mine < g.ns ? (mine + 1 < g.ns ? cpre[mine + 1] : total) : 0;
                 unsigned todo = __ballot_sync(0xffffffffu, to > from);
-                while (todo) {
-                    float z[4][4];
-                    int part[4];
+                // one part after another, the next two parts' logits on their way
+                Quad<T> ahead[2];
+                int part[2];
+                auto fetch = [&](int q) {
+                    part[q] = todo ? __ffs(todo) - 1 : -1;
+                    todo &= todo - 1u;
+                    if (part[q] >= 0) ahead[q].template load<kVec>(row, (p0 + part[q]) * kSub + lane * 4, V);
+                };
+                fetch(0);
+                fetch(1);
+#pragma unroll 1
+                while (part[0] >= 0) {
+                    float z[4];
+                    ahead[0].get(z);
+                    const int now = part[0];
+                    ahead[0] = ahead[1];
+                    part[0] = part[1];
+                    fetch(1);
+                    // the part's kept logits one after another in shared memory, then dense arithmetic
+                    const int i0 = (p0 + now) * kSub + lane * 4;
+                    int have = 0, at = 0;              // index order: a lane's four logits are neighbours
+                    unsigned keeps = 0;
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        part[q] = todo ? __ffs(todo) - 1 : -1;
-                        todo &= todo - 1u;
-                        if (part[q] >= 0) load4_raw<T, kVec>(row, (p0 + part[q]) * kSub + lane * 4, V, z[q]);
+                    for (int j = 0; j < 4; ++j) {
+                        const bool keep = (z[j] > zk && z[j] < INFINITY) || (z[j] == zk && i0 + j <= rec.tie);
+                        const unsigned m = __ballot_sync(0xffffffffu, keep);
+                        at += __popc(m & ((1u << lane) - 1u));
+                        have += __popc(m);
+                        keeps |= (keep ? 1u : 0u) << j;
                     }
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        if (part[q] < 0) break;
-                        // the part's kept logits one after another in shared memory, then dense arithmetic
-                        const int i0 = (p0 + part[q]) * kSub + lane * 4;
-                        int place = 0, have = 0;
-                        unsigned keeps = 0;
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const bool keep = (z[q][j] > zk && z[q][j] < INFINITY) || (z[q][j] == zk && i0 + j <= rec.tie);
-                            const unsigned m = __ballot_sync(0xffffffffu, keep);
-                            place += __popc(m & ((1u << lane) - 1u));
-                            have += __popc(m);
-                            keeps |= (keep ? 1u : 0u) << j;
+                    for (int j = 0; j < 4; ++j)
+                        if ((keeps >> j) & 1u) {
+                            kz[at] = z[j] + 0.f;
+                            ki[at] = static_cast<uint8_t>(lane * 4 + j);
+                            ++at;
                         }
-                        __syncwarp();
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            if ((keeps >> j) & 1u) {
-                                kz[place] = z[q][j] + 0.f;
-                                ki[place] = static_cast<uint8_t>(lane * 4 + j);
-                                ++place;
-                            }
-                        __syncwarp();
-                        const long long at = base + __shfl_sync(0xffffffffu, from, part[q]);
-                        for (int i = lane; i < have; i += 32) {
-                            if (at + i >= a.capacity) break;
-                            a.ids[at + i] = (p0 + part[q]) * kSub + ki[i];
-                            a.support_logq[at + i] = log_q(kz[i], rec);
-                        }
+                    __syncwarp();
+                    const long long to_at = base + __shfl_sync(0xffffffffu, from, now);
+                    for (int i = lane; i < have; i += 32) {
+                        if (to_at + i >= a.capacity) break;
+                        a.ids[to_at + i] = (p0 + now) * kSub + ki[i];
+                        a.support_logq[to_at + i] = log_q(kz[i], rec);
                     }
+                    __syncwarp();
                 }
             }
         }
