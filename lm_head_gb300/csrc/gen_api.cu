@@ -41,7 +41,7 @@ int check_attn_sizes(const rl_prefix_attn_args* a) {
         a->n_pages * a->Hkv * a->page_size >= kMax31 || a->max_q >= kMax31 || a->max_kv >= kMax31 || a->max_prefix >= kMax31)
         return fail(RL_ERR_UNSUPPORTED, "sizes too large (rows of queries and rows of the cache below 2^31)");
     if (a->T > 0 && a->R > 0 && a->max_q < 1) return fail(RL_ERR_ARG, "max_q must bound the step's lengths");
-    if (!(a->scale >= 0.f) || !std::isfinite(a->scale)) return fail(RL_ERR_ARG, "scale is negative or not finite");
+    if (!(a->scale >= 0.f) || !std::isfinite(a->scale * 1.5f)) return fail(RL_ERR_ARG, "scale is negative, not finite or too large");
     return RL_OK;
 }
 

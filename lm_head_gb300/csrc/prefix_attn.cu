@@ -23,7 +23,9 @@
 // shared prefix of 32,768 keys: 35 us in tile_attn_kernel, 980 TFLOP/s.  A decode step of 128
 // requests in 16 groups (0.1 GB): 33 us, where the chain of one part (lengths, page, keys, join: 6 us)
 // and the join count as much as the bytes.  Four requests of a 130-key prompt: 7.6 us.
+#include <cfloat>
 #include <climits>
+#include <cmath>
 #include <type_traits>
 
 #include <cuda_fp16.h>
@@ -620,7 +622,10 @@ static AttnArgs attn_view(const rl_prefix_attn_args* a, void* ws, size_t* bytes,
     AttnArgs p{};
     p.a = *a;
     p.gq = a->Hq / a->Hkv;
-    p.c = a->scale * kLog2e;
+    // A scale of 0 makes all weights alike.  Unseen keys are scores of -inf, and the tensor-core kernel scales
+    // after it masks: the least normal number in place of 0 keeps them out (-inf * 0 is NaN), and times
+    // any score below 2^100 it is less than half a step of a weight.
+    p.c = fmaxf(a->scale * kLog2e, FLT_MIN);
     const bool prefix = a->G > 0 && a->max_prefix > 0;
     *kp = kind_of(prefix ? (a->T * p.gq + a->G - 1) / a->G : 0);
     *ko = kind_of(a->max_q * p.gq);
