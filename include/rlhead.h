@@ -559,8 +559,10 @@ int rl_kv_append(const rl_kv_append_args* args, int32_t* dev_status, void* strea
  * is read once for all the queries of the group.  Scores, softmax statistics and sums in
  * fp32; the weights are rounded to the cache's type for the second product.  A row that sees
  * no key gets out = 0 and lse = -inf, as do rows past cu_q[R].  What the pages hold past a
- * length (never written entries, NaN included) does not reach the results; a key or value
- * inside a length that is not finite may reach every row of its request's step.
+ * length (never written entries, NaN included) does not reach the results.  A score of NaN or
+ * +inf makes its row NaN, in out and lse; a key whose score is -inf has no weight (a row of
+ * such keys alone is a row that sees none); a value inside a length that is not finite may reach
+ * every row of its request's step (of its group, in a prefix).
  * cu_q that decreases or leaves [0, T], kv_lens[r] < q_len, or a length above its bound sets
  * RL_STATUS_LENGTHS; a page id outside the cache sets RL_STATUS_PAGE_ID; the rows concerned
  * then hold no useful value. */

@@ -481,10 +481,10 @@ __global__ void __launch_bounds__(kWarpThreads)
         float ll = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
-            const float mw = sm[(w * kWarpRows + r) * 2];
-            if (mw == -INFINITY) continue;
+            const float mw = sm[(w * kWarpRows + r) * 2], lw = sm[(w * kWarpRows + r) * 2 + 1];
+            if (lw == 0.f) continue;                             // no key seen (NaN goes on)
             const float f = exp2_approx(mw - mm);
-            ll += f * sm[(w * kWarpRows + r) * 2 + 1];
+            ll += f * lw;
             const float4 v = *reinterpret_cast<const float4*>(so + (w * kWarpRows + r) * kPad + d);
             acc[0] += f * v.x;
             acc[1] += f * v.y;
@@ -493,12 +493,12 @@ __global__ void __launch_bounds__(kWarpThreads)
         }
         const long long row = static_cast<long long>(it.t0 + mr / p.gq) * a.Hq + it.h * p.gq + mr % p.gq;
         if (whole) {
-            const float inv = ll > 0.f ? 1.f / ll : 0.f;
+            const float inv = ll == 0.f ? 0.f : 1.f / ll;
             *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + row * D + d) =
                 make_uint2(Mma<T>::pack(acc[0] * inv, acc[1] * inv), Mma<T>::pack(acc[2] * inv, acc[3] * inv));
-            if (d == 0 && a.lse) a.lse[row] = ll > 0.f ? (mm + log2f(ll)) * kLn2 : -INFINITY;
+            if (d == 0 && a.lse) a.lse[row] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * kLn2;
         } else {
-            if (ll > 0.f) *reinterpret_cast<float4*>(p.po + (it.part * rows_all + row) * D + d) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+            if (ll != 0.f) *reinterpret_cast<float4*>(p.po + (it.part * rows_all + row) * D + d) = make_float4(acc[0], acc[1], acc[2], acc[3]);
             if (d == 0) *reinterpret_cast<float2*>(p.ml + (it.part * rows_all + row) * 2) = make_float2(mm, ll);
         }
     }
@@ -547,7 +547,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttnArgs p) {
     for (int j = 0; j < D / 32; ++j) acc[j] = 0.f;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
-        f[j] = ml[j].y > 0.f ? exp2_approx(ml[j].x - mm) : 0.f;
+        f[j] = ml[j].y == 0.f ? 0.f : exp2_approx(ml[j].x - mm);      // a sum of NaN makes the row NaN
         ll += f[j] * ml[j].y;
     }
     ll = warp_sum(ll);
@@ -582,11 +582,11 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttnArgs p) {
                 for (int d = 0; d < D / 32; ++d) acc[d] = fmaf(w[y], v[y][d], acc[d]);
         }
     }
-    const float inv = ll > 0.f ? 1.f / ll : 0.f;
+    const float inv = ll == 0.f ? 0.f : 1.f / ll;
     T* out = static_cast<T*>(a.out) + row * D + lane * (D / 32);
 #pragma unroll
     for (int j = 0; j < D / 32; j += 2) *reinterpret_cast<uint32_t*>(out + j) = Mma<T>::pack(acc[j] * inv, acc[j + 1] * inv);
-    if (lane == 0 && a.lse) a.lse[row] = ll > 0.f ? (mm + log2f(ll)) * kLn2 : -INFINITY;
+    if (lane == 0 && a.lse) a.lse[row] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * kLn2;
 }
 
 // ---- host ------------------------------------------------------------------------------

@@ -507,7 +507,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             const long long rows_all = a.T * a.Hq;
             const long long row = static_cast<long long>(it.t0 + m_row / p.gq) * a.Hq + it.h * p.gq + m_row % p.gq;
             const bool whole = p.sp + p.so == 1;
-            if (whole) f0 *= l > 0.f ? 1.f / l : 0.f, f1 *= l > 0.f ? 1.f / l : 0.f;
+            // a sum of 0 is a row that sees nothing; one of NaN stays NaN, in the result as in lse
+            const float inv = l == 0.f ? 0.f : whole || l != l ? 1.f / l : 1.f;
+            f0 *= inv;
+            f1 *= inv;
             // a row through shared memory, so that it leaves in one piece
 #pragma unroll 1
             for (int x = 0; x < D / 32; ++x) {
@@ -516,8 +519,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     uint32_t o[32];
                     tmem_load_row32(to + x * 32, o);
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] = f0 > 0.f ? __uint_as_float(o[j]) * f0 : 0.f;
-                    if (kKeys2 && two && f1 > 0.f)
+                    for (int j = 0; j < 32; ++j) v[j] = f0 != 0.f ? __uint_as_float(o[j]) * f0 : 0.f;
+                    if (kKeys2 && two && f1 != 0.f)
 #pragma unroll
                         for (int j = 0; j < 32; j += 4) {
                             const float4 q = *reinterpret_cast<const float4*>(stage + kTileRows * (D + 4) + x * 32 + j);
@@ -544,10 +547,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             fence_proxy_async_smem();
             if (valid) {
                 void* dst = whole ? static_cast<void*>(static_cast<T*>(a.out) + row * D) : static_cast<void*>(p.po + (it.part * rows_all + row) * D);
-                if (whole || l > 0.f) bulk_store(dst, stage, whole ? D * 2 : D * 4);
+                if (whole || l != 0.f) bulk_store(dst, stage, whole ? D * 2 : D * 4);
                 const float ml = m == -INFINITY ? m : m * p.c;        // in log2 units
                 if (whole) {
-                    if (a.lse) a.lse[row] = l > 0.f ? (ml + log2f(l)) * kLn2 : -INFINITY;
+                    if (a.lse) a.lse[row] = l == 0.f ? -INFINITY : (ml + log2f(l)) * kLn2;
                 } else {
                     *reinterpret_cast<float2*>(p.ml + (it.part * rows_all + row) * 2) = make_float2(ml, l);
                 }

@@ -29,3 +29,70 @@ def test_scale_zero_is_the_mean_of_the_values(kind, D, dtype):
     c = make(kind, D, dtype=dtype)
     c.scale = 0.0
     c.check()
+
+
+@pytest.mark.parametrize("kind", [k for k, _ in KINDS])
+def test_a_nan_query_gives_a_nan_row(kind):
+    """One row of one head is NaN in output and lse; all others are what they are without it."""
+    c = make(kind)
+    want = c.check()
+    for t in {0, c.q.shape[0] - 1}:
+        q = c.q.clone()
+        q[t, 3, 5] = float("nan")
+        a = c.run(q)
+        assert bool(torch.isnan(a.out[t, 3]).all()) and bool(torch.isnan(a.lse[t, 3]))
+        rest = torch.ones(c.q.shape[:2], dtype=torch.bool, device="cuda")
+        rest[t, 3] = False
+        assert torch.equal(a.out[rest], want.out[rest]) and torch.equal(a.lse[rest], want.lse[rest])
+
+
+def put(c, r, key, k=None, v=None):
+    """Overwrites key `key` of own pages r, or of group r - len(q_lens)'s prefix, in the cache."""
+    R = len(c.q_lens)
+    table = c.table[r] if r < R else c.ptable[r - R]
+    page = c.kc.shape[2]
+    for cache, x in ((c.kc, k), (c.vc, v)):
+        if x is not None:
+            cache[int(table[key // page]), :, key % page] = x
+
+
+@pytest.mark.parametrize("kind", [k for k, _ in KINDS])
+@pytest.mark.parametrize("what", ["k", "v"])
+def test_a_nan_key_or_value_reaches_every_row_that_sees_it(kind, what):
+    c = make(kind)
+    want = c.check()
+    R = len(c.q_lens)
+    first = [sum(c.q_lens[:r]) for r in range(R + 1)]
+    for r, key in [(R - 1, 0)] + ([(R, len(c.keys[R][0]) // 2)] if c.groups else []):
+        kc, vc = c.kc.clone(), c.vc.clone()
+        put(c, r, key, **{what: float("nan")})
+        a = c.run()
+        hit = torch.zeros(c.q.shape[0], dtype=torch.bool, device="cuda")
+        hit[first[R - 1] if r == R - 1 else 0:] = True       # key 0 is seen by all of the last request's tokens
+        assert bool(torch.isnan(a.out[hit]).all())
+        if what == "k":
+            assert bool(torch.isnan(a.lse[hit]).all())
+        assert torch.equal(a.out[~hit], want.out[~hit]) and torch.equal(a.lse[~hit], want.lse[~hit])
+        c.kc, c.vc = kc, vc
+
+
+@pytest.mark.parametrize("kind", [k for k, _ in KINDS])
+def test_infinite_scores(kind):
+    """A key with an infinity: a row whose score it makes +inf is NaN, as in softmax; where it makes it
+    -inf the key has no weight (and a row of no other key is one that sees none)."""
+    c = make(kind)
+    r = len(c.q_lens) - 1
+    x = c.keys[r][0][0].clone()
+    x[:, 7] = float("inf")
+    put(c, r, 0, k=x.cuda())
+    c.keys[r] = (torch.cat([x[None], c.keys[r][0][1:]]), c.keys[r][1])
+    a = c.run()
+    out, lse, vmax = c.reference()
+    out[lse == -float("inf")] = 0
+    bad = torch.isnan(out).any(-1)
+    assert bool(bad.any()) and bool((~bad).any())
+    got = a.out.cpu().double()
+    assert torch.equal(torch.isnan(got).any(-1), bad)
+    eps = torch.finfo(c.q.dtype).eps
+    bar = eps / 2 * (out.abs() + vmax[..., None]) + 2.0 ** -16 * vmax[..., None]
+    assert bool(((got - out).abs() <= bar)[~bad].all())
