@@ -679,12 +679,15 @@ static int launch_parts(AttnArgs p, AttnKind kind, bool prefix, bool own, bool f
     int rc = make_tmap_2d(&tmK, a.k_cache, dt, 2, rows, D, D, 64, box, 128);
     if (rc == RL_OK) rc = make_tmap_2d(&tmV, a.v_cache, dt, 2, rows, D, D, 64, box, 128);
     if (rc != RL_OK) return rc;
-    const auto kernel = kind == kWarp ? warp_attn_kernel<T, D> : kind == kKeys ? tile_attn_kernel<T, D, true> : tile_attn_kernel<T, D, false>;
+    const bool poll = kind != kWarp && p.wait_ns <= kPollBelowNs;
+    const auto kernel = kind == kWarp   ? warp_attn_kernel<T, D>
+                        : kind == kKeys ? (poll ? tile_attn_kernel<T, D, true, true> : tile_attn_kernel<T, D, true, false>)
+                                        : (poll ? tile_attn_kernel<T, D, false, true> : tile_attn_kernel<T, D, false, false>);
     const int smem = kind == kWarp   ? warp_smem_bytes<D>()
                      : kind == kKeys ? TileShape<D, true>::kSmemBytes
                                      : TileShape<D, false>::kSmemBytes;
-    static std::atomic<uint64_t> done[3];
-    if (!allow_smem(kernel, smem, done[kind])) return RL_ERR_CUDA;
+    static std::atomic<uint64_t> done[5];
+    if (!allow_smem(kernel, smem, done[poll ? kind + 2 : kind])) return RL_ERR_CUDA;
     ++*launches;
     return launch_after(kernel, dim3(static_cast<unsigned>(items)), kind == kWarp ? kWarpThreads : kTileThreads, smem, follows, stream, tmK, tmV, p);
 }

@@ -94,7 +94,34 @@ RL_DEVINL bool elect_one() {
 RL_DEVINL uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
 RL_DEVINL void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-template <typename T, int D, bool kKeys2>
+// Bounded wait.  A sleeping try of the hardware outlasts a limit of some microseconds: such limits are kept by
+// polling, in kernels of their own, since the polls beside the tries cost the others 2.5 to 5 % (94 us and 98.5 for
+// the ragged extension below).
+constexpr uint64_t kPollBelowNs = 10000;
+template <bool kPoll>
+RL_DEVINL bool wait_within(uint64_t* bar, uint32_t parity, const AttnArgs& p) {
+    if constexpr (kPoll) {
+        const long long t0 = clock64(), cycles = static_cast<long long>(2 * p.wait_ns);     // at 2.07 GHz at most
+        while (true) {
+            uint32_t ok;
+            asm volatile(
+                "{\n\t.reg .pred p;\n\t"
+                "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+                "selp.u32 %0, 1, 0, p;\n\t}"
+                : "=r"(ok)
+                : "r"(smem_addr(bar)), "r"(parity)
+                : "memory");
+            if (ok) return true;
+            if (clock64() - t0 > cycles) {
+                set_status(p.status, RL_STATUS_TIMEOUT);
+                return false;
+            }
+        }
+    }
+    return mbar_wait(bar, parity, p.status, p.wait_ns);
+}
+
+template <typename T, int D, bool kKeys2, bool kPoll>
 __global__ void __launch_bounds__(kTileThreads, 1)
     tile_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const AttnArgs p) {
     using Shape = TileShape<D, kKeys2>;
@@ -176,6 +203,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = uniform(*tmem_slot);
+    int issued_units = 0;                                             // warp 0: units of the ring filled so far
 
     if (warp == 0) {
         // ---------------- copies ----------------
@@ -185,7 +213,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const int past = static_cast<int>(a.n_pages * a.Hkv * a.page_size);     // a row past the cache: zeros
         int unit = 0;
         uint32_t phase = 0;
-        int issued = 0;
         bool ok = true;
         auto load = [&](const CUtensorMap* map, int tile) {
             const bool in_a = tile < na;
@@ -193,7 +220,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             int row = past;
             if (lane < per && key < (in_a ? pre.k1 : it.k1))
                 row = (page_of(p, in_a ? pre.table : it.table, key, shift, bits) * a.Hkv + it.h) * a.page_size + (key & (a.page_size - 1));
-            ok = mbar_wait(empty + unit, phase ^ 1u, p.status, p.wait_ns) && !*abort_flag;
+            ok = wait_within<kPoll>(empty + unit, phase ^ 1u, p) && !*abort_flag;
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) {
                 *abort_flag = 1;
@@ -205,7 +232,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
                 for (int x = 0; x < D / 64; ++x)
                     tma_load_2d(map, full + unit, smem + unit * kUnit + x * kTileKeys * 128 + lane * box * 128, x * 64, row);
-            ++issued;
+            ++issued_units;
             if (++unit == kUnits) {
                 unit = 0;
                 phase ^= 1u;
@@ -224,9 +251,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             }
         }
         set_status(p.status, bits);
-        __syncwarp();
-        if (!ok && lane == 0)       // what was issued lands before the block can end
-            for (int s = max(0, issued - kUnits); s < issued; ++s) mbar_wait(full + s % kUnits, (s / kUnits) & 1, p.status);
     } else if (warp == 1) {
         if (n > 0) {
             // ---------------- products ----------------
@@ -234,10 +258,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             int unit = 0;
             uint32_t phase = 0;
             bool issued = false;
-            bool ok = mbar_wait(q_full, 0, p.status, p.wait_ns) && !*abort_flag;
+            bool ok = wait_within<kPoll>(q_full, 0, p) && !*abort_flag;
             ok = __all_sync(0xffffffffu, ok);
             auto wait_unit = [&]() {
-                ok = ok && mbar_wait(full + unit, phase, p.status, p.wait_ns) && !*abort_flag;
+                ok = ok && wait_within<kPoll>(full + unit, phase, p) && !*abort_flag;
                 ok = __all_sync(0xffffffffu, ok);
                 tc_fence_after();
             };
@@ -281,7 +305,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     for (int x = 0; x < kTileKeys / 32; ++x) umma_ts(o, w + x * 8, v + x * (2048 >> 4), kIdescO, x != 0 ? 1u : more);
                 }
                 __syncwarp();
-                ok = ok && mbar_wait(p_ready + t, i & 1, p.status, p.wait_ns) && !*abort_flag;
+                ok = ok && wait_within<kPoll>(p_ready + t, i & 1, p) && !*abort_flag;
                 ok = __all_sync(0xffffffffu, ok);
                 tc_fence_after();
                 if (ok && elect_one()) {
@@ -291,7 +315,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 __syncwarp();
             };
             auto wait_p = [&](int t, int i) {
-                ok = ok && mbar_wait(p_half + t, i & 1, p.status, p.wait_ns) && !*abort_flag;
+                ok = ok && wait_within<kPoll>(p_half + t, i & 1, p) && !*abort_flag;
                 ok = __all_sync(0xffffffffu, ok);
                 tc_fence_after();
             };
@@ -380,7 +404,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         int steps = 0;
         if (active)
             for (int i = kKeys2 ? t : 0; i < n; i += kKeys2 ? 2 : 1, ++steps) {
-                ok = mbar_wait(s_full + t, steps & 1, p.status, p.wait_ns) && !*abort_flag;
+                ok = wait_within<kPoll>(s_full + t, steps & 1, p) && !*abort_flag;
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tc_fence_after();
@@ -419,7 +443,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 if ((kKeys2 || t == 0) && last < key0 + kTileKeys) {
                     // the last values' page may hold anything past the last key
                     const int u = !kKeys2 || i == n - 1 ? (n == 1 ? 1 : kKeys2 ? 2 * n - 1 : 2 * i + 1) : 2 * i + 2;  // place in the ring's order
-                    ok = mbar_wait(full + u % kUnits, (u / kUnits) & 1, p.status, p.wait_ns) && !*abort_flag;
+                    ok = wait_within<kPoll>(full + u % kUnits, (u / kUnits) & 1, p) && !*abort_flag;
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
                     uint8_t* v = smem + (u % kUnits) * kUnit;
@@ -470,7 +494,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
             }
         if (n > 0 && ok) {                  // with all products done the ring and the queries are free
-            ok = mbar_wait(o_full, 0, p.status, p.wait_ns) && (!two || mbar_wait(o_full + 1, 0, p.status, p.wait_ns)) && !*abort_flag;
+            ok = wait_within<kPoll>(o_full, 0, p) && (!two || wait_within<kPoll>(o_full + 1, 0, p)) && !*abort_flag;
             ok = __all_sync(0xffffffffu, ok);
             tc_fence_after();
         }
@@ -561,6 +585,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     }
     tc_fence_before();
     __syncthreads();
+    // Whichever role gave up, copies may be under way still (the first kUnits wait for nothing): they land
+    // before the block ends and its memory is another's.
+    if (warp == 0 && lane == 0 && *abort_flag)
+        for (int s = max(0, issued_units - kUnits); s < issued_units; ++s) mbar_wait(full + s % kUnits, (s / kUnits) & 1, p.status);
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);

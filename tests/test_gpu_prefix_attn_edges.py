@@ -5,7 +5,7 @@ The bars are those of test_gpu_prefix_attn.py.
 import pytest
 import torch
 
-import lm_head_gb300 as rh  # noqa: F401
+import lm_head_gb300 as rh
 from test_gpu_prefix_attn import BF, HF, Case
 
 pytestmark = pytest.mark.gpu
@@ -96,3 +96,22 @@ def test_infinite_scores(kind):
     eps = torch.finfo(c.q.dtype).eps
     bar = eps / 2 * (out.abs() + vmax[..., None]) + 2.0 ** -16 * vmax[..., None]
     assert bool(((got - out).abs() <= bar)[~bad].all())
+
+
+@pytest.mark.parametrize("kind", ["keys", "rows"])
+@pytest.mark.parametrize("groups", [[], [3, 5]])
+@pytest.mark.parametrize("D,dtype", [(64, HF), (128, BF)])
+def test_a_wait_that_runs_out_ends_the_tensor_core_kernels(kind, groups, D, dtype):
+    """With a limit of 1 us waits run out for certain (a step of these kernels takes longer): the call
+    ends with TIMEOUT and no other bit, and the next one, with the usual limit, is right."""
+    n = 32 if kind == "keys" else 100
+    c = Case(groups, [700] * len(groups), [n] * 8, [5000 - 300 * i for i in range(8)], 8, 2, D, 16, dtype, 10)
+    want = c.run()
+    rh.rl_set_option(rh.RL_OPT_WAIT_LIMIT_US, 1)
+    try:
+        bits = [c.run().status_bits() for _ in range(3)]
+    finally:
+        rh.rl_set_option(rh.RL_OPT_WAIT_LIMIT_US, 1_000_000)
+    assert bits == [0x200] * 3
+    again = c.run()
+    assert again.status_bits() == 0 and torch.equal(again.out, want.out) and torch.equal(again.lse, want.lse)
