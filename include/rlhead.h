@@ -580,7 +580,7 @@ typedef struct rl_prefix_attn_args {
     const int32_t* prefix_lens;     /* device [G] */
     const int32_t* prefix_table;    /* device [G, prefix_width] */
     int64_t prefix_width;
-    int64_t max_q, max_kv, max_prefix;   /* host bounds on q_len, kv_lens, prefix_lens */
+    int64_t max_q, max_kv, max_prefix;   /* host bounds on q_len, kv_lens, prefix_lens (0: no group has one) */
     int32_t Hq, Hkv, D, page_size, dtype;   /* D 64 or 128; page_size 16, 32, 64, 128; bf16 / fp16 */
     float scale;                    /* >= 0, below 2e38; 0: all weights of a row alike */
     void* out;                      /* device [T, Hq, D] dense */

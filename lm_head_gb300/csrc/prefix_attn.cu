@@ -589,6 +589,13 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttnArgs p) {
     if (lane == 0 && a.lse) a.lse[row] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * kLn2;
 }
 
+// A bound of 0 on the prefixes' lengths takes their parts out of the call: a length that says otherwise is an
+// error.  One block, in such calls alone (the check in the other kernels cost 1 % of a ragged extension).
+__global__ void __launch_bounds__(kJoinThreads) no_prefix_kernel(const AttnArgs p) {
+    for (long long g = threadIdx.x; g < p.a.G; g += kJoinThreads)
+        if (p.a.prefix_lens[g] != 0) set_status(p.status, RL_STATUS_LENGTHS);
+}
+
 // ---- host ------------------------------------------------------------------------------
 // Which kernel does the parts with so many query rows: mma.sync tiles of 16 (kWarp), one tensor-core
 // tile of 128 rows that takes two key tiles at a time (kKeys: bound by reading the keys), or two
@@ -697,6 +704,8 @@ static int attn_run(const AttnArgs& p, AttnKind kp, AttnKind ko, cudaStream_t st
     const rl_prefix_attn_args& a = p.a;
     ProfScope prof(RL_PROF_OTHER, stream);
     int launches = 0, rc;
+    const bool no_prefix = a.G > 0 && a.max_prefix == 0;
+    if (no_prefix) no_prefix_kernel<<<1, kJoinThreads, 0, stream>>>(p);
     if (p.sp > 0 && kp == ko) {
         rc = launch_parts<T, D>(p, kp, true, true, false, stream, &launches);
     } else {
@@ -710,7 +719,7 @@ static int attn_run(const AttnArgs& p, AttnKind kp, AttnKind ko, cudaStream_t st
         if (rc != RL_OK) return rc;
         ++launches;
     }
-    count_launch(launches);
+    count_launch(launches + (no_prefix ? 1 : 0));
     return cudaPeekAtLastError() == cudaSuccess ? RL_OK : RL_ERR_CUDA;
 }
 

@@ -200,11 +200,12 @@ class AttnOut:
 
 
 def rl_prefix_attn(q, k_cache, v_cache, cu_q, kv_lens, block_table, *, max_q: int, max_kv: int, group_offsets=None,
-                   prefix_lens=None, prefix_table=None, max_prefix: int = 0, scale: Optional[float] = None,
+                   prefix_lens=None, prefix_table=None, max_prefix: Optional[int] = None, scale: Optional[float] = None,
                    out: Optional[AttnOut] = None, ws=None, status=None, stream=None) -> AttnOut:
     """Attention of a step's queries q [T, Hq, D] (any token and head strides) over their
     group's shared prefix and each request's own keys, causal within the step.  max_q, max_kv
-    and max_prefix bound the device lengths.  scale: 1 / sqrt(D) by default."""
+    and max_prefix bound the device lengths (max_prefix: what prefix_table has room for, by
+    default).  scale: 1 / sqrt(D) by default."""
     kc, vc, dt = _cache(k_cache, v_cache)
     n_pages, Hkv, page, D = k_cache.shape
     if not q.is_cuda or q.dim() != 3 or q.dtype != k_cache.dtype or q.shape[2] != D or q.stride(2) != 1:
@@ -218,6 +219,8 @@ def rl_prefix_attn(q, k_cache, v_cache, cu_q, kv_lens, block_table, *, max_q: in
         if prefix_table is None or prefix_table.dim() != 2 or prefix_table.shape[0] != G:
             raise _err(f"prefix_table: expected [{G}, pages]")
         WP = prefix_table.shape[1]
+    if max_prefix is None:
+        max_prefix = WP * page
     head = (q.data_ptr(), q.stride(0), q.stride(1), kc, vc, n_pages, T, R, G, _dev("cu_q", cu_q, i32, R + 1),
             _dev("kv_lens", kv_lens, i32, R), _dev("block_table", block_table, i32), W,
             _dev("group_offsets", group_offsets, i32, None, True), _dev("prefix_lens", prefix_lens, i32, G, G == 0),

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import lm_head_gb300 as rh
-from test_gpu_prefix_attn import BF, HF, Case
+from test_gpu_prefix_attn import BF, HF, LENGTHS, Case
 
 pytestmark = pytest.mark.gpu
 
@@ -115,3 +115,19 @@ def test_a_wait_that_runs_out_ends_the_tensor_core_kernels(kind, groups, D, dtyp
     assert bits == [0x200] * 3
     again = c.run()
     assert again.status_bits() == 0 and torch.equal(again.out, want.out) and torch.equal(again.lse, want.lse)
+
+
+def test_a_prefix_without_its_bound_is_not_lost():
+    """max_prefix left out is the table's width; a bound of 0 with a prompt is an error, not a step
+    without its prompt."""
+    for kind in ("warp", "keys", "rows"):
+        c = make(kind)
+        c.check()
+        a = rh.rl_prefix_attn(c.q, c.kc, c.vc, c.cu, c.kvt, c.table, max_q=c.bounds["max_q"], max_kv=c.bounds["max_kv"],
+                              group_offsets=c.go, prefix_lens=c.pl, prefix_table=c.ptable, scale=c.scale)
+        c.check(a)
+        assert c.run(max_prefix=0).status_bits() == LENGTHS
+        c.pl = torch.zeros_like(c.pl)
+        assert c.run(max_prefix=0).status_bits() == 0
+        c.pl = torch.full_like(c.pl, -3)
+        assert c.run(max_prefix=0).status_bits() == LENGTHS
