@@ -500,7 +500,8 @@ int rl_rollout_metrics_named(const rl_rc_metrics* metrics, const rl_rc_params* p
  * of the group's own table (make them by a plan whose requests are the groups); a request's
  * table holds the pages of its own tokens only, so that a prompt may end inside a page.
  * Requests of one group are consecutive: group g has requests [group_offsets[g],
- * group_offsets[g+1]), and a request outside every group has no prefix.
+ * group_offsets[g+1]), and a request outside every group has no prefix; offsets that decrease or
+ * leave [0, R] set RL_STATUS_LENGTHS.
  * Lengths live on the device, so that a step can be captured in a CUDA graph and replayed
  * as they change; the host gives upper bounds.  Lengths and pages are checked on the device:
  * bad ones set RL_STATUS_* bits and are never followed out of the caller's buffers. */

@@ -310,6 +310,9 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanArgs 
             a.slot_map[t] = -1;
             if (a.positions) a.positions[t] = -1;
         }
+    if (grouped && blockIdx.x == 0 && tiles > 0)                     // (the scan's barriers have been passed)
+        for (int g = threadIdx.x; g < a.G; g += kPlanThreads)
+            if (go[g] < 0 || go[g + 1] < go[g] || go[g + 1] > a.R) bits |= RL_STATUS_LENGTHS;
     set_status(p.status, bits);
 }
 

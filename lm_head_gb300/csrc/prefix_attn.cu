@@ -84,6 +84,11 @@ RL_DEVINL void prefix_keys(const AttnArgs& p, long long g, int k0, int chunk, It
     it.k0 = k0;
     it.k1 = static_cast<int>(min(static_cast<long long>(k0) + chunk, static_cast<long long>(len)));
 }
+// Whether group g's requests are not a stretch of the call's, or not after those of the group before.
+RL_DEVINL bool bad_group(const rl_prefix_attn_args& a, long long g) {
+    const int ra = a.group_offsets[g], rb = a.group_offsets[g + 1];
+    return ra < 0 || rb < ra || rb > a.R;
+}
 // The whole prefix of the group of `it`'s request (none: no keys).  All lanes of a warp together.
 RL_DEVINL void find_prefix(const AttnArgs& p, const Item& it, Item& pre, int& bits) {
     const rl_prefix_attn_args& a = p.a;
@@ -91,6 +96,7 @@ RL_DEVINL void find_prefix(const AttnArgs& p, const Item& it, Item& pre, int& bi
     pre.k0 = pre.k1 = 0;
     for (long long g0 = 0; g0 < a.G; g0 += 32) {
         const long long g = g0 + lane;
+        if (g < a.G && bad_group(a, g)) bits |= RL_STATUS_LENGTHS;
         const bool mine = g < a.G && a.group_offsets[g] <= it.r && it.r < a.group_offsets[g + 1];
         const unsigned hit = __ballot_sync(0xffffffffu, mine);
         if (hit) {
@@ -518,6 +524,9 @@ template <typename T, int D>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttnArgs p) {
     const rl_prefix_attn_args& a = p.a;
     const int lane = threadIdx.x & 31;
+    if (blockIdx.x == 0 && p.sp > 0)
+        for (long long g = threadIdx.x; g < a.G; g += kJoinThreads)
+            if (bad_group(a, g)) set_status(p.status, RL_STATUS_LENGTHS);
     wait_for_previous();
     const long long row = static_cast<long long>(blockIdx.x) * (kJoinThreads / 32) + (threadIdx.x >> 5);
     const long long rows = a.T * a.Hq;

@@ -131,3 +131,27 @@ def test_a_prefix_without_its_bound_is_not_lost():
         assert c.run(max_prefix=0).status_bits() == 0
         c.pl = torch.full_like(c.pl, -3)
         assert c.run(max_prefix=0).status_bits() == LENGTHS
+
+
+# all of a step's rows over prefix and own keys in one block: many tokens a request, no join
+BOTH = dict(groups=[2, 0, 3, 1], prefixes=[300, 50, 129, 1], q_lens=[33, 257, 1, 0, 300, 128, 400, 129],
+            kv_lens=[33, 266, 6, 0, 427, 192, 600, 130], stray=1)
+
+
+@pytest.mark.parametrize("kind", ["warp", "keys", "rows", "both"])
+def test_group_offsets_that_do_not_add_up_set_status(kind):
+    if kind == "both":
+        c = Case(Hq=16, Hkv=2, D=64, page=16, dtype=BF, seed=2, **BOTH)
+        assert c.run().ws.numel() == 1          # no parts to join
+    else:
+        c = make(kind)
+    R, G = len(c.q_lens), len(c.groups)
+    for bad in (R + 1, -1):
+        go = c.go.clone()
+        go[-1 if bad > 0 else 0] = bad
+        good, c.go = c.go, go
+        assert c.run().status_bits() == LENGTHS
+        c.go = good
+    if G > 1:
+        c.go = c.go.flip(0).contiguous()
+        assert c.run().status_bits() == LENGTHS
