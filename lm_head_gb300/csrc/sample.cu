@@ -18,8 +18,9 @@
 //                    128-wide maxima shows that few can matter, else after a histogram that
 //                    brackets the border; then the weight of each part's kept tokens, and each
 //                    draw by a search over the parts and a scan of one.  Whole rows (no cut)
-//                    take the sums of 1.  Sums are integers (units of 2^-50 of the largest
-//                    weight in a part, 2^-44 over parts): their order does not matter.
+//                    take the sums of 1.  Sums are integers in a unit of the row's, the
+//                    finest 2^-p of the largest weight (p from 42 to 54) in which its total is sure
+//                    to fit: their order does not matter.
 //  3. emit_kernel    the support rows, one warp a part.
 //
 // Measured (one GB300, rows of 151,936 logits, device time):
@@ -214,6 +215,7 @@ RL_DEVINL void weight_pair(float x, float x_lo, FF c, float magic, const float2*
     hi = __uint_as_float(__float_as_uint(q.x) + (tb << 12));
     v = hi * fmaf(r, fmaf(r, 0.24022650695910072f, 0.69314718055994531f), q.y);
 }
+RL_DEVINL float power_of_2(int k) { return __int_as_float((127 + k) << 23); }
 // Sum of up to four weights of at most 1 in a lane, hi + v each: in a float that starts at 24, so
 // that it only takes whole steps of 2^-19, and the rest apart.  Both become integers through
 // their bits; a warp's total is (top << 31) + (low << 11) in units of 2^-50, rounded at 2^-39 a lane.
@@ -233,9 +235,9 @@ struct LaneSum {
         return w > 0 ? static_cast<unsigned long long>(w) : 0ull;
     }
 };
-// The weight of z relative to M in units of 2^-50; `zlow` = M - 64 / c, at least
+// The weight of z relative to M in units of 2^-k; `zlow` = M - 64 / c, at least
 // -FLT_MAX: below it the weight is 0 (M itself where the difference is lost).
-RL_DEVINL unsigned long long weight_fixed(float z, float M, FF c, float zlow, const float2* tab) {
+RL_DEVINL unsigned long long weight_fixed(float z, float M, FF c, float zlow, int k, const float2* tab) {
     if (!(z >= zlow)) return 0ull;
     float hi, v;
     const FF d = two_sum(z, -M);
@@ -243,10 +245,10 @@ RL_DEVINL unsigned long long weight_fixed(float z, float M, FF c, float zlow, co
     const float wh = __fadd_rn(hi, v), wl = __fsub_rn(v, __fsub_rn(wh, hi));
     if (!(wh < 2.f)) return 0ull;             // differences past the range of floats
     const uint32_t b = __float_as_uint(wh);
-    const int sh = static_cast<int>(b >> 23) - 127 - 23 + 50;          // the 24-bit significand times 2^sh
+    const int sh = static_cast<int>(b >> 23) - 127 - 23 + k;           // the 24-bit significand times 2^sh
     const unsigned long long m = (b & 0x7fffffu) | 0x800000u;
     const unsigned long long w = sh >= 0 ? m << sh : (sh > -25 ? (m + (1ull << (-sh - 1))) >> -sh : 0ull);
-    return w + static_cast<long long>(__float2int_rn(wl * 1125899906842624.f));
+    return w + static_cast<long long>(__float2int_rn(wl * power_of_2(k)));       // below 2^(k - 24)
 }
 // floor(f x) for 0 <= f < 1
 RL_DEVINL unsigned long long fraction_of(float f, unsigned long long x) {
@@ -467,7 +469,7 @@ template <typename T, bool kVec>
 struct Row {
     const SampleArgs& g;
     SelShared& s;
-    unsigned long long* cs;      // [ns] kept weight of each part (units of 2^-50)
+    unsigned long long* cs;      // [ns] kept weight of each part (units of 2^-prec)
     int* cnt;                    // [ns] kept tokens
     int* in;                     // [ns] tokens in the bracket
     uint16_t* subs;              // the parts that a pass reads
@@ -476,10 +478,13 @@ struct Row {
     int V, tid, lane, warp;
     float M, zlow;               // zlow: weights are 0 below
     FF c;
+    int prec;                    // sums are in units of 2^-prec of M's weight
     uint32_t bkey;               // the set that selection starts from: key > bkey, or equal and
     int btie;                    // index <= btie
 
-    RL_DEVINL unsigned long long weight(float z) const { return weight_fixed(z, M, c, zlow, s.tab); }
+    RL_DEVINL unsigned long long weight(float z) const { return weight_fixed(z, M, c, zlow, prec, s.tab); }
+    // What LaneSum gives, in the row's unit.
+    RL_DEVINL unsigned long long in_unit(unsigned long long w50) const { return prec >= 50 ? w50 << (prec - 50) : w50 >> (50 - prec); }
     RL_DEVINL bool in_base(uint32_t key, int i) const { return key > bkey || (key == bkey && i <= btie); }
 
     // Lists the parts with a logit >= lo, and clears the sums; returns how many there are.
@@ -583,7 +588,7 @@ struct Row {
                 const uint32_t wt = acc.warp_top();
                 const int wl = acc.warp_low();
                 if (lane == 0) {
-                    cs[part] = LaneSum::total(wt, wl);
+                    cs[part] = in_unit(LaneSum::total(wt, wl));
                     cnt[part] = n;
                 }
             }
@@ -603,10 +608,10 @@ struct Row {
         });
         __syncthreads();
     }
-    // Totals over the parts: weight in units of 2^-44, numbers.
+    // Totals over the parts: weight, numbers.
     RL_DEVINL unsigned long long sum_weight() {
         unsigned long long v = 0;
-        for (int i = tid; i < g.ns; i += kSelThreads) v += cs[i] >> 6;
+        for (int i = tid; i < g.ns; i += kSelThreads) v += cs[i];
         return block_sum(v, s.red);
     }
     RL_DEVINL long long sum_int(const int* x) {
@@ -639,11 +644,9 @@ struct Row {
         for (int i = tid; i < n; i += kSelThreads) s.wt[i] = weight(z_of(static_cast<uint32_t>(s.comp[i] >> 32)));
         __syncthreads();
     }
-    // How many of the sorted list come before the sum (above + those before) reaches target
-    // (both in units of 2^-44).
+    // How many of the sorted list come before the sum (above + those before) reaches target.
     RL_DEVINL int keep_by_weight(int n, unsigned long long above, unsigned long long target) {
-        const unsigned long long rest = target > above ? target - above : 0ull;
-        const unsigned long long lim = rest >> 58 ? ~0ull : rest << 6;
+        const unsigned long long lim = target > above ? target - above : 0ull;
         constexpr int kPer = kListCap / kSelThreads;
         const int per = (n + kSelThreads - 1) / kSelThreads;
         unsigned long long t = 0;
@@ -707,7 +710,7 @@ struct Row {
     }
 
     // Cuts the base set (of logits >= lo) to its first `k` tokens (k > 0) or to the shortest prefix
-    // whose weight reaches `top_p` of `mass` (the base set's weight, units of 2^-44); cs / cnt then
+    // whose weight reaches `top_p` of `mass` (the base set's weight); cs / cnt then
     // hold the kept ones, bkey / btie the border.  True: the sorted list begins with the whole
     // kept set.
     RL_DEVINL bool cut(long long k, float top_p, unsigned long long mass, float lo, bool few) {
@@ -732,7 +735,7 @@ struct Row {
             list_parts(lo);
             for (int i = tid; i < kBins; i += kSelThreads) h32[i] = 0;
             __syncthreads();
-            const float q = 2147483648.f / (static_cast<float>(mass) * 0x1p-44f);
+            const float q = 2147483648.f / (static_cast<float>(mass) * power_of_2(-prec));
             const bool all_base = btie == INT_MAX && key_of(lo) >= bkey;
             each([&](const float(&z)[4], int i0, int) {
                 // a rounded weight: this only says where to look
@@ -764,7 +767,7 @@ struct Row {
                 }
                 unsigned long long t = 0;
                 const int n = static_cast<int>(s.n_list);
-                for (int i = tid; i < n; i += kSelThreads) t += weight(z_of(static_cast<uint32_t>(s.comp[i] >> 32))) >> 6;
+                for (int i = tid; i < n; i += kSelThreads) t += weight(z_of(static_cast<uint32_t>(s.comp[i] >> 32)));
                 if (above + block_sum(t, s.red) < target && b.b < kBins - 1) {
                     ++b.b;
                     continue;
@@ -793,7 +796,7 @@ struct Row {
                     if (level > 0 && (key >> (shift + bits)) != prefix) continue;
                     // descending order: bin 0 holds the largest digit
                     const uint32_t d = (1u << bits) - 1u - ((key >> shift) & ((1u << bits) - 1u));
-                    atomicAdd(&h64[d], by_count ? 1ull : weight(z[j]) >> 6);
+                    atomicAdd(&h64[d], by_count ? 1ull : weight(z[j]));
                 }
             });
             __syncthreads();
@@ -825,9 +828,9 @@ struct Row {
         }
         // more equal logits than the list holds (the bracket is one key): the lowest indices stay
         const uint32_t key = b.b;
-        const unsigned long long w = weight(z_of(key)), w44 = w >> 6;
+        const unsigned long long w = weight(z_of(key));
         const unsigned long long rest = target > above ? target - above : 0ull;
-        long long keep = by_count ? k - n_above : w44 == 0 ? n : static_cast<long long>(min((rest + w44 - 1) / w44, 1ull << 40));
+        long long keep = by_count ? k - n_above : w == 0 ? n : static_cast<long long>(min((rest + w - 1) / w, 1ull << 40));
         keep = min(max(keep, n_above == 0 ? 1ll : 0ll), n);
         if (tid == 0) {
             s.pick = -1;
@@ -872,7 +875,7 @@ struct Row {
         __syncthreads();
     }
 
-    // One draw by one warp; cs holds the inclusive sums of the parts' weights in units of 2^-44.
+    // One draw by one warp; cs holds the inclusive sums of the parts' weights.
     RL_DEVINL void draw(long long r, int d, unsigned long long total) {
         float u = g.a.u[r * g.a.K + d];
         if (!(u >= 0.f) || !(u < 1.f)) {
@@ -887,7 +890,7 @@ struct Row {
             else lo = mid + 1;
         }
         const unsigned long long before = lo > 0 ? cs[lo - 1] : 0ull;
-        const unsigned long long want = (target > before ? target - before : 0ull) << 6;
+        const unsigned long long want = target > before ? target - before : 0ull;
         float z[4];
         const int i0 = lo * kSub + lane * 4;
         load4<T, kVec>(row, i0, V, z);
@@ -976,7 +979,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SampleArgs
     int* cnt = reinterpret_cast<int*>(cs + g.ns);
     Row<T, kVec> w{g, s, cs, cnt, cnt + g.ns, reinterpret_cast<uint16_t*>(cnt + 2 * g.ns),
                    static_cast<const T*>(a.logits) + r * a.row_stride, g.submax + r * g.ns, V,
-                   tid, tid & 31, tid >> 5, 0.f, 0.f, {0.f, 0.f}, 0u, INT_MAX};
+                   tid, tid & 31, tid >> 5, 0.f, 0.f, {0.f, 0.f}, 0, 0u, INT_MAX};
     const Knobs q = load_knobs(a, r);
     fill_table(s.tab, tid, kSelThreads);
     wait_for_previous();
@@ -1046,13 +1049,18 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SampleArgs
                 s.unit = (static_cast<unsigned long long>(hi * 8388608.f) << 39) + static_cast<long long>(v * 0x1p62f);
             }
         }
-        __syncthreads();
+        // the unit of the row's sums: with S the sum of the parts' largest weights, from 1 to 8192, the
+        // total is at most 128 S, below 2^62 units of 2^-(54 - floor(log2 S))
+        float likely = 0.f;
+        for (int i = tid; i < g.ns; i += kSelThreads) likely += exp2_approx(fmaxf(w.submax[i] - M, -FLT_MAX) * w.c.hi);
+        likely = block_sum(likely, reinterpret_cast<float*>(s.red));
+        w.prec = 54 - min(max(static_cast<int>(__float_as_uint(likely) >> 23) - 127, 0), 13);
         const float zmin = s.fpick;
         w.bkey = key_of(zmin);
         w.btie = INT_MAX;
-        unsigned long long mass = 0;                    // units of 2^-44
+        unsigned long long mass = 0;
         if (q.total) {
-            // the parts' sums relative to M's weight, in units of 2^-50
+            // the parts' sums relative to M's weight
             const float pm = __fmul_rn(M, w.c.hi);
             const bool plain = fabsf(pm) < kWholeRef;
             const int ref = plain ? static_cast<int>(ceilf(pm)) : 0;
@@ -1063,20 +1071,21 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SampleArgs
                 const int rc = g.ref[r * g.nc + i / kSubs];
                 if (x) {
                     if (plain && rc != INT_MIN) {
-                        const int n = ref - rc;
-                        x = n < 64 ? __umul64hi(x << 2, unit) >> n : 0ull;
+                        const int n = ref - rc + 54 - w.prec;          // at most 2^57 in, times 2^4 units of 2^-54
+                        x = n < 64 ? __umul64hi(x << 6, unit) >> n : 0ull;
                     } else {                            // very large logits: the slow way
                         const double cd = 1.4426950408889634 / static_cast<double>(q.T);
                         float cm = -INFINITY;
                         for (int j = i / kSubs * kSubs; j < min(i / kSubs * kSubs + kSubs, g.ns); ++j) cm = fmaxf(cm, w.submax[j]);
                         const double d = rc == INT_MIN ? (static_cast<double>(cm) - M) * cd : rc - M * cd;
-                        x = static_cast<unsigned long long>(static_cast<double>(x) * exp2(d));
+                        x = static_cast<unsigned long long>(static_cast<double>(x) * exp2(d + (w.prec - 50)));
                     }
                 }
                 cs[i] = x;
-                v += x >> 6;
+                v += x;
             }
-            mass = block_sum(v, s.red);
+            if (q.cut) mass = block_sum(v, s.red);
+            else __syncthreads();
         }
         if (!q.cut) {
             mode = kRowWhole;
@@ -1117,7 +1126,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SampleArgs
                     w.close_list(n, keep);
                 } else {
                     // a logit whose weight is below (1 - p) mass / V cannot be needed
-                    const float rest = (1.f - fmaxf(q.p, 0.f)) * (static_cast<float>(mass) * 0x1p-44f) / static_cast<float>(V) * 0.999f;
+                    const float rest = (1.f - fmaxf(q.p, 0.f)) * (static_cast<float>(mass) * power_of_2(-w.prec)) / static_cast<float>(V) * 0.999f;
                     const float need = M + q.T * fminf(logf(fmaxf(rest, 7.9e-31f)), 0.f);
                     lo = fmaxf(lo, fminf(need - 0x1p-18f * (q.T + fabsf(M)), M));
                     w.cut(0, q.p, mass, lo, w.list_parts(lo) * 10 < g.ns * 9);
@@ -1130,7 +1139,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SampleArgs
         for (int j = 0; j < per; ++j) {
             const int i = tid * per + j;
             if (i < g.ns) {
-                t += cs[i] >> 6;
+                t += cs[i];
                 cs[i] = t;
                 if (mode == kRowCut) tn += static_cast<unsigned>(cnt[i]);
             }
@@ -1155,10 +1164,10 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SampleArgs
         __syncthreads();
         const unsigned long long total = cs[g.ns - 1];
         if (tid == 0) {
-            // total / 2^44 as a float pair
+            // the total as a float pair
             const float th = __ull2float_rz(total);
             const float tl = static_cast<float>(static_cast<long long>(total - static_cast<unsigned long long>(th)));
-            s.rec = RowRec{M, inv_of(q.T), ln_pair(fast_two_sum(th * 0x1p-44f, tl * 0x1p-44f)), w.bkey, w.btie, mode};
+            s.rec = RowRec{M, inv_of(q.T), ln_pair(fast_two_sum(th * power_of_2(-w.prec), tl * power_of_2(-w.prec))), w.bkey, w.btie, mode};
         }
         __syncthreads();
         for (int d = w.warp; d < a.K; d += kSelWarps) w.draw(r, d, total);
