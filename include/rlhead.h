@@ -599,8 +599,8 @@ int rl_prefix_attn(const rl_prefix_attn_args* args, void* ws, size_t ws_bytes, i
  *                whose sum of w reaches top_p times the candidates' sum; at least one token
  *   q(i)         w_i / sum_S w
  *   draw u       the first token i of S, in index order, with sum_{j in S, j <= i} w_j > u sum_S w
- * Sums that decide a token or a set member are carried to about 2^-36 of the largest weight, so that these
- * agree with exact arithmetic except where a random number falls that near to a border.
+ * Sums that decide a token or a set member are carried to about 2^-36 of their row's total, so that
+ * these agree with exact arithmetic except where a random number falls that near to a border.
  * T = 0 is greedy: S is the largest logit (the lowest index of equal ones).  top_k outside
  * [1, V), top_p >= 1 and min_p <= 0 leave their cut out; top_p <= 0 and min_p > 1 keep one
  * token and the likeliest tokens.  T < 0 or not finite (greedy is used), a NaN knob (its cut is

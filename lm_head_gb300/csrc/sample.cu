@@ -217,8 +217,10 @@ RL_DEVINL void weight_pair(float x, float x_lo, FF c, float magic, const float2*
 }
 RL_DEVINL float power_of_2(int k) { return __int_as_float((127 + k) << 23); }
 // Sum of up to four weights of at most 1 in a lane, hi + v each: in a float that starts at 24, so
-// that it only takes whole steps of 2^-19, and the rest apart.  Both become integers through
-// their bits; a warp's total is (top << 31) + (low << 11) in units of 2^-50, rounded at 2^-39 a lane.
+// that it only takes whole steps of 2^-19, and the rest apart (below 2^-17).  Both become integers;
+// a warp's total is (top << 31) + (low << 7) in units of 2^-50, a lane's part rounded to 2^-43.  The
+// weights are relative to the largest of their chunk or part, so that the roundings of a long flat tail, which
+// all go one way, are small beside the tail and not beside the row's largest weight alone.
 struct LaneSum {
     float top = 24.f, low = 0.f;
     RL_DEVINL void add(float hi, float v) {
@@ -227,11 +229,9 @@ struct LaneSum {
         top = n;
     }
     RL_DEVINL uint32_t warp_top() const { return __reduce_add_sync(0xffffffffu, __float_as_uint(top) - 0x41c00000u); }
-    RL_DEVINL int warp_low() const {
-        return __reduce_add_sync(0xffffffffu, static_cast<int>(__float_as_uint(__fadd_rn(low, 0x1.8p-16f)) - 0x37c00000u));
-    }
+    RL_DEVINL int warp_low() const { return __reduce_add_sync(0xffffffffu, __float2int_rn(low * 0x1p43f)); }
     static RL_DEVINL unsigned long long total(uint32_t a, int b) {
-        const long long w = (static_cast<long long>(a) << 31) + (static_cast<long long>(b) << 11);
+        const long long w = (static_cast<long long>(a) << 31) + (static_cast<long long>(b) << 7);
         return w > 0 ? static_cast<unsigned long long>(w) : 0ull;
     }
 };
@@ -483,8 +483,11 @@ struct Row {
     int btie;                    // index <= btie
 
     RL_DEVINL unsigned long long weight(float z) const { return weight_fixed(z, M, c, zlow, prec, s.tab); }
-    // What LaneSum gives, in the row's unit.
-    RL_DEVINL unsigned long long in_unit(unsigned long long w50) const { return prec >= 50 ? w50 << (prec - 50) : w50 >> (50 - prec); }
+    // What LaneSum gives for weights relative to 2^ref of M's, in the row's unit.
+    RL_DEVINL unsigned long long in_unit(unsigned long long w50, int ref) const {
+        const int sh = prec - 50 + ref;
+        return sh >= 0 ? w50 << sh : sh > -64 ? (w50 + (1ull << (-sh - 1))) >> -sh : 0ull;
+    }
     RL_DEVINL bool in_base(uint32_t key, int i) const { return key > bkey || (key == bkey && i <= btie); }
 
     // Lists the parts with a logit >= lo, and clears the sums; returns how many there are.
@@ -547,6 +550,7 @@ struct Row {
         const float fb = static_cast<float>(k.b);
         const bool all_base = btie == INT_MAX && key_of(lo) >= bkey;
         each([&](const float(&z)[4], int i0, int part) {
+            const float ref = ceilf((submax[part] - M) * c.hi);
             bool up[4], mid[4], any_up = false, any_mid = false;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -581,14 +585,14 @@ struct Row {
                     const float x = dense[i];
                     const FF d = two_sum(fmaxf(x, zlow), -M);
                     float hi, v;
-                    weight_pair(d.hi, d.lo, c, 6144.f, s.tab, hi, v);
+                    weight_pair(d.hi, d.lo, c, 6144.f - ref, s.tab, hi, v);
                     if (x >= zlow) acc.add(hi, v);
                 }
                 __syncwarp();
                 const uint32_t wt = acc.warp_top();
                 const int wl = acc.warp_low();
                 if (lane == 0) {
-                    cs[part] = in_unit(LaneSum::total(wt, wl));
+                    cs[part] = LaneSum::total(wt, wl);
                     cnt[part] = n;
                 }
             }
@@ -606,6 +610,10 @@ struct Row {
                 if (lane == 0) in[part] = inside;
             }
         });
+        __syncthreads();
+        // the sums into the row's unit (a part a thread: 330 us for 256 flat nuclei, and 336 within the pass)
+        for (int i = tid; i < g.ns; i += kSelThreads)
+            if (cs[i]) cs[i] = in_unit(cs[i], static_cast<int>(ceilf((submax[i] - M) * c.hi)));
         __syncthreads();
     }
     // Totals over the parts: weight, numbers.
@@ -826,25 +834,42 @@ struct Row {
             close_list(static_cast<int>(n), static_cast<int>(keep));
             return;
         }
-        // more equal logits than the list holds (the bracket is one key): the lowest indices stay
+        // more equal logits than the list holds (the bracket is one key): the lowest indices stay.  Their
+        // number by the weight in 64 bits: a rounding of it to the row's unit would count once a token.
         const uint32_t key = b.b;
-        const unsigned long long w = weight(z_of(key));
-        const unsigned long long rest = target > above ? target - above : 0ull;
-        long long keep = by_count ? k - n_above : w == 0 ? n : static_cast<long long>(min((rest + w - 1) / w, 1ull << 40));
+        const float zk = z_of(key);
+        double w = 0.0;
+        if (zk >= zlow) {
+            float hi, v;
+            const FF d = two_sum(zk, -M);
+            weight_pair(d.hi, d.lo, c, 6144.f, s.tab, hi, v);
+            if (hi < 2.f) w = static_cast<double>(hi) + static_cast<double>(v);      // (differences past the range of floats)
+        }
+        long long keep = by_count ? k - n_above : n;
+        if (!by_count && w > 0.0) {
+            const double few = static_cast<double>(target > above ? target - above : 0ull) * static_cast<double>(power_of_2(-prec)) / w;
+            if (few < static_cast<double>(n)) keep = static_cast<long long>(ceil(few));
+        }
         keep = min(max(keep, n_above == 0 ? 1ll : 0ll), n);
-        if (tid == 0) {
-            s.pick = -1;
-            long long left = keep;
-            for (int i = 0; i < g.ns; ++i) {
-                const int t = static_cast<int>(min(left, static_cast<long long>(in[i])));
-                cs[i] += w * static_cast<unsigned long long>(t);
+        if (tid == 0) s.pick = -1;
+        const int per = (g.ns + kSelThreads - 1) / kSelThreads;
+        unsigned long long mine = 0;
+        for (int j = 0; j < per; ++j) {
+            const int i = tid * per + j;
+            if (i < g.ns) mine += static_cast<unsigned>(in[i]);
+        }
+        long long before = static_cast<long long>(block_scan(mine, s.red));
+        for (int j = 0; j < per; ++j) {
+            const int i = tid * per + j;
+            if (i < g.ns && in[i] > 0 && before < keep) {
+                const int t = static_cast<int>(min(keep - before, static_cast<long long>(in[i])));
+                cs[i] += __double2ull_rn(w * t * static_cast<double>(power_of_2(prec)));
                 cnt[i] += t;
-                if (t > 0 && left <= in[i]) {        // the last kept one is the left-th of this part
+                if (before + in[i] >= keep) {        // the last kept one is the t-th of this part
                     s.pick = i;
-                    s.bin_lo = static_cast<unsigned>(left);
-                    break;
+                    s.bin_lo = static_cast<unsigned>(t);
                 }
-                left -= t;
+                before += in[i];
             }
         }
         __syncthreads();
