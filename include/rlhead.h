@@ -629,8 +629,7 @@ typedef struct rl_sample_args {
     int64_t capacity;
     uint8_t* replayed;              /* device [N]; NULL to skip */
 } rl_sample_args;
-/* Zero the workspace once before its first use (16-byte aligned): every call leaves its counter
- * at zero again.  Calls that overlap on the GPU must not share a workspace. */
+/* 16-byte aligned, with any contents.  Calls that overlap on the GPU must not share a workspace. */
 size_t rl_sample_workspace_bytes(int64_t N, int64_t V, int32_t K);
 int rl_sample(const rl_sample_args* args, void* ws, size_t ws_bytes, int32_t* dev_status, void* stream);
 

@@ -102,7 +102,7 @@ struct SampleArgs {
     int* cpre;                     // [N, ns] kept tokens of the parts before
     int* count;                    // [N] entries of the support row
     RowRec* rec;                   // [N]
-    unsigned* done;                // rows finished (back to zero at the end of a call)
+    unsigned* done;                // rows finished (the call's first kernel clears it)
 };
 
 struct Knobs {
@@ -282,6 +282,7 @@ template <typename T, bool kVec>
 __global__ void __launch_bounds__(kStatThreads, 2) stats_kernel(const SampleArgs g) {
     __shared__ float2 tab[2048];
     const rl_sample_args& a = g.a;
+    if (blockIdx.x == 0 && threadIdx.x == 0) *g.done = 0;
     fill_table(tab, threadIdx.x, kStatThreads);
     __syncthreads();
     const int lane = threadIdx.x & 31;
@@ -1233,7 +1234,6 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SampleArgs
             if (tid == 0) {
                 a.offsets[a.N] = base;
                 if (base > a.capacity) bits |= RL_STATUS_CAPACITY;
-                *g.done = 0;
             }
         }
     }

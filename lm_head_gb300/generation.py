@@ -283,8 +283,8 @@ def rl_sample(logits, u, *, temperature=None, top_k=None, top_p=None, min_p=None
     if out is None:
         dev = logits.device
         e = lambda n, dt: torch.empty(n, dtype=dt, device=dev)  # noqa: E731
-        if ws is None:   # zeroed once: every call leaves its counter at zero
-            ws = torch.zeros(max(rl_sample_workspace_bytes(N, V, K), 1), dtype=torch.uint8, device=dev)
+        if ws is None:
+            ws = torch.empty(max(rl_sample_workspace_bytes(N, V, K), 1), dtype=torch.uint8, device=dev)
         out = SampleOut(e((N, K), i32), e((N, K), f32), e(N + 1, torch.int64) if capacity else None,
                         torch.zeros(capacity, dtype=i32, device=dev) if capacity else None,
                         torch.zeros(capacity, dtype=f32, device=dev) if capacity else None, e(N, torch.uint8), ws,
