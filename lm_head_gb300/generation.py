@@ -4,10 +4,12 @@ writes, attention over a shared prefix, and sampling with the head's support row
 Argument marshalling only, as in the package's other calls.  Every function takes its output
 buffers through `out` / `status`, so that a decode loop allocates nothing after its first step
 (and can be captured in a CUDA graph); without them it makes them.  The status word is
-never cleared by the library: read it with status_bits() and zero it.
+never cleared by the library: read it with status_bits() and zero it.  With stream=, what a call
+makes is made on that stream, as under torch.cuda.stream(stream).
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import dataclasses
 import struct
@@ -116,6 +118,12 @@ def _dev(name, t, dtype, n=None, optional=False):
     return t.data_ptr()
 
 
+def _on(stream):
+    """What a call makes is made on the stream that the call runs on: a buffer zeroed on another one
+    could be zeroed beside or after the call, and its memory be another's before the call is done."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
 def _status(status, device):
     return torch.zeros(1, dtype=torch.int32, device=device) if status is None else status
 
@@ -146,9 +154,11 @@ def rl_page_plan(q_lens, ctx_lens, block_table, free_pages, *, page_size: int, n
         dev = block_table.device
         if not block_table.is_cuda:
             raise _err("block_table: librlhead takes device tensors; got a CPU tensor")
-        out = PagePlan(torch.empty(R + 1, dtype=i32, device=dev), torch.empty(R, dtype=i32, device=dev),
-                       torch.empty(n_tokens, dtype=torch.int64, device=dev), torch.empty(n_tokens, dtype=i32, device=dev),
-                       torch.empty(1, dtype=i32, device=dev), _status(status, dev))
+        with _on(stream):
+            out = PagePlan(torch.empty(R + 1, dtype=i32, device=dev), torch.empty(R, dtype=i32, device=dev),
+                           torch.empty(n_tokens, dtype=torch.int64, device=dev),
+                           torch.empty(n_tokens, dtype=i32, device=dev), torch.empty(1, dtype=i32, device=dev),
+                           _status(status, dev))
     elif status is not None:
         out = dataclasses.replace(out, status=status)
     G = 0 if group_offsets is None else group_offsets.numel() - 1
@@ -181,7 +191,9 @@ def rl_kv_append(k, v, slot_map, k_cache, v_cache, *, status=None, stream=None) 
     for name, t in (("k", k), ("v", v)):
         if not t.is_cuda or t.dtype != k_cache.dtype or tuple(t.shape) != (T, Hkv, D) or (D > 1 and t.stride(2) != 1):
             raise _err(f"{name}: expected a device tensor [{T}, {Hkv}, {D}] of the cache's type with dense heads")
-    status = _status(status, k_cache.device)
+    if status is None:
+        with _on(stream):
+            status = _status(None, k_cache.device)
     a = _pack_append(k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1), v.stride(0), v.stride(1),
                        _dev("slot_map", slot_map, torch.int64, T), kc, vc, T, n_pages, Hkv, D, page, dt)
     _check(_load().rl_kv_append(a, _dev("status", status, torch.int32, 1), _stream(stream, k_cache)))
@@ -228,11 +240,12 @@ def rl_prefix_attn(q, k_cache, v_cache, cu_q, kv_lens, block_table, *, max_q: in
             D ** -0.5 if scale is None else scale)
     if out is None:
         dev = q.device
-        if ws is None:
-            n = int(_load().rl_prefix_attn_workspace_bytes(_pack_attn(*head, 0, 0)))
-            ws = torch.empty(max(n, 1), dtype=torch.uint8, device=dev)
-        out = AttnOut(torch.empty(T, Hq, D, dtype=q.dtype, device=dev), torch.empty(T, Hq, dtype=torch.float32, device=dev),
-                      ws, _status(status, dev))
+        with _on(stream):
+            if ws is None:
+                n = int(_load().rl_prefix_attn_workspace_bytes(_pack_attn(*head, 0, 0)))
+                ws = torch.empty(max(n, 1), dtype=torch.uint8, device=dev)
+            out = AttnOut(torch.empty(T, Hq, D, dtype=q.dtype, device=dev),
+                          torch.empty(T, Hq, dtype=torch.float32, device=dev), ws, _status(status, dev))
     elif status is not None or ws is not None:
         out = dataclasses.replace(out, status=out.status if status is None else status, ws=out.ws if ws is None else ws)
     a = _pack_attn(*head, _dev("out.out", out.out, q.dtype, T * Hq * D),
@@ -283,12 +296,13 @@ def rl_sample(logits, u, *, temperature=None, top_k=None, top_p=None, min_p=None
     if out is None:
         dev = logits.device
         e = lambda n, dt: torch.empty(n, dtype=dt, device=dev)  # noqa: E731
-        if ws is None:
-            ws = torch.empty(max(rl_sample_workspace_bytes(N, V, K), 1), dtype=torch.uint8, device=dev)
-        out = SampleOut(e((N, K), i32), e((N, K), f32), e(N + 1, torch.int64) if capacity else None,
-                        torch.zeros(capacity, dtype=i32, device=dev) if capacity else None,
-                        torch.zeros(capacity, dtype=f32, device=dev) if capacity else None, e(N, torch.uint8), ws,
-                        _status(status, dev))
+        with _on(stream):
+            if ws is None:
+                ws = torch.empty(max(rl_sample_workspace_bytes(N, V, K), 1), dtype=torch.uint8, device=dev)
+            out = SampleOut(e((N, K), i32), e((N, K), f32), e(N + 1, torch.int64) if capacity else None,
+                            torch.zeros(capacity, dtype=i32, device=dev) if capacity else None,
+                            torch.zeros(capacity, dtype=f32, device=dev) if capacity else None, e(N, torch.uint8), ws,
+                            _status(status, dev))
     elif status is not None or ws is not None:
         out = dataclasses.replace(out, status=out.status if status is None else status, ws=out.ws if ws is None else ws)
     a = _pack_sample(logits.data_ptr(), N, V, logits.stride(0) if N > 1 else V, _DTYPES.get(logits.dtype, -1), K,
