@@ -764,20 +764,25 @@ struct Row {
             find_bin(h32, by_count ? static_cast<unsigned long long>(k) : static_cast<unsigned long long>(fmaxf(top_p, 0.f) * 2147483648.f),
                      kBins, bin, before, inside);
             b.b = bin;
+            int way = 0;
             for (int tries = 0; tries < kBins; ++tries) {
                 collect(b, lo);
                 if (s.n_list > kListCap) break;
-                // the border may lie a bin further, by the rounding of the histogram's weights
+                // the border may lie a bin further, by the rounding of the histogram's weights; it is passed once (a
+                // target within the sums' rounding of a bin's edge is in neither of its bins)
                 if (by_count) break;
                 const unsigned long long above = sum_weight();
                 if (above >= target && b.b > 0) {
+                    if (way > 0) break;
+                    way = -1;
                     --b.b;
                     continue;
                 }
                 unsigned long long t = 0;
                 const int n = static_cast<int>(s.n_list);
                 for (int i = tid; i < n; i += kSelThreads) t += weight(z_of(static_cast<uint32_t>(s.comp[i] >> 32)));
-                if (above + block_sum(t, s.red) < target && b.b < kBins - 1) {
+                if (above + block_sum(t, s.red) < target && b.b < kBins - 1 && way >= 0) {
+                    way = 1;
                     ++b.b;
                     continue;
                 }

@@ -123,3 +123,19 @@ def test_a_border_among_many_near_equal_logits(seed, p):
     z[0, 5] = 0.0
     z[0, r.randint(0, V, 20)] = -3
     rows_agree(z, np.array([[0.5]]), p=[p])
+
+
+@pytest.mark.parametrize("n", [3, 700, 5000, 20000])
+def test_a_border_at_the_edge_of_a_stretch_of_logits(n):
+    """n logits well above 40,000 others; top_p a little below, at and above the share of the n."""
+    V = 60000
+    r = np.random.RandomState(n)
+    z = (-4 - 6 * r.rand(9, V)).astype(np.float32)
+    at = r.permutation(V)[:n]
+    z[:, at] = (0.5 * r.rand(9, n)).astype(np.float32)
+    w = np.exp(z[0].astype(np.float64))
+    z[:] = z[0]
+    share = np.float32(w[at].sum() / w.sum())
+    p = share + np.arange(-4, 5) * np.spacing(share)
+    assert {len(extended(z[0], [0.5], 1.0, float(x))[1]) for x in p} == {n, n + 1}
+    rows_agree(z, np.full((9, 1), 0.5), p=p)
