@@ -534,7 +534,8 @@ typedef struct rl_page_plan_args {
     int64_t n_pages;                /* pages of the cache */
     int32_t page_size;              /* 16, 32, 64 or 128 */
     int32_t* cu_q;                  /* device [R+1] out: first token of each request */
-    int32_t* kv_lens;               /* device [R] out: ctx + q */
+    int32_t* kv_lens;               /* device [R] out: ctx + q; may be ctx_lens (one block then does the
+                                       step), and shares no memory with it or q_lens otherwise */
     int64_t* slot_map;              /* device [T] out: cache slot of each token */
     int32_t* positions;             /* device [T] out: prefix + ctx + index in the step; NULL to skip */
 } rl_page_plan_args;

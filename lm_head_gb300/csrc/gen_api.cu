@@ -23,6 +23,12 @@ int check_device() {
     return RL_OK;
 }
 
+// Whether n and m elements of 4 bytes at p and q share memory.
+bool overlap(const void* p, int64_t n, const void* q, int64_t m) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+    return n > 0 && m > 0 && a < b + 4 * static_cast<uintptr_t>(m) && b < a + 4 * static_cast<uintptr_t>(n);
+}
+
 bool page_size_ok(int32_t p) { return p == 16 || p == 32 || p == 64 || p == 128; }
 
 constexpr int64_t kMaxVocab = int64_t(1) << 20;
@@ -63,6 +69,9 @@ int rl_page_plan(const rl_page_plan_args* a, int32_t* dev_status, void* stream) 
     if (a->G > 0 && (!a->group_offsets || !a->prefix_lens))
         return fail(RL_ERR_ARG, "group_offsets/prefix_lens NULL with G > 0");
     if (a->free_used == a->free_used_out) return fail(RL_ERR_ARG, "free_used_out must not be free_used");
+    if (overlap(a->cu_q, a->R + 1, a->q_lens, a->R) || overlap(a->cu_q, a->R + 1, a->ctx_lens, a->R) ||
+        overlap(a->kv_lens, a->R, a->q_lens, a->R) || (a->kv_lens != a->ctx_lens && overlap(a->kv_lens, a->R, a->ctx_lens, a->R)))
+        return fail(RL_ERR_ARG, "cu_q/kv_lens share memory with q_lens/ctx_lens");
     int rc = check_device();
     return rc != RL_OK ? rc : page_plan_impl(a, dev_status, static_cast<cudaStream_t>(stream));
 }

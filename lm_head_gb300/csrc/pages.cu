@@ -327,6 +327,9 @@ int page_plan_impl(const rl_page_plan_args* a, int32_t* status, cudaStream_t str
     const long long cap = 2ll * num_sms();
     const long long steps = (a->T + 1023) / 1024;
     p.tokens_per_block = ((steps + cap - 1) / cap) * 1024;
+    // lengths in place: every block reads them all, so one block does the step (a thread has read the lengths of its
+    // requests when it writes them)
+    if (a->R > 0 && a->kv_lens == a->ctx_lens) p.tokens_per_block = steps * 1024;
     if (p.tokens_per_block == 0) p.tokens_per_block = 1024;
     long long grid = (a->T + p.tokens_per_block - 1) / p.tokens_per_block;
     if (grid < 1) grid = 1;

@@ -147,7 +147,8 @@ def rl_page_plan(q_lens, ctx_lens, block_table, free_pages, *, page_size: int, n
                  stream=None) -> PagePlan:
     """Pages for a step's tokens: extends `block_table` [R, W] in place from the pool
     `free_pages` and returns the token offsets, key lengths, cache slots and positions.
-    n_tokens is sum(q_lens), known to whoever sized the step's tensors."""
+    n_tokens is sum(q_lens), known to whoever sized the step's tensors.  out.free_used is another
+    tensor than free_used; out.kv_lens may be ctx_lens."""
     R, W = block_table.shape
     i32 = torch.int32
     if out is None:
