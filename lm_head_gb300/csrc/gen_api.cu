@@ -106,7 +106,8 @@ int rl_prefix_attn(const rl_prefix_attn_args* a, void* ws, size_t ws_bytes, int3
             return fail(RL_ERR_ARG, "group_offsets/prefix_lens/prefix_table NULL with G > 0");
         if (!a->k_cache || !a->v_cache || a->n_pages == 0) return fail(RL_ERR_ARG, "the cache is missing");
         if (!aligned(a->k_cache, 16) || !aligned(a->v_cache, 16) || !aligned(a->out, 16)) return fail(RL_ERR_ARG, "cache/out not 16-byte aligned");
-        if (!aligned(a->q, 16) || a->q_stride_t % 8 != 0 || a->q_stride_h % 8 != 0)
+        // (the stride of an axis of one entry means nothing)
+        if (!aligned(a->q, 16) || (a->T > 1 && a->q_stride_t % 8 != 0) || (a->Hq > 1 && a->q_stride_h % 8 != 0))
             return fail(RL_ERR_ARG, "q rows not 16-byte aligned");
         const size_t need = prefix_attn_ws_bytes(a);
         if (ws_bytes < need) return fail(RL_ERR_WORKSPACE, "attention workspace too small");

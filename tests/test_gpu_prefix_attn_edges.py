@@ -155,3 +155,17 @@ def test_group_offsets_that_do_not_add_up_set_status(kind):
     if G > 1:
         c.go = c.go.flip(0).contiguous()
         assert c.run().status_bits() == LENGTHS
+
+
+@pytest.mark.parametrize("Hq", [1, 8])
+def test_strides_of_axes_of_one_entry_mean_nothing(Hq):
+    """One token, or one head, whose unused stride is odd."""
+    c = Case([1], [40], [1], [20], Hq, 1, 64, 16, BF, 3)
+    want = c.check()
+    a = c.run(torch.as_strided(c.q, c.q.shape, (515, c.q.stride(1), 1)))
+    assert torch.equal(a.out, want.out) and torch.equal(a.lse, want.lse)
+    if Hq == 1:
+        c = Case([1], [40], [5], [20], 1, 1, 64, 16, BF, 3)
+        want = c.check()
+        a = c.run(torch.as_strided(c.q, c.q.shape, (c.q.stride(0), 3, 1)))
+        assert torch.equal(a.out, want.out) and torch.equal(a.lse, want.lse)
