@@ -544,7 +544,7 @@ int rl_page_plan(const rl_page_plan_args* args, int32_t* dev_status, void* strea
 /* k_cache[slot] = k[t], v_cache[slot] = v[t] for every token with slot_map[t] >= 0.  k, v:
  * [T, Hkv, D] with any token and head strides (in elements; a token's head is contiguous).
  * A slot at or past n_pages * page_size is left out and sets RL_STATUS_PAGE_ID.  Slots are
- * distinct (of equal slots, either token's values may stay).  bf16 or fp16. */
+ * distinct (of equal slots, 16-byte pieces of either token may stay).  bf16 or fp16. */
 typedef struct rl_kv_append_args {
     const void *k, *v;
     int64_t k_stride_t, k_stride_h, v_stride_t, v_stride_h;
@@ -604,7 +604,7 @@ int rl_prefix_attn(const rl_prefix_attn_args* args, void* ws, size_t ws_bytes, i
  * these agree with exact arithmetic except where a random number falls that near to a border.
  * T = 0 is greedy: S is the largest logit (the lowest index of equal ones).  top_k outside
  * [1, V), top_p >= 1 and min_p <= 0 leave their cut out; top_p <= 0 and min_p > 1 keep one
- * token and the likeliest tokens.  T < 0 or not finite (greedy is used), a NaN knob (its cut is
+ * token and the likeliest tokens.  T < 0, not finite or in (0, 2^-124) (greedy is used), a NaN knob (its cut is
  * left out) and u outside [0, 1) (clamped) set RL_STATUS_KNOB.  NaN and +inf logits count as
  * -inf and set RL_STATUS_NONFINITE.  A row with no logit above -inf gets tokens -1, log q -inf,
  * an empty support and RL_STATUS_EMPTY_ROW.
@@ -630,7 +630,8 @@ typedef struct rl_sample_args {
     int64_t capacity;
     uint8_t* replayed;              /* device [N]; NULL to skip */
 } rl_sample_args;
-/* 16-byte aligned, with any contents.  Calls that overlap on the GPU must not share a workspace. */
+/* 16-byte aligned, with any contents; the size does not depend on K, which is checked.  Calls that overlap
+ * on the GPU must not share a workspace. */
 size_t rl_sample_workspace_bytes(int64_t N, int64_t V, int32_t K);
 int rl_sample(const rl_sample_args* args, void* ws, size_t ws_bytes, int32_t* dev_status, void* stream);
 

@@ -20,7 +20,7 @@ namespace rl {
 constexpr int kPlanThreads = 256;
 constexpr int kPlanItems = 8;                           // consecutive requests of one thread
 constexpr int kPlanTile = kPlanThreads * kPlanItems;
-constexpr int kPlanGroups = 1024;
+constexpr int kPlanGroups = 1024;                       // groups held in shared memory: 8 KB, as much as a tile's lengths
 
 // Exclusive block scan of two 64-bit sums; returns the thread's prefix, totals in (ta, tb).
 struct Scan2 {

@@ -21,8 +21,8 @@
 // Measured (one GB300, device time): 64 requests of up to 4096 own keys, 32 / 8 heads of 128, bf16
 // (0.54 GB of keys and values): 88 us in warp_attn_kernel, 6.1 TB/s, 91 % of a plain copy.  Their
 // shared prefix of 32,768 keys: 35 us in tile_attn_kernel, 980 TFLOP/s.  A decode step of 128
-// requests in 16 groups (0.1 GB): 33 us, where the chain of one part (lengths, page, keys, join: 6 us)
-// and the join count as much as the bytes.  Four requests of a 130-key prompt: 7.6 us.
+// requests in 16 groups (0.1 GB): 32.5 us, where the chain of one part (lengths, page, keys, join: 6 us)
+// and the join count as much as the bytes.  Four requests of a 130-key prompt: 7.5 us.
 #include <cfloat>
 #include <climits>
 #include <cmath>

@@ -28,8 +28,9 @@
 // (a row's chain - scores 1100, maximum 290, exponentials 950, hand-over - does not quite hide behind
 // the other accumulator's products); some 7000 cycles before a block's
 // first scores and 4600 after its last.
-// 32 requests of 0 to 256 tokens, 16 / 2 heads, up to 4096 shared and 1024 own keys: 97 us, 866 TFLOP/s
-// of the visible keys' products.
+// 32 requests of 0 to 256 tokens, 16 / 2 heads, up to 4096 shared and 1024 own keys: 95.5 us, 877 TFLOP/s
+// of the visible keys' products.  One prompt, 32 / 8 heads of 128, bf16: 157 us for 4096 tokens (877 TFLOP/s of the
+// causal products), 1520 for 16,384 (1447), 5665 for 32,768 (1553).
 //
 // Every wait is bounded; a wait that runs out raises the block's abort flag, all roles leave
 // their loops, and copies and products in flight are waited for before TMEM is released.

@@ -4,7 +4,7 @@
 // The token of a draw u is the first whose cumulative weight, in index order, passes u times
 // the total: a sum over up to the whole vocabulary decides which of two neighbours it is, so
 // fp32 sums would give another token every few thousand draws.  Weights and sums are therefore
-// carried to about 2^-36 of the largest weight:
+// carried to about 2^-36 of their row's total:
 //   w = 2^p, p = z log2(e) / T - ref with the factor as two floats;  p = n + j/2048 + r;
 //   2^(j/2048) = hi (1 + rho) from a table, 2^r - 1 = r ln2 + (r ln2)^2 / 2 (the next term is
 //   below 2^-40), so w = 2^n hi (1 + rho + ...) is the unevaluated pair (2^n hi, v).
@@ -24,10 +24,10 @@
 //  3. emit_kernel    the support rows, one warp a part.
 //
 // Measured (one GB300, rows of 151,936 logits, device time):
-//   stats   63 us for 256 fp32 rows (2.5 TB/s): bound by instruction issue, some 40 a logit where
+//   stats   64 us for 256 fp32 rows (2.4 TB/s): bound by instruction issue, some 40 a logit where
 //           sums are taken; the float-pair sum is what equality with exact arithmetic costs.
 //   select  17 us for 128 whole rows with 17 draws (latency: barriers and one part a draw);
-//           195 us for 256 rows whose nucleus is some 20,000 tokens: two passes over the row by one
+//           203 us for 256 rows whose nucleus is some 20,000 tokens: two passes over the row by one
 //           block, bound by issue and the instruction cache.  Clusters of 2, 4 and 8 blocks that
 //           share the passes were slower (the whole call 533 to 1036 us against 356 then): the
 //           others wait while the first sorts, scans and draws.  So was a block of 1024 threads
