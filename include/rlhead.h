@@ -60,7 +60,8 @@ extern "C" {
 
 /* ---- device status bits (OR-ed into *dev_status) -------------------------------- */
 #define RL_STATUS_OFFSETS            0x0001  /* offsets[0]!=0, decreasing, or offsets[N]!=nnz */
-#define RL_STATUS_ID_RANGE           0x0002  /* a support id or label outside [0, V)          */
+#define RL_STATUS_ID_RANGE           0x0002  /* a support id, label or drafted token outside [0, V), a
+                                                row of a fork outside the table or in it twice    */
 #define RL_STATUS_LOGQ               0x0004  /* a log q not finite or > 1e-6                  */
 #define RL_STATUS_LABEL_MISSING      0x0008  /* replayed row does not contain its label      */
 #define RL_STATUS_SUPPORT_MASS       0x0010  /* replayed row: |sum exp(log q) - 1| > 1e-3     */
@@ -70,7 +71,7 @@ extern "C" {
                                                 gradient has a dense softmax part            */
 #define RL_STATUS_NONFINITE          0x0100  /* a non-finite loss or logsumexp               */
 #define RL_STATUS_TIMEOUT            0x0200  /* a kernel's bounded wait ran out; outputs invalid */
-/* bits of the generation operators (rl_page_plan .. rl_sample) */
+/* bits of the generation operators (rl_page_plan .. rl_page_copy) */
 #define RL_STATUS_LENGTHS            0x0400  /* a negative length, lengths that do not add up, or a
                                                 length above the bound the caller gave         */
 #define RL_STATUS_PAGES              0x0800  /* the page pool ran out, or a table row is too short */
@@ -634,6 +635,123 @@ typedef struct rl_sample_args {
  * on the GPU must not share a workspace. */
 size_t rl_sample_workspace_bytes(int64_t N, int64_t V, int32_t K);
 int rl_sample(const rl_sample_args* args, void* ws, size_t ws_bytes, int32_t* dev_status, void* stream);
+
+/* ---- generation: several tokens a step, and the pages of a rollout's life ------------------
+ * A small model drafts tokens, the target runs on them in one step, rl_verify keeps what the
+ * target's own sampling would have given, and rl_page_release takes back the pages of what was
+ * turned down.  rl_page_fork continues a sequence in several rows that share its full pages.
+ * rl_page_compact moves the live pages together before the cache's memory is given to the
+ * trainer.  The pool is rl_page_plan's: free_pages[*free_used ..] are there to hand out, and
+ * what a call gives back it puts before them, so that it is handed out next.  Tables alone say
+ * which pages are in use; there are no owners' counts to keep. */
+
+/* Gives back the pages that rows no longer need: page p is given back if a row names it in an
+ * entry ceil(keep_lens/page_size) <= j < ceil(kv_lens/page_size) and no row names it in an entry below
+ * its ceil(keep_lens/page_size), nor a held row below ceil(held_lens/page_size).  The pages given
+ * back, ascending, become free_pages[*free_used - n .. *free_used) and *free_used_out is
+ * *free_used - n.  Tables are not written: entries past a length are never read, and rl_page_plan
+ * writes them anew.  All rows that may share a page have to be in the call.  Same inputs, same
+ * outputs: a second call with the same lengths and the same *free_used gives back the same
+ * pages (one with the new *free_used would give them back twice).
+ * keep_lens above kv_lens counts as kv_lens and sets RL_STATUS_LENGTHS, as does a negative length (0)
+ * or *free_used (0); a row shorter than its length, more pages given back than were handed out (the
+ * lowest are dropped) and *free_used above n_free set RL_STATUS_PAGES; a page id outside [0, n_pages) is left
+ * out and sets RL_STATUS_PAGE_ID. */
+typedef struct rl_page_release_args {
+    int64_t R;
+    const int32_t* kv_lens;         /* device [R] tokens that the row's pages hold */
+    const int32_t* keep_lens;       /* device [R] tokens that stay */
+    const int32_t* block_table;     /* device [R, table_width] */
+    int64_t table_width;
+    int64_t G;                      /* held rows (the groups' prompts, say) */
+    const int32_t* held_lens;       /* device [G] */
+    const int32_t* held_table;      /* device [G, held_width] */
+    int64_t held_width;
+    int32_t* free_pages;            /* device [n_free] in/out */
+    int64_t n_free;
+    const int32_t* free_used;       /* device [1] */
+    int32_t* free_used_out;         /* device [1]; not free_used */
+    int64_t n_pages;
+    int32_t page_size;              /* 16, 32, 64 or 128 */
+} rl_page_release_args;
+/* 16-byte aligned, with any contents. */
+size_t rl_page_release_workspace_bytes(int64_t n_pages);
+int rl_page_release(const rl_page_release_args* args, void* ws, size_t ws_bytes, int32_t* dev_status, void* stream);
+
+/* Rows that go on from other rows: row children[c] gets the first lens[c] tokens of row parents[c].
+ * Its entries j < lens/page_size are the parent's (the pages are shared), a last page in part
+ * is a new one, free_pages[*free_used + number of such children before c], entries after that are -1, and
+ * kv_lens[child] = lens[c].  src, dst and tokens say what is to be copied into the new pages in every
+ * layer's cache (rl_page_copy): the parent's page, the new page, lens % page_size; -1, -1, 0 where nothing is.
+ * Same inputs, same outputs.
+ * An entry with a row outside [0, R), with a child that an earlier entry has, or with a parent that is a child
+ * in the call is left out and sets RL_STATUS_ID_RANGE; so is one with lens < 0 or above
+ * the parent's kv_lens (RL_STATUS_LENGTHS) or a row too short for it (RL_STATUS_PAGES).  Where the pool runs out
+ * (RL_STATUS_PAGES) or a page id lies outside [0, n_pages) (RL_STATUS_PAGE_ID) the entry is -1 and nothing is
+ * copied. */
+typedef struct rl_page_fork_args {
+    int64_t R, C;                   /* rows of the table, entries of the call; < 2^31 */
+    const int32_t* parents;         /* device [C] */
+    const int32_t* children;        /* device [C] */
+    const int32_t* lens;            /* device [C] */
+    int32_t* kv_lens;               /* device [R] in/out */
+    int32_t* block_table;           /* device [R, table_width] in/out */
+    int64_t table_width;
+    const int32_t* free_pages;      /* device [n_free] */
+    int64_t n_free;
+    const int32_t* free_used;       /* device [1] */
+    int32_t* free_used_out;         /* device [1]; not free_used */
+    int64_t n_pages;
+    int32_t* src;                   /* device [C] out */
+    int32_t* dst;                   /* device [C] out */
+    int32_t* tokens;                /* device [C] out */
+    int32_t page_size;
+} rl_page_fork_args;
+size_t rl_page_fork_workspace_bytes(int64_t R, int64_t C);
+int rl_page_fork(const rl_page_fork_args* args, void* ws, size_t ws_bytes, int32_t* dev_status, void* stream);
+
+/* Moves the live pages (those that a row names below its length) to the ids [0, n_live): the k-th live page
+ * with an id of at least n_live goes to the k-th id below it that is not live, the others stay.  src and dst list the moves (-1
+ * after the last), for rl_page_copy in every layer's cache; no page is in both lists.  The tables are written with
+ * the new ids, and -1 past the rows' lengths; free_pages = 0 .. n_pages - 1 and *free_used_out = n_live, so that what
+ * is past n_live can be given up or handed out.  Negative lengths (as 0), rows shorter than their lengths and ids
+ * outside [0, n_pages) (-1 in the table) set status bits as in rl_page_release. */
+typedef struct rl_page_compact_args {
+    int64_t R;
+    const int32_t* kv_lens;         /* device [R] */
+    const int32_t* block_table;     /* device [R, table_width] */
+    int32_t* block_table_out;       /* device [R, table_width]; may be block_table */
+    int64_t table_width;
+    int64_t G;                      /* rows of a second table (the groups' prompts); 0: none */
+    const int32_t* prefix_lens;     /* device [G] */
+    const int32_t* prefix_table;    /* device [G, prefix_width] */
+    int32_t* prefix_table_out;      /* device [G, prefix_width]; may be prefix_table */
+    int64_t prefix_width;
+    int64_t n_pages;
+    int32_t* src;                   /* device [n_pages / 2] out */
+    int32_t* dst;                   /* device [n_pages / 2] out */
+    int32_t* free_pages;            /* device [n_pages] out */
+    int32_t* free_used_out;         /* device [1] out: n_live */
+    int32_t page_size;
+} rl_page_compact_args;
+size_t rl_page_compact_workspace_bytes(int64_t n_pages);
+int rl_page_compact(const rl_page_compact_args* args, void* ws, size_t ws_bytes, int32_t* dev_status, void* stream);
+
+/* Page dst[i] of each layer's k and v cache = page src[i]: its first tokens[i] tokens of every head, or
+ * all of it (tokens NULL).  Pairs with a negative id are left out.  No page may be written twice or
+ * both written and read in one call (what it holds is then not defined).  An id at or above n_pages is left out
+ * (RL_STATUS_PAGE_ID); tokens outside [0, page_size] are clamped (RL_STATUS_LENGTHS). */
+typedef struct rl_page_copy_args {
+    int64_t n;
+    const int32_t* src;             /* device [n] */
+    const int32_t* dst;             /* device [n] */
+    const int32_t* tokens;          /* device [n]; NULL: whole pages */
+    void *k_cache, *v_cache;        /* device [layers, n_pages, Hkv, page_size, D], 16-byte aligned */
+    int64_t layer_stride;           /* elements between two layers of a cache */
+    int64_t n_pages;
+    int32_t layers, Hkv, D, page_size, dtype;   /* any rl_dtype */
+} rl_page_copy_args;
+int rl_page_copy(const rl_page_copy_args* args, int32_t* dev_status, void* stream);
 
 /* ---- utilities ------------------------------------------------------------------ */
 /* The head contraction alone: D[M, N] fp32 = A[M, K] * B[N, K]^T, A and B bf16 row-major

@@ -15,6 +15,7 @@ Functions carry the C names:
                sums), rl_rollout_metrics_named (the page's named metrics from those sums)
   generation:  rl_page_plan, rl_kv_append, rl_prefix_attn, rl_sample (one decode step of a
                rollout batch; lm_head_gb300.generation)
+  pages:       rl_page_release, rl_page_fork, rl_page_compact, rl_page_copy (lm_head_gb300.pages)
   utilities:   rl_gemm_bf16, rl_gemm_bf16_tn, rl_status_read, rl_wait_selftest,
                rl_set_option / rl_get_option, rl_profile_enable / rl_profile_read,
                rl_kernel_launch_count, the *_workspace_bytes queries
@@ -138,12 +139,15 @@ from .generation import (  # noqa: E402
     RL_DTYPE_BF16, RL_DTYPE_F16, RL_DTYPE_F32, AttnOut, PagePlan, RlKvAppendArgs, RlPagePlanArgs,
     RlPrefixAttnArgs, RlSampleArgs,
     SampleOut, rl_kv_append, rl_page_plan, rl_prefix_attn, rl_sample, rl_sample_workspace_bytes)
-from . import generation as _generation  # noqa: E402
+from .pages import (  # noqa: E402
+    PageCompact, PageFork, PageRelease, rl_page_compact, rl_page_copy, rl_page_fork, rl_page_release)
+from . import generation as _generation, pages as _pages  # noqa: E402
 
 _lib = None
 
 _SIGS = {
     **_generation.SIGS,
+    **_pages.SIGS,
     "rl_head_saved_bytes": (ctypes.c_size_t, [ctypes.c_int64, ctypes.c_int64]),
     "rl_head_saved_bytes_ex": (ctypes.c_size_t, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int64,
                                                  ctypes.POINTER(RlParams)]),

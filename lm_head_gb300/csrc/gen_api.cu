@@ -145,4 +145,90 @@ int rl_sample(const rl_sample_args* a, void* ws, size_t ws_bytes, int32_t* dev_s
     return sample_impl(a, ws, dev_status, static_cast<cudaStream_t>(stream));
 }
 
+// ---- pages of a rollout's life ---------------------------------------------------------
+size_t rl_page_release_workspace_bytes(int64_t n_pages) {
+    return n_pages < 0 || n_pages >= kMax31 ? 0 : page_release_ws_bytes(n_pages);
+}
+
+int rl_page_release(const rl_page_release_args* a, void* ws, size_t ws_bytes, int32_t* dev_status, void* stream) {
+    if (!a || !dev_status) return fail(RL_ERR_ARG, "args/dev_status is NULL");
+    if (a->R < 0 || a->G < 0 || a->n_free < 0 || a->n_pages < 0 || a->table_width < 0 || a->held_width < 0)
+        return fail(RL_ERR_ARG, "negative size");
+    if (!page_size_ok(a->page_size)) return fail(RL_ERR_UNSUPPORTED, "page_size must be 16, 32, 64 or 128");
+    if (a->R >= kMax31 || a->G >= kMax31 || a->n_free >= kMax31 || a->n_pages >= kMax31 || a->table_width >= kMax31 || a->held_width >= kMax31)
+        return fail(RL_ERR_UNSUPPORTED, "R, G, n_free, n_pages or a table's width too large");
+    if (!a->free_used || !a->free_used_out || (a->R > 0 && (!a->kv_lens || !a->keep_lens)) ||
+        (a->R > 0 && a->table_width > 0 && !a->block_table) || (a->n_free > 0 && !a->free_pages))
+        return fail(RL_ERR_ARG, "required pointer is NULL");
+    if (a->G > 0 && (!a->held_lens || (a->held_width > 0 && !a->held_table)))
+        return fail(RL_ERR_ARG, "held_lens/held_table NULL with G > 0");
+    if (a->free_used == a->free_used_out) return fail(RL_ERR_ARG, "free_used_out must not be free_used");
+    if (ws_bytes < page_release_ws_bytes(a->n_pages)) return fail(RL_ERR_WORKSPACE, "release workspace too small");
+    if (a->n_pages > 0 && (!ws || !aligned(ws, 16))) return fail(RL_ERR_ARG, "ws is NULL or not 16-byte aligned");
+    int rc = check_device();
+    return rc != RL_OK ? rc : page_release_impl(a, ws, dev_status, static_cast<cudaStream_t>(stream));
+}
+
+size_t rl_page_fork_workspace_bytes(int64_t R, int64_t C) {
+    return R < 0 || C < 0 || R >= kMax31 || C >= kMax31 ? 0 : page_fork_ws_bytes(R, C);
+}
+
+int rl_page_fork(const rl_page_fork_args* a, void* ws, size_t ws_bytes, int32_t* dev_status, void* stream) {
+    if (!a || !dev_status) return fail(RL_ERR_ARG, "args/dev_status is NULL");
+    if (a->R < 0 || a->C < 0 || a->n_free < 0 || a->n_pages < 0 || a->table_width < 0) return fail(RL_ERR_ARG, "negative size");
+    if (!page_size_ok(a->page_size)) return fail(RL_ERR_UNSUPPORTED, "page_size must be 16, 32, 64 or 128");
+    if (a->R >= kMax31 || a->C >= kMax31 || a->n_free >= kMax31 || a->n_pages >= kMax31 || a->table_width >= kMax31)
+        return fail(RL_ERR_UNSUPPORTED, "R, C, n_free, n_pages or table_width too large");
+    if (!a->free_used || !a->free_used_out || (a->C > 0 && (!a->parents || !a->children || !a->lens || !a->src || !a->dst || !a->tokens)) ||
+        (a->C > 0 && a->R > 0 && (!a->kv_lens || (a->table_width > 0 && !a->block_table))) || (a->n_free > 0 && !a->free_pages))
+        return fail(RL_ERR_ARG, "required pointer is NULL");
+    if (a->free_used == a->free_used_out) return fail(RL_ERR_ARG, "free_used_out must not be free_used");
+    if (overlap(a->lens, a->C, a->kv_lens, a->R) || overlap(a->parents, a->C, a->tokens, a->C) || overlap(a->children, a->C, a->tokens, a->C) ||
+        overlap(a->lens, a->C, a->tokens, a->C))
+        return fail(RL_ERR_ARG, "lens shares memory with kv_lens, or an input with tokens");
+    if (ws_bytes < page_fork_ws_bytes(a->R, a->C)) return fail(RL_ERR_WORKSPACE, "fork workspace too small");
+    if (a->C > 0 && (!ws || !aligned(ws, 16))) return fail(RL_ERR_ARG, "ws is NULL or not 16-byte aligned");
+    int rc = check_device();
+    return rc != RL_OK ? rc : page_fork_impl(a, ws, dev_status, static_cast<cudaStream_t>(stream));
+}
+
+size_t rl_page_compact_workspace_bytes(int64_t n_pages) {
+    return n_pages < 0 || n_pages >= kMax31 ? 0 : page_compact_ws_bytes(n_pages);
+}
+
+int rl_page_compact(const rl_page_compact_args* a, void* ws, size_t ws_bytes, int32_t* dev_status, void* stream) {
+    if (!a || !dev_status) return fail(RL_ERR_ARG, "args/dev_status is NULL");
+    if (a->R < 0 || a->G < 0 || a->n_pages < 0 || a->table_width < 0 || a->prefix_width < 0) return fail(RL_ERR_ARG, "negative size");
+    if (!page_size_ok(a->page_size)) return fail(RL_ERR_UNSUPPORTED, "page_size must be 16, 32, 64 or 128");
+    if (a->R >= kMax31 || a->G >= kMax31 || a->n_pages >= kMax31 || a->table_width >= kMax31 || a->prefix_width >= kMax31)
+        return fail(RL_ERR_UNSUPPORTED, "R, G, n_pages or a table's width too large");
+    if (!a->free_used_out || (a->R > 0 && !a->kv_lens) || (a->R > 0 && a->table_width > 0 && (!a->block_table || !a->block_table_out)) ||
+        (a->n_pages > 0 && !a->free_pages) || (a->n_pages > 1 && (!a->src || !a->dst)))
+        return fail(RL_ERR_ARG, "required pointer is NULL");
+    if (a->G > 0 && (!a->prefix_lens || (a->prefix_width > 0 && (!a->prefix_table || !a->prefix_table_out))))
+        return fail(RL_ERR_ARG, "prefix_lens/prefix_table NULL with G > 0");
+    if (ws_bytes < page_compact_ws_bytes(a->n_pages)) return fail(RL_ERR_WORKSPACE, "compact workspace too small");
+    if (a->n_pages > 0 && (!ws || !aligned(ws, 16))) return fail(RL_ERR_ARG, "ws is NULL or not 16-byte aligned");
+    int rc = check_device();
+    return rc != RL_OK ? rc : page_compact_impl(a, ws, dev_status, static_cast<cudaStream_t>(stream));
+}
+
+int rl_page_copy(const rl_page_copy_args* a, int32_t* dev_status, void* stream) {
+    if (!a || !dev_status) return fail(RL_ERR_ARG, "args/dev_status is NULL");
+    if (a->n < 0 || a->n_pages < 0 || a->layers < 0 || a->Hkv <= 0 || a->D <= 0) return fail(RL_ERR_ARG, "negative or zero size");
+    if (!page_size_ok(a->page_size)) return fail(RL_ERR_UNSUPPORTED, "page_size must be 16, 32, 64 or 128");
+    if (a->dtype != RL_DTYPE_F32 && a->dtype != RL_DTYPE_BF16 && a->dtype != RL_DTYPE_F16)
+        return fail(RL_ERR_UNSUPPORTED, "dtype must be fp32, bf16 or fp16");
+    if (a->n >= kMax31 || a->n_pages >= kMax31 || int64_t(a->Hkv) * a->D >= (int64_t(1) << 24) || a->layers > 65536 ||
+        int64_t(a->layers) * a->Hkv >= (int64_t(1) << 30))
+        return fail(RL_ERR_UNSUPPORTED, "n, n_pages, layers or Hkv * D too large");
+    if (a->layers > 1 && (a->layer_stride < 0 || a->layer_stride < a->n_pages * a->Hkv * a->page_size * a->D))
+        return fail(RL_ERR_ARG, "layer_stride smaller than a layer");
+    if (a->n > 0 && (!a->src || !a->dst)) return fail(RL_ERR_ARG, "src/dst is NULL");
+    if (a->n > 0 && a->layers > 0 && a->n_pages > 0 && (!a->k_cache || !a->v_cache)) return fail(RL_ERR_ARG, "cache is NULL");
+    if (!aligned(a->k_cache, 16) || !aligned(a->v_cache, 16)) return fail(RL_ERR_ARG, "cache not 16-byte aligned");
+    int rc = check_device();
+    return rc != RL_OK ? rc : page_copy_impl(a, dev_status, static_cast<cudaStream_t>(stream));
+}
+
 }  // extern "C"
