@@ -753,6 +753,57 @@ typedef struct rl_page_copy_args {
 } rl_page_copy_args;
 int rl_page_copy(const rl_page_copy_args* args, int32_t* dev_status, void* stream);
 
+/* ---- distillation from a teacher's top tokens ---------------------------------------------
+ * Trains a model (the one that drafts tokens for the policy, say) on another's recorded top tokens:
+ * CSR rows of ids and log-probabilities, as rl_sample writes them and rl_support holds them.
+ * From the student's logits z [N, V], with P = softmax(z / T) and the row's support S:
+ *   tail = 0   p = softmax over S of logq / T (top logits or log-probabilities, up to a constant),
+ *              loss = sum_S p ln(p / P); kind RL_DISTILL_FORWARD only
+ *   tail = 1   p = exp(logq) on S (the teacher's log-probabilities at its own temperature), and the rest of the
+ *              vocabulary is one more outcome, of p_0 = max(1 - sum_S p, 2^-20) and P_0 = sum of P outside S
+ *              (left out where P_0 is 0); loss = sum over S and the rest of
+ *     RL_DISTILL_FORWARD  p ln(p / P)
+ *     RL_DISTILL_REVERSE  P ln(P / p)
+ *     RL_DISTILL_JSD      beta p ln(p / m) + (1 - beta) P ln(P / m),  m = beta p + (1 - beta) P
+ * dlogits = dloss dL/dz in the logits' type.  The outcomes are summed in pairs of floats, the rest's probability is
+ * a sum over its tokens (no 1 - sum), exponentials of the rest are fp32.
+ * A row without a support (no entry, or none with logq > -inf) has loss 0 and gradient 0, whatever its logits;
+ * a row with dloss 0 has gradient 0.  -inf logits have P = 0: where the forward kind's teacher wants such a token
+ * the loss is inf.  NaN and +inf logits, and a row of -inf alone, make the row's loss not finite; a loss that is not finite sets
+ * RL_STATUS_NONFINITE.
+ * Checked on the device: row bounds (RL_STATUS_OFFSETS, the row then has no support), ids in [0, V) and logq not NaN,
+ * not +inf and, with tail, at most 1e-6 (RL_STATUS_ID_RANGE, RL_STATUS_LOGQ; the entry is left out, but for a logq
+ * above 1e-6), ids strictly ascending (RL_STATUS_ROW_ORDER; the row's results are then not defined). */
+typedef enum { RL_DISTILL_FORWARD = 0, RL_DISTILL_REVERSE = 1, RL_DISTILL_JSD = 2 } rl_distill_kind;
+typedef struct rl_distill_args {
+    const void* logits;             /* device [N, V], rows row_stride elements apart; V * size at most 1,800,000 bytes */
+    int64_t N, V, row_stride;
+    int32_t dtype;                  /* rl_dtype */
+    int32_t kind;                   /* rl_distill_kind */
+    int32_t tail;                   /* 0 or 1 */
+    float temperature;              /* T, in [2^-20, 2^20] */
+    float beta;                     /* in (0, 1); RL_DISTILL_JSD only */
+    int32_t reserved;               /* 0 */
+    const int64_t* offsets;         /* device [N+1] */
+    const int32_t* ids;             /* device [nnz] strictly ascending in a row */
+    const float* logq;              /* device [nnz] */
+    int64_t nnz;
+    const float* dloss;             /* device [N]; not of the forward */
+    void* dlogits;                  /* device [N, V], the logits' type; not of the forward.  May be logits (same stride), else
+                                       shares no memory with them */
+    int64_t grad_stride;            /* elements between its rows */
+    float* loss;                    /* device [N]; not of the backward */
+    float* mass;                    /* device [N] the student's probability of the support (0 without one); NULL to skip */
+} rl_distill_args;
+/* State that the forward leaves for the backward, 16-byte aligned. */
+size_t rl_distill_saved_bytes(int64_t N, int64_t nnz);
+/* saved: device; NULL where no backward follows. */
+int rl_distill_fwd(const rl_distill_args* args, void* saved, int32_t* dev_status, void* stream);
+/* The gradients, from the same logits and support rows and what the forward saved (which stays as it is). */
+int rl_distill_bwd(const rl_distill_args* args, const void* saved, int32_t* dev_status, void* stream);
+/* Both in one pass over the logits, for a dloss known before. */
+int rl_distill_fwd_bwd(const rl_distill_args* args, int32_t* dev_status, void* stream);
+
 /* ---- utilities ------------------------------------------------------------------ */
 /* The head contraction alone: D[M, N] fp32 = A[M, K] * B[N, K]^T, A and B bf16 row-major
  * (K contiguous), device pointers, 16-byte aligned; K % 8 == 0, N % 4 == 0.  Same tcgen05

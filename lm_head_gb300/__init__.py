@@ -16,6 +16,7 @@ Functions carry the C names:
   generation:  rl_page_plan, rl_kv_append, rl_prefix_attn, rl_sample (one decode step of a
                rollout batch; lm_head_gb300.generation)
   pages:       rl_page_release, rl_page_fork, rl_page_compact, rl_page_copy (lm_head_gb300.pages)
+  distillation: rl_distill_fwd, rl_distill_bwd, rl_distill_fwd_bwd (lm_head_gb300.distill)
   utilities:   rl_gemm_bf16, rl_gemm_bf16_tn, rl_status_read, rl_wait_selftest,
                rl_set_option / rl_get_option, rl_profile_enable / rl_profile_read,
                rl_kernel_launch_count, the *_workspace_bytes queries
@@ -141,13 +142,17 @@ from .generation import (  # noqa: E402
     SampleOut, rl_kv_append, rl_page_plan, rl_prefix_attn, rl_sample, rl_sample_workspace_bytes)
 from .pages import (  # noqa: E402
     PageCompact, PageFork, PageRelease, rl_page_compact, rl_page_copy, rl_page_fork, rl_page_release)
-from . import generation as _generation, pages as _pages  # noqa: E402
+from .distill import (  # noqa: E402
+    RL_DISTILL_FORWARD, RL_DISTILL_JSD, RL_DISTILL_REVERSE, DistillOut, DistillParams, rl_distill_bwd, rl_distill_fwd,
+    rl_distill_fwd_bwd)
+from . import distill as _distill, generation as _generation, pages as _pages  # noqa: E402
 
 _lib = None
 
 _SIGS = {
     **_generation.SIGS,
     **_pages.SIGS,
+    **_distill.SIGS,
     "rl_head_saved_bytes": (ctypes.c_size_t, [ctypes.c_int64, ctypes.c_int64]),
     "rl_head_saved_bytes_ex": (ctypes.c_size_t, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int64,
                                                  ctypes.POINTER(RlParams)]),

@@ -95,6 +95,14 @@ RL_DEVINL FF exp_ff(float x) {
     return {ldexpf(p.hi, k), ldexpf(p.lo, k)};
 }
 
+// ln x for a positive float pair: one Newton step from the float's, to about 2^-46 absolute.
+RL_DEVINL FF ln_pair(FF x) {
+    const float y = logf(x.hi);
+    const FF r = ff_mul(x, exp_ff(-y));                  // 1 + d
+    const float d = __fadd_rn(__fsub_rn(r.hi, 1.f), r.lo);
+    return fast_two_sum(y, fmaf(-0.5f * d, d, d));
+}
+
 // ln t as a float-float pair (host): hi = the float nearest ln t, lo = the float nearest
 // the rest; -inf for t <= 0.
 inline FF ln_ff(double t) {

@@ -1,5 +1,5 @@
-// C ABI of the generation path (declared in include/rlhead.h): host-side argument checks
-// and dispatch.  Nothing here allocates device memory or synchronises.
+// C ABI of the generation path and of distillation (declared in include/rlhead.h): host-side
+// argument checks and dispatch.  Nothing here allocates device memory or synchronises.
 #include <cmath>
 
 #include "internal.h"
@@ -49,6 +49,35 @@ int check_attn_sizes(const rl_prefix_attn_args* a) {
     if (a->T > 0 && a->R > 0 && a->max_q < 1) return fail(RL_ERR_ARG, "max_q must bound the step's lengths");
     if (!(a->scale >= 0.f) || !std::isfinite(a->scale * 1.5f)) return fail(RL_ERR_ARG, "scale is negative, not finite or too large");
     return RL_OK;
+}
+
+int check_distill(const rl_distill_args* a, const int32_t* dev_status, int pass) {
+    if (!a || !dev_status) return fail(RL_ERR_ARG, "args/dev_status is NULL");
+    if (a->N < 0 || a->V <= 0 || a->nnz < 0) return fail(RL_ERR_ARG, "negative or zero size");
+    if (a->dtype != RL_DTYPE_F32 && a->dtype != RL_DTYPE_BF16 && a->dtype != RL_DTYPE_F16)
+        return fail(RL_ERR_UNSUPPORTED, "dtype must be fp32, bf16 or fp16");
+    const int64_t size = a->dtype == RL_DTYPE_F32 ? 4 : 2;
+    if (a->kind < RL_DISTILL_FORWARD || a->kind > RL_DISTILL_JSD || a->tail < 0 || a->tail > 1 || a->reserved != 0)
+        return fail(RL_ERR_ARG, "kind, tail or reserved out of range");
+    if (!a->tail && a->kind != RL_DISTILL_FORWARD) return fail(RL_ERR_ARG, "the reverse and JSD kinds need tail = 1");
+    if (!(a->temperature >= 0x1p-20f) || !(a->temperature <= 0x1p20f)) return fail(RL_ERR_ARG, "temperature out of range");
+    if (a->kind == RL_DISTILL_JSD && (!(a->beta > 0.f) || !(a->beta < 1.f))) return fail(RL_ERR_ARG, "beta must lie between 0 and 1");
+    if (a->V > kDistillRowBytes / size || a->N >= kMax31) return fail(RL_ERR_UNSUPPORTED, "N or V too large");
+    if (a->N > 1 && a->row_stride < a->V) return fail(RL_ERR_ARG, "row_stride smaller than V");
+    if (a->N == 0) return RL_OK;
+    if (!a->logits || !a->offsets || (a->nnz > 0 && (!a->ids || !a->logq))) return fail(RL_ERR_ARG, "logits/offsets/ids/logq is NULL");
+    if (!aligned(a->logits, size)) return fail(RL_ERR_ARG, "logits not aligned to their type");
+    if (pass != kDistillBwd && !a->loss) return fail(RL_ERR_ARG, "loss is NULL");
+    if (pass != kDistillFwd) {
+        if (!a->dloss || !a->dlogits) return fail(RL_ERR_ARG, "dloss/dlogits is NULL");
+        if (!aligned(a->dlogits, size)) return fail(RL_ERR_ARG, "dlogits not aligned to their type");
+        if (a->N > 1 && a->grad_stride < a->V) return fail(RL_ERR_ARG, "grad_stride smaller than V");
+        const bool in_place = a->logits == a->dlogits && (a->N == 1 || a->row_stride == a->grad_stride);
+        const uintptr_t x = reinterpret_cast<uintptr_t>(a->logits), y = reinterpret_cast<uintptr_t>(a->dlogits);
+        const uintptr_t nx = static_cast<uintptr_t>(((a->N - 1) * a->row_stride + a->V) * size), ny = static_cast<uintptr_t>(((a->N - 1) * a->grad_stride + a->V) * size);
+        if (!in_place && x < y + ny && y < x + nx) return fail(RL_ERR_ARG, "dlogits shares memory with logits");
+    }
+    return check_device();
 }
 
 }  // namespace
@@ -229,6 +258,26 @@ int rl_page_copy(const rl_page_copy_args* a, int32_t* dev_status, void* stream) 
     if (!aligned(a->k_cache, 16) || !aligned(a->v_cache, 16)) return fail(RL_ERR_ARG, "cache not 16-byte aligned");
     int rc = check_device();
     return rc != RL_OK ? rc : page_copy_impl(a, dev_status, static_cast<cudaStream_t>(stream));
+}
+
+// ---- distillation ------------------------------------------------------------------------
+size_t rl_distill_saved_bytes(int64_t N, int64_t nnz) { return N < 0 || nnz < 0 ? 0 : distill_saved_bytes(N, nnz); }
+
+int rl_distill_fwd(const rl_distill_args* a, void* saved, int32_t* dev_status, void* stream) {
+    if (!aligned(saved, 16)) return fail(RL_ERR_ARG, "saved not 16-byte aligned");
+    const int rc = check_distill(a, dev_status, kDistillFwd);
+    return rc != RL_OK ? rc : distill_impl(a, kDistillFwd, saved, dev_status, static_cast<cudaStream_t>(stream));
+}
+
+int rl_distill_bwd(const rl_distill_args* a, const void* saved, int32_t* dev_status, void* stream) {
+    if (!saved || !aligned(saved, 16)) return fail(RL_ERR_ARG, "saved is NULL or not 16-byte aligned");
+    const int rc = check_distill(a, dev_status, kDistillBwd);
+    return rc != RL_OK ? rc : distill_impl(a, kDistillBwd, const_cast<void*>(saved), dev_status, static_cast<cudaStream_t>(stream));
+}
+
+int rl_distill_fwd_bwd(const rl_distill_args* a, int32_t* dev_status, void* stream) {
+    const int rc = check_distill(a, dev_status, kDistillBoth);
+    return rc != RL_OK ? rc : distill_impl(a, kDistillBoth, nullptr, dev_status, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

@@ -213,5 +213,11 @@ int page_fork_impl(const rl_page_fork_args* a, void* ws, int32_t* status, cudaSt
 size_t page_compact_ws_bytes(int64_t n_pages);
 int page_compact_impl(const rl_page_compact_args* a, void* ws, int32_t* status, cudaStream_t stream);
 int page_copy_impl(const rl_page_copy_args* a, int32_t* status, cudaStream_t stream);
+// distillation: the forward, the backward on what it saved, or both in one pass
+enum { kDistillFwd = 0, kDistillBwd = 1, kDistillBoth = 2 };
+constexpr int64_t kDistillRowBytes = 1800000;   // longest row of logits that the slices of eight blocks hold
+constexpr int kDistillSliceBytes = 220 * 1024;
+size_t distill_saved_bytes(int64_t N, int64_t nnz);
+int distill_impl(const rl_distill_args* a, int pass, void* saved, int32_t* status, cudaStream_t stream);
 
 }  // namespace rl

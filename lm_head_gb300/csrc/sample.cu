@@ -259,13 +259,6 @@ RL_DEVINL unsigned long long fraction_of(float f, unsigned long long x) {
     const unsigned long long q = sh >= 0 ? m << sh : sh > -64 ? m >> -sh : 0ull;
     return __umul64hi(q, x);
 }
-// ln x for a positive float pair: one Newton step from the float's, to about 2^-46 absolute.
-RL_DEVINL FF ln_pair(FF x) {
-    const float y = logf(x.hi);
-    const FF r = ff_mul(x, exp_ff(-y));                  // 1 + d
-    const float d = __fadd_rn(__fsub_rn(r.hi, 1.f), r.lo);
-    return fast_two_sum(y, fmaf(-0.5f * d, d, d));
-}
 // ln q of a token
 RL_DEVINL float log_q(float z, const RowRec& r) {
     const FF d = two_sum(z, -r.M);
