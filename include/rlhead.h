@@ -645,6 +645,62 @@ int rl_sample(const rl_sample_args* args, void* ws, size_t ws_bytes, int32_t* de
  * what a call gives back it puts before them, so that it is handed out next.  Tables alone say
  * which pages are in use; there are no owners' counts to keep. */
 
+/* What rl_verify knows of the distributions of the step's rows: logits with a temperature, support rows as
+ * rl_sample writes them, or both, each row by its `replayed` flag. */
+typedef struct rl_dist {
+    const void* logits;             /* device [n_rows, V], rows row_stride elements apart; NULL: every row is a support row */
+    int64_t n_rows, row_stride;
+    const float* temperature;       /* device [n_rows]; NULL = 1 */
+    const int64_t* offsets;         /* device [n_rows+1]; NULL: every row is logits */
+    const int32_t* ids;             /* device [nnz] strictly ascending in a row */
+    const float* logq;              /* device [nnz] log-probabilities */
+    int64_t nnz;
+    const uint8_t* replayed;        /* device [n_rows]; 1: the support row is the distribution, 0: the logits.  NULL: the
+                                       one that is there */
+    const int32_t* rows;            /* device [T] the row of the step's row t; NULL: t */
+} rl_dist;
+
+/* Verification of drafted tokens against the target's probabilities, from given random numbers.  Request r has
+ * the step's rows cu_q[r] .. cu_q[r+1]: row t holds the target's distribution p_t after the token
+ * step_tokens[t], and for all but the request's last row the drafting model's q_t, from which the candidate
+ * x_t = step_tokens[t+1] was drawn (a request of one row has no drafts).  In order of the rows
+ *   x_t is accepted if u[t] q_t(x_t) < p_t(x_t);
+ *   the first that is not ends the step: its row's token y is drawn from max(p_t - q_t, 0) / sum
+ *     (from p_t where that is 0 everywhere); after the last row's drafts y is drawn from the last row's p_t;
+ *   y is the first token with sum_{j <= y} left_j > u_next[r] sum left.
+ * So the tokens are distributed as the target's own samples.  Row t's p is softmax(logits / T) of the vocabulary (T = 0: the largest
+ * logit, the lowest index of equal ones), or exp(logq) on its support row; q likewise, or, without any draft distribution, 1 for the
+ * candidate (drafts that were copied or greedy).  Probabilities and sums that decide a token are carried to about
+ * 2^-36 of the row's total.
+ * Outputs: tokens[t] = the accepted tokens, then y, then -1, in the request's rows; logq[t] = ln p_t of the token (0 where
+ * there is none); accepted[r]; keep_lens[r] = ctx_lens[r] + accepted[r] + 1, the tokens whose keys and values stay in the
+ * cache (rl_page_release).  A request without rows has accepted 0 and keep_lens = ctx_lens; rows that no request has
+ * get -1 and 0.
+ * Checked on the device: cu_q that decreases or leaves [0, T] (RL_STATUS_LENGTHS, the request then has no rows), candidates outside
+ * [0, V) (RL_STATUS_ID_RANGE, not accepted), support ids outside it (left out), row maps and row bounds (RL_STATUS_OFFSETS,
+ * the row then has no token), log-probabilities that are NaN or above 1e-6 (RL_STATUS_LOGQ, left out if NaN or +inf), ids not ascending in the row that y is
+ * drawn from (RL_STATUS_ROW_ORDER, y is then not defined), temperatures and random numbers as in rl_sample (RL_STATUS_KNOB), NaN and +inf logits
+ * (RL_STATUS_NONFINITE, they count as -inf).  A target row without a token accepts nothing and sets RL_STATUS_EMPTY_ROW, y = -1 and
+ * logq -inf if it is the last row looked at; a draft row without one sets it too. */
+typedef struct rl_verify_args {
+    int64_t R, T, V;                /* V <= 2^20 */
+    const int32_t* cu_q;            /* device [R+1] */
+    const int32_t* step_tokens;     /* device [T] */
+    const float* u;                 /* device [T] in [0, 1) (a request's last is not used) */
+    const float* u_next;            /* device [R] in [0, 1) */
+    rl_dist target;
+    rl_dist draft;                  /* logits and offsets NULL: the drafts were certain */
+    int32_t target_dtype, draft_dtype;      /* rl_dtype of the logits */
+    const int32_t* ctx_lens;        /* device [R]; NULL = 0 */
+    int32_t* tokens;                /* device [T] */
+    float* logq;                    /* device [T]; NULL to skip */
+    int32_t* accepted;              /* device [R] */
+    int32_t* keep_lens;             /* device [R]; NULL to skip; may be ctx_lens */
+} rl_verify_args;
+/* 16-byte aligned, with any contents; by T, V and which logits there are. */
+size_t rl_verify_workspace_bytes(const rl_verify_args* args);
+int rl_verify(const rl_verify_args* args, void* ws, size_t ws_bytes, int32_t* dev_status, void* stream);
+
 /* Gives back the pages that rows no longer need: page p is given back if a row names it in an
  * entry ceil(keep_lens/page_size) <= j < ceil(kv_lens/page_size) and no row names it in an entry below
  * its ceil(keep_lens/page_size), nor a held row below ceil(held_lens/page_size).  The pages given

@@ -15,6 +15,7 @@ Functions carry the C names:
                sums), rl_rollout_metrics_named (the page's named metrics from those sums)
   generation:  rl_page_plan, rl_kv_append, rl_prefix_attn, rl_sample (one decode step of a
                rollout batch; lm_head_gb300.generation)
+  drafts:      rl_verify (lm_head_gb300.verify)
   pages:       rl_page_release, rl_page_fork, rl_page_compact, rl_page_copy (lm_head_gb300.pages)
   distillation: rl_distill_fwd, rl_distill_bwd, rl_distill_fwd_bwd (lm_head_gb300.distill)
   utilities:   rl_gemm_bf16, rl_gemm_bf16_tn, rl_status_read, rl_wait_selftest,
@@ -145,7 +146,8 @@ from .pages import (  # noqa: E402
 from .distill import (  # noqa: E402
     RL_DISTILL_FORWARD, RL_DISTILL_JSD, RL_DISTILL_REVERSE, DistillOut, DistillParams, rl_distill_bwd, rl_distill_fwd,
     rl_distill_fwd_bwd)
-from . import distill as _distill, generation as _generation, pages as _pages  # noqa: E402
+from .verify import Dist, VerifyOut, rl_verify  # noqa: E402
+from . import distill as _distill, generation as _generation, pages as _pages, verify as _verify  # noqa: E402
 
 _lib = None
 
@@ -153,6 +155,7 @@ _SIGS = {
     **_generation.SIGS,
     **_pages.SIGS,
     **_distill.SIGS,
+    **_verify.SIGS,
     "rl_head_saved_bytes": (ctypes.c_size_t, [ctypes.c_int64, ctypes.c_int64]),
     "rl_head_saved_bytes_ex": (ctypes.c_size_t, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int64,
                                                  ctypes.POINTER(RlParams)]),

@@ -51,6 +51,29 @@ int check_attn_sizes(const rl_prefix_attn_args* a) {
     return RL_OK;
 }
 
+int check_dist(const rl_dist* d, int32_t dtype, int64_t V, bool needed) {
+    if (!d->logits && !d->offsets) return needed ? fail(RL_ERR_ARG, "a distribution has neither logits nor support rows") : RL_OK;
+    if (d->n_rows < 0 || d->nnz < 0) return fail(RL_ERR_ARG, "negative size");
+    if (d->n_rows >= kMax31) return fail(RL_ERR_UNSUPPORTED, "n_rows too large");
+    if (d->logits) {
+        if (dtype != RL_DTYPE_F32 && dtype != RL_DTYPE_BF16 && dtype != RL_DTYPE_F16)
+            return fail(RL_ERR_UNSUPPORTED, "dtype must be fp32, bf16 or fp16");
+        if (!aligned(d->logits, dtype == RL_DTYPE_F32 ? 4 : 2)) return fail(RL_ERR_ARG, "logits not aligned to their type");
+        if (d->n_rows > 1 && d->row_stride < V) return fail(RL_ERR_ARG, "row_stride smaller than V");
+    }
+    if (d->offsets && d->nnz > 0 && (!d->ids || !d->logq)) return fail(RL_ERR_ARG, "ids/logq NULL with support rows");
+    if (d->logits && d->offsets && !d->replayed) return fail(RL_ERR_ARG, "replayed NULL with logits and support rows");
+    return RL_OK;
+}
+
+int check_verify_sizes(const rl_verify_args* a) {
+    if (!a) return fail(RL_ERR_ARG, "args is NULL");
+    if (a->R < 0 || a->T < 0 || a->V <= 0) return fail(RL_ERR_ARG, "negative or zero size");
+    if (a->V > kMaxVocab || a->R >= kMax31 || a->T >= kMax31) return fail(RL_ERR_UNSUPPORTED, "R, T or V too large");
+    const int rc = check_dist(&a->target, a->target_dtype, a->V, true);
+    return rc != RL_OK ? rc : check_dist(&a->draft, a->draft_dtype, a->V, false);
+}
+
 int check_distill(const rl_distill_args* a, const int32_t* dev_status, int pass) {
     if (!a || !dev_status) return fail(RL_ERR_ARG, "args/dev_status is NULL");
     if (a->N < 0 || a->V <= 0 || a->nnz < 0) return fail(RL_ERR_ARG, "negative or zero size");
@@ -172,6 +195,24 @@ int rl_sample(const rl_sample_args* a, void* ws, size_t ws_bytes, int32_t* dev_s
         return RL_OK;
     }
     return sample_impl(a, ws, dev_status, static_cast<cudaStream_t>(stream));
+}
+
+// ---- verification of drafts ------------------------------------------------------------
+size_t rl_verify_workspace_bytes(const rl_verify_args* a) { return check_verify_sizes(a) != RL_OK ? 0 : verify_ws_bytes(a); }
+
+int rl_verify(const rl_verify_args* a, void* ws, size_t ws_bytes, int32_t* dev_status, void* stream) {
+    int rc = check_verify_sizes(a);
+    if (rc != RL_OK) return rc;
+    if (!dev_status) return fail(RL_ERR_ARG, "dev_status is NULL");
+    if ((a->R > 0 && (!a->cu_q || !a->u_next || !a->accepted)) || (a->T > 0 && (!a->step_tokens || !a->u || !a->tokens)))
+        return fail(RL_ERR_ARG, "required pointer is NULL");
+    if (a->keep_lens && a->keep_lens != a->ctx_lens && overlap(a->keep_lens, a->R, a->ctx_lens, a->ctx_lens ? a->R : 0))
+        return fail(RL_ERR_ARG, "keep_lens shares memory with ctx_lens");
+    if (overlap(a->tokens, a->T, a->step_tokens, a->T)) return fail(RL_ERR_ARG, "tokens shares memory with step_tokens");
+    if (ws_bytes < verify_ws_bytes(a)) return fail(RL_ERR_WORKSPACE, "verification workspace too small");
+    if (a->T > 0 && (!ws || !aligned(ws, 16))) return fail(RL_ERR_ARG, "ws is NULL or not 16-byte aligned");
+    rc = check_device();
+    return rc != RL_OK ? rc : verify_impl(a, ws, dev_status, static_cast<cudaStream_t>(stream));
 }
 
 // ---- pages of a rollout's life ---------------------------------------------------------

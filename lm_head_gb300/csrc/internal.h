@@ -206,6 +206,8 @@ int prefix_attn_impl(const rl_prefix_attn_args* a, void* ws, int32_t* status, cu
 size_t sample_ws_bytes(int64_t N, int64_t V);
 int sample_impl(const rl_sample_args* a, void* ws, int32_t* status, cudaStream_t stream);
 int kv_append_impl(const rl_kv_append_args* a, int32_t* status, cudaStream_t stream);
+size_t verify_ws_bytes(const rl_verify_args* a);
+int verify_impl(const rl_verify_args* a, void* ws, int32_t* status, cudaStream_t stream);
 size_t page_release_ws_bytes(int64_t n_pages);
 int page_release_impl(const rl_page_release_args* a, void* ws, int32_t* status, cudaStream_t stream);
 size_t page_fork_ws_bytes(int64_t R, int64_t C);
