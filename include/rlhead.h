@@ -683,7 +683,7 @@ typedef struct rl_dist {
  * (RL_STATUS_NONFINITE, they count as -inf).  A target row without a token accepts nothing and sets RL_STATUS_EMPTY_ROW, y = -1 and
  * logq -inf if it is the last row looked at; a draft row without one sets it too. */
 typedef struct rl_verify_args {
-    int64_t R, T, V;                /* V <= 2^20 */
+    int64_t R, T, V;                /* R < 2^28, V <= 2^20 */
     const int32_t* cu_q;            /* device [R+1] */
     const int32_t* step_tokens;     /* device [T] */
     const float* u;                 /* device [T] in [0, 1) (a request's last is not used) */

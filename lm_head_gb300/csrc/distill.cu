@@ -88,19 +88,6 @@ struct Pack {
     }
 };
 
-RL_DEVINL FF ff_neg(FF a) { return {-a.hi, -a.lo}; }
-// e^x of a pair (-inf gives 0)
-RL_DEVINL FF exp_pair(FF x) {
-    const FF e = exp_ff(x.hi);
-    return fast_two_sum(e.hi, e.hi > 0.f ? fmaf(e.hi, x.lo, e.lo) : 0.f);
-}
-// a / b
-RL_DEVINL FF ff_div(FF a, FF b) {
-    const float q = a.hi / b.hi;
-    const FF p = ff_mul(b, {q, 0.f});
-    const FF r = ff_add(a, ff_neg(p));
-    return fast_two_sum(q, r.hi / b.hi);
-}
 RL_DEVINL FF warp_sum_ff(FF v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v = ff_add(v, {__shfl_xor_sync(0xffffffffu, v.hi, o), __shfl_xor_sync(0xffffffffu, v.lo, o)});
@@ -150,13 +137,9 @@ RL_DEVINL void block_max2(DistShared& s, float& a, float& b) {
     }
 }
 
-RL_DEVINL void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-RL_DEVINL void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 RL_DEVINL float2 cluster_read(const float2* mine, int rank) {
-    uint32_t at;
     float2 v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_addr(mine)), "r"(rank));
-    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(at) : "memory");
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(cluster_addr(mine, rank)) : "memory");
     return v;
 }
 RL_DEVINL void bulk_store(void* dst, const void* src, uint32_t bytes) {

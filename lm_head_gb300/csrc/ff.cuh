@@ -103,6 +103,20 @@ RL_DEVINL FF ln_pair(FF x) {
     return fast_two_sum(y, fmaf(-0.5f * d, d, d));
 }
 
+RL_DEVINL FF ff_neg(FF a) { return {-a.hi, -a.lo}; }
+// e^x of a pair (-inf gives 0)
+RL_DEVINL FF exp_pair(FF x) {
+    const FF e = exp_ff(x.hi);
+    return fast_two_sum(e.hi, e.hi > 0.f ? fmaf(e.hi, x.lo, e.lo) : 0.f);
+}
+// a / b
+RL_DEVINL FF ff_div(FF a, FF b) {
+    const float q = a.hi / b.hi;
+    const FF p = ff_mul(b, {q, 0.f});
+    const FF r = ff_add(a, ff_neg(p));
+    return fast_two_sum(q, r.hi / b.hi);
+}
+
 // ln t as a float-float pair (host): hi = the float nearest ln t, lo = the float nearest
 // the rest; -inf for t <= 0.
 inline FF ln_ff(double t) {

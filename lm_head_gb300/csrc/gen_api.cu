@@ -69,7 +69,7 @@ int check_dist(const rl_dist* d, int32_t dtype, int64_t V, bool needed) {
 int check_verify_sizes(const rl_verify_args* a) {
     if (!a) return fail(RL_ERR_ARG, "args is NULL");
     if (a->R < 0 || a->T < 0 || a->V <= 0) return fail(RL_ERR_ARG, "negative or zero size");
-    if (a->V > kMaxVocab || a->R >= kMax31 || a->T >= kMax31) return fail(RL_ERR_UNSUPPORTED, "R, T or V too large");
+    if (a->V > kMaxVocab || a->R >= (int64_t(1) << 28) || a->T >= kMax31) return fail(RL_ERR_UNSUPPORTED, "R, T or V too large");
     const int rc = check_dist(&a->target, a->target_dtype, a->V, true);
     return rc != RL_OK ? rc : check_dist(&a->draft, a->draft_dtype, a->V, false);
 }

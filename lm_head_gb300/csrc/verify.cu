@@ -1,47 +1,53 @@
 // Verification of drafted tokens against the target's probabilities.
 //
-//  rows_kernel     one block a row of logits: its largest logit and the sum of its weights
-//  request_kernel  one block a request: the accepted drafts, then the token drawn from what is left of the
-//                  target at the first that is not, or from its last row
+// An acceptance u q(x) < p(x) compares two numbers, and almost always they are further apart than
+// fp32 sums are wrong; the token after the accepted ones is decided by a cumulative sum over up to the
+// whole vocabulary, where fp32 sums would give another one every few hundred requests.  So
+//
+//  1. chunk_kernel     the only pass over all rows of logits: a warp per 4 KB, its largest logit and the sum of its
+//                      weights in fp32.  Rows that no request looks at (a draft's row behind its last draft) are left out.
+//  2. request_kernel   a cluster of blocks a request: every block puts the rows' totals together and compares; a comparison
+//                      nearer than the bound of the fp32 sums' error is taken again with sums that are good to 2^-36.  Then
+//                      the row of the new token, a slice of the vocabulary a block: the sums of its parts of 128 as
+//                      integers (float-pair weights, see weights.cuh) of the target's weights, of
+//                      the draft's where it has logits, and of what is left, max(p - q, 0); the cluster adds them up,
+//                      and the block in whose slice the random number falls scans it.
+//                      With a draft's support row only its few tokens' probabilities are taken off the target's parts.
+//                      A target's support row is drawn from by one block.
 #include <cfloat>
 #include <climits>
 #include <cmath>
-
-#include <cuda_fp16.h>
+#include <type_traits>
 
 #include "common.cuh"
+#include "ff.cuh"
 #include "internal.h"
+#include "weights.cuh"
 
 namespace rl {
 
+constexpr int kVerPart = 128;                  // logits of a part
 constexpr int kVerThreads = 512;
 constexpr int kVerWarps = kVerThreads / 32;
+constexpr int kChunkThreads = 256;
+constexpr int kChunkPacks = 8;                 // 16-byte loads of a lane: 4 KB a warp
+constexpr int kUsedRows = 32768;               // rows of a step whose use is looked up in shared memory
+constexpr float kPlainRef = 1900.f;            // |max log2(e) / T| up to which weights need no difference to the maximum
 
-struct VerRow {
-    float M;            // the row's largest logit (-inf: none)
-    int at;             // its first index
-    double S;           // sum of e^((z - M) / T)
-};
 struct VerSide {
     rl_dist d;
     int dtype;
-    VerRow* rec;        // [T] of the step's rows
+    int nc;             // chunks of a row
+    float2* part;       // [T, nc] largest logit, sum of e^((z - it) / T) (T = 0: bits of its first index)
 };
 struct VerArgs {
     rl_verify_args a;
     VerSide side[2];    // target, draft
     int32_t* status;
     bool sure;          // no draft distribution
+    int cs, per;        // blocks a request; parts of a block's slice
 };
 
-RL_DEVINL float logit_at(const rl_dist& d, int dtype, long long row, long long j) {
-    const long long i = row * d.row_stride + j;
-    float z;
-    if (dtype == RL_DTYPE_F32) z = static_cast<const float*>(d.logits)[i];
-    else if (dtype == RL_DTYPE_BF16) z = __bfloat162float(static_cast<const __nv_bfloat16*>(d.logits)[i]);
-    else z = __half2float(static_cast<const __half*>(d.logits)[i]);
-    return z;
-}
 // The row of the distribution that the step's row t has; -1 where there is none.
 RL_DEVINL long long row_of(const rl_dist& d, long long t, int& bits) {
     const long long r = d.rows ? d.rows[t] : t;
@@ -66,110 +72,370 @@ RL_DEVINL float unit_of(float u, int& bits) {
     bits |= RL_STATUS_KNOB;
     return u >= 1.f ? 1.f - 5.9604645e-8f : 0.f;
 }
+RL_DEVINL float logit_at(const rl_dist& d, int dtype, long long row, long long j) {      // NaN and +inf as -inf
+    const long long i = row * d.row_stride + j;
+    const float z = dtype == RL_DTYPE_F32   ? static_cast<const float*>(d.logits)[i]
+                    : dtype == RL_DTYPE_BF16 ? to_f(static_cast<const __nv_bfloat16*>(d.logits)[i])
+                                             : to_f(static_cast<const __half*>(d.logits)[i]);
+    return z < INFINITY ? z : -INFINITY;
+}
 
+// ---- 1. chunks ---------------------------------------------------------------------------
+// Places: element i of a row lies at place i + phase, so that 16-byte packs of places are aligned.
 template <typename T>
-RL_DEVINL T vblock_sum(T v, T* red) {
+RL_DEVINL float2 chunk_of(const T* row, int V, int chunk, float Tm, bool& bad) {
+    constexpr int E = 16 / sizeof(T);
+    const int lane = threadIdx.x & 31;
+    const int phase = static_cast<int>((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T));
+    const int i0 = (chunk * kChunkPacks * 32 + lane) * E - phase;
+    uint4 q[kChunkPacks];
+#pragma unroll
+    for (int k = 0; k < kChunkPacks; ++k) {
+        const int i = i0 + k * 32 * E;
+        if (i >= 0 && i + E <= V) {
+            q[k] = __ldcs(reinterpret_cast<const uint4*>(row + i));
+        } else {
+            T t[E];
+#pragma unroll
+            for (int j = 0; j < E; ++j) t[j] = i + j >= 0 && i + j < V ? row[i + j] : static_cast<T>(-INFINITY);
+            memcpy(&q[k], t, 16);
+        }
+    }
+    auto get = [&](int k, int j) -> float {
+        const uint32_t w = j < E / 4 * 1 ? q[k].x : j < E / 4 * 2 ? q[k].y : j < E / 4 * 3 ? q[k].z : q[k].w;
+        if constexpr (sizeof(T) == 4) return __uint_as_float(w);
+        else if constexpr (std::is_same<T, __nv_bfloat16>::value) return __uint_as_float((j & 1) ? w & 0xffff0000u : w << 16);
+        else return __half2float(__ushort_as_half(static_cast<unsigned short>((j & 1) ? w >> 16 : w & 0xffffu)));
+    };
+    auto largest = [&]() -> uint32_t {
+        float m = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < kChunkPacks; ++k)
+#pragma unroll
+            for (int j = 0; j < E; ++j) m = max_nan(m, get(k, j));
+        return __reduce_max_sync(0xffffffffu, key_of(m + 0.f));
+    };
+    uint32_t key = largest();
+    const bool odd = key >= 0xff800000u;             // NaN or +inf among them: they count as -inf
+    if (odd) {
+        bad = true;
+        float m = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < kChunkPacks; ++k)
+#pragma unroll
+            for (int j = 0; j < E; ++j) {
+                const float z = get(k, j);
+                m = fmaxf(m, z < INFINITY ? z : -INFINITY);
+            }
+        key = __reduce_max_sync(0xffffffffu, key_of(m + 0.f));
+    }
+    const float m = z_of(key);
+    if (!(m > -INFINITY)) return make_float2(m, 0.f);
+    if (Tm == 0.f) {
+        int at = INT_MAX;
+#pragma unroll
+        for (int k = kChunkPacks - 1; k >= 0; --k)
+#pragma unroll
+            for (int j = E - 1; j >= 0; --j)
+                if (get(k, j) == m) at = i0 + k * 32 * E + j;
+        return make_float2(m, __uint_as_float(__reduce_min_sync(0xffffffffu, static_cast<unsigned>(at))));
+    }
+    const float c = kLog2eHi / Tm;
+    float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < kChunkPacks; ++k)
+#pragma unroll
+        for (int j = 0; j < E; ++j) {
+            const float z = get(k, j);
+            const float e = exp2_approx((z - m) * c);
+            s[j & 3] += !odd || z < INFINITY ? e : 0.f;
+        }
+    return make_float2(m, warp_sum((s[0] + s[1]) + (s[2] + s[3])));
+}
+
+__global__ void __launch_bounds__(kChunkThreads, 3) chunk_kernel(const __grid_constant__ VerArgs g) {
+    __shared__ uint32_t used[2][kUsedRows / 32];
+    const rl_verify_args& a = g.a;
+    const int V = static_cast<int>(a.V);
+    for (long long t = static_cast<long long>(blockIdx.x) * kChunkThreads + threadIdx.x; t < a.T; t += static_cast<long long>(gridDim.x) * kChunkThreads) {
+        a.tokens[t] = -1;
+        if (a.logq) a.logq[t] = 0.f;
+    }
+    // the rows that requests look at
+    const bool known = a.T <= kUsedRows;
+    if (known) {
+        const int words = static_cast<int>((a.T + 31) / 32);
+        for (int i = threadIdx.x; i < words; i += kChunkThreads) used[0][i] = used[1][i] = 0;
+        __syncthreads();
+        for (long long r = threadIdx.x; r < a.R; r += kChunkThreads) {
+            const long long t0 = a.cu_q[r], t1 = a.cu_q[r + 1];
+            if (t0 < 0 || t1 < t0 || t1 > a.T) continue;
+            for (int t = static_cast<int>(t0); t < t1; ++t) {
+                atomicOr(&used[0][t >> 5], 1u << (t & 31));
+                if (t + 1 < t1) atomicOr(&used[1][t >> 5], 1u << (t & 31));
+            }
+        }
+        __syncthreads();
+    }
+    const long long warps = static_cast<long long>(gridDim.x) * (kChunkThreads / 32);
+    const long long first = a.T * g.side[0].nc, units = first + a.T * g.side[1].nc;
+    int bits = 0;
+    bool bad = false;
+    for (long long id = static_cast<long long>(blockIdx.x) * (kChunkThreads / 32) + (threadIdx.x >> 5); id < units; id += warps) {
+        const int side = id >= first ? 1 : 0;
+        const VerSide& s = g.side[side];
+        const long long x = side ? id - first : id, t = x / s.nc;
+        const int chunk = static_cast<int>(x - t * s.nc);
+        if (known && !((used[side][t >> 5] >> (t & 31)) & 1u)) continue;
+        int row_bits = 0;
+        const long long row = row_of(s.d, t, row_bits);
+        if (row < 0 || is_support(s.d, row)) continue;
+        const float Tm = temperature_of(s.d, row, bits);
+        float2 v;
+        if (s.dtype == RL_DTYPE_F32) v = chunk_of(static_cast<const float*>(s.d.logits) + row * s.d.row_stride, V, chunk, Tm, bad);
+        else if (s.dtype == RL_DTYPE_BF16) v = chunk_of(static_cast<const __nv_bfloat16*>(s.d.logits) + row * s.d.row_stride, V, chunk, Tm, bad);
+        else v = chunk_of(static_cast<const __half*>(s.d.logits) + row * s.d.row_stride, V, chunk, Tm, bad);
+        if ((threadIdx.x & 31) == 0) s.part[t * s.nc + chunk] = v;
+    }
+    if (bad) bits |= RL_STATUS_NONFINITE;
+    set_status(g.status, bits);
+    let_next_start();
+}
+
+// ---- 2. requests ---------------------------------------------------------------------------
+enum { kDistNone, kDistDense, kDistPoint, kDistSupport };
+
+// A row's distribution.
+struct VerRow {
+    int mode, dtype, at;            // kDistPoint: all of it on `at`
+    const rl_dist* d;
+    long long row, eb, ee;
+    float M, S;                     // largest logit, fp32 sum of e^((z - M) / T)
+    FF c;                           // log2(e) / T
+    bool plain, vec;                // weights are 2^(z c - R), else 2^((z - M) c - R) with R = 0
+    float R;
+    int prec;                       // their sums are in units of 2^-prec
+    unsigned long long total;       // ... the sum of all of them
+};
+
+struct VerShared {
+    float2 tab[2048];
+    unsigned long long red[kVerWarps];
+    unsigned long long xch[2];
+    VerRow row[2];
+    int res[kVerWarps];
+    float lp[kVerWarps];
+    int flag;
+    float lpx;
+    int token;
+    FF lam;                         // log2 of the draft's total over the target's, as they are counted
+    unsigned long long unit;
+};
+
+RL_DEVINL unsigned long long vblock_sum(unsigned long long v, unsigned long long* red) {
     v = warp_sum(v);
     __syncthreads();
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
     __syncthreads();
-    T s = red[0];
-    for (int w = 1; w < kVerWarps; ++w) s += red[w];
+    unsigned long long s = 0;
+#pragma unroll
+    for (int w = 0; w < kVerWarps; ++w) s += red[w];
     return s;
 }
-
-__global__ void __launch_bounds__(kVerThreads) rows_kernel(const VerArgs g) {
-    __shared__ double red[kVerWarps];
-    __shared__ unsigned long long redk[kVerWarps];
-    const long long t = blockIdx.x;
-    const VerSide& s = g.side[blockIdx.y];
-    const int V = static_cast<int>(g.a.V);
-    int bits = 0;
-    if (blockIdx.y == 0 && threadIdx.x == 0) {
-        g.a.tokens[t] = -1;
-        if (g.a.logq) g.a.logq[t] = 0.f;
-    }
-    if (!s.d.logits) return;
-    const long long row = row_of(s.d, t, bits);
-    if (row < 0 || is_support(s.d, row)) return;
-    const float T = temperature_of(s.d, row, bits);
-    unsigned long long best = 0;             // key of the logit, then the lower index
-    for (int j = threadIdx.x; j < V; j += kVerThreads) {
-        float z = logit_at(s.d, s.dtype, row, j);
-        if (!(z < INFINITY)) {
-            bits |= RL_STATUS_NONFINITE;
-            z = -INFINITY;
-        }
-        const uint32_t b = __float_as_uint(z + 0.f);
-        const uint32_t k = b ^ ((b >> 31) ? 0xffffffffu : 0x80000000u);
-        best = max(best, (static_cast<unsigned long long>(k) << 32) | static_cast<uint32_t>(~j));
-    }
+RL_DEVINL unsigned long long vblock_scan(unsigned long long v, unsigned long long* red) {      // exclusive
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    unsigned long long i = v;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
-    if ((threadIdx.x & 31) == 0) redk[threadIdx.x >> 5] = best;
+    for (int o = 1; o < 32; o <<= 1) {
+        const unsigned long long x = __shfl_up_sync(0xffffffffu, i, o);
+        if (lane >= o) i += x;
+    }
     __syncthreads();
-    for (int w = 0; w < kVerWarps; ++w) best = max(best, redk[w]);
-    const uint32_t k = static_cast<uint32_t>(best >> 32);
-    const float M = __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xffffffffu));
-    double S = 0.0;
-    if (M > -INFINITY && T > 0.f)
-        for (int j = threadIdx.x; j < V; j += kVerThreads) {
-            const float z = logit_at(s.d, s.dtype, row, j);
-            if (z < INFINITY && z > -INFINITY) S += exp((static_cast<double>(z) - M) / T);
-        }
-    S = vblock_sum(S, red);
-    if (threadIdx.x == 0) s.rec[t] = VerRow{M, static_cast<int>(~static_cast<uint32_t>(best)), S};
-    set_status(g.status, bits);
+    if (lane == 31) red[warp] = i;
+    __syncthreads();
+    unsigned long long p = 0;
+    for (int w = 0; w < warp; ++w) p += red[w];
+    return p + i - v;
+}
+// hi + lo (normalised, 0 <= it < 2) in units of 2^-k, k <= 60
+RL_DEVINL unsigned long long fixed_of(float hi, float lo, int k) {
+    if (!(hi > 0.f)) return 0ull;
+    const uint32_t b = __float_as_uint(hi);
+    const int sh = static_cast<int>(b >> 23) - 127 - 23 + k;
+    const unsigned long long m = (b & 0x7fffffu) | ((b >> 23) ? 0x800000u : 0u);
+    const unsigned long long w = sh >= 0 ? m << sh : sh > -25 ? (m + (1ull << (-sh - 1))) >> -sh : 0ull;
+    const long long v = static_cast<long long>(w) + __float2ll_rn(lo * power_of_2(k));
+    return v > 0 ? static_cast<unsigned long long>(v) : 0ull;
+}
+// The weight of a logit over 2^ref (as in VerRow) times 2^-lam, as a normalised pair.  ref + the row's R holds lam's part in
+// steps of 2^-11, lam_lo the rest; the weight is below 2.
+RL_DEVINL FF weight_of(float z, const VerRow& w, float ref, float lam_lo, const float2* tab) {
+    float x = z, xl = 0.f;
+    if (!w.plain) {
+        const FF d = two_sum(z, -w.M);
+        x = d.hi;
+        xl = d.lo;
+    }
+    const float magic = 6144.f - (w.R + ref);
+    const float t = fmaf(x, w.c.hi, magic);
+    float r = fmaf(x, w.c.hi, -__fsub_rn(t, magic));
+    r = fmaf(x, w.c.lo, r);
+    r = fmaf(xl, w.c.hi, r) - lam_lo;
+    const uint32_t tb = __float_as_uint(t);
+    const float2 q = tab[tb & 2047u];
+    const float hi = __uint_as_float(__float_as_uint(q.x) + (tb << 12));
+    // 2^r - 1 to the third power: with lam_lo |r| may be 2^-11
+    return fast_two_sum(hi, hi * fmaf(r, fmaf(r, fmaf(r, 0.05550410866482158f, 0.24022650695910072f), 0.69314718055994531f), q.y));
+}
+// The logit at which the exponent over 2^ref is e.
+RL_DEVINL float logit_of(const VerRow& w, float ref, float e) {
+    const float x = (ref + w.R + e) / w.c.hi;
+    return w.plain ? x : w.M + x;
 }
 
-// A row's distribution, as a block sees it.
-struct VerDist {
-    enum { kNone, kDense, kPoint, kSupport };
-    int mode, dtype, at;                // kPoint: all of it on `at`
-    const rl_dist* d;
-    long long row, eb, ee;
-    float M, T;
-    double S;
+struct Four {
+    uint32_t w[4];
 };
-RL_DEVINL VerDist dist_at(const VerArgs& g, int side, long long t, int& bits) {
-    VerDist x{};
-    const VerSide& s = g.side[side];
-    x.d = &s.d;
-    x.dtype = s.dtype;
-    if (side == 1 && g.sure) {
-        x.mode = VerDist::kPoint;
-        x.at = t + 1 < g.a.T ? g.a.step_tokens[t + 1] : -1;
-        return x;
+// Four logits of a part by a lane, as they lie in memory (past the row's end -inf), and as numbers.
+RL_DEVINL Four four_raw(const VerRow& r, int V, int i) {
+    Four f;
+    const long long base = r.row * r.d->row_stride;
+    if (r.dtype == RL_DTYPE_F32) {
+        const float* p = static_cast<const float*>(r.d->logits) + base;
+        if (r.vec && i + 4 <= V) {
+            const uint4 q = *reinterpret_cast<const uint4*>(p + i);
+            f.w[0] = q.x; f.w[1] = q.y; f.w[2] = q.z; f.w[3] = q.w;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) f.w[j] = i + j < V ? __float_as_uint(p[i + j]) : 0xff800000u;
+        }
+    } else {
+        const uint16_t* p = static_cast<const uint16_t*>(r.d->logits) + base;
+        if (r.vec && i + 4 <= V) {
+            const uint2 q = *reinterpret_cast<const uint2*>(p + i);
+            f.w[0] = q.x; f.w[1] = q.y;
+        } else {
+            const uint32_t none = r.dtype == RL_DTYPE_BF16 ? 0xff80u : 0xfc00u;
+            uint32_t h[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) h[j] = i + j < V ? p[i + j] : none;
+            f.w[0] = h[0] | h[1] << 16;
+            f.w[1] = h[2] | h[3] << 16;
+        }
+        f.w[2] = f.w[3] = 0;
     }
-    x.row = row_of(s.d, t, bits);
-    if (x.row < 0) return x;
-    if (is_support(s.d, x.row)) {
-        x.eb = s.d.offsets[x.row];
-        x.ee = s.d.offsets[x.row + 1];
-        if (x.eb < 0 || x.ee < x.eb || x.ee > s.d.nnz) {
-            bits |= RL_STATUS_OFFSETS;
+    return f;
+}
+RL_DEVINL void four_get(const Four& f, int dtype, float (&z)[4]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if (dtype == RL_DTYPE_F32) {
+            z[j] = __uint_as_float(f.w[j]);
+        } else {
+            const uint32_t w = f.w[j >> 1], h = (j & 1) ? w >> 16 : w & 0xffffu;
+            z[j] = dtype == RL_DTYPE_BF16 ? __uint_as_float(h << 16) : __half2float(__ushort_as_half(static_cast<unsigned short>(h)));
+        }
+        z[j] = (z[j] < INFINITY ? z[j] : -INFINITY) + 0.f;
+    }
+}
+
+struct Request {
+    const VerArgs& g;
+    VerShared& s;
+    unsigned long long* cs;       // [per] sums of the slice's parts
+    int V, tid, lane, warp, rank, p0, p1;      // its parts
+    int phase;
+
+    // The cluster's sum of v (the same in a block's threads), and the sum of the blocks before.
+    RL_DEVINL unsigned long long cluster_sum(unsigned long long v, unsigned long long& before) {
+        before = 0;
+        if (g.cs == 1) return v;
+        unsigned long long* slot = &s.xch[phase & 1];
+        ++phase;
+        if (tid == 0) *slot = v;
+        __syncthreads();
+        cluster_arrive();
+        cluster_wait();
+        unsigned long long total = 0;
+        for (int k = 0; k < g.cs; ++k) {
+            unsigned long long x;
+            asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(x) : "r"(cluster_addr(slot, k)) : "memory");
+            if (k < rank) before += x;
+            total += x;
+        }
+        return total;
+    }
+
+    // One warp: the step's row t on one side, its fp32 total put together.
+    RL_DEVINL VerRow row_at(int side, long long t, int& bits) {
+        VerRow x{};
+        const VerSide& sd = g.side[side];
+        x.d = &sd.d;
+        x.dtype = sd.dtype;
+        if (side == 1 && g.sure) {
+            x.mode = kDistPoint;
+            x.at = t + 1 < g.a.T ? g.a.step_tokens[t + 1] : -1;
             return x;
         }
-        x.mode = VerDist::kSupport;
+        x.row = row_of(sd.d, t, bits);
+        if (x.row < 0) return x;
+        if (is_support(sd.d, x.row)) {
+            x.eb = sd.d.offsets[x.row];
+            x.ee = sd.d.offsets[x.row + 1];
+            if (x.eb < 0 || x.ee < x.eb || x.ee > sd.d.nnz) {
+                bits |= RL_STATUS_OFFSETS;
+                return x;
+            }
+            x.mode = kDistSupport;
+            return x;
+        }
+        const float T = temperature_of(sd.d, x.row, bits);
+        const float2* part = sd.part + t * sd.nc;
+        float M = -INFINITY;
+        for (int i = lane; i < sd.nc; i += 32) M = fmaxf(M, part[i].x);
+        M = warp_max(M);
+        if (!(M > -INFINITY)) return x;
+        x.M = M;
+        if (T == 0.f) {
+            unsigned at = UINT_MAX;
+            for (int i = lane; i < sd.nc; i += 32)
+                if (part[i].x == M) at = min(at, __float_as_uint(part[i].y));
+            x.at = static_cast<int>(__reduce_min_sync(0xffffffffu, at));
+            x.mode = kDistPoint;
+            return x;
+        }
+        x.c = scale_of(T);
+        float S = 0.f;
+        for (int i = lane; i < sd.nc; i += 32) {
+            const float2 v = part[i];
+            if (v.x > -INFINITY) S += v.y * exp2f((v.x - M) * x.c.hi);
+        }
+        x.S = warp_sum(S);
+        x.mode = kDistDense;
+        const float pm = __fmul_rn(M, x.c.hi);
+        x.plain = fabsf(pm) < kPlainRef;
+        x.R = x.plain ? ceilf(pm) : 0.f;
+        // S < 2^e, the sum below 2^61 units
+        const int e = static_cast<int>(__float_as_uint(x.S * 1.01f) >> 23) - 126;
+        x.prec = min(54, 61 - max(e, 1));
+        const uintptr_t mask = x.dtype == RL_DTYPE_F32 ? 15 : 7, size = x.dtype == RL_DTYPE_F32 ? 4 : 2;
+        x.vec = ((reinterpret_cast<uintptr_t>(x.d->logits) + static_cast<uintptr_t>(x.row * x.d->row_stride) * size) & mask) == 0;
         return x;
     }
-    const VerRow r = s.rec[t];
-    if (!(r.M > -INFINITY)) return x;
-    x.T = temperature_of(s.d, x.row, bits);
-    x.M = r.M;
-    x.S = r.S;
-    x.at = r.at;
-    x.mode = x.T > 0.f ? VerDist::kDense : VerDist::kPoint;
-    return x;
-}
-// ln of the probability of token j (0 <= j < V); -inf: none
-RL_DEVINL double log_prob(const VerDist& x, int j, int& bits) {
-    if (x.mode == VerDist::kPoint) return j == x.at ? 0.0 : -INFINITY;
-    if (x.mode == VerDist::kDense) {
-        const float z = logit_at(*x.d, x.dtype, x.row, j);
-        return z < INFINITY && z > -INFINITY ? (static_cast<double>(z) - x.M) / x.T - log(x.S) : -INFINITY;
+    // log2 of token j's probability, to fp32 sums; -inf: none
+    RL_DEVINL float log2_prob(const VerRow& x, int j, int& bits) {
+        if (x.mode == kDistPoint) return j == x.at ? 0.f : -INFINITY;
+        if (x.mode == kDistDense) {
+            const float z = logit_at(*x.d, x.dtype, x.row, j);
+            if (!(z > -INFINITY)) return -INFINITY;
+            const FF d = two_sum(z, -x.M);
+            return fmaf(d.hi, x.c.hi, fmaf(d.lo, x.c.hi, d.hi * x.c.lo)) - log2f(x.S);
+        }
+        return support_at(x, j, bits) * kLog2e;
     }
-    if (x.mode == VerDist::kSupport) {
+    // a support row's log-probability of token j
+    RL_DEVINL float support_at(const VerRow& x, int j, int& bits) {
+        if (x.mode != kDistSupport) return -INFINITY;
         long long lo = x.eb, hi = x.ee;
         while (lo < hi) {
             const long long mid = (lo + hi) >> 1;
@@ -179,129 +445,452 @@ RL_DEVINL double log_prob(const VerDist& x, int j, int& bits) {
         if (lo < x.ee && x.d->ids[lo] == j) {
             const float q = x.d->logq[lo];
             if (!(q <= 1e-6f)) bits |= RL_STATUS_LOGQ;
-            return q < INFINITY ? static_cast<double>(q) : -INFINITY;
+            return q < INFINITY ? q : -INFINITY;
+        }
+        return -INFINITY;
+    }
+    // ln of token j's probability, in 64 bits (a dense row's total has been counted)
+    RL_DEVINL double ln_prob(const VerRow& x, int j, int& bits) {
+        if (x.mode == kDistPoint) return j == x.at ? 0.0 : -INFINITY;
+        if (x.mode == kDistDense) {
+            const float z = logit_at(*x.d, x.dtype, x.row, j);
+            if (!(z > -INFINITY) || x.total == 0) return -INFINITY;
+            const double c = static_cast<double>(x.c.hi) + static_cast<double>(x.c.lo);
+            const double e = x.plain ? z * c : (static_cast<double>(z) - x.M) * c;
+            return 0.69314718055994530942 * (e - x.R - (log2(static_cast<double>(x.total)) - x.prec));
+        }
+        return support_at(x, j, bits);
+    }
+    // Rows t of both sides into shared memory.
+    RL_DEVINL void load_rows(long long t, bool both, int& bits) {
+        __syncthreads();
+        if (warp < 2 && (warp == 0 || both)) {
+            const VerRow x = row_at(warp, t, bits);
+            if (lane == 0) s.row[warp] = x;
+        } else if (warp == 1 && lane == 0) {
+            s.row[1].mode = kDistNone;
+        }
+        __syncthreads();
+    }
+
+    // The parts' sums of the slice; kLeft: of what is left of the target beside the draft's logits, else of the weights of
+    // one side.  Each part is summed relative to its own largest weight.
+    template <bool kLeft>
+    RL_DEVINL unsigned long long sum_parts(int side) {
+        const VerRow w = s.row[side];
+        const VerRow o = s.row[1];
+        const float lam_hi = kLeft ? rintf(s.lam.hi * 2048.f) * (1.f / 2048.f) : 0.f, lam_lo = kLeft ? (s.lam.hi - lam_hi) + s.lam.lo : 0.f;
+        unsigned long long mine = 0;
+        Four next{}, next_o{};
+        if (p0 + warp < p1) {
+            next = four_raw(w, V, (p0 + warp) * kVerPart + lane * 4);
+            if (kLeft) next_o = four_raw(o, V, (p0 + warp) * kVerPart + lane * 4);
+        }
+#pragma unroll 1
+        for (int p = p0 + warp; p < p1; p += kVerWarps) {
+            float z[4], y[4];
+            four_get(next, w.dtype, z);
+            if (kLeft) four_get(next_o, o.dtype, y);
+            if (p + kVerWarps < p1) {
+                next = four_raw(w, V, (p + kVerWarps) * kVerPart + lane * 4);
+                if (kLeft) next_o = four_raw(o, V, (p + kVerWarps) * kVerPart + lane * 4);
+            }
+            const float m = z_of(__reduce_max_sync(0xffffffffu, key_of(fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3])))));
+            const float ex = w.plain ? fmaf(m, w.c.hi, -w.R) : (m - w.M) * w.c.hi;
+            unsigned long long sum = 0;
+            if (ex > -100.f) {                       // (also not for -inf: below, the part is nothing beside the row)
+                const float ref = fminf(ceilf(ex), 1.f);
+                const float zlow = fmaxf(logit_of(w, ref, -64.f), -FLT_MAX);
+                const float ylow = kLeft ? fmaxf(logit_of(o, ref + lam_hi, -64.f), -FLT_MAX) : 0.f, yhigh = kLeft ? logit_of(o, ref + lam_hi, 0.75f) : 0.f;
+                LaneSum acc;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    FF v = weight_of(fmaxf(z[j], zlow), w, ref, 0.f, s.tab);
+                    if (z[j] < zlow) v = {0.f, 0.f};
+                    if (kLeft) {
+                        FF q = weight_of(fminf(fmaxf(y[j], ylow), yhigh), o, ref + lam_hi, lam_lo, s.tab);
+                        if (y[j] < ylow) q = {0.f, 0.f};
+                        v = left_of(v, q);
+                    }
+                    acc.add(v.hi, v.lo);
+                }
+                const uint32_t top = acc.warp_top();
+                const int low = acc.warp_low();
+                const unsigned long long w50 = LaneSum::total(top, low);
+                const int sh = w.prec - 50 + static_cast<int>(ref);
+                sum = sh >= 0 ? w50 << sh : sh > -64 ? (w50 + (1ull << (-sh - 1))) >> -sh : 0ull;
+            }
+            if (lane == 0) cs[p - p0] = sum;
+            mine += sum;
+        }
+        mine = lane == 0 ? mine : 0;
+        return vblock_sum(mine, s.red);
+    }
+    // max(v - q, 0) of normalised pairs
+    static RL_DEVINL FF left_of(FF v, FF q) {
+        if (!(v.hi >= q.hi)) return {0.f, 0.f};
+        const float d = __fsub_rn(v.hi, q.hi);
+        const FF r = two_sum(d, __fadd_rn(__fsub_rn(__fsub_rn(v.hi, d), q.hi), __fsub_rn(v.lo, q.lo)));
+        return r.hi > 0.f ? r : FF{0.f, 0.f};
+    }
+    // Counts a dense row's total; returns the slice's (its parts stay in cs) and the sum of the slices before.
+    RL_DEVINL unsigned long long count_total(int side, unsigned long long& before) {
+        const unsigned long long mine = sum_parts<false>(side);
+        const unsigned long long t = cluster_sum(mine, before);
+        __syncthreads();
+        if (tid == 0) s.row[side].total = t;
+        __syncthreads();
+        return mine;
+    }
+
+    // The comparison of row t with 64-bit logs and counted totals (every block of the cluster comes to the same).
+    RL_DEVINL int decide(long long t, int x, float u, int& bits) {
+        load_rows(t, true, bits);
+        for (int side = 0; side < 2; ++side)
+            if (s.row[side].mode == kDistDense) {
+                unsigned long long before;
+                count_total(side, before);
+            }
+        if (tid == 0) {
+            const double lp = ln_prob(s.row[0], x, bits), lq = ln_prob(s.row[1], x, bits);
+            s.flag = static_cast<double>(u) * exp(lq) < exp(lp) ? 0 : 1;
+            s.lpx = static_cast<float>(lp);
+        }
+        __syncthreads();
+        return s.flag;
+    }
+
+    // The draft's weight of token j in the target's units (its rows' totals counted), for a draw from support or point rows.
+    RL_DEVINL FF prob_pair(const VerRow& x, int j, FF ln_total, int& bits) {
+        if (x.mode == kDistPoint) return {j == x.at ? 1.f : 0.f, 0.f};
+        if (x.mode == kDistDense) {
+            const float z = logit_at(*x.d, x.dtype, x.row, j);
+            if (!(z > -INFINITY)) return {0.f, 0.f};
+            const FF d = x.plain ? FF{z, 0.f} : two_sum(z, -x.M);
+            // e = d c - R in log2 units, then to natural ones less the total's log
+            FF e = ff_add(ff_mul(d, x.c), {-x.R, 0.f});
+            e = ff_add(ff_mul(e, {0.693147182464599609375f, -1.90465429995775e-09f}), ff_neg(ln_total));
+            return exp_pair(e);
+        }
+        const float q = support_at(x, j, bits);
+        return q > -INFINITY ? exp_ff(q) : FF{0.f, 0.f};
+    }
+    // ln of a counted total, in the unit 2^R (2^0) of its weights
+    static RL_DEVINL FF ln_of(unsigned long long total, int prec) {
+        const float th = __ull2float_rz(total);
+        const float tl = static_cast<float>(static_cast<long long>(total - static_cast<unsigned long long>(th)));
+        return ln_pair(fast_two_sum(th * power_of_2(-prec), tl * power_of_2(-prec)));
+    }
+
+    // A draw from a support row, by one block.  Sums in units of 2^-52.
+    RL_DEVINL void draw_support(long long t, float u, int& bits) {
+        const VerRow p = s.row[0], q = s.row[1];
+        const long long n = p.ee - p.eb;
+        const FF lq = q.mode == kDistDense ? ln_of(q.total, q.prec) : FF{0.f, 0.f};
+        bool whole = q.mode == kDistNone;
+        auto left = [&](long long i) -> unsigned long long {
+            const int j = p.d->ids[p.eb + i];
+            const float l = p.d->logq[p.eb + i];
+            if (j < 0 || j >= V) {
+                bits |= RL_STATUS_ID_RANGE;
+                return 0ull;
+            }
+            if (i > 0 && p.d->ids[p.eb + i - 1] >= j) bits |= RL_STATUS_ROW_ORDER;
+            if (!(l <= 1e-6f)) bits |= RL_STATUS_LOGQ;
+            if (!(l < INFINITY) || !(l > -INFINITY)) return 0ull;
+            FF v = exp_ff(l);
+            if (!whole) v = left_of(v, prob_pair(q, j, lq, bits));
+            return fixed_of(v.hi, v.lo, 52);
+        };
+        // a stretch of the row a thread
+        const long long per = (n + kVerThreads - 1) / kVerThreads, i0 = min(tid * per, n), i1 = min(i0 + per, n);
+        unsigned long long mine = 0, total = 0;
+        for (int tries = 0; tries < 2; ++tries) {
+            mine = 0;
+            for (long long i = i0; i < i1; ++i) mine += left(i);
+            total = vblock_sum(mine, s.red);
+            if (total > 0 || whole) break;
+            whole = true;
+        }
+        const unsigned long long before = vblock_scan(mine, s.red), target = fraction_of(u, total);
+        if (tid == 0) s.token = -1;
+        __syncthreads();
+        if (total > 0 && mine > 0 && before <= target && target < before + mine) {
+            unsigned long long c = before;
+            for (long long i = i0; i < i1; ++i) {
+                c += left(i);
+                if (c > target) {
+                    s.token = p.d->ids[p.eb + i];
+                    s.lpx = p.d->logq[p.eb + i];
+                    break;
+                }
+            }
+        }
+        __syncthreads();
+        if (tid == 0) finish(t, s.token, s.lpx, bits);
+    }
+    RL_DEVINL void finish(long long t, int token, float l, int& bits) {
+        if (token < 0) bits |= RL_STATUS_EMPTY_ROW;
+        g.a.tokens[t] = token;
+        if (g.a.logq) g.a.logq[t] = token < 0 ? -INFINITY : l;
+    }
+
+    // What is left of token j of a dense target, z its logit, in the target's units.
+    RL_DEVINL unsigned long long left_at(float z, float y, int j, bool whole, int& bits) {
+        const VerRow& p = s.row[0];
+        const VerRow& q = s.row[1];
+        const float zlow = fmaxf(logit_of(p, 0.f, -64.f), -FLT_MAX);
+        if (!(z >= zlow)) return 0ull;
+        FF v = weight_of(z, p, 0.f, 0.f, s.tab);
+        if (!whole && q.mode == kDistDense) {
+            const float lam_hi = rintf(s.lam.hi * 2048.f) * (1.f / 2048.f), lam_lo = (s.lam.hi - lam_hi) + s.lam.lo;
+            const float ylow = fmaxf(logit_of(q, lam_hi, -64.f), -FLT_MAX), yhigh = logit_of(q, lam_hi, 0.75f);
+            if (y >= ylow) v = left_of(v, weight_of(fminf(y, yhigh), q, lam_hi, lam_lo, s.tab));
+            return fixed_of(v.hi, v.lo, p.prec);
+        }
+        unsigned long long w = fixed_of(v.hi, v.lo, p.prec);
+        if (!whole && q.mode != kDistNone) {
+            const unsigned long long x = taken(j, w, q.mode == kDistPoint ? (j == q.at ? 0.f : -INFINITY) : support_at(q, j, bits));
+            w -= x;
+        }
+        return w;
+    }
+    // What a draft's probability e^lq takes off a weight w: the smaller of the two.
+    RL_DEVINL unsigned long long taken(int, unsigned long long w, float lq) {
+        if (!(lq > -INFINITY)) return 0ull;
+        const FF e = exp_ff(lq);
+        const double x = (static_cast<double>(e.hi) + static_cast<double>(e.lo)) * static_cast<double>(s.row[0].total);
+        return x >= static_cast<double>(w) ? w : static_cast<unsigned long long>(__double2ll_rn(x));
+    }
+
+    // A draw from a row of logits, by the cluster.
+    RL_DEVINL void draw_dense(long long t, float u, int& bits) {
+        const VerRow& p = s.row[0];
+        const VerRow& q = s.row[1];
+        bool whole = q.mode == kDistNone;
+        unsigned long long before;
+        if (q.mode == kDistDense) count_total(1, before);
+        unsigned long long mine = count_total(0, before), total = p.total;
+        if (q.mode == kDistDense) {
+            if (tid == 0) {
+                const double lam = (log2(static_cast<double>(q.total)) - q.prec) - (log2(static_cast<double>(p.total)) - p.prec);
+                s.lam.hi = static_cast<float>(lam);
+                s.lam.lo = static_cast<float>(lam - static_cast<double>(s.lam.hi));
+            }
+            __syncthreads();
+        }
+        for (int tries = 0; tries < 2; ++tries) {
+            if (!whole && q.mode == kDistDense) {
+                mine = sum_parts<true>(0);
+            } else {
+                if (tries > 0) mine = sum_parts<false>(0);
+                if (!whole) {
+                    // the draft's tokens in the slice, off their parts
+                    const long long n = q.mode == kDistPoint ? 1 : q.ee - q.eb;
+                    for (long long i = tid; i < n; i += kVerThreads) {
+                        const int j = q.mode == kDistPoint ? q.at : q.d->ids[q.eb + i];
+                        if (j < 0 || j >= V) {
+                            if (q.mode == kDistSupport) bits |= RL_STATUS_ID_RANGE;
+                            continue;
+                        }
+                        float lq = 0.f;
+                        if (q.mode == kDistSupport) {
+                            lq = q.d->logq[q.eb + i];
+                            if (!(lq <= 1e-6f)) bits |= RL_STATUS_LOGQ;
+                            if (!(lq < INFINITY)) lq = -INFINITY;
+                            if (i > 0 && q.d->ids[q.eb + i - 1] >= j) bits |= RL_STATUS_ROW_ORDER;
+                        }
+                        const int part = j / kVerPart;
+                        if (part < p0 || part >= p1) continue;
+                        const unsigned long long w = left_at(logit_at(*p.d, p.dtype, p.row, j), 0.f, j, true, bits);
+                        atomicAdd(&cs[part - p0], 0ull - taken(j, w, lq));
+                    }
+                    __syncthreads();
+                    // (a part's sum and its tokens' weights are rounded apart)
+                    unsigned long long v = 0;
+                    for (int i = tid; i < p1 - p0; i += kVerThreads) {
+                        if (static_cast<long long>(cs[i]) < 0) cs[i] = 0;
+                        v += cs[i];
+                    }
+                    mine = vblock_sum(v, s.red);
+                }
+            }
+            if (tries > 0 || !whole) total = cluster_sum(mine, before);
+            if (total > 0 || whole) {
+                const unsigned long long target = fraction_of(u, total);
+                if (total > 0 && before <= target && target - before < mine) search(t, target - before, whole, bits);
+                else if (total == 0 && rank == 0 && tid == 0) finish(t, -1, 0.f, bits);
+                break;
+            }
+            whole = true;
         }
     }
-    return -INFINITY;
-}
+    // The block in whose slice the number falls: its part, then its token.
+    RL_DEVINL void search(long long t, unsigned long long want, bool whole, int& bits) {
+        const int n = p1 - p0, per = (n + kVerThreads - 1) / kVerThreads;
+        unsigned long long v = 0;
+        __syncthreads();
+        for (int j = 0; j < per; ++j) v += tid * per + j < n ? cs[tid * per + j] : 0ull;
+        unsigned long long c = vblock_scan(v, s.red);
+        if (c <= want && want < c + v)
+            for (int j = 0; j < per; ++j) {
+                const unsigned long long x = cs[tid * per + j];
+                if (want < c + x) {
+                    s.token = p0 + tid * per + j;
+                    s.unit = want - c;
+                    break;
+                }
+                c += x;
+            }
+        __syncthreads();
+        if (warp != 0) return;
+        const int part = s.token, i0 = part * kVerPart + lane * 4;
+        const unsigned long long rest = s.unit;
+        const VerRow& p = s.row[0];
+        const VerRow& q = s.row[1];
+        float z[4], y[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        four_get(four_raw(p, V, i0), p.dtype, z);
+        if (!whole && q.mode == kDistDense) four_get(four_raw(q, V, i0), q.dtype, y);
+        unsigned long long w[4], mine = 0;
+        int last = -1, likely = -1;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            w[j] = z[j] > -INFINITY ? left_at(z[j], y[j], i0 + j, whole, bits) : 0ull;
+            mine += w[j];
+            if (w[j] > 0) last = j;
+            if (z[j] > -INFINITY) likely = j;
+        }
+        unsigned long long incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const unsigned long long x = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += x;
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, incl > rest), some = __ballot_sync(0xffffffffu, last >= 0),
+                       any = __ballot_sync(0xffffffffu, likely >= 0);
+        int at = last >= 0 ? last : likely;
+        int src;
+        if (hit) {
+            src = __ffs(hit) - 1;
+            unsigned long long c2 = incl - mine;
+            bool got = false;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                c2 += w[j];
+                if (!got && c2 > rest) {
+                    got = true;
+                    at = j;
+                }
+            }
+        } else {                // the number met the part's sum to the last place
+            src = 31 - __clz(some ? some : any | 1u);
+        }
+        if (lane == src) {
+            const int token = i0 + max(at, 0);
+            finish(t, token, static_cast<float>(ln_prob(p, token, bits)), bits);
+        }
+    }
+};
 
-__global__ void __launch_bounds__(kVerThreads) request_kernel(const VerArgs g) {
-    __shared__ double red[kVerWarps];
-    __shared__ int s_token;
+__global__ void __launch_bounds__(kVerThreads, 2) request_kernel(const __grid_constant__ VerArgs g) {
+    extern __shared__ __align__(16) uint8_t raw[];
+    VerShared& s = *reinterpret_cast<VerShared*>(raw);
     const rl_verify_args& a = g.a;
-    const long long r = blockIdx.x;
-    const int tid = threadIdx.x, V = static_cast<int>(a.V);
+    const long long r = blockIdx.x / static_cast<unsigned>(g.cs);
+    const int tid = threadIdx.x, V = static_cast<int>(a.V), rank = static_cast<int>(blockIdx.x - r * g.cs);
+    const int ns = (V + kVerPart - 1) / kVerPart;
+    Request q{g, s, reinterpret_cast<unsigned long long*>(raw + sizeof(VerShared)), V, tid, tid & 31, tid >> 5, rank, min(rank * g.per, ns),
+              min((rank + 1) * g.per, ns), 0};
+    fill_table(s.tab, tid, kVerThreads);
     int bits = 0;
+    wait_for_previous();
     long long t0 = a.cu_q[r], t1 = a.cu_q[r + 1];
     if (t0 < 0 || t1 < t0 || t1 > a.T) {
         bits |= RL_STATUS_LENGTHS;
         t0 = t1 = 0;
     }
     long long t = t0;
-    for (; t + 1 < t1; ++t) {
-        const int x = a.step_tokens[t + 1];
-        const VerDist p = dist_at(g, 0, t, bits), q = dist_at(g, 1, t, bits);
-        if (p.mode == VerDist::kNone || q.mode == VerDist::kNone) bits |= RL_STATUS_EMPTY_ROW;
-        if (x < 0 || x >= V) {
-            bits |= RL_STATUS_ID_RANGE;
-            break;
+    bool going = t1 > t0;
+    while (going && t + 1 < t1) {
+        // a row a warp
+        const long long mine = t + q.warp;
+        __syncthreads();
+        if (mine + 1 < t1) {
+            int rb = 0;
+            const int x = a.step_tokens[mine + 1];
+            const VerRow p = q.row_at(0, mine, rb), d = q.row_at(1, mine, rb);
+            int res = 1;
+            float lp = -INFINITY;
+            if (p.mode == kDistNone || (d.mode == kDistNone)) rb |= RL_STATUS_EMPTY_ROW;
+            if (x < 0 || x >= V) {
+                rb |= RL_STATUS_ID_RANGE;
+            } else {
+                lp = q.log2_prob(p, x, rb);
+                const float lq = q.log2_prob(d, x, rb), lu = log2f(unit_of(a.u[mine], rb)) + lq;
+                // The bound of the difference's error: two totals of fp32 exponentials (2^-22 each, arguments' roundings, 24 additions)
+                // and the logs' own roundings
+                const float bound = 0x1p-15f + 0x1p-21f * (fabsf(lp) + fabsf(lu));
+                if (lp == -INFINITY) res = 1;
+                else if (lu == -INFINITY) res = 0;
+                else res = lu < lp - bound ? 0 : lu > lp + bound ? 1 : 2;
+            }
+            if (q.lane == 0) {
+                s.res[q.warp] = res | rb << 2;
+                s.lp[q.warp] = lp * kLn2;
+            }
         }
-        const double lp = log_prob(p, x, bits), lq = log_prob(q, x, bits);
-        const float u = unit_of(a.u[t], bits);
-        if (!(static_cast<double>(u) * exp(lq) < exp(lp))) break;
-        if (tid == 0) {
-            a.tokens[t] = x;
-            if (a.logq) a.logq[t] = static_cast<float>(lp);
+        __syncthreads();
+        const int n = static_cast<int>(min(static_cast<long long>(kVerWarps), t1 - 1 - t));
+        int k = 0;
+        for (; k < n; ++k) {
+            const int x = a.step_tokens[t + k + 1];
+            int res = s.res[k] & 3;
+            float l = s.lp[k];
+            bits |= s.res[k] >> 2;
+            if (res == 2) {
+                int none = 0;
+                res = q.decide(t + k, x, unit_of(a.u[t + k], none), none);
+                l = s.lpx;
+            }
+            if (res != 0) {
+                going = false;
+                break;
+            }
+            if (rank == 0 && tid == 0) {
+                a.tokens[t + k] = x;
+                if (a.logq) a.logq[t + k] = l;
+            }
         }
+        t += k;
     }
-    const long long accepted = t - t0;
-    if (tid == 0) {
-        a.accepted[r] = static_cast<int>(accepted);
-        if (a.keep_lens) a.keep_lens[r] = (a.ctx_lens ? a.ctx_lens[r] : 0) + static_cast<int>(t1 > t0 ? accepted + 1 : 0);
+    if (rank == 0 && tid == 0) {
+        a.accepted[r] = static_cast<int>(t - t0);
+        if (a.keep_lens) a.keep_lens[r] = (a.ctx_lens ? a.ctx_lens[r] : 0) + static_cast<int>(t1 > t0 ? t - t0 + 1 : 0);
     }
     if (t1 > t0) {
-        const bool refused = t + 1 < t1;
-        const VerDist p = dist_at(g, 0, t, bits);
-        VerDist q{};
-        if (refused) q = dist_at(g, 1, t, bits);
         const float u = unit_of(a.u_next[r], bits);
-        const bool listed = p.mode == VerDist::kSupport;
-        const long long n = listed ? p.ee - p.eb : V;
-        auto token = [&](long long i) -> int { return listed ? p.d->ids[p.eb + i] : static_cast<int>(i); };
-        // what is left of the i-th token; with `whole` all of it
-        auto left = [&](long long i, bool whole) -> double {
-            const int j = token(i);
-            if (j < 0 || j >= V) {
-                bits |= RL_STATUS_ID_RANGE;
-                return 0.0;
-            }
-            double lp;
-            if (listed) {
-                const float l = p.d->logq[p.eb + i];
-                if (!(l <= 1e-6f)) bits |= RL_STATUS_LOGQ;
-                if (i > 0 && p.d->ids[p.eb + i - 1] >= j) bits |= RL_STATUS_ROW_ORDER;
-                lp = l < INFINITY ? static_cast<double>(l) : -INFINITY;
-            } else {
-                lp = log_prob(p, j, bits);
-            }
-            const double v = exp(lp) - (whole ? 0.0 : exp(log_prob(q, j, bits)));
-            return v > 0.0 ? v : 0.0;
-        };
-        bool whole = q.mode == VerDist::kNone;
-        double total = 0.0;
-        if (p.mode != VerDist::kNone) {
-            for (int pass = 0; pass < 2; ++pass) {
-                double v = 0.0;
-                for (long long i = tid; i < n; i += kVerThreads) v += left(i, whole);
-                total = vblock_sum(v, red);
-                if (total > 0.0 || whole) break;
-                whole = true;
-            }
-        }
-        if (tid == 0) s_token = -1;
-        __syncthreads();
-        if (total > 0.0) {
-            const double target = static_cast<double>(u) * total;
-            double before = 0.0;
-            for (long long i0 = 0; i0 < n; i0 += kVerThreads) {
-                const long long i = i0 + tid;
-                const double v = i < n ? left(i, whole) : 0.0;
-                double c = v;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const double y = __shfl_up_sync(0xffffffffu, c, o);
-                    if ((tid & 31) >= o) c += y;
-                }
-                __syncthreads();
-                if ((tid & 31) == 31) red[tid >> 5] = c;
-                __syncthreads();
-                double base = before;
-                for (int w = 0; w < kVerWarps; ++w) {
-                    if (w < (tid >> 5)) base += red[w];
-                    before += red[w];
-                }
-                // (the last token with anything left, where rounding keeps the sum below the target)
-                if (v > 0.0 && base + c - v <= target) atomicMax(&s_token, static_cast<int>(i));
-            }
-            __syncthreads();
-        }
-        if (tid == 0) {
-            const int i = s_token;
-            int y = -1;
-            float l = -INFINITY;
-            if (i >= 0) {
-                y = token(i);
-                l = static_cast<float>(listed ? static_cast<double>(p.d->logq[p.eb + i]) : log_prob(p, y, bits));
-            } else {
-                bits |= RL_STATUS_EMPTY_ROW;
-            }
-            a.tokens[t] = y;
-            if (a.logq) a.logq[t] = l;
+        q.load_rows(t, t + 1 < t1, bits);
+        const VerRow& p = s.row[0];
+        if (p.mode == kDistDense) {
+            q.draw_dense(t, u, bits);
+        } else if (p.mode == kDistSupport) {
+            unsigned long long before;
+            if (s.row[1].mode == kDistDense) q.count_total(1, before);
+            if (rank == 0) q.draw_support(t, u, bits);
+        } else if (rank == 0 && tid == 0) {
+            // all of the target on one token: it is what is left, or what there is
+            q.finish(t, p.mode == kDistPoint ? p.at : -1, 0.f, bits);
         }
     }
     set_status(g.status, bits);
+    __syncthreads();
+    if (g.cs > 1) {                             // nobody leaves while its sums may be read
+        cluster_arrive();
+        cluster_wait();
+    }
 }
 
+// ---- host ------------------------------------------------------------------------------------
 static VerArgs verify_view(void* ws, const rl_verify_args* a, int32_t* status, size_t* bytes) {
     VerArgs g{};
     g.a = *a;
@@ -313,7 +902,11 @@ static VerArgs verify_view(void* ws, const rl_verify_args* a, int32_t* status, s
     g.side[1].dtype = a->draft_dtype;
     Carve cv(ws);
     for (auto& s : g.side)
-        if (s.d.logits) s.rec = cv.take<VerRow>(static_cast<size_t>(a->T));
+        if (s.d.logits) {
+            const int64_t e = s.dtype == RL_DTYPE_F32 ? 4 : 8, chunk = kChunkPacks * 32 * e;
+            s.nc = static_cast<int>((a->V + e - 1 + chunk - 1) / chunk);
+            s.part = cv.take<float2>(static_cast<size_t>(a->T) * s.nc);
+        }
     if (bytes) *bytes = align_up(cv.off, 256);
     return g;
 }
@@ -325,15 +918,45 @@ size_t verify_ws_bytes(const rl_verify_args* a) {
 }
 
 int verify_impl(const rl_verify_args* a, void* ws, int32_t* status, cudaStream_t stream) {
-    const VerArgs g = verify_view(ws, a, status, nullptr);
+    VerArgs g = verify_view(ws, a, status, nullptr);
     ProfScope prof(RL_PROF_OTHER, stream);
     int launches = 0;
     if (a->T > 0) {
-        rows_kernel<<<dim3(static_cast<unsigned>(a->T), g.side[1].d.logits ? 2u : 1u, 1), kVerThreads, 0, stream>>>(g);
+        const long long units = a->T * (g.side[0].nc + g.side[1].nc), fill = (a->T + kChunkThreads - 1) / kChunkThreads;
+        long long blocks = (units + kChunkThreads / 32 - 1) / (kChunkThreads / 32);
+        if (blocks < fill) blocks = fill;
+        const long long cap = 3ll * num_sms();
+        if (blocks > cap) blocks = cap;
+        chunk_kernel<<<static_cast<unsigned>(blocks), kChunkThreads, 0, stream>>>(g);
         ++launches;
     }
     if (a->R > 0) {
-        request_kernel<<<static_cast<unsigned>(a->R), kVerThreads, 0, stream>>>(g);
+        // a block's slice of the vocabulary: at least 64 parts of 128
+        const int ns = static_cast<int>((a->V + kVerPart - 1) / kVerPart);
+        g.cs = 1;
+        while (g.cs < 8 && ns > 64 * g.cs) g.cs *= 2;
+        g.per = (ns + g.cs - 1) / g.cs;
+        if (!a->target.logits && !a->draft.logits) {
+            g.cs = 1;
+            g.per = 0;
+        }
+        const size_t smem = sizeof(VerShared) + static_cast<size_t>(g.per) * 8;
+        static std::atomic<uint64_t> done{0};
+        if (!allow_smem(request_kernel, static_cast<int>(sizeof(VerShared) + (size_t(1) << 20) / kVerPart * 8), done)) return RL_ERR_CUDA;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(static_cast<unsigned>(a->R * g.cs), 1, 1);
+        cfg.blockDim = dim3(kVerThreads, 1, 1);
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = stream;
+        cudaLaunchAttribute attr[2];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = launches > 0 ? 1 : 0;
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = static_cast<unsigned>(g.cs);
+        attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 2;
+        if (cudaLaunchKernelEx(&cfg, request_kernel, g) != cudaSuccess) return RL_ERR_CUDA;
         ++launches;
     }
     count_launch(launches);

@@ -24,7 +24,7 @@ def test_refusals(lib):  # noqa: F811
     both = [(k, v, w) for k, v, w in (("n_rows", -1, ARG), ("nnz", -1, ARG), ("n_rows", 1 << 31, UNS), ("row_stride", 999, ARG),
                                       ("ids", None, ARG), ("logq", None, ARG), ("replayed", None, ARG), ("logits", FAKE + 1, ARG))]
     changes = [({s + k: v}, w) for s in ("target_", "draft_") for k, v, w in both]
-    changes += [(dict(R=-1), ARG), (dict(T=-1), ARG), (dict(V=0), ARG), (dict(V=(1 << 20) + 1), UNS), (dict(R=1 << 31), UNS),
+    changes += [(dict(R=-1), ARG), (dict(T=-1), ARG), (dict(V=0), ARG), (dict(V=(1 << 20) + 1), UNS), (dict(R=1 << 28), UNS),
                 (dict(T=1 << 31), UNS), (dict(target_dtype=3), UNS), (dict(draft_dtype=-1), UNS),
                 (dict(target_logits=None, target_offsets=None), ARG), (dict(cu_q=None), ARG), (dict(step_tokens=None), ARG),
                 (dict(u=None), ARG), (dict(u_next=None), ARG), (dict(tokens=None), ARG), (dict(accepted=None), ARG),
