@@ -86,56 +86,60 @@ struct Pack {
         memcpy(&q, t, 16);
         *static_cast<uint4*>(p) = q;
     }
+    // the largest that is a number (16-bit types two at a time)
+    RL_DEVINL float largest() const {
+        if constexpr (sizeof(T) == 4) {
+            return fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
+        } else if constexpr (std::is_same<T, __half>::value) {
+            __half2 h[4];
+            memcpy(h, t, 16);
+            const __half2 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+            return fmaxf(__low2float(m), __high2float(m));
+        } else {
+            __nv_bfloat162 h[4];
+            memcpy(h, t, 16);
+            const __nv_bfloat162 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+            return fmaxf(__low2float(m), __high2float(m));
+        }
+    }
+    RL_DEVINL void put(const float (&x)[E]) {
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int j = 0; j < E; ++j) t[j] = x[j];
+        } else {
+#pragma unroll
+            for (int j = 0; j < E; j += 2) {
+                if constexpr (std::is_same<T, __half>::value) {
+                    const __half2 h = __floats2half2_rn(x[j], x[j + 1]);
+                    memcpy(t + j, &h, 4);
+                } else {
+                    const __nv_bfloat162 h = __floats2bfloat162_rn(x[j], x[j + 1]);
+                    memcpy(t + j, &h, 4);
+                }
+            }
+        }
+    }
 };
 
+// (low parts are added up as they are, and the pair put in order at the end)
 RL_DEVINL FF warp_sum_ff(FF v) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v = ff_add(v, {__shfl_xor_sync(0xffffffffu, v.hi, o), __shfl_xor_sync(0xffffffffu, v.lo, o)});
-    return v;
+    for (int o = 16; o > 0; o >>= 1) {
+        const FF x = two_sum(v.hi, __shfl_xor_sync(0xffffffffu, v.hi, o));
+        v = {x.hi, x.lo + (v.lo + __shfl_xor_sync(0xffffffffu, v.lo, o))};
+    }
+    return fast_two_sum(v.hi, v.lo);
 }
 
 struct DistShared {
     uint64_t bar;
-    float2 part;                 // (maximum, sum) of the block's slice without the support
-    FF red[kDistWarps][2];
-    float redf[kDistWarps][2];
+    float2 part[kDistWarps];     // (maximum, sum) of each warp's stretch of the slice, without the support
+    float4 sup[kDistWarps];      // of each support warp: largest logit, sum relative to it, the same of the teacher's
+    FF sum[kDistWarps][2];       // pairs to be added up over the support warps
+    FF t0;                       // the teacher's probability of the rest
+    float A[kDistWarps];
+    float M, rest, total, held;
 };
-
-// Block sums of two pairs, in a fixed order; every thread gets them.
-RL_DEVINL void block_sum2(DistShared& s, FF& a, FF& b) {
-    a = warp_sum_ff(a);
-    b = warp_sum_ff(b);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) {
-        s.red[threadIdx.x >> 5][0] = a;
-        s.red[threadIdx.x >> 5][1] = b;
-    }
-    __syncthreads();
-    a = s.red[0][0];
-    b = s.red[0][1];
-#pragma unroll
-    for (int w = 1; w < kDistWarps; ++w) {
-        a = ff_add(a, s.red[w][0]);
-        b = ff_add(b, s.red[w][1]);
-    }
-}
-RL_DEVINL void block_max2(DistShared& s, float& a, float& b) {
-    a = warp_max(a);
-    b = warp_max(b);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) {
-        s.redf[threadIdx.x >> 5][0] = a;
-        s.redf[threadIdx.x >> 5][1] = b;
-    }
-    __syncthreads();
-    a = s.redf[0][0];
-    b = s.redf[0][1];
-#pragma unroll
-    for (int w = 1; w < kDistWarps; ++w) {
-        a = fmaxf(a, s.redf[w][0]);
-        b = fmaxf(b, s.redf[w][1]);
-    }
-}
 
 RL_DEVINL float2 cluster_read(const float2* mine, int rank) {
     float2 v;
@@ -188,13 +192,32 @@ RL_DEVINL Term term_of(int kind, float beta, FF t, FF lt, FF P, FF lp) {
     return r;
 }
 
+// P g of an outcome in fp32, for gradients.
+RL_DEVINL float slope_of(int kind, float beta, float t, float lt, float P, float lp) {
+    if (kind == RL_DISTILL_FORWARD) return -t;
+    if (lp == -INFINITY) return 0.f;
+    if (kind == RL_DISTILL_REVERSE) return P * (lp - lt);
+    const float a = 1.f - beta;
+    return a * P * (lp - logf(fmaf(beta, t, a * P)));
+}
+// Sum of v over the first n warps' threads (they alone call it), as a pair in every lane.
+RL_DEVINL FF support_sum(DistShared& s, FF v, int which, int n) {
+    v = warp_sum_ff(v);
+    if (n == 1) return v;
+    if ((threadIdx.x & 31) == 0) s.sum[threadIdx.x >> 5][which] = v;
+    asm volatile("bar.sync 1, %0;" ::"r"(n * 32) : "memory");
+    v = s.sum[0][which];
+    for (int w = 1; w < n; ++w) v = ff_add(v, s.sum[w][which]);
+    return v;
+}
+
 template <typename T>
-__global__ void __launch_bounds__(kDistThreads) distill_kernel(const DistArgs p, const DistSaved sv) {
+__global__ void __launch_bounds__(kDistThreads, 4) distill_kernel(const __grid_constant__ DistArgs p, const DistSaved sv) {
     extern __shared__ __align__(128) uint8_t raw[];
     __shared__ DistShared s;
     const rl_distill_args& a = p.a;
     constexpr int E = Pack<T>::E;
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const long long row = blockIdx.x / static_cast<unsigned>(p.cs);
     const int rank = static_cast<int>(blockIdx.x - row * p.cs);
     const int V = static_cast<int>(a.V);
@@ -211,12 +234,6 @@ __global__ void __launch_bounds__(kDistThreads) distill_kernel(const DistArgs p,
     T* buf = reinterpret_cast<T*>(raw);
     int bits = 0;
 
-    long long eb = a.offsets[row], ee = a.offsets[row + 1];
-    if (eb < 0 || ee < eb || ee > a.nnz) {
-        bits |= RL_STATUS_OFFSETS;
-        eb = ee = 0;
-    }
-    const float w = a.dloss && p.grad ? a.dloss[row] : 0.f;
     if (tid == 0) {
         mbar_init(&s.bar, 1);
         fence_mbar_init();
@@ -233,7 +250,15 @@ __global__ void __launch_bounds__(kDistThreads) distill_kernel(const DistArgs p,
     for (int q = tid; q < lead; q += kDistThreads) edge(q);
     for (int q = trail + tid; q < packs * E; q += kDistThreads) edge(q);
 
-    // ---- the support, while the slice is on its way
+    // ---- the support, while the slice is on its way: by as few warps as hold it, the same in every block of the cluster
+    long long eb = a.offsets[row], ee = a.offsets[row + 1];
+    if (eb < 0 || ee < eb || ee > a.nnz) {
+        bits |= RL_STATUS_OFFSETS;
+        eb = ee = 0;
+    }
+    const float w = a.dloss && p.grad ? a.dloss[row] : 0.f;
+    const int nw = static_cast<int>(min(static_cast<long long>(kDistWarps), (ee - eb + 31) / 32)), stride = nw * 32;
+    const bool mine = warp < nw;
     auto entry_at = [&](long long e) -> Entry {
         Entry x;
         x.id = a.ids[e];
@@ -242,192 +267,299 @@ __global__ void __launch_bounds__(kDistThreads) distill_kernel(const DistArgs p,
         x.z = x.in ? to_f32(z[x.id]) : -INFINITY;
         return x;
     };
-    Entry first{-1, -INFINITY, 0.f, false};
-    float mS = -INFINITY, mT = -INFINITY;
-    for (long long e = eb + tid; e < ee; e += kDistThreads) {
-        const Entry x = entry_at(e);
-        if (e == eb + tid) first = x;
-        if (x.id < 0 || x.id >= V) bits |= RL_STATUS_ID_RANGE;
-        if (!(x.lq < INFINITY) || (a.tail && x.lq > 1e-6f)) bits |= RL_STATUS_LOGQ;
-        if (e > eb && x.id <= a.ids[e - 1]) bits |= RL_STATUS_ROW_ORDER;
-        if (x.in) {
-            mS = fmaxf(mS, x.z);
-            mT = fmaxf(mT, x.lq);
-        }
-    }
-    block_max2(s, mS, mT);
-    const bool any = mT > -INFINITY;             // the row has a teacher
-    // f(entry, its index) for the entries that count; the thread's first is in registers
+    Entry first{-1, -INFINITY, 0.f, false};      // the thread's first entry stays in registers
+    // f(entry, its index) for the support warps' entries that count
     auto each = [&](auto f) {
-        for (long long e = eb + tid; e < ee; e += kDistThreads) {
+        for (long long e = eb + tid; e < ee; e += stride) {
             const Entry x = e == eb + tid ? first : entry_at(e);
             if (x.in) f(x, e);
         }
     };
-    // (z - m) / T
-    auto scaled = [&](float v, float m) -> FF { return v == -INFINITY ? FF{-INFINITY, 0.f} : ff_mul(two_sum(v, -m), p.inv_t); };
-    FF wS = {0.f, 0.f}, wT = {0.f, 0.f};
-    if (any) {
+    FF wT = {0.f, 0.f};                          // tail: the teacher's probabilities of the support
+    if (mine) {
+        float mS = -INFINITY, mT = -INFINITY;
+        for (long long e = eb + tid; e < ee; e += stride) {
+            const Entry x = entry_at(e);
+            if (e == eb + tid) first = x;
+            if (x.id < 0 || x.id >= V) bits |= RL_STATUS_ID_RANGE;
+            if (!(x.lq < INFINITY) || (a.tail && x.lq > 1e-6f)) bits |= RL_STATUS_LOGQ;
+            if (e > eb && x.id <= a.ids[e - 1]) bits |= RL_STATUS_ROW_ORDER;
+            if (x.in) {
+                mS = fmaxf(mS, x.z);
+                mT = fmaxf(mT, x.lq);
+                if (a.tail) wT = ff_add(wT, exp_ff(x.lq));
+            }
+        }
+        mS = warp_max(mS);
+        mT = warp_max(mT);
+        float sS = 0.f, sT = 0.f;
         each([&](const Entry& x, long long) {
-            if (mS > -INFINITY) wS = ff_add(wS, exp_pair(scaled(x.z, mS)));
-            wT = ff_add(wT, a.tail ? exp_ff(x.lq) : exp_pair(scaled(x.lq, mT)));
+            sS += x.z == -INFINITY ? 0.f : exp2f((x.z - mS) * p.c);
+            sT += exp2f((x.lq - mT) * p.c);
         });
-        block_sum2(s, wS, wT);
+        sS = warp_sum(sS);
+        sT = warp_sum(sT);
+        if (lane == 0) s.sup[warp] = make_float4(mS, sS, mT, sT);
     }
-    if (!mbar_wait(&s.bar, 0, p.status, p.wait_ns)) mbar_wait(&s.bar, 0, p.status);   // (the copy lands before the block goes on)
     __syncthreads();
-    // ---- the rest of the slice
-    if (any)
-        for (long long e = eb + tid; e < ee; e += kDistThreads) {
+    float mS = -INFINITY, mT = -INFINITY;
+    for (int k = 0; k < nw; ++k) {
+        mS = fmaxf(mS, s.sup[k].x);
+        mT = fmaxf(mT, s.sup[k].z);
+    }
+    const bool any = mT > -INFINITY;             // the row has a teacher
+    if (mine && a.tail) wT = support_sum(s, wT, 0, nw);
+    if (!mbar_wait(&s.bar, 0, p.status, p.wait_ns)) mbar_wait(&s.bar, 0, p.status);   // (the copy lands before the block goes on)
+    // ---- the rest of the slice: the support out of it, then each warp's maximum and sum
+    if (mine)
+        for (long long e = eb + tid; e < ee; e += stride) {
             const Entry x = e == eb + tid ? first : entry_at(e);
             if (x.in && x.id >= i0 && x.id < i1) buf[x.id - i0 + l0] = from_f32<T>(-INFINITY);
         }
     __syncthreads();
-    float m = -INFINITY, unused = 0.f;
-    for (int k = tid; k < packs; k += kDistThreads) {
-        Pack<T> v;
-        v.load(buf + k * E);
-#pragma unroll
-        for (int j = 0; j < E; ++j) m = fmaxf(m, to_f32(v.t[j]));
-    }
-    block_max2(s, m, unused);
-    float sum[4] = {0.f, 0.f, 0.f, 0.f};
-    const float mc = m > -INFINITY ? m : 0.f;
-    for (int k = tid; k < packs; k += kDistThreads) {
-        Pack<T> v;
-        v.load(buf + k * E);
-#pragma unroll
-        for (int j = 0; j < E; ++j) sum[j & 3] += exp2_approx((to_f32(v.t[j]) - mc) * p.c);
-    }
     {
-        FF t = ff_add(two_sum(sum[0], sum[1]), two_sum(sum[2], sum[3])), none = {0.f, 0.f};
-        block_sum2(s, t, none);
-        if (tid == 0) s.part = make_float2(m, t.hi + t.lo);
+        float m = -INFINITY;
+        for (int k = tid; k < packs; k += kDistThreads) {
+            Pack<T> v;
+            v.load(buf + k * E);
+            m = fmaxf(m, v.largest());
+        }
+        m = warp_max(m);
+        const float pm = m * p.c;
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        if (fabsf(pm) < 1e30f) {
+            // e^((z - m) / T) as 2^(z c - fl(m c)), one rounding of the argument; the sum is put right for fl(m c) after
+            for (int k = tid; k < packs; k += kDistThreads) {
+                Pack<T> v;
+                v.load(buf + k * E);
+#pragma unroll
+                for (int j = 0; j < E; ++j) sum[j & 3] += exp2_approx(fmaf(to_f32(v.t[j]), p.c, -pm));
+            }
+        } else {
+            const float mc = m > -INFINITY ? m : 0.f;
+            for (int k = tid; k < packs; k += kDistThreads) {
+                Pack<T> v;
+                v.load(buf + k * E);
+#pragma unroll
+                for (int j = 0; j < E; ++j) sum[j & 3] += exp2_approx((to_f32(v.t[j]) - mc) * p.c);
+            }
+        }
+        float t = warp_sum((sum[0] + sum[1]) + (sum[2] + sum[3]));
+        if (fabsf(pm) < 1e30f) t *= exp2f(-fmaf(m, p.c, -pm));
+        if (lane == 0) s.part[warp] = make_float2(m, t);
     }
     __syncthreads();
     cluster_arrive();
     cluster_wait();
-    float M = mS;
-    for (int k = 0; k < p.cs; ++k) M = fmaxf(M, cluster_read(&s.part, k).x);
-    float rest = 0.f;
-    for (int k = 0; k < p.cs; ++k) {
-        const float2 v = cluster_read(&s.part, k);
-        rest += v.x > -INFINITY ? v.y * exp2f((v.x - M) * p.c) : v.y;      // (a sum without a maximum is 0 or NaN)
-    }
     // ---- the outcomes
-    FF loss = {0.f, 0.f}, A = {0.f, 0.f}, P0 = {0.f, 0.f}, g0 = {0.f, 0.f};
-    FF lnT = {0.f, 0.f}, lnW = {0.f, 0.f};
-    float k_rest = 0.f;                                 // the gradient's factor outside the support, times T
-    float mass = 0.f;
-    int infinite = 0;
-    auto terms = [&](const Entry& x) -> Term {
-        const FF X = scaled(x.z, M);
-        const FF lp = X.hi == -INFINITY ? X : ff_add(X, ff_neg(lnT));
-        FF t, lt;
+    const float inv_T = p.inv_t.hi;
+    float M = 0.f, total = 1.f, lnT = 0.f, sT = 1.f, lnW = 0.f;
+    // a teacher's probability and its log, a student's
+    auto teacher = [&](const Entry& x, float& t, float& lt) {
         if (a.tail) {
-            t = exp_ff(x.lq);
-            lt = {x.lq, 0.f};
+            lt = x.lq;
+            t = expf(lt);
         } else {
-            lt = ff_add(scaled(x.lq, mT), ff_neg(lnW));
-            t = exp_pair(lt);
+            lt = (x.lq - mT) * inv_T - lnW;
+            t = exp2f((x.lq - mT) * p.c) / sT;
         }
-        return term_of(a.kind, a.beta, t, lt, exp_pair(lp), lp);
     };
-    if (any) {
-        const FF held = mS > -INFINITY ? ff_mul(wS, exp_pair(scaled(mS, M))) : FF{0.f, 0.f};
-        const FF total = ff_add({rest, 0.f}, held);
-        lnT = ln_pair(total);
-        if (!a.tail) lnW = ln_pair(wT);
-        bool inf = false;
-        each([&](const Entry& x, long long) {
-            const Term t = terms(x);
-            loss = ff_add(loss, t.f);
-            A = ff_add(A, t.g);
-            inf |= t.inf;
+    auto slope = [&](const Entry& x, float& P) -> float {
+        float t, lt;
+        teacher(x, t, lt);
+        const float d = x.z - M, lp = x.z == -INFINITY ? -INFINITY : d * inv_T - lnT;
+        P = x.z == -INFINITY ? 0.f : exp2f(d * p.c) / total;
+        return slope_of(a.kind, a.beta, t, lt, P, lp);
+    };
+    float P1 = 0.f, g1 = 0.f;                    // of the first entry
+    if (mine) {
+        M = mS;
+        float2 v[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int i = k * 32 + lane;
+            v[k] = i < p.cs * kDistWarps ? cluster_read(&s.part[i % kDistWarps], i / kDistWarps) : make_float2(-INFINITY, 0.f);
+            M = fmaxf(M, v[k].x);
+        }
+        M = warp_max(M);
+        float rest = 0.f;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) rest += v[k].x > -INFINITY ? v[k].y * exp2f((v[k].x - M) * p.c) : v[k].y;      // (a sum without a maximum is 0 or NaN)
+        rest = warp_sum(rest);
+        float held = 0.f;
+        sT = 0.f;
+        for (int k = 0; k < nw; ++k) {
+            const float4 x = s.sup[k];
+            if (x.x > -INFINITY) held += x.y * exp2f((x.x - M) * p.c);
+            else held += x.y;
+            if (x.z > -INFINITY) sT += x.w * exp2f((x.z - mT) * p.c);
+        }
+        total = rest + held;
+        lnT = logf(total);
+        lnW = logf(sT);
+        float A = 0.f;
+        each([&](const Entry& x, long long e) {
+            float P;
+            const float g = slope(x, P);
+            if (e == eb + tid) {
+                P1 = P;
+                g1 = g;
+            }
+            A += g;
         });
-        block_sum2(s, loss, A);
-        infinite = __syncthreads_or(inf);
-        P0 = ff_div({rest, 0.f}, total);
-        if (a.tail && rest > 0.f) {
+        A = warp_sum(A);
+        if (lane == 0) s.A[warp] = A;
+        if (tid == 0) {
+            s.M = M;
+            s.rest = rest;
+            s.total = total;
+            s.held = held;
+            if (a.tail) {
+                FF t0 = ff_add({1.f, 0.f}, ff_neg(wT));
+                if (!(t0.hi >= kMinTail)) t0 = {kMinTail, 0.f};
+                s.t0 = t0;
+            }
+        }
+    }
+    __syncthreads();
+    M = s.M;
+    total = s.total;
+    const float rest = s.rest;
+    // the gradient's factor outside the support (over the softmax's denominator, times T), and A
+    float k_rest = 0.f, A = 0.f;
+    if (any) {
+        for (int k = 0; k < nw; ++k) A += s.A[k];
+        float g0 = 0.f;
+        if (a.tail && !(rest <= 0.f)) {
+            const FF t0 = s.t0;
+            const float P0 = rest / total, x = slope_of(a.kind, a.beta, t0.hi, logf(t0.hi), P0, logf(P0));
+            A += x;
+            g0 = x / P0;
+        }
+        k_rest = (g0 - A) / total;
+    }
+    // ---- the loss, in pairs of floats, by the first block's support warps.  After the gradient, but for a support that
+    // does not stay in registers (its logits may be overwritten by then)
+    auto exact_loss = [&]() {
+        auto scaled = [&](float v, float m) -> FF { return v == -INFINITY ? FF{-INFINITY, 0.f} : ff_mul(two_sum(v, -m), p.inv_t); };
+        FF wS = {0.f, 0.f}, wQ = {0.f, 0.f};
+        each([&](const Entry& x, long long) {
+            wS = ff_add(wS, exp_pair(scaled(x.z, M)));
+            if (!a.tail) wQ = ff_add(wQ, exp_pair(scaled(x.lq, mT)));
+        });
+        wS = support_sum(s, wS, 1, nw);
+        if (!a.tail) wQ = support_sum(s, wQ, 0, nw);
+        const FF sum = ff_add({rest, 0.f}, wS);
+        const FF lnS = ln_pair(sum), lnQ = a.tail ? FF{0.f, 0.f} : ln_pair(wQ);
+        FF loss = {0.f, 0.f};
+        float inf = 0.f;
+        each([&](const Entry& x, long long) {
+            const FF X = scaled(x.z, M);
+            const FF lp = X.hi == -INFINITY ? X : ff_add(X, ff_neg(lnS));
+            FF t, lt;
+            if (a.tail) {
+                t = exp_ff(x.lq);
+                lt = {x.lq, 0.f};
+            } else {
+                lt = ff_add(scaled(x.lq, mT), ff_neg(lnQ));
+                t = exp_pair(lt);
+            }
+            const Term r = term_of(a.kind, a.beta, t, lt, exp_pair(lp), lp);
+            loss = ff_add(loss, r.f);
+            if (r.inf) inf = 1.f;
+        });
+        if (nw > 1) asm volatile("bar.sync 1, %0;" ::"r"(stride) : "memory");      // (the sums before have been read)
+        loss = support_sum(s, loss, 1, nw);
+        inf = support_sum(s, {inf, 0.f}, 0, nw).hi;
+        if (a.tail && !(rest <= 0.f)) {
             FF t0 = ff_add({1.f, 0.f}, ff_neg(wT));
             if (!(t0.hi >= kMinTail)) t0 = {kMinTail, 0.f};
-            const Term t = term_of(a.kind, a.beta, t0, ln_pair(t0), P0, ln_pair(P0));
-            loss = ff_add(loss, t.f);
-            A = ff_add(A, t.g);
-            g0 = t.g;
+            const FF P0 = ff_div({rest, 0.f}, sum);
+            loss = ff_add(loss, term_of(a.kind, a.beta, t0, ln_pair(t0), P0, ln_pair(P0)).f);
         }
-        // g of the rest less A, over the total
-        const FF d = ff_add(rest > 0.f ? ff_div(g0, P0) : FF{0.f, 0.f}, ff_neg(A));
-        k_rest = (d.hi + d.lo) / (total.hi + total.lo);
-        mass = (held.hi + held.lo) / (total.hi + total.lo);
-        if (infinite || !(fabsf(loss.hi) < INFINITY) || !(total.hi > 0.f)) bits |= RL_STATUS_NONFINITE;
+        if (inf > 0.f || !(fabsf(loss.hi) < INFINITY) || !(sum.hi > 0.f)) bits |= RL_STATUS_NONFINITE;
+        if (tid == 0) {
+            // (a row of -inf alone has no probabilities)
+            if (a.loss) a.loss[row] = !(sum.hi > 0.f) ? NAN : inf > 0.f && loss.hi == loss.hi ? INFINITY : loss.hi + loss.lo;
+            if (a.mass) a.mass[row] = (wS.hi + wS.lo) / (sum.hi + sum.lo);
+        }
+    };
+    if (rank == 0 && !any && tid == 0) {
+        if (a.loss) a.loss[row] = 0.f;
+        if (a.mass) a.mass[row] = 0.f;
     }
-    const float l = infinite && loss.hi == loss.hi ? INFINITY : loss.hi + loss.lo;
-    if (rank == 0 && tid == 0) {
-        if (a.loss) a.loss[row] = l;
-        if (a.mass) a.mass[row] = mass;
+    const bool early = ee - eb > kDistThreads || !p.grad;
+    if (early) {
+        if (rank == 0 && any && mine) exact_loss();
+        __syncthreads();
     }
-    const float inv_T = p.inv_t.hi;
+    cluster_arrive();                            // nobody leaves, or writes over logits, while they may be read
     if (!p.grad) {
-        if (sv.M) {
-            if (rank == 0 && tid == 0) {
+        if (rank == 0 && sv.M) {
+            if (tid == 0) {
                 sv.M[row] = M;
                 sv.rest[row] = any ? k_rest * inv_T : 0.f;
             }
-            if (rank == 0)
-                for (long long e = eb + tid; e < ee; e += kDistThreads) {
+            if (mine)
+                for (long long e = eb + tid; e < ee; e += stride) {
                     const Entry x = e == eb + tid ? first : entry_at(e);
-                    float d = 0.f;
-                    if (x.in) {
-                        const Term t = terms(x);
-                        const FF v = ff_add(t.g, ff_neg(ff_mul(t.P, A)));
-                        d = (v.hi + v.lo) * inv_T;
-                    }
-                    sv.entry[e] = d;
+                    float P = P1, g = g1;
+                    if (x.in && e != eb + tid) g = slope(x, P);
+                    sv.entry[e] = x.in ? (g - P * A) * inv_T : 0.f;
                 }
         }
         set_status(p.status, bits);
         __syncthreads();
-        cluster_arrive();                       // nobody leaves while its part may be read
         cluster_wait();
         return;
     }
     // ---- the gradient, in place
     const float kr = any ? w * inv_T * k_rest : 0.f;
-    const bool zero = !any || w == 0.f;
-    for (int k = tid; k < packs; k += kDistThreads) {
-        Pack<T> v;
-        v.load(buf + k * E);
+    if (!any || w == 0.f) {
+        for (int k = tid; k < packs; k += kDistThreads) *reinterpret_cast<uint4*>(buf + k * E) = make_uint4(0, 0, 0, 0);
+    } else {
+        const float pm = M * p.c;
+        const bool big = !(fabsf(pm) < 1e30f);
+        const float k2 = big ? kr : kr * exp2f(-fmaf(M, p.c, -pm));
+        for (int k = tid; k < packs; k += kDistThreads) {
+            Pack<T> v;
+            v.load(buf + k * E);
+            float d[E];
 #pragma unroll
-        for (int j = 0; j < E; ++j) v.t[j] = from_f32<T>(zero ? 0.f : kr * exp2_approx((to_f32(v.t[j]) - M) * p.c));
-        v.store(buf + k * E);
+            for (int j = 0; j < E; ++j) {
+                const float x = to_f32(v.t[j]);
+                d[j] = k2 * exp2_approx(big ? (x - M) * p.c : fmaf(x, p.c, -pm));
+            }
+            v.put(d);
+            v.store(buf + k * E);
+        }
+        __syncthreads();
+        if (mine)
+            each([&](const Entry& x, long long e) {
+                if (x.id < i0 || x.id >= i1) return;
+                float P = P1, g = g1;
+                if (e != eb + tid) g = slope(x, P);
+                buf[x.id - i0 + l0] = from_f32<T>(w * inv_T * (g - P * A));
+            });
     }
-    __syncthreads();
-    if (!zero)
-        each([&](const Entry& x, long long) {
-            if (x.id < i0 || x.id >= i1) return;
-            const Term t = terms(x);
-            const FF v = ff_add(t.g, ff_neg(ff_mul(t.P, A)));
-            buf[x.id - i0 + l0] = from_f32<T>(w * inv_T * (v.hi + v.lo));
-        });
-    set_status(p.status, bits);
     fence_proxy_async_smem();
     __syncthreads();
-    cluster_arrive();                           // all of the row's logits have been read: the gradient may take their place
-    cluster_wait();
+    cluster_wait();                             // all of the row's logits have been read: the gradient may take their place
     T* d = static_cast<T*>(a.dlogits) + row * a.grad_stride;
     const bool same = (reinterpret_cast<uintptr_t>(d) & 15) / sizeof(T) == static_cast<unsigned>(phase);
     if (same) {
-        if (tid == 0 && b1 > b0) {
+        if (tid == kDistThreads - 1 && b1 > b0) {
             bulk_store(d + (b0 - l0 + i0), buf + b0, static_cast<uint32_t>((b1 - b0) * sizeof(T)));
             bulk_commit();
         }
         for (int q = l0 + tid; q < min(lead, l1); q += kDistThreads) d[q - l0 + i0] = buf[q];
         for (int q = trail + tid; q < l1; q += kDistThreads) d[q - l0 + i0] = buf[q];
-        if (tid == 0) bulk_wait_read<0>();
     } else {
         for (int q = l0 + tid; q < l1; q += kDistThreads) d[q - l0 + i0] = buf[q];
     }
+    if (rank == 0 && any && mine && !early) exact_loss();
+    set_status(p.status, bits);
+    if (same && tid == kDistThreads - 1) bulk_wait_read<0>();
 }
 
 // ---- the backward alone: gradients from what the forward saved --------------------------------

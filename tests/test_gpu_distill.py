@@ -104,6 +104,13 @@ def test_against_the_definition(kind, tail, dtype, V):
     check(make(9, V, dtype, k, T, tail), p, dtype)
 
 
+@pytest.mark.parametrize("kind,tail", KINDS)
+def test_long_supports(kind, tail):
+    """Supports that do not stay in a block's registers, on rows of several blocks."""
+    p = rh.DistillParams(kind=kind, tail=tail, temperature=1.0, beta=0.7)
+    check(make(5, 60000, "fp32", np.array([257, 3000, 60000, 1, 20000]), 1.0, tail), p, "fp32")
+
+
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
 @pytest.mark.parametrize("N,V", [(1, 151936), (3, 50257), (40, 65537), (300, 4099)])
 def test_long_and_many_rows(dtype, N, V):
@@ -210,6 +217,17 @@ def test_logits_that_are_not_numbers(value, where):
         assert o.status_bits() == NONFINITE
         assert not bool(torch.isfinite(o.loss[1])) and bool(torch.isfinite(o.loss[[0, 2]]).all())
         assert not bool(torch.isfinite(d[1]).all()) and bool(torch.isfinite(d[[0, 2]]).all())
+
+
+def test_a_row_of_minus_inf_alone():
+    c = make(3, 700, "bf16", np.array([4, 4, 4]))
+    c["z"][1] = float("-inf")
+    c["dl"][:] = 1
+    for kind, tail in KINDS:
+        p = rh.DistillParams(kind=kind, tail=tail)
+        o, d = rh.rl_distill_fwd_bwd(c["z"], c["off"], c["ids"], c["q"], c["dl"], p)
+        assert o.status_bits() == NONFINITE and not bool(torch.isfinite(o.loss[1]))
+        assert bool(torch.isfinite(o.loss[[0, 2]]).all()) and bool(torch.isfinite(d[[0, 2]]).all())
 
 
 def test_bad_rows_set_bits():
