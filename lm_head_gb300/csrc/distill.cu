@@ -31,8 +31,7 @@
 
 namespace rl {
 
-constexpr int kDistThreads = 256;
-constexpr int kDistWarps = kDistThreads / 32;
+constexpr int kDistWarps = 12;                  // most of a block
 constexpr float kMinTail = 0x1p-20f;            // what fp32 log-probabilities leave certain of a teacher's rest
 
 struct DistArgs {
@@ -131,14 +130,15 @@ RL_DEVINL FF warp_sum_ff(FF v) {
     return fast_two_sum(v.hi, v.lo);
 }
 
-struct DistShared {
+struct DistShared {              // (small: three blocks with slices of 76 KB are to fit on a multiprocessor)
     uint64_t bar;
-    float2 part[kDistWarps];     // (maximum, sum) of each warp's stretch of the slice, without the support
+    float2 part[kDistWarps];     // (maximum, sum) of each warp's share of the slice, without the support
     float4 sup[kDistWarps];      // of each support warp: largest logit, sum relative to it, the same of the teacher's
     FF sum[kDistWarps][2];       // pairs to be added up over the support warps
     FF t0;                       // the teacher's probability of the rest
     float A[kDistWarps];
-    float M, rest, total, held;
+    int inf[kDistWarps];
+    float M, rest, total;
 };
 
 RL_DEVINL float2 cluster_read(const float2* mine, int rank) {
@@ -211,54 +211,57 @@ RL_DEVINL FF support_sum(DistShared& s, FF v, int which, int n) {
     return v;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kDistThreads, 4) distill_kernel(const __grid_constant__ DistArgs p, const DistSaved sv) {
+template <typename T, int NT, int kBlocks>
+__global__ void __launch_bounds__(NT, kBlocks) distill_kernel(const __grid_constant__ DistArgs p, const DistSaved sv) {
     extern __shared__ __align__(128) uint8_t raw[];
     __shared__ DistShared s;
     const rl_distill_args& a = p.a;
-    constexpr int E = Pack<T>::E;
+    constexpr int E = Pack<T>::E, kWarps = NT / 32;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const long long row = blockIdx.x / static_cast<unsigned>(p.cs);
     const int rank = static_cast<int>(blockIdx.x - row * p.cs);
     const int V = static_cast<int>(a.V);
+    long long eb = a.offsets[row], ee = a.offsets[row + 1];
+    const float w = a.dloss && p.grad ? a.dloss[row] : 0.f;
     const T* z = static_cast<const T*>(a.logits) + row * a.row_stride;
     // Places: the row's element i lies at place i + phase, so that a multiple of E places is 16-byte
-    // aligned in memory and in shared memory alike.  This block has places [q0, q0 + slice).
+    // aligned in memory and in shared memory alike.  This block has places [q0, q0 + slice), of which [l0, l1) are
+    // the row's and [b0, b1) whole 16 bytes of it.
     const int phase = static_cast<int>((reinterpret_cast<uintptr_t>(z) & 15) / sizeof(T));
     const long long q0 = static_cast<long long>(rank) * p.slice;
     const int i0 = static_cast<int>(max(q0 - phase, 0ll)), i1 = static_cast<int>(min(max(q0 + p.slice - phase, 0ll), static_cast<long long>(V)));
-    const int n = max(i1 - i0, 0);                               // the slice's elements
-    const int l0 = static_cast<int>(i0 + phase - q0), l1 = l0 + n;     // their places in shared memory
-    const int b0 = (l0 + E - 1) / E * E, b1 = l1 / E * E;        // the aligned stretch of them
+    const int n = max(i1 - i0, 0);
+    const int l0 = static_cast<int>(i0 + phase - q0), l1 = l0 + n;
+    const int b0 = (l0 + E - 1) / E * E, b1 = max(l1 / E * E, b0);
+    const int at0 = i0 - l0;                                     // place q holds the row's element q + at0
     const int packs = n > 0 ? (l1 + E - 1) / E : 0;
     T* buf = reinterpret_cast<T*>(raw);
     int bits = 0;
 
-    if (tid == 0) {
+    if (tid == NT - 1) {
         mbar_init(&s.bar, 1);
         fence_mbar_init();
-        if (n > 0 && b1 > b0) {
+        if (b1 > b0) {
             mbar_arrive_expect_tx(&s.bar, static_cast<uint32_t>((b1 - b0) * sizeof(T)));
-            bulk_load(buf + b0, z + (b0 - l0 + i0), static_cast<uint32_t>((b1 - b0) * sizeof(T)), &s.bar);
+            bulk_load(buf + b0, z + b0 + at0, static_cast<uint32_t>((b1 - b0) * sizeof(T)), &s.bar);
         } else {
             mbar_arrive(&s.bar);
         }
     }
-    // the edges by themselves; places that are not the row's hold -inf
-    const int lead = b1 > b0 ? b0 : packs * E, trail = b1 > b0 ? b1 : packs * E;
-    auto edge = [&](int q) { buf[q] = q >= l0 && q < l1 ? z[q - l0 + i0] : from_f32<T>(-INFINITY); };
-    for (int q = tid; q < lead; q += kDistThreads) edge(q);
-    for (int q = trail + tid; q < packs * E; q += kDistThreads) edge(q);
+    // the places that the copy leaves out: the row's edges, and -inf beside them
+    auto edges = [&](auto f) {
+        for (int q = tid; q < min(packs * E, b0); q += NT) f(q);
+        for (int q = b1 + tid; q < packs * E; q += NT) f(q);
+    };
+    edges([&](int q) { buf[q] = q >= l0 && q < l1 ? z[q + at0] : from_f32<T>(-INFINITY); });
 
     // ---- the support, while the slice is on its way: by as few warps as hold it, the same in every block of the cluster
-    long long eb = a.offsets[row], ee = a.offsets[row + 1];
     if (eb < 0 || ee < eb || ee > a.nnz) {
         bits |= RL_STATUS_OFFSETS;
         eb = ee = 0;
     }
-    const float w = a.dloss && p.grad ? a.dloss[row] : 0.f;
-    const int nw = static_cast<int>(min(static_cast<long long>(kDistWarps), (ee - eb + 31) / 32)), stride = nw * 32;
-    const bool mine = warp < nw;
+    const int nw = static_cast<int>(min(static_cast<long long>(kWarps), (ee - eb + 31) / 32)), stride = nw * 32;
+    const bool mine = warp < nw, listed = ee - eb <= NT;         // a thread has one entry at most, which stays in registers
     auto entry_at = [&](long long e) -> Entry {
         Entry x;
         x.id = a.ids[e];
@@ -267,15 +270,17 @@ __global__ void __launch_bounds__(kDistThreads, 4) distill_kernel(const __grid_c
         x.z = x.in ? to_f32(z[x.id]) : -INFINITY;
         return x;
     };
-    Entry first{-1, -INFINITY, 0.f, false};      // the thread's first entry stays in registers
-    // f(entry, its index) for the support warps' entries that count
+    Entry first{-1, -INFINITY, 0.f, false};
+    // f(entry, whether it is the thread's first, its index) for the support warps' entries that count
     auto each = [&](auto f) {
         for (long long e = eb + tid; e < ee; e += stride) {
-            const Entry x = e == eb + tid ? first : entry_at(e);
-            if (x.in) f(x, e);
+            const bool is_first = e == eb + tid;
+            const Entry x = is_first ? first : entry_at(e);
+            if (x.in) f(x, is_first, e);
         }
     };
     FF wT = {0.f, 0.f};                          // tail: the teacher's probabilities of the support
+    FF t1 = {0.f, 0.f};                          // of the first entry
     if (mine) {
         float mS = -INFINITY, mT = -INFINITY;
         for (long long e = eb + tid; e < ee; e += stride) {
@@ -287,13 +292,17 @@ __global__ void __launch_bounds__(kDistThreads, 4) distill_kernel(const __grid_c
             if (x.in) {
                 mS = fmaxf(mS, x.z);
                 mT = fmaxf(mT, x.lq);
-                if (a.tail) wT = ff_add(wT, exp_ff(x.lq));
+                if (a.tail) {
+                    const FF t = exp_ff(x.lq);
+                    if (e == eb + tid) t1 = t;
+                    wT = ff_add(wT, t);
+                }
             }
         }
         mS = warp_max(mS);
         mT = warp_max(mT);
         float sS = 0.f, sT = 0.f;
-        each([&](const Entry& x, long long) {
+        each([&](const Entry& x, bool, long long) {
             sS += x.z == -INFINITY ? 0.f : exp2f((x.z - mS) * p.c);
             sT += exp2f((x.lq - mT) * p.c);
         });
@@ -312,14 +321,13 @@ __global__ void __launch_bounds__(kDistThreads, 4) distill_kernel(const __grid_c
     if (!mbar_wait(&s.bar, 0, p.status, p.wait_ns)) mbar_wait(&s.bar, 0, p.status);   // (the copy lands before the block goes on)
     // ---- the rest of the slice: the support out of it, then each warp's maximum and sum
     if (mine)
-        for (long long e = eb + tid; e < ee; e += stride) {
-            const Entry x = e == eb + tid ? first : entry_at(e);
-            if (x.in && x.id >= i0 && x.id < i1) buf[x.id - i0 + l0] = from_f32<T>(-INFINITY);
-        }
+        each([&](const Entry& x, bool, long long) {
+            if (x.id >= i0 && x.id < i1) buf[x.id - at0] = from_f32<T>(-INFINITY);
+        });
     __syncthreads();
     {
         float m = -INFINITY;
-        for (int k = tid; k < packs; k += kDistThreads) {
+        for (int k = tid; k < packs; k += NT) {
             Pack<T> v;
             v.load(buf + k * E);
             m = fmaxf(m, v.largest());
@@ -329,7 +337,7 @@ __global__ void __launch_bounds__(kDistThreads, 4) distill_kernel(const __grid_c
         float sum[4] = {0.f, 0.f, 0.f, 0.f};
         if (fabsf(pm) < 1e30f) {
             // e^((z - m) / T) as 2^(z c - fl(m c)), one rounding of the argument; the sum is put right for fl(m c) after
-            for (int k = tid; k < packs; k += kDistThreads) {
+            for (int k = tid; k < packs; k += NT) {
                 Pack<T> v;
                 v.load(buf + k * E);
 #pragma unroll
@@ -337,7 +345,7 @@ __global__ void __launch_bounds__(kDistThreads, 4) distill_kernel(const __grid_c
             }
         } else {
             const float mc = m > -INFINITY ? m : 0.f;
-            for (int k = tid; k < packs; k += kDistThreads) {
+            for (int k = tid; k < packs; k += NT) {
                 Pack<T> v;
                 v.load(buf + k * E);
 #pragma unroll
@@ -348,14 +356,15 @@ __global__ void __launch_bounds__(kDistThreads, 4) distill_kernel(const __grid_c
         if (fabsf(pm) < 1e30f) t *= exp2f(-fmaf(m, p.c, -pm));
         if (lane == 0) s.part[warp] = make_float2(m, t);
     }
-    __syncthreads();
+    __syncwarp();
     cluster_arrive();
     cluster_wait();
     // ---- the outcomes
     const float inv_T = p.inv_t.hi;
     float M = 0.f, total = 1.f, lnT = 0.f, sT = 1.f, lnW = 0.f;
-    // a teacher's probability and its log, a student's
-    auto teacher = [&](const Entry& x, float& t, float& lt) {
+    // P g of an entry, and P
+    auto slope = [&](const Entry& x, float& P) -> float {
+        float t, lt;
         if (a.tail) {
             lt = x.lq;
             t = expf(lt);
@@ -363,10 +372,6 @@ __global__ void __launch_bounds__(kDistThreads, 4) distill_kernel(const __grid_c
             lt = (x.lq - mT) * inv_T - lnW;
             t = exp2f((x.lq - mT) * p.c) / sT;
         }
-    };
-    auto slope = [&](const Entry& x, float& P) -> float {
-        float t, lt;
-        teacher(x, t, lt);
         const float d = x.z - M, lp = x.z == -INFINITY ? -INFINITY : d * inv_T - lnT;
         P = x.z == -INFINITY ? 0.f : exp2f(d * p.c) / total;
         return slope_of(a.kind, a.beta, t, lt, P, lp);
@@ -374,17 +379,18 @@ __global__ void __launch_bounds__(kDistThreads, 4) distill_kernel(const __grid_c
     float P1 = 0.f, g1 = 0.f;                    // of the first entry
     if (mine) {
         M = mS;
-        float2 v[2];
+        constexpr int kReads = kWarps / 4;                       // up to eight blocks' parts
+        float2 v[kReads];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
+        for (int k = 0; k < kReads; ++k) {
             const int i = k * 32 + lane;
-            v[k] = i < p.cs * kDistWarps ? cluster_read(&s.part[i % kDistWarps], i / kDistWarps) : make_float2(-INFINITY, 0.f);
+            v[k] = i < p.cs * kWarps ? cluster_read(&s.part[i % kWarps], i / kWarps) : make_float2(-INFINITY, 0.f);
             M = fmaxf(M, v[k].x);
         }
         M = warp_max(M);
         float rest = 0.f;
 #pragma unroll
-        for (int k = 0; k < 2; ++k) rest += v[k].x > -INFINITY ? v[k].y * exp2f((v[k].x - M) * p.c) : v[k].y;      // (a sum without a maximum is 0 or NaN)
+        for (int k = 0; k < kReads; ++k) rest += v[k].x > -INFINITY ? v[k].y * exp2f((v[k].x - M) * p.c) : v[k].y;      // (a sum without a maximum is 0 or NaN)
         rest = warp_sum(rest);
         float held = 0.f;
         sT = 0.f;
@@ -398,10 +404,10 @@ __global__ void __launch_bounds__(kDistThreads, 4) distill_kernel(const __grid_c
         lnT = logf(total);
         lnW = logf(sT);
         float A = 0.f;
-        each([&](const Entry& x, long long e) {
+        each([&](const Entry& x, bool is_first, long long) {
             float P;
             const float g = slope(x, P);
-            if (e == eb + tid) {
+            if (is_first) {
                 P1 = P;
                 g1 = g;
             }
@@ -413,7 +419,6 @@ __global__ void __launch_bounds__(kDistThreads, 4) distill_kernel(const __grid_c
             s.M = M;
             s.rest = rest;
             s.total = total;
-            s.held = held;
             if (a.tail) {
                 FF t0 = ff_add({1.f, 0.f}, ff_neg(wT));
                 if (!(t0.hi >= kMinTail)) t0 = {kMinTail, 0.f};
@@ -431,8 +436,7 @@ __global__ void __launch_bounds__(kDistThreads, 4) distill_kernel(const __grid_c
         for (int k = 0; k < nw; ++k) A += s.A[k];
         float g0 = 0.f;
         if (a.tail && !(rest <= 0.f)) {
-            const FF t0 = s.t0;
-            const float P0 = rest / total, x = slope_of(a.kind, a.beta, t0.hi, logf(t0.hi), P0, logf(P0));
+            const float t0 = s.t0.hi, P0 = rest / total, x = slope_of(a.kind, a.beta, t0, logf(t0), P0, logf(P0));
             A += x;
             g0 = x / P0;
         }
@@ -442,45 +446,54 @@ __global__ void __launch_bounds__(kDistThreads, 4) distill_kernel(const __grid_c
     // does not stay in registers (its logits may be overwritten by then)
     auto exact_loss = [&]() {
         auto scaled = [&](float v, float m) -> FF { return v == -INFINITY ? FF{-INFINITY, 0.f} : ff_mul(two_sum(v, -m), p.inv_t); };
-        FF wS = {0.f, 0.f}, wQ = {0.f, 0.f};
-        each([&](const Entry& x, long long) {
-            wS = ff_add(wS, exp_pair(scaled(x.z, M)));
-            if (!a.tail) wQ = ff_add(wQ, exp_pair(scaled(x.lq, mT)));
+        auto weights = [&](const Entry& x, bool is_first, FF& W, FF& Q) {
+            W = exp_pair(scaled(x.z, M));
+            Q = !a.tail ? exp_pair(scaled(x.lq, mT)) : is_first ? t1 : exp_ff(x.lq);
+        };
+        FF wS = {0.f, 0.f}, wQ = {0.f, 0.f}, W1 = {0.f, 0.f}, Q1 = {0.f, 0.f};
+        each([&](const Entry& x, bool is_first, long long) {
+            FF W, Q;
+            weights(x, is_first, W, Q);
+            if (is_first) {
+                W1 = W;
+                Q1 = Q;
+            }
+            wS = ff_add(wS, W);
+            if (!a.tail) wQ = ff_add(wQ, Q);
         });
         wS = support_sum(s, wS, 1, nw);
         if (!a.tail) wQ = support_sum(s, wQ, 0, nw);
         const FF sum = ff_add({rest, 0.f}, wS);
-        const FF lnS = ln_pair(sum), lnQ = a.tail ? FF{0.f, 0.f} : ln_pair(wQ);
+        const FF t0 = a.tail ? s.t0 : FF{1.f, 0.f};
+        // three logs, a lane each
+        const FF ln = ln_pair(lane == 0 ? sum : lane == 1 ? (a.tail ? t0 : wQ) : FF{rest, 0.f});
+        auto lane_of = [&](FF v, int k) -> FF { return {__shfl_sync(0xffffffffu, v.hi, k), __shfl_sync(0xffffffffu, v.lo, k)}; };
+        const FF lnS = lane_of(ln, 0), ln1 = lane_of(ln, 1), lnR = lane_of(ln, 2);
+        const FF inv_S = ff_div({1.f, 0.f}, sum), inv_Q = a.tail ? FF{1.f, 0.f} : ff_div({1.f, 0.f}, wQ);
         FF loss = {0.f, 0.f};
-        float inf = 0.f;
-        each([&](const Entry& x, long long) {
+        bool inf = false;
+        each([&](const Entry& x, bool is_first, long long) {
+            FF W = W1, Q = Q1;
+            if (!is_first) weights(x, false, W, Q);
             const FF X = scaled(x.z, M);
             const FF lp = X.hi == -INFINITY ? X : ff_add(X, ff_neg(lnS));
-            FF t, lt;
-            if (a.tail) {
-                t = exp_ff(x.lq);
-                lt = {x.lq, 0.f};
-            } else {
-                lt = ff_add(scaled(x.lq, mT), ff_neg(lnQ));
-                t = exp_pair(lt);
-            }
-            const Term r = term_of(a.kind, a.beta, t, lt, exp_pair(lp), lp);
+            const FF lt = a.tail ? FF{x.lq, 0.f} : ff_add(scaled(x.lq, mT), ff_neg(ln1)), t = a.tail ? Q : ff_mul(Q, inv_Q);
+            const Term r = term_of(a.kind, a.beta, t, lt, ff_mul(W, inv_S), lp);
             loss = ff_add(loss, r.f);
-            if (r.inf) inf = 1.f;
+            inf |= r.inf;
         });
-        if (nw > 1) asm volatile("bar.sync 1, %0;" ::"r"(stride) : "memory");      // (the sums before have been read)
-        loss = support_sum(s, loss, 1, nw);
-        inf = support_sum(s, {inf, 0.f}, 0, nw).hi;
-        if (a.tail && !(rest <= 0.f)) {
-            FF t0 = ff_add({1.f, 0.f}, ff_neg(wT));
-            if (!(t0.hi >= kMinTail)) t0 = {kMinTail, 0.f};
-            const FF P0 = ff_div({rest, 0.f}, sum);
-            loss = ff_add(loss, term_of(a.kind, a.beta, t0, ln_pair(t0), P0, ln_pair(P0)).f);
+        inf = __any_sync(0xffffffffu, inf);
+        if (nw > 1) {
+            if (lane == 0) s.inf[warp] = inf;
+            asm volatile("bar.sync 1, %0;" ::"r"(stride) : "memory");      // (and the sums before have been read)
+            for (int k = 0; k < nw; ++k) inf |= s.inf[k] != 0;
         }
-        if (inf > 0.f || !(fabsf(loss.hi) < INFINITY) || !(sum.hi > 0.f)) bits |= RL_STATUS_NONFINITE;
+        loss = support_sum(s, loss, 1, nw);
+        if (a.tail && !(rest <= 0.f)) loss = ff_add(loss, term_of(a.kind, a.beta, t0, ln1, ff_mul({rest, 0.f}, inv_S), ff_add(lnR, ff_neg(lnS))).f);
+        if (inf || !(fabsf(loss.hi) < INFINITY) || !(sum.hi > 0.f)) bits |= RL_STATUS_NONFINITE;
         if (tid == 0) {
             // (a row of -inf alone has no probabilities)
-            if (a.loss) a.loss[row] = !(sum.hi > 0.f) ? NAN : inf > 0.f && loss.hi == loss.hi ? INFINITY : loss.hi + loss.lo;
+            if (a.loss) a.loss[row] = !(sum.hi > 0.f) ? NAN : inf && loss.hi == loss.hi ? INFINITY : loss.hi + loss.lo;
             if (a.mass) a.mass[row] = (wS.hi + wS.lo) / (sum.hi + sum.lo);
         }
     };
@@ -488,11 +501,12 @@ __global__ void __launch_bounds__(kDistThreads, 4) distill_kernel(const __grid_c
         if (a.loss) a.loss[row] = 0.f;
         if (a.mass) a.mass[row] = 0.f;
     }
-    const bool early = ee - eb > kDistThreads || !p.grad;
+    const bool early = !listed || !p.grad;
     if (early) {
         if (rank == 0 && any && mine) exact_loss();
         __syncthreads();
     }
+    __syncwarp();
     cluster_arrive();                            // nobody leaves, or writes over logits, while they may be read
     if (!p.grad) {
         if (rank == 0 && sv.M) {
@@ -509,37 +523,44 @@ __global__ void __launch_bounds__(kDistThreads, 4) distill_kernel(const __grid_c
                 }
         }
         set_status(p.status, bits);
-        __syncthreads();
+        __syncwarp();
         cluster_wait();
         return;
     }
     // ---- the gradient, in place
-    const float kr = any ? w * inv_T * k_rest : 0.f;
     if (!any || w == 0.f) {
-        for (int k = tid; k < packs; k += kDistThreads) *reinterpret_cast<uint4*>(buf + k * E) = make_uint4(0, 0, 0, 0);
+        for (int k = tid; k < packs; k += NT) *reinterpret_cast<uint4*>(buf + k * E) = make_uint4(0, 0, 0, 0);
     } else {
-        const float pm = M * p.c;
-        const bool big = !(fabsf(pm) < 1e30f);
-        const float k2 = big ? kr : kr * exp2f(-fmaf(M, p.c, -pm));
-        for (int k = tid; k < packs; k += kDistThreads) {
-            Pack<T> v;
-            v.load(buf + k * E);
-            float d[E];
+        const float kr = w * inv_T * k_rest, pm = M * p.c;
+        if (fabsf(pm) < 1e30f) {
+            const float k2 = kr * exp2f(-fmaf(M, p.c, -pm));
+            for (int k = tid; k < packs; k += NT) {
+                Pack<T> v;
+                v.load(buf + k * E);
+                float d[E];
 #pragma unroll
-            for (int j = 0; j < E; ++j) {
-                const float x = to_f32(v.t[j]);
-                d[j] = k2 * exp2_approx(big ? (x - M) * p.c : fmaf(x, p.c, -pm));
+                for (int j = 0; j < E; ++j) d[j] = k2 * exp2_approx(fmaf(to_f32(v.t[j]), p.c, -pm));
+                v.put(d);
+                v.store(buf + k * E);
             }
-            v.put(d);
-            v.store(buf + k * E);
+        } else {
+            for (int k = tid; k < packs; k += NT) {
+                Pack<T> v;
+                v.load(buf + k * E);
+                float d[E];
+#pragma unroll
+                for (int j = 0; j < E; ++j) d[j] = kr * exp2_approx((to_f32(v.t[j]) - M) * p.c);
+                v.put(d);
+                v.store(buf + k * E);
+            }
         }
         __syncthreads();
         if (mine)
-            each([&](const Entry& x, long long e) {
+            each([&](const Entry& x, bool is_first, long long) {
                 if (x.id < i0 || x.id >= i1) return;
                 float P = P1, g = g1;
-                if (e != eb + tid) g = slope(x, P);
-                buf[x.id - i0 + l0] = from_f32<T>(w * inv_T * (g - P * A));
+                if (!is_first) g = slope(x, P);
+                buf[x.id - at0] = from_f32<T>(w * inv_T * (g - P * A));
             });
     }
     fence_proxy_async_smem();
@@ -548,18 +569,19 @@ __global__ void __launch_bounds__(kDistThreads, 4) distill_kernel(const __grid_c
     T* d = static_cast<T*>(a.dlogits) + row * a.grad_stride;
     const bool same = (reinterpret_cast<uintptr_t>(d) & 15) / sizeof(T) == static_cast<unsigned>(phase);
     if (same) {
-        if (tid == kDistThreads - 1 && b1 > b0) {
-            bulk_store(d + (b0 - l0 + i0), buf + b0, static_cast<uint32_t>((b1 - b0) * sizeof(T)));
+        if (tid == NT - 1 && b1 > b0) {
+            bulk_store(d + b0 + at0, buf + b0, static_cast<uint32_t>((b1 - b0) * sizeof(T)));
             bulk_commit();
         }
-        for (int q = l0 + tid; q < min(lead, l1); q += kDistThreads) d[q - l0 + i0] = buf[q];
-        for (int q = trail + tid; q < l1; q += kDistThreads) d[q - l0 + i0] = buf[q];
+        edges([&](int q) {
+            if (q >= l0 && q < l1) d[q + at0] = buf[q];
+        });
     } else {
-        for (int q = l0 + tid; q < l1; q += kDistThreads) d[q - l0 + i0] = buf[q];
+        for (int q = l0 + tid; q < l1; q += NT) d[q + at0] = buf[q];
     }
     if (rank == 0 && any && mine && !early) exact_loss();
     set_status(p.status, bits);
-    if (same && tid == kDistThreads - 1) bulk_wait_read<0>();
+    if (same && tid == NT - 1) bulk_wait_read<0>();
 }
 
 // ---- the backward alone: gradients from what the forward saved --------------------------------
@@ -620,9 +642,31 @@ static DistArgs dist_args(const rl_distill_args* a, int32_t* status) {
     return p;
 }
 
-constexpr int kSliceTarget = 40 * 1024;         // bytes: five blocks a multiprocessor, whose loads, sums and stores overlap
+constexpr int kSliceTarget = 75 * 1024;         // bytes: three blocks a multiprocessor, whose loads, sums and stores overlap
 constexpr int kSliceLeast = 4 * 1024;
+constexpr int kMiddleSlice = 50 * 1024, kShortSlice = 12 * 1024;
 static_assert(kDistillRowBytes <= 8 * (kDistillSliceBytes - 64), "a cluster of eight holds the longest row");
+
+template <typename T, int NT, int kBlocks>
+static int distill_launch(const DistArgs& p, const DistSaved& sv, cudaStream_t stream) {
+    static std::atomic<uint64_t> done{0};
+    if (!allow_smem(distill_kernel<T, NT, kBlocks>, kDistillSliceBytes, done)) return RL_ERR_CUDA;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(p.a.N * p.cs), 1, 1);
+    cfg.blockDim = dim3(NT, 1, 1);
+    cfg.dynamicSmemBytes = static_cast<size_t>(p.slice) * sizeof(T);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(p.cs);
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    ProfScope prof(RL_PROF_OTHER, stream);
+    if (cudaLaunchKernelEx(&cfg, distill_kernel<T, NT, kBlocks>, p, sv) != cudaSuccess) return RL_ERR_CUDA;
+    count_launch();
+    return cudaPeekAtLastError() == cudaSuccess ? RL_OK : RL_ERR_CUDA;
+}
 
 template <typename T>
 static int distill_run(DistArgs p, const DistSaved& sv, cudaStream_t stream) {
@@ -630,7 +674,7 @@ static int distill_run(DistArgs p, const DistSaved& sv, cudaStream_t stream) {
     // the fewest blocks a row whose slices leave room for others on the multiprocessor; more of them where
     // there are too few rows to fill the GPU
     int cs = 1;
-    while (cs < 8 && (bytes / cs > kSliceTarget || (p.a.N * cs < num_sms() && bytes / cs >= 2 * kSliceLeast))) cs *= 2;
+    while (cs < 8 && (bytes / cs > kSliceTarget || (p.a.N * cs < num_sms() && bytes / cs >= 2 * kSliceLeast))) ++cs;
     const int quantum = 32 / static_cast<int>(sizeof(T));
     p.cs = cs;
     p.slice = static_cast<int>(((p.a.V + 16 / sizeof(T)) + cs * quantum - 1) / (cs * quantum)) * quantum;
@@ -638,24 +682,8 @@ static int distill_run(DistArgs p, const DistSaved& sv, cudaStream_t stream) {
         set_last_error("too many rows");
         return RL_ERR_UNSUPPORTED;
     }
-    const int smem = p.slice * static_cast<int>(sizeof(T));
-    static std::atomic<uint64_t> done{0};
-    if (!allow_smem(distill_kernel<T>, kDistillSliceBytes, done)) return RL_ERR_CUDA;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(p.a.N * cs), 1, 1);
-    cfg.blockDim = dim3(kDistThreads, 1, 1);
-    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = static_cast<unsigned>(cs);
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    ProfScope prof(RL_PROF_OTHER, stream);
-    if (cudaLaunchKernelEx(&cfg, distill_kernel<T>, p, sv) != cudaSuccess) return RL_ERR_CUDA;
-    count_launch();
-    return cudaPeekAtLastError() == cudaSuccess ? RL_OK : RL_ERR_CUDA;
+    const int own = p.slice * static_cast<int>(sizeof(T));
+    return own <= kShortSlice ? distill_launch<T, 128, 8>(p, sv, stream) : own <= kMiddleSlice ? distill_launch<T, 256, 4>(p, sv, stream) : distill_launch<T, 256, 3>(p, sv, stream);
 }
 
 template <typename T>
