@@ -68,6 +68,8 @@ RL_DEVINL uint32_t smem_addr(const void* p) {
 // Barrier of the whole cluster (every thread of every block, warps converged), and the address of another
 // block's counterpart of a shared variable.
 RL_DEVINL void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+// (without an order of the memory operations before it: a release waits for all of them, 3000 cycles after a block's first loads)
+RL_DEVINL void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
 RL_DEVINL void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 RL_DEVINL uint32_t cluster_addr(const void* mine, int rank) {
     uint32_t at;

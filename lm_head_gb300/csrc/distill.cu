@@ -28,10 +28,11 @@
 #include "common.cuh"
 #include "ff.cuh"
 #include "internal.h"
+#include "weights.cuh"
 
 namespace rl {
 
-constexpr int kDistWarps = 12;                  // most of a block
+constexpr int kDistWarps = 8;                   // most of a block
 constexpr float kMinTail = 0x1p-20f;            // what fp32 log-probabilities leave certain of a teacher's rest
 
 struct DistArgs {
@@ -47,7 +48,7 @@ struct DistArgs {
 
 // What the forward leaves for the backward.
 struct DistSaved {
-    float* M;              // [N] the row's largest logit
+    float* M;              // [N] the row's reference logit
     float* rest;           // [N] d L / d z of a token outside the support over its exp((z - M) / T)
     float* entry;          // [nnz] d L / d z of the support's entries
 };
@@ -131,8 +132,9 @@ RL_DEVINL FF warp_sum_ff(FF v) {
 }
 
 struct DistShared {              // (small: three blocks with slices of 76 KB are to fit on a multiprocessor)
-    uint64_t bar;
-    float2 part[kDistWarps];     // (maximum, sum) of each warp's share of the slice, without the support
+    uint64_t bar, xbar;          // the slice has landed; the parts of the row's blocks have
+    float2 xpart[8];             // (reference, sum) of each block of the cluster, without the support
+    float2 part[kDistWarps];     // of each warp of this block
     float4 sup[kDistWarps];      // of each support warp: largest logit, sum relative to it, the same of the teacher's
     FF sum[kDistWarps][2];       // pairs to be added up over the support warps
     FF t0;                       // the teacher's probability of the rest
@@ -141,11 +143,15 @@ struct DistShared {              // (small: three blocks with slices of 76 KB ar
     float M, rest, total;
 };
 
-RL_DEVINL float2 cluster_read(const float2* mine, int rank) {
-    float2 v;
-    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(cluster_addr(mine, rank)) : "memory");
-    return v;
+// v into another block's `to`, counted by its barrier `bar` (both given by this block's own addresses).
+RL_DEVINL void cluster_send(float2 v, const float2* to, const uint64_t* bar, int rank) {
+    const unsigned long long x = static_cast<unsigned long long>(__float_as_uint(v.y)) << 32 | __float_as_uint(v.x);
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b64 [%0], %1, [%2];" ::"r"(cluster_addr(to, rank)), "l"(x),
+                 "r"(cluster_addr(bar, rank))
+                 : "memory");
 }
+// Largest of a warp's values (NaN is not looked at).
+RL_DEVINL float warp_largest(float v) { return z_of(__reduce_max_sync(0xffffffffu, key_of(v + 0.f))); }
 RL_DEVINL void bulk_store(void* dst, const void* src, uint32_t bytes) {
     asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(reinterpret_cast<uint64_t>(dst)),
                  "r"(smem_addr(src)), "r"(bytes)
@@ -158,6 +164,15 @@ struct Entry {
     float z, lq;
     bool in;               // it counts: a token of the vocabulary with a log-probability above -inf
 };
+template <typename T>
+RL_DEVINL Entry entry_of(const rl_distill_args& a, const T* z, long long e) {
+    Entry x;
+    x.id = a.ids[e];
+    x.lq = a.logq[e];
+    x.in = x.id >= 0 && x.id < a.V && x.lq > -INFINITY && x.lq < INFINITY;
+    x.z = x.in ? to_f32(z[x.id]) : -INFINITY;
+    return x;
+}
 // Its terms: P, f and P g.
 struct Term {
     FF P, f, g;
@@ -183,7 +198,7 @@ RL_DEVINL Term term_of(int kind, float beta, FF t, FF lt, FF P, FF lp) {
         const FF m = ff_add(ff_mul(b, t), ff_mul(a, P));
         r.f = r.g = {0.f, 0.f};
         if (m.hi != 0.f) {
-            const FF lm = ln_pair(m);
+            const FF lm = ln_table(m);
             if (t.hi > 0.f) r.f = ff_mul(ff_mul(b, t), ff_add(lt, ff_neg(lm)));
             if (!none) r.g = ff_mul(ff_mul(a, P), ff_add(lp, ff_neg(lm)));
             r.f = ff_add(r.f, r.g);
@@ -209,6 +224,72 @@ RL_DEVINL FF support_sum(DistShared& s, FF v, int which, int n) {
     v = s.sum[0][which];
     for (int w = 1; w < n; ++w) v = ff_add(v, s.sum[w][which]);
     return v;
+}
+
+// The row's loss in pairs of floats, by the warps of its support (the first nw).  Returns status bits.
+template <typename T>
+__device__ __noinline__ int row_loss(const DistArgs& p, DistShared& s, const T* z, long long row, long long eb, long long ee, const Entry first,
+                                     const FF t1, float M, float mT, float rest, int nw) {
+    const rl_distill_args& a = p.a;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, stride = nw * 32;
+    auto each = [&](auto f) {
+        for (long long e = eb + tid; e < ee; e += stride) {
+            const bool is_first = e == eb + tid;
+            const Entry x = is_first ? first : entry_of(a, z, e);
+            if (x.in) f(x, is_first);
+        }
+    };
+    auto scaled = [&](float v, float m) -> FF { return v == -INFINITY ? FF{-INFINITY, 0.f} : ff_mul(two_sum(v, -m), p.inv_t); };
+    auto weights = [&](const Entry& x, bool is_first, FF& W, FF& Q) {
+        W = exp_table(scaled(x.z, M));
+        Q = !a.tail ? exp_table(scaled(x.lq, mT)) : is_first ? t1 : exp_table({x.lq, 0.f});
+    };
+    FF wS = {0.f, 0.f}, wQ = {0.f, 0.f}, W1 = {0.f, 0.f}, Q1 = {0.f, 0.f};
+    each([&](const Entry& x, bool is_first) {
+        FF W, Q;
+        weights(x, is_first, W, Q);
+        if (is_first) {
+            W1 = W;
+            Q1 = Q;
+        }
+        wS = ff_add(wS, W);
+        if (!a.tail) wQ = ff_add(wQ, Q);
+    });
+    wS = support_sum(s, wS, 1, nw);
+    if (!a.tail) wQ = support_sum(s, wQ, 0, nw);
+    const FF sum = ff_add({rest, 0.f}, wS);
+    const FF t0 = a.tail ? s.t0 : FF{1.f, 0.f};
+    // three logs, a lane each
+    const FF ln = ln_table(lane == 0 ? sum : lane == 1 ? (a.tail ? t0 : wQ) : FF{rest, 0.f});
+    auto lane_of = [&](FF v, int k) -> FF { return {__shfl_sync(0xffffffffu, v.hi, k), __shfl_sync(0xffffffffu, v.lo, k)}; };
+    const FF lnS = lane_of(ln, 0), ln1 = lane_of(ln, 1), lnR = lane_of(ln, 2);
+    const FF inv_S = ff_div({1.f, 0.f}, sum), inv_Q = a.tail ? FF{1.f, 0.f} : ff_div({1.f, 0.f}, wQ);
+    FF loss = {0.f, 0.f};
+    bool inf = false;
+    each([&](const Entry& x, bool is_first) {
+        FF W = W1, Q = Q1;
+        if (!is_first) weights(x, false, W, Q);
+        const FF X = scaled(x.z, M);
+        const FF lp = X.hi == -INFINITY ? X : ff_add(X, ff_neg(lnS));
+        const FF lt = a.tail ? FF{x.lq, 0.f} : ff_add(scaled(x.lq, mT), ff_neg(ln1)), t = a.tail ? Q : ff_mul(Q, inv_Q);
+        const Term r = term_of(a.kind, a.beta, t, lt, ff_mul(W, inv_S), lp);
+        loss = ff_add(loss, r.f);
+        inf |= r.inf;
+    });
+    inf = __any_sync(0xffffffffu, inf);
+    if (nw > 1) {
+        if (lane == 0) s.inf[warp] = inf;
+        asm volatile("bar.sync 1, %0;" ::"r"(stride) : "memory");      // (and the sums before have been read)
+        for (int k = 0; k < nw; ++k) inf |= s.inf[k] != 0;
+    }
+    loss = support_sum(s, loss, 1, nw);
+    if (a.tail && !(rest <= 0.f)) loss = ff_add(loss, term_of(a.kind, a.beta, t0, ln1, ff_mul({rest, 0.f}, inv_S), ff_add(lnR, ff_neg(lnS))).f);
+    if (tid == 0) {
+        // (a row of -inf alone has no probabilities)
+        if (a.loss) a.loss[row] = !(sum.hi > 0.f) ? NAN : inf && loss.hi == loss.hi ? INFINITY : loss.hi + loss.lo;
+        if (a.mass) a.mass[row] = (wS.hi + wS.lo) / (sum.hi + sum.lo);
+    }
+    return inf || !(fabsf(loss.hi) < INFINITY) || !(sum.hi > 0.f) ? RL_STATUS_NONFINITE : 0;
 }
 
 template <typename T, int NT, int kBlocks>
@@ -240,7 +321,9 @@ __global__ void __launch_bounds__(NT, kBlocks) distill_kernel(const __grid_const
 
     if (tid == NT - 1) {
         mbar_init(&s.bar, 1);
+        mbar_init(&s.xbar, 1);
         fence_mbar_init();
+        mbar_arrive_expect_tx(&s.xbar, static_cast<uint32_t>(p.cs) * 8u);
         if (b1 > b0) {
             mbar_arrive_expect_tx(&s.bar, static_cast<uint32_t>((b1 - b0) * sizeof(T)));
             bulk_load(buf + b0, z + b0 + at0, static_cast<uint32_t>((b1 - b0) * sizeof(T)), &s.bar);
@@ -248,6 +331,8 @@ __global__ void __launch_bounds__(NT, kBlocks) distill_kernel(const __grid_const
             mbar_arrive(&s.bar);
         }
     }
+    __syncwarp();
+    cluster_arrive_relaxed();                    // the barriers are there (fence_mbar_init is their release)
     // the places that the copy leaves out: the row's edges, and -inf beside them
     auto edges = [&](auto f) {
         for (int q = tid; q < min(packs * E, b0); q += NT) f(q);
@@ -262,14 +347,7 @@ __global__ void __launch_bounds__(NT, kBlocks) distill_kernel(const __grid_const
     }
     const int nw = static_cast<int>(min(static_cast<long long>(kWarps), (ee - eb + 31) / 32)), stride = nw * 32;
     const bool mine = warp < nw, listed = ee - eb <= NT;         // a thread has one entry at most, which stays in registers
-    auto entry_at = [&](long long e) -> Entry {
-        Entry x;
-        x.id = a.ids[e];
-        x.lq = a.logq[e];
-        x.in = x.id >= 0 && x.id < V && x.lq > -INFINITY && x.lq < INFINITY;
-        x.z = x.in ? to_f32(z[x.id]) : -INFINITY;
-        return x;
-    };
+    auto entry_at = [&](long long e) { return entry_of(a, z, e); };
     Entry first{-1, -INFINITY, 0.f, false};
     // f(entry, whether it is the thread's first, its index) for the support warps' entries that count
     auto each = [&](auto f) {
@@ -293,14 +371,14 @@ __global__ void __launch_bounds__(NT, kBlocks) distill_kernel(const __grid_const
                 mS = fmaxf(mS, x.z);
                 mT = fmaxf(mT, x.lq);
                 if (a.tail) {
-                    const FF t = exp_ff(x.lq);
+                    const FF t = exp_table({x.lq, 0.f});
                     if (e == eb + tid) t1 = t;
                     wT = ff_add(wT, t);
                 }
             }
         }
-        mS = warp_max(mS);
-        mT = warp_max(mT);
+        mS = warp_largest(mS);
+        mT = warp_largest(mT);
         float sS = 0.f, sT = 0.f;
         each([&](const Entry& x, bool, long long) {
             sS += x.z == -INFINITY ? 0.f : exp2f((x.z - mS) * p.c);
@@ -326,39 +404,59 @@ __global__ void __launch_bounds__(NT, kBlocks) distill_kernel(const __grid_const
         });
     __syncthreads();
     {
-        float m = -INFINITY;
-        for (int k = tid; k < packs; k += NT) {
-            Pack<T> v;
-            v.load(buf + k * E);
-            m = fmaxf(m, v.largest());
-        }
-        m = warp_max(m);
-        const float pm = m * p.c;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
-        if (fabsf(pm) < 1e30f) {
-            // e^((z - m) / T) as 2^(z c - fl(m c)), one rounding of the argument; the sum is put right for fl(m c) after
+        // e^((z - m) / T) as 2^(z c - fl(m c)): one rounding of the argument, and the sum is put right for fl(m c) after.  The
+        // reference m need not be the largest logit: the support's largest will do, unless the sum leaves the range
+        float sum[4], t = 0.f, m = mS;
+        auto add = [&](float pm) -> float {
+            sum[0] = sum[1] = sum[2] = sum[3] = 0.f;
             for (int k = tid; k < packs; k += NT) {
                 Pack<T> v;
                 v.load(buf + k * E);
 #pragma unroll
                 for (int j = 0; j < E; ++j) sum[j & 3] += exp2_approx(fmaf(to_f32(v.t[j]), p.c, -pm));
             }
-        } else {
-            const float mc = m > -INFINITY ? m : 0.f;
+            return warp_sum((sum[0] + sum[1]) + (sum[2] + sum[3]));
+        };
+        bool far = !(fabsf(m * p.c) < 1e30f);
+        if (!far) {
+            t = add(m * p.c);
+            far = !(t < 1e30f && t > 1e-25f);
+        }
+        if (any && far) {
+            m = -INFINITY;
             for (int k = tid; k < packs; k += NT) {
                 Pack<T> v;
                 v.load(buf + k * E);
-#pragma unroll
-                for (int j = 0; j < E; ++j) sum[j & 3] += exp2_approx((to_f32(v.t[j]) - mc) * p.c);
+                m = fmaxf(m, v.largest());
+            }
+            m = warp_largest(m);
+            if (fabsf(m * p.c) < 1e30f) {
+                t = add(m * p.c);
+            } else {
+                const float mc = m > -INFINITY ? m : 0.f;
+                sum[0] = 0.f;
+                for (int k = tid; k < packs; k += NT)
+#pragma unroll 1
+                    for (int j = 0; j < E; ++j) sum[0] += exp2_approx((to_f32(buf[k * E + j]) - mc) * p.c);
+                t = warp_sum(sum[0]);
             }
         }
-        float t = warp_sum((sum[0] + sum[1]) + (sum[2] + sum[3]));
-        if (fabsf(pm) < 1e30f) t *= exp2f(-fmaf(m, p.c, -pm));
+        if (fabsf(m * p.c) < 1e30f) t *= exp2f(-fmaf(m, p.c, -(m * p.c)));
         if (lane == 0) s.part[warp] = make_float2(m, t);
     }
-    __syncwarp();
-    cluster_arrive();
+    // (reference, sum) of n parts, a lane each (a sum without a reference is 0 or NaN)
+    auto join = [&](const float2* v, int parts, float from) -> float2 {
+        const float2 x = lane < parts ? v[lane] : make_float2(-INFINITY, 0.f);
+        const float m = fmaxf(from, warp_largest(x.x));
+        return make_float2(m, warp_sum(x.x > -INFINITY ? x.y * exp2f((x.x - m) * p.c) : x.y));
+    };
+    __syncthreads();
     cluster_wait();
+    if (warp == 0) {
+        const float2 v = join(s.part, kWarps, -INFINITY);
+        if (lane < p.cs) cluster_send(v, &s.xpart[rank], &s.xbar, lane);
+    }
+    if (!mbar_wait(&s.xbar, 0, p.status, p.wait_ns)) mbar_wait(&s.xbar, 0, p.status);
     // ---- the outcomes
     const float inv_T = p.inv_t.hi;
     float M = 0.f, total = 1.f, lnT = 0.f, sT = 1.f, lnW = 0.f;
@@ -378,20 +476,9 @@ __global__ void __launch_bounds__(NT, kBlocks) distill_kernel(const __grid_const
     };
     float P1 = 0.f, g1 = 0.f;                    // of the first entry
     if (mine) {
-        M = mS;
-        constexpr int kReads = kWarps / 4;                       // up to eight blocks' parts
-        float2 v[kReads];
-#pragma unroll
-        for (int k = 0; k < kReads; ++k) {
-            const int i = k * 32 + lane;
-            v[k] = i < p.cs * kWarps ? cluster_read(&s.part[i % kWarps], i / kWarps) : make_float2(-INFINITY, 0.f);
-            M = fmaxf(M, v[k].x);
-        }
-        M = warp_max(M);
-        float rest = 0.f;
-#pragma unroll
-        for (int k = 0; k < kReads; ++k) rest += v[k].x > -INFINITY ? v[k].y * exp2f((v[k].x - M) * p.c) : v[k].y;      // (a sum without a maximum is 0 or NaN)
-        rest = warp_sum(rest);
+        const float2 v = join(s.xpart, p.cs, mS);
+        M = v.x;
+        const float rest = v.y;
         float held = 0.f;
         sT = 0.f;
         for (int k = 0; k < nw; ++k) {
@@ -442,61 +529,9 @@ __global__ void __launch_bounds__(NT, kBlocks) distill_kernel(const __grid_const
         }
         k_rest = (g0 - A) / total;
     }
-    // ---- the loss, in pairs of floats, by the first block's support warps.  After the gradient, but for a support that
-    // does not stay in registers (its logits may be overwritten by then)
-    auto exact_loss = [&]() {
-        auto scaled = [&](float v, float m) -> FF { return v == -INFINITY ? FF{-INFINITY, 0.f} : ff_mul(two_sum(v, -m), p.inv_t); };
-        auto weights = [&](const Entry& x, bool is_first, FF& W, FF& Q) {
-            W = exp_pair(scaled(x.z, M));
-            Q = !a.tail ? exp_pair(scaled(x.lq, mT)) : is_first ? t1 : exp_ff(x.lq);
-        };
-        FF wS = {0.f, 0.f}, wQ = {0.f, 0.f}, W1 = {0.f, 0.f}, Q1 = {0.f, 0.f};
-        each([&](const Entry& x, bool is_first, long long) {
-            FF W, Q;
-            weights(x, is_first, W, Q);
-            if (is_first) {
-                W1 = W;
-                Q1 = Q;
-            }
-            wS = ff_add(wS, W);
-            if (!a.tail) wQ = ff_add(wQ, Q);
-        });
-        wS = support_sum(s, wS, 1, nw);
-        if (!a.tail) wQ = support_sum(s, wQ, 0, nw);
-        const FF sum = ff_add({rest, 0.f}, wS);
-        const FF t0 = a.tail ? s.t0 : FF{1.f, 0.f};
-        // three logs, a lane each
-        const FF ln = ln_pair(lane == 0 ? sum : lane == 1 ? (a.tail ? t0 : wQ) : FF{rest, 0.f});
-        auto lane_of = [&](FF v, int k) -> FF { return {__shfl_sync(0xffffffffu, v.hi, k), __shfl_sync(0xffffffffu, v.lo, k)}; };
-        const FF lnS = lane_of(ln, 0), ln1 = lane_of(ln, 1), lnR = lane_of(ln, 2);
-        const FF inv_S = ff_div({1.f, 0.f}, sum), inv_Q = a.tail ? FF{1.f, 0.f} : ff_div({1.f, 0.f}, wQ);
-        FF loss = {0.f, 0.f};
-        bool inf = false;
-        each([&](const Entry& x, bool is_first, long long) {
-            FF W = W1, Q = Q1;
-            if (!is_first) weights(x, false, W, Q);
-            const FF X = scaled(x.z, M);
-            const FF lp = X.hi == -INFINITY ? X : ff_add(X, ff_neg(lnS));
-            const FF lt = a.tail ? FF{x.lq, 0.f} : ff_add(scaled(x.lq, mT), ff_neg(ln1)), t = a.tail ? Q : ff_mul(Q, inv_Q);
-            const Term r = term_of(a.kind, a.beta, t, lt, ff_mul(W, inv_S), lp);
-            loss = ff_add(loss, r.f);
-            inf |= r.inf;
-        });
-        inf = __any_sync(0xffffffffu, inf);
-        if (nw > 1) {
-            if (lane == 0) s.inf[warp] = inf;
-            asm volatile("bar.sync 1, %0;" ::"r"(stride) : "memory");      // (and the sums before have been read)
-            for (int k = 0; k < nw; ++k) inf |= s.inf[k] != 0;
-        }
-        loss = support_sum(s, loss, 1, nw);
-        if (a.tail && !(rest <= 0.f)) loss = ff_add(loss, term_of(a.kind, a.beta, t0, ln1, ff_mul({rest, 0.f}, inv_S), ff_add(lnR, ff_neg(lnS))).f);
-        if (inf || !(fabsf(loss.hi) < INFINITY) || !(sum.hi > 0.f)) bits |= RL_STATUS_NONFINITE;
-        if (tid == 0) {
-            // (a row of -inf alone has no probabilities)
-            if (a.loss) a.loss[row] = !(sum.hi > 0.f) ? NAN : inf && loss.hi == loss.hi ? INFINITY : loss.hi + loss.lo;
-            if (a.mass) a.mass[row] = (wS.hi + wS.lo) / (sum.hi + sum.lo);
-        }
-    };
+    // ---- the loss, by the first block's support warps: after the gradient, but for a support that does not stay in
+    // registers (its logits may be overwritten by then)
+    auto exact_loss = [&]() { bits |= row_loss(p, s, z, row, eb, ee, first, t1, M, mT, rest, nw); };
     if (rank == 0 && !any && tid == 0) {
         if (a.loss) a.loss[row] = 0.f;
         if (a.mass) a.mass[row] = 0.f;
@@ -506,8 +541,11 @@ __global__ void __launch_bounds__(NT, kBlocks) distill_kernel(const __grid_const
         if (rank == 0 && any && mine) exact_loss();
         __syncthreads();
     }
-    __syncwarp();
-    cluster_arrive();                            // nobody leaves, or writes over logits, while they may be read
+    if (!listed) {                               // (in place: its logits are read again until here)
+        __syncthreads();
+        cluster_arrive();
+        cluster_wait();
+    }
     if (!p.grad) {
         if (rank == 0 && sv.M) {
             if (tid == 0) {
@@ -523,8 +561,6 @@ __global__ void __launch_bounds__(NT, kBlocks) distill_kernel(const __grid_const
                 }
         }
         set_status(p.status, bits);
-        __syncwarp();
-        cluster_wait();
         return;
     }
     // ---- the gradient, in place
@@ -563,9 +599,10 @@ __global__ void __launch_bounds__(NT, kBlocks) distill_kernel(const __grid_const
                 buf[x.id - at0] = from_f32<T>(w * inv_T * (g - P * A));
             });
     }
+    // (Every block of the row has read the support's logits: it sent its part after that.  So the gradient may take the
+    // logits' place.)
     fence_proxy_async_smem();
     __syncthreads();
-    cluster_wait();                             // all of the row's logits have been read: the gradient may take their place
     T* d = static_cast<T*>(a.dlogits) + row * a.grad_stride;
     const bool same = (reinterpret_cast<uintptr_t>(d) & 15) / sizeof(T) == static_cast<unsigned>(phase);
     if (same) {
