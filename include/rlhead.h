@@ -851,14 +851,13 @@ typedef struct rl_distill_args {
     float* loss;                    /* device [N]; not of the backward */
     float* mass;                    /* device [N] the student's probability of the support (0 without one); NULL to skip */
 } rl_distill_args;
-/* State that the forward leaves for the backward, 16-byte aligned. */
+/* Workspace of a forward and state that it leaves for the backward, 16-byte aligned, with any contents. */
 size_t rl_distill_saved_bytes(int64_t N, int64_t nnz);
-/* saved: device; NULL where no backward follows. */
 int rl_distill_fwd(const rl_distill_args* args, void* saved, int32_t* dev_status, void* stream);
 /* The gradients, from the same logits and support rows and what the forward saved (which stays as it is). */
 int rl_distill_bwd(const rl_distill_args* args, const void* saved, int32_t* dev_status, void* stream);
-/* Both in one pass over the logits, for a dloss known before. */
-int rl_distill_fwd_bwd(const rl_distill_args* args, int32_t* dev_status, void* stream);
+/* Both in one pass over the logits, for a dloss known before; saved is workspace only. */
+int rl_distill_fwd_bwd(const rl_distill_args* args, void* saved, int32_t* dev_status, void* stream);
 
 /* ---- utilities ------------------------------------------------------------------ */
 /* The head contraction alone: D[M, N] fp32 = A[M, K] * B[N, K]^T, A and B bf16 row-major

@@ -13,10 +13,10 @@
 // One kernel, a cluster of blocks a row: each block brings its slice of the row into shared memory by one
 // bulk copy, while it works through the row's support (few entries, every block of the cluster does them all);
 // takes the support out of the slice (-inf), so that the rest's sum is a sum and not a difference of nearly equal ones;
-// then the cluster exchanges (maximum, sum) of its slices, and each block turns its slice into the gradient
+// then the blocks send each other (reference, sum) of their slices, and each block turns its slice into the gradient
 // in place and sends it off by one bulk copy.  So logits are read once and gradients written once.
 //
-// A divergence is a small difference of the outcomes' terms: they are carried as pairs of floats (2^-44), with
+// A divergence is a small difference of the outcomes' terms: a second kernel takes it in pairs of floats (2^-38), with
 // the rest's sum of fp32 exponentials the only fp32 part; an error of it moves L in second order
 // only, since all probabilities are divided by the same total.
 #include <cfloat>
@@ -46,9 +46,11 @@ struct DistArgs {
     uint64_t wait_ns;
 };
 
-// What the forward leaves for the backward.
+// What the pass over the logits leaves for the loss and for the backward.
 struct DistSaved {
     float* M;              // [N] the row's reference logit
+    float* sum;            // [N] sum of e^((z - M) / T) outside the support
+    float* z;              // [nnz] the support's logits
     float* rest;           // [N] d L / d z of a token outside the support over its exp((z - M) / T)
     float* entry;          // [nnz] d L / d z of the support's entries
 };
@@ -56,6 +58,8 @@ static DistSaved dist_saved(void* base, int64_t N, int64_t nnz, size_t* bytes) {
     Carve c(base);
     DistSaved s;
     s.M = c.take<float>(static_cast<size_t>(N));
+    s.sum = c.take<float>(static_cast<size_t>(N));
+    s.z = c.take<float>(static_cast<size_t>(nnz));
     s.rest = c.take<float>(static_cast<size_t>(N));
     s.entry = c.take<float>(static_cast<size_t>(nnz));
     if (bytes) *bytes = align_up(c.off, 256);
@@ -136,10 +140,9 @@ struct DistShared {              // (small: three blocks with slices of 76 KB ar
     float2 xpart[8];             // (reference, sum) of each block of the cluster, without the support
     float2 part[kDistWarps];     // of each warp of this block
     float4 sup[kDistWarps];      // of each support warp: largest logit, sum relative to it, the same of the teacher's
-    FF sum[kDistWarps][2];       // pairs to be added up over the support warps
-    FF t0;                       // the teacher's probability of the rest
+    FF sum[kDistWarps];          // pairs to be added up over the support warps
+    float t0;                    // the teacher's probability of the rest
     float A[kDistWarps];
-    int inf[kDistWarps];
     float M, rest, total;
 };
 
@@ -216,80 +219,18 @@ RL_DEVINL float slope_of(int kind, float beta, float t, float lt, float P, float
     return a * P * (lp - logf(fmaf(beta, t, a * P)));
 }
 // Sum of v over the first n warps' threads (they alone call it), as a pair in every lane.
-RL_DEVINL FF support_sum(DistShared& s, FF v, int which, int n) {
+RL_DEVINL FF support_sum(FF* part, FF v, int n) {
     v = warp_sum_ff(v);
     if (n == 1) return v;
-    if ((threadIdx.x & 31) == 0) s.sum[threadIdx.x >> 5][which] = v;
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
     asm volatile("bar.sync 1, %0;" ::"r"(n * 32) : "memory");
-    v = s.sum[0][which];
-    for (int w = 1; w < n; ++w) v = ff_add(v, s.sum[w][which]);
+    v = part[0];
+    for (int w = 1; w < n; ++w) v = ff_add(v, part[w]);
     return v;
 }
-
-// The row's loss in pairs of floats, by the warps of its support (the first nw).  Returns status bits.
-template <typename T>
-__device__ __noinline__ int row_loss(const DistArgs& p, DistShared& s, const T* z, long long row, long long eb, long long ee, const Entry first,
-                                     const FF t1, float M, float mT, float rest, int nw) {
-    const rl_distill_args& a = p.a;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, stride = nw * 32;
-    auto each = [&](auto f) {
-        for (long long e = eb + tid; e < ee; e += stride) {
-            const bool is_first = e == eb + tid;
-            const Entry x = is_first ? first : entry_of(a, z, e);
-            if (x.in) f(x, is_first);
-        }
-    };
-    auto scaled = [&](float v, float m) -> FF { return v == -INFINITY ? FF{-INFINITY, 0.f} : ff_mul(two_sum(v, -m), p.inv_t); };
-    auto weights = [&](const Entry& x, bool is_first, FF& W, FF& Q) {
-        W = exp_table(scaled(x.z, M));
-        Q = !a.tail ? exp_table(scaled(x.lq, mT)) : is_first ? t1 : exp_table({x.lq, 0.f});
-    };
-    FF wS = {0.f, 0.f}, wQ = {0.f, 0.f}, W1 = {0.f, 0.f}, Q1 = {0.f, 0.f};
-    each([&](const Entry& x, bool is_first) {
-        FF W, Q;
-        weights(x, is_first, W, Q);
-        if (is_first) {
-            W1 = W;
-            Q1 = Q;
-        }
-        wS = ff_add(wS, W);
-        if (!a.tail) wQ = ff_add(wQ, Q);
-    });
-    wS = support_sum(s, wS, 1, nw);
-    if (!a.tail) wQ = support_sum(s, wQ, 0, nw);
-    const FF sum = ff_add({rest, 0.f}, wS);
-    const FF t0 = a.tail ? s.t0 : FF{1.f, 0.f};
-    // three logs, a lane each
-    const FF ln = ln_table(lane == 0 ? sum : lane == 1 ? (a.tail ? t0 : wQ) : FF{rest, 0.f});
-    auto lane_of = [&](FF v, int k) -> FF { return {__shfl_sync(0xffffffffu, v.hi, k), __shfl_sync(0xffffffffu, v.lo, k)}; };
-    const FF lnS = lane_of(ln, 0), ln1 = lane_of(ln, 1), lnR = lane_of(ln, 2);
-    const FF inv_S = ff_div({1.f, 0.f}, sum), inv_Q = a.tail ? FF{1.f, 0.f} : ff_div({1.f, 0.f}, wQ);
-    FF loss = {0.f, 0.f};
-    bool inf = false;
-    each([&](const Entry& x, bool is_first) {
-        FF W = W1, Q = Q1;
-        if (!is_first) weights(x, false, W, Q);
-        const FF X = scaled(x.z, M);
-        const FF lp = X.hi == -INFINITY ? X : ff_add(X, ff_neg(lnS));
-        const FF lt = a.tail ? FF{x.lq, 0.f} : ff_add(scaled(x.lq, mT), ff_neg(ln1)), t = a.tail ? Q : ff_mul(Q, inv_Q);
-        const Term r = term_of(a.kind, a.beta, t, lt, ff_mul(W, inv_S), lp);
-        loss = ff_add(loss, r.f);
-        inf |= r.inf;
-    });
-    inf = __any_sync(0xffffffffu, inf);
-    if (nw > 1) {
-        if (lane == 0) s.inf[warp] = inf;
-        asm volatile("bar.sync 1, %0;" ::"r"(stride) : "memory");      // (and the sums before have been read)
-        for (int k = 0; k < nw; ++k) inf |= s.inf[k] != 0;
-    }
-    loss = support_sum(s, loss, 1, nw);
-    if (a.tail && !(rest <= 0.f)) loss = ff_add(loss, term_of(a.kind, a.beta, t0, ln1, ff_mul({rest, 0.f}, inv_S), ff_add(lnR, ff_neg(lnS))).f);
-    if (tid == 0) {
-        // (a row of -inf alone has no probabilities)
-        if (a.loss) a.loss[row] = !(sum.hi > 0.f) ? NAN : inf && loss.hi == loss.hi ? INFINITY : loss.hi + loss.lo;
-        if (a.mass) a.mass[row] = (wS.hi + wS.lo) / (sum.hi + sum.lo);
-    }
-    return inf || !(fabsf(loss.hi) < INFINITY) || !(sum.hi > 0.f) ? RL_STATUS_NONFINITE : 0;
+RL_DEVINL FF rest_of(FF held) {                  // the teacher's probability of the rest
+    const FF t0 = ff_add({1.f, 0.f}, ff_neg(held));
+    return t0.hi >= kMinTail ? t0 : FF{kMinTail, 0.f};
 }
 
 template <typename T, int NT, int kBlocks>
@@ -319,6 +260,7 @@ __global__ void __launch_bounds__(NT, kBlocks) distill_kernel(const __grid_const
     T* buf = reinterpret_cast<T*>(raw);
     int bits = 0;
 
+    let_next_start();
     if (tid == NT - 1) {
         mbar_init(&s.bar, 1);
         mbar_init(&s.xbar, 1);
@@ -358,7 +300,6 @@ __global__ void __launch_bounds__(NT, kBlocks) distill_kernel(const __grid_const
         }
     };
     FF wT = {0.f, 0.f};                          // tail: the teacher's probabilities of the support
-    FF t1 = {0.f, 0.f};                          // of the first entry
     if (mine) {
         float mS = -INFINITY, mT = -INFINITY;
         for (long long e = eb + tid; e < ee; e += stride) {
@@ -370,12 +311,9 @@ __global__ void __launch_bounds__(NT, kBlocks) distill_kernel(const __grid_const
             if (x.in) {
                 mS = fmaxf(mS, x.z);
                 mT = fmaxf(mT, x.lq);
-                if (a.tail) {
-                    const FF t = exp_table({x.lq, 0.f});
-                    if (e == eb + tid) t1 = t;
-                    wT = ff_add(wT, t);
-                }
+                if (a.tail) wT = ff_add(wT, exp_table({x.lq, 0.f}));
             }
+            if (rank == 0) sv.z[e] = x.z;
         }
         mS = warp_largest(mS);
         mT = warp_largest(mT);
@@ -395,7 +333,6 @@ __global__ void __launch_bounds__(NT, kBlocks) distill_kernel(const __grid_const
         mT = fmaxf(mT, s.sup[k].z);
     }
     const bool any = mT > -INFINITY;             // the row has a teacher
-    if (mine && a.tail) wT = support_sum(s, wT, 0, nw);
     if (!mbar_wait(&s.bar, 0, p.status, p.wait_ns)) mbar_wait(&s.bar, 0, p.status);   // (the copy lands before the block goes on)
     // ---- the rest of the slice: the support out of it, then each warp's maximum and sum
     if (mine)
@@ -456,6 +393,7 @@ __global__ void __launch_bounds__(NT, kBlocks) distill_kernel(const __grid_const
         const float2 v = join(s.part, kWarps, -INFINITY);
         if (lane < p.cs) cluster_send(v, &s.xpart[rank], &s.xbar, lane);
     }
+    if (mine && a.tail) wT = support_sum(s.sum, wT, nw);
     if (!mbar_wait(&s.xbar, 0, p.status, p.wait_ns)) mbar_wait(&s.xbar, 0, p.status);
     // ---- the outcomes
     const float inv_T = p.inv_t.hi;
@@ -506,10 +444,10 @@ __global__ void __launch_bounds__(NT, kBlocks) distill_kernel(const __grid_const
             s.M = M;
             s.rest = rest;
             s.total = total;
-            if (a.tail) {
-                FF t0 = ff_add({1.f, 0.f}, ff_neg(wT));
-                if (!(t0.hi >= kMinTail)) t0 = {kMinTail, 0.f};
-                s.t0 = t0;
+            if (a.tail) s.t0 = rest_of(wT).hi;
+            if (rank == 0) {
+                sv.M[row] = M;
+                sv.sum[row] = rest;
             }
         }
     }
@@ -523,23 +461,11 @@ __global__ void __launch_bounds__(NT, kBlocks) distill_kernel(const __grid_const
         for (int k = 0; k < nw; ++k) A += s.A[k];
         float g0 = 0.f;
         if (a.tail && !(rest <= 0.f)) {
-            const float t0 = s.t0.hi, P0 = rest / total, x = slope_of(a.kind, a.beta, t0, logf(t0), P0, logf(P0));
+            const float t0 = s.t0, P0 = rest / total, x = slope_of(a.kind, a.beta, t0, logf(t0), P0, logf(P0));
             A += x;
             g0 = x / P0;
         }
         k_rest = (g0 - A) / total;
-    }
-    // ---- the loss, by the first block's support warps: after the gradient, but for a support that does not stay in
-    // registers (its logits may be overwritten by then)
-    auto exact_loss = [&]() { bits |= row_loss(p, s, z, row, eb, ee, first, t1, M, mT, rest, nw); };
-    if (rank == 0 && !any && tid == 0) {
-        if (a.loss) a.loss[row] = 0.f;
-        if (a.mass) a.mass[row] = 0.f;
-    }
-    const bool early = !listed || !p.grad;
-    if (early) {
-        if (rank == 0 && any && mine) exact_loss();
-        __syncthreads();
     }
     if (!listed) {                               // (in place: its logits are read again until here)
         __syncthreads();
@@ -547,9 +473,8 @@ __global__ void __launch_bounds__(NT, kBlocks) distill_kernel(const __grid_const
         cluster_wait();
     }
     if (!p.grad) {
-        if (rank == 0 && sv.M) {
+        if (rank == 0) {
             if (tid == 0) {
-                sv.M[row] = M;
                 sv.rest[row] = any ? k_rest * inv_T : 0.f;
             }
             if (mine)
@@ -616,9 +541,112 @@ __global__ void __launch_bounds__(NT, kBlocks) distill_kernel(const __grid_const
     } else {
         for (int q = l0 + tid; q < l1; q += NT) d[q + at0] = buf[q];
     }
-    if (rank == 0 && any && mine && !early) exact_loss();
     set_status(p.status, bits);
     if (same && tid == NT - 1) bulk_wait_read<0>();
+}
+
+// ---- the loss, in pairs of floats --------------------------------------------------------------
+// A block a row, as many of its warps as hold the support.  A kernel of its own: as the last step of a row's first
+// block it kept that block's slice of the multiprocessor for 9000 cycles, half as long again as the pass itself.
+constexpr int kLossThreads = 128, kLossWarps = kLossThreads / 32;
+
+__global__ void __launch_bounds__(kLossThreads) distill_loss_kernel(const __grid_constant__ DistArgs p, const DistSaved sv) {
+    __shared__ FF part[3][kLossWarps];
+    __shared__ float largest[kLossWarps];
+    __shared__ int infinite[kLossWarps];
+    const rl_distill_args& a = p.a;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const long long row = blockIdx.x;
+    long long eb = a.offsets[row], ee = a.offsets[row + 1];
+    if (eb < 0 || ee < eb || ee > a.nnz) eb = ee = 0;
+    const int nw = static_cast<int>(min(static_cast<long long>(kLossWarps), max((ee - eb + 31) / 32, 1ll))), stride = nw * 32;
+    if (warp >= nw) return;
+    auto entry_at = [&](long long e) -> Entry {
+        Entry x;
+        x.id = a.ids[e];
+        x.lq = a.logq[e];
+        x.in = x.id >= 0 && x.id < a.V && x.lq > -INFINITY && x.lq < INFINITY;
+        x.z = -INFINITY;
+        return x;
+    };
+    Entry first{-1, -INFINITY, 0.f, false};
+    float mT = -INFINITY;
+    for (long long e = eb + tid; e < ee; e += stride) {
+        const Entry x = entry_at(e);
+        if (e == eb + tid) first = x;
+        if (x.in) mT = fmaxf(mT, x.lq);
+    }
+    mT = warp_largest(mT);
+    if (nw > 1) {
+        if (lane == 0) largest[warp] = mT;
+        asm volatile("bar.sync 1, %0;" ::"r"(stride) : "memory");
+        for (int k = 0; k < nw; ++k) mT = fmaxf(mT, largest[k]);
+    }
+    wait_for_previous();
+    if (!(mT > -INFINITY)) {                     // no teacher
+        if (tid == 0) {
+            a.loss[row] = 0.f;
+            if (a.mass) a.mass[row] = 0.f;
+        }
+        return;
+    }
+    const float M = sv.M[row], rest = sv.sum[row];
+    auto scaled = [&](float v, float m) -> FF { return v == -INFINITY ? FF{-INFINITY, 0.f} : ff_mul(two_sum(v, -m), p.inv_t); };
+    // f(entry, W, Q) with the weights of the student's and the teacher's softmax; the thread's first stay in registers
+    FF W1 = {0.f, 0.f}, Q1 = {0.f, 0.f};
+    auto each = [&](bool again, auto f) {
+        for (long long e = eb + tid; e < ee; e += stride) {
+            const bool is_first = e == eb + tid;
+            Entry x = is_first ? first : entry_at(e);
+            if (!x.in) continue;
+            if (!is_first || !again) x.z = sv.z[e];
+            FF W = W1, Q = Q1;
+            if (!is_first || !again) {
+                W = exp_table(scaled(x.z, M));
+                Q = exp_table(a.tail ? FF{x.lq, 0.f} : scaled(x.lq, mT));
+            }
+            if (is_first && !again) {
+                first.z = x.z;
+                W1 = W;
+                Q1 = Q;
+            }
+            f(x, W, Q);
+        }
+    };
+    FF wS = {0.f, 0.f}, wQ = {0.f, 0.f};
+    each(false, [&](const Entry&, FF W, FF Q) {
+        wS = ff_add(wS, W);
+        wQ = ff_add(wQ, Q);
+    });
+    wS = support_sum(part[0], wS, nw);
+    wQ = support_sum(part[1], wQ, nw);
+    const FF sum = ff_add({rest, 0.f}, wS), t0 = a.tail ? rest_of(wQ) : FF{1.f, 0.f};
+    // three logs, a lane each
+    const FF ln = ln_table(lane == 0 ? sum : lane == 1 ? (a.tail ? t0 : wQ) : FF{rest, 0.f});
+    auto lane_of = [&](FF v, int k) -> FF { return {__shfl_sync(0xffffffffu, v.hi, k), __shfl_sync(0xffffffffu, v.lo, k)}; };
+    const FF lnS = lane_of(ln, 0), ln1 = lane_of(ln, 1), lnR = lane_of(ln, 2);
+    const FF inv_S = ff_div({1.f, 0.f}, sum), inv_Q = a.tail ? FF{1.f, 0.f} : ff_div({1.f, 0.f}, wQ);
+    FF loss = {0.f, 0.f};
+    bool inf = false;
+    each(true, [&](const Entry& x, FF W, FF Q) {
+        const FF X = scaled(x.z, M);
+        const FF lp = X.hi == -INFINITY ? X : ff_add(X, ff_neg(lnS));
+        const FF lt = a.tail ? FF{x.lq, 0.f} : ff_add(scaled(x.lq, mT), ff_neg(ln1)), t = a.tail ? Q : ff_mul(Q, inv_Q);
+        const Term r = term_of(a.kind, a.beta, t, lt, ff_mul(W, inv_S), lp);
+        loss = ff_add(loss, r.f);
+        inf |= r.inf;
+    });
+    inf = __any_sync(0xffffffffu, inf);
+    if (lane == 0) infinite[warp] = inf;
+    loss = support_sum(part[2], loss, nw);
+    for (int k = 0; k < nw; ++k) inf |= nw > 1 && infinite[k] != 0;
+    if (a.tail && !(rest <= 0.f)) loss = ff_add(loss, term_of(a.kind, a.beta, t0, ln1, ff_mul({rest, 0.f}, inv_S), ff_add(lnR, ff_neg(lnS))).f);
+    if (tid == 0) {
+        // (a row of -inf alone has no probabilities)
+        a.loss[row] = !(sum.hi > 0.f) ? NAN : inf && loss.hi == loss.hi ? INFINITY : loss.hi + loss.lo;
+        if (a.mass) a.mass[row] = (wS.hi + wS.lo) / (sum.hi + sum.lo);
+        if (inf || !(fabsf(loss.hi) < INFINITY) || !(sum.hi > 0.f)) set_status(p.status, RL_STATUS_NONFINITE);
+    }
 }
 
 // ---- the backward alone: gradients from what the forward saved --------------------------------
@@ -701,8 +729,9 @@ static int distill_launch(const DistArgs& p, const DistSaved& sv, cudaStream_t s
     cfg.numAttrs = 1;
     ProfScope prof(RL_PROF_OTHER, stream);
     if (cudaLaunchKernelEx(&cfg, distill_kernel<T, NT, kBlocks>, p, sv) != cudaSuccess) return RL_ERR_CUDA;
-    count_launch();
-    return cudaPeekAtLastError() == cudaSuccess ? RL_OK : RL_ERR_CUDA;
+    const int rc = launch_after(distill_loss_kernel, dim3(static_cast<unsigned>(p.a.N)), kLossThreads, 0, true, stream, p, sv);
+    count_launch(2);
+    return rc == RL_OK && cudaPeekAtLastError() == cudaSuccess ? RL_OK : RL_ERR_CUDA;
 }
 
 template <typename T>
@@ -742,8 +771,7 @@ int distill_impl(const rl_distill_args* a, int pass, void* saved, int32_t* statu
     if (a->N == 0) return RL_OK;
     DistArgs p = dist_args(a, status);
     p.grad = pass == kDistillBoth;
-    DistSaved sv{nullptr, nullptr, nullptr};
-    if (saved) sv = dist_saved(saved, a->N, a->nnz, nullptr);
+    const DistSaved sv = dist_saved(saved, a->N, a->nnz, nullptr);
     if (pass == kDistillBwd)
         return a->dtype == RL_DTYPE_F32 ? distill_bwd_run<float>(p, sv, stream)
                : a->dtype == RL_DTYPE_BF16 ? distill_bwd_run<__nv_bfloat16>(p, sv, stream) : distill_bwd_run<__half>(p, sv, stream);

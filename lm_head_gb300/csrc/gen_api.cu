@@ -305,7 +305,7 @@ int rl_page_copy(const rl_page_copy_args* a, int32_t* dev_status, void* stream) 
 size_t rl_distill_saved_bytes(int64_t N, int64_t nnz) { return N < 0 || nnz < 0 ? 0 : distill_saved_bytes(N, nnz); }
 
 int rl_distill_fwd(const rl_distill_args* a, void* saved, int32_t* dev_status, void* stream) {
-    if (!aligned(saved, 16)) return fail(RL_ERR_ARG, "saved not 16-byte aligned");
+    if (!saved || !aligned(saved, 16)) return fail(RL_ERR_ARG, "saved is NULL or not 16-byte aligned");
     const int rc = check_distill(a, dev_status, kDistillFwd);
     return rc != RL_OK ? rc : distill_impl(a, kDistillFwd, saved, dev_status, static_cast<cudaStream_t>(stream));
 }
@@ -316,9 +316,10 @@ int rl_distill_bwd(const rl_distill_args* a, const void* saved, int32_t* dev_sta
     return rc != RL_OK ? rc : distill_impl(a, kDistillBwd, const_cast<void*>(saved), dev_status, static_cast<cudaStream_t>(stream));
 }
 
-int rl_distill_fwd_bwd(const rl_distill_args* a, int32_t* dev_status, void* stream) {
+int rl_distill_fwd_bwd(const rl_distill_args* a, void* saved, int32_t* dev_status, void* stream) {
+    if (!saved || !aligned(saved, 16)) return fail(RL_ERR_ARG, "saved is NULL or not 16-byte aligned");
     const int rc = check_distill(a, dev_status, kDistillBoth);
-    return rc != RL_OK ? rc : distill_impl(a, kDistillBoth, nullptr, dev_status, static_cast<cudaStream_t>(stream));
+    return rc != RL_OK ? rc : distill_impl(a, kDistillBoth, saved, dev_status, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

@@ -23,7 +23,7 @@ SIGS = {
     "rl_distill_saved_bytes": (ctypes.c_size_t, [_I64, _I64]),
     "rl_distill_fwd": (ctypes.c_int, [_P, _P, _P, _P]),
     "rl_distill_bwd": (ctypes.c_int, [_P, _P, _P, _P]),
-    "rl_distill_fwd_bwd": (ctypes.c_int, [_P, _P, _P]),
+    "rl_distill_fwd_bwd": (ctypes.c_int, [_P, _P, _P, _P]),
 }
 _pack = _packer(RlDistillArgs)
 
@@ -42,8 +42,8 @@ class DistillParams:
 class DistillOut:
     loss: torch.Tensor              # [N] fp32
     mass: torch.Tensor              # [N] fp32: the student's probability of the support
+    saved: torch.Tensor             # workspace; what the forward leaves for the backward
     status: torch.Tensor
-    saved: Optional[torch.Tensor] = None    # the forward's, for the backward
 
     def status_bits(self) -> int:
         return int(self.status.item())
@@ -60,12 +60,16 @@ def _head(logits, offsets, ids, logq, p):
             _dev("logq", logq, torch.float32, nnz), nnz)
 
 
-def _outputs(logits, out, status, stream):
+def _outputs(logits, nnz, out, status, stream):
+    N = logits.shape[0]
+    n = int(_load().rl_distill_saved_bytes(N, nnz))
     if out is None:
         with _on(stream):
-            dev, N = logits.device, logits.shape[0]
-            e = lambda: torch.empty(N, dtype=torch.float32, device=dev)  # noqa: E731
-            return DistillOut(e(), e(), _status(status, dev))
+            dev = logits.device
+            e = lambda k, t: torch.empty(k, dtype=t, device=dev)  # noqa: E731
+            return DistillOut(e(N, torch.float32), e(N, torch.float32), e(max(n, 1), torch.uint8), _status(status, dev))
+    if out.saved.numel() < n:
+        raise _err(f"out.saved: expected {n} bytes")
     return out if status is None else dataclasses.replace(out, status=status)
 
 
@@ -84,23 +88,15 @@ def _tail_args(o, N):
     return _dev("out.loss", o.loss, f32, N), _dev("out.mass", o.mass, f32, N, True)
 
 
-def rl_distill_fwd(logits, offsets, ids, logq, params: DistillParams, *, save: bool = True, out: Optional[DistillOut] = None,
-                   status=None, stream=None) -> DistillOut:
+def rl_distill_fwd(logits, offsets, ids, logq, params: DistillParams, *, out: Optional[DistillOut] = None, status=None,
+                   stream=None) -> DistillOut:
     """The loss of each row of `logits` [N, V] against its support row of a teacher (offsets [N+1] int64, ids int32
-    ascending, logq fp32).  save: also keep what rl_distill_bwd needs (out.saved)."""
+    ascending, logq fp32), and what rl_distill_bwd needs (out.saved)."""
     head = _head(logits, offsets, ids, logq, params)
-    N, nnz = logits.shape[0], ids.numel()
-    out = _outputs(logits, out, status, stream)
-    if save:
-        n = int(_load().rl_distill_saved_bytes(N, nnz))
-        if out.saved is None:
-            with _on(stream):
-                out = dataclasses.replace(out, saved=torch.empty(max(n, 1), dtype=torch.uint8, device=logits.device))
-        elif out.saved.numel() < n:
-            raise _err(f"out.saved: expected {n} bytes")
-    saved = _dev("out.saved", out.saved, torch.uint8) if save else 0
-    a = _pack(*head, 0, 0, 0, *_tail_args(out, N))
-    _check(_load().rl_distill_fwd(a, saved, _dev("status", out.status, torch.int32, 1), _stream(stream, logits)))
+    out = _outputs(logits, ids.numel(), out, status, stream)
+    a = _pack(*head, 0, 0, 0, *_tail_args(out, logits.shape[0]))
+    _check(_load().rl_distill_fwd(a, _dev("out.saved", out.saved, torch.uint8), _dev("status", out.status, torch.int32, 1),
+                                  _stream(stream, logits)))
     return out
 
 
@@ -125,9 +121,10 @@ def rl_distill_fwd_bwd(logits, offsets, ids, logq, dloss, params: DistillParams,
     """Loss and gradients in one pass over the logits; dlogits may be logits.  Returns (out, dlogits)."""
     head = _head(logits, offsets, ids, logq, params)
     N = logits.shape[0]
-    out = _outputs(logits, out, status, stream)
+    out = _outputs(logits, ids.numel(), out, status, stream)
     d = _grad(logits, dlogits, stream)
     a = _pack(*head, _dev("dloss", dloss, torch.float32, N), d.data_ptr(), d.stride(0) if N > 1 else logits.shape[1],
               *_tail_args(out, N))
-    _check(_load().rl_distill_fwd_bwd(a, _dev("status", out.status, torch.int32, 1), _stream(stream, logits)))
+    _check(_load().rl_distill_fwd_bwd(a, _dev("out.saved", out.saved, torch.uint8), _dev("status", out.status, torch.int32, 1),
+                                      _stream(stream, logits)))
     return out, d

@@ -33,15 +33,16 @@ def test_refusals(lib):  # noqa: F811
     for changes, call in (
             (COMMON + [(dict(loss=None), ARG)], lambda a: lib.rl_distill_fwd(a, FAKE, FAKE, None)),
             (COMMON + GRAD, lambda a: lib.rl_distill_bwd(a, FAKE, FAKE, None)),
-            (COMMON + GRAD + [(dict(loss=None), ARG)], lambda a: lib.rl_distill_fwd_bwd(a, FAKE, None))):
+            (COMMON + GRAD + [(dict(loss=None), ARG)], lambda a: lib.rl_distill_fwd_bwd(a, FAKE, FAKE, None))):
         for change, want in changes:
             assert call(ctypes.byref(make(**change))) == want, change
         assert call(None) == ARG
     a = ctypes.byref(make())
     assert lib.rl_distill_fwd(a, FAKE, None, None) == ARG                # no status word
     assert lib.rl_distill_bwd(a, None, FAKE, None) == ARG                # nothing saved
-    assert lib.rl_distill_fwd(a, FAKE + 8, FAKE, None) == ARG
-    assert rh.load().rl_distill_saved_bytes(-1, 0) == 0 and rh.load().rl_distill_saved_bytes(10, 20) >= 4 * 40
+    assert lib.rl_distill_fwd(a, FAKE + 8, FAKE, None) == ARG and lib.rl_distill_fwd(a, None, FAKE, None) == ARG
+    assert lib.rl_distill_fwd_bwd(a, None, FAKE, None) == ARG
+    assert rh.load().rl_distill_saved_bytes(-1, 0) == 0 and rh.load().rl_distill_saved_bytes(10, 20) >= 4 * 70
     assert ctypes.sizeof(ds.RlDistillArgs) == 4 * 8 + 6 * 4 + 9 * 8
 
 

@@ -281,7 +281,7 @@ def test_gradient_against_differences(kind, tail):
     p = rh.DistillParams(kind=kind, tail=tail, temperature=T, beta=0.35)
     n = 2 * V
     off = torch.arange(n + 1, device="cuda") * 7
-    o = rh.rl_distill_fwd(rows, off, c["ids"].repeat(n), c["q"].repeat(n), p, save=False)
+    o = rh.rl_distill_fwd(rows, off, c["ids"].repeat(n), c["q"].repeat(n), p)
     got = (o.loss[:V].double() - o.loss[V:].double()) / step
     _, d = rh.rl_distill_fwd_bwd(c["z"], c["off"], c["ids"], c["q"], torch.ones(1, device="cuda"), p)
     size = float(o.loss.abs().max()) + 1
