@@ -6,14 +6,13 @@
 //
 //  1. chunk_kernel     the only pass over all rows of logits: a warp per 4 KB, its largest logit and the sum of its
 //                      weights in fp32.  Rows that no request looks at (a draft's row behind its last draft) are left out.
-//  2. request_kernel   a cluster of blocks a request: every block puts the rows' totals together and compares; a comparison
-//                      nearer than the bound of the fp32 sums' error is taken again with sums that are good to 2^-36.  Then
-//                      the row of the new token, a slice of the vocabulary a block: the sums of its parts of 128 as
-//                      integers (float-pair weights, see weights.cuh) of the target's weights, of
-//                      the draft's where it has logits, and of what is left, max(p - q, 0); the cluster adds them up,
-//                      and the block in whose slice the random number falls scans it.
-//                      With a draft's support row only its few tokens' probabilities are taken off the target's parts.
-//                      A target's support row is drawn from by one block.
+//  2. decide_kernel    a block a request: puts the rows' totals together and compares; a comparison nearer than the bound
+//                      of the fp32 sums' error is taken again with sums that are good to 2^-36.  Draws from support rows.
+//  3. draw_kernel      a cluster of blocks a request whose new token comes from a row of logits, a slice of the vocabulary a
+//                      block: the sums of its parts of 128 as integers (float-pair weights, see weights.cuh) of the target's
+//                      weights, of the draft's where it has logits, and of what is left, max(p - q, 0); the cluster adds them
+//                      up, and the block in whose slice the random number falls scans it.  With a draft's support row only
+//                      its few tokens' probabilities are taken off the target's parts.
 #include <cfloat>
 #include <climits>
 #include <cmath>
@@ -27,8 +26,9 @@
 namespace rl {
 
 constexpr int kVerPart = 128;                  // logits of a part
-constexpr int kVerThreads = 512;
-constexpr int kVerWarps = kVerThreads / 32;
+constexpr int kVerStep = 4;                    // parts that a warp sums up at a time
+constexpr int kDecideThreads = 512;            // a row of either side a warp
+constexpr int kDrawThreads = 256;
 constexpr int kChunkThreads = 256;
 constexpr int kChunkPacks = 8;                 // 16-byte loads of a lane: 4 KB a warp
 constexpr int kUsedRows = 32768;               // rows of a step whose use is looked up in shared memory
@@ -45,7 +45,8 @@ struct VerArgs {
     VerSide side[2];    // target, draft
     int32_t* status;
     bool sure;          // no draft distribution
-    int cs, per;        // blocks a request; parts of a block's slice
+    int cs, per;        // blocks of a request's draw; steps of a block's slice
+    struct VerDraw* draws;      // [R] (NULL: no logits on either side)
 };
 
 // The row of the distribution that the step's row t has; -1 where there is none.
@@ -208,55 +209,37 @@ enum { kDistNone, kDistDense, kDistPoint, kDistSupport };
 // A row's distribution.
 struct VerRow {
     int mode, dtype, at;            // kDistPoint: all of it on `at`
-    const rl_dist* d;
+    int prec;                       // sums are in units of 2^-prec
     long long row, eb, ee;
     float M, S;                     // largest logit, fp32 sum of e^((z - M) / T)
     FF c;                           // log2(e) / T
-    bool plain, vec;                // weights are 2^(z c - R), else 2^((z - M) c - R) with R = 0
-    float R;
-    int prec;                       // their sums are in units of 2^-prec
-    unsigned long long total;       // ... the sum of all of them
+    float inv_c, R;                 // weights are 2^(z c - R) where `plain`, else 2^((z - M) c) with R = 0
+    int plain, vec;
+    unsigned long long total;       // the sum of all weights, once it is counted
+};
+// What a request's new token is drawn from.
+struct VerDraw {
+    long long t;                    // -1: nothing is left to draw
+    float u;
+    int refused;
+    VerRow row[2];
 };
 
+template <int NT>
 struct VerShared {
     float2 tab[2048];
-    unsigned long long red[kVerWarps];
+    unsigned long long red[NT / 32];
     unsigned long long xch[2];
-    VerRow row[2];
-    int res[kVerWarps];
-    float lp[kVerWarps];
-    int flag;
+    VerDraw draw;
+    VerRow rows[NT / 32];           // the rows of a stretch of the request, target and draft in turn
+    float lp[NT / 32];              // log2 of the candidate's probability
+    int bits[NT / 32];
+    int flag, token;
     float lpx;
-    int token;
     FF lam;                         // log2 of the draft's total over the target's, as they are counted
     unsigned long long unit;
 };
 
-RL_DEVINL unsigned long long vblock_sum(unsigned long long v, unsigned long long* red) {
-    v = warp_sum(v);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-    __syncthreads();
-    unsigned long long s = 0;
-#pragma unroll
-    for (int w = 0; w < kVerWarps; ++w) s += red[w];
-    return s;
-}
-RL_DEVINL unsigned long long vblock_scan(unsigned long long v, unsigned long long* red) {      // exclusive
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    unsigned long long i = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const unsigned long long x = __shfl_up_sync(0xffffffffu, i, o);
-        if (lane >= o) i += x;
-    }
-    __syncthreads();
-    if (lane == 31) red[warp] = i;
-    __syncthreads();
-    unsigned long long p = 0;
-    for (int w = 0; w < warp; ++w) p += red[w];
-    return p + i - v;
-}
 // hi + lo (normalised, 0 <= it < 2) in units of 2^-k, k <= 60
 RL_DEVINL unsigned long long fixed_of(float hi, float lo, int k) {
     if (!(hi > 0.f)) return 0ull;
@@ -267,110 +250,260 @@ RL_DEVINL unsigned long long fixed_of(float hi, float lo, int k) {
     const long long v = static_cast<long long>(w) + __float2ll_rn(lo * power_of_2(k));
     return v > 0 ? static_cast<unsigned long long>(v) : 0ull;
 }
-// The weight of a logit over 2^ref (as in VerRow) times 2^-lam, as a normalised pair.  ref + the row's R holds lam's part in
-// steps of 2^-11, lam_lo the rest; the weight is below 2.
-RL_DEVINL FF weight_of(float z, const VerRow& w, float ref, float lam_lo, const float2* tab) {
-    float x = z, xl = 0.f;
-    if (!w.plain) {
-        const FF d = two_sum(z, -w.M);
-        x = d.hi;
-        xl = d.lo;
-    }
-    const float magic = 6144.f - (w.R + ref);
-    const float t = fmaf(x, w.c.hi, magic);
-    float r = fmaf(x, w.c.hi, -__fsub_rn(t, magic));
-    r = fmaf(x, w.c.lo, r);
-    r = fmaf(xl, w.c.hi, r) - lam_lo;
+// 2^(x c - ref - lam_lo) as a normalised pair, below 2; magic = 6144 - ref with ref in steps of 2^-11 (see weight_pair; with
+// lam_lo |r| may be 2^-11, so 2^r - 1 goes to the third power).
+RL_DEVINL FF weight_off(float x, float xl, FF c, float magic, float lam_lo, const float2* tab) {
+    const float t = fmaf(x, c.hi, magic);
+    float r = fmaf(x, c.hi, -__fsub_rn(t, magic));
+    r = fmaf(x, c.lo, r);
+    r = fmaf(xl, c.hi, r) - lam_lo;
     const uint32_t tb = __float_as_uint(t);
     const float2 q = tab[tb & 2047u];
     const float hi = __uint_as_float(__float_as_uint(q.x) + (tb << 12));
-    // 2^r - 1 to the third power: with lam_lo |r| may be 2^-11
     return fast_two_sum(hi, hi * fmaf(r, fmaf(r, fmaf(r, 0.05550410866482158f, 0.24022650695910072f), 0.69314718055994531f), q.y));
+}
+// The weight of a logit over 2^ref (as in VerRow) times 2^-lam.  ref holds lam's part in steps of 2^-11, lam_lo the rest.
+RL_DEVINL FF weight_of(float z, const VerRow& w, float ref, float lam_lo, const float2* tab) {
+    const FF d = w.plain ? FF{z, 0.f} : two_sum(z, -w.M);
+    return weight_off(d.hi, d.lo, w.c, 6144.f - (w.R + ref), lam_lo, tab);
 }
 // The logit at which the exponent over 2^ref is e.
 RL_DEVINL float logit_of(const VerRow& w, float ref, float e) {
-    const float x = (ref + w.R + e) / w.c.hi;
+    const float x = (ref + w.R + e) * w.inv_c;
     return w.plain ? x : w.M + x;
 }
+// max(v - q, 0) of normalised pairs
+RL_DEVINL FF left_of(FF v, FF q) {
+    if (!(v.hi >= q.hi)) return {0.f, 0.f};
+    const float d = __fsub_rn(v.hi, q.hi);
+    const FF r = two_sum(d, __fadd_rn(__fsub_rn(__fsub_rn(v.hi, d), q.hi), __fsub_rn(v.lo, q.lo)));
+    return r.hi > 0.f ? r : FF{0.f, 0.f};
+}
 
-struct Four {
-    uint32_t w[4];
-};
-// Four logits of a part by a lane, as they lie in memory (past the row's end -inf), and as numbers.
-RL_DEVINL Four four_raw(const VerRow& r, int V, int i) {
-    Four f;
-    const long long base = r.row * r.d->row_stride;
+// A lane's logits of kVerStep parts from element i0 on, four of each, past the row's end -inf.
+RL_DEVINL void step_load(const rl_dist& d, const VerRow& r, int V, int i0, float (&z)[kVerStep][4]) {
+    const int lane = threadIdx.x & 31;
+    const long long base = r.row * d.row_stride;
+    const bool whole = r.vec && i0 + kVerStep * kVerPart <= V;
     if (r.dtype == RL_DTYPE_F32) {
-        const float* p = static_cast<const float*>(r.d->logits) + base;
-        if (r.vec && i + 4 <= V) {
-            const uint4 q = *reinterpret_cast<const uint4*>(p + i);
-            f.w[0] = q.x; f.w[1] = q.y; f.w[2] = q.z; f.w[3] = q.w;
+        const float* p = static_cast<const float*>(d.logits) + base + i0 + lane * 4;
+        if (whole) {
+#pragma unroll
+            for (int s = 0; s < kVerStep; ++s) {
+                const float4 q = *reinterpret_cast<const float4*>(p + s * kVerPart);
+                z[s][0] = q.x; z[s][1] = q.y; z[s][2] = q.z; z[s][3] = q.w;
+            }
         } else {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) f.w[j] = i + j < V ? __float_as_uint(p[i + j]) : 0xff800000u;
+            for (int s = 0; s < kVerStep; ++s)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) z[s][j] = i0 + s * kVerPart + lane * 4 + j < V ? p[s * kVerPart + j] : -INFINITY;
         }
+        return;
+    }
+    const uint16_t* p = static_cast<const uint16_t*>(d.logits) + base + i0 + lane * 4;
+    uint2 q[kVerStep];
+    if (whole) {
+#pragma unroll
+        for (int s = 0; s < kVerStep; ++s) q[s] = *reinterpret_cast<const uint2*>(p + s * kVerPart);
     } else {
-        const uint16_t* p = static_cast<const uint16_t*>(r.d->logits) + base;
-        if (r.vec && i + 4 <= V) {
-            const uint2 q = *reinterpret_cast<const uint2*>(p + i);
-            f.w[0] = q.x; f.w[1] = q.y;
-        } else {
-            const uint32_t none = r.dtype == RL_DTYPE_BF16 ? 0xff80u : 0xfc00u;
+        const uint32_t none = r.dtype == RL_DTYPE_BF16 ? 0xff80u : 0xfc00u;
+#pragma unroll
+        for (int s = 0; s < kVerStep; ++s) {
             uint32_t h[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) h[j] = i + j < V ? p[i + j] : none;
-            f.w[0] = h[0] | h[1] << 16;
-            f.w[1] = h[2] | h[3] << 16;
+            for (int j = 0; j < 4; ++j) h[j] = i0 + s * kVerPart + lane * 4 + j < V ? p[s * kVerPart + j] : none;
+            q[s] = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
         }
-        f.w[2] = f.w[3] = 0;
     }
-    return f;
-}
-RL_DEVINL void four_get(const Four& f, int dtype, float (&z)[4]) {
+    if (r.dtype == RL_DTYPE_BF16) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        if (dtype == RL_DTYPE_F32) {
-            z[j] = __uint_as_float(f.w[j]);
-        } else {
-            const uint32_t w = f.w[j >> 1], h = (j & 1) ? w >> 16 : w & 0xffffu;
-            z[j] = dtype == RL_DTYPE_BF16 ? __uint_as_float(h << 16) : __half2float(__ushort_as_half(static_cast<unsigned short>(h)));
+        for (int s = 0; s < kVerStep; ++s) {
+            z[s][0] = __uint_as_float(q[s].x << 16);
+            z[s][1] = __uint_as_float(q[s].x & 0xffff0000u);
+            z[s][2] = __uint_as_float(q[s].y << 16);
+            z[s][3] = __uint_as_float(q[s].y & 0xffff0000u);
         }
-        z[j] = (z[j] < INFINITY ? z[j] : -INFINITY) + 0.f;
+    } else {
+#pragma unroll
+        for (int s = 0; s < kVerStep; ++s) {
+            const __half2 a = *reinterpret_cast<const __half2*>(&q[s].x), b = *reinterpret_cast<const __half2*>(&q[s].y);
+            z[s][0] = __low2float(a); z[s][1] = __high2float(a); z[s][2] = __low2float(b); z[s][3] = __high2float(b);
+        }
     }
 }
+// The warp's largest of them; NaN and +inf become -inf.
+RL_DEVINL float step_largest(float (&z)[kVerStep][4]) {
+    float m = -INFINITY;
+#pragma unroll
+    for (int s = 0; s < kVerStep; ++s)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) m = max_nan(m, z[s][j]);
+    uint32_t key = __reduce_max_sync(0xffffffffu, key_of(m + 0.f));
+    if (key >= 0xff800000u) {
+        m = -INFINITY;
+#pragma unroll
+        for (int s = 0; s < kVerStep; ++s)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                z[s][j] = z[s][j] < INFINITY ? z[s][j] : -INFINITY;
+                m = fmaxf(m, z[s][j]);
+            }
+        key = __reduce_max_sync(0xffffffffu, key_of(m + 0.f));
+    }
+    return z_of(key);
+}
 
-struct Request {
-    const VerArgs& g;
-    VerShared& s;
-    unsigned long long* cs;       // [per] sums of the slice's parts
-    int V, tid, lane, warp, rank, p0, p1;      // its parts
-    int phase;
-
-    // The cluster's sum of v (the same in a block's threads), and the sum of the blocks before.
-    RL_DEVINL unsigned long long cluster_sum(unsigned long long v, unsigned long long& before) {
-        before = 0;
-        if (g.cs == 1) return v;
-        unsigned long long* slot = &s.xch[phase & 1];
-        ++phase;
-        if (tid == 0) *slot = v;
-        __syncthreads();
-        cluster_arrive();
-        cluster_wait();
-        unsigned long long total = 0;
-        for (int k = 0; k < g.cs; ++k) {
-            unsigned long long x;
-            asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(x) : "r"(cluster_addr(slot, k)) : "memory");
-            if (k < rank) before += x;
-            total += x;
+// Sums of the weights of `steps` steps of a row from step `from` on, by a warp that takes every `stride`-th; the parts' sums
+// into cs where it is given.  Each step is summed relative to its own largest weight.  Lane 0 has the sum.
+__device__ __noinline__ unsigned long long sum_steps(const rl_dist& d, const VerRow* row, int V, int from, int steps, int first, int stride,
+                                                     unsigned long long* cs, const float2* tab) {
+    const VerRow w = *row;
+    const int lane = threadIdx.x & 31;
+    unsigned long long mine = 0;
+#pragma unroll 1
+    for (int k = first; k < steps; k += stride) {
+        float z[kVerStep][4];
+        step_load(d, w, V, (from + k) * kVerStep * kVerPart, z);
+        const float m = step_largest(z);
+        const float ex = w.plain ? fmaf(m, w.c.hi, -w.R) : (m - w.M) * w.c.hi;
+        unsigned long long sum = 0;
+        if (ex > -100.f) {                       // (also not for -inf: below, the step is nothing beside the row)
+            const float ref = fminf(ceilf(ex), 1.f), magic = 6144.f - (w.R + ref);
+            const float zlow = fmaxf(logit_of(w, ref, -64.f), -FLT_MAX);
+            uint32_t top = 0;
+            int low = 0;
+#pragma unroll
+            for (int s = 0; s < kVerStep; ++s) {
+                LaneSum acc;
+                float hi[4], v[4];
+                if (w.plain) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) weight_pair(fmaxf(z[s][j], zlow), 0.f, w.c, magic, tab, hi[j], v[j]);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const FF x = two_sum(fmaxf(z[s][j], zlow), -w.M);
+                        weight_pair(x.hi, x.lo, w.c, magic, tab, hi[j], v[j]);
+                    }
+                }
+                const float least = fminf(fminf(z[s][0], z[s][1]), fminf(z[s][2], z[s][3]));
+                if (__any_sync(0xffffffffu, least < zlow)) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (z[s][j] < zlow) hi[j] = v[j] = 0.f;
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc.add(hi[j], v[j]);
+                const uint32_t t = acc.warp_top();
+                const int l = acc.warp_low();
+                if (lane == s) {
+                    top = t;
+                    low = l;
+                }
+            }
+            const unsigned long long w50 = LaneSum::total(top, low);
+            const int sh = w.prec - 50 + static_cast<int>(ref);
+            sum = sh >= 0 ? w50 << sh : sh > -64 ? (w50 + (1ull << (-sh - 1))) >> -sh : 0ull;
         }
-        return total;
+        if (lane < kVerStep) {
+            if (cs) cs[k * kVerStep + lane] = sum;
+            mine += sum;
+        }
+    }
+    mine = lane < kVerStep ? mine : 0ull;
+    return warp_sum(mine);
+}
+// The same of what is left of a target's weights beside a draft's logits.
+__device__ __noinline__ unsigned long long sum_left(const rl_dist& dp, const VerRow* rp, const rl_dist& dq, const VerRow* rq, FF lam, int V, int from,
+                                                    int steps, int first, int stride, unsigned long long* cs, const float2* tab) {
+    const VerRow w = *rp, o = *rq;
+    const int lane = threadIdx.x & 31;
+    const float lam_hi = rintf(lam.hi * 2048.f) * (1.f / 2048.f), lam_lo = (lam.hi - lam_hi) + lam.lo;
+    unsigned long long mine = 0;
+#pragma unroll 1
+    for (int k = first; k < steps; k += stride) {
+        float z[kVerStep][4], y[kVerStep][4];
+        step_load(dp, w, V, (from + k) * kVerStep * kVerPart, z);
+        step_load(dq, o, V, (from + k) * kVerStep * kVerPart, y);
+        const float m = step_largest(z);
+        const float ex = w.plain ? fmaf(m, w.c.hi, -w.R) : (m - w.M) * w.c.hi;
+        unsigned long long sum = 0;
+        if (ex > -100.f) {
+            const float ref = fminf(ceilf(ex), 1.f), ref_q = ref + lam_hi;
+            const float zlow = fmaxf(logit_of(w, ref, -64.f), -FLT_MAX), ylow = fmaxf(logit_of(o, ref_q, -64.f), -FLT_MAX),
+                        yhigh = logit_of(o, ref_q, 0.75f);
+            uint32_t top = 0;
+            int low = 0;
+#pragma unroll
+            for (int s = 0; s < kVerStep; ++s) {
+                LaneSum acc;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    FF v = weight_of(fmaxf(z[s][j], zlow), w, ref, 0.f, tab);
+                    const float x = y[s][j] < INFINITY ? y[s][j] : -INFINITY;
+                    FF q = weight_of(fminf(fmaxf(x, ylow), yhigh), o, ref_q, lam_lo, tab);
+                    if (x < ylow) q = {0.f, 0.f};
+                    v = left_of(v, q);
+                    if (z[s][j] < zlow) v = {0.f, 0.f};
+                    acc.add(v.hi, v.lo);
+                }
+                const uint32_t t = acc.warp_top();
+                const int l = acc.warp_low();
+                if (lane == s) {
+                    top = t;
+                    low = l;
+                }
+            }
+            const unsigned long long w50 = LaneSum::total(top, low);
+            const int sh = w.prec - 50 + static_cast<int>(ref);
+            sum = sh >= 0 ? w50 << sh : sh > -64 ? (w50 + (1ull << (-sh - 1))) >> -sh : 0ull;
+        }
+        if (lane < kVerStep) {
+            cs[k * kVerStep + lane] = sum;
+            mine += sum;
+        }
+    }
+    mine = lane < kVerStep ? mine : 0ull;
+    return warp_sum(mine);
+}
+
+template <int NT>
+struct Request {
+    static constexpr int kWarps = NT / 32;
+    const VerArgs& g;
+    VerShared<NT>& s;
+    int V, tid, lane, warp;
+
+    RL_DEVINL unsigned long long block_sum(unsigned long long v) {
+        v = warp_sum(v);
+        __syncthreads();
+        if (lane == 0) s.red[warp] = v;
+        __syncthreads();
+        unsigned long long x = 0;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) x += s.red[w];
+        return x;
+    }
+    RL_DEVINL unsigned long long block_scan(unsigned long long v) {      // exclusive
+        unsigned long long i = v;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const unsigned long long x = __shfl_up_sync(0xffffffffu, i, o);
+            if (lane >= o) i += x;
+        }
+        __syncthreads();
+        if (lane == 31) s.red[warp] = i;
+        __syncthreads();
+        unsigned long long p = 0;
+        for (int w = 0; w < warp; ++w) p += s.red[w];
+        return p + i - v;
     }
 
     // One warp: the step's row t on one side, its fp32 total put together.
     RL_DEVINL VerRow row_at(int side, long long t, int& bits) {
         VerRow x{};
         const VerSide& sd = g.side[side];
-        x.d = &sd.d;
         x.dtype = sd.dtype;
         if (side == 1 && g.sure) {
             x.mode = kDistPoint;
@@ -391,9 +524,17 @@ struct Request {
         }
         const float T = temperature_of(sd.d, x.row, bits);
         const float2* part = sd.part + t * sd.nc;
+        // (most rows' parts stay in registers)
+        constexpr int kKept = 6;
+        float2 v[kKept];
         float M = -INFINITY;
-        for (int i = lane; i < sd.nc; i += 32) M = fmaxf(M, part[i].x);
-        M = warp_max(M);
+#pragma unroll
+        for (int k = 0; k < kKept; ++k) {
+            v[k] = k * 32 + lane < sd.nc ? part[k * 32 + lane] : make_float2(-INFINITY, 0.f);
+            M = fmaxf(M, v[k].x);
+        }
+        for (int i = kKept * 32 + lane; i < sd.nc; i += 32) M = fmaxf(M, part[i].x);
+        M = z_of(__reduce_max_sync(0xffffffffu, key_of(M + 0.f)));
         if (!(M > -INFINITY)) return x;
         x.M = M;
         if (T == 0.f) {
@@ -405,10 +546,14 @@ struct Request {
             return x;
         }
         x.c = scale_of(T);
+        x.inv_c = 1.f / x.c.hi;
         float S = 0.f;
-        for (int i = lane; i < sd.nc; i += 32) {
-            const float2 v = part[i];
-            if (v.x > -INFINITY) S += v.y * exp2f((v.x - M) * x.c.hi);
+#pragma unroll
+        for (int k = 0; k < kKept; ++k)
+            if (v[k].x > -INFINITY) S += v[k].y * exp2f((v[k].x - M) * x.c.hi);
+        for (int i = kKept * 32 + lane; i < sd.nc; i += 32) {
+            const float2 y = part[i];
+            if (y.x > -INFINITY) S += y.y * exp2f((y.x - M) * x.c.hi);
         }
         x.S = warp_sum(S);
         x.mode = kDistDense;
@@ -419,152 +564,54 @@ struct Request {
         const int e = static_cast<int>(__float_as_uint(x.S * 1.01f) >> 23) - 126;
         x.prec = min(54, 61 - max(e, 1));
         const uintptr_t mask = x.dtype == RL_DTYPE_F32 ? 15 : 7, size = x.dtype == RL_DTYPE_F32 ? 4 : 2;
-        x.vec = ((reinterpret_cast<uintptr_t>(x.d->logits) + static_cast<uintptr_t>(x.row * x.d->row_stride) * size) & mask) == 0;
+        x.vec = ((reinterpret_cast<uintptr_t>(sd.d.logits) + static_cast<uintptr_t>(x.row * sd.d.row_stride) * size) & mask) == 0;
         return x;
     }
     // log2 of token j's probability, to fp32 sums; -inf: none
-    RL_DEVINL float log2_prob(const VerRow& x, int j, int& bits) {
+    RL_DEVINL float log2_prob(int side, const VerRow& x, int j, int& bits) {
         if (x.mode == kDistPoint) return j == x.at ? 0.f : -INFINITY;
         if (x.mode == kDistDense) {
-            const float z = logit_at(*x.d, x.dtype, x.row, j);
+            const float z = logit_at(g.side[side].d, x.dtype, x.row, j);
             if (!(z > -INFINITY)) return -INFINITY;
             const FF d = two_sum(z, -x.M);
             return fmaf(d.hi, x.c.hi, fmaf(d.lo, x.c.hi, d.hi * x.c.lo)) - log2f(x.S);
         }
-        return support_at(x, j, bits) * kLog2e;
+        return support_at(side, x, j, bits) * kLog2e;
     }
     // a support row's log-probability of token j
-    RL_DEVINL float support_at(const VerRow& x, int j, int& bits) {
+    RL_DEVINL float support_at(int side, const VerRow& x, int j, int& bits) {
         if (x.mode != kDistSupport) return -INFINITY;
+        const rl_dist& d = g.side[side].d;
         long long lo = x.eb, hi = x.ee;
         while (lo < hi) {
             const long long mid = (lo + hi) >> 1;
-            if (x.d->ids[mid] < j) lo = mid + 1;
+            if (d.ids[mid] < j) lo = mid + 1;
             else hi = mid;
         }
-        if (lo < x.ee && x.d->ids[lo] == j) {
-            const float q = x.d->logq[lo];
+        if (lo < x.ee && d.ids[lo] == j) {
+            const float q = d.logq[lo];
             if (!(q <= 1e-6f)) bits |= RL_STATUS_LOGQ;
             return q < INFINITY ? q : -INFINITY;
         }
         return -INFINITY;
     }
     // ln of token j's probability, in 64 bits (a dense row's total has been counted)
-    RL_DEVINL double ln_prob(const VerRow& x, int j, int& bits) {
+    RL_DEVINL double ln_prob(int side, const VerRow& x, int j, int& bits) {
         if (x.mode == kDistPoint) return j == x.at ? 0.0 : -INFINITY;
         if (x.mode == kDistDense) {
-            const float z = logit_at(*x.d, x.dtype, x.row, j);
+            const float z = logit_at(g.side[side].d, x.dtype, x.row, j);
             if (!(z > -INFINITY) || x.total == 0) return -INFINITY;
             const double c = static_cast<double>(x.c.hi) + static_cast<double>(x.c.lo);
             const double e = x.plain ? z * c : (static_cast<double>(z) - x.M) * c;
             return 0.69314718055994530942 * (e - x.R - (log2(static_cast<double>(x.total)) - x.prec));
         }
-        return support_at(x, j, bits);
+        return support_at(side, x, j, bits);
     }
-    // Rows t of both sides into shared memory.
-    RL_DEVINL void load_rows(long long t, bool both, int& bits) {
-        __syncthreads();
-        if (warp < 2 && (warp == 0 || both)) {
-            const VerRow x = row_at(warp, t, bits);
-            if (lane == 0) s.row[warp] = x;
-        } else if (warp == 1 && lane == 0) {
-            s.row[1].mode = kDistNone;
-        }
-        __syncthreads();
-    }
-
-    // The parts' sums of the slice; kLeft: of what is left of the target beside the draft's logits, else of the weights of
-    // one side.  Each part is summed relative to its own largest weight.
-    template <bool kLeft>
-    RL_DEVINL unsigned long long sum_parts(int side) {
-        const VerRow w = s.row[side];
-        const VerRow o = s.row[1];
-        const float lam_hi = kLeft ? rintf(s.lam.hi * 2048.f) * (1.f / 2048.f) : 0.f, lam_lo = kLeft ? (s.lam.hi - lam_hi) + s.lam.lo : 0.f;
-        unsigned long long mine = 0;
-        Four next{}, next_o{};
-        if (p0 + warp < p1) {
-            next = four_raw(w, V, (p0 + warp) * kVerPart + lane * 4);
-            if (kLeft) next_o = four_raw(o, V, (p0 + warp) * kVerPart + lane * 4);
-        }
-#pragma unroll 1
-        for (int p = p0 + warp; p < p1; p += kVerWarps) {
-            float z[4], y[4];
-            four_get(next, w.dtype, z);
-            if (kLeft) four_get(next_o, o.dtype, y);
-            if (p + kVerWarps < p1) {
-                next = four_raw(w, V, (p + kVerWarps) * kVerPart + lane * 4);
-                if (kLeft) next_o = four_raw(o, V, (p + kVerWarps) * kVerPart + lane * 4);
-            }
-            const float m = z_of(__reduce_max_sync(0xffffffffu, key_of(fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3])))));
-            const float ex = w.plain ? fmaf(m, w.c.hi, -w.R) : (m - w.M) * w.c.hi;
-            unsigned long long sum = 0;
-            if (ex > -100.f) {                       // (also not for -inf: below, the part is nothing beside the row)
-                const float ref = fminf(ceilf(ex), 1.f);
-                const float zlow = fmaxf(logit_of(w, ref, -64.f), -FLT_MAX);
-                const float ylow = kLeft ? fmaxf(logit_of(o, ref + lam_hi, -64.f), -FLT_MAX) : 0.f, yhigh = kLeft ? logit_of(o, ref + lam_hi, 0.75f) : 0.f;
-                LaneSum acc;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    FF v = weight_of(fmaxf(z[j], zlow), w, ref, 0.f, s.tab);
-                    if (z[j] < zlow) v = {0.f, 0.f};
-                    if (kLeft) {
-                        FF q = weight_of(fminf(fmaxf(y[j], ylow), yhigh), o, ref + lam_hi, lam_lo, s.tab);
-                        if (y[j] < ylow) q = {0.f, 0.f};
-                        v = left_of(v, q);
-                    }
-                    acc.add(v.hi, v.lo);
-                }
-                const uint32_t top = acc.warp_top();
-                const int low = acc.warp_low();
-                const unsigned long long w50 = LaneSum::total(top, low);
-                const int sh = w.prec - 50 + static_cast<int>(ref);
-                sum = sh >= 0 ? w50 << sh : sh > -64 ? (w50 + (1ull << (-sh - 1))) >> -sh : 0ull;
-            }
-            if (lane == 0) cs[p - p0] = sum;
-            mine += sum;
-        }
-        mine = lane == 0 ? mine : 0;
-        return vblock_sum(mine, s.red);
-    }
-    // max(v - q, 0) of normalised pairs
-    static RL_DEVINL FF left_of(FF v, FF q) {
-        if (!(v.hi >= q.hi)) return {0.f, 0.f};
-        const float d = __fsub_rn(v.hi, q.hi);
-        const FF r = two_sum(d, __fadd_rn(__fsub_rn(__fsub_rn(v.hi, d), q.hi), __fsub_rn(v.lo, q.lo)));
-        return r.hi > 0.f ? r : FF{0.f, 0.f};
-    }
-    // Counts a dense row's total; returns the slice's (its parts stay in cs) and the sum of the slices before.
-    RL_DEVINL unsigned long long count_total(int side, unsigned long long& before) {
-        const unsigned long long mine = sum_parts<false>(side);
-        const unsigned long long t = cluster_sum(mine, before);
-        __syncthreads();
-        if (tid == 0) s.row[side].total = t;
-        __syncthreads();
-        return mine;
-    }
-
-    // The comparison of row t with 64-bit logs and counted totals (every block of the cluster comes to the same).
-    RL_DEVINL int decide(long long t, int x, float u, int& bits) {
-        load_rows(t, true, bits);
-        for (int side = 0; side < 2; ++side)
-            if (s.row[side].mode == kDistDense) {
-                unsigned long long before;
-                count_total(side, before);
-            }
-        if (tid == 0) {
-            const double lp = ln_prob(s.row[0], x, bits), lq = ln_prob(s.row[1], x, bits);
-            s.flag = static_cast<double>(u) * exp(lq) < exp(lp) ? 0 : 1;
-            s.lpx = static_cast<float>(lp);
-        }
-        __syncthreads();
-        return s.flag;
-    }
-
-    // The draft's weight of token j in the target's units (its rows' totals counted), for a draw from support or point rows.
+    // A draft's probability of token j as a pair (a dense row's total has been counted, ln_total its log).
     RL_DEVINL FF prob_pair(const VerRow& x, int j, FF ln_total, int& bits) {
         if (x.mode == kDistPoint) return {j == x.at ? 1.f : 0.f, 0.f};
         if (x.mode == kDistDense) {
-            const float z = logit_at(*x.d, x.dtype, x.row, j);
+            const float z = logit_at(g.side[1].d, x.dtype, x.row, j);
             if (!(z > -INFINITY)) return {0.f, 0.f};
             const FF d = x.plain ? FF{z, 0.f} : two_sum(z, -x.M);
             // e = d c - R in log2 units, then to natural ones less the total's log
@@ -572,7 +619,7 @@ struct Request {
             e = ff_add(ff_mul(e, {0.693147182464599609375f, -1.90465429995775e-09f}), ff_neg(ln_total));
             return exp_pair(e);
         }
-        const float q = support_at(x, j, bits);
+        const float q = support_at(1, x, j, bits);
         return q > -INFINITY ? exp_ff(q) : FF{0.f, 0.f};
     }
     // ln of a counted total, in the unit 2^R (2^0) of its weights
@@ -582,20 +629,26 @@ struct Request {
         return ln_pair(fast_two_sum(th * power_of_2(-prec), tl * power_of_2(-prec)));
     }
 
+    RL_DEVINL void finish(long long t, int token, float l, int& bits) {
+        if (token < 0) bits |= RL_STATUS_EMPTY_ROW;
+        g.a.tokens[t] = token;
+        if (g.a.logq) g.a.logq[t] = token < 0 ? -INFINITY : l;
+    }
     // A draw from a support row, by one block.  Sums in units of 2^-52.
     RL_DEVINL void draw_support(long long t, float u, int& bits) {
-        const VerRow p = s.row[0], q = s.row[1];
+        const VerRow p = s.draw.row[0], q = s.draw.row[1];
+        const rl_dist& d = g.side[0].d;
         const long long n = p.ee - p.eb;
         const FF lq = q.mode == kDistDense ? ln_of(q.total, q.prec) : FF{0.f, 0.f};
         bool whole = q.mode == kDistNone;
         auto left = [&](long long i) -> unsigned long long {
-            const int j = p.d->ids[p.eb + i];
-            const float l = p.d->logq[p.eb + i];
+            const int j = d.ids[p.eb + i];
+            const float l = d.logq[p.eb + i];
             if (j < 0 || j >= V) {
                 bits |= RL_STATUS_ID_RANGE;
                 return 0ull;
             }
-            if (i > 0 && p.d->ids[p.eb + i - 1] >= j) bits |= RL_STATUS_ROW_ORDER;
+            if (i > 0 && d.ids[p.eb + i - 1] >= j) bits |= RL_STATUS_ROW_ORDER;
             if (!(l <= 1e-6f)) bits |= RL_STATUS_LOGQ;
             if (!(l < INFINITY) || !(l > -INFINITY)) return 0ull;
             FF v = exp_ff(l);
@@ -603,16 +656,16 @@ struct Request {
             return fixed_of(v.hi, v.lo, 52);
         };
         // a stretch of the row a thread
-        const long long per = (n + kVerThreads - 1) / kVerThreads, i0 = min(tid * per, n), i1 = min(i0 + per, n);
+        const long long per = (n + NT - 1) / NT, i0 = min(tid * per, n), i1 = min(i0 + per, n);
         unsigned long long mine = 0, total = 0;
         for (int tries = 0; tries < 2; ++tries) {
             mine = 0;
             for (long long i = i0; i < i1; ++i) mine += left(i);
-            total = vblock_sum(mine, s.red);
+            total = block_sum(mine);
             if (total > 0 || whole) break;
             whole = true;
         }
-        const unsigned long long before = vblock_scan(mine, s.red), target = fraction_of(u, total);
+        const unsigned long long before = block_scan(mine), target = fraction_of(u, total);
         if (tid == 0) s.token = -1;
         __syncthreads();
         if (total > 0 && mine > 0 && before <= target && target < before + mine) {
@@ -620,8 +673,8 @@ struct Request {
             for (long long i = i0; i < i1; ++i) {
                 c += left(i);
                 if (c > target) {
-                    s.token = p.d->ids[p.eb + i];
-                    s.lpx = p.d->logq[p.eb + i];
+                    s.token = d.ids[p.eb + i];
+                    s.lpx = d.logq[p.eb + i];
                     break;
                 }
             }
@@ -629,16 +682,185 @@ struct Request {
         __syncthreads();
         if (tid == 0) finish(t, s.token, s.lpx, bits);
     }
-    RL_DEVINL void finish(long long t, int token, float l, int& bits) {
-        if (token < 0) bits |= RL_STATUS_EMPTY_ROW;
-        g.a.tokens[t] = token;
-        if (g.a.logq) g.a.logq[t] = token < 0 ? -INFINITY : l;
-    }
+};
 
-    // What is left of token j of a dense target, z its logit, in the target's units.
+// A block a request: what is accepted, and the new token where no row of logits has to be summed up for it.
+__global__ void __launch_bounds__(kDecideThreads, 2) decide_kernel(const __grid_constant__ VerArgs g) {
+    extern __shared__ __align__(16) uint8_t raw[];
+    VerShared<kDecideThreads>& s = *reinterpret_cast<VerShared<kDecideThreads>*>(raw);
+    const rl_verify_args& a = g.a;
+    const long long r = blockIdx.x;
+    const int tid = threadIdx.x, V = static_cast<int>(a.V);
+    Request<kDecideThreads> q{g, s, V, tid, tid & 31, tid >> 5};
+    constexpr int kRows = kDecideThreads / 64;
+    int bits = 0;
+    bool table = false;
+    wait_for_previous();
+    let_next_start();
+    long long t0 = a.cu_q[r], t1 = a.cu_q[r + 1];
+    if (t0 < 0 || t1 < t0 || t1 > a.T) {
+        bits |= RL_STATUS_LENGTHS;
+        t0 = t1 = 0;
+    }
+    // Row k of a stretch of the request: a warp its target, the next its draft (the last row has none).
+    long long t = t0;
+    bool going = t1 > t0;
+    int at = 0;                                  // the row that the new token is drawn from, in the stretch
+    while (going) {
+        const long long mine = t + (q.warp >> 1);
+        const int side = q.warp & 1;
+        __syncthreads();
+        if (mine < t1) {
+            VerRow x{};
+            int rb = 0;
+            float lp = -INFINITY;
+            const bool candidate = mine + 1 < t1;
+            if (candidate || side == 0) {
+                const int token = candidate ? a.step_tokens[mine + 1] : -1;
+                x = q.row_at(side, mine, rb);
+                if (candidate) {
+                    if (x.mode == kDistNone) rb |= RL_STATUS_EMPTY_ROW;
+                    if (token < 0 || token >= V) rb |= RL_STATUS_ID_RANGE;
+                    else lp = q.log2_prob(side, x, token, rb);
+                }
+            }
+            if (q.lane == 0) {
+                s.rows[q.warp] = x;
+                s.lp[q.warp] = lp;
+                s.bits[q.warp] = rb;
+            }
+        }
+        __syncthreads();
+        const int n = static_cast<int>(min(static_cast<long long>(kRows), t1 - t));
+        int k = 0;
+        for (; k < n; ++k) {
+            if (t + k + 1 >= t1) {               // the last row
+                going = false;
+                bits |= s.bits[2 * k];
+                break;
+            }
+            bits |= s.bits[2 * k] | s.bits[2 * k + 1];
+            const int x = a.step_tokens[t + k + 1];
+            const float u = unit_of(a.u[t + k], bits), lp = s.lp[2 * k], lu = log2f(u) + s.lp[2 * k + 1];
+            // The bound of the difference's error: two totals of fp32 exponentials (2^-22 each, arguments' roundings, 60 additions)
+            // and the logs' own roundings
+            const float bound = 0x1p-15f + 0x1p-21f * (fabsf(lp) + fabsf(lu));
+            float l = lp * kLn2;
+            int res;
+            if (lp == -INFINITY) res = 1;
+            else if (lu == -INFINITY) res = 0;
+            else res = lu < lp - bound ? 0 : lu > lp + bound ? 1 : 2;
+            if (res == 2) {                      // too near: with counted totals and 64-bit logs
+                if (!table) fill_table(s.tab, tid, kDecideThreads);
+                table = true;
+                const int steps = (V + kVerStep * kVerPart - 1) / (kVerStep * kVerPart);
+                for (int sd = 0; sd < 2; ++sd) {
+                    VerRow& w = s.rows[2 * k + sd];
+                    if (w.mode != kDistDense) continue;
+                    __syncthreads();
+                    const unsigned long long sum = sum_steps(g.side[sd].d, &w, V, 0, steps, q.warp, kDecideThreads / 32, nullptr, s.tab);
+                    const unsigned long long total = q.block_sum(q.lane == 0 ? sum : 0ull);
+                    if (tid == 0) w.total = total;
+                }
+                __syncthreads();
+                if (tid == 0) {
+                    const double dp = q.ln_prob(0, s.rows[2 * k], x, bits), dq = q.ln_prob(1, s.rows[2 * k + 1], x, bits);
+                    s.flag = static_cast<double>(u) * exp(dq) < exp(dp) ? 0 : 1;
+                    s.lpx = static_cast<float>(dp);
+                }
+                __syncthreads();
+                res = s.flag;
+                l = s.lpx;
+            }
+            if (res != 0) {
+                going = false;
+                break;
+            }
+            if (tid == 0) {
+                a.tokens[t + k] = x;
+                if (a.logq) a.logq[t + k] = l;
+            }
+        }
+        t += k;
+        at = k;
+    }
+    if (tid == 0) {
+        a.accepted[r] = static_cast<int>(t - t0);
+        if (a.keep_lens) a.keep_lens[r] = (a.ctx_lens ? a.ctx_lens[r] : 0) + static_cast<int>(t1 > t0 ? t - t0 + 1 : 0);
+    }
+    bool rest = false;
+    if (t1 > t0) {
+        const float u = unit_of(a.u_next[r], bits);
+        const bool refused = t + 1 < t1;
+        if (tid == 0) {
+            s.draw.t = t;
+            s.draw.u = u;
+            s.draw.refused = refused;
+            s.draw.row[0] = s.rows[2 * at];
+            s.draw.row[1] = s.rows[2 * at + 1];
+            if (!refused) s.draw.row[1].mode = kDistNone;
+        }
+        __syncthreads();
+        const int p = s.draw.row[0].mode, d = s.draw.row[1].mode;
+        if (p == kDistDense || (p == kDistSupport && d == kDistDense)) rest = true;
+        else if (p == kDistSupport) q.draw_support(t, u, bits);
+        // (all of the target on one token: it is what is left, or what there is)
+        else if (tid == 0) q.finish(t, p == kDistPoint ? s.draw.row[0].at : -1, 0.f, bits);
+    }
+    if (g.draws) {
+        __syncthreads();
+        if (rest) {
+            const int words = static_cast<int>(sizeof(VerDraw) / 8);
+            if (tid < words) reinterpret_cast<unsigned long long*>(g.draws + r)[tid] = reinterpret_cast<const unsigned long long*>(&s.draw)[tid];
+        } else if (tid == 0) {
+            g.draws[r].t = -1;
+        }
+    }
+    set_status(g.status, bits);
+}
+
+// A cluster of blocks a request: the new token from rows of logits.
+struct Draw : Request<kDrawThreads> {
+    unsigned long long* cs;       // sums of the slice's parts
+    int rank, from, steps, phase; // its steps
+
+    // The cluster's sum of v (the same in a block's threads), and the sum of the blocks before.
+    RL_DEVINL unsigned long long cluster_sum(unsigned long long v, unsigned long long& before) {
+        before = 0;
+        if (g.cs == 1) return v;
+        unsigned long long* slot = &s.xch[phase & 1];
+        ++phase;
+        if (tid == 0) *slot = v;
+        __syncthreads();
+        cluster_arrive();
+        cluster_wait();
+        unsigned long long total = 0;
+        for (int k = 0; k < g.cs; ++k) {
+            unsigned long long x;
+            asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(x) : "r"(cluster_addr(slot, k)) : "memory");
+            if (k < rank) before += x;
+            total += x;
+        }
+        return total;
+    }
+    RL_DEVINL unsigned long long slice_sum(int side) {
+        __syncthreads();
+        const unsigned long long x = sum_steps(g.side[side].d, &s.draw.row[side], V, from, steps, warp, kWarps, cs, s.tab);
+        return block_sum(lane == 0 ? x : 0ull);
+    }
+    // Counts a dense row's total; returns the slice's (its parts stay in cs) and the sum of the slices before.
+    RL_DEVINL unsigned long long count_total(int side, unsigned long long& before) {
+        const unsigned long long mine = slice_sum(side);
+        const unsigned long long t = cluster_sum(mine, before);
+        __syncthreads();
+        if (tid == 0) s.draw.row[side].total = t;
+        __syncthreads();
+        return mine;
+    }
+    // What is left of a token of a dense target, z its logit and y the draft's, in the target's units.
     RL_DEVINL unsigned long long left_at(float z, float y, int j, bool whole, int& bits) {
-        const VerRow& p = s.row[0];
-        const VerRow& q = s.row[1];
+        const VerRow& p = s.draw.row[0];
+        const VerRow& q = s.draw.row[1];
         const float zlow = fmaxf(logit_of(p, 0.f, -64.f), -FLT_MAX);
         if (!(z >= zlow)) return 0ull;
         FF v = weight_of(z, p, 0.f, 0.f, s.tab);
@@ -648,25 +870,23 @@ struct Request {
             if (y >= ylow) v = left_of(v, weight_of(fminf(y, yhigh), q, lam_hi, lam_lo, s.tab));
             return fixed_of(v.hi, v.lo, p.prec);
         }
-        unsigned long long w = fixed_of(v.hi, v.lo, p.prec);
-        if (!whole && q.mode != kDistNone) {
-            const unsigned long long x = taken(j, w, q.mode == kDistPoint ? (j == q.at ? 0.f : -INFINITY) : support_at(q, j, bits));
-            w -= x;
-        }
-        return w;
+        const unsigned long long w = fixed_of(v.hi, v.lo, p.prec);
+        if (whole || q.mode == kDistNone) return w;
+        return w - taken(w, q.mode == kDistPoint ? (j == q.at ? 0.f : -INFINITY) : support_at(1, q, j, bits));
     }
     // What a draft's probability e^lq takes off a weight w: the smaller of the two.
-    RL_DEVINL unsigned long long taken(int, unsigned long long w, float lq) {
+    RL_DEVINL unsigned long long taken(unsigned long long w, float lq) {
         if (!(lq > -INFINITY)) return 0ull;
         const FF e = exp_ff(lq);
-        const double x = (static_cast<double>(e.hi) + static_cast<double>(e.lo)) * static_cast<double>(s.row[0].total);
+        const double x = (static_cast<double>(e.hi) + static_cast<double>(e.lo)) * static_cast<double>(s.draw.row[0].total);
         return x >= static_cast<double>(w) ? w : static_cast<unsigned long long>(__double2ll_rn(x));
     }
 
-    // A draw from a row of logits, by the cluster.
     RL_DEVINL void draw_dense(long long t, float u, int& bits) {
-        const VerRow& p = s.row[0];
-        const VerRow& q = s.row[1];
+        const VerRow& p = s.draw.row[0];
+        const VerRow& q = s.draw.row[1];
+        const rl_dist& dp = g.side[0].d;
+        const rl_dist& dq = g.side[1].d;
         bool whole = q.mode == kDistNone;
         unsigned long long before;
         if (q.mode == kDistDense) count_total(1, before);
@@ -679,40 +899,42 @@ struct Request {
             }
             __syncthreads();
         }
+        const int p0 = from * kVerStep, parts = steps * kVerStep;
         for (int tries = 0; tries < 2; ++tries) {
             if (!whole && q.mode == kDistDense) {
-                mine = sum_parts<true>(0);
+                const unsigned long long x = sum_left(dp, &p, dq, &q, s.lam, V, from, steps, warp, kWarps, cs, s.tab);
+                mine = block_sum(lane == 0 ? x : 0ull);
             } else {
-                if (tries > 0) mine = sum_parts<false>(0);
+                if (tries > 0) mine = slice_sum(0);
                 if (!whole) {
                     // the draft's tokens in the slice, off their parts
                     const long long n = q.mode == kDistPoint ? 1 : q.ee - q.eb;
-                    for (long long i = tid; i < n; i += kVerThreads) {
-                        const int j = q.mode == kDistPoint ? q.at : q.d->ids[q.eb + i];
+                    for (long long i = tid; i < n; i += kDrawThreads) {
+                        const int j = q.mode == kDistPoint ? q.at : dq.ids[q.eb + i];
                         if (j < 0 || j >= V) {
                             if (q.mode == kDistSupport) bits |= RL_STATUS_ID_RANGE;
                             continue;
                         }
                         float lq = 0.f;
                         if (q.mode == kDistSupport) {
-                            lq = q.d->logq[q.eb + i];
+                            lq = dq.logq[q.eb + i];
                             if (!(lq <= 1e-6f)) bits |= RL_STATUS_LOGQ;
                             if (!(lq < INFINITY)) lq = -INFINITY;
-                            if (i > 0 && q.d->ids[q.eb + i - 1] >= j) bits |= RL_STATUS_ROW_ORDER;
+                            if (i > 0 && dq.ids[q.eb + i - 1] >= j) bits |= RL_STATUS_ROW_ORDER;
                         }
-                        const int part = j / kVerPart;
-                        if (part < p0 || part >= p1) continue;
-                        const unsigned long long w = left_at(logit_at(*p.d, p.dtype, p.row, j), 0.f, j, true, bits);
-                        atomicAdd(&cs[part - p0], 0ull - taken(j, w, lq));
+                        const int part = j / kVerPart - p0;
+                        if (part < 0 || part >= parts) continue;
+                        const unsigned long long w = left_at(logit_at(dp, p.dtype, p.row, j), 0.f, j, true, bits);
+                        atomicAdd(&cs[part], 0ull - taken(w, lq));
                     }
                     __syncthreads();
                     // (a part's sum and its tokens' weights are rounded apart)
                     unsigned long long v = 0;
-                    for (int i = tid; i < p1 - p0; i += kVerThreads) {
+                    for (int i = tid; i < parts; i += kDrawThreads) {
                         if (static_cast<long long>(cs[i]) < 0) cs[i] = 0;
                         v += cs[i];
                     }
-                    mine = vblock_sum(v, s.red);
+                    mine = block_sum(v);
                 }
             }
             if (tries > 0 || !whole) total = cluster_sum(mine, before);
@@ -727,16 +949,16 @@ struct Request {
     }
     // The block in whose slice the number falls: its part, then its token.
     RL_DEVINL void search(long long t, unsigned long long want, bool whole, int& bits) {
-        const int n = p1 - p0, per = (n + kVerThreads - 1) / kVerThreads;
+        const int n = steps * kVerStep, per = (n + kDrawThreads - 1) / kDrawThreads;
         unsigned long long v = 0;
         __syncthreads();
         for (int j = 0; j < per; ++j) v += tid * per + j < n ? cs[tid * per + j] : 0ull;
-        unsigned long long c = vblock_scan(v, s.red);
+        unsigned long long c = block_scan(v);
         if (c <= want && want < c + v)
             for (int j = 0; j < per; ++j) {
                 const unsigned long long x = cs[tid * per + j];
                 if (want < c + x) {
-                    s.token = p0 + tid * per + j;
+                    s.token = from * kVerStep + tid * per + j;
                     s.unit = want - c;
                     break;
                 }
@@ -744,21 +966,20 @@ struct Request {
             }
         __syncthreads();
         if (warp != 0) return;
-        const int part = s.token, i0 = part * kVerPart + lane * 4;
+        const int i0 = s.token * kVerPart + lane * 4;
         const unsigned long long rest = s.unit;
-        const VerRow& p = s.row[0];
-        const VerRow& q = s.row[1];
-        float z[4], y[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        four_get(four_raw(p, V, i0), p.dtype, z);
-        if (!whole && q.mode == kDistDense) four_get(four_raw(q, V, i0), q.dtype, y);
+        const VerRow& p = s.draw.row[0];
+        const VerRow& q = s.draw.row[1];
         unsigned long long w[4], mine = 0;
         int last = -1, likely = -1;
-#pragma unroll
+#pragma unroll 1
         for (int j = 0; j < 4; ++j) {
-            w[j] = z[j] > -INFINITY ? left_at(z[j], y[j], i0 + j, whole, bits) : 0ull;
+            const float z = i0 + j < V ? logit_at(g.side[0].d, p.dtype, p.row, i0 + j) : -INFINITY;
+            const float y = i0 + j < V && !whole && q.mode == kDistDense ? logit_at(g.side[1].d, q.dtype, q.row, i0 + j) : -INFINITY;
+            w[j] = z > -INFINITY ? left_at(z, y, i0 + j, whole, bits) : 0ull;
             mine += w[j];
             if (w[j] > 0) last = j;
-            if (z[j] > -INFINITY) likely = j;
+            if (z > -INFINITY) likely = j;
         }
         unsigned long long incl = mine;
 #pragma unroll
@@ -787,100 +1008,32 @@ struct Request {
         }
         if (lane == src) {
             const int token = i0 + max(at, 0);
-            finish(t, token, static_cast<float>(ln_prob(p, token, bits)), bits);
+            finish(t, token, static_cast<float>(ln_prob(0, p, token, bits)), bits);
         }
     }
 };
 
-__global__ void __launch_bounds__(kVerThreads, 2) request_kernel(const __grid_constant__ VerArgs g) {
+__global__ void __launch_bounds__(kDrawThreads, 4) draw_kernel(const __grid_constant__ VerArgs g) {
     extern __shared__ __align__(16) uint8_t raw[];
-    VerShared& s = *reinterpret_cast<VerShared*>(raw);
-    const rl_verify_args& a = g.a;
+    VerShared<kDrawThreads>& s = *reinterpret_cast<VerShared<kDrawThreads>*>(raw);
     const long long r = blockIdx.x / static_cast<unsigned>(g.cs);
-    const int tid = threadIdx.x, V = static_cast<int>(a.V), rank = static_cast<int>(blockIdx.x - r * g.cs);
-    const int ns = (V + kVerPart - 1) / kVerPart;
-    Request q{g, s, reinterpret_cast<unsigned long long*>(raw + sizeof(VerShared)), V, tid, tid & 31, tid >> 5, rank, min(rank * g.per, ns),
-              min((rank + 1) * g.per, ns), 0};
-    fill_table(s.tab, tid, kVerThreads);
+    const int tid = threadIdx.x, V = static_cast<int>(g.a.V), rank = static_cast<int>(blockIdx.x - r * g.cs);
+    const int all = (V + kVerStep * kVerPart - 1) / (kVerStep * kVerPart), from = min(rank * g.per, all);
+    Draw q{{g, s, V, tid, tid & 31, tid >> 5}, reinterpret_cast<unsigned long long*>(raw + sizeof(VerShared<kDrawThreads>)), rank, from,
+           min(g.per, all - from), 0};
     int bits = 0;
     wait_for_previous();
-    long long t0 = a.cu_q[r], t1 = a.cu_q[r + 1];
-    if (t0 < 0 || t1 < t0 || t1 > a.T) {
-        bits |= RL_STATUS_LENGTHS;
-        t0 = t1 = 0;
-    }
-    long long t = t0;
-    bool going = t1 > t0;
-    while (going && t + 1 < t1) {
-        // a row a warp
-        const long long mine = t + q.warp;
-        __syncthreads();
-        if (mine + 1 < t1) {
-            int rb = 0;
-            const int x = a.step_tokens[mine + 1];
-            const VerRow p = q.row_at(0, mine, rb), d = q.row_at(1, mine, rb);
-            int res = 1;
-            float lp = -INFINITY;
-            if (p.mode == kDistNone || (d.mode == kDistNone)) rb |= RL_STATUS_EMPTY_ROW;
-            if (x < 0 || x >= V) {
-                rb |= RL_STATUS_ID_RANGE;
-            } else {
-                lp = q.log2_prob(p, x, rb);
-                const float lq = q.log2_prob(d, x, rb), lu = log2f(unit_of(a.u[mine], rb)) + lq;
-                // The bound of the difference's error: two totals of fp32 exponentials (2^-22 each, arguments' roundings, 24 additions)
-                // and the logs' own roundings
-                const float bound = 0x1p-15f + 0x1p-21f * (fabsf(lp) + fabsf(lu));
-                if (lp == -INFINITY) res = 1;
-                else if (lu == -INFINITY) res = 0;
-                else res = lu < lp - bound ? 0 : lu > lp + bound ? 1 : 2;
-            }
-            if (q.lane == 0) {
-                s.res[q.warp] = res | rb << 2;
-                s.lp[q.warp] = lp * kLn2;
-            }
-        }
-        __syncthreads();
-        const int n = static_cast<int>(min(static_cast<long long>(kVerWarps), t1 - 1 - t));
-        int k = 0;
-        for (; k < n; ++k) {
-            const int x = a.step_tokens[t + k + 1];
-            int res = s.res[k] & 3;
-            float l = s.lp[k];
-            bits |= s.res[k] >> 2;
-            if (res == 2) {
-                int none = 0;
-                res = q.decide(t + k, x, unit_of(a.u[t + k], none), none);
-                l = s.lpx;
-            }
-            if (res != 0) {
-                going = false;
-                break;
-            }
-            if (rank == 0 && tid == 0) {
-                a.tokens[t + k] = x;
-                if (a.logq) a.logq[t + k] = l;
-            }
-        }
-        t += k;
-    }
-    if (rank == 0 && tid == 0) {
-        a.accepted[r] = static_cast<int>(t - t0);
-        if (a.keep_lens) a.keep_lens[r] = (a.ctx_lens ? a.ctx_lens[r] : 0) + static_cast<int>(t1 > t0 ? t - t0 + 1 : 0);
-    }
-    if (t1 > t0) {
-        const float u = unit_of(a.u_next[r], bits);
-        q.load_rows(t, t + 1 < t1, bits);
-        const VerRow& p = s.row[0];
-        if (p.mode == kDistDense) {
-            q.draw_dense(t, u, bits);
-        } else if (p.mode == kDistSupport) {
-            unsigned long long before;
-            if (s.row[1].mode == kDistDense) q.count_total(1, before);
-            if (rank == 0) q.draw_support(t, u, bits);
-        } else if (rank == 0 && tid == 0) {
-            // all of the target on one token: it is what is left, or what there is
-            q.finish(t, p.mode == kDistPoint ? p.at : -1, 0.f, bits);
-        }
+    const int words = static_cast<int>(sizeof(VerDraw) / 8);
+    if (tid < words) reinterpret_cast<unsigned long long*>(&s.draw)[tid] = reinterpret_cast<const unsigned long long*>(g.draws + r)[tid];
+    if (g.draws[r].t < 0) return;                // (all blocks of the cluster alike)
+    fill_table(s.tab, tid, kDrawThreads);
+    __syncthreads();
+    if (s.draw.row[0].mode == kDistDense) {
+        q.draw_dense(s.draw.t, s.draw.u, bits);
+    } else {
+        unsigned long long before;
+        q.count_total(1, before);
+        if (rank == 0) q.draw_support(s.draw.t, s.draw.u, bits);
     }
     set_status(g.status, bits);
     __syncthreads();
@@ -907,6 +1060,7 @@ static VerArgs verify_view(void* ws, const rl_verify_args* a, int32_t* status, s
             s.nc = static_cast<int>((a->V + e - 1 + chunk - 1) / chunk);
             s.part = cv.take<float2>(static_cast<size_t>(a->T) * s.nc);
         }
+    if (a->target.logits || a->draft.logits) g.draws = cv.take<VerDraw>(static_cast<size_t>(a->R));
     if (bytes) *bytes = align_up(cv.off, 256);
     return g;
 }
@@ -931,33 +1085,36 @@ int verify_impl(const rl_verify_args* a, void* ws, int32_t* status, cudaStream_t
         ++launches;
     }
     if (a->R > 0) {
-        // a block's slice of the vocabulary: at least 64 parts of 128
-        const int ns = static_cast<int>((a->V + kVerPart - 1) / kVerPart);
-        g.cs = 1;
-        while (g.cs < 8 && ns > 64 * g.cs) g.cs *= 2;
-        g.per = (ns + g.cs - 1) / g.cs;
-        if (!a->target.logits && !a->draft.logits) {
-            g.cs = 1;
-            g.per = 0;
-        }
-        const size_t smem = sizeof(VerShared) + static_cast<size_t>(g.per) * 8;
-        static std::atomic<uint64_t> done{0};
-        if (!allow_smem(request_kernel, static_cast<int>(sizeof(VerShared) + (size_t(1) << 20) / kVerPart * 8), done)) return RL_ERR_CUDA;
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(static_cast<unsigned>(a->R * g.cs), 1, 1);
-        cfg.blockDim = dim3(kVerThreads, 1, 1);
-        cfg.dynamicSmemBytes = smem;
-        cfg.stream = stream;
-        cudaLaunchAttribute attr[2];
-        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[0].val.programmaticStreamSerializationAllowed = launches > 0 ? 1 : 0;
-        attr[1].id = cudaLaunchAttributeClusterDimension;
-        attr[1].val.clusterDim.x = static_cast<unsigned>(g.cs);
-        attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 2;
-        if (cudaLaunchKernelEx(&cfg, request_kernel, g) != cudaSuccess) return RL_ERR_CUDA;
+        static std::atomic<uint64_t> decide{0}, draw{0};
+        const int smem = static_cast<int>(sizeof(VerShared<kDecideThreads>));
+        if (!allow_smem(decide_kernel, smem, decide)) return RL_ERR_CUDA;
+        int rc = launch_after(decide_kernel, dim3(static_cast<unsigned>(a->R)), kDecideThreads, static_cast<size_t>(smem), launches > 0, stream, g);
+        if (rc != RL_OK) return rc;
         ++launches;
+        if (g.draws) {
+            // a block's slice of the vocabulary: at least 16 steps of 512, two for each of its warps
+            const int all = static_cast<int>((a->V + kVerStep * kVerPart - 1) / (kVerStep * kVerPart));
+            g.cs = 1;
+            while (g.cs < 8 && all > 16 * g.cs) g.cs *= 2;
+            g.per = (all + g.cs - 1) / g.cs;
+            const size_t fixed = sizeof(VerShared<kDrawThreads>), most = ((size_t(1) << 20) / kVerPart / 8 + kVerStep) * 8;
+            if (!allow_smem(draw_kernel, static_cast<int>(fixed + most), draw)) return RL_ERR_CUDA;
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(static_cast<unsigned>(a->R * g.cs), 1, 1);
+            cfg.blockDim = dim3(kDrawThreads, 1, 1);
+            cfg.dynamicSmemBytes = fixed + static_cast<size_t>(g.per) * kVerStep * 8;
+            cfg.stream = stream;
+            cudaLaunchAttribute attr[2];
+            attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+            attr[0].val.programmaticStreamSerializationAllowed = 1;
+            attr[1].id = cudaLaunchAttributeClusterDimension;
+            attr[1].val.clusterDim.x = static_cast<unsigned>(g.cs);
+            attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+            cfg.attrs = attr;
+            cfg.numAttrs = 2;
+            if (cudaLaunchKernelEx(&cfg, draw_kernel, g) != cudaSuccess) return RL_ERR_CUDA;
+            ++launches;
+        }
     }
     count_launch(launches);
     return cudaPeekAtLastError() == cudaSuccess ? RL_OK : RL_ERR_CUDA;
