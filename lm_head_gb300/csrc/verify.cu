@@ -29,6 +29,7 @@ constexpr int kVerPart = 128;                  // logits of a part
 constexpr int kVerStep = 4;                    // parts that a warp sums up at a time
 constexpr int kDecideThreads = 512;            // a row of either side a warp
 constexpr int kDrawThreads = 256;
+constexpr int kDrawBlocks = 4;                 // of them on a multiprocessor
 constexpr int kChunkThreads = 256;
 constexpr int kChunkPacks = 8;                 // 16-byte loads of a lane: 4 KB a warp
 constexpr int kUsedRows = 32768;               // rows of a step whose use is looked up in shared memory
@@ -108,29 +109,49 @@ RL_DEVINL float2 chunk_of(const T* row, int V, int chunk, float Tm, bool& bad) {
         else if constexpr (std::is_same<T, __nv_bfloat16>::value) return __uint_as_float((j & 1) ? w & 0xffff0000u : w << 16);
         else return __half2float(__ushort_as_half(static_cast<unsigned short>((j & 1) ? w >> 16 : w & 0xffffu)));
     };
-    auto largest = [&]() -> uint32_t {
-        float m = -INFINITY;
+    float m;
+    if constexpr (sizeof(T) == 4) {
+        m = -INFINITY;
 #pragma unroll
-        for (int k = 0; k < kChunkPacks; ++k)
+        for (int k = 0; k < kChunkPacks; ++k) m = max_nan(max_nan(m, max_nan(get(k, 0), get(k, 1))), max_nan(get(k, 2), get(k, 3)));
+    } else {             // two at a time
+        using T2 = typename std::conditional<std::is_same<T, __half>::value, __half2, __nv_bfloat162>::type;
+        T2 x[kChunkPacks * 4];
+        memcpy(x, q, sizeof(x));
+        T2 best = x[0];
 #pragma unroll
-            for (int j = 0; j < E; ++j) m = max_nan(m, get(k, j));
-        return __reduce_max_sync(0xffffffffu, key_of(m + 0.f));
-    };
-    uint32_t key = largest();
-    const bool odd = key >= 0xff800000u;             // NaN or +inf among them: they count as -inf
-    if (odd) {
+        for (int k = 1; k < kChunkPacks * 4; ++k) best = __hmax2_nan(best, x[k]);
+        m = max_nan(__low2float(best), __high2float(best));
+    }
+    uint32_t key = __reduce_max_sync(0xffffffffu, key_of(m + 0.f));
+    if (key >= 0xff800000u) {            // NaN or +inf among them: they count as -inf
         bad = true;
-        float m = -INFINITY;
+        const uint32_t none = sizeof(T) == 4 ? 0xff800000u : std::is_same<T, __half>::value ? 0xfc00u : 0xff80u;
+        m = -INFINITY;
+#pragma unroll 1
+        for (int k = 0; k < kChunkPacks; ++k) {
+            uint32_t w[4];
 #pragma unroll
-        for (int k = 0; k < kChunkPacks; ++k)
+            for (int c = 0; c < kChunkPacks; ++c)
+                if (c == k) memcpy(w, &q[c], 16);
 #pragma unroll
             for (int j = 0; j < E; ++j) {
-                const float z = get(k, j);
-                m = fmaxf(m, z < INFINITY ? z : -INFINITY);
+                const int at = sizeof(T) == 4 ? j : j >> 1, sh = sizeof(T) == 4 ? 0 : (j & 1) * 16;
+                const uint32_t mask = sizeof(T) == 4 ? 0xffffffffu : 0xffffu;
+                T t;
+                const uint32_t bitsj = (w[at] >> sh) & mask;
+                memcpy(&t, &bitsj, sizeof(T));
+                const float z = to_f(t);
+                if (!(z < INFINITY)) w[at] = (w[at] & ~(mask << sh)) | (none << sh);
+                else m = fmaxf(m, z);
             }
+#pragma unroll
+            for (int c = 0; c < kChunkPacks; ++c)
+                if (c == k) memcpy(&q[c], w, 16);
+        }
         key = __reduce_max_sync(0xffffffffu, key_of(m + 0.f));
     }
-    const float m = z_of(key);
+    m = z_of(key);
     if (!(m > -INFINITY)) return make_float2(m, 0.f);
     if (Tm == 0.f) {
         int at = INT_MAX;
@@ -141,16 +162,20 @@ RL_DEVINL float2 chunk_of(const T* row, int V, int chunk, float Tm, bool& bad) {
                 if (get(k, j) == m) at = i0 + k * 32 * E + j;
         return make_float2(m, __uint_as_float(__reduce_min_sync(0xffffffffu, static_cast<unsigned>(at))));
     }
-    const float c = kLog2eHi / Tm;
+    // e^((z - m) / T) as 2^(z c - fl(m c)): one rounding of the argument; the sum is put right for fl(m c) after
+    const float c = kLog2eHi / Tm, pm = m * c;
     float s[4] = {0.f, 0.f, 0.f, 0.f};
+    if (fabsf(pm) < 1e30f) {
+#pragma unroll
+        for (int k = 0; k < kChunkPacks; ++k)
+#pragma unroll
+            for (int j = 0; j < E; ++j) s[j & 3] += exp2_approx(fmaf(get(k, j), c, -pm));
+        return make_float2(m, warp_sum((s[0] + s[1]) + (s[2] + s[3])) * exp2f(-fmaf(m, c, -pm)));
+    }
 #pragma unroll
     for (int k = 0; k < kChunkPacks; ++k)
 #pragma unroll
-        for (int j = 0; j < E; ++j) {
-            const float z = get(k, j);
-            const float e = exp2_approx((z - m) * c);
-            s[j & 3] += !odd || z < INFINITY ? e : 0.f;
-        }
+        for (int j = 0; j < E; ++j) s[j & 3] += exp2_approx((get(k, j) - m) * c);
     return make_float2(m, warp_sum((s[0] + s[1]) + (s[2] + s[3])));
 }
 
@@ -280,36 +305,37 @@ RL_DEVINL FF left_of(FF v, FF q) {
     return r.hi > 0.f ? r : FF{0.f, 0.f};
 }
 
-// A lane's logits of kVerStep parts from element i0 on, four of each, past the row's end -inf.
-RL_DEVINL void step_load(const rl_dist& d, const VerRow& r, int V, int i0, float (&z)[kVerStep][4]) {
+// A lane's logits of N parts from element i0 on, four of each, past the row's end -inf.
+template <int N>
+RL_DEVINL void step_load(const rl_dist& d, const VerRow& r, int V, int i0, float (&z)[N][4]) {
     const int lane = threadIdx.x & 31;
     const long long base = r.row * d.row_stride;
-    const bool whole = r.vec && i0 + kVerStep * kVerPart <= V;
+    const bool whole = r.vec && i0 + N * kVerPart <= V;
     if (r.dtype == RL_DTYPE_F32) {
         const float* p = static_cast<const float*>(d.logits) + base + i0 + lane * 4;
         if (whole) {
 #pragma unroll
-            for (int s = 0; s < kVerStep; ++s) {
+            for (int s = 0; s < N; ++s) {
                 const float4 q = *reinterpret_cast<const float4*>(p + s * kVerPart);
                 z[s][0] = q.x; z[s][1] = q.y; z[s][2] = q.z; z[s][3] = q.w;
             }
         } else {
 #pragma unroll
-            for (int s = 0; s < kVerStep; ++s)
+            for (int s = 0; s < N; ++s)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) z[s][j] = i0 + s * kVerPart + lane * 4 + j < V ? p[s * kVerPart + j] : -INFINITY;
         }
         return;
     }
     const uint16_t* p = static_cast<const uint16_t*>(d.logits) + base + i0 + lane * 4;
-    uint2 q[kVerStep];
+    uint2 q[N];
     if (whole) {
 #pragma unroll
-        for (int s = 0; s < kVerStep; ++s) q[s] = *reinterpret_cast<const uint2*>(p + s * kVerPart);
+        for (int s = 0; s < N; ++s) q[s] = *reinterpret_cast<const uint2*>(p + s * kVerPart);
     } else {
         const uint32_t none = r.dtype == RL_DTYPE_BF16 ? 0xff80u : 0xfc00u;
 #pragma unroll
-        for (int s = 0; s < kVerStep; ++s) {
+        for (int s = 0; s < N; ++s) {
             uint32_t h[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) h[j] = i0 + s * kVerPart + lane * 4 + j < V ? p[s * kVerPart + j] : none;
@@ -318,7 +344,7 @@ RL_DEVINL void step_load(const rl_dist& d, const VerRow& r, int V, int i0, float
     }
     if (r.dtype == RL_DTYPE_BF16) {
 #pragma unroll
-        for (int s = 0; s < kVerStep; ++s) {
+        for (int s = 0; s < N; ++s) {
             z[s][0] = __uint_as_float(q[s].x << 16);
             z[s][1] = __uint_as_float(q[s].x & 0xffff0000u);
             z[s][2] = __uint_as_float(q[s].y << 16);
@@ -326,24 +352,25 @@ RL_DEVINL void step_load(const rl_dist& d, const VerRow& r, int V, int i0, float
         }
     } else {
 #pragma unroll
-        for (int s = 0; s < kVerStep; ++s) {
+        for (int s = 0; s < N; ++s) {
             const __half2 a = *reinterpret_cast<const __half2*>(&q[s].x), b = *reinterpret_cast<const __half2*>(&q[s].y);
             z[s][0] = __low2float(a); z[s][1] = __high2float(a); z[s][2] = __low2float(b); z[s][3] = __high2float(b);
         }
     }
 }
 // The warp's largest of them; NaN and +inf become -inf.
-RL_DEVINL float step_largest(float (&z)[kVerStep][4]) {
+template <int N>
+RL_DEVINL float step_largest(float (&z)[N][4]) {
     float m = -INFINITY;
 #pragma unroll
-    for (int s = 0; s < kVerStep; ++s)
+    for (int s = 0; s < N; ++s)
 #pragma unroll
         for (int j = 0; j < 4; ++j) m = max_nan(m, z[s][j]);
     uint32_t key = __reduce_max_sync(0xffffffffu, key_of(m + 0.f));
     if (key >= 0xff800000u) {
         m = -INFINITY;
 #pragma unroll
-        for (int s = 0; s < kVerStep; ++s)
+        for (int s = 0; s < N; ++s)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 z[s][j] = z[s][j] < INFINITY ? z[s][j] : -INFINITY;
@@ -420,33 +447,49 @@ __device__ __noinline__ unsigned long long sum_left(const rl_dist& dp, const Ver
     const VerRow w = *rp, o = *rq;
     const int lane = threadIdx.x & 31;
     const float lam_hi = rintf(lam.hi * 2048.f) * (1.f / 2048.f), lam_lo = (lam.hi - lam_hi) + lam.lo;
+    const bool plain = w.plain && o.plain;
     unsigned long long mine = 0;
+    constexpr int N = kVerStep / 2;              // half a step at a time, for the registers
+    from *= 2;
+    steps *= 2;
 #pragma unroll 1
     for (int k = first; k < steps; k += stride) {
-        float z[kVerStep][4], y[kVerStep][4];
-        step_load(dp, w, V, (from + k) * kVerStep * kVerPart, z);
-        step_load(dq, o, V, (from + k) * kVerStep * kVerPart, y);
+        const int i0 = (from + k) * N * kVerPart;
+        float z[N][4], y[N][4];
+        step_load(dp, w, V, i0, z);
+        step_load(dq, o, V, i0, y);
         const float m = step_largest(z);
         const float ex = w.plain ? fmaf(m, w.c.hi, -w.R) : (m - w.M) * w.c.hi;
         unsigned long long sum = 0;
         if (ex > -100.f) {
             const float ref = fminf(ceilf(ex), 1.f), ref_q = ref + lam_hi;
             const float zlow = fmaxf(logit_of(w, ref, -64.f), -FLT_MAX), ylow = fmaxf(logit_of(o, ref_q, -64.f), -FLT_MAX),
-                        yhigh = logit_of(o, ref_q, 0.75f);
+                        yhigh = logit_of(o, ref_q, 0.75f), magic = 6144.f - (w.R + ref), magic_q = 6144.f - (o.R + ref_q);
+            step_largest(y);                     // (NaN and +inf become -inf)
             uint32_t top = 0;
             int low = 0;
 #pragma unroll
-            for (int s = 0; s < kVerStep; ++s) {
+            for (int s = 0; s < N; ++s) {
                 LaneSum acc;
+                FF v[4], q[4];
+                if (plain) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        v[j] = weight_off(fmaxf(z[s][j], zlow), 0.f, w.c, magic, 0.f, tab);
+                        q[j] = weight_off(fminf(fmaxf(y[s][j], ylow), yhigh), 0.f, o.c, magic_q, lam_lo, tab);
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        v[j] = weight_of(fmaxf(z[s][j], zlow), w, ref, 0.f, tab);
+                        q[j] = weight_of(fminf(fmaxf(y[s][j], ylow), yhigh), o, ref_q, lam_lo, tab);
+                    }
+                }
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    FF v = weight_of(fmaxf(z[s][j], zlow), w, ref, 0.f, tab);
-                    const float x = y[s][j] < INFINITY ? y[s][j] : -INFINITY;
-                    FF q = weight_of(fminf(fmaxf(x, ylow), yhigh), o, ref_q, lam_lo, tab);
-                    if (x < ylow) q = {0.f, 0.f};
-                    v = left_of(v, q);
-                    if (z[s][j] < zlow) v = {0.f, 0.f};
-                    acc.add(v.hi, v.lo);
+                    if (y[s][j] < ylow) q[j] = {0.f, 0.f};
+                    const FF x = z[s][j] < zlow ? FF{0.f, 0.f} : left_of(v[j], q[j]);
+                    acc.add(x.hi, x.lo);
                 }
                 const uint32_t t = acc.warp_top();
                 const int l = acc.warp_low();
@@ -459,12 +502,12 @@ __device__ __noinline__ unsigned long long sum_left(const rl_dist& dp, const Ver
             const int sh = w.prec - 50 + static_cast<int>(ref);
             sum = sh >= 0 ? w50 << sh : sh > -64 ? (w50 + (1ull << (-sh - 1))) >> -sh : 0ull;
         }
-        if (lane < kVerStep) {
-            cs[k * kVerStep + lane] = sum;
+        if (lane < N) {
+            cs[k * N + lane] = sum;
             mine += sum;
         }
     }
-    mine = lane < kVerStep ? mine : 0ull;
+    mine = lane < N ? mine : 0ull;
     return warp_sum(mine);
 }
 
@@ -1013,7 +1056,7 @@ struct Draw : Request<kDrawThreads> {
     }
 };
 
-__global__ void __launch_bounds__(kDrawThreads, 4) draw_kernel(const __grid_constant__ VerArgs g) {
+__global__ void __launch_bounds__(kDrawThreads, kDrawBlocks) draw_kernel(const __grid_constant__ VerArgs g) {
     extern __shared__ __align__(16) uint8_t raw[];
     VerShared<kDrawThreads>& s = *reinterpret_cast<VerShared<kDrawThreads>*>(raw);
     const long long r = blockIdx.x / static_cast<unsigned>(g.cs);
@@ -1092,12 +1135,14 @@ int verify_impl(const rl_verify_args* a, void* ws, int32_t* status, cudaStream_t
         if (rc != RL_OK) return rc;
         ++launches;
         if (g.draws) {
-            // a block's slice of the vocabulary: at least 16 steps of 512, two for each of its warps
+            // as many blocks a request as the GPU holds at once (a second round of blocks that start anew costs more than longer
+            // slices: 128 requests took 238 us in 1024 blocks and 234 us in 512), up to eight, each of at least 16 steps of 512
             const int all = static_cast<int>((a->V + kVerStep * kVerPart - 1) / (kVerStep * kVerPart));
-            g.cs = 1;
-            while (g.cs < 8 && all > 16 * g.cs) g.cs *= 2;
+            const long long room = static_cast<long long>(kDrawBlocks) * num_sms() / a->R;
+            g.cs = static_cast<int>(room < 1 ? 1 : room < 8 ? room : 8);
+            while (g.cs > 1 && all < 16 * (g.cs - 1)) --g.cs;
             g.per = (all + g.cs - 1) / g.cs;
-            const size_t fixed = sizeof(VerShared<kDrawThreads>), most = ((size_t(1) << 20) / kVerPart / 8 + kVerStep) * 8;
+            const size_t fixed = sizeof(VerShared<kDrawThreads>), most = ((size_t(1) << 20) / kVerPart + kVerStep) * 8;
             if (!allow_smem(draw_kernel, static_cast<int>(fixed + most), draw)) return RL_ERR_CUDA;
             cudaLaunchConfig_t cfg = {};
             cfg.gridDim = dim3(static_cast<unsigned>(a->R * g.cs), 1, 1);
