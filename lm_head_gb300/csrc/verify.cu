@@ -28,8 +28,8 @@ namespace rl {
 constexpr int kVerPart = 128;                  // logits of a part
 constexpr int kVerStep = 4;                    // parts that a warp sums up at a time
 constexpr int kDecideThreads = 512;            // a row of either side a warp
-constexpr int kDrawThreads = 256;
-constexpr int kDrawBlocks = 4;                 // of them on a multiprocessor
+constexpr int kDrawThreads = 512;
+constexpr int kDrawBlocks = 2;                 // of them on a multiprocessor
 constexpr int kChunkThreads = 256;
 constexpr int kChunkPacks = 8;                 // 16-byte loads of a lane: 4 KB a warp
 constexpr int kUsedRows = 32768;               // rows of a step whose use is looked up in shared memory
@@ -250,6 +250,12 @@ struct VerDraw {
     VerRow row[2];
 };
 
+// 2^lam as it enters the draft's weights: an integer power, a part in steps of 2^-11 in [0, 1) and the rest.
+struct Lam {
+    int whole;
+    float hi, lo;
+};
+
 template <int NT>
 struct VerShared {
     float2 tab[2048];
@@ -262,6 +268,8 @@ struct VerShared {
     int flag, token;
     float lpx;
     FF lam;                         // log2 of the draft's total over the target's, as they are counted
+    Lam lam0;                       // as their fp32 sums have it
+    float turn;                     // ln 2 times the difference
     unsigned long long unit;
 };
 
@@ -381,6 +389,11 @@ RL_DEVINL float step_largest(float (&z)[N][4]) {
     return z_of(key);
 }
 
+// Units of 2^(ref - 50) in units of 2^-prec.
+RL_DEVINL unsigned long long in_units(unsigned long long w50, int ref, int prec) {
+    const int sh = prec - 50 + ref;
+    return sh >= 0 ? w50 << sh : sh > -64 ? (w50 + (1ull << (-sh - 1))) >> -sh : 0ull;
+}
 // Sums of the weights of `steps` steps of a row from step `from` on, by a warp that takes every `stride`-th; the parts' sums
 // into cs where it is given.  Each step is summed relative to its own largest weight.  Lane 0 has the sum.
 __device__ __noinline__ unsigned long long sum_steps(const rl_dist& d, const VerRow* row, int V, int from, int steps, int first, int stride,
@@ -429,9 +442,7 @@ __device__ __noinline__ unsigned long long sum_steps(const rl_dist& d, const Ver
                     low = l;
                 }
             }
-            const unsigned long long w50 = LaneSum::total(top, low);
-            const int sh = w.prec - 50 + static_cast<int>(ref);
-            sum = sh >= 0 ? w50 << sh : sh > -64 ? (w50 + (1ull << (-sh - 1))) >> -sh : 0ull;
+            sum = in_units(LaneSum::total(top, low), static_cast<int>(ref), w.prec);
         }
         if (lane < kVerStep) {
             if (cs) cs[k * kVerStep + lane] = sum;
@@ -441,74 +452,94 @@ __device__ __noinline__ unsigned long long sum_steps(const rl_dist& d, const Ver
     mine = lane < kVerStep ? mine : 0ull;
     return warp_sum(mine);
 }
-// The same of what is left of a target's weights beside a draft's logits.
-__device__ __noinline__ unsigned long long sum_left(const rl_dist& dp, const VerRow* rp, const rl_dist& dq, const VerRow* rq, FF lam, int V, int from,
-                                                    int steps, int first, int stride, unsigned long long* cs, const float2* tab) {
-    const VerRow w = *rp, o = *rq;
-    const int lane = threadIdx.x & 31;
-    const float lam_hi = rintf(lam.hi * 2048.f) * (1.f / 2048.f), lam_lo = (lam.hi - lam_hi) + lam.lo;
-    const bool plain = w.plain && o.plain;
-    unsigned long long mine = 0;
+// Up to 15 weights of at most 1 in a lane (as LaneSum, from 16 on, where the last place is 2^-19 too).
+struct LongSum {
+    float top = 16.f, low = 0.f;
+    RL_DEVINL void add(FF x) {
+        const float n = __fadd_rn(top, __fadd_rn(x.hi, x.lo));
+        low += __fadd_rn(__fsub_rn(x.hi, __fsub_rn(n, top)), x.lo);
+        top = n;
+    }
+    RL_DEVINL unsigned long long warp_total() const {
+        return LaneSum::total(__reduce_add_sync(0xffffffffu, __float_as_uint(top) - 0x41800000u), __reduce_add_sync(0xffffffffu, __float2int_rn(low * 0x1p43f)));
+    }
+};
+// A target's and a draft's rows of logits in one pass: the totals of both, and of each part what is left, max(p - q, 0), with the ratio
+// of the totals taken from the fp32 sums (2^lam) - and the draft's weight where something is left, in ds, by which the parts are put
+// right once the ratio is known: what is left changes by q d(lam) ln 2 there, and the tokens at which p and q change places matter in
+// second order (d(lam)^2, below 2^-36).  Three passes (both totals, then what is left) took half as long again.
+// The draft's total comes out as 2^-(hi + lo) times itself.
+template <bool kPlain>
+RL_DEVINL void sum_both_of(const rl_dist& dp, const VerRow& w, const rl_dist& dq, const VerRow& o, Lam lam, int V, int from, int steps, int first,
+                           int stride, unsigned long long* cs, float* ds, const float2* tab, unsigned long long& tp, unsigned long long& tq) {
     constexpr int N = kVerStep / 2;              // half a step at a time, for the registers
-    from *= 2;
-    steps *= 2;
+    const int lane = threadIdx.x & 31;
+    const bool wp = kPlain || w.plain, op = kPlain || o.plain;
 #pragma unroll 1
-    for (int k = first; k < steps; k += stride) {
-        const int i0 = (from + k) * N * kVerPart;
-        float z[N][4], y[N][4];
-        step_load(dp, w, V, i0, z);
-        step_load(dq, o, V, i0, y);
-        const float m = step_largest(z);
-        const float ex = w.plain ? fmaf(m, w.c.hi, -w.R) : (m - w.M) * w.c.hi;
+    for (int k = first; k < 2 * steps; k += stride) {
+        const int i0 = (2 * from + k) * N * kVerPart;
         unsigned long long sum = 0;
-        if (ex > -100.f) {
-            const float ref = fminf(ceilf(ex), 1.f), ref_q = ref + lam_hi;
-            const float zlow = fmaxf(logit_of(w, ref, -64.f), -FLT_MAX), ylow = fmaxf(logit_of(o, ref_q, -64.f), -FLT_MAX),
-                        yhigh = logit_of(o, ref_q, 0.75f), magic = 6144.f - (w.R + ref), magic_q = 6144.f - (o.R + ref_q);
-            step_largest(y);                     // (NaN and +inf become -inf)
+        float d_out = 0.f;
+        if (i0 < V) {
+            float z[N][4], y[N][4];
+            step_load(dp, w, V, i0, z);
+            step_load(dq, o, V, i0, y);
+            const float mz = step_largest(z), my = step_largest(y);
+            const float ez = wp ? fmaf(mz, w.c.hi, -w.R) : (mz - w.M) * w.c.hi, ey = op ? fmaf(my, o.c.hi, -o.R) : (my - o.M) * o.c.hi;
+            // (below 2^-100 of its row's largest, or -inf, a side is nothing here)
+            const float rz = ez > -100.f ? fminf(ceilf(ez), 1.f) : 0.f, ry = ey > -100.f ? fminf(ceilf(ey), 1.f) : 0.f;
+            const float zlow = ez > -100.f ? fmaxf(wp ? (rz + w.R - 64.f) * w.inv_c : w.M + (rz - 64.f) * w.inv_c, -FLT_MAX) : FLT_MAX;
+            const float ylow = ey > -100.f ? fmaxf(op ? (ry + o.R - 64.f) * o.inv_c : o.M + (ry - 64.f) * o.inv_c, -FLT_MAX) : FLT_MAX;
+            const float magic_z = 6144.f - (w.R + rz), magic_y = 6144.f - (o.R + ry + lam.hi);
+            const float scale = power_of_2(min(max(static_cast<int>(ry - rz) - lam.whole, -126), 100));
+            LongSum sp, sq;
             uint32_t top = 0;
-            int low = 0;
+            int low = 0, d_in = 0;
 #pragma unroll
             for (int s = 0; s < N; ++s) {
                 LaneSum acc;
-                FF v[4], q[4];
-                if (plain) {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        v[j] = weight_off(fmaxf(z[s][j], zlow), 0.f, w.c, magic, 0.f, tab);
-                        q[j] = weight_off(fminf(fmaxf(y[s][j], ylow), yhigh), 0.f, o.c, magic_q, lam_lo, tab);
-                    }
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        v[j] = weight_of(fmaxf(z[s][j], zlow), w, ref, 0.f, tab);
-                        q[j] = weight_of(fminf(fmaxf(y[s][j], ylow), yhigh), o, ref_q, lam_lo, tab);
-                    }
-                }
+                float d = 0.f;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    if (y[s][j] < ylow) q[j] = {0.f, 0.f};
-                    const FF x = z[s][j] < zlow ? FF{0.f, 0.f} : left_of(v[j], q[j]);
-                    acc.add(x.hi, x.lo);
+                    // (a clamped logit's weight is not used, but has to be one)
+                    const float a = z[s][j] < zlow ? (wp ? w.R * w.inv_c : w.M) : z[s][j], b = y[s][j] < ylow ? (op ? o.R * o.inv_c : o.M) : y[s][j];
+                    const FF da = wp ? FF{a, 0.f} : two_sum(a, -w.M), db = op ? FF{b, 0.f} : two_sum(b, -o.M);
+                    FF v = weight_off(da.hi, da.lo, w.c, magic_z, 0.f, tab), q = weight_off(db.hi, db.lo, o.c, magic_y, lam.lo, tab);
+                    if (z[s][j] < zlow) v = {0.f, 0.f};
+                    if (y[s][j] < ylow) q = {0.f, 0.f};
+                    sp.add(v);
+                    sq.add(q);
+                    q = {q.hi * scale, q.lo * scale};
+                    v = left_of(v, q);
+                    if (v.hi > 0.f) d += q.hi;
+                    acc.add(v.hi, v.lo);
                 }
                 const uint32_t t = acc.warp_top();
-                const int l = acc.warp_low();
+                const int l = acc.warp_low(), e = __reduce_add_sync(0xffffffffu, __float2int_rn(d * 0x1p20f));
                 if (lane == s) {
                     top = t;
                     low = l;
+                    d_in = e;
                 }
             }
-            const unsigned long long w50 = LaneSum::total(top, low);
-            const int sh = w.prec - 50 + static_cast<int>(ref);
-            sum = sh >= 0 ? w50 << sh : sh > -64 ? (w50 + (1ull << (-sh - 1))) >> -sh : 0ull;
+            sum = in_units(LaneSum::total(top, low), static_cast<int>(rz), w.prec);
+            d_out = static_cast<float>(d_in) * power_of_2(static_cast<int>(rz) - 20);
+            const unsigned long long a = in_units(sp.warp_total(), static_cast<int>(rz), w.prec), b = in_units(sq.warp_total(), static_cast<int>(ry), o.prec);
+            tp += a;
+            tq += b;
         }
         if (lane < N) {
             cs[k * N + lane] = sum;
-            mine += sum;
+            ds[k * N + lane] = d_out;
         }
     }
-    mine = lane < N ? mine : 0ull;
-    return warp_sum(mine);
+}
+__device__ __noinline__ ulonglong2 sum_both(const rl_dist& dp, const VerRow* rp, const rl_dist& dq, const VerRow* rq, Lam lam, int V, int from, int steps,
+                                            int first, int stride, unsigned long long* cs, float* ds, const float2* tab) {
+    unsigned long long tp = 0, tq = 0;
+    if (rp->plain && rq->plain) sum_both_of<true>(dp, *rp, dq, *rq, lam, V, from, steps, first, stride, cs, ds, tab, tp, tq);
+    else sum_both_of<false>(dp, *rp, dq, *rq, lam, V, from, steps, first, stride, cs, ds, tab, tp, tq);
+    return make_ulonglong2(tp, tq);
 }
 
 template <int NT>
@@ -865,6 +896,7 @@ __global__ void __launch_bounds__(kDecideThreads, 2) decide_kernel(const __grid_
 // A cluster of blocks a request: the new token from rows of logits.
 struct Draw : Request<kDrawThreads> {
     unsigned long long* cs;       // sums of the slice's parts
+    float* ds;                    // and the draft's weight where something is left
     int rank, from, steps, phase; // its steps
 
     // The cluster's sum of v (the same in a block's threads), and the sum of the blocks before.
@@ -925,29 +957,61 @@ struct Draw : Request<kDrawThreads> {
         return x >= static_cast<double>(w) ? w : static_cast<unsigned long long>(__double2ll_rn(x));
     }
 
+    // What is left of a dense target beside a dense draft: the slice's sum (its parts in cs); counts both totals.
+    RL_DEVINL unsigned long long left_of_rows() {
+        VerRow& p = s.draw.row[0];
+        VerRow& q = s.draw.row[1];
+        // log2 of a total in the row's unit, by the fp32 sums: S e^(M / T) over 2^R
+        auto rough = [](const VerRow& w) -> double {
+            const double c = static_cast<double>(w.c.hi) + static_cast<double>(w.c.lo);
+            return static_cast<double>(log2f(w.S)) + (w.plain ? w.M * c - w.R : 0.0);
+        };
+        if (tid == 0) {
+            const double lam = rough(q) - rough(p);
+            s.lam0.whole = static_cast<int>(floor(lam));
+            const double f = lam - s.lam0.whole;
+            s.lam0.hi = static_cast<float>(floor(f * 2048.0)) * (1.f / 2048.f);
+            s.lam0.lo = static_cast<float>(f - static_cast<double>(s.lam0.hi));
+        }
+        __syncthreads();
+        const Lam lam0 = s.lam0;
+        const ulonglong2 x = sum_both(g.side[0].d, &p, g.side[1].d, &q, lam0, V, from, steps, warp, kWarps, cs, ds, s.tab);
+        unsigned long long before;
+        const unsigned long long tp = cluster_sum(block_sum(lane == 0 ? x.x : 0ull), before), tq = cluster_sum(block_sum(lane == 0 ? x.y : 0ull), before);
+        __syncthreads();
+        if (tid == 0) {
+            const double f = static_cast<double>(lam0.hi) + static_cast<double>(lam0.lo);
+            const double lam = (log2(static_cast<double>(tq)) - q.prec + f) - (log2(static_cast<double>(tp)) - p.prec);
+            s.lam.hi = static_cast<float>(lam);
+            s.lam.lo = static_cast<float>(lam - static_cast<double>(s.lam.hi));
+            s.turn = static_cast<float>((lam - lam0.whole - f) * 0.69314718055994530942);
+            p.total = tp;
+            q.total = tq;                        // (times 2^-f: only lam is read of it)
+        }
+        __syncthreads();
+        const float turn = s.turn * power_of_2(p.prec);
+        unsigned long long v = 0;
+        for (int i = tid; i < steps * kVerStep; i += kDrawThreads) {
+            const long long y = static_cast<long long>(cs[i]) + __float2ll_rn(ds[i] * turn);
+            cs[i] = y > 0 ? static_cast<unsigned long long>(y) : 0ull;
+            v += cs[i];
+        }
+        return block_sum(v);
+    }
+
     RL_DEVINL void draw_dense(long long t, float u, int& bits) {
         const VerRow& p = s.draw.row[0];
         const VerRow& q = s.draw.row[1];
         const rl_dist& dp = g.side[0].d;
         const rl_dist& dq = g.side[1].d;
         bool whole = q.mode == kDistNone;
-        unsigned long long before;
-        if (q.mode == kDistDense) count_total(1, before);
-        unsigned long long mine = count_total(0, before), total = p.total;
-        if (q.mode == kDistDense) {
-            if (tid == 0) {
-                const double lam = (log2(static_cast<double>(q.total)) - q.prec) - (log2(static_cast<double>(p.total)) - p.prec);
-                s.lam.hi = static_cast<float>(lam);
-                s.lam.lo = static_cast<float>(lam - static_cast<double>(s.lam.hi));
-            }
-            __syncthreads();
-        }
         const int p0 = from * kVerStep, parts = steps * kVerStep;
+        unsigned long long before, mine, total = 0;
+        if (q.mode == kDistDense) mine = left_of_rows();
+        else mine = count_total(0, before);
+        if (whole) total = p.total;
         for (int tries = 0; tries < 2; ++tries) {
-            if (!whole && q.mode == kDistDense) {
-                const unsigned long long x = sum_left(dp, &p, dq, &q, s.lam, V, from, steps, warp, kWarps, cs, s.tab);
-                mine = block_sum(lane == 0 ? x : 0ull);
-            } else {
+            if (whole || q.mode != kDistDense) {         // (else it is summed up already)
                 if (tries > 0) mine = slice_sum(0);
                 if (!whole) {
                     // the draft's tokens in the slice, off their parts
@@ -1062,8 +1126,8 @@ __global__ void __launch_bounds__(kDrawThreads, kDrawBlocks) draw_kernel(const _
     const long long r = blockIdx.x / static_cast<unsigned>(g.cs);
     const int tid = threadIdx.x, V = static_cast<int>(g.a.V), rank = static_cast<int>(blockIdx.x - r * g.cs);
     const int all = (V + kVerStep * kVerPart - 1) / (kVerStep * kVerPart), from = min(rank * g.per, all);
-    Draw q{{g, s, V, tid, tid & 31, tid >> 5}, reinterpret_cast<unsigned long long*>(raw + sizeof(VerShared<kDrawThreads>)), rank, from,
-           min(g.per, all - from), 0};
+    unsigned long long* cs = reinterpret_cast<unsigned long long*>(raw + sizeof(VerShared<kDrawThreads>));
+    Draw q{{g, s, V, tid, tid & 31, tid >> 5}, cs, reinterpret_cast<float*>(cs + g.per * kVerStep), rank, from, min(g.per, all - from), 0};
     int bits = 0;
     wait_for_previous();
     const int words = static_cast<int>(sizeof(VerDraw) / 8);
@@ -1135,19 +1199,21 @@ int verify_impl(const rl_verify_args* a, void* ws, int32_t* status, cudaStream_t
         if (rc != RL_OK) return rc;
         ++launches;
         if (g.draws) {
-            // as many blocks a request as the GPU holds at once (a second round of blocks that start anew costs more than longer
-            // slices: 128 requests took 238 us in 1024 blocks and 234 us in 512), up to eight, each of at least 16 steps of 512
+            // as many blocks a request as the GPU holds at once, up to eight, each of at least 16 steps of 512: a second round of
+            // blocks that start anew costs more than longer slices (of 256 threads: 128 requests 196 us in 1024 blocks, 188 us in
+            // 512).  Where targets may be support rows about half of the requests are expected to be done (256 of them 145 us in
+            // 512 blocks, 121 us in 1024)
             const int all = static_cast<int>((a->V + kVerStep * kVerPart - 1) / (kVerStep * kVerPart));
-            const long long room = static_cast<long long>(kDrawBlocks) * num_sms() / a->R;
+            const long long room = static_cast<long long>(kDrawBlocks) * num_sms() * (a->target.offsets ? 2 : 1) / a->R;
             g.cs = static_cast<int>(room < 1 ? 1 : room < 8 ? room : 8);
             while (g.cs > 1 && all < 16 * (g.cs - 1)) --g.cs;
             g.per = (all + g.cs - 1) / g.cs;
-            const size_t fixed = sizeof(VerShared<kDrawThreads>), most = ((size_t(1) << 20) / kVerPart + kVerStep) * 8;
+            const size_t fixed = sizeof(VerShared<kDrawThreads>), most = ((size_t(1) << 20) / kVerPart + kVerStep) * 12;
             if (!allow_smem(draw_kernel, static_cast<int>(fixed + most), draw)) return RL_ERR_CUDA;
             cudaLaunchConfig_t cfg = {};
             cfg.gridDim = dim3(static_cast<unsigned>(a->R * g.cs), 1, 1);
             cfg.blockDim = dim3(kDrawThreads, 1, 1);
-            cfg.dynamicSmemBytes = fixed + static_cast<size_t>(g.per) * kVerStep * 8;
+            cfg.dynamicSmemBytes = fixed + static_cast<size_t>(g.per) * kVerStep * 12;
             cfg.stream = stream;
             cudaLaunchAttribute attr[2];
             attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
