@@ -51,6 +51,7 @@ struct MarkArgs {
 };
 
 __global__ void __launch_bounds__(kMoveThreads) mark_kernel(const MarkArgs p) {
+    let_next_start();
     const int lane = threadIdx.x & 31;
     const long long warps = static_cast<long long>(gridDim.x) * (kMoveThreads / 32);
     const long long first = p.t[0].rows * p.t[0].segs, units = first + p.t[1].rows * p.t[1].segs;
@@ -79,6 +80,22 @@ __global__ void __launch_bounds__(kMoveThreads) mark_kernel(const MarkArgs p) {
     }
     set_status(p.status, bits);
 }
+
+// f(words, their number) over a bitmap's words [0, n), 16 bytes a thread and four loads at a time (bitmaps are 16-byte aligned and
+// padded to 16 bytes with zeros).
+template <typename F>
+RL_DEVINL void each_words(const uint32_t* map, long long n, F f) {
+    const uint4* m = reinterpret_cast<const uint4*>(map);
+    const long long q = (n + 3) / 4;
+    for (long long i = threadIdx.x; i < q; i += 4 * blockDim.x) {
+        uint4 v[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = i + k * blockDim.x < q ? m[i + k * blockDim.x] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) f(v[k], (i + k * blockDim.x) * 4);
+    }
+}
+RL_DEVINL int bits_of(uint4 v) { return __popc(v.x) + __popc(v.y) + __popc(v.z) + __popc(v.w); }
 
 // Block sums of two numbers; every thread gets the totals.
 RL_DEVINL long long block_total(long long v, long long* red) {
@@ -128,11 +145,15 @@ __global__ void __launch_bounds__(kSweepThreads) sweep_kernel(const SweepArgs p)
     const long long w0 = blockIdx.x * p.per_block, w1 = min(w0 + p.per_block, p.words);
     int bits = 0;
     long long before = 0, all = 0;
-    for (long long w = threadIdx.x; w < p.words; w += kSweepThreads) {
-        const int n = __popc(p.drop[w] & ~p.live[w]);
+    wait_for_previous();
+    const uint4* live4 = reinterpret_cast<const uint4*>(p.live);
+    each_words(p.drop, p.words, [&](uint4 v, long long w) {
+        if (w >= p.words) return;
+        const uint4 l = live4[w / 4];
+        const int n = bits_of(make_uint4(v.x & ~l.x, v.y & ~l.y, v.z & ~l.z, v.w & ~l.w));
         all += n;
         if (w < w0) before += n;
-    }
+    });
     all = block_total(all, red);
     long long rank = block_total(before, red);
     long long used = *p.free_used;
@@ -161,7 +182,7 @@ __global__ void __launch_bounds__(kSweepThreads) sweep_kernel(const SweepArgs p)
     set_status(p.status, bits);
 }
 
-static long long words_of(int64_t n_pages) { return (n_pages + 31) / 32; }
+static long long words_of(int64_t n_pages) { return (n_pages + 127) / 128 * 4; }      // whole 16 bytes
 static int mark_blocks(long long units) {
     const long long blocks = (units + kMoveThreads / 32 - 1) / (kMoveThreads / 32), cap = 8ll * num_sms();
     return static_cast<int>(blocks < 1 ? 1 : blocks < cap ? blocks : cap);
@@ -194,7 +215,8 @@ int page_release_impl(const rl_page_release_args* a, void* ws, int32_t* status, 
     if (steps < 1) steps = 1;
     const long long grid = steps < num_sms() ? steps : num_sms();
     s.per_block = (steps + grid - 1) / grid * kSweepThreads;
-    sweep_kernel<<<static_cast<unsigned>(grid), kSweepThreads, 0, stream>>>(s);
+    const int rc = launch_after(sweep_kernel, dim3(static_cast<unsigned>(grid)), kSweepThreads, 0, true, stream, s);
+    if (rc != RL_OK) return rc;
     count_launch(2);
     return cudaPeekAtLastError() == cudaSuccess ? RL_OK : RL_ERR_CUDA;
 }
@@ -212,6 +234,7 @@ struct ForkArgs {
 
 __global__ void __launch_bounds__(kForkThreads) fork_plan_kernel(const ForkArgs p) {
     __shared__ int red[kForkThreads / 32];
+    let_next_start();
     const rl_page_fork_args& a = p.a;
     const int mask = a.page_size - 1;
     int bits = 0;
@@ -290,6 +313,7 @@ __global__ void __launch_bounds__(kMoveThreads) fork_rows_kernel(const ForkArgs 
     const long long segs = (a.table_width + kSeg - 1) / kSeg, units = a.C * segs;
     const long long warps = static_cast<long long>(gridDim.x) * (kMoveThreads / 32);
     int bits = 0;
+    wait_for_previous();
     for (long long id = static_cast<long long>(blockIdx.x) * (kMoveThreads / 32) + (threadIdx.x >> 5); id < units; id += warps) {
         const long long c = id / segs, j0 = (id - c * segs) * kSeg, end = min(j0 + kSeg, static_cast<long long>(a.table_width));
         const int page = p.takes[c];
@@ -329,7 +353,8 @@ int page_fork_impl(const rl_page_fork_args* a, void* ws, int32_t* status, cudaSt
     int launches = 1;
     const long long units = a->C * ((a->table_width + kSeg - 1) / kSeg);
     if (units > 0) {
-        fork_rows_kernel<<<mark_blocks(units), kMoveThreads, 0, stream>>>(p);
+        const int rc = launch_after(fork_rows_kernel, dim3(static_cast<unsigned>(mark_blocks(units))), kMoveThreads, 0, true, stream, p);
+        if (rc != RL_OK) return rc;
         ++launches;
     }
     count_launch(launches);
@@ -352,19 +377,25 @@ __global__ void __launch_bounds__(kSweepThreads) compact_plan_kernel(const Compa
     const rl_page_compact_args& a = p.a;
     const long long w0 = blockIdx.x * p.per_block, w1 = min(w0 + p.per_block, p.words);
     long long before = 0, all = 0;
-    for (long long w = threadIdx.x; w < p.words; w += kSweepThreads) {
-        const int n = __popc(p.live[w]);
+    wait_for_previous();
+    let_next_start();
+    each_words(p.live, p.words, [&](uint4 v, long long w) {
+        const int n = bits_of(v);
         all += n;
         if (w < w0) before += n;
-    }
+    });
     const long long n_live = block_total(all, red);
     long long rank = block_total(before, red);
     // live pages below n_live: they stay
     long long stay = 0;
-    for (long long w = threadIdx.x; w * 32 < n_live; w += kSweepThreads) {
-        const uint32_t x = p.live[w];
-        stay += __popc(n_live - w * 32 < 32 ? x & ((1u << (n_live - w * 32)) - 1u) : x);
-    }
+    each_words(p.live, (n_live + 31) / 32, [&](uint4 v, long long w) {
+        const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const long long n = n_live - (w + k) * 32;             // pages of the word below n_live
+            if (n > 0) stay += __popc(n < 32 ? x[k] & ((1u << n) - 1u) : x[k]);
+        }
+    });
     stay = block_total(stay, red);
     const long long moves = n_live - stay;
     for (long long w = w0; w < w1; w += kSweepThreads) {
@@ -402,6 +433,7 @@ __global__ void __launch_bounds__(kMoveThreads) compact_rows_kernel(const Compac
     const long long segs[2] = {(a.table_width + kSeg - 1) / kSeg, (a.prefix_width + kSeg - 1) / kSeg};
     const long long first = a.R * segs[0], units = first + a.G * segs[1];
     const long long warps = static_cast<long long>(gridDim.x) * (kMoveThreads / 32);
+    wait_for_previous();
     const int n_live = *a.free_used_out;
     int stay = 0;
     if (n_live > 0) {
@@ -457,11 +489,13 @@ int page_compact_impl(const rl_page_compact_args* a, void* ws, int32_t* status, 
     if (steps < 1) steps = 1;
     const long long grid = steps < num_sms() ? steps : num_sms();
     p.per_block = (steps + grid - 1) / grid * kSweepThreads;
-    compact_plan_kernel<<<static_cast<unsigned>(grid), kSweepThreads, 0, stream>>>(p);
+    int rc = launch_after(compact_plan_kernel, dim3(static_cast<unsigned>(grid)), kSweepThreads, 0, true, stream, p);
+    if (rc != RL_OK) return rc;
     int launches = 2;
     const long long units = a->R * ((a->table_width + kSeg - 1) / kSeg) + a->G * ((a->prefix_width + kSeg - 1) / kSeg);
     if (units > 0) {
-        compact_rows_kernel<<<mark_blocks(units), kMoveThreads, 0, stream>>>(p);
+        rc = launch_after(compact_rows_kernel, dim3(static_cast<unsigned>(mark_blocks(units))), kMoveThreads, 0, true, stream, p);
+        if (rc != RL_OK) return rc;
         ++launches;
     }
     count_launch(launches);

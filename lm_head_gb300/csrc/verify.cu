@@ -46,6 +46,7 @@ struct VerArgs {
     VerSide side[2];    // target, draft
     int32_t* status;
     bool sure;          // no draft distribution
+    int group;          // chunks that a warp takes one after another
     int cs, per;        // blocks of a request's draw; steps of a block's slice
     struct VerDraw* draws;      // [R] (NULL: no logits on either side)
 };
@@ -91,6 +92,11 @@ RL_DEVINL float2 chunk_of(const T* row, int V, int chunk, float Tm, bool& bad) {
     const int phase = static_cast<int>((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T));
     const int i0 = (chunk * kChunkPacks * 32 + lane) * E - phase;
     uint4 q[kChunkPacks];
+    const int first = chunk * kChunkPacks * 32 * E - phase;
+    if (first >= 0 && first + kChunkPacks * 32 * E <= V) {
+#pragma unroll
+        for (int k = 0; k < kChunkPacks; ++k) q[k] = __ldcs(reinterpret_cast<const uint4*>(row + i0 + k * 32 * E));
+    } else
 #pragma unroll
     for (int k = 0; k < kChunkPacks; ++k) {
         const int i = i0 + k * 32 * E;
@@ -203,25 +209,35 @@ __global__ void __launch_bounds__(kChunkThreads, 3) chunk_kernel(const __grid_co
         }
         __syncthreads();
     }
+    // one or two chunks of a row a warp
     const long long warps = static_cast<long long>(gridDim.x) * (kChunkThreads / 32);
-    const long long first = a.T * g.side[0].nc, units = first + a.T * g.side[1].nc;
+    const int groups[2] = {(g.side[0].nc + g.group - 1) / g.group, (g.side[1].nc + g.group - 1) / g.group};
+    const long long first = a.T * groups[0], units = first + a.T * groups[1];
     int bits = 0;
     bool bad = false;
     for (long long id = static_cast<long long>(blockIdx.x) * (kChunkThreads / 32) + (threadIdx.x >> 5); id < units; id += warps) {
         const int side = id >= first ? 1 : 0;
         const VerSide& s = g.side[side];
-        const long long x = side ? id - first : id, t = x / s.nc;
-        const int chunk = static_cast<int>(x - t * s.nc);
+        const long long x = side ? id - first : id;
+        const long long t = x <= UINT_MAX ? static_cast<uint32_t>(x) / static_cast<uint32_t>(groups[side]) : x / groups[side];
+        const int c0 = static_cast<int>(x - t * groups[side]) * g.group, c1 = min(c0 + g.group, s.nc);
         if (known && !((used[side][t >> 5] >> (t & 31)) & 1u)) continue;
         int row_bits = 0;
         const long long row = row_of(s.d, t, row_bits);
         if (row < 0 || is_support(s.d, row)) continue;
         const float Tm = temperature_of(s.d, row, bits);
-        float2 v;
-        if (s.dtype == RL_DTYPE_F32) v = chunk_of(static_cast<const float*>(s.d.logits) + row * s.d.row_stride, V, chunk, Tm, bad);
-        else if (s.dtype == RL_DTYPE_BF16) v = chunk_of(static_cast<const __nv_bfloat16*>(s.d.logits) + row * s.d.row_stride, V, chunk, Tm, bad);
-        else v = chunk_of(static_cast<const __half*>(s.d.logits) + row * s.d.row_stride, V, chunk, Tm, bad);
-        if ((threadIdx.x & 31) == 0) s.part[t * s.nc + chunk] = v;
+        float2 mine = make_float2(0.f, 0.f);
+        auto each = [&](auto* p) {
+#pragma unroll 1
+            for (int c = c0; c < c1; ++c) {
+                const float2 v = chunk_of(p, V, c, Tm, bad);
+                if ((threadIdx.x & 31) == c - c0) mine = v;
+            }
+        };
+        if (s.dtype == RL_DTYPE_F32) each(static_cast<const float*>(s.d.logits) + row * s.d.row_stride);
+        else if (s.dtype == RL_DTYPE_BF16) each(static_cast<const __nv_bfloat16*>(s.d.logits) + row * s.d.row_stride);
+        else each(static_cast<const __half*>(s.d.logits) + row * s.d.row_stride);
+        if (static_cast<int>(threadIdx.x & 31) < c1 - c0) s.part[t * s.nc + c0 + (threadIdx.x & 31)] = mine;
     }
     if (bad) bits |= RL_STATUS_NONFINITE;
     set_status(g.status, bits);
@@ -1183,10 +1199,12 @@ int verify_impl(const rl_verify_args* a, void* ws, int32_t* status, cudaStream_t
     ProfScope prof(RL_PROF_OTHER, stream);
     int launches = 0;
     if (a->T > 0) {
-        const long long units = a->T * (g.side[0].nc + g.side[1].nc), fill = (a->T + kChunkThreads - 1) / kChunkThreads;
+        // (two chunks share the look-up of their row; of few rows each warp gets one: 128 requests 186 us by ones, 178 by twos)
+        const long long cap = 3ll * num_sms(), chunks = a->T * (g.side[0].nc + g.side[1].nc);
+        g.group = chunks > cap * (kChunkThreads / 32) ? 2 : 1;
+        const long long units = a->T * ((g.side[0].nc + g.group - 1) / g.group + (g.side[1].nc + g.group - 1) / g.group), fill = (a->T + kChunkThreads - 1) / kChunkThreads;
         long long blocks = (units + kChunkThreads / 32 - 1) / (kChunkThreads / 32);
         if (blocks < fill) blocks = fill;
-        const long long cap = 3ll * num_sms();
         if (blocks > cap) blocks = cap;
         chunk_kernel<<<static_cast<unsigned>(blocks), kChunkThreads, 0, stream>>>(g);
         ++launches;
