@@ -139,11 +139,11 @@ struct DistShared {              // (small: three blocks with slices of 76 KB ar
     uint64_t bar, xbar;          // the slice has landed; the parts of the row's blocks have
     float2 xpart[8];             // (reference, sum) of each block of the cluster, without the support
     float2 part[kDistWarps];     // of each warp of this block
-    float4 sup[kDistWarps];      // of each support warp: largest logit, sum relative to it, the same of the teacher's
+    float4 sup[kDistWarps];      // of each support warp: largest logit, largest of the teacher's, sums relative to the block's largest
     FF sum[kDistWarps];          // pairs to be added up over the support warps
     float t0;                    // the teacher's probability of the rest
     float A[kDistWarps];
-    float M, rest, total;
+    float M, rest, inv_total;
 };
 
 // v into another block's `to`, counted by its barrier `bar` (both given by this block's own addresses).
@@ -311,26 +311,18 @@ __global__ void __launch_bounds__(NT, kBlocks) distill_kernel(const __grid_const
             if (x.in) {
                 mS = fmaxf(mS, x.z);
                 mT = fmaxf(mT, x.lq);
-                if (a.tail) wT = ff_add(wT, exp_table({x.lq, 0.f}));
             }
             if (rank == 0) sv.z[e] = x.z;
         }
         mS = warp_largest(mS);
         mT = warp_largest(mT);
-        float sS = 0.f, sT = 0.f;
-        each([&](const Entry& x, bool, long long) {
-            sS += x.z == -INFINITY ? 0.f : exp2f((x.z - mS) * p.c);
-            sT += exp2f((x.lq - mT) * p.c);
-        });
-        sS = warp_sum(sS);
-        sT = warp_sum(sT);
-        if (lane == 0) s.sup[warp] = make_float4(mS, sS, mT, sT);
+        if (lane == 0) s.sup[warp] = make_float4(mS, mT, 0.f, 0.f);
     }
     __syncthreads();
     float mS = -INFINITY, mT = -INFINITY;
     for (int k = 0; k < nw; ++k) {
         mS = fmaxf(mS, s.sup[k].x);
-        mT = fmaxf(mT, s.sup[k].z);
+        mT = fmaxf(mT, s.sup[k].y);
     }
     const bool any = mT > -INFINITY;             // the row has a teacher
     if (!mbar_wait(&s.bar, 0, p.status, p.wait_ns)) mbar_wait(&s.bar, 0, p.status);   // (the copy lands before the block goes on)
@@ -393,11 +385,25 @@ __global__ void __launch_bounds__(NT, kBlocks) distill_kernel(const __grid_const
         const float2 v = join(s.part, kWarps, -INFINITY);
         if (lane < p.cs) cluster_send(v, &s.xpart[rank], &s.xbar, lane);
     }
-    if (mine && a.tail) wT = support_sum(s.sum, wT, nw);
+    // (while the parts are on their way) the support's sums, of the student's weights and of the teacher's
+    if (mine) {
+        float sS = 0.f, sT = 0.f;
+        each([&](const Entry& x, bool, long long) {
+            sS += x.z == -INFINITY ? 0.f : exp2f((x.z - mS) * p.c);
+            if (a.tail) wT = ff_add(wT, exp_table({x.lq, 0.f}));
+            else sT += exp2f((x.lq - mT) * p.c);
+        });
+        sS = warp_sum(sS);
+        if (!a.tail) sT = warp_sum(sT);
+        if (lane == 0) s.sup[warp] = make_float4(0.f, 0.f, sS, sT);
+        if (a.tail) wT = support_sum(s.sum, wT, nw);
+        else if (nw > 1) asm volatile("bar.sync 1, %0;" ::"r"(stride) : "memory");
+        __syncwarp();
+    }
     if (!mbar_wait(&s.xbar, 0, p.status, p.wait_ns)) mbar_wait(&s.xbar, 0, p.status);
     // ---- the outcomes
     const float inv_T = p.inv_t.hi;
-    float M = 0.f, total = 1.f, lnT = 0.f, sT = 1.f, lnW = 0.f;
+    float M = 0.f, total = 1.f, inv_total = 1.f, lnT = 0.f, sT = 1.f, inv_sT = 1.f, lnW = 0.f;
     // P g of an entry, and P
     auto slope = [&](const Entry& x, float& P) -> float {
         float t, lt;
@@ -406,10 +412,10 @@ __global__ void __launch_bounds__(NT, kBlocks) distill_kernel(const __grid_const
             t = expf(lt);
         } else {
             lt = (x.lq - mT) * inv_T - lnW;
-            t = exp2f((x.lq - mT) * p.c) / sT;
+            t = exp2f((x.lq - mT) * p.c) * inv_sT;
         }
         const float d = x.z - M, lp = x.z == -INFINITY ? -INFINITY : d * inv_T - lnT;
-        P = x.z == -INFINITY ? 0.f : exp2f(d * p.c) / total;
+        P = x.z == -INFINITY ? 0.f : exp2f(d * p.c) * inv_total;
         return slope_of(a.kind, a.beta, t, lt, P, lp);
     };
     float P1 = 0.f, g1 = 0.f;                    // of the first entry
@@ -420,14 +426,17 @@ __global__ void __launch_bounds__(NT, kBlocks) distill_kernel(const __grid_const
         float held = 0.f;
         sT = 0.f;
         for (int k = 0; k < nw; ++k) {
-            const float4 x = s.sup[k];
-            if (x.x > -INFINITY) held += x.y * exp2f((x.x - M) * p.c);
-            else held += x.y;
-            if (x.z > -INFINITY) sT += x.w * exp2f((x.z - mT) * p.c);
+            held += s.sup[k].z;
+            sT += s.sup[k].w;
         }
+        if (mS > -INFINITY) held *= exp2f((mS - M) * p.c);
         total = rest + held;
+        inv_total = 1.f / total;
         lnT = logf(total);
-        lnW = logf(sT);
+        if (!a.tail) {
+            lnW = logf(sT);
+            inv_sT = 1.f / sT;
+        }
         float A = 0.f;
         each([&](const Entry& x, bool is_first, long long) {
             float P;
@@ -443,7 +452,7 @@ __global__ void __launch_bounds__(NT, kBlocks) distill_kernel(const __grid_const
         if (tid == 0) {
             s.M = M;
             s.rest = rest;
-            s.total = total;
+            s.inv_total = inv_total;
             if (a.tail) s.t0 = rest_of(wT).hi;
             if (rank == 0) {
                 sv.M[row] = M;
@@ -453,7 +462,7 @@ __global__ void __launch_bounds__(NT, kBlocks) distill_kernel(const __grid_const
     }
     __syncthreads();
     M = s.M;
-    total = s.total;
+    inv_total = s.inv_total;
     const float rest = s.rest;
     // the gradient's factor outside the support (over the softmax's denominator, times T), and A
     float k_rest = 0.f, A = 0.f;
@@ -461,11 +470,11 @@ __global__ void __launch_bounds__(NT, kBlocks) distill_kernel(const __grid_const
         for (int k = 0; k < nw; ++k) A += s.A[k];
         float g0 = 0.f;
         if (a.tail && !(rest <= 0.f)) {
-            const float t0 = s.t0, P0 = rest / total, x = slope_of(a.kind, a.beta, t0, logf(t0), P0, logf(P0));
+            const float t0 = s.t0, P0 = rest * inv_total, x = slope_of(a.kind, a.beta, t0, logf(t0), P0, logf(P0));
             A += x;
             g0 = x / P0;
         }
-        k_rest = (g0 - A) / total;
+        k_rest = (g0 - A) * inv_total;
     }
     if (!listed) {                               // (in place: its logits are read again until here)
         __syncthreads();

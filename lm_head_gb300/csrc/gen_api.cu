@@ -209,8 +209,9 @@ int rl_verify(const rl_verify_args* a, void* ws, size_t ws_bytes, int32_t* dev_s
     if (a->keep_lens && a->keep_lens != a->ctx_lens && overlap(a->keep_lens, a->R, a->ctx_lens, a->ctx_lens ? a->R : 0))
         return fail(RL_ERR_ARG, "keep_lens shares memory with ctx_lens");
     if (overlap(a->tokens, a->T, a->step_tokens, a->T)) return fail(RL_ERR_ARG, "tokens shares memory with step_tokens");
-    if (ws_bytes < verify_ws_bytes(a)) return fail(RL_ERR_WORKSPACE, "verification workspace too small");
-    if (a->T > 0 && (!ws || !aligned(ws, 16))) return fail(RL_ERR_ARG, "ws is NULL or not 16-byte aligned");
+    const size_t need = verify_ws_bytes(a);
+    if (ws_bytes < need) return fail(RL_ERR_WORKSPACE, "verification workspace too small");
+    if (need > 0 && (!ws || !aligned(ws, 16))) return fail(RL_ERR_ARG, "ws is NULL or not 16-byte aligned");
     rc = check_device();
     return rc != RL_OK ? rc : verify_impl(a, ws, dev_status, static_cast<cudaStream_t>(stream));
 }
@@ -277,6 +278,9 @@ int rl_page_compact(const rl_page_compact_args* a, void* ws, size_t ws_bytes, in
         return fail(RL_ERR_ARG, "required pointer is NULL");
     if (a->G > 0 && (!a->prefix_lens || (a->prefix_width > 0 && (!a->prefix_table || !a->prefix_table_out))))
         return fail(RL_ERR_ARG, "prefix_lens/prefix_table NULL with G > 0");
+    const auto apart = [](const int32_t* x, const int32_t* y, int64_t n) { return x == y || !overlap(x, n, y, n); };
+    if (!apart(a->block_table, a->block_table_out, a->R * a->table_width) || !apart(a->prefix_table, a->prefix_table_out, a->G * a->prefix_width))
+        return fail(RL_ERR_ARG, "a table's output shares memory with it and is not it");
     if (ws_bytes < page_compact_ws_bytes(a->n_pages)) return fail(RL_ERR_WORKSPACE, "compact workspace too small");
     if (a->n_pages > 0 && (!ws || !aligned(ws, 16))) return fail(RL_ERR_ARG, "ws is NULL or not 16-byte aligned");
     int rc = check_device();

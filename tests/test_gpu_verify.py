@@ -369,6 +369,20 @@ def test_no_requests_and_no_rows():
     assert (o.tokens == -1).all() and o.status_bits() == 0
 
 
+def test_more_rows_than_are_looked_up():
+    """A step of more rows than a block keeps a list of."""
+    rng = np.random.default_rng(2)
+    R, n, V, kept = 9000, 4, 24, 40
+    z = torch.randn(kept, V, generator=torch.Generator().manual_seed(2)) * 2
+    zd = z + 0.3 * torch.randn(kept, V, generator=torch.Generator().manual_seed(3))
+    rows = rng.integers(0, kept, R * n)
+    c = dict(step=rng.integers(0, V, R * n), cu=np.arange(0, R * n + 1, n), u=(rng.integers(0, 1 << 24, R * n) / 2.0 ** 24).astype(np.float32),
+             un=(rng.integers(0, 1 << 24, R) / 2.0 ** 24).astype(np.float32), V=V, ctx=np.zeros(R, int), target=Half(V, z, rows=rows),
+             draft=Half(V, zd, rows=rows))
+    ref, _ = check(c, skips=2)
+    assert ref["accepted"].sum() > R / 2
+
+
 def test_tokens_are_the_targets_samples():
     """Over many requests with one draft each the new tokens at the first place follow p: six deviations of each count."""
     V, R = 12, 200000

@@ -61,7 +61,8 @@ def test_compact_refusals(lib):  # noqa: F811
     names = ("kv_lens", "block_table", "block_table_out", "prefix_lens", "prefix_table", "prefix_table_out", "src", "dst",
              "free_pages", "free_used_out")
     _refused(lib, "rl_page_compact", make, [({s: -1}, ARG) for s in sizes] + [({s: BIG}, UNS) for s in sizes] +
-             [({n: None}, ARG) for n in names] + [(dict(page_size=17), UNS)], tail=WS)
+             [({n: None}, ARG) for n in names] + [(dict(page_size=17), UNS), (dict(block_table_out=FAKE + 4), ARG), (dict(prefix_table_out=FAKE + 4), ARG)],
+             tail=WS)
     a = make(n_pages=1 << 20)
     assert lib.rl_page_compact(ctypes.byref(a), FAKE, 1 << 17, FAKE, None) == rh.RL_ERR_WORKSPACE
     assert lib.rl_page_compact(ctypes.byref(a), None, 1 << 30, FAKE, None) == ARG
