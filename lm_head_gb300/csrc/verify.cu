@@ -277,6 +277,8 @@ struct VerShared {
     float2 tab[2048];
     unsigned long long red[NT / 32];
     unsigned long long xch[2];
+    ulonglong2 pair;                // (written once)
+    unsigned long long red2[NT / 32];
     VerDraw draw;
     VerRow rows[NT / 32];           // the rows of a stretch of the request, target and draft in turn
     float lp[NT / 32];              // log2 of the candidate's probability
@@ -301,11 +303,13 @@ RL_DEVINL unsigned long long fixed_of(float hi, float lo, int k) {
 }
 // 2^(x c - ref - lam_lo) as a normalised pair, below 2; magic = 6144 - ref with ref in steps of 2^-11 (see weight_pair; with
 // lam_lo |r| may be 2^-11, so 2^r - 1 goes to the third power).
+template <bool kLow = true>
 RL_DEVINL FF weight_off(float x, float xl, FF c, float magic, float lam_lo, const float2* tab) {
     const float t = fmaf(x, c.hi, magic);
     float r = fmaf(x, c.hi, -__fsub_rn(t, magic));
     r = fmaf(x, c.lo, r);
-    r = fmaf(xl, c.hi, r) - lam_lo;
+    if (kLow) r = fmaf(xl, c.hi, r);             // (x is not a pair where weights need no difference)
+    r -= lam_lo;
     const uint32_t tb = __float_as_uint(t);
     const float2 q = tab[tb & 2047u];
     const float hi = __uint_as_float(__float_as_uint(q.x) + (tb << 12));
@@ -321,13 +325,12 @@ RL_DEVINL float logit_of(const VerRow& w, float ref, float e) {
     const float x = (ref + w.R + e) * w.inv_c;
     return w.plain ? x : w.M + x;
 }
-// max(v - q, 0) of normalised pairs
+// max(v - q, 0) of normalised pairs, as a pair that is not in order
 RL_DEVINL FF left_of(FF v, FF q) {
-    if (!(v.hi >= q.hi)) return {0.f, 0.f};
-    const float d = __fsub_rn(v.hi, q.hi);
-    const FF r = two_sum(d, __fadd_rn(__fsub_rn(__fsub_rn(v.hi, d), q.hi), __fsub_rn(v.lo, q.lo)));
-    return r.hi > 0.f ? r : FF{0.f, 0.f};
+    const float d = __fsub_rn(v.hi, q.hi), e = __fadd_rn(__fsub_rn(__fsub_rn(v.hi, d), q.hi), __fsub_rn(v.lo, q.lo));
+    return v.hi >= q.hi && __fadd_rn(d, e) > 0.f ? FF{d, e} : FF{0.f, 0.f};
 }
+RL_DEVINL FF ordered(FF x) { return two_sum(x.hi, x.lo); }
 
 // A lane's logits of N parts from element i0 on, four of each, past the row's end -inf.
 template <int N>
@@ -468,17 +471,16 @@ __device__ __noinline__ unsigned long long sum_steps(const rl_dist& d, const Ver
     mine = lane < kVerStep ? mine : 0ull;
     return warp_sum(mine);
 }
-// Up to 15 weights of at most 1 in a lane (as LaneSum, from 16 on, where the last place is 2^-19 too).
+// Up to 15 weights of at most 1 in a lane, pairs in order (as LaneSum, from 16 on, where the last place is 2^-19 too).
 struct LongSum {
     float top = 16.f, low = 0.f;
     RL_DEVINL void add(FF x) {
-        const float n = __fadd_rn(top, __fadd_rn(x.hi, x.lo));
+        const float n = __fadd_rn(top, x.hi);
         low += __fadd_rn(__fsub_rn(x.hi, __fsub_rn(n, top)), x.lo);
         top = n;
     }
-    RL_DEVINL unsigned long long warp_total() const {
-        return LaneSum::total(__reduce_add_sync(0xffffffffu, __float_as_uint(top) - 0x41800000u), __reduce_add_sync(0xffffffffu, __float2int_rn(low * 0x1p43f)));
-    }
+    RL_DEVINL uint32_t warp_top() const { return __reduce_add_sync(0xffffffffu, __float_as_uint(top) - 0x41800000u); }
+    RL_DEVINL int warp_low() const { return __reduce_add_sync(0xffffffffu, __float2int_rn(low * 0x1p43f)); }
 };
 // A target's and a draft's rows of logits in one pass: the totals of both, and of each part what is left, max(p - q, 0), with the ratio
 // of the totals taken from the fp32 sums (2^lam) - and the draft's weight where something is left, in ds, by which the parts are put
@@ -486,11 +488,12 @@ struct LongSum {
 // second order (d(lam)^2, below 2^-36).  Three passes (both totals, then what is left) took half as long again.
 // The draft's total comes out as 2^-(hi + lo) times itself.
 template <bool kPlain>
-RL_DEVINL void sum_both_of(const rl_dist& dp, const VerRow& w, const rl_dist& dq, const VerRow& o, Lam lam, int V, int from, int steps, int first,
-                           int stride, unsigned long long* cs, float* ds, const float2* tab, unsigned long long& tp, unsigned long long& tq) {
+RL_DEVINL ulonglong2 sum_both_of(const rl_dist& dp, const VerRow& w, const rl_dist& dq, const VerRow& o, Lam lam, int V, int from, int steps, int first,
+                                 int stride, unsigned long long* cs, float* ds, const float2* tab) {
     constexpr int N = kVerStep / 2;              // half a step at a time, for the registers
     const int lane = threadIdx.x & 31;
     const bool wp = kPlain || w.plain, op = kPlain || o.plain;
+    unsigned long long mine = 0;
 #pragma unroll 1
     for (int k = first; k < 2 * steps; k += stride) {
         const int i0 = (2 * from + k) * N * kVerPart;
@@ -520,14 +523,14 @@ RL_DEVINL void sum_both_of(const rl_dist& dp, const VerRow& w, const rl_dist& dq
                     // (a clamped logit's weight is not used, but has to be one)
                     const float a = z[s][j] < zlow ? (wp ? w.R * w.inv_c : w.M) : z[s][j], b = y[s][j] < ylow ? (op ? o.R * o.inv_c : o.M) : y[s][j];
                     const FF da = wp ? FF{a, 0.f} : two_sum(a, -w.M), db = op ? FF{b, 0.f} : two_sum(b, -o.M);
-                    FF v = weight_off(da.hi, da.lo, w.c, magic_z, 0.f, tab), q = weight_off(db.hi, db.lo, o.c, magic_y, lam.lo, tab);
+                    FF v = weight_off<!kPlain>(da.hi, da.lo, w.c, magic_z, 0.f, tab), q = weight_off<!kPlain>(db.hi, db.lo, o.c, magic_y, lam.lo, tab);
                     if (z[s][j] < zlow) v = {0.f, 0.f};
                     if (y[s][j] < ylow) q = {0.f, 0.f};
                     sp.add(v);
                     sq.add(q);
                     q = {q.hi * scale, q.lo * scale};
                     v = left_of(v, q);
-                    if (v.hi > 0.f) d += q.hi;
+                    if (v.hi != 0.f || v.lo != 0.f) d += q.hi;
                     acc.add(v.hi, v.lo);
                 }
                 const uint32_t t = acc.warp_top();
@@ -538,24 +541,29 @@ RL_DEVINL void sum_both_of(const rl_dist& dp, const VerRow& w, const rl_dist& dq
                     d_in = e;
                 }
             }
-            sum = in_units(LaneSum::total(top, low), static_cast<int>(rz), w.prec);
             d_out = static_cast<float>(d_in) * power_of_2(static_cast<int>(rz) - 20);
-            const unsigned long long a = in_units(sp.warp_total(), static_cast<int>(rz), w.prec), b = in_units(sq.warp_total(), static_cast<int>(ry), o.prec);
-            tp += a;
-            tq += b;
+            // lanes 0 .. N - 1 the parts, N the target's total, N + 1 the draft's
+            const uint32_t tz = sp.warp_top(), ty = sq.warp_top();
+            const int lz = sp.warp_low(), ly = sq.warp_low();
+            if (lane >= N) {
+                top = lane == N ? tz : ty;
+                low = lane == N ? lz : ly;
+            }
+            sum = in_units(LaneSum::total(top, low), static_cast<int>(lane <= N ? rz : ry), lane <= N ? w.prec : o.prec);
         }
         if (lane < N) {
             cs[k * N + lane] = sum;
             ds[k * N + lane] = d_out;
+        } else {
+            mine += sum;
         }
     }
+    return make_ulonglong2(__shfl_sync(0xffffffffu, mine, N), __shfl_sync(0xffffffffu, mine, N + 1));
 }
 __device__ __noinline__ ulonglong2 sum_both(const rl_dist& dp, const VerRow* rp, const rl_dist& dq, const VerRow* rq, Lam lam, int V, int from, int steps,
                                             int first, int stride, unsigned long long* cs, float* ds, const float2* tab) {
-    unsigned long long tp = 0, tq = 0;
-    if (rp->plain && rq->plain) sum_both_of<true>(dp, *rp, dq, *rq, lam, V, from, steps, first, stride, cs, ds, tab, tp, tq);
-    else sum_both_of<false>(dp, *rp, dq, *rq, lam, V, from, steps, first, stride, cs, ds, tab, tp, tq);
-    return make_ulonglong2(tp, tq);
+    if (rp->plain && rq->plain) return sum_both_of<true>(dp, *rp, dq, *rq, lam, V, from, steps, first, stride, cs, ds, tab);
+    return sum_both_of<false>(dp, *rp, dq, *rq, lam, V, from, steps, first, stride, cs, ds, tab);
 }
 
 template <int NT>
@@ -742,7 +750,7 @@ struct Request {
             if (!(l <= 1e-6f)) bits |= RL_STATUS_LOGQ;
             if (!(l < INFINITY) || !(l > -INFINITY)) return 0ull;
             FF v = exp_ff(l);
-            if (!whole) v = left_of(v, prob_pair(q, j, lq, bits));
+            if (!whole) v = ordered(left_of(v, prob_pair(q, j, lq, bits)));
             return fixed_of(v.hi, v.lo, 52);
         };
         // a stretch of the row a thread
@@ -934,6 +942,22 @@ struct Draw : Request<kDrawThreads> {
         }
         return total;
     }
+    // The cluster's sums of two numbers.
+    RL_DEVINL ulonglong2 cluster_sum2(ulonglong2 v) {
+        if (g.cs == 1) return v;
+        if (tid == 0) s.pair = v;
+        __syncthreads();
+        cluster_arrive();
+        cluster_wait();
+        ulonglong2 total = make_ulonglong2(0, 0);
+        for (int k = 0; k < g.cs; ++k) {
+            unsigned long long x, y;
+            asm volatile("ld.shared::cluster.v2.u64 {%0, %1}, [%2];" : "=l"(x), "=l"(y) : "r"(cluster_addr(&s.pair, k)) : "memory");
+            total.x += x;
+            total.y += y;
+        }
+        return total;
+    }
     RL_DEVINL unsigned long long slice_sum(int side) {
         __syncthreads();
         const unsigned long long x = sum_steps(g.side[side].d, &s.draw.row[side], V, from, steps, warp, kWarps, cs, s.tab);
@@ -958,7 +982,7 @@ struct Draw : Request<kDrawThreads> {
         if (!whole && q.mode == kDistDense) {
             const float lam_hi = rintf(s.lam.hi * 2048.f) * (1.f / 2048.f), lam_lo = (s.lam.hi - lam_hi) + s.lam.lo;
             const float ylow = fmaxf(logit_of(q, lam_hi, -64.f), -FLT_MAX), yhigh = logit_of(q, lam_hi, 0.75f);
-            if (y >= ylow) v = left_of(v, weight_of(fminf(y, yhigh), q, lam_hi, lam_lo, s.tab));
+            if (y >= ylow) v = ordered(left_of(v, weight_of(fminf(y, yhigh), q, lam_hi, lam_lo, s.tab)));
             return fixed_of(v.hi, v.lo, p.prec);
         }
         const unsigned long long w = fixed_of(v.hi, v.lo, p.prec);
@@ -978,31 +1002,49 @@ struct Draw : Request<kDrawThreads> {
         VerRow& p = s.draw.row[0];
         VerRow& q = s.draw.row[1];
         // log2 of a total in the row's unit, by the fp32 sums: S e^(M / T) over 2^R
-        auto rough = [](const VerRow& w) -> double {
-            const double c = static_cast<double>(w.c.hi) + static_cast<double>(w.c.lo);
-            return static_cast<double>(log2f(w.S)) + (w.plain ? w.M * c - w.R : 0.0);
+        auto rough = [](const VerRow& w) -> FF {
+            const FF l = {log2f(w.S), 0.f};
+            if (!w.plain) return l;
+            const FF m = ff_add(ff_mul({w.M, 0.f}, w.c), {-w.R, 0.f});
+            return ff_add(l, m);
         };
         if (tid == 0) {
-            const double lam = rough(q) - rough(p);
-            s.lam0.whole = static_cast<int>(floor(lam));
-            const double f = lam - s.lam0.whole;
-            s.lam0.hi = static_cast<float>(floor(f * 2048.0)) * (1.f / 2048.f);
-            s.lam0.lo = static_cast<float>(f - static_cast<double>(s.lam0.hi));
+            const FF lam = ff_add(rough(q), ff_neg(rough(p)));
+            const float whole = floorf(lam.hi);
+            const FF f = ff_add(lam, {-whole, 0.f});
+            s.lam0.whole = static_cast<int>(whole);
+            s.lam0.hi = floorf(f.hi * 2048.f) * (1.f / 2048.f);
+            s.lam0.lo = __fadd_rn(__fsub_rn(f.hi, s.lam0.hi), f.lo);
         }
         __syncthreads();
         const Lam lam0 = s.lam0;
-        const ulonglong2 x = sum_both(g.side[0].d, &p, g.side[1].d, &q, lam0, V, from, steps, warp, kWarps, cs, ds, s.tab);
-        unsigned long long before;
-        const unsigned long long tp = cluster_sum(block_sum(lane == 0 ? x.x : 0ull), before), tq = cluster_sum(block_sum(lane == 0 ? x.y : 0ull), before);
+        ulonglong2 x = sum_both(g.side[0].d, &p, g.side[1].d, &q, lam0, V, from, steps, warp, kWarps, cs, ds, s.tab);
         __syncthreads();
-        if (tid == 0) {
-            const double f = static_cast<double>(lam0.hi) + static_cast<double>(lam0.lo);
-            const double lam = (log2(static_cast<double>(tq)) - q.prec + f) - (log2(static_cast<double>(tp)) - p.prec);
-            s.lam.hi = static_cast<float>(lam);
-            s.lam.lo = static_cast<float>(lam - static_cast<double>(s.lam.hi));
-            s.turn = static_cast<float>((lam - lam0.whole - f) * 0.69314718055994530942);
-            p.total = tp;
-            q.total = tq;                        // (times 2^-f: only lam is read of it)
+        if (lane == 0) {
+            s.red[warp] = x.x;
+            s.red2[warp] = x.y;
+        }
+        __syncthreads();
+        x = make_ulonglong2(0, 0);
+#pragma unroll
+        for (int k = 0; k < kWarps; ++k) {
+            x.x += s.red[k];
+            x.y += s.red2[k];
+        }
+        x = cluster_sum2(x);
+        if (warp == 0) {
+            // the logs of both, a lane each, in the rows' units; log2 of the draft's total over the target's as a pair
+            const FF l = ln_of(lane == 0 ? x.x : x.y, lane == 0 ? p.prec : q.prec);
+            const FF lq = {__shfl_sync(0xffffffffu, l.hi, 1), __shfl_sync(0xffffffffu, l.lo, 1)};
+            if (lane == 0) {
+                FF d = ff_add(ff_mul(ff_add(lq, ff_neg(l)), {kLog2eHi, kLog2eLo}), {lam0.hi, lam0.lo});      // log2 and the part that the sum left out
+                s.lam = d;
+                d = ff_add(d, {-static_cast<float>(lam0.whole), 0.f});
+                d = ff_add(d, {-lam0.hi, -lam0.lo});
+                s.turn = (d.hi + d.lo) * kLn2;
+                p.total = x.x;
+                q.total = x.y;                   // (less that part: only the ratio is read of it)
+            }
         }
         __syncthreads();
         const float turn = s.turn * power_of_2(p.prec);
