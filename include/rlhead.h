@@ -681,7 +681,8 @@ typedef struct rl_dist {
  * the row then has no token), log-probabilities that are NaN or above 1e-6 (RL_STATUS_LOGQ, left out if NaN or +inf), ids not ascending in the row that y is
  * drawn from (RL_STATUS_ROW_ORDER, y is then not defined), temperatures and random numbers as in rl_sample (RL_STATUS_KNOB), NaN and +inf logits
  * (RL_STATUS_NONFINITE, they count as -inf).  A target row without a token accepts nothing and sets RL_STATUS_EMPTY_ROW, y = -1 and
- * logq -inf if it is the last row looked at; a draft row without one sets it too. */
+ * logq -inf if it is the last row looked at; a draft row without one sets it too.
+ * Outputs share no memory with inputs, but for keep_lens. */
 typedef struct rl_verify_args {
     int64_t R, T, V;                /* R < 2^28, V <= 2^20 */
     const int32_t* cu_q;            /* device [R+1] */
@@ -744,7 +745,7 @@ int rl_page_release(const rl_page_release_args* args, void* ws, size_t ws_bytes,
  * in the call is left out and sets RL_STATUS_ID_RANGE; so is one with lens < 0 or above
  * the parent's kv_lens (RL_STATUS_LENGTHS) or a row too short for it (RL_STATUS_PAGES).  Where the pool runs out
  * (RL_STATUS_PAGES) or a page id lies outside [0, n_pages) (RL_STATUS_PAGE_ID) the entry is -1 and nothing is
- * copied. */
+ * copied.  parents, children and lens share no memory with kv_lens, src, dst and tokens. */
 typedef struct rl_page_fork_args {
     int64_t R, C;                   /* rows of the table, entries of the call; < 2^31 */
     const int32_t* parents;         /* device [C] */

@@ -208,10 +208,16 @@ int rl_verify(const rl_verify_args* a, void* ws, size_t ws_bytes, int32_t* dev_s
         return fail(RL_ERR_ARG, "required pointer is NULL");
     if (a->keep_lens && a->keep_lens != a->ctx_lens && overlap(a->keep_lens, a->R, a->ctx_lens, a->ctx_lens ? a->R : 0))
         return fail(RL_ERR_ARG, "keep_lens shares memory with ctx_lens");
-    if (overlap(a->tokens, a->T, a->step_tokens, a->T)) return fail(RL_ERR_ARG, "tokens shares memory with step_tokens");
     const size_t need = verify_ws_bytes(a);
     if (ws_bytes < need) return fail(RL_ERR_WORKSPACE, "verification workspace too small");
     if (need > 0 && (!ws || !aligned(ws, 16))) return fail(RL_ERR_ARG, "ws is NULL or not 16-byte aligned");
+    // (outputs are written before the last request has read its inputs)
+    const struct { const void* p; int64_t n; } in[] = {{a->cu_q, a->R + 1}, {a->step_tokens, a->T}, {a->u, a->T}, {a->u_next, a->R}},
+                                               out[] = {{a->tokens, a->T}, {a->logq, a->logq ? a->T : 0}, {a->accepted, a->R}, {a->keep_lens, a->keep_lens ? a->R : 0}};
+    for (const auto& x : in)
+        for (const auto& y : out)
+            if (overlap(x.p, x.n, y.p, y.n)) return fail(RL_ERR_ARG, "an output shares memory with an input");
+    if (overlap(a->accepted, a->R, a->ctx_lens, a->ctx_lens ? a->R : 0)) return fail(RL_ERR_ARG, "accepted shares memory with ctx_lens");
     rc = check_device();
     return rc != RL_OK ? rc : verify_impl(a, ws, dev_status, static_cast<cudaStream_t>(stream));
 }
@@ -254,11 +260,14 @@ int rl_page_fork(const rl_page_fork_args* a, void* ws, size_t ws_bytes, int32_t*
         (a->C > 0 && a->R > 0 && (!a->kv_lens || (a->table_width > 0 && !a->block_table))) || (a->n_free > 0 && !a->free_pages))
         return fail(RL_ERR_ARG, "required pointer is NULL");
     if (a->free_used == a->free_used_out) return fail(RL_ERR_ARG, "free_used_out must not be free_used");
-    if (overlap(a->lens, a->C, a->kv_lens, a->R) || overlap(a->parents, a->C, a->tokens, a->C) || overlap(a->children, a->C, a->tokens, a->C) ||
-        overlap(a->lens, a->C, a->tokens, a->C))
-        return fail(RL_ERR_ARG, "lens shares memory with kv_lens, or an input with tokens");
     if (ws_bytes < page_fork_ws_bytes(a->R, a->C)) return fail(RL_ERR_WORKSPACE, "fork workspace too small");
     if (a->C > 0 && (!ws || !aligned(ws, 16))) return fail(RL_ERR_ARG, "ws is NULL or not 16-byte aligned");
+    // (the rows are written after the lists)
+    for (const int32_t* in : {a->parents, a->children, a->lens}) {
+        if (overlap(in, a->C, a->kv_lens, a->R)) return fail(RL_ERR_ARG, "an input shares memory with kv_lens");
+        for (const int32_t* out : {a->src, a->dst, a->tokens})
+            if (overlap(in, a->C, out, a->C)) return fail(RL_ERR_ARG, "an input shares memory with an output");
+    }
     int rc = check_device();
     return rc != RL_OK ? rc : page_fork_impl(a, ws, dev_status, static_cast<cudaStream_t>(stream));
 }

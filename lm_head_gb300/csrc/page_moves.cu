@@ -97,7 +97,7 @@ RL_DEVINL void each_words(const uint32_t* map, long long n, F f) {
 }
 RL_DEVINL int bits_of(uint4 v) { return __popc(v.x) + __popc(v.y) + __popc(v.z) + __popc(v.w); }
 
-// Block sums of two numbers; every thread gets the totals.
+// The block's sum of v, in every thread.
 RL_DEVINL long long block_total(long long v, long long* red) {
     v = warp_sum(v);
     __syncthreads();

@@ -262,7 +262,6 @@ struct VerRow {
 struct VerDraw {
     long long t;                    // -1: nothing is left to draw
     float u;
-    int refused;
     VerRow row[2];
 };
 
@@ -893,7 +892,6 @@ __global__ void __launch_bounds__(kDecideThreads, 2) decide_kernel(const __grid_
         if (tid == 0) {
             s.draw.t = t;
             s.draw.u = u;
-            s.draw.refused = refused;
             s.draw.row[0] = s.rows[2 * at];
             s.draw.row[1] = s.rows[2 * at + 1];
             if (!refused) s.draw.row[1].mode = kDistNone;

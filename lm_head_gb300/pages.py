@@ -12,7 +12,7 @@ from typing import Optional
 
 import torch
 
-from .generation import _DTYPES, _F, _I32, _I64, _P, _check, _dev, _err, _load, _on, _packer, _status, _stream  # noqa: F401
+from .generation import _DTYPES, _I32, _I64, _P, _check, _dev, _err, _load, _on, _packer, _status, _stream
 
 
 class RlPageReleaseArgs(ctypes.Structure):

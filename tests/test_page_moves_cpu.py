@@ -54,6 +54,20 @@ def test_fork_refusals(lib):  # noqa: F811
     assert lib.rl_page_fork(ctypes.byref(a), None, 1 << 30, FAKE, None) == ARG
 
 
+def test_fork_lists_that_share_memory(lib):  # noqa: F811
+    apart = {n: FAKE + (k << 12) for k, n in enumerate(("kv_lens", "lens", "parents", "children", "src", "dst", "tokens"), 1)}
+
+    def call(**kw):
+        a = _fill(pg.RlPageForkArgs, **{**apart, **dict(R=4, C=2, table_width=2, n_free=8, n_pages=8, page_size=16,
+                                                        free_used_out=FAKE + 64), **kw})
+        return lib.rl_page_fork(ctypes.byref(a), *WS, FAKE, None)
+    if not torch.cuda.is_available():
+        assert call() not in (rh.RL_OK, ARG)                 # (no device)
+    for x in ("parents", "children", "lens"):
+        for y in ("kv_lens", "src", "dst", "tokens"):
+            assert call(**{y: apart[x] + 4}) == ARG, (x, y)
+
+
 def test_compact_refusals(lib):  # noqa: F811
     def make(**kw):
         return _fill(pg.RlPageCompactArgs, **{**dict(R=4, G=2, table_width=2, prefix_width=2, n_pages=8, page_size=16), **kw})

@@ -39,6 +39,21 @@ def test_refusals(lib):  # noqa: F811
     assert ctypes.sizeof(vf.RlVerifyArgs) == (7 + 20 + 1 + 5) * 8
 
 
+def test_outputs_that_share_memory_with_inputs(lib):  # noqa: F811
+    apart = {n: FAKE + (k << 16) for k, n in enumerate(("cu_q", "step_tokens", "u", "u_next", "ctx_lens", "tokens", "logq", "accepted",
+                                                        "keep_lens"))}
+
+    def call(**kw):
+        a = make(**{**apart, **kw})
+        return lib.rl_verify(ctypes.byref(a), FAKE, 1 << 40, FAKE, None)
+    if not torch.cuda.is_available():
+        assert call() not in (rh.RL_OK, ARG) and call(keep_lens=apart["ctx_lens"]) != ARG      # (no device)
+    for x in ("cu_q", "step_tokens", "u", "u_next"):
+        for y in ("tokens", "logq", "accepted", "keep_lens"):
+            assert call(**{y: apart[x] + 4}) == ARG, (x, y)
+    assert call(accepted=apart["ctx_lens"]) == ARG
+
+
 def test_binding_refuses_host_tensors_and_missing_rows():
     i, f = torch.zeros(3, dtype=torch.int32), torch.zeros(3)
     with pytest.raises(rh.RLHeadError):
