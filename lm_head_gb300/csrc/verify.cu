@@ -8,11 +8,12 @@
 //                      weights in fp32.  Rows that no request looks at (a draft's row behind its last draft) are left out.
 //  2. decide_kernel    a block a request: puts the rows' totals together and compares; a comparison nearer than the bound
 //                      of the fp32 sums' error is taken again with sums that are good to 2^-36.  Draws from support rows.
-//  3. draw_kernel      a cluster of blocks a request whose new token comes from a row of logits, a slice of the vocabulary a
-//                      block: the sums of its parts of 128 as integers (float-pair weights, see weights.cuh) of the target's
-//                      weights, of the draft's where it has logits, and of what is left, max(p - q, 0); the cluster adds them
-//                      up, and the block in whose slice the random number falls scans it.  With a draft's support row only
-//                      its few tokens' probabilities are taken off the target's parts.
+//  3. sum_kernel       the rows of logits that a request's new token comes from, a step of 512 tokens a warp at a time, every warp of
+//                      the GPU the same number of them whatever the number of requests: of each part of 128 the sums, as integers
+//                      (float-pair weights, see weights.cuh), of the target's weights, or of what is left, max(p - q, 0), where the
+//                      draft has logits too.
+//  4. pick_kernel      a block a request: adds the parts up, takes a draft's support row off the target's parts, and scans
+//                      the part in which the random number falls.
 #include <cfloat>
 #include <climits>
 #include <cmath>
@@ -28,8 +29,9 @@ namespace rl {
 constexpr int kVerPart = 128;                  // logits of a part
 constexpr int kVerStep = 4;                    // parts that a warp sums up at a time
 constexpr int kDecideThreads = 512;            // a row of either side a warp
-constexpr int kDrawThreads = 512;
-constexpr int kDrawBlocks = 2;                 // of them on a multiprocessor
+constexpr int kSumThreads = 512;
+constexpr int kSumBlocks = 2;                  // of them on a multiprocessor
+constexpr int kPickThreads = 512;
 constexpr int kChunkThreads = 256;
 constexpr int kChunkPacks = 8;                 // 16-byte loads of a lane: 4 KB a warp
 constexpr int kUsedRows = 32768;               // rows of a step whose use is looked up in shared memory
@@ -47,8 +49,10 @@ struct VerArgs {
     int32_t* status;
     bool sure;          // no draft distribution
     int group;          // chunks that a warp takes one after another
-    int cs, per;        // blocks of a request's draw; steps of a block's slice
+    int steps;          // of a row
     struct VerDraw* draws;      // [R] (NULL: no logits on either side)
+    struct VerStep* sums;       // [R, steps]
+    int32_t *todo, *n_todo;     // [R] the requests with sums to take, in any order; their number
 };
 
 // The row of the distribution that the step's row t has; -1 where there is none.
@@ -193,6 +197,7 @@ __global__ void __launch_bounds__(kChunkThreads, 3) chunk_kernel(const __grid_co
         a.tokens[t] = -1;
         if (a.logq) a.logq[t] = 0.f;
     }
+    if (g.draws && blockIdx.x == 0 && threadIdx.x == 0) *g.n_todo = 0;
     // the rows that requests look at
     const bool known = a.T <= kUsedRows;
     if (known) {
@@ -258,25 +263,29 @@ struct VerRow {
     int plain, vec;
     unsigned long long total;       // the sum of all weights, once it is counted
 };
-// What a request's new token is drawn from.
-struct VerDraw {
-    long long t;                    // -1: nothing is left to draw
-    float u;
-    VerRow row[2];
-};
-
 // 2^lam as it enters the draft's weights: an integer power, a part in steps of 2^-11 in [0, 1) and the rest.
 struct Lam {
     int whole;
     float hi, lo;
+};
+// What a request's new token is drawn from.
+struct VerDraw {
+    long long t;                    // -1: nothing is left to draw
+    float u;
+    Lam lam;                        // of two rows of logits: log2 of the draft's total over the target's, as their fp32 sums have it
+    VerRow row[2];
+};
+// The sums of a step, in the rows' units.
+struct alignas(16) VerStep {
+    unsigned long long part[kVerStep];      // of each part, what the token is drawn from
+    float drop[kVerStep];                   // of two rows of logits: the draft's weight where something is left,
+    unsigned long long p, q;                // and both totals
 };
 
 template <int NT>
 struct VerShared {
     float2 tab[2048];
     unsigned long long red[NT / 32];
-    unsigned long long xch[2];
-    ulonglong2 pair;                // (written once)
     unsigned long long red2[NT / 32];
     VerDraw draw;
     VerRow rows[NT / 32];           // the rows of a stretch of the request, target and draft in turn
@@ -285,8 +294,7 @@ struct VerShared {
     int flag, token;
     float lpx;
     FF lam;                         // log2 of the draft's total over the target's, as they are counted
-    Lam lam0;                       // as their fp32 sums have it
-    float turn;                     // ln 2 times the difference
+    float turn;                     // ln 2 times the difference to the fp32 sums'
     unsigned long long unit;
 };
 
@@ -413,9 +421,9 @@ RL_DEVINL unsigned long long in_units(unsigned long long w50, int ref, int prec)
     return sh >= 0 ? w50 << sh : sh > -64 ? (w50 + (1ull << (-sh - 1))) >> -sh : 0ull;
 }
 // Sums of the weights of `steps` steps of a row from step `from` on, by a warp that takes every `stride`-th; the parts' sums
-// into cs where it is given.  Each step is summed relative to its own largest weight.  Lane 0 has the sum.
+// into `out` where it is given.  Each step is summed relative to its own largest weight.  Lane 0 has the sum.
 __device__ __noinline__ unsigned long long sum_steps(const rl_dist& d, const VerRow* row, int V, int from, int steps, int first, int stride,
-                                                     unsigned long long* cs, const float2* tab) {
+                                                     VerStep* out, const float2* tab) {
     const VerRow w = *row;
     const int lane = threadIdx.x & 31;
     unsigned long long mine = 0;
@@ -463,7 +471,7 @@ __device__ __noinline__ unsigned long long sum_steps(const rl_dist& d, const Ver
             sum = in_units(LaneSum::total(top, low), static_cast<int>(ref), w.prec);
         }
         if (lane < kVerStep) {
-            if (cs) cs[k * kVerStep + lane] = sum;
+            if (out) out[k].part[lane] = sum;
             mine += sum;
         }
     }
@@ -482,19 +490,19 @@ struct LongSum {
     RL_DEVINL int warp_low() const { return __reduce_add_sync(0xffffffffu, __float2int_rn(low * 0x1p43f)); }
 };
 // A target's and a draft's rows of logits in one pass: the totals of both, and of each part what is left, max(p - q, 0), with the ratio
-// of the totals taken from the fp32 sums (2^lam) - and the draft's weight where something is left, in ds, by which the parts are put
+// of the totals taken from the fp32 sums (2^lam) - and the draft's weight where something is left, by which the parts are put
 // right once the ratio is known: what is left changes by q d(lam) ln 2 there, and the tokens at which p and q change places matter in
 // second order (d(lam)^2, below 2^-36).  Three passes (both totals, then what is left) took half as long again.
 // The draft's total comes out as 2^-(hi + lo) times itself.
 template <bool kPlain>
-RL_DEVINL ulonglong2 sum_both_of(const rl_dist& dp, const VerRow& w, const rl_dist& dq, const VerRow& o, Lam lam, int V, int from, int steps, int first,
-                                 int stride, unsigned long long* cs, float* ds, const float2* tab) {
+RL_DEVINL void sum_both_of(const rl_dist& dp, const VerRow& w, const rl_dist& dq, const VerRow& o, Lam lam, int V, int from, int steps, VerStep* out,
+                           const float2* tab) {
     constexpr int N = kVerStep / 2;              // half a step at a time, for the registers
     const int lane = threadIdx.x & 31;
     const bool wp = kPlain || w.plain, op = kPlain || o.plain;
     unsigned long long mine = 0;
 #pragma unroll 1
-    for (int k = first; k < 2 * steps; k += stride) {
+    for (int k = 0; k < 2 * steps; ++k) {
         const int i0 = (2 * from + k) * N * kVerPart;
         unsigned long long sum = 0;
         float d_out = 0.f;
@@ -550,19 +558,24 @@ RL_DEVINL ulonglong2 sum_both_of(const rl_dist& dp, const VerRow& w, const rl_di
             }
             sum = in_units(LaneSum::total(top, low), static_cast<int>(lane <= N ? rz : ry), lane <= N ? w.prec : o.prec);
         }
+        VerStep& to = out[k >> 1];
         if (lane < N) {
-            cs[k * N + lane] = sum;
-            ds[k * N + lane] = d_out;
+            to.part[(k & 1) * N + lane] = sum;
+            to.drop[(k & 1) * N + lane] = d_out;
         } else {
             mine += sum;
+            if (k & 1) {
+                if (lane < N + 2) (lane == N ? to.p : to.q) = mine;
+                mine = 0;
+            }
         }
     }
-    return make_ulonglong2(__shfl_sync(0xffffffffu, mine, N), __shfl_sync(0xffffffffu, mine, N + 1));
 }
-__device__ __noinline__ ulonglong2 sum_both(const rl_dist& dp, const VerRow* rp, const rl_dist& dq, const VerRow* rq, Lam lam, int V, int from, int steps,
-                                            int first, int stride, unsigned long long* cs, float* ds, const float2* tab) {
-    if (rp->plain && rq->plain) return sum_both_of<true>(dp, *rp, dq, *rq, lam, V, from, steps, first, stride, cs, ds, tab);
-    return sum_both_of<false>(dp, *rp, dq, *rq, lam, V, from, steps, first, stride, cs, ds, tab);
+__device__ __noinline__ void sum_both(const rl_dist& dp, const VerRow* rp, const rl_dist& dq, const VerRow* rq, Lam lam, int V, int from, int steps,
+                                      VerStep* out, const float2* tab) {
+    const VerRow w = *rp, o = *rq;               // (in registers: read again after each store the sums took 7 us more of 85)
+    if (w.plain && o.plain) sum_both_of<true>(dp, w, dq, o, lam, V, from, steps, out, tab);
+    else sum_both_of<false>(dp, w, dq, o, lam, V, from, steps, out, tab);
 }
 
 template <int NT>
@@ -781,6 +794,22 @@ struct Request {
     }
 };
 
+// log2 of the draft's total over the target's, by the fp32 sums, in the rows' units: S e^(M / T) over 2^R.
+RL_DEVINL Lam rough_ratio(const VerRow& p, const VerRow& q) {
+    auto rough = [](const VerRow& w) -> FF {
+        const FF l = {log2f(w.S), 0.f};
+        return w.plain ? ff_add(l, ff_add(ff_mul({w.M, 0.f}, w.c), {-w.R, 0.f})) : l;
+    };
+    const FF lam = ff_add(rough(q), ff_neg(rough(p)));
+    const float whole = floorf(lam.hi);
+    const FF f = ff_add(lam, {-whole, 0.f});
+    Lam x;
+    x.whole = static_cast<int>(whole);
+    x.hi = floorf(f.hi * 2048.f) * (1.f / 2048.f);
+    x.lo = __fadd_rn(__fsub_rn(f.hi, x.hi), f.lo);
+    return x;
+}
+
 // A block a request: what is accepted, and the new token where no row of logits has to be summed up for it.
 __global__ void __launch_bounds__(kDecideThreads, 2) decide_kernel(const __grid_constant__ VerArgs g) {
     extern __shared__ __align__(16) uint8_t raw[];
@@ -895,6 +924,7 @@ __global__ void __launch_bounds__(kDecideThreads, 2) decide_kernel(const __grid_
             s.draw.row[0] = s.rows[2 * at];
             s.draw.row[1] = s.rows[2 * at + 1];
             if (!refused) s.draw.row[1].mode = kDistNone;
+            if (s.draw.row[0].mode == kDistDense && s.draw.row[1].mode == kDistDense) s.draw.lam = rough_ratio(s.draw.row[0], s.draw.row[1]);
         }
         __syncthreads();
         const int p = s.draw.row[0].mode, d = s.draw.row[1].mode;
@@ -908,6 +938,7 @@ __global__ void __launch_bounds__(kDecideThreads, 2) decide_kernel(const __grid_
         if (rest) {
             const int words = static_cast<int>(sizeof(VerDraw) / 8);
             if (tid < words) reinterpret_cast<unsigned long long*>(g.draws + r)[tid] = reinterpret_cast<const unsigned long long*>(&s.draw)[tid];
+            if (tid == 0) g.todo[atomicAdd(g.n_todo, 1)] = static_cast<int>(r);      // (whose order no result depends on)
         } else if (tid == 0) {
             g.draws[r].t = -1;
         }
@@ -915,60 +946,51 @@ __global__ void __launch_bounds__(kDecideThreads, 2) decide_kernel(const __grid_
     set_status(g.status, bits);
 }
 
-// A cluster of blocks a request: the new token from rows of logits.
-struct Draw : Request<kDrawThreads> {
-    unsigned long long* cs;       // sums of the slice's parts
-    float* ds;                    // and the draft's weight where something is left
-    int rank, from, steps, phase; // its steps
+// ---- 3. sums ---------------------------------------------------------------------------------
+// All warps take the same number of steps: block b's warp w the (w * blocks + b)-th stretch, so that few steps are spread over all
+// multiprocessors.
+__global__ void __launch_bounds__(kSumThreads, kSumBlocks) sum_kernel(const __grid_constant__ VerArgs g) {
+    __shared__ float2 tab[2048];
+    const int V = static_cast<int>(g.a.V), steps = g.steps;
+    fill_table(tab, threadIdx.x, kSumThreads);
+    __syncthreads();
+    wait_for_previous();
+    let_next_start();
+    const long long units = static_cast<long long>(*g.n_todo) * steps, warps = static_cast<long long>(gridDim.x) * (kSumThreads / 32);
+    const long long per = (units + warps - 1) / warps, w = static_cast<long long>(threadIdx.x >> 5) * gridDim.x + blockIdx.x;
+    const long long end = min((w + 1) * per, units);
+    for (long long k = w * per; k < end;) {
+        const long long i = k / steps;
+        const int from = static_cast<int>(k - i * steps), n = static_cast<int>(min(end - k, static_cast<long long>(steps - from)));
+        const int r = g.todo[i];
+        const VerDraw& d = g.draws[r];
+        VerStep* out = g.sums + static_cast<long long>(r) * steps + from;
+        const bool p = d.row[0].mode == kDistDense, q = d.row[1].mode == kDistDense;
+        if (p && q) sum_both(g.side[0].d, &d.row[0], g.side[1].d, &d.row[1], d.lam, V, from, n, out, tab);
+        else sum_steps(g.side[p ? 0 : 1].d, &d.row[p ? 0 : 1], V, from, n, 0, 1, out, tab);
+        k += n;
+    }
+}
 
-    // The cluster's sum of v (the same in a block's threads), and the sum of the blocks before.
-    RL_DEVINL unsigned long long cluster_sum(unsigned long long v, unsigned long long& before) {
-        before = 0;
-        if (g.cs == 1) return v;
-        unsigned long long* slot = &s.xch[phase & 1];
-        ++phase;
-        if (tid == 0) *slot = v;
-        __syncthreads();
-        cluster_arrive();
-        cluster_wait();
-        unsigned long long total = 0;
-        for (int k = 0; k < g.cs; ++k) {
-            unsigned long long x;
-            asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(x) : "r"(cluster_addr(slot, k)) : "memory");
-            if (k < rank) before += x;
-            total += x;
+// ---- 4. the token ----------------------------------------------------------------------------
+// A block a request: the new token from rows of logits.
+struct Pick : Request<kPickThreads> {
+    unsigned long long* cs;       // sums of the row's parts
+    VerStep* sums;                // of its steps
+    int steps;
+
+    // The parts' sums into cs; returns the total.
+    RL_DEVINL unsigned long long take_parts() {
+        unsigned long long v = 0;
+        for (int k = tid; k < steps; k += kPickThreads) {
+            const ulonglong2* x = reinterpret_cast<const ulonglong2*>(sums[k].part);
+            const ulonglong2 a = x[0], b = x[1];
+            ulonglong2* to = reinterpret_cast<ulonglong2*>(cs + k * kVerStep);
+            to[0] = a;
+            to[1] = b;
+            v += (a.x + a.y) + (b.x + b.y);
         }
-        return total;
-    }
-    // The cluster's sums of two numbers.
-    RL_DEVINL ulonglong2 cluster_sum2(ulonglong2 v) {
-        if (g.cs == 1) return v;
-        if (tid == 0) s.pair = v;
-        __syncthreads();
-        cluster_arrive();
-        cluster_wait();
-        ulonglong2 total = make_ulonglong2(0, 0);
-        for (int k = 0; k < g.cs; ++k) {
-            unsigned long long x, y;
-            asm volatile("ld.shared::cluster.v2.u64 {%0, %1}, [%2];" : "=l"(x), "=l"(y) : "r"(cluster_addr(&s.pair, k)) : "memory");
-            total.x += x;
-            total.y += y;
-        }
-        return total;
-    }
-    RL_DEVINL unsigned long long slice_sum(int side) {
-        __syncthreads();
-        const unsigned long long x = sum_steps(g.side[side].d, &s.draw.row[side], V, from, steps, warp, kWarps, cs, s.tab);
-        return block_sum(lane == 0 ? x : 0ull);
-    }
-    // Counts a dense row's total; returns the slice's (its parts stay in cs) and the sum of the slices before.
-    RL_DEVINL unsigned long long count_total(int side, unsigned long long& before) {
-        const unsigned long long mine = slice_sum(side);
-        const unsigned long long t = cluster_sum(mine, before);
-        __syncthreads();
-        if (tid == 0) s.draw.row[side].total = t;
-        __syncthreads();
-        return mine;
+        return block_sum(v);
     }
     // What is left of a token of a dense target, z its logit and y the draft's, in the target's units.
     RL_DEVINL unsigned long long left_at(float z, float y, int j, bool whole, int& bits) {
@@ -995,50 +1017,38 @@ struct Draw : Request<kDrawThreads> {
         return x >= static_cast<double>(w) ? w : static_cast<unsigned long long>(__double2ll_rn(x));
     }
 
-    // What is left of a dense target beside a dense draft: the slice's sum (its parts in cs); counts both totals.
+    // What is left of a dense target beside a dense draft, by parts in cs; returns the total, and sets both rows' totals.
     RL_DEVINL unsigned long long left_of_rows() {
         VerRow& p = s.draw.row[0];
         VerRow& q = s.draw.row[1];
-        // log2 of a total in the row's unit, by the fp32 sums: S e^(M / T) over 2^R
-        auto rough = [](const VerRow& w) -> FF {
-            const FF l = {log2f(w.S), 0.f};
-            if (!w.plain) return l;
-            const FF m = ff_add(ff_mul({w.M, 0.f}, w.c), {-w.R, 0.f});
-            return ff_add(l, m);
-        };
-        if (tid == 0) {
-            const FF lam = ff_add(rough(q), ff_neg(rough(p)));
-            const float whole = floorf(lam.hi);
-            const FF f = ff_add(lam, {-whole, 0.f});
-            s.lam0.whole = static_cast<int>(whole);
-            s.lam0.hi = floorf(f.hi * 2048.f) * (1.f / 2048.f);
-            s.lam0.lo = __fadd_rn(__fsub_rn(f.hi, s.lam0.hi), f.lo);
+        ulonglong2 x = make_ulonglong2(0, 0);
+        for (int k = tid; k < steps; k += kPickThreads) {
+            x.x += sums[k].p;
+            x.y += sums[k].q;
         }
-        __syncthreads();
-        const Lam lam0 = s.lam0;
-        ulonglong2 x = sum_both(g.side[0].d, &p, g.side[1].d, &q, lam0, V, from, steps, warp, kWarps, cs, ds, s.tab);
-        __syncthreads();
+        x.x = warp_sum(x.x);
+        x.y = warp_sum(x.y);
         if (lane == 0) {
             s.red[warp] = x.x;
             s.red2[warp] = x.y;
         }
         __syncthreads();
-        x = make_ulonglong2(0, 0);
-#pragma unroll
-        for (int k = 0; k < kWarps; ++k) {
-            x.x += s.red[k];
-            x.y += s.red2[k];
-        }
-        x = cluster_sum2(x);
         if (warp == 0) {
+            x = make_ulonglong2(0, 0);
+#pragma unroll
+            for (int k = 0; k < kWarps; ++k) {
+                x.x += s.red[k];
+                x.y += s.red2[k];
+            }
             // the logs of both, a lane each, in the rows' units; log2 of the draft's total over the target's as a pair
+            const Lam lam = s.draw.lam;
             const FF l = ln_of(lane == 0 ? x.x : x.y, lane == 0 ? p.prec : q.prec);
             const FF lq = {__shfl_sync(0xffffffffu, l.hi, 1), __shfl_sync(0xffffffffu, l.lo, 1)};
             if (lane == 0) {
-                FF d = ff_add(ff_mul(ff_add(lq, ff_neg(l)), {kLog2eHi, kLog2eLo}), {lam0.hi, lam0.lo});      // log2 and the part that the sum left out
+                FF d = ff_add(ff_mul(ff_add(lq, ff_neg(l)), {kLog2eHi, kLog2eLo}), {lam.hi, lam.lo});        // log2 and the part that the sum left out
                 s.lam = d;
-                d = ff_add(d, {-static_cast<float>(lam0.whole), 0.f});
-                d = ff_add(d, {-lam0.hi, -lam0.lo});
+                d = ff_add(d, {-static_cast<float>(lam.whole), 0.f});
+                d = ff_add(d, {-lam.hi, -lam.lo});
                 s.turn = (d.hi + d.lo) * kLn2;
                 p.total = x.x;
                 q.total = x.y;                   // (less that part: only the ratio is read of it)
@@ -1047,11 +1057,13 @@ struct Draw : Request<kDrawThreads> {
         __syncthreads();
         const float turn = s.turn * power_of_2(p.prec);
         unsigned long long v = 0;
-        for (int i = tid; i < steps * kVerStep; i += kDrawThreads) {
-            const long long y = static_cast<long long>(cs[i]) + __float2ll_rn(ds[i] * turn);
-            cs[i] = y > 0 ? static_cast<unsigned long long>(y) : 0ull;
-            v += cs[i];
-        }
+        for (int k = tid; k < steps; k += kPickThreads)
+#pragma unroll
+            for (int j = 0; j < kVerStep; ++j) {
+                const long long y = static_cast<long long>(sums[k].part[j]) + __float2ll_rn(sums[k].drop[j] * turn);
+                cs[k * kVerStep + j] = y > 0 ? static_cast<unsigned long long>(y) : 0ull;
+                v += cs[k * kVerStep + j];
+            }
         return block_sum(v);
     }
 
@@ -1061,58 +1073,54 @@ struct Draw : Request<kDrawThreads> {
         const rl_dist& dp = g.side[0].d;
         const rl_dist& dq = g.side[1].d;
         bool whole = q.mode == kDistNone;
-        const int p0 = from * kVerStep, parts = steps * kVerStep;
-        unsigned long long before, mine, total = 0;
-        if (q.mode == kDistDense) mine = left_of_rows();
-        else mine = count_total(0, before);
-        if (whole) total = p.total;
-        for (int tries = 0; tries < 2; ++tries) {
-            if (whole || q.mode != kDistDense) {         // (else it is summed up already)
-                if (tries > 0) mine = slice_sum(0);
-                if (!whole) {
-                    // the draft's tokens in the slice, off their parts
-                    const long long n = q.mode == kDistPoint ? 1 : q.ee - q.eb;
-                    for (long long i = tid; i < n; i += kDrawThreads) {
-                        const int j = q.mode == kDistPoint ? q.at : dq.ids[q.eb + i];
-                        if (j < 0 || j >= V) {
-                            if (q.mode == kDistSupport) bits |= RL_STATUS_ID_RANGE;
-                            continue;
-                        }
-                        float lq = 0.f;
-                        if (q.mode == kDistSupport) {
-                            lq = dq.logq[q.eb + i];
-                            if (!(lq <= 1e-6f)) bits |= RL_STATUS_LOGQ;
-                            if (!(lq < INFINITY)) lq = -INFINITY;
-                            if (i > 0 && dq.ids[q.eb + i - 1] >= j) bits |= RL_STATUS_ROW_ORDER;
-                        }
-                        const int part = j / kVerPart - p0;
-                        if (part < 0 || part >= parts) continue;
-                        const unsigned long long w = left_at(logit_at(dp, p.dtype, p.row, j), 0.f, j, true, bits);
-                        atomicAdd(&cs[part], 0ull - taken(w, lq));
-                    }
-                    __syncthreads();
-                    // (a part's sum and its tokens' weights are rounded apart)
-                    unsigned long long v = 0;
-                    for (int i = tid; i < parts; i += kDrawThreads) {
-                        if (static_cast<long long>(cs[i]) < 0) cs[i] = 0;
-                        v += cs[i];
-                    }
-                    mine = block_sum(v);
-                }
-            }
-            if (tries > 0 || !whole) total = cluster_sum(mine, before);
-            if (total > 0 || whole) {
-                const unsigned long long target = fraction_of(u, total);
-                if (total > 0 && before <= target && target - before < mine) search(t, target - before, whole, bits);
-                else if (total == 0 && rank == 0 && tid == 0) finish(t, -1, 0.f, bits);
-                break;
-            }
-            whole = true;
+        unsigned long long total;
+        if (q.mode == kDistDense) {
+            total = left_of_rows();
+        } else {
+            total = take_parts();
+            if (tid == 0) s.draw.row[0].total = total;
+            __syncthreads();
         }
+        if (q.mode == kDistPoint || q.mode == kDistSupport) {
+            // the draft's tokens off their parts
+            const long long n = q.mode == kDistPoint ? 1 : q.ee - q.eb;
+            for (long long i = tid; i < n; i += kPickThreads) {
+                const int j = q.mode == kDistPoint ? q.at : dq.ids[q.eb + i];
+                if (j < 0 || j >= V) {
+                    if (q.mode == kDistSupport) bits |= RL_STATUS_ID_RANGE;
+                    continue;
+                }
+                float lq = 0.f;
+                if (q.mode == kDistSupport) {
+                    lq = dq.logq[q.eb + i];
+                    if (!(lq <= 1e-6f)) bits |= RL_STATUS_LOGQ;
+                    if (!(lq < INFINITY)) lq = -INFINITY;
+                    if (i > 0 && dq.ids[q.eb + i - 1] >= j) bits |= RL_STATUS_ROW_ORDER;
+                }
+                const unsigned long long w = left_at(logit_at(dp, p.dtype, p.row, j), 0.f, j, true, bits);
+                atomicAdd(&cs[j / kVerPart], 0ull - taken(w, lq));
+            }
+            __syncthreads();
+            // (a part's sum and its tokens' weights are rounded apart)
+            unsigned long long v = 0;
+            for (int i = tid; i < steps * kVerStep; i += kPickThreads) {
+                if (static_cast<long long>(cs[i]) < 0) cs[i] = 0;
+                v += cs[i];
+            }
+            total = block_sum(v);
+        }
+        if (total == 0 && !whole) {              // nothing is left: from the target
+            whole = true;
+            sum_steps(dp, &s.draw.row[0], V, 0, steps, warp, kWarps, sums, s.tab);
+            __syncthreads();
+            total = take_parts();
+        }
+        if (total > 0) search(t, fraction_of(u, total), whole, bits);
+        else if (tid == 0) finish(t, -1, 0.f, bits);
     }
-    // The block in whose slice the number falls: its part, then its token.
+    // The part in which the number falls, then its token.
     RL_DEVINL void search(long long t, unsigned long long want, bool whole, int& bits) {
-        const int n = steps * kVerStep, per = (n + kDrawThreads - 1) / kDrawThreads;
+        const int n = steps * kVerStep, per = (n + kPickThreads - 1) / kPickThreads;
         unsigned long long v = 0;
         __syncthreads();
         for (int j = 0; j < per; ++j) v += tid * per + j < n ? cs[tid * per + j] : 0ull;
@@ -1121,7 +1129,7 @@ struct Draw : Request<kDrawThreads> {
             for (int j = 0; j < per; ++j) {
                 const unsigned long long x = cs[tid * per + j];
                 if (want < c + x) {
-                    s.token = from * kVerStep + tid * per + j;
+                    s.token = tid * per + j;
                     s.unit = want - c;
                     break;
                 }
@@ -1176,34 +1184,28 @@ struct Draw : Request<kDrawThreads> {
     }
 };
 
-__global__ void __launch_bounds__(kDrawThreads, kDrawBlocks) draw_kernel(const __grid_constant__ VerArgs g) {
+__global__ void __launch_bounds__(kPickThreads, 2) pick_kernel(const __grid_constant__ VerArgs g) {
     extern __shared__ __align__(16) uint8_t raw[];
-    VerShared<kDrawThreads>& s = *reinterpret_cast<VerShared<kDrawThreads>*>(raw);
-    const long long r = blockIdx.x / static_cast<unsigned>(g.cs);
-    const int tid = threadIdx.x, V = static_cast<int>(g.a.V), rank = static_cast<int>(blockIdx.x - r * g.cs);
-    const int all = (V + kVerStep * kVerPart - 1) / (kVerStep * kVerPart), from = min(rank * g.per, all);
-    unsigned long long* cs = reinterpret_cast<unsigned long long*>(raw + sizeof(VerShared<kDrawThreads>));
-    Draw q{{g, s, V, tid, tid & 31, tid >> 5}, cs, reinterpret_cast<float*>(cs + g.per * kVerStep), rank, from, min(g.per, all - from), 0};
+    VerShared<kPickThreads>& s = *reinterpret_cast<VerShared<kPickThreads>*>(raw);
+    const long long r = blockIdx.x;
+    const int tid = threadIdx.x, V = static_cast<int>(g.a.V);
+    Pick q{{g, s, V, tid, tid & 31, tid >> 5}, reinterpret_cast<unsigned long long*>(raw + (sizeof(VerShared<kPickThreads>) + 15) / 16 * 16), g.sums + r * g.steps, g.steps};
     int bits = 0;
+    fill_table(s.tab, tid, kPickThreads);
     wait_for_previous();
     const int words = static_cast<int>(sizeof(VerDraw) / 8);
     if (tid < words) reinterpret_cast<unsigned long long*>(&s.draw)[tid] = reinterpret_cast<const unsigned long long*>(g.draws + r)[tid];
-    if (g.draws[r].t < 0) return;                // (all blocks of the cluster alike)
-    fill_table(s.tab, tid, kDrawThreads);
     __syncthreads();
+    if (s.draw.t < 0) return;
     if (s.draw.row[0].mode == kDistDense) {
         q.draw_dense(s.draw.t, s.draw.u, bits);
     } else {
-        unsigned long long before;
-        q.count_total(1, before);
-        if (rank == 0) q.draw_support(s.draw.t, s.draw.u, bits);
+        const unsigned long long total = q.take_parts();
+        if (tid == 0) s.draw.row[1].total = total;
+        __syncthreads();
+        q.draw_support(s.draw.t, s.draw.u, bits);
     }
     set_status(g.status, bits);
-    __syncthreads();
-    if (g.cs > 1) {                             // nobody leaves while its sums may be read
-        cluster_arrive();
-        cluster_wait();
-    }
 }
 
 // ---- host ------------------------------------------------------------------------------------
@@ -1223,7 +1225,13 @@ static VerArgs verify_view(void* ws, const rl_verify_args* a, int32_t* status, s
             s.nc = static_cast<int>((a->V + e - 1 + chunk - 1) / chunk);
             s.part = cv.take<float2>(static_cast<size_t>(a->T) * s.nc);
         }
-    if (a->target.logits || a->draft.logits) g.draws = cv.take<VerDraw>(static_cast<size_t>(a->R));
+    g.steps = static_cast<int>((a->V + kVerStep * kVerPart - 1) / (kVerStep * kVerPart));
+    if (a->target.logits || a->draft.logits) {
+        g.draws = cv.take<VerDraw>(static_cast<size_t>(a->R));
+        g.sums = cv.take<VerStep>(static_cast<size_t>(a->R) * g.steps);
+        g.todo = cv.take<int32_t>(static_cast<size_t>(a->R));
+        g.n_todo = cv.take<int32_t>(1);
+    }
     if (bytes) *bytes = align_up(cv.off, 256);
     return g;
 }
@@ -1250,39 +1258,21 @@ int verify_impl(const rl_verify_args* a, void* ws, int32_t* status, cudaStream_t
         ++launches;
     }
     if (a->R > 0) {
-        static std::atomic<uint64_t> decide{0}, draw{0};
+        static std::atomic<uint64_t> decide{0}, pick{0};
         const int smem = static_cast<int>(sizeof(VerShared<kDecideThreads>));
         if (!allow_smem(decide_kernel, smem, decide)) return RL_ERR_CUDA;
         int rc = launch_after(decide_kernel, dim3(static_cast<unsigned>(a->R)), kDecideThreads, static_cast<size_t>(smem), launches > 0, stream, g);
         if (rc != RL_OK) return rc;
         ++launches;
-        if (g.draws) {
-            // as many blocks a request as the GPU holds at once, up to eight, each of at least 16 steps of 512: a second round of
-            // blocks that start anew costs more than longer slices (of 256 threads: 128 requests 196 us in 1024 blocks, 188 us in
-            // 512).  Where targets may be support rows about half of the requests are expected to be done (256 of them 145 us in
-            // 512 blocks, 121 us in 1024)
-            const int all = static_cast<int>((a->V + kVerStep * kVerPart - 1) / (kVerStep * kVerPart));
-            const long long room = static_cast<long long>(kDrawBlocks) * num_sms() * (a->target.offsets ? 2 : 1) / a->R;
-            g.cs = static_cast<int>(room < 1 ? 1 : room < 8 ? room : 8);
-            while (g.cs > 1 && all < 16 * (g.cs - 1)) --g.cs;
-            g.per = (all + g.cs - 1) / g.cs;
-            const size_t fixed = sizeof(VerShared<kDrawThreads>), most = ((size_t(1) << 20) / kVerPart + kVerStep) * 12;
-            if (!allow_smem(draw_kernel, static_cast<int>(fixed + most), draw)) return RL_ERR_CUDA;
-            cudaLaunchConfig_t cfg = {};
-            cfg.gridDim = dim3(static_cast<unsigned>(a->R * g.cs), 1, 1);
-            cfg.blockDim = dim3(kDrawThreads, 1, 1);
-            cfg.dynamicSmemBytes = fixed + static_cast<size_t>(g.per) * kVerStep * 12;
-            cfg.stream = stream;
-            cudaLaunchAttribute attr[2];
-            attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-            attr[0].val.programmaticStreamSerializationAllowed = 1;
-            attr[1].id = cudaLaunchAttributeClusterDimension;
-            attr[1].val.clusterDim.x = static_cast<unsigned>(g.cs);
-            attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-            cfg.attrs = attr;
-            cfg.numAttrs = 2;
-            if (cudaLaunchKernelEx(&cfg, draw_kernel, g) != cudaSuccess) return RL_ERR_CUDA;
-            ++launches;
+        if (g.draws && a->T > 0) {
+            const long long most = static_cast<long long>(kSumBlocks) * num_sms(), units = a->R * g.steps;
+            rc = launch_after(sum_kernel, dim3(static_cast<unsigned>(units < most ? units : most)), kSumThreads, 0, true, stream, g);
+            if (rc != RL_OK) return rc;
+            const size_t fixed = (sizeof(VerShared<kPickThreads>) + 15) / 16 * 16, longest = ((size_t(1) << 20) / kVerPart + kVerStep) * 8;
+            if (!allow_smem(pick_kernel, static_cast<int>(fixed + longest), pick)) return RL_ERR_CUDA;
+            rc = launch_after(pick_kernel, dim3(static_cast<unsigned>(a->R)), kPickThreads, fixed + static_cast<size_t>(g.steps) * kVerStep * 8, true, stream, g);
+            if (rc != RL_OK) return rc;
+            launches += 2;
         }
     }
     count_launch(launches);
