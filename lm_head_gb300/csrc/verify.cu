@@ -35,6 +35,7 @@ constexpr int kPickThreads = 512;
 constexpr int kChunkThreads = 256;
 constexpr int kChunkPacks = 8;                 // 16-byte loads of a lane: 4 KB a warp
 constexpr int kUsedRows = 32768;               // rows of a step whose use is looked up in shared memory
+constexpr int kListedRows = 8192;              // rows of a step of which those that are read are listed
 constexpr float kPlainRef = 1900.f;            // |max log2(e) / T| up to which weights need no difference to the maximum
 
 struct VerSide {
@@ -191,6 +192,8 @@ RL_DEVINL float2 chunk_of(const T* row, int V, int chunk, float Tm, bool& bad) {
 
 __global__ void __launch_bounds__(kChunkThreads, 3) chunk_kernel(const __grid_constant__ VerArgs g) {
     __shared__ uint32_t used[2][kUsedRows / 32];
+    __shared__ uint16_t list[2 * kListedRows];   // the rows of logits that are read, the target's first
+    __shared__ int sums[kChunkThreads / 32];
     const rl_verify_args& a = g.a;
     const int V = static_cast<int>(a.V);
     for (long long t = static_cast<long long>(blockIdx.x) * kChunkThreads + threadIdx.x; t < a.T; t += static_cast<long long>(gridDim.x) * kChunkThreads) {
@@ -214,22 +217,62 @@ __global__ void __launch_bounds__(kChunkThreads, 3) chunk_kernel(const __grid_co
         }
         __syncthreads();
     }
+    // Where many rows may be support rows, those that are read are listed, so that all warps read as many: 256 requests, half of
+    // them with support rows, 95 us, 104 us without the list.  It takes 1.5 us (128 requests of logits 154 us, 152 us without).
+    const bool listed = a.T <= kListedRows && ((g.side[0].d.logits && g.side[0].d.offsets) || (g.side[1].d.logits && g.side[1].d.offsets));
+    long long n_rows[2] = {a.T, a.T};
+    if (listed) {
+        const int T = static_cast<int>(a.T), per = (T + kChunkThreads - 1) / kChunkThreads, t0 = min(static_cast<int>(threadIdx.x) * per, T), t1 = min(t0 + per, T);
+        int at = 0;
+        for (int side = 0; side < 2; ++side) {
+            const rl_dist& d = g.side[side].d;
+            auto read = [&](int t) {
+                int none = 0;
+                if (!d.logits || !((used[side][t >> 5] >> (t & 31)) & 1u)) return false;
+                const long long row = row_of(d, t, none);
+                return row >= 0 && !is_support(d, row);
+            };
+            int n = 0;
+            for (int t = t0; t < t1; ++t) n += read(t);
+            int before = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int x = __shfl_up_sync(0xffffffffu, before, o);
+                if (static_cast<int>(threadIdx.x & 31) >= o) before += x;
+            }
+            __syncthreads();
+            if ((threadIdx.x & 31) == 31) sums[threadIdx.x >> 5] = before;
+            __syncthreads();
+            before += at - n;
+            int total = 0;
+            for (int w = 0; w < kChunkThreads / 32; ++w) {
+                if (w < static_cast<int>(threadIdx.x >> 5)) before += sums[w];
+                total += sums[w];
+            }
+            for (int t = t0; t < t1 && n > 0; ++t)
+                if (read(t)) list[before++] = static_cast<uint16_t>(t);
+            n_rows[side] = total;
+            at += total;
+        }
+        __syncthreads();
+    }
     // one or two chunks of a row a warp
     const long long warps = static_cast<long long>(gridDim.x) * (kChunkThreads / 32);
     const int groups[2] = {(g.side[0].nc + g.group - 1) / g.group, (g.side[1].nc + g.group - 1) / g.group};
-    const long long first = a.T * groups[0], units = first + a.T * groups[1];
+    const long long first = n_rows[0] * groups[0], units = first + n_rows[1] * groups[1];
     int bits = 0;
     bool bad = false;
     for (long long id = static_cast<long long>(blockIdx.x) * (kChunkThreads / 32) + (threadIdx.x >> 5); id < units; id += warps) {
         const int side = id >= first ? 1 : 0;
         const VerSide& s = g.side[side];
         const long long x = side ? id - first : id;
-        const long long t = x <= UINT_MAX ? static_cast<uint32_t>(x) / static_cast<uint32_t>(groups[side]) : x / groups[side];
-        const int c0 = static_cast<int>(x - t * groups[side]) * g.group, c1 = min(c0 + g.group, s.nc);
-        if (known && !((used[side][t >> 5] >> (t & 31)) & 1u)) continue;
+        const long long k = x <= UINT_MAX ? static_cast<uint32_t>(x) / static_cast<uint32_t>(groups[side]) : x / groups[side];
+        const int c0 = static_cast<int>(x - k * groups[side]) * g.group, c1 = min(c0 + g.group, s.nc);
+        const long long t = listed ? list[(side ? n_rows[0] : 0) + k] : k;
+        if (!listed && known && !((used[side][t >> 5] >> (t & 31)) & 1u)) continue;
         int row_bits = 0;
         const long long row = row_of(s.d, t, row_bits);
-        if (row < 0 || is_support(s.d, row)) continue;
+        if (!listed && (row < 0 || is_support(s.d, row))) continue;
         const float Tm = temperature_of(s.d, row, bits);
         float2 mine = make_float2(0.f, 0.f);
         auto each = [&](auto* p) {
