@@ -770,10 +770,10 @@ struct Request {
             // e = d c - R in log2 units, then to natural ones less the total's log
             FF e = ff_add(ff_mul(d, x.c), {-x.R, 0.f});
             e = ff_add(ff_mul(e, {0.693147182464599609375f, -1.90465429995775e-09f}), ff_neg(ln_total));
-            return exp_pair(e);
+            return exp_table(e);
         }
         const float q = support_at(1, x, j, bits);
-        return q > -INFINITY ? exp_ff(q) : FF{0.f, 0.f};
+        return q > -INFINITY ? exp_table({q, 0.f}) : FF{0.f, 0.f};
     }
     // ln of a counted total, in the unit 2^R (2^0) of its weights
     static RL_DEVINL FF ln_of(unsigned long long total, int prec) {
@@ -804,7 +804,7 @@ struct Request {
             if (i > 0 && d.ids[p.eb + i - 1] >= j) bits |= RL_STATUS_ROW_ORDER;
             if (!(l <= 1e-6f)) bits |= RL_STATUS_LOGQ;
             if (!(l < INFINITY) || !(l > -INFINITY)) return 0ull;
-            FF v = exp_ff(l);
+            FF v = exp_table({l, 0.f});
             if (!whole) v = ordered(left_of(v, prob_pair(q, j, lq, bits)));
             return fixed_of(v.hi, v.lo, 52);
         };
@@ -1055,7 +1055,7 @@ struct Pick : Request<kPickThreads> {
     // What a draft's probability e^lq takes off a weight w: the smaller of the two.
     RL_DEVINL unsigned long long taken(unsigned long long w, float lq) {
         if (!(lq > -INFINITY)) return 0ull;
-        const FF e = exp_ff(lq);
+        const FF e = exp_table({lq, 0.f});
         const double x = (static_cast<double>(e.hi) + static_cast<double>(e.lo)) * static_cast<double>(s.draw.row[0].total);
         return x >= static_cast<double>(w) ? w : static_cast<unsigned long long>(__double2ll_rn(x));
     }

@@ -383,6 +383,23 @@ def test_more_rows_than_are_looked_up():
     assert ref["accepted"].sum() > R / 2
 
 
+@pytest.mark.parametrize("R", [2000, 2100])
+def test_mixed_rows_about_as_many_as_are_listed(R):
+    """Rows that may be support rows are listed up to a number of them: steps of 8000 and 8400 rows."""
+    rng = np.random.default_rng(R)
+    n, V, kept = 4, 40, 60
+    z = torch.randn(kept, V, generator=torch.Generator().manual_seed(2)) * 2
+    zd = z + 0.3 * torch.randn(kept, V, generator=torch.Generator().manual_seed(3))
+    halves = []
+    for x in (z, zd):
+        ids, lq = support_of(x, None, rng, 20)
+        halves.append(Half(V, x, ids=ids, lq=lq, rep=(rng.random(kept) < 0.5).astype(np.uint8), rows=rng.integers(0, kept, R * n)))
+    c = dict(step=rng.integers(0, V, R * n), cu=np.arange(0, R * n + 1, n), u=(rng.integers(0, 1 << 24, R * n) / 2.0 ** 24).astype(np.float32),
+             un=(rng.integers(0, 1 << 24, R) / 2.0 ** 24).astype(np.float32), V=V, ctx=np.zeros(R, int), target=halves[0], draft=halves[1])
+    ref, _ = check(c, skips=2)
+    assert ref["accepted"].sum() > R / 4
+
+
 def test_tokens_are_the_targets_samples():
     """Over many requests with one draft each the new tokens at the first place follow p: six deviations of each count."""
     V, R = 12, 200000
