@@ -104,11 +104,6 @@ RL_DEVINL FF ln_pair(FF x) {
 }
 
 RL_DEVINL FF ff_neg(FF a) { return {-a.hi, -a.lo}; }
-// e^x of a pair (-inf gives 0)
-RL_DEVINL FF exp_pair(FF x) {
-    const FF e = exp_ff(x.hi);
-    return fast_two_sum(e.hi, e.hi > 0.f ? fmaf(e.hi, x.lo, e.lo) : 0.f);
-}
 // a / b
 RL_DEVINL FF ff_div(FF a, FF b) {
     const float q = a.hi / b.hi;

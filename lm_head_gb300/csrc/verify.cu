@@ -14,6 +14,13 @@
 //                      draft has logits too.
 //  4. pick_kernel      a block a request: adds the parts up, takes a draft's support row off the target's parts, and scans
 //                      the part in which the random number falls.
+//
+// 128 requests of five bf16 rows of 151,936 logits on both sides, 152 us: the pass over 350 MB 62 us (82 % of a copy's rate),
+// the decisions 9, the sums 84 and the tokens 16 by themselves, each kernel's start under the one before.  The
+// sums read 78 MB that are mostly in L2; what bounds them is the issue of some 50 instructions a weight (two table look-ups,
+// two polynomials and three sums in pairs of floats for a token), 2.6 of 4 a cycle.  Sums that stay with a request (a
+// cluster of two to eight blocks for each, which scans its own parts) left multiprocessors without blocks: 160 us, one
+// request 24 us instead of 20, eight 37 instead of 31.
 #include <cfloat>
 #include <climits>
 #include <cmath>
@@ -89,6 +96,8 @@ RL_DEVINL float logit_at(const rl_dist& d, int dtype, long long row, long long j
 }
 
 // ---- 1. chunks ---------------------------------------------------------------------------
+// HBM: 350 MB in 62 us.  A warp's eight 16-byte loads a lane are all on their way before the first is used; 24 warps a
+// multiprocessor, 98 KB in flight.
 // Places: element i of a row lies at place i + phase, so that 16-byte packs of places are aligned.
 template <typename T>
 RL_DEVINL float2 chunk_of(const T* row, int V, int chunk, float Tm, bool& bad) {
@@ -293,6 +302,8 @@ __global__ void __launch_bounds__(kChunkThreads, 3) chunk_kernel(const __grid_co
 }
 
 // ---- 2. requests ---------------------------------------------------------------------------
+// Latency: a row's parts (75 of 4 KB), its candidate's logit, one comparison (9 us by itself); support rows' draws are
+// a block's sums and a scan (256 requests, half of them support rows, 18 us).
 enum { kDistNone, kDistDense, kDistPoint, kDistSupport };
 
 // A row's distribution.
@@ -991,7 +1002,9 @@ __global__ void __launch_bounds__(kDecideThreads, 2) decide_kernel(const __grid_
 
 // ---- 3. sums ---------------------------------------------------------------------------------
 // All warps take the same number of steps: block b's warp w the (w * blocks + b)-th stretch, so that few steps are spread over all
-// multiprocessors.
+// multiprocessors.  Two blocks of 512 threads (64 registers) a multiprocessor; of 384 (80 registers, nothing spilled) 128 requests
+// take 1 us longer, four blocks of 256 4 us longer (a table each).  Steps that a block's warps take one by one as they get done: one
+// block of 1024 7 us less for 128 requests with drafts' rows, but 3 us more for those without and for eight requests.
 __global__ void __launch_bounds__(kSumThreads, kSumBlocks) sum_kernel(const __grid_constant__ VerArgs g) {
     __shared__ float2 tab[2048];
     const int V = static_cast<int>(g.a.V), steps = g.steps;
@@ -1016,6 +1029,8 @@ __global__ void __launch_bounds__(kSumThreads, kSumBlocks) sum_kernel(const __gr
 }
 
 // ---- 4. the token ----------------------------------------------------------------------------
+// Latency: the parts' sums of a row of 151,936 are 19 KB, and loads, block sums, two logs and the scan of one part follow on one
+// another (16 us by itself, some 7 of them after the sums).
 // A block a request: the new token from rows of logits.
 struct Pick : Request<kPickThreads> {
     unsigned long long* cs;       // sums of the row's parts
@@ -1290,7 +1305,7 @@ int verify_impl(const rl_verify_args* a, void* ws, int32_t* status, cudaStream_t
     ProfScope prof(RL_PROF_OTHER, stream);
     int launches = 0;
     if (a->T > 0) {
-        // (two chunks share the look-up of their row; of few rows each warp gets one: 128 requests 186 us by ones, 178 by twos)
+        // (two chunks share the look-up of their row, 8 us less for 128 requests; of few rows each warp gets one)
         const long long cap = 3ll * num_sms(), chunks = a->T * (g.side[0].nc + g.side[1].nc);
         g.group = chunks > cap * (kChunkThreads / 32) ? 2 : 1;
         const long long units = a->T * ((g.side[0].nc + g.group - 1) / g.group + (g.side[1].nc + g.group - 1) / g.group), fill = (a->T + kChunkThreads - 1) / kChunkThreads;
