@@ -193,6 +193,8 @@ def rl_page_copy(src, dst, k_cache, v_cache, *, tokens=None, status=None, stream
     for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
         if not t.is_cuda:
             raise _err(f"{name}: librlhead takes device tensors; got a CPU tensor")
+        if t.is_contiguous() and v_cache.is_contiguous():
+            continue
         one = t[0] if many and layers else t
         if not one.is_contiguous() or (many and layers > 1 and t.stride(0) != stride):
             raise _err(f"{name}: expected dense layers, as far apart in both caches")
