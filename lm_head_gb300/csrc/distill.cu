@@ -16,8 +16,8 @@
 // then the blocks send each other (reference, sum) of their slices, and each block turns its slice into the gradient
 // in place and sends it off by one bulk copy.  So logits are read once and gradients written once.
 //
-// HBM bounds it for long rows: 4096 bf16 rows of 151,936 logits 410 us (89 % of a copy's rate), 2048 fp32 rows 434 us with a rest
-// and up to 128 entries (85 %), 387 us without (95 %).  Each row waits for its support and its cluster; slices of
+// HBM bounds it for long rows: 4096 bf16 rows of 151,936 logits 411 us (89 % of a copy's rate), 2048 fp32 rows 436 us with a rest
+// and up to 128 entries (84 %), 387 us without (95 %).  Each row waits for its support and its cluster; slices of
 // 75 KB leave room for three blocks on a multiprocessor, whose loads, sums and stores fill one another's waits.  The forward
 // alone, whose blocks store nothing, is at 72 % (254 us): their loads do not follow one another closely enough.
 //

@@ -315,6 +315,23 @@ def test_graphs_streams_and_kept_outputs():
     assert all(torch.equal(a.loss, want.loss) and torch.equal(b, wd) for a, b in res)
 
 
+def test_waits_that_run_out():
+    """With the shortest limit a call ends, with TIMEOUT and no other bit if a wait ran out, and the next one, with the usual
+    limit, is right."""
+    c = make(304, 65537, "fp32", np.arange(304) % 30)
+    args = (c["z"], c["off"], c["ids"], c["q"], c["dl"], rh.DistillParams(kind="reverse", tail=True))
+    want, wd = rh.rl_distill_fwd_bwd(*args)
+    rh.rl_set_option(rh.RL_OPT_WAIT_LIMIT_US, 1)
+    try:
+        bits = [rh.rl_distill_fwd_bwd(*args)[0].status_bits() for _ in range(3)]
+    finally:
+        rh.rl_set_option(rh.RL_OPT_WAIT_LIMIT_US, 1_000_000)
+    print("bits", bits)
+    assert all(b in (0, 0x200) for b in bits)
+    again, d = rh.rl_distill_fwd_bwd(*args)
+    assert again.status_bits() == 0 and torch.equal(again.loss, want.loss) and torch.equal(d, wd)
+
+
 def test_no_rows():
     z = torch.zeros(0, 100, device="cuda")
     e = torch.zeros(0, device="cuda")
