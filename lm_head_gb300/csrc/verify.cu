@@ -36,8 +36,8 @@ namespace rl {
 constexpr int kVerPart = 128;                  // logits of a part
 constexpr int kVerStep = 4;                    // parts that a warp sums up at a time
 constexpr int kDecideThreads = 512;            // a row of either side a warp
-constexpr int kSumThreads = 512;
-constexpr int kSumBlocks = 2;                  // of them on a multiprocessor
+constexpr int kSumThreads = 1024;
+constexpr int kSumBlocks = 1;                  // of them on a multiprocessor
 constexpr int kPickThreads = 512;
 constexpr int kChunkThreads = 256;
 constexpr int kChunkPacks = 8;                 // 16-byte loads of a lane: 4 KB a warp
@@ -393,14 +393,16 @@ RL_DEVINL FF left_of(FF v, FF q) {
 }
 RL_DEVINL FF ordered(FF x) { return two_sum(x.hi, x.lo); }
 
+RL_DEVINL const void* logits_of(const rl_dist& d, const VerRow& r) {
+    return static_cast<const char*>(d.logits) + ((r.row * d.row_stride) << (r.dtype == RL_DTYPE_F32 ? 2 : 1));
+}
 // A lane's logits of N parts from element i0 on, four of each, past the row's end -inf.
 template <int N>
-RL_DEVINL void step_load(const rl_dist& d, const VerRow& r, int V, int i0, float (&z)[N][4]) {
+RL_DEVINL void step_load(const void* logits, const VerRow& r, int V, int i0, float (&z)[N][4]) {
     const int lane = threadIdx.x & 31;
-    const long long base = r.row * d.row_stride;
     const bool whole = r.vec && i0 + N * kVerPart <= V;
     if (r.dtype == RL_DTYPE_F32) {
-        const float* p = static_cast<const float*>(d.logits) + base + i0 + lane * 4;
+        const float* p = static_cast<const float*>(logits) + i0 + lane * 4;
         if (whole) {
 #pragma unroll
             for (int s = 0; s < N; ++s) {
@@ -415,7 +417,7 @@ RL_DEVINL void step_load(const rl_dist& d, const VerRow& r, int V, int i0, float
         }
         return;
     }
-    const uint16_t* p = static_cast<const uint16_t*>(d.logits) + base + i0 + lane * 4;
+    const uint16_t* p = static_cast<const uint16_t*>(logits) + i0 + lane * 4;
     uint2 q[N];
     if (whole) {
 #pragma unroll
@@ -474,17 +476,28 @@ RL_DEVINL unsigned long long in_units(unsigned long long w50, int ref, int prec)
     const int sh = prec - 50 + ref;
     return sh >= 0 ? w50 << sh : sh > -64 ? (w50 + (1ull << (-sh - 1))) >> -sh : 0ull;
 }
-// Sums of the weights of `steps` steps of a row from step `from` on, by a warp that takes every `stride`-th; the parts' sums
+// The step that a warp takes after step k: every `stride`-th, or the next that no warp of the block has.
+struct Steps {
+    int stride;
+    int* next;                    // in shared memory; NULL: by stride
+    RL_DEVINL int after(int k) const {
+        if (!next) return k + stride;
+        int x = 0;
+        if ((threadIdx.x & 31) == 0) x = atomicAdd(next, 1);
+        return __shfl_sync(0xffffffffu, x, 0);
+    }
+};
+// Sums of the weights of a row's steps that are numbers base + k, k < end, by a warp that begins with k; the parts' sums
 // into `out` where it is given.  Each step is summed relative to its own largest weight.  Lane 0 has the sum.
-__device__ __noinline__ unsigned long long sum_steps(const rl_dist& d, const VerRow* row, int V, int from, int steps, int first, int stride,
+__device__ __noinline__ unsigned long long sum_steps(const void* logits, const VerRow* row, int V, int base, int end, int& k, Steps by,
                                                      VerStep* out, const float2* tab) {
     const VerRow w = *row;
     const int lane = threadIdx.x & 31;
     unsigned long long mine = 0;
 #pragma unroll 1
-    for (int k = first; k < steps; k += stride) {
+    for (; k < end; k = by.after(k)) {
         float z[kVerStep][4];
-        step_load(d, w, V, (from + k) * kVerStep * kVerPart, z);
+        step_load(logits, w, V, (base + k) * kVerStep * kVerPart, z);
         const float m = step_largest(z);
         const float ex = w.plain ? fmaf(m, w.c.hi, -w.R) : (m - w.M) * w.c.hi;
         unsigned long long sum = 0;
@@ -525,7 +538,7 @@ __device__ __noinline__ unsigned long long sum_steps(const rl_dist& d, const Ver
             sum = in_units(LaneSum::total(top, low), static_cast<int>(ref), w.prec);
         }
         if (lane < kVerStep) {
-            if (out) out[k].part[lane] = sum;
+            if (out) out[base + k].part[lane] = sum;
             mine += sum;
         }
     }
@@ -549,21 +562,21 @@ struct LongSum {
 // second order (d(lam)^2, below 2^-36).  Three passes (both totals, then what is left) took half as long again.
 // The draft's total comes out as 2^-(hi + lo) times itself.
 template <bool kPlain>
-RL_DEVINL void sum_both_of(const rl_dist& dp, const VerRow& w, const rl_dist& dq, const VerRow& o, Lam lam, int V, int from, int steps, VerStep* out,
-                           const float2* tab) {
+RL_DEVINL void sum_both_of(const void* zp, const VerRow& w, const void* yp, const VerRow& o, Lam lam, int V, int base, int end, int& at, Steps by,
+                           VerStep* out, const float2* tab) {
     constexpr int N = kVerStep / 2;              // half a step at a time, for the registers
     const int lane = threadIdx.x & 31;
     const bool wp = kPlain || w.plain, op = kPlain || o.plain;
     unsigned long long mine = 0;
 #pragma unroll 1
-    for (int k = 0; k < 2 * steps; ++k) {
-        const int i0 = (2 * from + k) * N * kVerPart;
+    for (int k = 2 * at; at < end;) {
+        const int i0 = (2 * base + k) * N * kVerPart;
         unsigned long long sum = 0;
         float d_out = 0.f;
         if (i0 < V) {
             float z[N][4], y[N][4];
-            step_load(dp, w, V, i0, z);
-            step_load(dq, o, V, i0, y);
+            step_load(zp, w, V, i0, z);
+            step_load(yp, o, V, i0, y);
             const float mz = step_largest(z), my = step_largest(y);
             const float ez = wp ? fmaf(mz, w.c.hi, -w.R) : (mz - w.M) * w.c.hi, ey = op ? fmaf(my, o.c.hi, -o.R) : (my - o.M) * o.c.hi;
             // (below 2^-100 of its row's largest, or -inf, a side is nothing here)
@@ -612,7 +625,7 @@ RL_DEVINL void sum_both_of(const rl_dist& dp, const VerRow& w, const rl_dist& dq
             }
             sum = in_units(LaneSum::total(top, low), static_cast<int>(lane <= N ? rz : ry), lane <= N ? w.prec : o.prec);
         }
-        VerStep& to = out[k >> 1];
+        VerStep& to = out[base + at];
         if (lane < N) {
             to.part[(k & 1) * N + lane] = sum;
             to.drop[(k & 1) * N + lane] = d_out;
@@ -623,13 +636,19 @@ RL_DEVINL void sum_both_of(const rl_dist& dp, const VerRow& w, const rl_dist& dq
                 mine = 0;
             }
         }
+        if (k & 1) {
+            at = by.after(at);
+            k = 2 * at;
+        } else {
+            ++k;
+        }
     }
 }
-__device__ __noinline__ void sum_both(const rl_dist& dp, const VerRow* rp, const rl_dist& dq, const VerRow* rq, Lam lam, int V, int from, int steps,
-                                      VerStep* out, const float2* tab) {
+__device__ __noinline__ void sum_both(const void* zp, const VerRow* rp, const void* yp, const VerRow* rq, Lam lam, int V, int base, int end,
+                                      int& at, Steps by, VerStep* out, const float2* tab) {
     const VerRow w = *rp, o = *rq;               // (in registers: read again after each store the sums took 7 us more of 85)
-    if (w.plain && o.plain) sum_both_of<true>(dp, w, dq, o, lam, V, from, steps, out, tab);
-    else sum_both_of<false>(dp, w, dq, o, lam, V, from, steps, out, tab);
+    if (w.plain && o.plain) sum_both_of<true>(zp, w, yp, o, lam, V, base, end, at, by, out, tab);
+    else sum_both_of<false>(zp, w, yp, o, lam, V, base, end, at, by, out, tab);
 }
 
 template <int NT>
@@ -938,7 +957,8 @@ __global__ void __launch_bounds__(kDecideThreads, 2) decide_kernel(const __grid_
                     VerRow& w = s.rows[2 * k + sd];
                     if (w.mode != kDistDense) continue;
                     __syncthreads();
-                    const unsigned long long sum = sum_steps(g.side[sd].d, &w, V, 0, steps, q.warp, kDecideThreads / 32, nullptr, s.tab);
+                    int first = q.warp;
+                    const unsigned long long sum = sum_steps(logits_of(g.side[sd].d, w), &w, V, 0, steps, first, {kDecideThreads / 32, nullptr}, nullptr, s.tab);
                     const unsigned long long total = q.block_sum(q.lane == 0 ? sum : 0ull);
                     if (tid == 0) w.total = total;
                 }
@@ -1001,30 +1021,26 @@ __global__ void __launch_bounds__(kDecideThreads, 2) decide_kernel(const __grid_
 }
 
 // ---- 3. sums ---------------------------------------------------------------------------------
-// All warps take the same number of steps: block b's warp w the (w * blocks + b)-th stretch, so that few steps are spread over all
-// multiprocessors.  Two blocks of 512 threads (64 registers) a multiprocessor; of 384 (80 registers, nothing spilled) 128 requests
-// take 1 us longer, four blocks of 256 4 us longer (a table each).  Steps that a block's warps take one by one as they get done: one
-// block of 1024 7 us less for 128 requests with drafts' rows, but 3 us more for those without and for eight requests.
+// A block takes as many steps as another, its warps one after another as they get done.
 __global__ void __launch_bounds__(kSumThreads, kSumBlocks) sum_kernel(const __grid_constant__ VerArgs g) {
     __shared__ float2 tab[2048];
+    __shared__ int next;
     const int V = static_cast<int>(g.a.V), steps = g.steps;
     fill_table(tab, threadIdx.x, kSumThreads);
+    if (threadIdx.x == 0) next = kSumThreads / 32;
     __syncthreads();
     wait_for_previous();
     let_next_start();
-    const long long units = static_cast<long long>(*g.n_todo) * steps, warps = static_cast<long long>(gridDim.x) * (kSumThreads / 32);
-    const long long per = (units + warps - 1) / warps, w = static_cast<long long>(threadIdx.x >> 5) * gridDim.x + blockIdx.x;
-    const long long end = min((w + 1) * per, units);
-    for (long long k = w * per; k < end;) {
-        const long long i = k / steps;
-        const int from = static_cast<int>(k - i * steps), n = static_cast<int>(min(end - k, static_cast<long long>(steps - from)));
-        const int r = g.todo[i];
+    const long long units = static_cast<long long>(*g.n_todo) * steps, first = units * blockIdx.x / gridDim.x;
+    const int n = static_cast<int>(units * (blockIdx.x + 1) / gridDim.x - first);
+    for (int k = threadIdx.x >> 5; k < n;) {
+        const long long i = (first + k) / steps;
+        const int base = static_cast<int>(first - i * steps), end = min(n, steps - base), r = g.todo[i];      // (the request's step 0 is -base of the block's)
         const VerDraw& d = g.draws[r];
-        VerStep* out = g.sums + static_cast<long long>(r) * steps + from;
+        VerStep* out = g.sums + static_cast<long long>(r) * steps;
         const bool p = d.row[0].mode == kDistDense, q = d.row[1].mode == kDistDense;
-        if (p && q) sum_both(g.side[0].d, &d.row[0], g.side[1].d, &d.row[1], d.lam, V, from, n, out, tab);
-        else sum_steps(g.side[p ? 0 : 1].d, &d.row[p ? 0 : 1], V, from, n, 0, 1, out, tab);
-        k += n;
+        if (p && q) sum_both(logits_of(g.side[0].d, d.row[0]), &d.row[0], logits_of(g.side[1].d, d.row[1]), &d.row[1], d.lam, V, base, end, k, {0, &next}, out, tab);
+        else sum_steps(logits_of(g.side[p ? 0 : 1].d, d.row[p ? 0 : 1]), &d.row[p ? 0 : 1], V, base, end, k, {0, &next}, out, tab);
     }
 }
 
@@ -1169,7 +1185,8 @@ struct Pick : Request<kPickThreads> {
         }
         if (total == 0 && !whole) {              // nothing is left: from the target
             whole = true;
-            sum_steps(dp, &s.draw.row[0], V, 0, steps, warp, kWarps, sums, s.tab);
+            int first = warp;
+            sum_steps(logits_of(dp, p), &s.draw.row[0], V, 0, steps, first, {kWarps, nullptr}, sums, s.tab);
             __syncthreads();
             total = take_parts();
         }
