@@ -487,11 +487,14 @@ struct Steps {
         return __shfl_sync(0xffffffffu, x, 0);
     }
 };
+// The table by its shared address: a pointer that a call passes would be a generic one, with slower loads.
+RL_DEVINL const float2* table_at(uint32_t table) { return static_cast<const float2*>(__cvta_shared_to_generic(table)); }
 // Sums of the weights of a row's steps that are numbers base + k, k < end, by a warp that begins with k; the parts' sums
 // into `out` where it is given.  Each step is summed relative to its own largest weight.  Lane 0 has the sum.
 __device__ __noinline__ unsigned long long sum_steps(const void* logits, const VerRow* row, int V, int base, int end, int& k, Steps by,
-                                                     VerStep* out, const float2* tab) {
+                                                     VerStep* out, uint32_t table) {
     const VerRow w = *row;
+    const float2* tab = table_at(table);
     const int lane = threadIdx.x & 31;
     unsigned long long mine = 0;
 #pragma unroll 1
@@ -645,7 +648,8 @@ RL_DEVINL void sum_both_of(const void* zp, const VerRow& w, const void* yp, cons
     }
 }
 __device__ __noinline__ void sum_both(const void* zp, const VerRow* rp, const void* yp, const VerRow* rq, Lam lam, int V, int base, int end,
-                                      int& at, Steps by, VerStep* out, const float2* tab) {
+                                      int& at, Steps by, VerStep* out, uint32_t table) {
+    const float2* tab = table_at(table);
     const VerRow w = *rp, o = *rq;               // (in registers: read again after each store the sums took 7 us more of 85)
     if (w.plain && o.plain) sum_both_of<true>(zp, w, yp, o, lam, V, base, end, at, by, out, tab);
     else sum_both_of<false>(zp, w, yp, o, lam, V, base, end, at, by, out, tab);
@@ -958,7 +962,7 @@ __global__ void __launch_bounds__(kDecideThreads, 2) decide_kernel(const __grid_
                     if (w.mode != kDistDense) continue;
                     __syncthreads();
                     int first = q.warp;
-                    const unsigned long long sum = sum_steps(logits_of(g.side[sd].d, w), &w, V, 0, steps, first, {kDecideThreads / 32, nullptr}, nullptr, s.tab);
+                    const unsigned long long sum = sum_steps(logits_of(g.side[sd].d, w), &w, V, 0, steps, first, {kDecideThreads / 32, nullptr}, nullptr, smem_addr(s.tab));
                     const unsigned long long total = q.block_sum(q.lane == 0 ? sum : 0ull);
                     if (tid == 0) w.total = total;
                 }
@@ -1039,8 +1043,8 @@ __global__ void __launch_bounds__(kSumThreads, kSumBlocks) sum_kernel(const __gr
         const VerDraw& d = g.draws[r];
         VerStep* out = g.sums + static_cast<long long>(r) * steps;
         const bool p = d.row[0].mode == kDistDense, q = d.row[1].mode == kDistDense;
-        if (p && q) sum_both(logits_of(g.side[0].d, d.row[0]), &d.row[0], logits_of(g.side[1].d, d.row[1]), &d.row[1], d.lam, V, base, end, k, {0, &next}, out, tab);
-        else sum_steps(logits_of(g.side[p ? 0 : 1].d, d.row[p ? 0 : 1]), &d.row[p ? 0 : 1], V, base, end, k, {0, &next}, out, tab);
+        if (p && q) sum_both(logits_of(g.side[0].d, d.row[0]), &d.row[0], logits_of(g.side[1].d, d.row[1]), &d.row[1], d.lam, V, base, end, k, {0, &next}, out, smem_addr(tab));
+        else sum_steps(logits_of(g.side[p ? 0 : 1].d, d.row[p ? 0 : 1]), &d.row[p ? 0 : 1], V, base, end, k, {0, &next}, out, smem_addr(tab));
     }
 }
 
@@ -1186,7 +1190,7 @@ struct Pick : Request<kPickThreads> {
         if (total == 0 && !whole) {              // nothing is left: from the target
             whole = true;
             int first = warp;
-            sum_steps(logits_of(dp, p), &s.draw.row[0], V, 0, steps, first, {kWarps, nullptr}, sums, s.tab);
+            sum_steps(logits_of(dp, p), &s.draw.row[0], V, 0, steps, first, {kWarps, nullptr}, sums, smem_addr(s.tab));
             __syncthreads();
             total = take_parts();
         }
