@@ -8,17 +8,17 @@
 //                      weights in fp32.  Rows that no request looks at (a draft's row behind its last draft) are left out.
 //  2. decide_kernel    a block a request: puts the rows' totals together and compares; a comparison nearer than the bound
 //                      of the fp32 sums' error is taken again with sums that are good to 2^-36.  Draws from support rows.
-//  3. sum_kernel       the rows of logits that a request's new token comes from, a step of 512 tokens a warp at a time, every warp of
-//                      the GPU the same number of them whatever the number of requests: of each part of 128 the sums, as integers
+//  3. sum_kernel       the rows of logits that a request's new token comes from, a step of 512 tokens a warp at a time, every
+//                      multiprocessor the same number of them whatever the number of requests: of each part of 128 the sums, as integers
 //                      (float-pair weights, see weights.cuh), of the target's weights, or of what is left, max(p - q, 0), where the
 //                      draft has logits too.
 //  4. pick_kernel      a block a request: adds the parts up, takes a draft's support row off the target's parts, and scans
 //                      the part in which the random number falls.
 //
-// 128 requests of five bf16 rows of 151,936 logits on both sides, 152 us: the pass over 350 MB 62 us (82 % of a copy's rate),
-// the decisions 9, the sums 84 and the tokens 16 by themselves, each kernel's start under the one before.  The
+// 128 requests of five bf16 rows of 151,936 logits on both sides, 149 us: the pass over 350 MB 62 us (82 % of a copy's rate),
+// the decisions 9, the sums 78 and the tokens 16 by themselves, each kernel's start under the one before.  The
 // sums read 78 MB that are mostly in L2; what bounds them is the issue of some 50 instructions a weight (two table look-ups,
-// two polynomials and three sums in pairs of floats for a token), 2.6 of 4 a cycle.  Sums that stay with a request (a
+// two polynomials and three sums in pairs of floats for a token), 2.7 of 4 a cycle.  Sums that stay with a request (a
 // cluster of two to eight blocks for each, which scans its own parts) left multiprocessors without blocks: 160 us, one
 // request 24 us instead of 20, eight 37 instead of 31.
 #include <cfloat>
@@ -1025,7 +1025,9 @@ __global__ void __launch_bounds__(kDecideThreads, 2) decide_kernel(const __grid_
 }
 
 // ---- 3. sums ---------------------------------------------------------------------------------
-// A block takes as many steps as another, its warps one after another as they get done.
+// A block takes as many steps as another, its warps one after another as they get done (with the same number of steps for each warp,
+// 128 requests take 3 us longer: a multiprocessor's warps do not end together).  One block of 1024 threads (64 registers) a
+// multiprocessor; of 768 1 us longer, two of 512 6 us longer.
 __global__ void __launch_bounds__(kSumThreads, kSumBlocks) sum_kernel(const __grid_constant__ VerArgs g) {
     __shared__ float2 tab[2048];
     __shared__ int next;
