@@ -190,10 +190,11 @@ def rl_page_copy(src, dst, k_cache, v_cache, *, tokens=None, status=None, stream
         raise _err("k_cache / v_cache: two tensors [layers, n_pages, Hkv, page_size, D] of one type")
     many = k_cache.dim() == 5
     layers, stride = (shape[0], k_cache.stride(0)) if many else (1, 0)
+    dense = k_cache.is_contiguous() and v_cache.is_contiguous()
     for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
         if not t.is_cuda:
             raise _err(f"{name}: librlhead takes device tensors; got a CPU tensor")
-        if t.is_contiguous() and v_cache.is_contiguous():
+        if dense:
             continue
         one = t[0] if many and layers else t
         if not one.is_contiguous() or (many and layers > 1 and t.stride(0) != stride):

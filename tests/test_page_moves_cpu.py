@@ -109,3 +109,33 @@ def test_binding_refuses_host_tensors_and_shapes():
         rh.rl_page_copy(one, one, cache, cache[:, :, :8])
     with pytest.raises(rh.RLHeadError):
         rh.rl_page_copy(one, one, cache.to(torch.int16), cache.to(torch.int16))
+
+
+class OnDevice:
+    """A host tensor that says it lies on the device (for what the binding looks at before any device work)."""
+    is_cuda = True
+
+    def __init__(self, t):
+        self.t = t
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+    def __getitem__(self, i):
+        return OnDevice(self.t[i])
+
+
+def test_copies_of_caches_with_layers_differently_far_apart(lib):  # noqa: F811
+    """One call knows one distance between layers: a spaced cache beside a dense one is refused, whichever is which."""
+    both = torch.zeros(3, 2, 5, 2, 16, 8, dtype=torch.bfloat16)
+    spaced, dense, wider = both[:, 0], torch.zeros(3, 5, 2, 16, 8, dtype=torch.bfloat16), torch.zeros(3, 3, 5, 2, 16, 8, dtype=torch.bfloat16)[:, 1]
+    none, status = OnDevice(torch.zeros(0, dtype=torch.int32)), OnDevice(torch.zeros(1, dtype=torch.int32))
+
+    def call(k, v):
+        with pytest.raises(rh.RLHeadError) as e:
+            rh.rl_page_copy(none, none, OnDevice(k), OnDevice(v), status=status, stream=type("S", (), {"cuda_stream": 0}))
+        return "dense layers" in str(e.value)
+    assert call(spaced, dense) and call(dense, spaced) and call(spaced, wider)
+    assert call(dense, dense.transpose(3, 4).contiguous().transpose(3, 4))
+    if not torch.cuda.is_available():       # (what is sound gets as far as the missing device)
+        assert not call(dense, dense) and not call(spaced, both[:, 1])
