@@ -185,7 +185,7 @@ RL_DEVINL float2 chunk_of(const T* row, int V, int chunk, float Tm, bool& bad) {
     // e^((z - m) / T) as 2^(z c - fl(m c)): one rounding of the argument; the sum is put right for fl(m c) after
     const float c = kLog2eHi / Tm, pm = m * c;
     float s[4] = {0.f, 0.f, 0.f, 0.f};
-    if (fabsf(pm) < 1e30f) {
+    if (fabsf(pm) < kFusedRef) {
 #pragma unroll
         for (int k = 0; k < kChunkPacks; ++k)
 #pragma unroll

@@ -15,6 +15,9 @@
 namespace rl {
 
 constexpr float kLog2eHi = 1.44269502162933349609f, kLog2eLo = 1.92596299112661746887e-8f;
+// |m c| up to which a sum of 2^(z c - fl(m c)) can be put right by 2^(fl(m c) - m c): half a last place is at most 1/2 there
+// (past 2^31 both factors leave the range of floats, the one upwards and the other down).
+constexpr float kFusedRef = 0x1p24f;
 
 // Entry j: bits of the float nearest 2^(j/2048) less j << 12 (so that adding the phase's bits
 // gives the scaled value), and the relative error of that float.  Made by the compiler, by the

@@ -1,0 +1,66 @@
+"""Verification at the ends of the range: small temperatures, masks of finite size."""
+import numpy as np
+import pytest
+import torch
+
+import lm_head_gb300 as rh  # noqa: F401
+from test_gpu_verify import DT, Half, check
+
+pytestmark = pytest.mark.gpu
+
+
+def rows_case(z, zd, temp, temp_d, seed, likely=0.6):
+    """Requests of three rows; candidates are the largest logits of either side or a token whose p or q does not underflow in the
+    64-bit reference (u q < p of two numbers below that is not its to decide)."""
+    rng = np.random.default_rng(seed)
+    T, V = z.shape
+    step = np.zeros(T, int)
+    for t in range(T):
+        a, b = ((x[t].double() - x[t].double().max()) / float(k[t]) for x, k in ((z, temp), (zd, temp_d)))
+        some = torch.nonzero(torch.maximum(a, b) > -700)[:, 0]
+        x = rng.random()
+        step[(t + 1) % T] = int(a.argmax() if x < likely else b.argmax() if x < likely + 0.15 else some[rng.integers(0, len(some))])
+    f = lambda k: (rng.integers(0, 1 << 24, k) / 2.0 ** 24).astype(np.float32)  # noqa: E731
+    return dict(step=step, cu=np.arange(0, T + 1, 3), u=f(T), un=f(T // 3), V=V, ctx=np.zeros(T // 3, int), target=Half(V, z, temp),
+                draft=Half(V, zd, temp_d))
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "fp16"])
+@pytest.mark.parametrize("T", [1e-5, 3e-7, 3e-8, 1e-8, 3e-9, 1e-9, 1e-10, 1e-12, 1e-20, 1e-33])
+def test_small_temperatures(T, dtype):
+    """Exponents z / T of any size, on either side and on both, over several chunks: rows whose largest logits are apart."""
+    n, V = 24, 4500
+    g = torch.Generator().manual_seed(int(-np.log10(T) * 10))
+    z = (torch.randn(n, V, generator=g) * 6).to(DT[dtype])
+    zd = (z.float() + torch.randn(n, V, generator=g)).to(DT[dtype])
+    for x in (z, zd):           # (no ties)
+        x[torch.arange(n), torch.randint(0, V, (n,), generator=g)] = 40.0
+    small, one = np.full(n, T, np.float32), np.ones(n, np.float32)
+    for a, b in ((small, small), (small, one), (one, small)):
+        check(rows_case(z, zd, a, b, 5))
+        check(dict(rows_case(z, zd, a, b, 6), draft=None))
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("mask", [-6e4, -1e9, -1e10, -1e20, None])
+@pytest.mark.parametrize("T", [1.0, 0.3, 0.1])
+def test_whole_chunks_masked_by_a_finite_number(T, mask, dtype):
+    """Masks of a size between the logits' own and the type's lowest, over more than a chunk's tokens of either side."""
+    least = torch.finfo(DT[dtype]).min
+    mask = least if mask is None else max(mask, least)
+    n, V = 24, 9000
+    g = torch.Generator().manual_seed(3)
+    z = (torch.randn(n, V, generator=g) * 3).to(DT[dtype])
+    zd = (z.float() + 0.7 * torch.randn(n, V, generator=g)).to(DT[dtype])
+    z[:, 2000:6500] = mask
+    z[1::4, :8990] = mask       # all but a few
+    zd[::2, 2040:6400] = mask
+    zd[1::2, 4000:] = mask
+    t = np.full(n, T, np.float32)
+    check(rows_case(z, zd, t, t, 7))
+    check(dict(rows_case(z, zd, t, t, 8), draft=None))
+    ids = [np.array([1, 7, 4000, 5000, 8995])] * n
+    lq = [np.log(np.array([0.1, 0.2, 0.3, 0.3, 0.1])).astype(np.float32)] * n
+    c = rows_case(z, zd, t, t, 9, likely=1.0)       # (a support row gives a token without an entry no probability at all)
+    c["step"][1::3] = 7
+    check(dict(c, draft=Half(V, ids=ids, lq=lq)))
