@@ -381,6 +381,10 @@ RL_DEVINL FF weight_of(float z, const VerRow& w, float ref, float lam_lo, const 
     const FF d = w.plain ? FF{z, 0.f} : two_sum(z, -w.M);
     return weight_off(d.hi, d.lo, w.c, 6144.f - (w.R + ref), lam_lo, tab);
 }
+// Its exponent, as a float.
+RL_DEVINL float exponent_of(float z, const VerRow& w, float ref) {
+    return fmaf(w.plain ? z : two_sum(z, -w.M).hi, w.c.hi, -(w.R + ref));
+}
 // The logit at which the exponent over 2^ref is e.
 RL_DEVINL float logit_of(const VerRow& w, float ref, float e) {
     const float x = (ref + w.R + e) * w.inv_c;
@@ -506,7 +510,7 @@ __device__ __noinline__ unsigned long long sum_steps(const void* logits, const V
         unsigned long long sum = 0;
         if (ex > -100.f) {                       // (also not for -inf: below, the step is nothing beside the row)
             const float ref = fminf(ceilf(ex), 1.f), magic = 6144.f - (w.R + ref);
-            const float zlow = fmaxf(logit_of(w, ref, -64.f), -FLT_MAX);
+            const float zlow = fmaxf(logit_of(w, ref, kLeastExp), -FLT_MAX);
             uint32_t top = 0;
             int low = 0;
 #pragma unroll
@@ -584,8 +588,8 @@ RL_DEVINL void sum_both_of(const void* zp, const VerRow& w, const void* yp, cons
             const float ez = wp ? fmaf(mz, w.c.hi, -w.R) : (mz - w.M) * w.c.hi, ey = op ? fmaf(my, o.c.hi, -o.R) : (my - o.M) * o.c.hi;
             // (below 2^-100 of its row's largest, or -inf, a side is nothing here)
             const float rz = ez > -100.f ? fminf(ceilf(ez), 1.f) : 0.f, ry = ey > -100.f ? fminf(ceilf(ey), 1.f) : 0.f;
-            const float zlow = ez > -100.f ? fmaxf(wp ? (rz + w.R - 64.f) * w.inv_c : w.M + (rz - 64.f) * w.inv_c, -FLT_MAX) : FLT_MAX;
-            const float ylow = ey > -100.f ? fmaxf(op ? (ry + o.R - 64.f) * o.inv_c : o.M + (ry - 64.f) * o.inv_c, -FLT_MAX) : FLT_MAX;
+            const float zlow = ez > -100.f ? fmaxf(wp ? (rz + w.R + kLeastExp) * w.inv_c : w.M + (rz + kLeastExp) * w.inv_c, -FLT_MAX) : FLT_MAX;
+            const float ylow = ey > -100.f ? fmaxf(op ? (ry + o.R + kLeastExp) * o.inv_c : o.M + (ry + kLeastExp) * o.inv_c, -FLT_MAX) : FLT_MAX;
             const float magic_z = 6144.f - (w.R + rz), magic_y = 6144.f - (o.R + ry + lam.hi);
             const float scale = power_of_2(min(max(static_cast<int>(ry - rz) - lam.whole, -126), 100));
             LongSum sp, sq;
@@ -1076,13 +1080,14 @@ struct Pick : Request<kPickThreads> {
     RL_DEVINL unsigned long long left_at(float z, float y, int j, bool whole, int& bits) {
         const VerRow& p = s.draw.row[0];
         const VerRow& q = s.draw.row[1];
-        const float zlow = fmaxf(logit_of(p, 0.f, -64.f), -FLT_MAX);
-        if (!(z >= zlow)) return 0ull;
+        // (by exponents: where the logits' spacing is worth several of them, their bounds as logits would be rounded past a logit)
+        if (!(exponent_of(z, p, 0.f) >= kLeastExp)) return 0ull;
         FF v = weight_of(z, p, 0.f, 0.f, s.tab);
         if (!whole && q.mode == kDistDense) {
             const float lam_hi = rintf(s.lam.hi * 2048.f) * (1.f / 2048.f), lam_lo = (s.lam.hi - lam_hi) + s.lam.lo;
-            const float ylow = fmaxf(logit_of(q, lam_hi, -64.f), -FLT_MAX), yhigh = logit_of(q, lam_hi, 0.75f);
-            if (y >= ylow) v = ordered(left_of(v, weight_of(fminf(y, yhigh), q, lam_hi, lam_lo, s.tab)));
+            const float e = exponent_of(y, q, lam_hi);
+            if (e > 0.75f) return 0ull;          // (the target's weight is at most 1)
+            if (e >= kLeastExp) v = ordered(left_of(v, weight_of(y, q, lam_hi, lam_lo, s.tab)));
             return fixed_of(v.hi, v.lo, p.prec);
         }
         const unsigned long long w = fixed_of(v.hi, v.lo, p.prec);

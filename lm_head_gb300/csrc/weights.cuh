@@ -78,7 +78,11 @@ RL_DEVINL float max_nan(float a, float b) {           // NaN if either is
 RL_DEVINL void fill_table(float2* tab, int tid, int threads) {
     for (int j = tid; j < 2048; j += threads) tab[j] = make_float2(__uint_as_float(kExpTable.bits[j]), kExpTable.rho[j]);
 }
-// 2^(x c - ref) as hi + v, for x c - ref in [-66, 1] and magic = 6144 - ref: the last place of
+// Weights of lower exponents count as 0.  As a bound of logits, M + kLeastExp / c, it is rounded to a float: where the logits' spacing is as
+// large as the bound's distance, the last of them that passes has an exponent of -(62 + spacing c / 2), and no spacing c
+// above 124 lets any pass.  So weights' exponents stay above -126, where the addition to a float's exponent is sound.
+constexpr float kLeastExp = -62.f;
+// 2^(x c - ref) as hi + v, for x c - ref in [-126, 1] and magic = 6144 - ref: the last place of
 // 6144 + y is 2^-11, so the bits of t are 0x45C00000 + 2048 n + j for the nearest n + j/2048, and
 // what is left of x c, r, comes from one more product.  (x + x_lo for an argument of two floats.)
 RL_DEVINL void weight_pair(float x, float x_lo, FF c, float magic, const float2* tab, float& hi, float& v) {

@@ -64,3 +64,48 @@ def test_whole_chunks_masked_by_a_finite_number(T, mask, dtype):
     c = rows_case(z, zd, t, t, 9, likely=1.0)       # (a support row gives a token without an entry no probability at all)
     c["step"][1::3] = 7
     check(dict(c, draft=Half(V, ids=ids, lq=lq)))
+
+
+SPACING = [0.9, 1.6, 5, 15, 40, 90, 110, 123, 125, 126.5, 127.2, 127.5, 127.9, 128.5, 200]
+
+
+@pytest.mark.parametrize("M", [20.0, 3.0])
+@pytest.mark.parametrize("steps", SPACING)
+def test_temperatures_at_which_one_float_is_many_powers_of_two(steps, M):
+    """T such that two floats next to each other near the largest logit have weights 2^-steps apart; a float below the largest on
+    either side, twice and in every part."""
+    n, V = 24, 700
+    T = np.float32(np.log2(np.e) * float(np.spacing(np.float32(M))) / steps)
+    rng = np.random.default_rng(int(steps * 10))
+    z, zd = torch.full((n, V), -5.0), torch.full((n, V), -5.0)
+    for t in range(n):
+        for x in (z, zd):
+            x[t, 50::90] = float(np.nextafter(np.float32(M), np.float32(0)))
+            x[t, 51::90] = float(np.nextafter(np.nextafter(np.float32(M), np.float32(0)), np.float32(0)))
+            x[t, rng.integers(0, V)] = M
+    small, one = np.full(n, T, np.float32), np.ones(n, np.float32)
+    for a, b in ((small, small), (small, one), (one, small)):
+        check(rows_case(z, zd, a, b, 5), skips=4)
+        check(dict(rows_case(z, zd, a, b, 6), draft=None), skips=4)
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("steps", SPACING)
+def test_ties_beside_a_sure_draft_at_small_temperatures(steps, dtype):
+    """The target's largest logit many times, the draft's once among them: the token is not the draft's, and those after it
+    in its part of the row are where they belong."""
+    R, V, ties = 32, 1500, 1024
+    T = np.float32(np.log2(np.e) * float(np.spacing(np.float32(20.0))) / steps)
+    z, zd = torch.full((2 * R, V), -5.0), torch.full((2 * R, V), -5.0)
+    z[:, :ties] = 20.0
+    step, un = np.zeros(2 * R, int), np.zeros(R, np.float32)
+    for r in range(R):
+        x = 128 * (r % 8) + 5 + r
+        zd[2 * r, x] = 20.0
+        step[2 * r + 1] = x
+        un[r] = (128 * (r % 8) + 60.3 + r) / (ties - 1)
+    small = np.full(2 * R, T, np.float32)
+    c = dict(step=step, cu=np.arange(0, 2 * R + 1, 2), u=np.full(2 * R, 0.5, np.float32), un=un, V=V, ctx=np.zeros(R, int),
+             target=Half(V, z.to(DT[dtype]), small), draft=Half(V, zd.to(DT[dtype]), small))
+    check(c)
+    check(dict(c, draft=Half(V, zd.to(DT[dtype]), np.ones(2 * R, np.float32))))
