@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(kStatThreads, 2) stats_kernel(const SampleArgs
             const FF cs = scale_of(q.T);
             const float pm = m * cs.hi;
             if (fabsf(pm) < kWholeRef) {
-                const float ref = ceilf(pm), magic = 6144.f - ref, zlow = fmaxf((ref - 64.f) / cs.hi, -FLT_MAX);
+                const float ref = ceilf(pm), magic = 6144.f - ref, zlow = fmaxf((ref + kLeastExp) / cs.hi, -FLT_MAX);
                 ref_out = static_cast<int>(ref);
 #pragma unroll
                 for (int s = 0; s < kSubs; ++s) {
@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(kStatThreads, 2) stats_kernel(const SampleArgs
                     }
                 }
             } else {
-                const float zlow = fmaxf(m - 64.f / cs.hi, -FLT_MAX);
+                const float zlow = fmaxf(m + kLeastExp / cs.hi, -FLT_MAX);
                 ref_out = INT_MIN;
 #pragma unroll
                 for (int s = 0; s < kSubs; ++s) {
@@ -940,7 +940,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SampleArgs
             for (int i = tid; i < g.ns; i += kSelThreads) g.cpre[r * g.ns + i] = i > at / kSub ? 1 : 0;
     } else {
         w.c = scale_of(q.T);
-        w.zlow = fmaxf(M - 64.f / w.c.hi, -FLT_MAX);
+        w.zlow = fmaxf(M + kLeastExp / w.c.hi, -FLT_MAX);
         // the least logit whose weight is at least min_p and 2^-100: M + T ln(...), rounded up
         if (tid == 0) {
             FF lim = q.mp > 0.f ? ln_pair({fmaxf(q.mp, 7.888609e-31f), 0.f}) : FF{-69.31472016f, 1.5413417e-06f};

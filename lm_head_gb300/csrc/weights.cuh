@@ -115,7 +115,7 @@ struct LaneSum {
         return w > 0 ? static_cast<unsigned long long>(w) : 0ull;
     }
 };
-// The weight of z relative to M in units of 2^-k; `zlow` = M - 64 / c, at least
+// The weight of z relative to M in units of 2^-k; `zlow` = M + kLeastExp / c, at least
 // -FLT_MAX: below it the weight is 0 (M itself where the difference is lost).
 RL_DEVINL unsigned long long weight_fixed(float z, float M, FF c, float zlow, int k, const float2* tab) {
     if (!(z >= zlow)) return 0ull;
