@@ -765,7 +765,8 @@ struct Request {
             const float z = logit_at(g.side[side].d, x.dtype, x.row, j);
             if (!(z > -INFINITY)) return -INFINITY;
             const FF d = two_sum(z, -x.M);
-            return fmaf(d.hi, x.c.hi, fmaf(d.lo, x.c.hi, d.hi * x.c.lo)) - log2f(x.S);
+            const float e = fmaf(d.hi, x.c.hi, fmaf(d.lo, x.c.hi, d.hi * x.c.lo));
+            return e > -INFINITY ? e - log2f(x.S) : -INFINITY;       // (a product past the range of floats, or two of them: NaN)
         }
         return support_at(side, x, j, bits) * kLog2e;
     }
@@ -803,7 +804,7 @@ struct Request {
         if (x.mode == kDistPoint) return {j == x.at ? 1.f : 0.f, 0.f};
         if (x.mode == kDistDense) {
             const float z = logit_at(g.side[1].d, x.dtype, x.row, j);
-            if (!(z > -INFINITY)) return {0.f, 0.f};
+            if (!(exponent_of(z, x, 0.f) > -200.f)) return {0.f, 0.f};       // (-inf, or a product past the range of floats)
             const FF d = x.plain ? FF{z, 0.f} : two_sum(z, -x.M);
             // e = d c - R in log2 units, then to natural ones less the total's log
             FF e = ff_add(ff_mul(d, x.c), {-x.R, 0.f});

@@ -109,3 +109,26 @@ def test_ties_beside_a_sure_draft_at_small_temperatures(steps, dtype):
              target=Half(V, z.to(DT[dtype]), small), draft=Half(V, zd.to(DT[dtype]), small))
     check(c)
     check(dict(c, draft=Half(V, zd.to(DT[dtype]), np.ones(2 * R, np.float32))))
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("T", [3.0, 1.0, 0.7, 0.1, 1e-6])
+def test_support_rows_beside_drafts_masked_by_the_lowest_number(T, dtype):
+    """Tokens of the target's support row whose draft logits are the type's lowest number have no probability in the draft, whatever
+    the temperature makes of the number: all of the target's is left."""
+    R, V = 32, 3000
+    g = torch.Generator().manual_seed(4)
+    zd = (torch.randn(2 * R, V, generator=g) * 3).to(DT[dtype])
+    ids = [np.array([1, 7, 700, 1500, 2995])] * (2 * R)
+    lq = [np.log(np.array([0.1, 0.2, 0.3, 0.3, 0.1])).astype(np.float32)] * (2 * R)
+    step = np.zeros(2 * R, int)
+    for r in range(R):
+        zd[2 * r, [1, 700, 2995]] = torch.finfo(DT[dtype]).min
+        zd[2 * r, 7] = 400.0                # what the draft gives, more often than the target
+        step[2 * r + 1] = 7
+    un = ((np.arange(R) + 0.5) / R).astype(np.float32)
+    temp = np.full(2 * R, T, np.float32)
+    c = dict(step=step, cu=np.arange(0, 2 * R + 1, 2), u=np.full(2 * R, 0.9, np.float32), un=un, V=V, ctx=np.zeros(R, int),
+             target=Half(V, ids=ids, lq=lq), draft=Half(V, zd, temp))
+    ref, _ = check(c)
+    assert set(ref["tokens"][::2]) == {1, 700, 1500, 2995}
