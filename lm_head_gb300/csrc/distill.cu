@@ -351,7 +351,7 @@ __global__ void __launch_bounds__(NT, kBlocks) distill_kernel(const __grid_const
             }
             return warp_sum((sum[0] + sum[1]) + (sum[2] + sum[3]));
         };
-        bool far = !(fabsf(m * p.c) < 1e30f);
+        bool far = !(fabsf(m * p.c) < kFusedRef);
         if (!far) {
             t = add(m * p.c);
             far = !(t < 1e30f && t > 1e-25f);
@@ -364,7 +364,7 @@ __global__ void __launch_bounds__(NT, kBlocks) distill_kernel(const __grid_const
                 m = fmaxf(m, v.largest());
             }
             m = warp_largest(m);
-            if (fabsf(m * p.c) < 1e30f) {
+            if (fabsf(m * p.c) < kFusedRef) {
                 t = add(m * p.c);
             } else {
                 const float mc = m > -INFINITY ? m : 0.f;
@@ -375,7 +375,7 @@ __global__ void __launch_bounds__(NT, kBlocks) distill_kernel(const __grid_const
                 t = warp_sum(sum[0]);
             }
         }
-        if (fabsf(m * p.c) < 1e30f) t *= exp2f(-fmaf(m, p.c, -(m * p.c)));
+        if (fabsf(m * p.c) < kFusedRef) t *= exp2f(-fmaf(m, p.c, -(m * p.c)));
         if (lane == 0) s.part[warp] = make_float2(m, t);
     }
     // (reference, sum) of n parts, a lane each (a sum without a reference is 0 or NaN)
@@ -507,7 +507,7 @@ __global__ void __launch_bounds__(NT, kBlocks) distill_kernel(const __grid_const
         for (int k = tid; k < packs; k += NT) *reinterpret_cast<uint4*>(buf + k * E) = make_uint4(0, 0, 0, 0);
     } else {
         const float kr = w * inv_T * k_rest, pm = M * p.c;
-        if (fabsf(pm) < 1e30f) {
+        if (fabsf(pm) < kFusedRef) {
             const float k2 = kr * exp2f(-fmaf(M, p.c, -pm));
             for (int k = tid; k < packs; k += NT) {
                 Pack<T> v;
@@ -695,7 +695,7 @@ __global__ void __launch_bounds__(kBwdThreads) distill_bwd_kernel(const DistArgs
     const float k = zero ? 0.f : w * rest;
     // one rounding of the argument, as in the pass over the logits
     const float pm = M * p.c;
-    const bool fused = fabsf(pm) < 1e30f;
+    const bool fused = fabsf(pm) < kFusedRef;
     const float k2 = fused ? k * exp2f(-fmaf(M, p.c, -pm)) : k;
     auto grad = [&](float x) -> float { return k == 0.f ? 0.f : fused ? k2 * exp2_approx(fmaf(x, p.c, -pm)) : k * exp2_approx((x - M) * p.c); };
     for (int i = i0 + tid; i < b0; i += kBwdThreads) d[i] = from_f32<T>(grad(to_f32(z[i])));

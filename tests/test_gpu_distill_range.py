@@ -1,0 +1,52 @@
+"""Distillation at the ends of the range: finite masks, small temperatures, probabilities that underflow."""
+import numpy as np
+import pytest
+import torch
+
+import lm_head_gb300 as rh
+from test_gpu_distill import DT, KINDS, check, make
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("kind,tail", KINDS)
+@pytest.mark.parametrize("dtype,V", [("fp32", 5003), ("bf16", 5003), ("fp32", 151936), ("bf16", 151936)])
+@pytest.mark.parametrize("mask", [-1e9, -1e10, -1e20, None])
+def test_rows_masked_by_a_finite_number(kind, tail, dtype, V, mask):
+    """All but a few tokens masked, whole slices of a row among them, with and without a token of the rest that is not."""
+    N = 6
+    mask = torch.finfo(DT[dtype]).min if mask is None else mask
+    for T in (1.0, 0.3):
+        c = make(N, V, dtype, np.array([5, 9, 3, 70, 8, 2]), T, tail, seed=3)
+        off, ids = c["off"].tolist(), c["ids"].long()
+        for r in range(N):
+            keep = torch.zeros(V, dtype=torch.bool, device="cuda")
+            keep[ids[off[r]:off[r + 1]]] = True
+            if r % 3:
+                keep[[11, V // 2]] = True
+            if r == 4:
+                keep[:V // 3] = True
+            c["z"][r][~keep] = mask
+        check(c, rh.DistillParams(kind=kind, tail=tail, temperature=T, beta=0.4), dtype)
+
+
+@pytest.mark.parametrize("kind,tail", KINDS)
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("scale,T", [(1e4, 2.0 ** -20), (30.0, 2.0 ** -20), (1e10, 1.0), (3e6, 0.25)])
+def test_exponents_of_any_size(kind, tail, dtype, scale, T):
+    """Logits over the temperature from 2^24 to 2^34, the largest in the support and outside it, alone and several times."""
+    N, V = 8, 3001
+    c = make(N, V, dtype, np.array([5, 9, 3, 70, 8, 2, 4, 6]), 1.0, tail, seed=5, scale=1.0)
+    off, ids = c["off"].tolist(), c["ids"].long()
+    c["z"].mul_(scale)
+    for r in range(N):
+        top = c["z"][r].float().max() * 1.25
+        S = ids[off[r]:off[r + 1]]
+        other = [j for j in (100, 2000, 2999, 17, 18) if j not in S.tolist()]
+        if r % 4 < 2:
+            c["z"][r, S[0]] = top.to(DT[dtype])
+        if r % 4 == 1:
+            c["z"][r, S[1]] = top.to(DT[dtype])
+        if r % 4:
+            c["z"][r, other[:r % 4]] = top.to(DT[dtype])
+    check(c, rh.DistillParams(kind=kind, tail=tail, temperature=T, beta=0.4), dtype)
