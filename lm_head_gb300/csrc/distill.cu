@@ -220,8 +220,8 @@ RL_DEVINL float slope_of(int kind, float beta, float t, float lt, float P, float
     if (kind == RL_DISTILL_FORWARD) return -t;
     if (lp == -INFINITY) return 0.f;
     if (kind == RL_DISTILL_REVERSE) return P * (lp - lt);
-    const float a = 1.f - beta;
-    return a * P * (lp - logf(fmaf(beta, t, a * P)));
+    const float a = 1.f - beta, m = fmaf(beta, t, a * P);
+    return m != 0.f ? a * P * (lp - logf(m)) : 0.f;          // (both of them underflow: NaN goes on)
 }
 // Sum of v over the first n warps' threads (they alone call it), as a pair in every lane.
 RL_DEVINL FF support_sum(FF* part, FF v, int n) {

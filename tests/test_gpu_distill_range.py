@@ -50,3 +50,26 @@ def test_exponents_of_any_size(kind, tail, dtype, scale, T):
         if r % 4:
             c["z"][r, other[:r % 4]] = top.to(DT[dtype])
     check(c, rh.DistillParams(kind=kind, tail=tail, temperature=T, beta=0.4), dtype)
+
+
+@pytest.mark.parametrize("kind,tail", KINDS)
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("beta", [0.4, 0.999])
+def test_tokens_that_neither_side_gives(kind, tail, dtype, beta):
+    """Entries of the support whose probabilities underflow on both sides, on one of them, and rows of little else."""
+    N, V = 6, 2000
+    c = make(N, V, dtype, np.array([6, 6, 6, 6, 300, 6]), 1.0, tail, seed=8)
+    off, ids = c["off"].tolist(), c["ids"].long()
+    for r in range(N):
+        S = ids[off[r]:off[r + 1]]
+        q = c["q"][off[r]:off[r + 1]]
+        if r == 4:
+            # (above the 64-bit reference's own underflow)
+            q[10:] = torch.linspace(-110, -650, len(S) - 10).cuda()
+            c["z"][r, S[10:]] = torch.linspace(-650, -130, len(S) - 10).cuda().to(DT[dtype])
+            continue
+        c["z"][r, S[1]] = -130.0
+        q[1] = (-120.0, -1e4, -106.0, -3e4, 0, -104.5)[r]
+        c["z"][r, S[2]] = -1e4
+        q[3] = -150.0
+    check(c, rh.DistillParams(kind=kind, tail=tail, beta=beta), dtype)
