@@ -158,10 +158,13 @@ RL_DEVINL FF exp_table(FF x) {
 }
 // ln x of a positive pair, likewise: one Newton step from the float's.
 RL_DEVINL FF ln_table(FF x) {
+    const bool small = x.hi < 0x1p-64f;                  // (1 / x is to be a float, and subnormal ones hold fewer bits)
+    if (small) x = {x.hi * 0x1p100f, x.lo * 0x1p100f};
     const float y = logf(x.hi);
     const FF r = ff_mul(x, exp_table({-y, 0.f}));        // 1 + d
     const float d = __fadd_rn(__fsub_rn(r.hi, 1.f), r.lo);
-    return fast_two_sum(y, fmaf(-0.5f * d, d, d));
+    const FF l = fast_two_sum(y, fmaf(-0.5f * d, d, d));
+    return small ? ff_add(l, {-69.31472015380859375f, 2.0978141e-06f}) : l;      // - 100 ln 2
 }
 
 }  // namespace rl

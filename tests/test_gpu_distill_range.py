@@ -73,3 +73,18 @@ def test_tokens_that_neither_side_gives(kind, tail, dtype, beta):
         c["z"][r, S[2]] = -1e4
         q[3] = -150.0
     check(c, rh.DistillParams(kind=kind, tail=tail, beta=beta), dtype)
+
+
+@pytest.mark.parametrize("kind", ["forward", "reverse", "jsd"])
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_probabilities_next_to_the_least_float(kind, dtype):
+    """Entries whose student's probability is subnormal while their weight relative to the row's largest is not, beside a teacher's
+    probability of the same size and of none."""
+    N, V = 8, 3000
+    c = make(N, V, dtype, np.full(N, 40), 1.0, True, seed=9, scale=0.1)
+    off, ids = c["off"].tolist(), c["ids"].long()
+    for r in range(N):
+        S = ids[off[r]:off[r + 1]]
+        c["z"][r, S[5:35]] = torch.linspace(-86.5, -78, 30).cuda().to(DT[dtype])
+        c["q"][off[r] + 5:off[r] + 35] = torch.linspace(-80, -95, 30).cuda() if r % 2 else -200.0
+    check(c, rh.DistillParams(kind=kind, tail=True, beta=0.3), dtype)
