@@ -825,7 +825,8 @@ int rl_page_copy(const rl_page_copy_args* args, int32_t* dev_status, void* strea
  * dlogits = dloss dL/dz in the logits' type.  The outcomes are summed in pairs of floats, the rest's probability is
  * a sum over its tokens (no 1 - sum), exponentials of the rest are fp32.
  * A row without a support (no entry, or none with logq > -inf) has loss 0 and gradient 0, whatever its logits;
- * a row with dloss 0 has gradient 0.  -inf logits have P = 0: where the forward kind's teacher wants such a token
+ * a row with dloss 0 has gradient 0.  -inf logits have P = 0, as have those that lie more than 3.4e38 T below the
+ * row's largest: where the forward kind's teacher wants such a token
  * the loss is inf.  NaN and +inf logits, and a row of -inf alone, make the row's loss not finite; a loss that is not finite sets
  * RL_STATUS_NONFINITE.
  * Checked on the device: row bounds (RL_STATUS_OFFSETS, the row then has no support), ids in [0, V) and logq not NaN,

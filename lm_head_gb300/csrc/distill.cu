@@ -605,7 +605,10 @@ __global__ void __launch_bounds__(kLossThreads) distill_loss_kernel(const __grid
         return;
     }
     const float M = sv.M[row], rest = sv.sum[row];
-    auto scaled = [&](float v, float m) -> FF { return v == -INFINITY ? FF{-INFINITY, 0.f} : ff_mul(two_sum(v, -m), p.inv_t); };
+    // (v - m) / T; past the range of floats (the type's lowest number at T < 1, say) it is -inf, which pairs do not carry through
+    auto scaled = [&](float v, float m) -> FF {
+        return (v - m) * p.inv_t.hi == -INFINITY ? FF{-INFINITY, 0.f} : ff_mul(two_sum(v, -m), p.inv_t);
+    };
     // f(entry, W, Q) with the weights of the student's and the teacher's softmax; the thread's first stay in registers
     FF W1 = {0.f, 0.f}, Q1 = {0.f, 0.f};
     auto each = [&](bool again, auto f) {

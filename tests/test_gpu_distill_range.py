@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import lm_head_gb300 as rh
-from test_gpu_distill import DT, KINDS, check, make
+from test_gpu_distill import DT, KINDS, NONFINITE, check, make
 
 pytestmark = pytest.mark.gpu
 
@@ -88,3 +88,25 @@ def test_probabilities_next_to_the_least_float(kind, dtype):
         c["z"][r, S[5:35]] = torch.linspace(-86.5, -78, 30).cuda().to(DT[dtype])
         c["q"][off[r] + 5:off[r] + 35] = torch.linspace(-80, -95, 30).cuda() if r % 2 else -200.0
     check(c, rh.DistillParams(kind=kind, tail=True, beta=0.3), dtype)
+
+
+@pytest.mark.parametrize("kind,tail", KINDS)
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("T", [0.7, 2.0 ** -20])
+def test_support_tokens_masked_by_the_lowest_number(kind, tail, dtype, T):
+    """The quotient of the type's lowest number and T is no float: the token has no probability, as one of -inf."""
+    N, V = 5, 1500
+    c = make(N, V, dtype, np.full(N, 8), 1.0, tail, seed=7)       # (every token of it wanted)
+    off, ids = c["off"].tolist(), c["ids"].long()
+    low = c["z"].clone()
+    for r in range(N):
+        c["z"][r, ids[off[r] + r]] = torch.finfo(DT[dtype]).min
+        low[r, ids[off[r] + r]] = float("-inf")
+    p = rh.DistillParams(kind=kind, tail=tail, temperature=T, beta=0.4)
+    if kind != "forward":       # (there the loss is of that size, or inf)
+        check(c, p, dtype)
+    args = (c["off"], c["ids"], c["q"], c["dl"], p)
+    o, d = rh.rl_distill_fwd_bwd(c["z"], *args)
+    want, wd = rh.rl_distill_fwd_bwd(low, *args)
+    assert torch.equal(o.loss, want.loss) and torch.equal(o.mass, want.mass) and torch.equal(d, wd)
+    assert o.status_bits() == want.status_bits() == (NONFINITE if kind == "forward" else 0)
