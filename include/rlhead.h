@@ -818,7 +818,8 @@ int rl_page_copy(const rl_page_copy_args* args, int32_t* dev_status, void* strea
  *              loss = sum_S p ln(p / P); kind RL_DISTILL_FORWARD only
  *   tail = 1   p = exp(logq) on S (the teacher's log-probabilities at its own temperature), and the rest of the
  *              vocabulary is one more outcome, of p_0 = max(1 - sum_S p, 2^-20) and P_0 = sum of P outside S
- *              (left out where P_0 is 0); loss = sum over S and the rest of
+ *              (left out where all logits outside S are -inf or more than 745 T below the row's largest, where P_0
+ *              is 0 in 64 bits too); loss = sum over S and the rest of
  *     RL_DISTILL_FORWARD  p ln(p / P)
  *     RL_DISTILL_REVERSE  P ln(P / p)
  *     RL_DISTILL_JSD      beta p ln(p / m) + (1 - beta) P ln(P / m),  m = beta p + (1 - beta) P

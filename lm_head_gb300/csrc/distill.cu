@@ -39,6 +39,7 @@ namespace rl {
 
 constexpr int kDistWarps = 8;                   // most of a block
 constexpr float kMinTail = 0x1p-20f;            // what fp32 log-probabilities leave certain of a teacher's rest
+constexpr float kRestGone = -745.f;             // ln of a ratio to the row's largest weight below which the rest is no outcome (0 in 64 bits)
 
 struct DistArgs {
     rl_distill_args a;
@@ -54,15 +55,17 @@ struct DistArgs {
 // What the pass over the logits leaves for the loss and for the backward.
 struct DistSaved {
     float* M;              // [N] the row's reference logit
-    float* sum;            // [N] sum of e^((z - M) / T) outside the support
+    float* ref;            // [N] the reference logit of what is outside the support (-inf: nothing is)
+    float* sum;            // [N] sum of e^((z - ref) / T) there
     float* z;              // [nnz] the support's logits
-    float* rest;           // [N] d L / d z of a token outside the support over its exp((z - M) / T)
+    float* rest;           // [N] d L / d z of a token outside the support over its exp((z - ref) / T)
     float* entry;          // [nnz] d L / d z of the support's entries
 };
 static DistSaved dist_saved(void* base, int64_t N, int64_t nnz, size_t* bytes) {
     Carve c(base);
     DistSaved s;
     s.M = c.take<float>(static_cast<size_t>(N));
+    s.ref = c.take<float>(static_cast<size_t>(N));
     s.sum = c.take<float>(static_cast<size_t>(N));
     s.z = c.take<float>(static_cast<size_t>(nnz));
     s.rest = c.take<float>(static_cast<size_t>(N));
@@ -146,9 +149,9 @@ struct DistShared {              // (small: three blocks with slices of 76 KB ar
     float2 part[kDistWarps];     // of each warp of this block
     float4 sup[kDistWarps];      // of each support warp: largest logit, largest of the teacher's, sums relative to the block's largest
     FF sum[kDistWarps];          // pairs to be added up over the support warps
-    float t0;                    // the teacher's probability of the rest
     float A[kDistWarps];
-    float M, rest, inv_total;
+    float rest_ref, rest_sum;    // of the rest: reference logit, sum relative to it,
+    float unit, x0;              // the probability of a weight of 1 in the sum, and P g
 };
 
 // v into another block's `to`, counted by its barrier `bar` (both given by this block's own addresses).
@@ -379,15 +382,15 @@ __global__ void __launch_bounds__(NT, kBlocks) distill_kernel(const __grid_const
         if (lane == 0) s.part[warp] = make_float2(m, t);
     }
     // (reference, sum) of n parts, a lane each (a sum without a reference is 0 or NaN)
-    auto join = [&](const float2* v, int parts, float from) -> float2 {
+    auto join = [&](const float2* v, int parts) -> float2 {
         const float2 x = lane < parts ? v[lane] : make_float2(-INFINITY, 0.f);
-        const float m = fmaxf(from, warp_largest(x.x));
+        const float m = warp_largest(x.x);
         return make_float2(m, warp_sum(x.x > -INFINITY ? x.y * exp2f((x.x - m) * p.c) : x.y));
     };
     __syncthreads();
     cluster_wait();
     if (warp == 0) {
-        const float2 v = join(s.part, kWarps, -INFINITY);
+        const float2 v = join(s.part, kWarps);
         if (lane < p.cs) cluster_send(v, &s.xpart[rank], &s.xbar, lane);
     }
     // (while the parts are on their way) the support's sums, of the student's weights and of the teacher's
@@ -407,6 +410,8 @@ __global__ void __launch_bounds__(NT, kBlocks) distill_kernel(const __grid_const
     }
     if (!mbar_wait(&s.xbar, 0, p.status, p.wait_ns)) mbar_wait(&s.xbar, 0, p.status);
     // ---- the outcomes
+    // The rest stays relative to its own reference: its probability may underflow, and its share of the gradient not (the
+    // forward kind's teacher wants t0 of it, however little the student gives).
     const float inv_T = p.inv_t.hi;
     float M = 0.f, total = 1.f, inv_total = 1.f, lnT = 0.f, sT = 1.f, inv_sT = 1.f, lnW = 0.f;
     // P g of an entry, and P
@@ -425,9 +430,9 @@ __global__ void __launch_bounds__(NT, kBlocks) distill_kernel(const __grid_const
     };
     float P1 = 0.f, g1 = 0.f;                    // of the first entry
     if (mine) {
-        const float2 v = join(s.xpart, p.cs, mS);
-        M = v.x;
-        const float rest = v.y;
+        const float2 v = join(s.xpart, p.cs);
+        M = fmaxf(v.x, mS);
+        const float scale = v.y != 0.f ? exp2f((v.x - M) * p.c) : 0.f, rest = v.y * scale;
         float held = 0.f;
         sT = 0.f;
         for (int k = 0; k < nw; ++k) {
@@ -455,31 +460,30 @@ __global__ void __launch_bounds__(NT, kBlocks) distill_kernel(const __grid_const
         A = warp_sum(A);
         if (lane == 0) s.A[warp] = A;
         if (tid == 0) {
-            s.M = M;
-            s.rest = rest;
-            s.inv_total = inv_total;
-            if (a.tail) s.t0 = rest_of(wT).hi;
+            s.rest_ref = v.x;
+            s.rest_sum = v.y;
+            s.unit = scale * inv_total;
+            const float far = (v.x - M) * inv_T;
+            s.x0 = 0.f;
+            if (a.tail && v.y != 0.f && !(far < kRestGone)) {
+                const float t0 = rest_of(wT).hi;
+                s.x0 = slope_of(a.kind, a.beta, t0, logf(t0), rest * inv_total, far + logf(v.y) - lnT);
+            }
             if (rank == 0) {
                 sv.M[row] = M;
-                sv.sum[row] = rest;
+                sv.ref[row] = v.x;
+                sv.sum[row] = v.y;
             }
         }
     }
     __syncthreads();
-    M = s.M;
-    inv_total = s.inv_total;
-    const float rest = s.rest;
-    // the gradient's factor outside the support (over the softmax's denominator, times T), and A
+    // the gradient's factor outside the support (over a weight of the sum, times T), and A
+    const float ref = s.rest_ref, sum = s.rest_sum;
     float k_rest = 0.f, A = 0.f;
     if (any) {
         for (int k = 0; k < nw; ++k) A += s.A[k];
-        float g0 = 0.f;
-        if (a.tail && !(rest <= 0.f)) {
-            const float t0 = s.t0, P0 = rest * inv_total, x = slope_of(a.kind, a.beta, t0, logf(t0), P0, logf(P0));
-            A += x;
-            g0 = x / P0;
-        }
-        k_rest = (g0 - A) * inv_total;
+        A += s.x0;
+        if (sum != 0.f) k_rest = s.x0 / sum - A * s.unit;
     }
     if (!listed) {                               // (in place: its logits are read again until here)
         __syncthreads();
@@ -503,12 +507,13 @@ __global__ void __launch_bounds__(NT, kBlocks) distill_kernel(const __grid_const
         return;
     }
     // ---- the gradient, in place
-    if (!any || w == 0.f) {
+    const bool zero = !any || w == 0.f;
+    if (zero || k_rest == 0.f) {
         for (int k = tid; k < packs; k += NT) *reinterpret_cast<uint4*>(buf + k * E) = make_uint4(0, 0, 0, 0);
     } else {
-        const float kr = w * inv_T * k_rest, pm = M * p.c;
+        const float kr = w * inv_T * k_rest, pm = ref * p.c;
         if (fabsf(pm) < kFusedRef) {
-            const float k2 = kr * exp2f(-fmaf(M, p.c, -pm));
+            const float k2 = kr * exp2f(-fmaf(ref, p.c, -pm));
             for (int k = tid; k < packs; k += NT) {
                 Pack<T> v;
                 v.load(buf + k * E);
@@ -524,11 +529,13 @@ __global__ void __launch_bounds__(NT, kBlocks) distill_kernel(const __grid_const
                 v.load(buf + k * E);
                 float d[E];
 #pragma unroll
-                for (int j = 0; j < E; ++j) d[j] = kr * exp2_approx((to_f32(v.t[j]) - M) * p.c);
+                for (int j = 0; j < E; ++j) d[j] = kr * exp2_approx((to_f32(v.t[j]) - ref) * p.c);
                 v.put(d);
                 v.store(buf + k * E);
             }
         }
+    }
+    if (!zero) {
         __syncthreads();
         if (mine)
             each([&](const Entry& x, bool is_first, long long) {
@@ -604,7 +611,7 @@ __global__ void __launch_bounds__(kLossThreads) distill_loss_kernel(const __grid
         }
         return;
     }
-    const float M = sv.M[row], rest = sv.sum[row];
+    const float M = sv.M[row], ref = sv.ref[row], rest = sv.sum[row];
     // (v - m) / T; past the range of floats (the type's lowest number at T < 1, say) it is -inf, which pairs do not carry through
     auto scaled = [&](float v, float m) -> FF {
         return (v - m) * p.inv_t.hi == -INFINITY ? FF{-INFINITY, 0.f} : ff_mul(two_sum(v, -m), p.inv_t);
@@ -637,7 +644,9 @@ __global__ void __launch_bounds__(kLossThreads) distill_loss_kernel(const __grid
     });
     wS = support_sum(part[0], wS, nw);
     wQ = support_sum(part[1], wQ, nw);
-    const FF sum = ff_add({rest, 0.f}, wS), t0 = a.tail ? rest_of(wQ) : FF{1.f, 0.f};
+    // the rest's sum, relative to the row's reference
+    const FF far = rest != 0.f ? scaled(ref, M) : FF{-INFINITY, 0.f}, wR = rest != 0.f ? ff_mul({rest, 0.f}, exp_table(far)) : FF{0.f, 0.f};
+    const FF sum = ff_add(wR, wS), t0 = a.tail ? rest_of(wQ) : FF{1.f, 0.f};
     // three logs, a lane each
     const FF ln = ln_table(lane == 0 ? sum : lane == 1 ? (a.tail ? t0 : wQ) : FF{rest, 0.f});
     auto lane_of = [&](FF v, int k) -> FF { return {__shfl_sync(0xffffffffu, v.hi, k), __shfl_sync(0xffffffffu, v.lo, k)}; };
@@ -657,7 +666,8 @@ __global__ void __launch_bounds__(kLossThreads) distill_loss_kernel(const __grid
     if (lane == 0) infinite[warp] = inf;
     loss = support_sum(part[2], loss, nw);
     for (int k = 0; k < nw; ++k) inf |= nw > 1 && infinite[k] != 0;
-    if (a.tail && !(rest <= 0.f)) loss = ff_add(loss, term_of(a.kind, a.beta, t0, ln1, ff_mul({rest, 0.f}, inv_S), ff_add(lnR, ff_neg(lnS))).f);
+    if (a.tail && rest != 0.f && !((ref - M) * p.inv_t.hi < kRestGone))
+        loss = ff_add(loss, term_of(a.kind, a.beta, t0, ln1, ff_mul(wR, inv_S), ff_add(ff_add(far, lnR), ff_neg(lnS))).f);
     if (tid == 0) {
         // (a row of -inf alone has no probabilities)
         a.loss[row] = !(sum.hi > 0.f) ? NAN : inf && loss.hi == loss.hi ? INFINITY : loss.hi + loss.lo;
@@ -691,16 +701,16 @@ __global__ void __launch_bounds__(kBwdThreads) distill_bwd_kernel(const DistArgs
 #pragma unroll
     for (int u = 0; u < kDeep; ++u)
         if (u * kBwdThreads + tid < packed) v[u].load(z + b0 + (u * kBwdThreads + tid) * E);
-    const float w = a.dloss[row], M = sv.M[row], rest = sv.rest[row];
+    const float w = a.dloss[row], ref = sv.ref[row], rest = sv.rest[row];
     long long eb = a.offsets[row], ee = a.offsets[row + 1];
     if (eb < 0 || ee < eb || ee > a.nnz) eb = ee = 0;
     const bool zero = w == 0.f || eb == ee;
     const float k = zero ? 0.f : w * rest;
     // one rounding of the argument, as in the pass over the logits
-    const float pm = M * p.c;
+    const float pm = ref * p.c;
     const bool fused = fabsf(pm) < kFusedRef;
-    const float k2 = fused ? k * exp2f(-fmaf(M, p.c, -pm)) : k;
-    auto grad = [&](float x) -> float { return k == 0.f ? 0.f : fused ? k2 * exp2_approx(fmaf(x, p.c, -pm)) : k * exp2_approx((x - M) * p.c); };
+    const float k2 = fused ? k * exp2f(-fmaf(ref, p.c, -pm)) : k;
+    auto grad = [&](float x) -> float { return k == 0.f ? 0.f : fused ? k2 * exp2_approx(fmaf(x, p.c, -pm)) : k * exp2_approx((x - ref) * p.c); };
     for (int i = i0 + tid; i < b0; i += kBwdThreads) d[i] = from_f32<T>(grad(to_f32(z[i])));
     auto each = [&](auto f) {
 #pragma unroll

@@ -90,6 +90,33 @@ def test_probabilities_next_to_the_least_float(kind, dtype):
     check(c, rh.DistillParams(kind=kind, tail=True, beta=0.3), dtype)
 
 
+@pytest.mark.parametrize("kind", ["forward", "reverse", "jsd"])
+@pytest.mark.parametrize("dtype,V", [("fp32", 1000), ("bf16", 1000), ("fp16", 1000), ("fp32", 70001), ("bf16", 151936)])
+@pytest.mark.parametrize("T", [1.0, 0.1])
+def test_a_rest_far_below_the_support(kind, dtype, V, T):
+    """Gaps of up to 700 temperatures between the support's logits and the rest's, and the other way round: where the student gives
+    the rest next to nothing, the forward kind's teacher still wants its share of it."""
+    gaps = [20, 55, 60, 80, 86, 88, 90, 95, 100, 104, 110, 200, 700, -60, -90, -200]
+    N = len(gaps)
+    c = make(N, V, dtype, np.full(N, 7), T, True, seed=6, scale=T)
+    off, ids = c["off"].tolist(), c["ids"].long()
+    c["dl"][:] = 0.7
+    for r, g in enumerate(gaps):
+        S = ids[off[r]:off[r + 1]]
+        c["z"][r, S] = (c["z"][r, S].float() * 0.2 + g * T).to(DT[dtype])
+        if r % 2:           # (a teacher who gives the rest some tenths, and one who gives it a hundredth)
+            c["q"][off[r]:off[r + 1]] = torch.log(torch.tensor([0.1, 0.2, 0.05, 0.1, 0.04, 0.01, 0.1])).cuda()
+        else:
+            c["q"][off[r]:off[r + 1]] = torch.log(torch.tensor([0.3, 0.4, 0.05, 0.1, 0.04, 0.05, 0.05])).cuda()
+    o, d = check(c, rh.DistillParams(kind=kind, tail=True, temperature=T, beta=0.4), dtype)
+    if kind == "forward":   # (the rest's gradient sums to P_0 - t_0)
+        rest = d.float()
+        for r in range(13):
+            rest[r, ids[off[r]:off[r + 1]]] = 0
+        share = torch.tensor([0.01, 0.4]).repeat(N)[:13].cuda() * 0.7 / T
+        assert (((rest[:13].double().sum(1) + share) / share).abs() <= (0.02 if dtype != "fp16" else 0.3)).all()
+
+
 @pytest.mark.parametrize("kind,tail", KINDS)
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
 @pytest.mark.parametrize("T", [0.7, 2.0 ** -20])
