@@ -29,6 +29,24 @@ bool overlap(const void* p, int64_t n, const void* q, int64_t m) {
     return n > 0 && m > 0 && a < b + 4 * static_cast<uintptr_t>(m) && b < a + 4 * static_cast<uintptr_t>(n);
 }
 
+// n pieces of `bytes` bytes, `stride` bytes apart.
+struct Pieces {
+    const void* p;
+    int64_t n, bytes, stride;
+};
+// Whether they share memory.  Pieces of b may lie between those of a where both are as far apart, or b is one.
+bool share(const Pieces& a, const Pieces& b) {
+    using I = __int128;
+    if (!a.p || !b.p || a.n <= 0 || b.n <= 0) return false;
+    const I x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    if (x >= y + I(b.n - 1) * b.stride + b.bytes || y >= x + I(a.n - 1) * a.stride + a.bytes) return false;
+    if (a.n == 1) return b.n == 1 || share(b, a);
+    if (b.n > 1 && b.stride != a.stride) return true;
+    const I k = (y < x ? y - x - (a.stride - 1) : y - x) / a.stride, d = y - x - k * a.stride;      // b begins d bytes after the piece k of a
+    if (b.n > 1) return d < a.bytes || a.stride - d < b.bytes;
+    return (k >= 0 && k < a.n && d < a.bytes) || (k + 1 >= 0 && k + 1 < a.n && a.stride - d < b.bytes);
+}
+
 bool page_size_ok(int32_t p) { return p == 16 || p == 32 || p == 64 || p == 128; }
 
 constexpr int64_t kMaxVocab = int64_t(1) << 20;
@@ -96,9 +114,8 @@ int check_distill(const rl_distill_args* a, const int32_t* dev_status, int pass)
         if (!aligned(a->dlogits, size)) return fail(RL_ERR_ARG, "dlogits not aligned to their type");
         if (a->N > 1 && a->grad_stride < a->V) return fail(RL_ERR_ARG, "grad_stride smaller than V");
         const bool in_place = a->logits == a->dlogits && (a->N == 1 || a->row_stride == a->grad_stride);
-        const uintptr_t x = reinterpret_cast<uintptr_t>(a->logits), y = reinterpret_cast<uintptr_t>(a->dlogits);
-        const uintptr_t nx = static_cast<uintptr_t>(((a->N - 1) * a->row_stride + a->V) * size), ny = static_cast<uintptr_t>(((a->N - 1) * a->grad_stride + a->V) * size);
-        if (!in_place && x < y + ny && y < x + nx) return fail(RL_ERR_ARG, "dlogits shares memory with logits");
+        const Pieces z = {a->logits, a->N, a->V * size, a->row_stride * size}, d = {a->dlogits, a->N, a->V * size, a->grad_stride * size};
+        if (!in_place && share(z, d)) return fail(RL_ERR_ARG, "dlogits shares memory with logits");
     }
     return check_device();
 }

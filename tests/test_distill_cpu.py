@@ -53,3 +53,18 @@ def test_binding_refuses_wrong_tensors():
         rh.rl_distill_fwd(z, off, ids, e, rh.DistillParams())
     with pytest.raises(rh.RLHeadError):
         rh.rl_distill_fwd_bwd(z.to(torch.int32), off, ids, e, torch.ones(2), rh.DistillParams())
+
+
+def test_gradients_between_the_rows_of_the_logits(lib):  # noqa: F811
+    """Halves of one buffer share no memory, whatever their ranges; anything that does is refused."""
+    def call(**kw):
+        a = make(row_stride=2000, grad_stride=2000, **kw)
+        return lib.rl_distill_bwd(ctypes.byref(a), FAKE + (1 << 28), FAKE, None)
+    if not torch.cuda.is_available():
+        for d in (1000, -1000, 1000 - 2 * 2000, 1000 + 3 * 2000):
+            assert call(dlogits=FAKE + 4 * d) not in (rh.RL_OK, ARG), d         # (no device)
+        assert call(dlogits=FAKE + 4 * 1000, N=1) not in (rh.RL_OK, ARG)
+    for d in (999, 1001, -999, -1001, 2000, 1, 4001, -2000):
+        assert call(dlogits=FAKE + 4 * d) == ARG, d
+    a = make(row_stride=2000, grad_stride=3000, dlogits=FAKE + 4000)             # (other strides: some rows do)
+    assert lib.rl_distill_bwd(ctypes.byref(a), FAKE + (1 << 28), FAKE, None) == ARG

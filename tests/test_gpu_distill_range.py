@@ -137,3 +137,23 @@ def test_support_tokens_masked_by_the_lowest_number(kind, tail, dtype, T):
     want, wd = rh.rl_distill_fwd_bwd(low, *args)
     assert torch.equal(o.loss, want.loss) and torch.equal(o.mass, want.mass) and torch.equal(d, wd)
     assert o.status_bits() == want.status_bits() == (NONFINITE if kind == "forward" else 0)
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("V", [1001, 70001])
+def test_gradients_beside_the_logits_in_one_buffer(dtype, V):
+    c = make(5, V, dtype, np.array([3, 0, 5, 20, 1]), 1.0, True, seed=2)
+    args = (c["off"], c["ids"], c["q"])
+    p = rh.DistillParams(kind="reverse", tail=True)
+    for first in (0, V):
+        buf = torch.zeros(5, 2 * V, dtype=DT[dtype], device="cuda")
+        z, g = buf[:, first:first + V], buf[:, V - first:2 * V - first]
+        z.copy_(c["z"])
+        want, wd = rh.rl_distill_fwd_bwd(z, *args, c["dl"], p)
+        o, d = rh.rl_distill_fwd_bwd(z, *args, c["dl"], p, dlogits=g)
+        assert d is g and torch.equal(o.loss, want.loss) and torch.equal(g, wd) and torch.equal(z, c["z"])
+        f = rh.rl_distill_fwd(z, *args, p)
+        want2, _ = rh.rl_distill_bwd(z, *args, p, f.saved, c["dl"])
+        g.zero_()
+        rh.rl_distill_bwd(z, *args, p, f.saved, c["dl"], dlogits=g)
+        assert torch.equal(g, want2) and torch.equal(z, c["z"])
