@@ -682,7 +682,7 @@ typedef struct rl_dist {
  * drawn from (RL_STATUS_ROW_ORDER, y is then not defined), temperatures and random numbers as in rl_sample (RL_STATUS_KNOB), NaN and +inf logits
  * (RL_STATUS_NONFINITE, they count as -inf).  A target row without a token accepts nothing and sets RL_STATUS_EMPTY_ROW, y = -1 and
  * logq -inf if it is the last row looked at; a draft row without one sets it too.
- * Outputs share no memory with inputs, but for keep_lens. */
+ * Outputs share no memory with inputs (RL_ERR_ARG), but for keep_lens with ctx_lens. */
 typedef struct rl_verify_args {
     int64_t R, T, V;                /* R < 2^28, V <= 2^20 */
     const int32_t* cu_q;            /* device [R+1] */

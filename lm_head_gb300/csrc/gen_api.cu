@@ -34,6 +34,7 @@ struct Pieces {
     const void* p;
     int64_t n, bytes, stride;
 };
+Pieces whole(const void* p, int64_t n, int64_t size) { return {p, p && n > 0 ? 1 : 0, n * size, 0}; }
 // Whether they share memory.  Pieces of b may lie between those of a where both are as far apart, or b is one.
 bool share(const Pieces& a, const Pieces& b) {
     using I = __int128;
@@ -229,12 +230,23 @@ int rl_verify(const rl_verify_args* a, void* ws, size_t ws_bytes, int32_t* dev_s
     if (ws_bytes < need) return fail(RL_ERR_WORKSPACE, "verification workspace too small");
     if (need > 0 && (!ws || !aligned(ws, 16))) return fail(RL_ERR_ARG, "ws is NULL or not 16-byte aligned");
     // (outputs are written before the last request has read its inputs)
-    const struct { const void* p; int64_t n; } in[] = {{a->cu_q, a->R + 1}, {a->step_tokens, a->T}, {a->u, a->T}, {a->u_next, a->R}},
-                                               out[] = {{a->tokens, a->T}, {a->logq, a->logq ? a->T : 0}, {a->accepted, a->R}, {a->keep_lens, a->keep_lens ? a->R : 0}};
-    for (const auto& x : in)
-        for (const auto& y : out)
-            if (overlap(x.p, x.n, y.p, y.n)) return fail(RL_ERR_ARG, "an output shares memory with an input");
-    if (overlap(a->accepted, a->R, a->ctx_lens, a->ctx_lens ? a->R : 0)) return fail(RL_ERR_ARG, "accepted shares memory with ctx_lens");
+    const Pieces out[] = {whole(a->tokens, a->T, 4), whole(a->logq, a->T, 4), whole(a->accepted, a->R, 4), whole(a->keep_lens, a->R, 4)};
+    const auto shared = [&](const Pieces& in, int n) {
+        for (int k = 0; k < n; ++k)
+            if (share(in, out[k])) return true;
+        return false;
+    };
+    if (shared(whole(a->cu_q, a->R + 1, 4), 4) || shared(whole(a->step_tokens, a->T, 4), 4) || shared(whole(a->u, a->T, 4), 4) ||
+        shared(whole(a->u_next, a->R, 4), 4) || shared(whole(a->ctx_lens, a->R, 4), 3))
+        return fail(RL_ERR_ARG, "an output shares memory with an input");
+    const struct { const rl_dist& d; int64_t size; } sides[] = {{a->target, a->target_dtype == RL_DTYPE_F32 ? 4 : 2}, {a->draft, a->draft_dtype == RL_DTYPE_F32 ? 4 : 2}};
+    for (const auto& s : sides) {
+        if (!s.d.logits && !s.d.offsets) continue;
+        if (shared({s.d.logits, s.d.n_rows, a->V * s.size, s.d.row_stride * s.size}, 4) || shared(whole(s.d.temperature, s.d.n_rows, 4), 4) ||
+            shared(whole(s.d.rows, a->T, 4), 4) || shared(whole(s.d.replayed, s.d.logits && s.d.offsets ? s.d.n_rows : 0, 1), 4) ||
+            (s.d.offsets && (shared(whole(s.d.offsets, s.d.n_rows + 1, 8), 4) || shared(whole(s.d.ids, s.d.nnz, 4), 4) || shared(whole(s.d.logq, s.d.nnz, 4), 4))))
+            return fail(RL_ERR_ARG, "an output shares memory with a distribution");
+    }
     rc = check_device();
     return rc != RL_OK ? rc : verify_impl(a, ws, dev_status, static_cast<cudaStream_t>(stream));
 }

@@ -77,3 +77,30 @@ def test_the_rule_gives_the_targets_distribution():
                 t = verify_reference([0, x], [0, 2], [(i + 0.5) / n, 0], [(k + 0.5) / n], Side(V, z, rows=rows), Side(V, zd, rows=rows))
                 got[t["tokens"][0]] += q[x] / n / n
     assert np.abs(got - p).max() < 2.0 / n          # the grid's own coarseness
+
+
+def test_outputs_that_share_memory_with_the_distributions(lib):  # noqa: F811
+    """Each array of either side, its first and its last element; outputs between the rows of the logits are sound."""
+    names = ["cu_q", "step_tokens", "u", "u_next", "ctx_lens", "tokens", "logq", "accepted", "keep_lens"]
+    size = dict(logits=8 * 1000 * 4, temperature=32, offsets=72, ids=40, logq=40, replayed=8, rows=32)
+    names += [s + n for s in ("target_", "draft_") for n in size]
+    apart = {n: FAKE + (k << 16) for k, n in enumerate(names)}
+
+    def call(**kw):
+        a = make(**{**apart, **kw})
+        return lib.rl_verify(ctypes.byref(a), FAKE + (1 << 28), 1 << 40, FAKE + (1 << 27), None)
+    outs = ("tokens", "logq", "accepted", "keep_lens")
+    for s in ("target_", "draft_"):
+        for n, z in size.items():
+            last = 8 * 1000 * 2 if (s, n) == ("draft_", "logits") else z
+            for y in outs:
+                assert call(**{y: apart[s + n]}) == call(**{y: apart[s + n] + last // 4 * 4 - 4}) == ARG, (s, n, y)
+    for y in ("tokens", "logq", "accepted"):
+        assert call(**{y: apart["ctx_lens"] + 12}) == ARG, y
+    if not torch.cuda.is_available():
+        assert call() not in (rh.RL_OK, ARG) and call(keep_lens=apart["ctx_lens"]) not in (rh.RL_OK, ARG)     # (no device)
+        for n, z in size.items():       # just past each
+            assert call(tokens=apart["target_" + n] + (z + 3) // 4 * 4) not in (rh.RL_OK, ARG), n
+        assert call(target_row_stride=1100, tokens=apart["target_logits"] + 4 * 1040) not in (rh.RL_OK, ARG)
+        assert call(draft_logits=None, draft_offsets=None, tokens=apart["draft_ids"]) not in (rh.RL_OK, ARG)
+    assert call(target_row_stride=1100, tokens=apart["target_logits"] + 4 * 1098) == ARG
