@@ -832,7 +832,9 @@ int rl_page_copy(const rl_page_copy_args* args, int32_t* dev_status, void* strea
  * RL_STATUS_NONFINITE.
  * Checked on the device: row bounds (RL_STATUS_OFFSETS, the row then has no support), ids in [0, V) and logq not NaN,
  * not +inf and, with tail, at most 1e-6 (RL_STATUS_ID_RANGE, RL_STATUS_LOGQ; the entry is left out, but for a logq
- * above 1e-6), ids strictly ascending (RL_STATUS_ROW_ORDER; the row's results are then not defined). */
+ * above 1e-6), ids strictly ascending (RL_STATUS_ROW_ORDER; the row's results are then not defined).
+ * loss, mass, dlogits and saved share no memory with each other or with inputs (RL_ERR_ARG), but for dlogits with logits as below
+ * and loss or mass with dloss. */
 typedef enum { RL_DISTILL_FORWARD = 0, RL_DISTILL_REVERSE = 1, RL_DISTILL_JSD = 2 } rl_distill_kind;
 typedef struct rl_distill_args {
     const void* logits;             /* device [N, V], rows row_stride elements apart; V * size at most 1,800,000 bytes */

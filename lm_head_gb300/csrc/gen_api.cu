@@ -93,7 +93,7 @@ int check_verify_sizes(const rl_verify_args* a) {
     return rc != RL_OK ? rc : check_dist(&a->draft, a->draft_dtype, a->V, false);
 }
 
-int check_distill(const rl_distill_args* a, const int32_t* dev_status, int pass) {
+int check_distill(const rl_distill_args* a, const void* saved, const int32_t* dev_status, int pass) {
     if (!a || !dev_status) return fail(RL_ERR_ARG, "args/dev_status is NULL");
     if (a->N < 0 || a->V <= 0 || a->nnz < 0) return fail(RL_ERR_ARG, "negative or zero size");
     if (a->dtype != RL_DTYPE_F32 && a->dtype != RL_DTYPE_BF16 && a->dtype != RL_DTYPE_F16)
@@ -118,6 +118,21 @@ int check_distill(const rl_distill_args* a, const int32_t* dev_status, int pass)
         const Pieces z = {a->logits, a->N, a->V * size, a->row_stride * size}, d = {a->dlogits, a->N, a->V * size, a->grad_stride * size};
         if (!in_place && share(z, d)) return fail(RL_ERR_ARG, "dlogits shares memory with logits");
     }
+    // (the support rows are read until the loss and the gradients are written; dloss before the loss is)
+    const Pieces none = {nullptr, 0, 0, 0}, state = whole(saved, 1, static_cast<int64_t>(distill_saved_bytes(a->N, a->nnz)));
+    const Pieces d = pass == kDistillFwd ? none : Pieces{a->dlogits, a->N, a->V * size, a->grad_stride * size};
+    const Pieces out[] = {pass == kDistillBwd ? none : whole(a->loss, a->N, 4), pass == kDistillBwd ? none : whole(a->mass, a->N, 4), d, state};
+    const Pieces in[] = {whole(a->offsets, a->N + 1, 8), whole(a->ids, a->nnz, 4), whole(a->logq, a->nnz, 4)};
+    for (const Pieces& y : out) {
+        for (const Pieces& x : in)
+            if (share(x, y)) return fail(RL_ERR_ARG, "an output shares memory with a support row");
+        if (&y != out + 2 && share({a->logits, a->N, a->V * size, a->row_stride * size}, y))
+            return fail(RL_ERR_ARG, "an output shares memory with logits");
+    }
+    if (share(state, out[0]) || share(state, out[1]) || share(state, d) || share(d, out[0]) || share(d, out[1]) || share(out[0], out[1]))
+        return fail(RL_ERR_ARG, "outputs share memory with each other");
+    if (pass != kDistillFwd && (share(whole(a->dloss, a->N, 4), d) || share(whole(a->dloss, a->N, 4), state)))
+        return fail(RL_ERR_ARG, "an output shares memory with dloss");
     return check_device();
 }
 
@@ -348,19 +363,19 @@ size_t rl_distill_saved_bytes(int64_t N, int64_t nnz) { return N < 0 || nnz < 0 
 
 int rl_distill_fwd(const rl_distill_args* a, void* saved, int32_t* dev_status, void* stream) {
     if (!saved || !aligned(saved, 16)) return fail(RL_ERR_ARG, "saved is NULL or not 16-byte aligned");
-    const int rc = check_distill(a, dev_status, kDistillFwd);
+    const int rc = check_distill(a, saved, dev_status, kDistillFwd);
     return rc != RL_OK ? rc : distill_impl(a, kDistillFwd, saved, dev_status, static_cast<cudaStream_t>(stream));
 }
 
 int rl_distill_bwd(const rl_distill_args* a, const void* saved, int32_t* dev_status, void* stream) {
     if (!saved || !aligned(saved, 16)) return fail(RL_ERR_ARG, "saved is NULL or not 16-byte aligned");
-    const int rc = check_distill(a, dev_status, kDistillBwd);
+    const int rc = check_distill(a, saved, dev_status, kDistillBwd);
     return rc != RL_OK ? rc : distill_impl(a, kDistillBwd, const_cast<void*>(saved), dev_status, static_cast<cudaStream_t>(stream));
 }
 
 int rl_distill_fwd_bwd(const rl_distill_args* a, void* saved, int32_t* dev_status, void* stream) {
     if (!saved || !aligned(saved, 16)) return fail(RL_ERR_ARG, "saved is NULL or not 16-byte aligned");
-    const int rc = check_distill(a, dev_status, kDistillBoth);
+    const int rc = check_distill(a, saved, dev_status, kDistillBoth);
     return rc != RL_OK ? rc : distill_impl(a, kDistillBoth, saved, dev_status, static_cast<cudaStream_t>(stream));
 }
 

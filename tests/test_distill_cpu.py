@@ -68,3 +68,37 @@ def test_gradients_between_the_rows_of_the_logits(lib):  # noqa: F811
         assert call(dlogits=FAKE + 4 * d) == ARG, d
     a = make(row_stride=2000, grad_stride=3000, dlogits=FAKE + 4000)             # (other strides: some rows do)
     assert lib.rl_distill_bwd(ctypes.byref(a), FAKE + (1 << 28), FAKE, None) == ARG
+
+
+def test_outputs_that_share_memory(lib):  # noqa: F811
+    """Each input's first and last element under each output; the loss in dloss's place is sound."""
+    size = dict(logits=16000, offsets=40, ids=40, logq=40, dloss=16, loss=16, mass=16, dlogits=16000)
+    apart = {n: FAKE + (k << 16) for k, n in enumerate(size)}
+    state = FAKE + (1 << 28)
+    calls = dict(fwd=lib.rl_distill_fwd, bwd=lib.rl_distill_bwd, fwd_bwd=lib.rl_distill_fwd_bwd)
+    outs = dict(fwd=("loss", "mass"), bwd=("dlogits",), fwd_bwd=("loss", "mass", "dlogits"))
+
+    def call(name, saved=state, **kw):
+        a = make(**{**apart, **kw})
+        return calls[name](ctypes.byref(a), saved, FAKE + (1 << 27), None)
+    for name, fn in calls.items():
+        ins = ["logits", "offsets", "ids", "logq"] + (["dloss"] if name != "fwd" else [])
+        for x in ins:
+            for y in outs[name]:
+                if (x, y) in (("logits", "dlogits"), ("dloss", "loss"), ("dloss", "mass")):
+                    continue
+                assert call(name, **{y: apart[x]}) == call(name, **{y: apart[x] + size[x] - 4}) == ARG, (name, x, y)
+            assert call(name, saved=apart[x]) == ARG, (name, x)
+        for y in outs[name]:
+            assert call(name, saved=apart[y]) == ARG, (name, y)
+        if not torch.cuda.is_available():
+            assert call(name) not in (rh.RL_OK, ARG), name        # (no device)
+            for y in ("loss", "mass"):
+                assert call(name, **{y: apart["dloss"]}) not in (rh.RL_OK, ARG), (name, y)
+            for y in outs[name]:
+                assert call(name, **{y: apart["ids"] + 40}) not in (rh.RL_OK, ARG), (name, y)
+    for y in ("loss", "mass"):
+        assert call("fwd_bwd", **{y: apart["dlogits"] + 15996}) == ARG
+    assert call("fwd", loss=apart["mass"] + 12) == ARG
+    if not torch.cuda.is_available():
+        assert call("bwd", loss=apart["ids"], mass=apart["logits"]) not in (rh.RL_OK, ARG)      # (not of the backward)

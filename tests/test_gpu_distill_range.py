@@ -157,3 +157,14 @@ def test_gradients_beside_the_logits_in_one_buffer(dtype, V):
         g.zero_()
         rh.rl_distill_bwd(z, *args, p, f.saved, c["dl"], dlogits=g)
         assert torch.equal(g, want2) and torch.equal(z, c["z"])
+
+
+def test_the_loss_in_dloss_s_place():
+    c = make(300, 4099, "bf16", np.arange(300) % 40, 1.0, True)
+    args = (c["z"], c["off"], c["ids"], c["q"])
+    p = rh.DistillParams(kind="jsd", tail=True)
+    want, wd = rh.rl_distill_fwd_bwd(*args, c["dl"], p)
+    o, _ = rh.rl_distill_fwd_bwd(*args, c["dl"], p)
+    o.loss = c["dl"].clone()
+    o, d = rh.rl_distill_fwd_bwd(*args, o.loss, p, out=o)
+    assert torch.equal(o.loss, want.loss) and torch.equal(d, wd) and torch.equal(o.mass, want.mass)
