@@ -79,7 +79,9 @@ def _dist(name, d, V, T):
         raise _err(f"{name}: {n} rows for a step of {T}")
     has = d.offsets is not None
     nnz = d.ids.numel() if has and d.ids is not None else 0
-    return (0 if z is None else z.data_ptr(), n, stride, _dev(f"{name}.temperature", d.temperature, f32, n, True),
+    # (no rows have no address, and a null one would say that there are no logits at all; nothing of it is read)
+    at = 0 if z is None else z.data_ptr() or 16
+    return (at, n, stride, _dev(f"{name}.temperature", d.temperature, f32, n, True),
             _dev(f"{name}.offsets", d.offsets, torch.int64, None, True), _dev(f"{name}.ids", d.ids, i32, None, not has),
             _dev(f"{name}.logq", d.logq, f32, nnz, not has), nnz, _dev(f"{name}.replayed", d.replayed, torch.uint8, n, True),
             _dev(f"{name}.rows", d.rows, i32, T, True)), dt

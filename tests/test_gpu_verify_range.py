@@ -132,3 +132,26 @@ def test_support_rows_beside_drafts_masked_by_the_lowest_number(T, dtype):
              target=Half(V, ids=ids, lq=lq), draft=Half(V, zd, temp))
     ref, _ = check(c)
     assert set(ref["tokens"][::2]) == {1, 700, 1500, 2995}
+
+
+def test_logits_of_no_rows():
+    """A step without tokens, a step without drafts, and a row map into no rows at all."""
+    V, R = 300, 3
+    i = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    f = lambda *x: torch.tensor(x, dtype=torch.float32, device="cuda")  # noqa: E731
+    none = torch.zeros(0, V, device="cuda")
+    z = torch.randn(R, V, generator=torch.Generator().manual_seed(1)).cuda()
+    for draft in (rh.Dist(logits=none), None):
+        o = rh.rl_verify(i(), i(0, 0, 0, 0), f(), f(0.1, 0.2, 0.3), rh.Dist(logits=none), draft, vocab=V, ctx_lens=i(4, 5, 6))
+        assert o.accepted.tolist() == [0, 0, 0] and o.keep_lens.tolist() == [4, 5, 6] and o.status_bits() == 0
+        o = rh.rl_verify(i(), i(0), f(), f(), rh.Dist(logits=none), draft, vocab=V)
+        assert o.status_bits() == 0
+    # requests of one token: a draft of no rows is not looked at
+    rows = rh.Dist(logits=none, rows=i(0, 0, 0))
+    args = (i(1, 2, 3), i(0, 1, 2, 3), f(0, 0, 0), f(0.1, 0.5, 0.9), rh.Dist(logits=z))
+    o, want = rh.rl_verify(*args, rows, vocab=V), rh.rl_verify(*args, None, vocab=V)
+    assert torch.equal(o.tokens, want.tokens) and torch.equal(o.logq, want.logq) and o.status_bits() == 0
+    # a candidate whose draft row does not exist: not a sure draft
+    args = (i(1, 2, 3), i(0, 3), f(0.5, 0.5, 0.5), f(0.5), rh.Dist(logits=z))
+    assert rh.rl_verify(*args, rows, vocab=V).status_bits() == 0x21          # OFFSETS, EMPTY_ROW
+    assert rh.rl_verify(*args, None, vocab=V).status_bits() == 0
