@@ -150,8 +150,8 @@ struct DistShared {              // (small: three blocks with slices of 76 KB ar
     float4 sup[kDistWarps];      // of each support warp: largest logit, largest of the teacher's, sums relative to the block's largest
     FF sum[kDistWarps];          // pairs to be added up over the support warps
     float A[kDistWarps];
-    float rest_ref, rest_sum;    // of the rest: reference logit, sum relative to it,
-    float unit, x0;              // the probability of a weight of 1 in the sum, and P g
+    float rest_ref;              // of the rest: reference logit,
+    float unit, x0, g0;          // the probability of a weight of 1 in the sum, P g, and P g over the sum
 };
 
 // v into another block's `to`, counted by its barrier `bar` (both given by this block's own addresses).
@@ -461,13 +461,14 @@ __global__ void __launch_bounds__(NT, kBlocks) distill_kernel(const __grid_const
         if (lane == 0) s.A[warp] = A;
         if (tid == 0) {
             s.rest_ref = v.x;
-            s.rest_sum = v.y;
             s.unit = scale * inv_total;
             const float far = (v.x - M) * inv_T;
-            s.x0 = 0.f;
+            s.x0 = s.g0 = 0.f;
             if (a.tail && v.y != 0.f && !(far < kRestGone)) {
                 const float t0 = rest_of(wT).hi;
-                s.x0 = slope_of(a.kind, a.beta, t0, logf(t0), rest * inv_total, far + logf(v.y) - lnT);
+                const float x0 = slope_of(a.kind, a.beta, t0, logf(t0), rest * inv_total, far + logf(v.y) - lnT);
+                s.x0 = x0;
+                s.g0 = x0 / v.y;
             }
             if (rank == 0) {
                 sv.M[row] = M;
@@ -478,12 +479,12 @@ __global__ void __launch_bounds__(NT, kBlocks) distill_kernel(const __grid_const
     }
     __syncthreads();
     // the gradient's factor outside the support (over a weight of the sum, times T), and A
-    const float ref = s.rest_ref, sum = s.rest_sum;
+    const float ref = s.rest_ref;
     float k_rest = 0.f, A = 0.f;
     if (any) {
         for (int k = 0; k < nw; ++k) A += s.A[k];
         A += s.x0;
-        if (sum != 0.f) k_rest = s.x0 / sum - A * s.unit;
+        k_rest = s.g0 - A * s.unit;
     }
     if (!listed) {                               // (in place: its logits are read again until here)
         __syncthreads();
