@@ -432,7 +432,7 @@ __global__ void __launch_bounds__(NT, kBlocks) distill_kernel(const __grid_const
     if (mine) {
         const float2 v = join(s.xpart, p.cs);
         M = fmaxf(v.x, mS);
-        const float scale = v.y != 0.f ? exp2f((v.x - M) * p.c) : 0.f, rest = v.y * scale;
+        const float scale = v.x == M ? 1.f : v.y != 0.f ? exp2f((v.x - M) * p.c) : 0.f, rest = v.y * scale;
         float held = 0.f;
         sT = 0.f;
         for (int k = 0; k < nw; ++k) {
@@ -447,7 +447,13 @@ __global__ void __launch_bounds__(NT, kBlocks) distill_kernel(const __grid_const
             lnW = logf(sT);
             inv_sT = 1.f / sT;
         }
-        float A = 0.f;
+        float x0 = 0.f, g0 = 0.f, A = 0.f;
+        const float far = (v.x - M) * inv_T;
+        if (a.tail && v.y != 0.f && !(far < kRestGone)) {
+            const float t0 = rest_of(wT).hi;
+            x0 = slope_of(a.kind, a.beta, t0, logf(t0), rest * inv_total, far + logf(v.y) - lnT);
+            g0 = x0 / v.y;
+        }
         each([&](const Entry& x, bool is_first, long long) {
             float P;
             const float g = slope(x, P);
@@ -462,14 +468,8 @@ __global__ void __launch_bounds__(NT, kBlocks) distill_kernel(const __grid_const
         if (tid == 0) {
             s.rest_ref = v.x;
             s.unit = scale * inv_total;
-            const float far = (v.x - M) * inv_T;
-            s.x0 = s.g0 = 0.f;
-            if (a.tail && v.y != 0.f && !(far < kRestGone)) {
-                const float t0 = rest_of(wT).hi;
-                const float x0 = slope_of(a.kind, a.beta, t0, logf(t0), rest * inv_total, far + logf(v.y) - lnT);
-                s.x0 = x0;
-                s.g0 = x0 / v.y;
-            }
+            s.x0 = x0;
+            s.g0 = g0;
             if (rank == 0) {
                 sv.M[row] = M;
                 sv.ref[row] = v.x;
@@ -570,9 +570,11 @@ __global__ void __launch_bounds__(NT, kBlocks) distill_kernel(const __grid_const
 // ---- the loss, in pairs of floats --------------------------------------------------------------
 // A block a row, as many of its warps as hold the support.  A kernel of its own: as the last step of a row's first
 // block it kept that block's slice of the multiprocessor for 9000 cycles, half as long again as the pass itself.
+// Latency, so blocks on a multiprocessor count: ten of 48 registers a thread (4096 fp32 rows of 1000 logits, both kernels 32.1 us), not
+// eight of 64 (35.0).
 constexpr int kLossThreads = 128, kLossWarps = kLossThreads / 32;
 
-__global__ void __launch_bounds__(kLossThreads) distill_loss_kernel(const __grid_constant__ DistArgs p, const DistSaved sv) {
+__global__ void __launch_bounds__(kLossThreads, 10) distill_loss_kernel(const __grid_constant__ DistArgs p, const DistSaved sv) {
     __shared__ FF part[3][kLossWarps];
     __shared__ float largest[kLossWarps];
     __shared__ int infinite[kLossWarps];
@@ -646,7 +648,11 @@ __global__ void __launch_bounds__(kLossThreads) distill_loss_kernel(const __grid
     wS = support_sum(part[0], wS, nw);
     wQ = support_sum(part[1], wQ, nw);
     // the rest's sum, relative to the row's reference
-    const FF far = rest != 0.f ? scaled(ref, M) : FF{-INFINITY, 0.f}, wR = rest != 0.f ? ff_mul({rest, 0.f}, exp_table(far)) : FF{0.f, 0.f};
+    FF far = {0.f, 0.f}, wR = {rest, 0.f};
+    if (ref != M && rest != 0.f) {
+        far = scaled(ref, M);
+        wR = ff_mul(wR, exp_table(far));
+    }
     const FF sum = ff_add(wR, wS), t0 = a.tail ? rest_of(wQ) : FF{1.f, 0.f};
     // three logs, a lane each
     const FF ln = ln_table(lane == 0 ? sum : lane == 1 ? (a.tail ? t0 : wQ) : FF{rest, 0.f});

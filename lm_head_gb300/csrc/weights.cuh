@@ -163,8 +163,9 @@ RL_DEVINL FF ln_table(FF x) {
     const float y = logf(x.hi);
     const FF r = ff_mul(x, exp_table({-y, 0.f}));        // 1 + d
     const float d = __fadd_rn(__fsub_rn(r.hi, 1.f), r.lo);
-    const FF l = fast_two_sum(y, fmaf(-0.5f * d, d, d));
-    return small ? ff_add(l, {-69.31472015380859375f, 2.0978141e-06f}) : l;      // - 100 ln 2
+    FF l = fast_two_sum(y, fmaf(-0.5f * d, d, d));
+    if (small) l = ff_add(l, {-69.31472015380859375f, 2.0978141e-06f});      // - 100 ln 2
+    return l;
 }
 
 }  // namespace rl
