@@ -673,7 +673,8 @@ typedef struct rl_dist {
  * candidate (drafts that were copied or greedy).  Probabilities and sums that decide a token are carried to about
  * 2^-36 of the row's total.
  * Outputs: tokens[t] = the accepted tokens, then y, then -1, in the request's rows; logq[t] = ln p_t of the token (0 where
- * there is none); accepted[r]; keep_lens[r] = ctx_lens[r] + accepted[r] + 1, the tokens whose keys and values stay in the
+ * there is none; of y from a row of logits by the sums that drew it, to fp32 rounding, of an accepted token by fp32 sums, within
+ * 6.2e-6 + 2^-22 |logq|; of a support row its own, to fp32 rounding); accepted[r]; keep_lens[r] = ctx_lens[r] + accepted[r] + 1, the tokens whose keys and values stay in the
  * cache (rl_page_release).  A request without rows has accepted 0 and keep_lens = ctx_lens; rows that no request has
  * get -1 and 0.
  * Checked on the device: cu_q that decreases or leaves [0, T] (RL_STATUS_LENGTHS, the request then has no rows), candidates outside
@@ -698,7 +699,8 @@ typedef struct rl_verify_args {
     int32_t* accepted;              /* device [R] */
     int32_t* keep_lens;             /* device [R]; NULL to skip; may be ctx_lens */
 } rl_verify_args;
-/* 16-byte aligned, with any contents; by T, V and which logits there are. */
+/* 16-byte aligned, with any contents.  Its size goes by R, T, V, which logits there are and their types, and grows with R (64 bytes for each
+ * 512 tokens of V) and T (8 bytes for each 4 KB of a row). */
 size_t rl_verify_workspace_bytes(const rl_verify_args* args);
 int rl_verify(const rl_verify_args* args, void* ws, size_t ws_bytes, int32_t* dev_status, void* stream);
 
@@ -745,7 +747,11 @@ int rl_page_release(const rl_page_release_args* args, void* ws, size_t ws_bytes,
  * in the call is left out and sets RL_STATUS_ID_RANGE; so is one with lens < 0 or above
  * the parent's kv_lens (RL_STATUS_LENGTHS) or a row too short for it (RL_STATUS_PAGES).  Where the pool runs out
  * (RL_STATUS_PAGES) or a page id lies outside [0, n_pages) (RL_STATUS_PAGE_ID) the entry is -1 and nothing is
- * copied.  parents, children and lens share no memory with kv_lens, src, dst and tokens. */
+ * copied; but where only the parent's last page lies outside, the child's entry is its new page, which has been handed out, with nothing
+ * copied into it.
+ * What the rows share is read-only: tokens may be appended to a row only past its shared pages.  A row that is stepped back into
+ * one (keep_lens below lens / page_size pages) goes on from a fork of itself into another row, which gets that page anew.
+ * parents, children and lens share no memory with kv_lens, src, dst and tokens. */
 typedef struct rl_page_fork_args {
     int64_t R, C;                   /* rows of the table, entries of the call; < 2^31 */
     const int32_t* parents;         /* device [C] */

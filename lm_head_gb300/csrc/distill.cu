@@ -12,14 +12,15 @@
 //
 // One kernel, a cluster of blocks a row: each block brings its slice of the row into shared memory by one
 // bulk copy, while it works through the row's support (few entries, every block of the cluster does them all);
-// takes the support out of the slice (-inf), so that the rest's sum is a sum and not a difference of nearly equal ones;
+// takes the support out of the slice (-inf), so that the rest's sum is a sum and not a difference of nearly equal ones,
+// kept relative to the rest's own largest logit where that lies far below the support's;
 // then the blocks send each other (reference, sum) of their slices, and each block turns its slice into the gradient
 // in place and sends it off by one bulk copy.  So logits are read once and gradients written once.
 //
-// HBM bounds it for long rows: 4096 bf16 rows of 151,936 logits 411 us (89 % of a copy's rate), 2048 fp32 rows 436 us with a rest
-// and up to 128 entries (84 %), 387 us without (95 %).  Each row waits for its support and its cluster; slices of
+// HBM bounds it for long rows: 4096 bf16 rows of 151,936 logits 411 us (89 % of a copy's rate), 2048 fp32 rows 431 us with a rest
+// and up to 128 entries (85 %), 387 us without (95 %).  Each row waits for its support and its cluster; slices of
 // 75 KB leave room for three blocks on a multiprocessor, whose loads, sums and stores fill one another's waits.  The forward
-// alone, whose blocks store nothing, is at 72 % (254 us): their loads do not follow one another closely enough.
+// alone, whose blocks store nothing, is at 70 % (260 us): their loads do not follow one another closely enough.
 //
 // A divergence is a small difference of the outcomes' terms: a second kernel takes it in pairs of floats (2^-38), with
 // the rest's sum of fp32 exponentials the only fp32 part; an error of it moves L in second order

@@ -15,8 +15,10 @@
 //                  it (the fewest moves), then the tables by a look-up in the bitmap's running counts
 //  page_copy_kernel  a warp copies a head's tokens of one page
 //
-// Lists and tables are latency: launches, one look at every table entry by atomics in L2, and the counts.  A release of
-// 128 requests 8.3 us, of 8192 (524,288 entries) 13.7 us; a compaction's lists and tables 12 us.  Copies are HBM:
+// Lists and tables are latency: launches, and loads that follow on one another (a row's length, its entries, their words; the
+// counts before a block's words).  A release of 128 requests 8.3 us, of 8192 13.0 us: by themselves, caches cold, the marks take 7.7 us
+// with L2 at 16 % of its rate and the sweep 11 us with L2 at 3 %, most of it each block's count; a compaction's lists and tables
+// 12 us (the plan by itself 11).  Copies are HBM:
 // 2.35 GB read and written for 512 sequences' moves in 700 us, 6.7 TB/s, as a copy's rate; 0.8 GB of half-filled pages in
 // 257 us, 6.3 TB/s.
 #include <climits>
