@@ -1196,20 +1196,26 @@ struct Pick : Request<kPickThreads> {
             }
             total = block_sum(v);
         }
-        if (total == 0 && !whole) {              // nothing is left: from the target
+        if (total > 0 && !whole) {
+            if (search(t, fraction_of(u, total), false, bits)) return;
+            total = 0;
+        }
+        if (!whole) {                            // nothing is left: from the target
             whole = true;
             int first = warp;
             sum_steps(logits_of(dp, p), &s.draw.row[0], V, 0, steps, first, {kWarps, nullptr}, sums, smem_addr(s.tab));
             __syncthreads();
             total = take_parts();
         }
-        if (total > 0) search(t, fraction_of(u, total), whole, bits);
+        if (total > 0) search(t, fraction_of(u, total), true, bits);
         else if (tid == 0) finish(t, -1, 0.f, bits);
     }
-    // The part in which the number falls, then its token.
-    RL_DEVINL void search(long long t, unsigned long long want, bool whole, int& bits) {
+    // The part in which the number falls, then its token.  False if nothing is left of any token of the part: what was summed up
+    // is the sums' own error (p and q are the same to their accuracy).
+    RL_DEVINL bool search(long long t, unsigned long long want, bool whole, int& bits) {
         const int n = steps * kVerStep, per = (n + kPickThreads - 1) / kPickThreads;
         unsigned long long v = 0;
+        if (tid == 0) s.flag = 1;
         __syncthreads();
         for (int j = 0; j < per; ++j) v += tid * per + j < n ? cs[tid * per + j] : 0ull;
         unsigned long long c = block_scan(v);
@@ -1224,7 +1230,11 @@ struct Pick : Request<kPickThreads> {
                 c += x;
             }
         __syncthreads();
-        if (warp != 0) return;
+        if (warp == 0) token_of(t, whole, bits);
+        __syncthreads();
+        return s.flag != 0;
+    }
+    RL_DEVINL void token_of(long long t, bool whole, int& bits) {
         const int i0 = s.token * kVerPart + lane * 4;
         const unsigned long long rest = s.unit;
         const VerRow& p = s.draw.row[0];
@@ -1248,6 +1258,10 @@ struct Pick : Request<kPickThreads> {
         }
         const unsigned hit = __ballot_sync(0xffffffffu, incl > rest), some = __ballot_sync(0xffffffffu, last >= 0),
                        any = __ballot_sync(0xffffffffu, likely >= 0);
+        if (!whole && !some) {
+            if (lane == 0) s.flag = 0;
+            return;
+        }
         int at = last >= 0 ? last : likely;
         int src;
         if (hit) {

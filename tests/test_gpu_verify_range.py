@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import lm_head_gb300 as rh  # noqa: F401
-from test_gpu_verify import DT, Half, check
+from test_gpu_verify import DT, Half, call, check
 
 pytestmark = pytest.mark.gpu
 
@@ -155,3 +155,35 @@ def test_logits_of_no_rows():
     args = (i(1, 2, 3), i(0, 3), f(0.5, 0.5, 0.5), f(0.5), rh.Dist(logits=z))
     assert rh.rl_verify(*args, rows, vocab=V).status_bits() == 0x21          # OFFSETS, EMPTY_ROW
     assert rh.rl_verify(*args, None, vocab=V).status_bits() == 0
+
+
+@pytest.mark.parametrize("form", ["dense", "rows", "sure"])
+@pytest.mark.parametrize("V", [2, 130, 1500])
+def test_nothing_left_but_the_sums_own_error(V, form):
+    """Both sides give one token all but e^-40; a candidate that only the draft gives anything (e^-46) is turned down.  What is left
+    of the likely token, 1e-20, is far below the sums' accuracy, and of the others it is less by 1e6 and more: the token is the likely
+    one, not any that happens to lie beside it."""
+    R = 128
+    rng = np.random.default_rng(V)
+    T, Td = rng.uniform(0.01, 0.05, 2 * R), rng.uniform(0.001, 0.05, 2 * R)
+    M, Md = rng.uniform(3, 9, 2 * R), rng.uniform(3, 9, 2 * R)
+    z = torch.from_numpy(M[:, None] - 200 * T[:, None] * np.ones(V)).float()
+    zd = torch.from_numpy(Md[:, None] - 200 * Td[:, None] * np.ones(V)).float()
+    a = rng.integers(0, V, 2 * R)
+    step = np.zeros(2 * R, int)
+    rows = torch.arange(2 * R)
+    z[rows, a], zd[rows, a] = torch.from_numpy(M).float(), torch.from_numpy(Md).float()
+    b = (a + 1 + rng.integers(0, max(V - 1, 1), 2 * R) % (V - 1)) % V
+    step[1::2] = b[::2]
+    zd[rows, b] = torch.from_numpy(Md - 46 * Td).float()
+    temp, temp_d = T.astype(np.float32), Td.astype(np.float32)
+    draft = Half(V, zd, temp_d) if form == "dense" else None
+    if form == "rows":
+        ids = [np.sort([x, y]) for x, y in zip(a, b)]
+        draft = Half(V, ids=ids, lq=[np.where(i == x, 0, -46).astype(np.float32) for i, x in zip(ids, a)])
+    c = dict(step=step, cu=np.arange(0, 2 * R + 1, 2), u=np.full(2 * R, 0.9, np.float32), un=rng.random(R).astype(np.float32), V=V,
+             ctx=np.zeros(R, int), target=Half(V, z, temp), draft=draft)
+    for dtype in ("fp32", "bf16"):
+        o = call(dict(c, target=Half(V, z.to(DT[dtype]), temp)))
+        assert not o.accepted.any() and o.status_bits() == 0
+        assert (o.tokens.cpu().numpy()[::2] == a[::2]).all(), np.flatnonzero(o.tokens.cpu().numpy()[::2] != a[::2])
