@@ -666,7 +666,7 @@ typedef struct rl_dist {
  * x_t = step_tokens[t+1] was drawn (a request of one row has no drafts).  In order of the rows
  *   x_t is accepted if u[t] q_t(x_t) < p_t(x_t);
  *   the first that is not ends the step: its row's token y is drawn from max(p_t - q_t, 0) / sum
- *     (from p_t where that is 0 everywhere); after the last row's drafts y is drawn from the last row's p_t;
+ *     (from p_t where that is 0 everywhere, to the accuracy below); after the last row's drafts y is drawn from the last row's p_t;
  *   y is the first token with sum_{j <= y} left_j > u_next[r] sum left.
  * So the tokens are distributed as the target's own samples.  Row t's p is softmax(logits / T) of the vocabulary (T = 0: the largest
  * logit, the lowest index of equal ones), or exp(logq) on its support row; q likewise, or, without any draft distribution, 1 for the
